@@ -339,8 +339,8 @@ def _f32(x):
 def _mix(x):
     """A whole number below 2^32 from another: two rounds of multiplying and folding."""
     x = x ^ (x >> 16)
-    x = (x * 0x6A09E667) & 0xFFFFFFFF
-    x = x ^ (x >> 15)
+    x = (x * 0x3C6EF373) & 0xFFFFFFFF
+    x = x ^ (x >> 14)
     x = (x * 0xBB67AE85) & 0xFFFFFFFF
     return x ^ (x >> 16)
 
