@@ -396,6 +396,145 @@ rdt_status rdt_embedding_backward(const int32_t* ids, int32_t tokens, const floa
                                   int64_t vocab, int32_t accumulate, void* ws, size_t ws_bytes,
                                   void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Log probabilities of given tokens from logits, with entropy, log-sum-exp and
+ * the most likely alternatives, and their gradient. The fused cross-entropy
+ * above returns a target's NLL together with the gradient of its mean; these
+ * calls are for what needs the values themselves or another loss: scoring,
+ * distillation, policy training, sampling reports.
+ *
+ * A row z of `vocab` logits stands for the distribution p = softmax(logit_scale
+ * z); logit_scale is 1 / temperature, finite and > 0. Logits are fp32, bf16 or
+ * fp16, [rows, vocab] with row stride ld elements (ld >= vocab, any alignment
+ * an element has); all arithmetic is fp32.
+ *
+ * rdt_token_logprobs, for each row t:
+ *   logp[t]     = ln p[targets[t]]
+ *   entropy[t]  = -sum_j p_j ln p_j
+ *   lse[t]      = ln sum_j exp(logit_scale z_j)
+ *   stats[2t]   = max_j z_j, stats[2t + 1] = lse[t] - logit_scale max_j z_j:
+ *                 what the gradient needs (lse alone loses digits when the
+ *                 logits are large)
+ *   top_ids / top_logp [t * top + i]: id and ln p of the i-th largest logit,
+ *                 equal logits in order of id; `top` in [0, RDT_MAX_TOP]
+ * Each output may be null (logp needs targets; top_ids and top_logp go
+ * together, with top >= 1); at least one is given.
+ *  - targets int32 [rows], or null: no logp, every row is computed. A row with
+ *    targets[t] < 0 is not scored and its logits are not read: its outputs
+ *    are 0 and its ids -1. targets[t] >= vocab gives logp NaN.
+ *  - A logit of -inf is a masked token: p = 0, never an alternative; a masked
+ *    target has logp -inf. Where fewer than `top` tokens are left, the rest
+ *    has id -1 and ln p -inf. A row with every token masked has lse, logp,
+ *    stats[2t] and top_logp -inf, entropy and stats[2t + 1] 0, ids -1.
+ *  - A row that holds a NaN or +inf has NaN outputs and ids -1.
+ * rows may be 0. logits and outputs must not overlap.
+ *
+ * rdt_token_logprobs_backward: the gradient of sum_t (d_logp[t] logp[t] +
+ * d_entropy[t] entropy[t] + d_lse[t] lse[t]) with respect to the logits,
+ *   d_logits[t, j] = logit_scale ( [j = targets[t]] d_logp[t]
+ *        + p_j (d_lse[t] - d_logp[t] - d_entropy[t] (ln p_j + entropy[t])) ),
+ * rounded once to d_dtype. logits, logit_scale and targets as in the forward,
+ * stats and entropy as it wrote them. d_logp, d_entropy, d_lse fp32 [rows],
+ * each may be null for 0 but not all; d_logp needs targets, d_entropy needs
+ * entropy. d_logits [rows, vocab] with row stride ld_d; it may be the logits
+ * themselves (same pointer, type and stride), else they must not overlap.
+ * Rows not scored (targets[t] < 0) or with every token masked get zeros;
+ * targets[t] >= vocab and rows with NaN stats get NaN.
+ * ------------------------------------------------------------------------- */
+typedef enum rdt_dtype { RDT_F32 = 0, RDT_BF16 = 1, RDT_F16 = 2 } rdt_dtype;
+#define RDT_MAX_TOP 32
+
+rdt_status rdt_token_logprobs(const void* logits, int32_t dtype, int64_t ld, int32_t rows,
+                              int32_t vocab, float logit_scale, const int32_t* targets,
+                              float* logp, float* entropy, float* lse, float* stats, int32_t top,
+                              int32_t* top_ids, float* top_logp, void* stream);
+rdt_status rdt_token_logprobs_backward(const void* logits, int32_t dtype, int64_t ld,
+                                       int32_t rows, int32_t vocab, float logit_scale,
+                                       const int32_t* targets, const float* stats,
+                                       const float* entropy, const float* d_logp,
+                                       const float* d_entropy, const float* d_lse, void* d_logits,
+                                       int32_t d_dtype, int64_t ld_d, void* stream);
+
+/* Final RMSNorm + LM head + rdt_token_logprobs: scores hidden states with the
+ * head of rdt_fused_cross_entropy, without its gradients.
+ *   hn = bf16(RMSNorm(h, gamma_f)); z = hn W_lm^T in fp32, a chunk of rows at
+ *   a time (at most 1 GiB of logits, and at least 128 rows).
+ * h fp32 [tokens, H], gamma_f fp32 [H], w_lm bf16 [V, H]; the other arguments
+ * as in rdt_token_logprobs. ws: rdt_head_logprobs_workspace_bytes(cfg, tokens)
+ * bytes of scratch, 256-byte aligned (0 for an unsupported cfg). */
+size_t rdt_head_logprobs_workspace_bytes(const rdt_config* cfg, int32_t tokens);
+rdt_status rdt_head_logprobs(const rdt_config* cfg, int32_t tokens, const float* h,
+                             const float* gamma_f, const rdt_bf16* w_lm, float logit_scale,
+                             const int32_t* targets, float* logp, float* entropy, float* lse,
+                             int32_t top, int32_t* top_ids, float* top_logp, void* ws,
+                             size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * One clip and AdamW update of many tensors at once (rdt_sq_sum and
+ * rdt_adamw_step take 64 buffers and one flat buffer): parameters that live in
+ * allocations of their own, with a learning rate and weight decay each, fp32
+ * or bf16 gradients, and moments in 32 bits or in 8.
+ *
+ * tensors is a HOST array of `count` entries (0 to 1,000,000), read before the
+ * call returns. An entry with n == 0 is skipped. Device pointers 16-byte
+ * aligned, scales 4-byte aligned; no two entries may share memory that the
+ * call writes (entries whose w overlap are rejected).
+ *
+ * rdt_tensors_sq_sum: *sumsq = sum over all g of g^2, relative error
+ *   below 1e-12 where the squares lie in [1e-30, 1e38] (they are formed in
+ *   fp32, with their rounding errors kept); order of summation fixed by the
+ *   sizes. Only g and n of each entry are read. For
+ *   rdt_clip_scale. ws: rdt_tensors_sq_sum_workspace_bytes(tensors, count)
+ *   bytes, 8-byte aligned.
+ *
+ * rdt_tensors_adamw, step t (>= 1, or *step_dev), each operation rounded to
+ * fp32 in this order, so the result does not depend on the launch:
+ *   g' = g scale;  m = b1 m + (1 - b1) g';  v = b2 v + ((1 - b2) g') g'
+ *   w = w (1 - lr weight_decay) - (m / (sqrt(v) / sqrt(1 - b2^t) + eps)) (lr / (1 - b1^t))
+ * (1 - b1, 1 - b2, 1 / (1 - b1^t) and 1 / sqrt(1 - b2^t) are formed in double
+ * and rounded once; sqrt(v) is multiplied by the last.) w_bf16, where not
+ * null, receives the bf16 copy of w. scale, skip_flag and step_dev as in
+ * rdt_adamw_step; with *skip_flag != 0 nothing is written.
+ *
+ * state_bits 32: m and v are fp32 [n]; m_scale and v_scale are not read.
+ * state_bits 8: m and v are e4m3 codes, one byte per element; each run of 256
+ *   elements of a tensor (the last may be shorter) has one scale in m_scale
+ *   and v_scale, fp32 [ceil(n / 256)]. m = code m_scale. v's codes hold its
+ *   square root: sqrt(v) = code v_scale, whose range of exponents is half of
+ *   v's. A scale is the run's largest magnitude / 448, and a code is rounded
+ *   from value (1 / largest) 448; a run whose largest is below 2^-100 is
+ *   stored as zeros. The update uses the new m and v before they are rounded.
+ *   A sqrt(v) > 0 never becomes code 0, so no later step divides by eps alone.
+ *   Zeroed codes and scales are the initial state.
+ *   seed < 0: codes are rounded to nearest even. seed in [0, 2^32): rounded up
+ *   or down with the probability of the distance, from 16 bits that are a
+ *   function of (seed, step, index of the entry, index of the element): the
+ *   expected state is exact, so that changes smaller than half a code (a decay
+ *   of v by 1 - b2) are not lost. Ignored for 32 bits.
+ *   A NaN in g makes its element NaN; an infinite g makes its run of 256 NaN
+ *   (rdt_clip_scale's nonfinite flag, passed as skip_flag, prevents both).
+ * ------------------------------------------------------------------------- */
+typedef struct rdt_opt_tensor {
+  float* w;
+  const void* g;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  rdt_bf16* w_bf16;
+  int64_t n;
+  float lr;
+  float weight_decay;
+} rdt_opt_tensor;
+
+size_t rdt_tensors_sq_sum_workspace_bytes(const rdt_opt_tensor* tensors, int32_t count);
+rdt_status rdt_tensors_sq_sum(const rdt_opt_tensor* tensors, int32_t count, int32_t g_dtype,
+                              double* sumsq, void* ws, size_t ws_bytes, void* stream);
+rdt_status rdt_tensors_adamw(const rdt_opt_tensor* tensors, int32_t count, int32_t g_dtype,
+                             int32_t state_bits, int64_t seed, const float* scale,
+                             const int32_t* skip_flag, int32_t step, const int32_t* step_dev,
+                             float beta1, float beta2, float eps, void* stream);
+
 /* Thread-local description of the last failure on this thread ("" if none). */
 const char* rdt_last_error(void);
 

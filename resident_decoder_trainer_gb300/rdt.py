@@ -33,7 +33,13 @@ EXPORTS = (
     "rdt_lora_shadow_count", "rdt_lora_shadow", "rdt_nf4_saved_bytes", "rdt_nf4_workspace_bytes",
     "rdt_nf4_block_forward", "rdt_nf4_block_backward", "rdt_embedding_workspace_bytes",
     "rdt_embedding_forward", "rdt_embedding_backward", "rdt_step_advance", "rdt_wait_probe",
+    "rdt_token_logprobs", "rdt_token_logprobs_backward", "rdt_head_logprobs_workspace_bytes",
+    "rdt_head_logprobs", "rdt_tensors_sq_sum_workspace_bytes", "rdt_tensors_sq_sum",
+    "rdt_tensors_adamw",
 )
+RDT_MAX_TOP = 32  # alternatives per row of token_logprobs
+STATE_RUN = 256  # elements that share one scale of an 8-bit AdamW state
+_DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
 class RdtError(RuntimeError):
@@ -52,6 +58,15 @@ class Config(ctypes.Structure):
     def from_shape(cls, s) -> "Config":
         return cls(s.hidden, s.n_heads, s.n_kv_heads, s.head_dim, s.intermediate, s.vocab,
                    s.eps, s.theta)
+
+
+class OptTensor(ctypes.Structure):
+    """rdt_opt_tensor: one tensor of a rdt_tensors_* call."""
+    _fields_ = [("w", ctypes.c_void_p), ("g", ctypes.c_void_p), ("m", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("w_bf16", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("lr", ctypes.c_float),
+                ("weight_decay", ctypes.c_float)]
 
 
 def _load() -> ctypes.CDLL:
@@ -106,6 +121,14 @@ def _load() -> ctypes.CDLL:
                                         P]),
         "rdt_nf4_block_backward": (I32, [CP, I32, F32, I32, I32, P, P, P, P, P, P, SZ, P, P, P,
                                          P, P, SZ, P]),
+        "rdt_token_logprobs": (I32, [P, I32, I64, I32, I32, F32, P, P, P, P, P, I32, P, P, P]),
+        "rdt_token_logprobs_backward": (I32, [P, I32, I64, I32, I32, F32, P, P, P, P, P, P, P, I32,
+                                              I64, P]),
+        "rdt_head_logprobs_workspace_bytes": (SZ, [CP, I32]),
+        "rdt_head_logprobs": (I32, [CP, I32, P, P, P, F32, P, P, P, P, I32, P, P, P, SZ, P]),
+        "rdt_tensors_sq_sum_workspace_bytes": (SZ, [P, I32]),
+        "rdt_tensors_sq_sum": (I32, [P, I32, I32, P, P, SZ, P]),
+        "rdt_tensors_adamw": (I32, [P, I32, I32, I32, I64, P, P, I32, P, F32, F32, F32, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -264,6 +287,204 @@ def gemm_nf4(a, codes, scales, w_rows, w_cols, b_mn, c, a2=None, b2=None, split_
                               0 if b2 is None else b2.stride(0), k2, a.shape[0], _ptr(c),
                               c.stride(0), _ptr(split_ws),
                               0 if split_ws is None else split_ws.numel(), _stream(stream)))
+
+
+# ------------------------------------------------- token log probabilities
+def _here(t, what, dtypes, shape=None):
+    """Checks that t is a tensor the library may be handed: on the current device, of one of
+    the types, and, where a shape is given, of that shape and contiguous."""
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{what} must be on the current CUDA device")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{what} has type {t.dtype}")
+    if shape is not None and (tuple(t.shape) != shape or not t.is_contiguous()):
+        raise ValueError(f"{what} must be contiguous and of shape {shape}")
+
+
+_F32, _I32 = (torch.float32,), (torch.int32,)
+
+
+def _rows_of(logits, what):
+    _here(logits, what, _DTYPE)
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError(f"{what} must be [rows, vocab] with contiguous rows")
+    rows, vocab = logits.shape
+    return rows, vocab, logits.stride(0) if rows > 1 else vocab
+
+
+def token_logprobs(logits, targets=None, logp=None, entropy=None, lse=None, stats=None,
+                   top_ids=None, top_logp=None, logit_scale=1.0, stream=None):
+    """Log probabilities of given tokens, entropy, log-sum-exp and the most likely
+    alternatives of softmax(logit_scale logits), written to the tensors that are given
+    (rdt_token_logprobs). logits [rows, vocab] fp32, bf16 or fp16, any row stride;
+    targets int32 [rows]; logp, entropy, lse fp32 [rows]; stats fp32 [rows, 2] (for the
+    gradient); top_ids int32 and top_logp fp32 [rows, k], k <= RDT_MAX_TOP."""
+    rows, vocab, ld = _rows_of(logits, "logits")
+    for t, what, dtype in ((targets, "targets", _I32), (logp, "logp", _F32),
+                           (entropy, "entropy", _F32), (lse, "lse", _F32)):
+        if t is not None:
+            _here(t, what, dtype, (rows,))
+    if stats is not None:
+        _here(stats, "stats", _F32, (rows, 2))
+    top = 0 if top_ids is None else top_ids.shape[-1]
+    if top_ids is not None:
+        _here(top_ids, "top_ids", _I32, (rows, top))
+    if top_logp is not None:
+        _here(top_logp, "top_logp", _F32, (rows, top))
+    _check(lib().rdt_token_logprobs(_ptr(logits), _DTYPE[logits.dtype], ld, rows, vocab,
+                                    logit_scale, _ptr(targets), _ptr(logp), _ptr(entropy),
+                                    _ptr(lse), _ptr(stats), top, _ptr(top_ids), _ptr(top_logp),
+                                    _stream(stream)))
+
+
+def token_logprobs_backward(logits, targets, stats, d_logits, d_logp=None, entropy=None,
+                            d_entropy=None, d_lse=None, logit_scale=1.0, stream=None):
+    """Gradient of token_logprobs with respect to the logits, written to d_logits
+    (rdt_token_logprobs_backward): [rows, vocab] of any of the three types, or the logits
+    tensor itself. stats and entropy as token_logprobs wrote them; d_logp, d_entropy, d_lse
+    fp32 [rows] or None."""
+    rows, vocab, ld = _rows_of(logits, "logits")
+    d_rows, d_vocab, ld_d = _rows_of(d_logits, "d_logits")
+    if (d_rows, d_vocab) != (rows, vocab):
+        raise ValueError("d_logits must have the shape of logits")
+    _here(stats, "stats", _F32, (rows, 2))
+    for t, what, dtype in ((targets, "targets", _I32), (entropy, "entropy", _F32),
+                           (d_logp, "d_logp", _F32), (d_entropy, "d_entropy", _F32),
+                           (d_lse, "d_lse", _F32)):
+        if t is not None:
+            _here(t, what, dtype, (rows,))
+    _check(lib().rdt_token_logprobs_backward(_ptr(logits), _DTYPE[logits.dtype], ld, rows, vocab,
+                                             logit_scale, _ptr(targets), _ptr(stats),
+                                             _ptr(entropy), _ptr(d_logp), _ptr(d_entropy),
+                                             _ptr(d_lse), _ptr(d_logits),
+                                             _DTYPE[d_logits.dtype], ld_d, _stream(stream)))
+
+
+def head_logprobs_workspace_bytes(cfg: Config, tokens: int) -> int:
+    return lib().rdt_head_logprobs_workspace_bytes(ctypes.byref(cfg), int(tokens))
+
+
+def head_logprobs(cfg, h, gamma_f, w_lm, ws, targets=None, logp=None, entropy=None, lse=None,
+                  top_ids=None, top_logp=None, logit_scale=1.0, stream=None):
+    """token_logprobs of the LM head's logits for hidden states h fp32 [tokens, hidden]
+    (rdt_head_logprobs): final RMSNorm, head, scores; the logits are held a chunk of rows
+    at a time in ws."""
+    tokens = h.shape[0]
+    top = 0 if top_ids is None else top_ids.shape[-1]
+    _here(h, "h", _F32, (tokens, cfg.hidden))
+    _here(gamma_f, "gamma_f", _F32, (cfg.hidden,))
+    _here(w_lm, "w_lm", (torch.bfloat16,), (cfg.vocab, cfg.hidden))
+    for t, what, dtype in ((targets, "targets", _I32), (logp, "logp", _F32),
+                           (entropy, "entropy", _F32), (lse, "lse", _F32)):
+        if t is not None:
+            _here(t, what, dtype, (tokens,))
+    if top_ids is not None:
+        _here(top_ids, "top_ids", _I32, (tokens, top))
+    if top_logp is not None:
+        _here(top_logp, "top_logp", _F32, (tokens, top))
+    _check(lib().rdt_head_logprobs(ctypes.byref(cfg), tokens, _ptr(h), _ptr(gamma_f), _ptr(w_lm),
+                                   logit_scale, _ptr(targets), _ptr(logp), _ptr(entropy),
+                                   _ptr(lse), top, _ptr(top_ids), _ptr(top_logp), _ptr(ws),
+                                   ws.numel() * ws.element_size(), _stream(stream)))
+
+
+# ------------------------------------------------- many tensors: clip and AdamW
+class OptTensors:
+    """The tensors of one optimizer step (rdt_opt_tensor entries; lists of equal length).
+
+    g: gradients, all fp32 or all bf16. w, m, v: fp32 masters and AdamW moments, for
+    tensors_adamw; moments of uint8 or float8_e4m3fn are 8-bit states and need m_scale and
+    v_scale (fp32, one value per STATE_RUN elements, the last run may be shorter). w_bf16:
+    optional bf16 copies. lr, weight_decay: a number, or a list with one per tensor. The
+    tensors are held, not copied; all on one device and contiguous."""
+
+    def __init__(self, g, w=None, m=None, v=None, m_scale=None, v_scale=None, w_bf16=None, lr=0.0,
+                 weight_decay=0.0):
+        count = len(g)
+        columns = {"g": g, "w": w, "m": m, "v": v, "m_scale": m_scale, "v_scale": v_scale,
+                   "w_bf16": w_bf16}
+        self.tensors = {k: list(x) for k, x in columns.items() if x is not None}
+        self.g_dtype = g[0].dtype if count else torch.float32
+        moment = self.tensors["m"][0].dtype if "m" in self.tensors and count else torch.float32
+        self.state_bits = 32 if moment == torch.float32 else 8
+        types = {"g": self.g_dtype, "w": torch.float32, "m": moment, "v": moment,
+                 "m_scale": torch.float32, "v_scale": torch.float32, "w_bf16": torch.bfloat16}
+        if self.g_dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"gradients of type {self.g_dtype}")
+        if moment not in (torch.float32, torch.uint8, torch.float8_e4m3fn):
+            raise ValueError(f"moments of type {moment}")
+        self.device = g[0].get_device() if count else None
+        self.entries = (OptTensor * max(count, 1))()
+        self.count = count
+        for name, column in self.tensors.items():
+            if len(column) != count:
+                raise ValueError(f"{len(column)} tensors in {name}, {count} in g")
+            for e, t, gi in zip(self.entries, column, self.tensors["g"]):
+                n = gi.numel()
+                want = -(-n // STATE_RUN) if name.endswith("_scale") else n
+                if t.dtype != types[name] or t.numel() != want or not t.is_contiguous():
+                    raise ValueError(f"{name}: want {want} contiguous elements of {types[name]}, "
+                                     f"got {tuple(t.shape)} of {t.dtype}")
+                if not t.is_cuda or t.get_device() != self.device:
+                    raise ValueError(f"{name}: every tensor must be on one CUDA device")
+                setattr(e, name, t.data_ptr())
+        for e, gi in zip(self.entries, self.tensors["g"]):
+            e.n = gi.numel()
+        self.set_lr(lr)
+        self.set_weight_decay(weight_decay)
+
+    def _fill(self, field, values):
+        if not isinstance(values, (list, tuple)):
+            values = [values] * self.count
+        if len(values) != self.count:
+            raise ValueError(f"{len(values)} values of {field} for {self.count} tensors")
+        for e, x in zip(self.entries, values):
+            setattr(e, field, float(x))
+
+    def set_lr(self, lr):
+        """A number, or one per tensor; used by the calls that follow."""
+        self._fill("lr", lr)
+
+    def set_weight_decay(self, weight_decay):
+        self._fill("weight_decay", weight_decay)
+
+    def _on_device(self):
+        if self.device is not None and self.device != torch.cuda.current_device():
+            raise ValueError("the tensors are not on the current CUDA device")
+
+
+def tensors_sq_sum_workspace_bytes(tensors: OptTensors) -> int:
+    return lib().rdt_tensors_sq_sum_workspace_bytes(tensors.entries, tensors.count)
+
+
+def tensors_sq_sum(tensors: OptTensors, sumsq, ws, stream=None):
+    """sumsq (fp64 device scalar) = the squared sum of every gradient of the list."""
+    tensors._on_device()
+    _here(sumsq, "sumsq", (torch.float64,))
+    _here(ws, "ws", (ws.dtype,))
+    _check(lib().rdt_tensors_sq_sum(tensors.entries, tensors.count, _DTYPE[tensors.g_dtype],
+                                    _ptr(sumsq), _ptr(ws), ws.numel() * ws.element_size(),
+                                    _stream(stream)))
+
+
+def tensors_adamw(tensors: OptTensors, step, beta1, beta2, eps, scale=None, skip=None,
+                  step_dev=None, seed=None, stream=None):
+    """One AdamW step of every tensor of the list (rdt_tensors_adamw). step: host int
+    (>= 1), or None with step_dev: a device int32 holding it. seed: for 8-bit states, None
+    rounds them to nearest, a number in [0, 2^32) up or down at random."""
+    if "m" not in tensors.tensors and tensors.count:
+        raise ValueError("the list has no moments")
+    if seed is not None and not 0 <= seed < 1 << 32:
+        raise ValueError("seed must be in [0, 2^32)")
+    tensors._on_device()
+    for t, what, dtype in ((scale, "scale", _F32), (skip, "skip", _I32),
+                           (step_dev, "step_dev", _I32)):
+        if t is not None:
+            _here(t, what, dtype)
+    _check(lib().rdt_tensors_adamw(tensors.entries, tensors.count, _DTYPE[tensors.g_dtype],
+                                   tensors.state_bits, -1 if seed is None else seed, _ptr(scale),
+                                   _ptr(skip), int(step or 0), _ptr(step_dev), beta1, beta2, eps,
+                                   _stream(stream)))
 
 
 # ------------------------------------------------- NF4 + LoRA block
