@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cuda_fp8.h>
 #include <new>
+#include <type_traits>
 #include <utility>
 #include <vector>
 
@@ -53,33 +54,136 @@ __device__ __forceinline__ int owner_of(const Table& tab, int tile) {
   return lo;
 }
 
-template <bool kBf16>
-__device__ __forceinline__ void load8(const void* p, int64_t i, int have, float* x) {
+// A lane's eight elements of its warp's run are two groups of four, 128
+// elements apart, so that every access of the warp is one contiguous piece.
+// `have` counts the run's elements from the lane's first on; the masked forms
+// serve the run that ends a tensor.
+__device__ __forceinline__ int group_have(int have, int h) {
+  return have - 128 * h > 4 ? 4 : have - 128 * h;
+}
+
+template <bool kFull>
+__device__ __forceinline__ void load8(const float* p, int have, float* x) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    if constexpr (kBf16)
-      x[k] = k < have ? __bfloat162float(static_cast<const bf16*>(p)[i + k]) : 0.f;
-    else
-      x[k] = k < have ? static_cast<const float*>(p)[i + k] : 0.f;
+  for (int h = 0; h < 2; ++h) {
+    if (kFull) {
+      const float4 a = *reinterpret_cast<const float4*>(p + 128 * h);
+      x[4 * h] = a.x; x[4 * h + 1] = a.y; x[4 * h + 2] = a.z; x[4 * h + 3] = a.w;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[4 * h + k] = k < group_have(have, h) ? p[128 * h + k] : 0.f;
+    }
   }
+}
+template <bool kFull>
+__device__ __forceinline__ void load8(const bf16* p, int have, float* x) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (kFull) {
+      const uint2 a = *reinterpret_cast<const uint2*>(p + 128 * h);
+      x[4 * h] = bf16lo(a.x); x[4 * h + 1] = bf16hi(a.x);
+      x[4 * h + 2] = bf16lo(a.y); x[4 * h + 3] = bf16hi(a.y);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        x[4 * h + k] = k < group_have(have, h) ? bf16_to_f(p[128 * h + k]) : 0.f;
+    }
+  }
+}
+template <bool kFull>
+__device__ __forceinline__ void store8(float* p, int have, const float* x) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (kFull) {
+      *reinterpret_cast<float4*>(p + 128 * h) =
+          make_float4(x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k < group_have(have, h)) p[128 * h + k] = x[4 * h + k];
+    }
+  }
+}
+template <bool kFull>
+__device__ __forceinline__ void store8(bf16* p, int have, const float* x) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (kFull) {
+      *reinterpret_cast<uint2*>(p + 128 * h) =
+          make_uint2(pack_bf16x2(x[4 * h], x[4 * h + 1]), pack_bf16x2(x[4 * h + 2], x[4 * h + 3]));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k < group_have(have, h)) p[128 * h + k] = __float2bfloat16_rn(x[4 * h + k]);
+    }
+  }
+}
+// Eight one-byte codes, four to a word.
+template <bool kFull>
+__device__ __forceinline__ void load8(const uint8_t* p, int have, uint32_t* c) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (kFull) {
+      c[h] = *reinterpret_cast<const uint32_t*>(p + 128 * h);
+    } else {
+      c[h] = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k < group_have(have, h)) c[h] |= static_cast<uint32_t>(p[128 * h + k]) << (8 * k);
+    }
+  }
+}
+template <bool kFull>
+__device__ __forceinline__ void store8(uint8_t* p, int have, const uint32_t* c) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (kFull) {
+      *reinterpret_cast<uint32_t*>(p + 128 * h) = c[h];
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k < group_have(have, h)) p[128 * h + k] = static_cast<uint8_t>(c[h] >> (8 * k));
+    }
+  }
+}
+
+// hi + lo += x x, with the rounding errors of the product and of the sum kept
+// in lo: a sum of n squares is right to about n 2^-48. (fp64 has 1/64 of
+// fp32's rate here: the same sum in fp64 took 1.82 ms for 490 M fp32 values.)
+__device__ __forceinline__ void add_square(float x, float& hi, float& lo) {
+  const float p = __fmul_rn(x, x);
+  const float e = __fmaf_rn(x, x, -p);
+  const float t = __fadd_rn(hi, p);
+  const float b = __fsub_rn(t, hi);
+  const float c = __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(p, b));
+  hi = t;
+  lo = __fadd_rn(lo, __fadd_rn(c, e));
 }
 
 template <bool kBf16>
 __global__ void __launch_bounds__(kThreads) tensors_sq_sum_kernel(
     const __grid_constant__ Table tab, int tiles, double* __restrict__ partials) {
   __shared__ double red[kThreads / 32];
-  double acc = 0.0;
+  using G = typename std::conditional<kBf16, bf16, float>::type;
+  const int at = (threadIdx.x >> 5) * kRun + (threadIdx.x & 31) * 4;
+  float hi[4] = {0.f, 0.f, 0.f, 0.f}, lo[4] = {0.f, 0.f, 0.f, 0.f};
   for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     const int o = owner_of(tab, tile);
     const Tensor& t = tab.t[o];
-    const int64_t i =
-        static_cast<int64_t>(tile - (o ? tab.end[o - 1] : 0)) * kTile + threadIdx.x * 8;
-    if (i >= t.n) continue;
+    const int64_t first = static_cast<int64_t>(tile - (o ? tab.end[o - 1] : 0)) * kTile;
+    const G* g = static_cast<const G*>(t.g) + first + at;
+    const int64_t left = t.n - first;
     float x[8];
-    load8<kBf16>(t.g, i, static_cast<int>(min(t.n - i, static_cast<int64_t>(8))), x);
+    if (left >= kTile)
+      load8<true>(g, 0, x);
+    else
+      load8<false>(g, static_cast<int>(left) - at, x);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) acc += static_cast<double>(x[k]) * x[k];
+    for (int k = 0; k < 8; ++k) add_square(x[k], hi[k & 3], lo[k & 3]);
   }
+  double acc = 0.0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) acc += static_cast<double>(hi[k]) + static_cast<double>(lo[k]);
   acc = warp_sum_d(acc);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = acc;
   __syncthreads();
@@ -118,11 +222,21 @@ constexpr float kE4m3Max = 448.f;
 constexpr float kE4m3Tiny = 0x1p-9f;
 constexpr float kAbsmaxTiny = 0x1p-100f;
 
-__device__ __forceinline__ float e4m3_value(uint8_t c) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
+// Four e4m3 codes of a word to fp32 and back (round to nearest even, saturating).
+__device__ __forceinline__ void e4m3_decode4(uint32_t c, float* x) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c >> (16 * h)),
+                                                     __NV_E4M3);
+    const float2 f = __half22float2(__half2(r));
+    x[2 * h] = f.x;
+    x[2 * h + 1] = f.y;
+  }
 }
-__device__ __forceinline__ uint8_t e4m3_code(float x) {
-  return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
+__device__ __forceinline__ uint32_t e4m3_encode4(const float* x) {
+  const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(x[2], x[3]), __NV_SATFINITE, __NV_E4M3);
+  return a | (b << 16);
 }
 
 // A 32-bit number from another, each bit of the result depending on every bit
@@ -158,9 +272,89 @@ __device__ __forceinline__ void run_scale(float big, float& scale, float& unit) 
   unit = there ? __fmul_rn(__frcp_rn(big), kE4m3Max) : 0.f;
 }
 
-template <int kBits, bool kBf16>
+// One run of 256 elements of tensor t, `first` its first element's index; the
+// lane's own elements start at first + 4 lane.
+template <int kBits, bool kBf16, bool kRandom, bool kFull>
+__device__ __forceinline__ void adamw_run(const Tensor& t, int64_t first, const AdamArgs& p,
+                                          float sc, float inv_bc1, float inv_root_bc2,
+                                          uint32_t key) {
+  using G = typename std::conditional<kBf16, bf16, float>::type;
+  const int lane = threadIdx.x & 31;
+  const int64_t i = first + lane * 4;
+  const int have = kFull ? kRun : static_cast<int>(t.n - i);
+  const int64_t run = first / kRun;
+  float w[8], g[8], m[8], r[8];
+  load8<kFull>(t.w + i, have, w);
+  load8<kFull>(static_cast<const G*>(t.g) + i, have, g);
+  if constexpr (kBits == 32) {
+    load8<kFull>(static_cast<const float*>(t.m) + i, have, m);
+    load8<kFull>(static_cast<const float*>(t.v) + i, have, r);
+  } else {
+    uint32_t mc[2], vc[2];
+    load8<kFull>(static_cast<const uint8_t*>(t.m) + i, have, mc);
+    load8<kFull>(static_cast<const uint8_t*>(t.v) + i, have, vc);
+    const float ms = t.m_scale[run], vs = t.v_scale[run];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      e4m3_decode4(mc[h], m + 4 * h);
+      e4m3_decode4(vc[h], r + 4 * h);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      m[k] = __fmul_rn(m[k], ms);
+      r[k] = __fmul_rn(r[k], vs);
+      r[k] = __fmul_rn(r[k], r[k]);
+    }
+  }
+  const float rate = __fmul_rn(t.lr, inv_bc1), keep = __fsub_rn(1.f, __fmul_rn(t.lr, t.wd));
+  float big_m = 0.f, big_r = 0.f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float gs = __fmul_rn(g[k], sc);
+    m[k] = __fadd_rn(__fmul_rn(m[k], p.b1), __fmul_rn(gs, p.omb1));
+    const float v = __fadd_rn(__fmul_rn(r[k], p.b2), __fmul_rn(__fmul_rn(gs, p.omb2), gs));
+    const float root = __fsqrt_rn(v);
+    const float u = __fdiv_rn(m[k], __fadd_rn(__fmul_rn(root, inv_root_bc2), p.eps));
+    w[k] = __fsub_rn(__fmul_rn(w[k], keep), __fmul_rn(u, rate));
+    r[k] = kBits == 32 ? v : root;
+    big_m = fmaxf(big_m, fabsf(m[k]));
+    big_r = fmaxf(big_r, root);
+  }
+  store8<kFull>(t.w + i, have, w);
+  if (t.wb) store8<kFull>(t.wb + i, have, w);
+  if constexpr (kBits == 32) {
+    store8<kFull>(static_cast<float*>(t.m) + i, have, m);
+    store8<kFull>(static_cast<float*>(t.v) + i, have, r);
+  } else {
+    float ms, vs, um, uv;
+    run_scale(warp_max(big_m), ms, um);
+    run_scale(warp_max(big_r), vs, uv);
+    if (lane == 0) {
+      t.m_scale[run] = ms;
+      t.v_scale[run] = vs;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float qm = __fmul_rn(m[k], um), qr = __fmul_rn(r[k], uv);
+      if constexpr (kRandom) {
+        const uint32_t x = mix(static_cast<uint32_t>(i + (k & 3) + 32 * (k & 4)) ^ key);
+        qm = qm != qm ? qm : round_random(fminf(fmaxf(qm, -kE4m3Max), kE4m3Max), x & 0xffffu);
+        qr = qr != qr ? qr : round_random(fminf(qr, kE4m3Max), x >> 16);
+      }
+      if (r[k] > 0.f && uv > 0.f && qr < kE4m3Tiny) qr = kE4m3Tiny;
+      m[k] = qm;
+      r[k] = qr;
+    }
+    uint32_t mc[2] = {e4m3_encode4(m), e4m3_encode4(m + 4)};
+    uint32_t vc[2] = {e4m3_encode4(r), e4m3_encode4(r + 4)};
+    store8<kFull>(static_cast<uint8_t*>(t.m) + i, have, mc);
+    store8<kFull>(static_cast<uint8_t*>(t.v) + i, have, vc);
+  }
+}
+
+template <int kBits, bool kBf16, bool kRandom>
 __global__ void __launch_bounds__(kThreads) tensors_adamw_kernel(
-    const __grid_constant__ Table tab, int tiles, const AdamArgs p, bool random) {
+    const __grid_constant__ Table tab, int tiles, const AdamArgs p) {
   if (p.skip && *p.skip) return;
   const float sc = p.scale ? *p.scale : 1.f;
   float inv_bc1 = p.inv_bc1, inv_root_bc2 = p.inv_root_bc2;
@@ -175,73 +369,13 @@ __global__ void __launch_bounds__(kThreads) tensors_adamw_kernel(
   for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     const int o = owner_of(tab, tile);
     const Tensor& t = tab.t[o];
-    const int64_t i =
-        static_cast<int64_t>(tile - (o ? tab.end[o - 1] : 0)) * kTile + threadIdx.x * 8;
-    if (i - (threadIdx.x & 31) * 8 >= t.n) continue;  // the whole warp's run
-    const int have = static_cast<int>(max(min(t.n - i, static_cast<int64_t>(8)), static_cast<int64_t>(0)));
-    const int64_t run = i / kRun;
-    float w[8], g[8], m[8], r[8];
-    load8<false>(t.w, i, have, w);
-    load8<kBf16>(t.g, i, have, g);
-    if constexpr (kBits == 32) {
-      load8<false>(t.m, i, have, m);
-      load8<false>(t.v, i, have, r);
-    } else {
-      const float ms = t.m_scale[run], vs = t.v_scale[run];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        m[k] = k < have ? __fmul_rn(e4m3_value(static_cast<uint8_t*>(t.m)[i + k]), ms) : 0.f;
-        const float q = k < have ? __fmul_rn(e4m3_value(static_cast<uint8_t*>(t.v)[i + k]), vs) : 0.f;
-        r[k] = __fmul_rn(q, q);
-      }
-    }
-    const float rate = __fmul_rn(t.lr, inv_bc1), keep = __fsub_rn(1.f, __fmul_rn(t.lr, t.wd));
-    float big_m = 0.f, big_r = 0.f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float gs = __fmul_rn(g[k], sc);
-      m[k] = __fadd_rn(__fmul_rn(m[k], p.b1), __fmul_rn(gs, p.omb1));
-      const float v = __fadd_rn(__fmul_rn(r[k], p.b2), __fmul_rn(__fmul_rn(gs, p.omb2), gs));
-      const float root = __fsqrt_rn(v);
-      const float u = __fdiv_rn(m[k], __fadd_rn(__fmul_rn(root, inv_root_bc2), p.eps));
-      w[k] = __fsub_rn(__fmul_rn(w[k], keep), __fmul_rn(u, rate));
-      r[k] = kBits == 32 ? v : root;
-      big_m = fmaxf(big_m, fabsf(m[k]));
-      big_r = fmaxf(big_r, root);
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      if (k >= have) continue;
-      t.w[i + k] = w[k];
-      if (t.wb) t.wb[i + k] = __float2bfloat16_rn(w[k]);
-      if constexpr (kBits == 32) {
-        static_cast<float*>(t.m)[i + k] = m[k];
-        static_cast<float*>(t.v)[i + k] = r[k];
-      }
-    }
-    if constexpr (kBits == 8) {
-      float ms, vs, um, uv;
-      run_scale(warp_max(big_m), ms, um);
-      run_scale(warp_max(big_r), vs, uv);
-      if ((threadIdx.x & 31) == 0) {
-        t.m_scale[run] = ms;
-        t.v_scale[run] = vs;
-      }
-      const uint32_t key = mix(key0 + o) ^ static_cast<uint32_t>(i >> 32) * 0x9E3779B1u;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (k >= have) continue;
-        float qm = __fmul_rn(m[k], um), qr = __fmul_rn(r[k], uv);
-        if (random) {
-          const uint32_t x = mix(static_cast<uint32_t>(i + k) ^ key);
-          qm = qm != qm ? qm : round_random(fminf(fmaxf(qm, -kE4m3Max), kE4m3Max), x & 0xffffu);
-          qr = qr != qr ? qr : round_random(fminf(qr, kE4m3Max), x >> 16);
-        }
-        if (r[k] > 0.f && uv > 0.f && qr < kE4m3Tiny) qr = kE4m3Tiny;
-        static_cast<uint8_t*>(t.m)[i + k] = e4m3_code(qm);
-        static_cast<uint8_t*>(t.v)[i + k] = e4m3_code(qr);
-      }
-    }
+    const int64_t first = static_cast<int64_t>(tile - (o ? tab.end[o - 1] : 0)) * kTile +
+                          (threadIdx.x >> 5) * kRun;
+    const uint32_t key = mix(key0 + o) ^ static_cast<uint32_t>(first >> 32) * 0x9E3779B1u;
+    if (first + kRun <= t.n)
+      adamw_run<kBits, kBf16, kRandom, true>(t, first, p, sc, inv_bc1, inv_root_bc2, key);
+    else if (first < t.n)
+      adamw_run<kBits, kBf16, kRandom, false>(t, first, p, sc, inv_bc1, inv_root_bc2, key);
   }
 }
 
@@ -413,17 +547,14 @@ rdt_status rdt_tensors_adamw(const rdt_opt_tensor* tensors, int32_t count, int32
     if (tiles == 0) return cudaSuccess;
     const int blocks = static_cast<int>(std::min<int64_t>(tiles, 8LL * num_sms()));
     note_launch();
-    if (state_bits == 32) {
-      if (g_dtype == RDT_BF16)
-        tensors_adamw_kernel<32, true><<<blocks, kThreads, 0, s>>>(tab, tiles, a, random);
-      else
-        tensors_adamw_kernel<32, false><<<blocks, kThreads, 0, s>>>(tab, tiles, a, random);
-    } else {
-      if (g_dtype == RDT_BF16)
-        tensors_adamw_kernel<8, true><<<blocks, kThreads, 0, s>>>(tab, tiles, a, random);
-      else
-        tensors_adamw_kernel<8, false><<<blocks, kThreads, 0, s>>>(tab, tiles, a, random);
-    }
+    const bool half = g_dtype == RDT_BF16;
+    auto kernel = state_bits == 32 ? (half ? tensors_adamw_kernel<32, true, false>
+                                           : tensors_adamw_kernel<32, false, false>)
+                  : random ? (half ? tensors_adamw_kernel<8, true, true>
+                                   : tensors_adamw_kernel<8, false, true>)
+                           : (half ? tensors_adamw_kernel<8, true, false>
+                                   : tensors_adamw_kernel<8, false, false>);
+    kernel<<<blocks, kThreads, 0, s>>>(tab, tiles, a);
     return cudaGetLastError();
   }));
 }
