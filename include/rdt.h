@@ -404,9 +404,9 @@ rdt_status rdt_embedding_backward(const int32_t* ids, int32_t tokens, const floa
  * distillation, policy training, sampling reports.
  *
  * A row z of `vocab` logits stands for the distribution p = softmax(logit_scale
- * z); logit_scale is 1 / temperature, finite and > 0. Logits are fp32, bf16 or
+ * z); logit_scale is 1 / temperature, in (0, 1e30]. Logits are fp32, bf16 or
  * fp16, [rows, vocab] with row stride ld elements (ld >= vocab, any alignment
- * an element has); all arithmetic is fp32.
+ * an element has), vocab in [1, 2^30]; all arithmetic is fp32.
  *
  * rdt_token_logprobs, for each row t:
  *   logp[t]     = ln p[targets[t]]

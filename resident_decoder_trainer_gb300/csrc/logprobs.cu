@@ -14,8 +14,6 @@ namespace rdt {
 
 namespace {
 
-constexpr int kThreads = 256;
-
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(bf16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
@@ -23,6 +21,26 @@ template <typename T> __device__ __forceinline__ T from_f(float x);
 template <> __device__ __forceinline__ float from_f<float>(float x) { return x; }
 template <> __device__ __forceinline__ bf16 from_f<bf16>(float x) { return __float2bfloat16_rn(x); }
 template <> __device__ __forceinline__ __half from_f<__half>(float x) { return __float2half_rn(x); }
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.693147180559945309417f;
+// Exponents of 2 are kept above this (2^-1000 is 0 in fp32): -inf would make
+// the products p ln p of masked tokens NaN.
+constexpr float kLowest = -1000.f;
+
+// 2^x, relative error below 2^-21, 0 for x < -126.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// max(x, kLowest), NaN if x is (fmaxf would drop it).
+__device__ __forceinline__ float keep_finite(float x) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(kLowest));
+  return r;
+}
+__device__ __forceinline__ float nan_f() { return __int_as_float(0x7fffffff); }
 
 // Larger value first, equal values in order of index: a whole number whose
 // order is that order; 0 for -inf (never an alternative). NaN must not come here.
@@ -35,6 +53,170 @@ __device__ __forceinline__ uint64_t order_key(float z, uint32_t idx) {
 __device__ __forceinline__ float key_value(uint64_t key) {
   const uint32_t b = static_cast<uint32_t>(key >> 32);
   return __uint_as_float((b & 0x80000000u) ? (b & 0x7fffffffu) : ~b);
+}
+__device__ __forceinline__ uint32_t key_index(uint64_t key) {
+  return 0xffffffffu - static_cast<uint32_t>(key);
+}
+
+// ------------------------------------------------------------ 16-byte vectors
+// kPer elements of a row, as loaded; filled with -inf where the row has none.
+template <typename T> struct Vec;
+template <> struct Vec<float> {
+  static constexpr int kPer = 4;
+  static constexpr uint32_t kNone = 0xff800000u;
+  static __device__ __forceinline__ void unpack(const uint4& r, float* x) {
+    x[0] = __uint_as_float(r.x); x[1] = __uint_as_float(r.y);
+    x[2] = __uint_as_float(r.z); x[3] = __uint_as_float(r.w);
+  }
+  static __device__ __forceinline__ float max(const uint4& r) {
+    return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)),
+                 fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+  }
+};
+template <> struct Vec<bf16> {
+  static constexpr int kPer = 8;
+  static constexpr uint32_t kNone = 0xff80ff80u;
+  static __device__ __forceinline__ void unpack(const uint4& r, float* x) {
+    x[0] = bf16lo(r.x); x[1] = bf16hi(r.x); x[2] = bf16lo(r.y); x[3] = bf16hi(r.y);
+    x[4] = bf16lo(r.z); x[5] = bf16hi(r.z); x[6] = bf16lo(r.w); x[7] = bf16hi(r.w);
+  }
+  static __device__ __forceinline__ float max(const uint4& r) {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&r);
+    const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+};
+template <> struct Vec<__half> {
+  static constexpr int kPer = 8;
+  static constexpr uint32_t kNone = 0xfc00fc00u;
+  static __device__ __forceinline__ void unpack(const uint4& r, float* x) {
+    const __half2* h = reinterpret_cast<const __half2*>(&r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(h[i]);
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    }
+  }
+  static __device__ __forceinline__ float max(const uint4& r) {
+    const __half2* h = reinterpret_cast<const __half2*>(&r);
+    const __half2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+};
+
+// A row as 16-byte vectors of memory: vector v holds elements v kPer - head to
+// that + kPer - 1. The first and the last may reach outside the row; only
+// their elements inside it are read.
+template <typename T>
+struct Row {
+  const T* z;      // element 0
+  const uint4* v0; // the vector that holds it
+  int head, vocab;
+  int vectors;
+  __device__ __forceinline__ Row(const T* row, int n) : z(row), vocab(n) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row);
+    v0 = reinterpret_cast<const uint4*>(at & ~static_cast<uintptr_t>(15));
+    head = static_cast<int>((at & 15) / sizeof(T));
+    vectors = static_cast<int>((static_cast<int64_t>(head) + n + Vec<T>::kPer - 1) / Vec<T>::kPer);
+  }
+  __device__ __forceinline__ int first_of(int v) const { return v * Vec<T>::kPer - head; }
+  // v in [0, vectors)
+  __device__ __forceinline__ uint4 load(int v) const {
+    const int j = first_of(v);
+    if (j >= 0 && j <= vocab - Vec<T>::kPer) return __ldg(v0 + v);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        w[i] = static_cast<unsigned>(j + i) < static_cast<unsigned>(vocab)
+                   ? __float_as_uint(to_f(z[j + i])) : Vec<T>::kNone;
+      } else {
+        const uint16_t* h = reinterpret_cast<const uint16_t*>(z);
+        const int e = j + 2 * i;
+        const uint32_t none = Vec<T>::kNone & 0xffffu;
+        const uint32_t lo = static_cast<unsigned>(e) < static_cast<unsigned>(vocab) ? h[e] : none;
+        const uint32_t hi =
+            static_cast<unsigned>(e + 1) < static_cast<unsigned>(vocab) ? h[e + 1] : none;
+        w[i] = lo | (hi << 16);
+      }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  static __device__ __forceinline__ uint4 none() {
+    return make_uint4(Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone);
+  }
+};
+
+// ------------------------------------------------------------ running softmax
+// Of a set of logits z, with c = logit_scale log2 e and t = c (z - m):
+// m the maximum (-inf for none; a NaN is not seen), s0 = sum 2^t, s1 = sum
+// 2^t t. A NaN or +inf in the set makes s0 NaN.
+struct Sums {
+  float m, s0, s1;
+};
+__device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
+// The same sums with the larger reference m.
+__device__ __forceinline__ void rebase(Sums& a, float m, float c) {
+  const float t = keep_finite((a.m - base_of(m)) * c);
+  const float f = exp2_fast(t);
+  a.s1 = f * fmaf(t, a.s0, a.s1);
+  a.s0 = f * a.s0;
+  a.m = m;
+}
+__device__ __forceinline__ Sums join(Sums a, Sums b, float c) {
+  const float m = fmaxf(a.m, b.m);
+  rebase(a, m, c);
+  rebase(b, m, c);
+  return Sums{m, a.s0 + b.s0, a.s1 + b.s1};
+}
+
+// ------------------------------------------------------- lists of 32, by lane
+// A warp holds a list of 32 keys, one per lane, largest in lane 0.
+constexpr unsigned kAll = 0xffffffffu;
+__device__ __forceinline__ uint64_t keep_of(uint64_t a, uint64_t b, bool larger) {
+  return (a > b) == larger ? a : b;
+}
+// Any 32 keys into order (bitonic: runs of 2, 4, ... 32).
+__device__ __forceinline__ uint64_t sort32(uint64_t k) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int run = 2; run <= 32; run <<= 1) {
+#pragma unroll
+    for (int step = run >> 1; step > 0; step >>= 1) {
+      const uint64_t other = __shfl_xor_sync(kAll, k, step);
+      const bool down = (lane & run) == 0 || run == 32;
+      k = keep_of(k, other, ((lane & step) == 0) == down);
+    }
+  }
+  return k;
+}
+// The 32 largest of two ordered lists, in order; `back` holds the second one's
+// keys in reverse (its lane i the key of place 31 - i).
+__device__ __forceinline__ uint64_t merge32(uint64_t k, uint64_t back) {
+  const int lane = threadIdx.x & 31;
+  k = k > back ? k : back;
+#pragma unroll
+  for (int step = 16; step > 0; step >>= 1) {
+    const uint64_t other = __shfl_xor_sync(kAll, k, step);
+    k = keep_of(k, other, (lane & step) == 0);
+  }
+  return k;
+}
+// Puts one key (the same in every lane, in the list nowhere yet) in its place.
+__device__ __forceinline__ uint64_t insert32(uint64_t k, uint64_t x) {
+  const int lane = threadIdx.x & 31;
+  const int place = __popc(__ballot_sync(kAll, k > x));
+  const uint64_t up = __shfl_up_sync(kAll, k, 1);
+  return lane < place ? k : lane == place ? x : up;
+}
+
+// Stores to shared memory of a CTA of the cluster (address from mapa_shared).
+__device__ __forceinline__ void st_cluster_f32(uint32_t at, float x) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(x) : "memory");
+}
+__device__ __forceinline__ void st_cluster_u64(uint32_t at, uint64_t x) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(x) : "memory");
 }
 
 struct LogprobArgs {
@@ -50,93 +232,249 @@ struct LogprobArgs {
   float* top_logp;
 };
 
-template <typename V, typename F>
-__device__ __forceinline__ V block_reduce(V v, V* red, F f) {
+constexpr int kMaxSplit = 8;  // CTAs that share a row (a cluster of the portable size)
+constexpr int kUnroll = 4;    // vectors a thread has under way
+
+template <int kWarps>
+struct Shared {
+  Sums warp_sums[kWarps];
+  Sums part[kMaxSplit];                  // of the cluster's CTAs, in its first CTA
+  unsigned long long list[kWarps][32];
+  unsigned long long parts[kMaxSplit][32];
+};
+
+// The CTA's 32 largest of its warps' lists, in every thread of warp 0 and in
+// list[0]. All threads call it.
+template <int kWarps>
+__device__ __forceinline__ uint64_t join_lists(uint64_t k, unsigned long long (*list)[32]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  list[warp][lane] = k;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
+  for (int step = kWarps / 2; step > 0; step >>= 1) {
+    __syncthreads();
+    if (warp < step) {
+      k = merge32(k, list[warp + step][31 - lane]);
+      list[warp][lane] = k;
+    }
+  }
   __syncthreads();
-  if (lane == 0) red[warp] = v;
-  __syncthreads();
-  v = red[0];
-  for (int w = 1; w < kThreads / 32; ++w) v = f(v, red[w]);
-  return v;
+  return k;
 }
 
-// One CTA per row: maximum, then sums, then one pass per alternative.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a) {
-  __shared__ float redf[kThreads / 32];
-  __shared__ unsigned long long redk[kThreads / 32];
-  const int row = blockIdx.x, tid = threadIdx.x;
-  const T* z = static_cast<const T*>(a.logits) + static_cast<int64_t>(row) * a.ld;
-  const int target = a.targets ? a.targets[row] : 0;
+// A row (or, in a cluster of `split` CTAs, 1 / split of it) per CTA, read once.
+// Each thread keeps the running maximum and sums of its vectors in registers;
+// warps, the CTA and the cluster join them in a fixed order.
+//
+// Alternatives need no work in the loop: the `top`-th largest of the threads'
+// maxima is a lower bound of the row's `top`-th largest logit, and the logits
+// above it belong to the `top` threads with the largest maxima. Only those
+// threads' vectors (top / threads of the row, from L2) are read again and
+// filtered by the bound into sorted lists of 32, one key per lane.
+template <typename T, int kThreads, bool kTop>
+__global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a, int split) {
+  constexpr int kWarps = kThreads / 32;
+  constexpr int kPer = Vec<T>::kPer;
+  __shared__ Shared<kWarps> sh;
+  const int row_i = split == 1 ? blockIdx.x : blockIdx.x / split;
+  const int part = split == 1 ? 0 : blockIdx.x % split;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int target = a.targets ? a.targets[row_i] : 0;
   const float inf = INFINITY;
-  float m = -inf, bad = 0.f, s0 = 0.f, s1 = 0.f;
-  const bool scored = target >= 0;
-  if (scored) {
-    for (int j = tid; j < a.vocab; j += kThreads) {
-      const float x = to_f(z[j]);
-      m = fmaxf(m, x);
-      if (!(x < inf)) bad = 1.f;
+  if (target < 0) {  // not scored (the same in every CTA of the cluster)
+    if (part == 0 && tid == 0) {
+      if (a.logp) a.logp[row_i] = 0.f;
+      if (a.entropy) a.entropy[row_i] = 0.f;
+      if (a.lse) a.lse[row_i] = 0.f;
+      if (a.stats) a.stats[row_i] = make_float2(0.f, 0.f);
     }
-    auto fmx = [](float x, float y) { return fmaxf(x, y); };
-    auto fad = [](float x, float y) { return x + y; };
-    m = block_reduce(m, redf, fmx);
-    bad = block_reduce(bad, redf, fmx);
-    if (bad == 0.f && m > -inf) {
-      for (int j = tid; j < a.vocab; j += kThreads) {
-        const float d = (to_f(z[j]) - m) * a.scale;
-        const float e = expf(d);
-        s0 += e;
-        s1 += e > 0.f ? e * d : 0.f;
+    if (kTop && part == 0 && tid < a.top) {
+      a.top_ids[static_cast<int64_t>(row_i) * a.top + tid] = -1;
+      a.top_logp[static_cast<int64_t>(row_i) * a.top + tid] = 0.f;
+    }
+    return;
+  }
+  // shared memory of another CTA may be written once that CTA runs: every CTA says so here and
+  // waits for the others only before its stores
+  if (split > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+  const Row<T> row(static_cast<const T*>(a.logits) + static_cast<int64_t>(row_i) * a.ld, a.vocab);
+  const int v0 = static_cast<int>(static_cast<int64_t>(row.vectors) * part / split);
+  const int v1 = static_cast<int>(static_cast<int64_t>(row.vectors) * (part + 1) / split);
+  const float c = a.scale * kLog2e;
+
+  Sums s{-inf, 0.f, 0.f};
+  int best_at = v0 + tid;  // the first vector of the group that brought the maximum
+  for (int v = v0 + tid; v < v1; v += kUnroll * kThreads) {
+    uint4 r[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      r[u] = v + u * kThreads < v1 ? row.load(v + u * kThreads) : Row<T>::none();
+    float m = Vec<T>::max(r[0]);
+#pragma unroll
+    for (int u = 1; u < kUnroll; ++u) m = fmaxf(m, Vec<T>::max(r[u]));
+    if (m > s.m) {
+      rebase(s, m, c);
+      if (kTop) best_at = v;
+    }
+    const float base = base_of(s.m);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      float x[kPer];
+      Vec<T>::unpack(r[u], x);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const float t = keep_finite((x[i] - base) * c);
+        const float e = exp2_fast(t);
+        s.s0 += e;
+        s.s1 = fmaf(e, t, s.s1);
       }
-      s0 = block_reduce(s0, redf, fad);
-      s1 = block_reduce(s1, redf, fad);
     }
   }
-  const bool live = scored && bad == 0.f, some = live && m > -inf;
-  const float log_sum = some ? logf(s0) : 0.f;
-  const float nan = __int_as_float(0x7fffffff);
-  if (tid == 0) {
-    const float dead = scored ? nan : 0.f;  // for rows that are not live
+
+  Sums all = s;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const Sums other{__shfl_xor_sync(kAll, all.m, o), __shfl_xor_sync(kAll, all.s0, o),
+                     __shfl_xor_sync(kAll, all.s1, o)};
+    all = lane & o ? join(other, all, c) : join(all, other, c);
+  }
+  if (lane == 0) sh.warp_sums[warp] = all;
+  __syncthreads();
+  all = sh.warp_sums[0];
+  for (int w = 1; w < kWarps; ++w) all = join(all, sh.warp_sums[w], c);
+
+  uint64_t list = 0;
+  if (kTop && all.s0 == all.s0 && all.m > -inf) {  // the same in every thread
+    // this thread's maximum and its lowest index
+    uint64_t mine = 0;
+    if (s.m > -inf) {
+      for (int u = 0; u < kUnroll && mine == 0; ++u) {
+        const int v = best_at + u * kThreads;
+        if (v >= v1) break;
+        float x[kPer];
+        Vec<T>::unpack(row.load(v), x);
+#pragma unroll
+        for (int i = kPer - 1; i >= 0; --i)
+          if (x[i] == s.m) mine = order_key(x[i], row.first_of(v) + i);
+      }
+    }
+    join_lists<kWarps>(sort32(mine), sh.list);
+    const uint64_t leader = sh.list[0][lane];  // lane i: the i-th largest of the maxima
+    const uint64_t bound = __shfl_sync(kAll, leader, a.top - 1);
+    const int leaders = __popc(__ballot_sync(kAll, lane < a.top && leader != 0));
+    __syncthreads();
+    const int turns = (v1 - v0 + kThreads - 1) / kThreads;
+    for (int i = warp; i < leaders; i += kWarps) {
+      const uint64_t key = __shfl_sync(kAll, leader, i);
+      const int v = (static_cast<int>(key_index(key)) + row.head) / kPer;
+      const int owner = (v - v0) % kThreads;
+      for (int n = 0; n < turns; n += 32) {
+        const int at = v0 + owner + (n + lane) * kThreads;
+        float x[kPer];
+        Vec<T>::unpack(n + lane < turns && at < v1 ? row.load(at) : Row<T>::none(), x);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+          const uint64_t k = order_key(x[e], row.first_of(at) + e);
+          const uint64_t least = __shfl_sync(kAll, list, a.top - 1);
+          unsigned who = __ballot_sync(kAll, k != 0 && k >= bound && k > least);
+          while (who) {
+            const int l = __ffs(who) - 1;
+            who &= who - 1;
+            list = insert32(list, __shfl_sync(kAll, k, l));
+          }
+        }
+      }
+    }
+    list = join_lists<kWarps>(list, sh.list);
+  }
+
+  if (split > 1) {
+    // every part to the cluster's first CTA; it joins them in order
+    asm volatile("barrier.cluster.wait;" ::: "memory");
+    if (warp == 0) {
+      const uint32_t p = mapa_shared(smem_u32(&sh.part[part]), 0);
+      if (lane == 0) {
+        st_cluster_f32(p, all.m);
+        st_cluster_f32(p + 4, all.s0);
+        st_cluster_f32(p + 8, all.s1);
+      }
+      if (kTop) st_cluster_u64(mapa_shared(smem_u32(&sh.parts[part][lane]), 0), list);
+    }
+    cluster_sync();
+    if (part != 0) return;
+    if (warp == 0) {
+      all = sh.part[0];
+      for (int w = 1; w < split; ++w) all = join(all, sh.part[w], c);
+      if (kTop) {
+        list = sh.parts[0][lane];
+        for (int w = 1; w < split; ++w) list = merge32(list, sh.parts[w][31 - lane]);
+      }
+    }
+  }
+  if (warp != 0) return;
+  const bool live = all.s0 == all.s0, some = live && all.m > -inf;
+  const float log_sum = some ? logf(all.s0) : 0.f;
+  if (lane == 0) {
     if (a.logp) {
-      float lp = dead;
-      if (live) {
-        lp = target >= a.vocab ? nan
-             : some            ? (to_f(z[target]) - m) * a.scale - log_sum
-                               : -inf;
-      }
-      a.logp[row] = lp;
+      float lp = nan_f();
+      if (live && target < a.vocab)
+        lp = some ? (to_f(row.z[target]) - all.m) * a.scale - log_sum : -inf;
+      a.logp[row_i] = lp;
     }
-    if (a.entropy) a.entropy[row] = some ? log_sum - s1 / s0 : live ? 0.f : dead;
-    if (a.lse) a.lse[row] = some ? m * a.scale + log_sum : live ? -inf : dead;
-    if (a.stats) a.stats[row] = live ? make_float2(m, log_sum) : make_float2(dead, dead);
+    if (a.entropy)
+      a.entropy[row_i] = some ? log_sum - kLn2 * (all.s1 / all.s0) : live ? 0.f : nan_f();
+    if (a.lse) a.lse[row_i] = some ? fmaf(all.m, a.scale, log_sum) : live ? -inf : nan_f();
+    if (a.stats)
+      a.stats[row_i] = live ? make_float2(all.m, log_sum) : make_float2(nan_f(), nan_f());
   }
-  uint64_t last = ~0ull;
-  for (int i = 0; i < a.top; ++i) {
-    unsigned long long best = 0;
-    if (some && last) {
-      for (int j = tid; j < a.vocab; j += kThreads) {
-        const uint64_t k = order_key(to_f(z[j]), j);
-        if (k < last && k > best) best = k;
-      }
-      best = block_reduce(best, redk, [](unsigned long long x, unsigned long long y) {
-        return x > y ? x : y;
-      });
-      last = best;
-    }
-    if (tid == 0) {
-      const int64_t at = static_cast<int64_t>(row) * a.top + i;
-      a.top_ids[at] = best ? static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(best)) : -1;
-      a.top_logp[at] = best    ? (key_value(best) - m) * a.scale - log_sum
-                       : live  ? -inf
-                       : scored ? nan
-                                : 0.f;
-    }
+  if (kTop && lane < a.top) {
+    const int64_t at = static_cast<int64_t>(row_i) * a.top + lane;
+    const bool there = some && list != 0;
+    a.top_ids[at] = there ? static_cast<int32_t>(key_index(list)) : -1;
+    a.top_logp[at] = there  ? (key_value(list) - all.m) * a.scale - log_sum
+                     : live ? -inf
+                            : nan_f();
   }
 }
 
+template <typename T, int kThreads, bool kTop>
+cudaError_t launch_logprobs(const LogprobArgs& a, int split, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * split, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = static_cast<unsigned>(split);
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = split > 1 ? 1 : 0;
+  note_launch();
+  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, kThreads, kTop>, a, split);
+}
+
+// Threads by the row's vectors (a thread should have a few), CTAs per row by
+// how many rows there are to fill the GPU with.
+template <typename T>
+cudaError_t logprobs_of(const LogprobArgs& a, cudaStream_t s) {
+  const int vectors = a.vocab / Vec<T>::kPer;
+  if (vectors <= 1024)
+    return a.top ? launch_logprobs<T, 64, true>(a, 1, s) : launch_logprobs<T, 64, false>(a, 1, s);
+  int split = 1;
+  while (split < kMaxSplit && static_cast<int64_t>(a.rows) * split * 2 <= 2 * num_sms() &&
+         vectors / (2 * split) >= 512)
+    split *= 2;
+  return a.top ? launch_logprobs<T, 512, true>(a, split, s)
+               : launch_logprobs<T, 512, false>(a, split, s);
+}
+
+cudaError_t logprobs(const LogprobArgs& a, int dtype, cudaStream_t s) {
+  return dtype == RDT_F32    ? logprobs_of<float>(a, s)
+         : dtype == RDT_BF16 ? logprobs_of<bf16>(a, s)
+                             : logprobs_of<__half>(a, s);
+}
+
+// ------------------------------------------------------------------ gradient
 struct GradArgs {
   const void* logits;
   int64_t ld;
@@ -147,34 +485,116 @@ struct GradArgs {
   const float *entropy, *d_logp, *d_entropy, *d_lse;
   void* out;
   int64_t ld_out;
+  int pieces;  // CTAs per row
 };
 
+constexpr int kGradThreads = 256;
+constexpr int kGradPer = 8;     // elements of a thread's piece: 16 bytes of a 16-bit type
+constexpr int kGradUnroll = 2;  // pieces a thread has under way
+
+// Eight elements; inside: all of them in the row and p 16-byte aligned.
+template <typename T>
+__device__ __forceinline__ void load_piece(const T* p, int j, int vocab, bool inside, float* x) {
+  if (inside) {
+    if constexpr (sizeof(T) == 4) {
+      Vec<T>::unpack(*reinterpret_cast<const uint4*>(p + j), x);
+      Vec<T>::unpack(*reinterpret_cast<const uint4*>(p + j + 4), x + 4);
+    } else {
+      Vec<T>::unpack(*reinterpret_cast<const uint4*>(p + j), x);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kGradPer; ++i)
+      x[i] = static_cast<unsigned>(j + i) < static_cast<unsigned>(vocab) ? to_f(p[j + i]) : 0.f;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store_piece(T* p, int j, int vocab, bool inside, const float* x) {
+  if (inside) {
+    if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<float4*>(p + j) = make_float4(x[0], x[1], x[2], x[3]);
+      *reinterpret_cast<float4*>(p + j + 4) = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+      uint4 r;
+      T* h = reinterpret_cast<T*>(&r);
+#pragma unroll
+      for (int i = 0; i < kGradPer; ++i) h[i] = from_f<T>(x[i]);
+      *reinterpret_cast<uint4*>(p + j) = r;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kGradPer; ++i)
+      if (static_cast<unsigned>(j + i) < static_cast<unsigned>(vocab)) p[j + i] = from_f<T>(x[i]);
+  }
+}
+
+// With t = log2 p, A = logit_scale (d_lse - d_logp - d_entropy entropy) and
+// B = logit_scale d_entropy ln 2 a row's gradient is p (A - B t), plus
+// logit_scale d_logp at the target. Pieces of eight elements start where the
+// output is 16-byte aligned, so the stores are whole; a row whose logits have
+// another phase there loads them one by one.
 template <typename T, typename O>
-__global__ void __launch_bounds__(kThreads) logprobs_grad_kernel(const GradArgs a) {
-  const int row = blockIdx.x;
+__global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const GradArgs a) {
+  const int row = blockIdx.x / a.pieces, part = blockIdx.x % a.pieces;
   const T* z = static_cast<const T*>(a.logits) + static_cast<int64_t>(row) * a.ld;
   O* out = static_cast<O*>(a.out) + static_cast<int64_t>(row) * a.ld_out;
   const int target = a.targets ? a.targets[row] : 0;
   const float2 st = a.stats[row];
   const float g = a.d_logp ? a.d_logp[row] : 0.f, h = a.d_entropy ? a.d_entropy[row] : 0.f;
-  float c = (a.d_lse ? a.d_lse[row] : 0.f) - g;
-  if (a.d_entropy) c -= h * a.entropy[row];
+  float coef = (a.d_lse ? a.d_lse[row] : 0.f) - g;
+  if (a.d_entropy) coef -= h * a.entropy[row];
   const bool none = target < 0 || st.x == -INFINITY;
   const bool wrong = target >= a.vocab;
-  for (int j = threadIdx.x; j < a.vocab; j += kThreads) {
-    float r = 0.f;
-    if (wrong) {
-      r = __int_as_float(0x7fffffff);
-    } else if (!none) {
-      const float lp = (to_f(z[j]) - st.x) * a.scale - st.y;
-      const float p = expf(lp);
-      r = p == 0.f ? 0.f : p * (c - h * lp);
-      if (a.targets && j == target) r += g;
-      r *= a.scale;
+  const float c = a.scale * kLog2e, shift = st.y * kLog2e;
+  const float big_a = wrong ? nan_f() : a.scale * coef, big_b = a.scale * h * kLn2;
+  const int head = static_cast<int>((reinterpret_cast<uintptr_t>(out) / sizeof(O)) % kGradPer);
+  const int pieces = static_cast<int>((static_cast<int64_t>(head) + a.vocab + kGradPer - 1) / kGradPer);
+  const bool same = (reinterpret_cast<uintptr_t>(z - head) & 15) == 0;
+  const int stride = a.pieces * kGradThreads;
+  for (int q = part * kGradThreads + threadIdx.x; q < pieces; q += kGradUnroll * stride) {
+    float x[kGradUnroll][kGradPer];
+#pragma unroll
+    for (int u = 0; u < kGradUnroll; ++u) {
+      const int j = (q + u * stride) * kGradPer - head;
+      if (q + u * stride < pieces && !none)
+        load_piece(z, j, a.vocab, same && j >= 0 && j <= a.vocab - kGradPer, x[u]);
     }
-    out[j] = from_f<O>(r);
+#pragma unroll
+    for (int u = 0; u < kGradUnroll; ++u) {
+      if (q + u * stride >= pieces) break;
+      const int j = (q + u * stride) * kGradPer - head;
+#pragma unroll
+      for (int i = 0; i < kGradPer; ++i) {
+        const float t = keep_finite(fmaf(x[u][i] - st.x, c, -shift));
+        float r = exp2_fast(t) * fmaf(-big_b, t, big_a);
+        if (a.d_logp && j + i == target) r = fmaf(a.scale, g, r);
+        x[u][i] = none ? 0.f : r;
+      }
+      store_piece(out, j, a.vocab, j >= 0 && j <= a.vocab - kGradPer, x[u]);
+    }
   }
 }
+
+template <typename T>
+void launch_grad(GradArgs a, int d_dtype, cudaStream_t s) {
+  const int pieces = (a.vocab + kGradPer - 1) / kGradPer;
+  a.pieces = (pieces + kGradThreads * kGradUnroll - 1) / (kGradThreads * kGradUnroll);
+  // a CTA per piece of the row while there are few rows, else a few per row
+  const int64_t enough = 16LL * num_sms();
+  if (static_cast<int64_t>(a.rows) * a.pieces > enough)
+    a.pieces = static_cast<int>(std::max<int64_t>(
+        std::min<int64_t>(a.pieces, 4), enough / a.rows));
+  if (static_cast<int64_t>(a.rows) * a.pieces > INT32_MAX) a.pieces = 1;
+  const unsigned grid = static_cast<unsigned>(a.rows) * a.pieces;
+  if (d_dtype == RDT_F32)
+    logprobs_grad_kernel<T, float><<<grid, kGradThreads, 0, s>>>(a);
+  else if (d_dtype == RDT_BF16)
+    logprobs_grad_kernel<T, bf16><<<grid, kGradThreads, 0, s>>>(a);
+  else
+    logprobs_grad_kernel<T, __half><<<grid, kGradThreads, 0, s>>>(a);
+}
+
+constexpr int kMaxVocab = 1 << 30;  // indexes of a row's elements stay inside 32 bits
 
 bool dtype_ok(int dtype) { return dtype == RDT_F32 || dtype == RDT_BF16 || dtype == RDT_F16; }
 int dtype_bytes(int dtype) { return dtype == RDT_F32 ? 4 : 2; }
@@ -189,34 +609,14 @@ rdt_status launched(cudaError_t e) {
   return RDT_ECUDA;
 }
 
-cudaError_t logprobs(const LogprobArgs& a, int dtype, cudaStream_t s) {
-  note_launch();
-  if (dtype == RDT_F32)
-    logprobs_kernel<float><<<a.rows, kThreads, 0, s>>>(a);
-  else if (dtype == RDT_BF16)
-    logprobs_kernel<bf16><<<a.rows, kThreads, 0, s>>>(a);
-  else
-    logprobs_kernel<__half><<<a.rows, kThreads, 0, s>>>(a);
-  return cudaGetLastError();
-}
-
-template <typename T>
-void launch_grad(const GradArgs& a, int d_dtype, cudaStream_t s) {
-  if (d_dtype == RDT_F32)
-    logprobs_grad_kernel<T, float><<<a.rows, kThreads, 0, s>>>(a);
-  else if (d_dtype == RDT_BF16)
-    logprobs_grad_kernel<T, bf16><<<a.rows, kThreads, 0, s>>>(a);
-  else
-    logprobs_grad_kernel<T, __half><<<a.rows, kThreads, 0, s>>>(a);
-}
-
 // What both calls check of their logits.
 const char* logits_problem(const void* logits, int dtype, int64_t ld, int rows, int vocab,
                            float scale) {
   if (!dtype_ok(dtype)) return "dtype must be RDT_F32, RDT_BF16 or RDT_F16";
-  if (rows < 0 || vocab < 1) return "rows must be >= 0 and vocab >= 1";
+  if (rows < 0 || vocab < 1 || vocab > kMaxVocab)
+    return "rows must be >= 0 and vocab in [1, 2^30]";
   if (ld < vocab) return "ld must be >= vocab";
-  if (!(scale > 0.f) || !std::isfinite(scale)) return "logit_scale must be finite and > 0";
+  if (!(scale > 0.f) || !(scale <= 1e30f)) return "logit_scale must be in (0, 1e30]";
   if (rows > 0 && !logits) return "null pointer";
   if (reinterpret_cast<uintptr_t>(logits) % dtype_bytes(dtype))
     return "logits must be aligned to their type";
@@ -317,7 +717,7 @@ rdt_status rdt_token_logprobs_backward(const void* logits, int32_t dtype, int64_
     return refuse("d_logits overlaps logits without being them");
   GradArgs a{logits,  ld,     rows,      vocab, logit_scale, targets,
              reinterpret_cast<const float2*>(stats),
-             entropy, d_logp, d_entropy, d_lse, d_logits,    ld_d};
+             entropy, d_logp, d_entropy, d_lse, d_logits,    ld_d, 1};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   note_launch();
   if (dtype == RDT_F32)
@@ -348,8 +748,8 @@ rdt_status rdt_head_logprobs(const rdt_config* cfg, int32_t tokens, const float*
   if (const char* why = top_problem(top, top_ids, top_logp)) return refuse(why);
   if (logp && !targets) return refuse("logp needs targets");
   if (!logp && !entropy && !lse && top == 0) return refuse("null pointer: no output");
-  if (!(logit_scale > 0.f) || !std::isfinite(logit_scale))
-    return refuse("logit_scale must be finite and > 0");
+  if (!(logit_scale > 0.f) || !(logit_scale <= 1e30f))
+    return refuse("logit_scale must be in (0, 1e30]");
   const HeadScratch k = head_scratch(cfg, tokens, ws);
   if (ws_bytes < k.bytes) return refuse("workspace too small");
   const int H = cfg->hidden, V = cfg->vocab, step = head_rows(tokens, V);
