@@ -404,7 +404,7 @@ rdt_status rdt_embedding_backward(const int32_t* ids, int32_t tokens, const floa
  * distillation, policy training, sampling reports.
  *
  * A row z of `vocab` logits stands for the distribution p = softmax(logit_scale
- * z); logit_scale is 1 / temperature, in (0, 1e30]. Logits are fp32, bf16 or
+ * z); logit_scale is 1 / temperature, in [1e-6, 1e6]. Logits are fp32, bf16 or
  * fp16, [rows, vocab] with row stride ld elements (ld >= vocab, any alignment
  * an element has), vocab in [1, 2^30]; all arithmetic is fp32.
  *

@@ -40,6 +40,42 @@ __device__ __forceinline__ float keep_finite(float x) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(kLowest));
   return r;
 }
+// In a row whose maximum is above it, a logit of kFloor or less has
+// probability 0 for every logit_scale; raised to it, it needs no case of its
+// own (c (z - m) stays finite).
+constexpr float kFloor = -0x1p100f;
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 __device__ __forceinline__ float nan_f() { return __int_as_float(0x7fffffff); }
 
 // Larger value first, equal values in order of index: a whole number whose
@@ -72,6 +108,12 @@ template <> struct Vec<float> {
     return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)),
                  fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
   }
+  // The elements, raised to kFloor (NaN stays).
+  static __device__ __forceinline__ void raised(const uint4& r, float* x) {
+    unpack(r, x);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) x[i] = max_nan(x[i], kFloor);
+  }
 };
 template <> struct Vec<bf16> {
   static constexpr int kPer = 8;
@@ -84,6 +126,15 @@ template <> struct Vec<bf16> {
     const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&r);
     const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
     return fmaxf(__low2float(m), __high2float(m));
+  }
+  // A power of 2 is a bf16 value: two elements are raised at once.
+  static __device__ __forceinline__ void raised(const uint4& r, float* x) {
+    const __nv_bfloat162 low = __float2bfloat162_rn(kFloor);
+    uint4 q = r;
+    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&q);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __hmax2_nan(h[i], low);
+    unpack(q, x);
   }
 };
 template <> struct Vec<__half> {
@@ -102,6 +153,12 @@ template <> struct Vec<__half> {
     const __half2* h = reinterpret_cast<const __half2*>(&r);
     const __half2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
     return fmaxf(__low2float(m), __high2float(m));
+  }
+  // In fp32: kFloor is below every fp16 value.
+  static __device__ __forceinline__ void raised(const uint4& r, float* x) {
+    unpack(r, x);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) x[i] = max_nan(x[i], kFloor);
   }
 };
 
@@ -261,6 +318,99 @@ __device__ __forceinline__ uint64_t join_lists(uint64_t k, unsigned long long (*
   return k;
 }
 
+// The CTA's sums from its threads', in every thread.
+template <int kWarps>
+__device__ __forceinline__ Sums join_sums(Sums s, float c, Sums* warp_sums) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const Sums other{__shfl_xor_sync(kAll, s.m, o), __shfl_xor_sync(kAll, s.s0, o),
+                     __shfl_xor_sync(kAll, s.s1, o)};
+    s = lane & o ? join(other, s, c) : join(s, other, c);
+  }
+  if (lane == 0) warp_sums[warp] = s;
+  __syncthreads();
+  s = warp_sums[0];
+#pragma unroll 1
+  for (int w = 1; w < kWarps; ++w) s = join(s, warp_sums[w], c);
+  return s;
+}
+
+// A thread's vectors v, v + kThreads, ... below v1, whatever they hold; `at`
+// becomes the first vector of the group of kUnroll that brought the maximum.
+template <typename T, int kThreads>
+__device__ __noinline__ Sums sums_of_any(const Row<T>& row, int v, int v1, float c, int& at) {
+  constexpr int kPer = Vec<T>::kPer;
+  Sums s{-INFINITY, 0.f, 0.f};
+  for (; v < v1; v += kUnroll * kThreads) {
+#pragma unroll 1
+    for (int u = 0; u < kUnroll && v + u * kThreads < v1; ++u) {
+      const uint4 r = row.load(v + u * kThreads);
+      const float m = Vec<T>::max(r);
+      if (m > s.m) {
+        rebase(s, m, c);
+        at = v;
+      }
+      const float base = base_of(s.m);
+      float x[kPer];
+      Vec<T>::unpack(r, x);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const float t = keep_finite((x[i] - base) * c);
+        const float e = exp2_fast(t);
+        s.s0 += e;
+        s.s1 = fmaf(e, t, s.s1);
+      }
+    }
+  }
+  return s;
+}
+
+// The same for values whose maximum (over the CTA) is in (kFloor, -kFloor],
+// without special values but NaN and with two elements to an instruction. A
+// thread with nothing above kFloor returns m = kFloor. t is 0 and 2^t 1 at the
+// maximum itself, so a row with one token left has ln p = 0.
+template <typename T, int kThreads>
+__device__ __forceinline__ Sums sums_of(const Row<T>& row, int v, int v1, float c, int& at) {
+  constexpr int kPer = Vec<T>::kPer;
+  float m = kFloor;
+  uint64_t s0 = 0, s1 = 0;
+  const uint64_t cc = pack2(c, c);
+  for (; v < v1; v += kUnroll * kThreads) {
+    uint4 r[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      r[u] = v + u * kThreads < v1 ? row.load(v + u * kThreads) : Row<T>::none();
+    float top = Vec<T>::max(r[0]);
+#pragma unroll
+    for (int u = 1; u < kUnroll; ++u) top = fmaxf(top, Vec<T>::max(r[u]));
+    if (top > m) {
+      const float t = keep_finite((m - top) * c), f = exp2_fast(t);
+      const uint64_t ff = pack2(f, f), tt = pack2(t, t);
+      s1 = mul2(ff, fma2(tt, s0, s1));
+      s0 = mul2(ff, s0);
+      m = top;
+      at = v;
+    }
+    const uint64_t mm = pack2(-m, -m);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      float x[kPer];
+      Vec<T>::raised(r[u], x);
+#pragma unroll
+      for (int i = 0; i < kPer; i += 2) {
+        const uint64_t t = mul2(add2(pack2(x[i], x[i + 1]), mm), cc);
+        const float2 f = unpack2(t);
+        const uint64_t e = pack2(exp2_fast(f.x), exp2_fast(f.y));
+        s0 = add2(s0, e);
+        s1 = fma2(e, t, s1);
+      }
+    }
+  }
+  const float2 a = unpack2(s0), b = unpack2(s1);
+  return Sums{m, a.x + a.y, b.x + b.y};
+}
+
 // A row (or, in a cluster of `split` CTAs, 1 / split of it) per CTA, read once.
 // Each thread keeps the running maximum and sums of its vectors in registers;
 // warps, the CTA and the cluster join them in a fixed order.
@@ -301,79 +451,74 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a,
   const int v1 = static_cast<int>(static_cast<int64_t>(row.vectors) * (part + 1) / split);
   const float c = a.scale * kLog2e;
 
-  Sums s{-inf, 0.f, 0.f};
   int best_at = v0 + tid;  // the first vector of the group that brought the maximum
-  for (int v = v0 + tid; v < v1; v += kUnroll * kThreads) {
-    uint4 r[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      r[u] = v + u * kThreads < v1 ? row.load(v + u * kThreads) : Row<T>::none();
-    float m = Vec<T>::max(r[0]);
-#pragma unroll
-    for (int u = 1; u < kUnroll; ++u) m = fmaxf(m, Vec<T>::max(r[u]));
-    if (m > s.m) {
-      rebase(s, m, c);
-      if (kTop) best_at = v;
-    }
-    const float base = base_of(s.m);
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      float x[kPer];
-      Vec<T>::unpack(r[u], x);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const float t = keep_finite((x[i] - base) * c);
-        const float e = exp2_fast(t);
-        s.s0 += e;
-        s.s1 = fmaf(e, t, s.s1);
-      }
-    }
+  Sums s = sums_of<T, kThreads>(row, v0 + tid, v1, c, best_at);
+  Sums all = join_sums<kWarps>(s, c, sh.warp_sums);
+  const bool near = all.m > kFloor && all.m <= -kFloor;
+  if (!near) {  // nothing left, or a maximum beyond the fast range
+    best_at = v0 + tid;
+    s = sums_of_any<T, kThreads>(row, v0 + tid, v1, c, best_at);
+    __syncthreads();
+    all = join_sums<kWarps>(s, c, sh.warp_sums);
   }
-
-  Sums all = s;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const Sums other{__shfl_xor_sync(kAll, all.m, o), __shfl_xor_sync(kAll, all.s0, o),
-                     __shfl_xor_sync(kAll, all.s1, o)};
-    all = lane & o ? join(other, all, c) : join(all, other, c);
-  }
-  if (lane == 0) sh.warp_sums[warp] = all;
-  __syncthreads();
-  all = sh.warp_sums[0];
-  for (int w = 1; w < kWarps; ++w) all = join(all, sh.warp_sums[w], c);
 
   uint64_t list = 0;
   if (kTop && all.s0 == all.s0 && all.m > -inf) {  // the same in every thread
     // this thread's maximum and its lowest index
     uint64_t mine = 0;
-    if (s.m > -inf) {
-      for (int u = 0; u < kUnroll && mine == 0; ++u) {
-        const int v = best_at + u * kThreads;
-        if (v >= v1) break;
+    if (near ? s.m > kFloor : s.m > -inf) {
+      uint4 r[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        r[u] = best_at + u * kThreads < v1 ? row.load(best_at + u * kThreads) : Row<T>::none();
+#pragma unroll
+      for (int u = kUnroll - 1; u >= 0; --u) {
+        float x[kPer];
+        Vec<T>::unpack(r[u], x);
+#pragma unroll
+        for (int i = kPer - 1; i >= 0; --i)
+          if (x[i] == s.m) mine = order_key(x[i], row.first_of(best_at + u * kThreads) + i);
+      }
+    } else {
+      for (int v = v0 + tid; v < v1; v += kThreads) {
         float x[kPer];
         Vec<T>::unpack(row.load(v), x);
 #pragma unroll
-        for (int i = kPer - 1; i >= 0; --i)
-          if (x[i] == s.m) mine = order_key(x[i], row.first_of(v) + i);
+        for (int i = 0; i < kPer; ++i) {
+          const uint64_t k = order_key(x[i], row.first_of(v) + i);
+          mine = k > mine ? k : mine;
+        }
       }
     }
     join_lists<kWarps>(sort32(mine), sh.list);
     const uint64_t leader = sh.list[0][lane];  // lane i: the i-th largest of the maxima
     const uint64_t bound = __shfl_sync(kAll, leader, a.top - 1);
+    const float low = bound ? key_value(bound) : -inf;
     const int leaders = __popc(__ballot_sync(kAll, lane < a.top && leader != 0));
+    const int owner =
+        ((static_cast<int>(key_index(leader)) + row.head) / kPer - v0) % kThreads;
     __syncthreads();
+    // vector n of leader l as pair l turns + n, kUnroll pairs of a thread under way
     const int turns = (v1 - v0 + kThreads - 1) / kThreads;
-    for (int i = warp; i < leaders; i += kWarps) {
-      const uint64_t key = __shfl_sync(kAll, leader, i);
-      const int v = (static_cast<int>(key_index(key)) + row.head) / kPer;
-      const int owner = (v - v0) % kThreads;
-      for (int n = 0; n < turns; n += 32) {
-        const int at = v0 + owner + (n + lane) * kThreads;
+    const int pairs = leaders * turns;
+    for (int q = tid; q - lane < pairs; q += kUnroll * kThreads) {
+      uint4 r[kUnroll];
+      int at[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int pair = q + u * kThreads;
+        const int l = min(pair / turns, 31);
+        at[u] = v0 + __shfl_sync(kAll, owner, l) + (pair - l * turns) * kThreads;
+        r[u] = pair < pairs && at[u] < v1 ? row.load(at[u]) : Row<T>::none();
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        if (!__any_sync(kAll, Vec<T>::max(r[u]) >= low)) continue;
         float x[kPer];
-        Vec<T>::unpack(n + lane < turns && at < v1 ? row.load(at) : Row<T>::none(), x);
+        Vec<T>::unpack(r[u], x);
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
-          const uint64_t k = order_key(x[e], row.first_of(at) + e);
+          const uint64_t k = order_key(x[e], row.first_of(at[u]) + e);
           const uint64_t least = __shfl_sync(kAll, list, a.top - 1);
           unsigned who = __ballot_sync(kAll, k != 0 && k >= bound && k > least);
           while (who) {
@@ -616,7 +761,7 @@ const char* logits_problem(const void* logits, int dtype, int64_t ld, int rows, 
   if (rows < 0 || vocab < 1 || vocab > kMaxVocab)
     return "rows must be >= 0 and vocab in [1, 2^30]";
   if (ld < vocab) return "ld must be >= vocab";
-  if (!(scale > 0.f) || !(scale <= 1e30f)) return "logit_scale must be in (0, 1e30]";
+  if (!(scale >= 1e-6f && scale <= 1e6f)) return "logit_scale must be in [1e-6, 1e6]";
   if (rows > 0 && !logits) return "null pointer";
   if (reinterpret_cast<uintptr_t>(logits) % dtype_bytes(dtype))
     return "logits must be aligned to their type";
@@ -684,8 +829,9 @@ rdt_status rdt_token_logprobs(const void* logits, int32_t dtype, int64_t ld, int
   if (!aligned4(targets) || !aligned4(logp) || !aligned4(entropy) || !aligned4(lse) ||
       (reinterpret_cast<uintptr_t>(stats) & 7) || !aligned4(top_ids) || !aligned4(top_logp))
     return refuse("targets and outputs must be 4-byte aligned (stats 8-byte)");
-  LogprobArgs a{logits,  ld,  rows, vocab, logit_scale, targets, logp,
-                entropy, lse, reinterpret_cast<float2*>(stats), top, top_ids, top_logp};
+  LogprobArgs a{logits,  ld,   rows,    vocab, logit_scale,
+                targets, logp, entropy, lse,   reinterpret_cast<float2*>(stats),
+                top,     top_ids, top_logp};
   return launched(rdt::logprobs(a, dtype, static_cast<cudaStream_t>(stream)));
 }
 
@@ -748,8 +894,8 @@ rdt_status rdt_head_logprobs(const rdt_config* cfg, int32_t tokens, const float*
   if (const char* why = top_problem(top, top_ids, top_logp)) return refuse(why);
   if (logp && !targets) return refuse("logp needs targets");
   if (!logp && !entropy && !lse && top == 0) return refuse("null pointer: no output");
-  if (!(logit_scale > 0.f) || !(logit_scale <= 1e30f))
-    return refuse("logit_scale must be in (0, 1e30]");
+  if (!(logit_scale >= 1e-6f && logit_scale <= 1e6f))
+    return refuse("logit_scale must be in [1e-6, 1e6]");
   const HeadScratch k = head_scratch(cfg, tokens, ws);
   if (ws_bytes < k.bytes) return refuse("workspace too small");
   const int H = cfg->hidden, V = cfg->vocab, step = head_rows(tokens, V);
