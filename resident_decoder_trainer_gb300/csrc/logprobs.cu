@@ -2,6 +2,7 @@
 // logits, their gradient, and the scoring head that calls them
 // (rdt_token_logprobs, rdt_token_logprobs_backward, rdt_head_logprobs).
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <cuda_fp16.h>
@@ -178,10 +179,25 @@ struct Row {
     vectors = static_cast<int>((static_cast<int64_t>(head) + n + Vec<T>::kPer - 1) / Vec<T>::kPer);
   }
   __device__ __forceinline__ int first_of(int v) const { return v * Vec<T>::kPer - head; }
+  __device__ __forceinline__ bool whole(int v) const {
+    const int j = first_of(v);
+    return j >= 0 && j <= vocab - Vec<T>::kPer;
+  }
   // v in [0, vectors)
   __device__ __forceinline__ uint4 load(int v) const {
-    const int j = first_of(v);
-    if (j >= 0 && j <= vocab - Vec<T>::kPer) return __ldg(v0 + v);
+    return whole(v) ? __ldg(v0 + v) : load_part(first_of(v));
+  }
+  // Starts to copy vector v to shared memory; the thread that called finds it there after a
+  // wait for its copies.
+  __device__ __forceinline__ void fetch(int v, uint4* to) const {
+    if (whole(v))
+      asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(smem_u32(to)),
+                   "l"(v0 + v)
+                   : "memory");
+    else
+      *to = load_part(first_of(v));
+  }
+  __device__ __noinline__ uint4 load_part(int j) const {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -234,20 +250,6 @@ constexpr unsigned kAll = 0xffffffffu;
 __device__ __forceinline__ uint64_t keep_of(uint64_t a, uint64_t b, bool larger) {
   return (a > b) == larger ? a : b;
 }
-// Any 32 keys into order (bitonic: runs of 2, 4, ... 32).
-__device__ __forceinline__ uint64_t sort32(uint64_t k) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int run = 2; run <= 32; run <<= 1) {
-#pragma unroll
-    for (int step = run >> 1; step > 0; step >>= 1) {
-      const uint64_t other = __shfl_xor_sync(kAll, k, step);
-      const bool down = (lane & run) == 0 || run == 32;
-      k = keep_of(k, other, ((lane & step) == 0) == down);
-    }
-  }
-  return k;
-}
 // The 32 largest of two ordered lists, in order; `back` holds the second one's
 // keys in reverse (its lane i the key of place 31 - i).
 __device__ __forceinline__ uint64_t merge32(uint64_t k, uint64_t back) {
@@ -290,77 +292,72 @@ struct LogprobArgs {
 };
 
 constexpr int kMaxSplit = 8;  // CTAs that share a row (a cluster of the portable size)
-constexpr int kUnroll = 4;    // vectors a thread has under way
+constexpr int kUnroll = 4;    // vectors a thread works on at once: a group
+constexpr int kStages = 3;    // groups a thread holds in shared memory
+constexpr int kSegments = 8;  // parts of a thread's groups whose maxima are kept
+constexpr int kSample = 64;   // sets of threads whose maxima bound the row's alternatives
+constexpr int kKeys = 256;    // candidates that are ranked by counting
 
-template <int kWarps>
+template <int kThreads, bool kTop>
 struct Shared {
-  Sums warp_sums[kWarps];
-  Sums part[kMaxSplit];                  // of the cluster's CTAs, in its first CTA
-  unsigned long long list[kWarps][32];
+  Sums warp_sums[kThreads / 32];
+  Sums part[kMaxSplit];  // of the cluster's CTAs, in its first CTA
+};
+template <int kThreads>
+struct Shared<kThreads, true> {
+  Sums warp_sums[kThreads / 32];
+  Sums part[kMaxSplit];
   unsigned long long parts[kMaxSplit][32];
+  unsigned long long best[32];
+  unsigned long long key[kKeys];
+  float segment[kSegments][kThreads];
+  float sample[kSample];
+  float bound;
+  int items, keys;
 };
 
-// The CTA's 32 largest of its warps' lists, in every thread of warp 0 and in
-// list[0]. All threads call it.
-template <int kWarps>
-__device__ __forceinline__ uint64_t join_lists(uint64_t k, unsigned long long (*list)[32]) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  list[warp][lane] = k;
-#pragma unroll
-  for (int step = kWarps / 2; step > 0; step >>= 1) {
-    __syncthreads();
-    if (warp < step) {
-      k = merge32(k, list[warp + step][31 - lane]);
-      list[warp][lane] = k;
-    }
-  }
-  __syncthreads();
-  return k;
-}
-
-// The CTA's sums from its threads', in every thread.
+// The CTA's sums from its threads', in every thread: the maximum first, one
+// rebase, then plain sums, within warps and then between them.
 template <int kWarps>
 __device__ __forceinline__ Sums join_sums(Sums s, float c, Sums* warp_sums) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const Sums other{__shfl_xor_sync(kAll, s.m, o), __shfl_xor_sync(kAll, s.s0, o),
-                     __shfl_xor_sync(kAll, s.s1, o)};
-    s = lane & o ? join(other, s, c) : join(s, other, c);
-  }
+  rebase(s, warp_max(s.m), c);
+  s.s0 = warp_sum(s.s0);
+  s.s1 = warp_sum(s.s1);
   if (lane == 0) warp_sums[warp] = s;
   __syncthreads();
-  s = warp_sums[0];
-#pragma unroll 1
-  for (int w = 1; w < kWarps; ++w) s = join(s, warp_sums[w], c);
+  s = warp_sums[lane % kWarps];
+  float m = s.m;
+#pragma unroll
+  for (int o = kWarps / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+  rebase(s, m, c);
+#pragma unroll
+  for (int o = kWarps / 2; o > 0; o >>= 1) {
+    s.s0 += __shfl_xor_sync(kAll, s.s0, o);
+    s.s1 += __shfl_xor_sync(kAll, s.s1, o);
+  }
   return s;
 }
 
-// A thread's vectors v, v + kThreads, ... below v1, whatever they hold; `at`
-// becomes the first vector of the group of kUnroll that brought the maximum.
+// A thread's vectors v, v + kThreads, ... below v1, whatever they hold.
 template <typename T, int kThreads>
-__device__ __noinline__ Sums sums_of_any(const Row<T>& row, int v, int v1, float c, int& at) {
+__device__ __noinline__ Sums sums_of_any(const Row<T>& row, int v, int v1, float c) {
   constexpr int kPer = Vec<T>::kPer;
   Sums s{-INFINITY, 0.f, 0.f};
-  for (; v < v1; v += kUnroll * kThreads) {
 #pragma unroll 1
-    for (int u = 0; u < kUnroll && v + u * kThreads < v1; ++u) {
-      const uint4 r = row.load(v + u * kThreads);
-      const float m = Vec<T>::max(r);
-      if (m > s.m) {
-        rebase(s, m, c);
-        at = v;
-      }
-      const float base = base_of(s.m);
-      float x[kPer];
-      Vec<T>::unpack(r, x);
+  for (; v < v1; v += kThreads) {
+    const uint4 r = row.load(v);
+    const float m = Vec<T>::max(r);
+    if (m > s.m) rebase(s, m, c);
+    const float base = base_of(s.m);
+    float x[kPer];
+    Vec<T>::unpack(r, x);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const float t = keep_finite((x[i] - base) * c);
-        const float e = exp2_fast(t);
-        s.s0 += e;
-        s.s1 = fmaf(e, t, s.s1);
-      }
+    for (int i = 0; i < kPer; ++i) {
+      const float t = keep_finite((x[i] - base) * c);
+      const float e = exp2_fast(t);
+      s.s0 += e;
+      s.s1 = fmaf(e, t, s.s1);
     }
   }
   return s;
@@ -370,17 +367,38 @@ __device__ __noinline__ Sums sums_of_any(const Row<T>& row, int v, int v1, float
 // without special values but NaN and with two elements to an instruction. A
 // thread with nothing above kFloor returns m = kFloor. t is 0 and 2^t 1 at the
 // maximum itself, so a row with one token left has ln p = 0.
+//
+// The loads run kStages - 1 groups ahead, each thread's into its own part of
+// `ring` (no barrier: a thread reads only what it copied). `segment`, where not
+// null, receives the maxima of kSegments runs of `length` groups (as they
+// are: -inf for none, NaN not seen).
 template <typename T, int kThreads>
-__device__ __forceinline__ Sums sums_of(const Row<T>& row, int v, int v1, float c, int& at) {
+__device__ __forceinline__ Sums sums_of(const Row<T>& row, int v, int v1, float c, uint4* ring,
+                                        float (*segment)[kThreads], int length) {
   constexpr int kPer = Vec<T>::kPer;
-  float m = kFloor;
+  static_assert(kStages * kUnroll * 16 >= kSegments * 2 + 8, "the ring holds the lists");
+  constexpr int kStep = kUnroll * kThreads;
+  ring += threadIdx.x;
+  auto fetch = [&](int g, int stage) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (g + u * kThreads < v1) row.fetch(g + u * kThreads, ring + (stage * kUnroll + u) * kThreads);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(v + i * kStep, i);
+  float m = kFloor, segment_m = -INFINITY;
+  int left = length, filled = 0;
   uint64_t s0 = 0, s1 = 0;
   const uint64_t cc = pack2(c, c);
-  for (; v < v1; v += kUnroll * kThreads) {
+  for (int stage = 0; v < v1; v += kStep) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
     uint4 r[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
-      r[u] = v + u * kThreads < v1 ? row.load(v + u * kThreads) : Row<T>::none();
+      r[u] = v + u * kThreads < v1 ? ring[(stage * kUnroll + u) * kThreads] : Row<T>::none();
+    fetch(v + (kStages - 1) * kStep, stage == 0 ? kStages - 1 : stage - 1);
+    stage = stage == kStages - 1 ? 0 : stage + 1;
     float top = Vec<T>::max(r[0]);
 #pragma unroll
     for (int u = 1; u < kUnroll; ++u) top = fmaxf(top, Vec<T>::max(r[u]));
@@ -390,7 +408,14 @@ __device__ __forceinline__ Sums sums_of(const Row<T>& row, int v, int v1, float 
       s1 = mul2(ff, fma2(tt, s0, s1));
       s0 = mul2(ff, s0);
       m = top;
-      at = v;
+    }
+    if (segment) {
+      segment_m = fmaxf(segment_m, top);
+      if (--left == 0) {
+        segment[filled++][threadIdx.x] = segment_m;
+        segment_m = -INFINITY;
+        left = length;
+      }
     }
     const uint64_t mm = pack2(-m, -m);
 #pragma unroll
@@ -407,24 +432,98 @@ __device__ __forceinline__ Sums sums_of(const Row<T>& row, int v, int v1, float 
       }
     }
   }
+  if (segment)
+    for (; filled < kSegments; ++filled) {
+      segment[filled][threadIdx.x] = segment_m;
+      segment_m = -INFINITY;
+    }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   const float2 a = unpack2(s0), b = unpack2(s1);
   return Sums{m, a.x + a.y, b.x + b.y};
+}
+
+// f(element, index) for the elements of the listed (segment, thread) pairs'
+// vectors whose maximum is at least `low`; the vectors are spread over the
+// threads, kUnroll of each under way. With kWhole f is called by whole warps,
+// with -inf where a lane has no such element.
+template <typename T, int kThreads, bool kWhole, typename F>
+__device__ __forceinline__ void for_each_candidate(const Row<T>& row, int v0, int v1,
+                                                   const uint16_t* item, int items, int length,
+                                                   float low, F f) {
+  constexpr int kPer = Vec<T>::kPer;
+  const int lane = threadIdx.x & 31;
+  const int each = length * kUnroll, pairs = items * each;
+  for (int q = threadIdx.x; q - lane < pairs; q += kUnroll * kThreads) {
+    uint4 r[kUnroll];
+    int at[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int pair = q + u * kThreads;
+      r[u] = Row<T>::none();
+      at[u] = v0;
+      if (pair < pairs) {
+        const int i = pair / each, n = pair - i * each, id = item[i];
+        at[u] = v0 + id % kThreads + (id / kThreads * each + n) * kThreads;
+        if (at[u] < v1) r[u] = row.load(at[u]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const bool some = Vec<T>::max(r[u]) >= low;
+      if (kWhole ? !__any_sync(kAll, some) : !some) continue;
+      float x[kPer];
+      Vec<T>::unpack(r[u], x);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) f(x[e] >= low ? x[e] : -INFINITY, row.first_of(at[u]) + e);
+    }
+  }
+}
+
+// The CTA's 32 largest elements among the candidates, to best[]: for any
+// number of them (ties, or few finite logits). list: scratch, 32 keys a warp.
+template <typename T, int kThreads>
+__device__ __noinline__ void select_any(const Row<T>& row, int v0, int v1, const uint16_t* item,
+                                        int items, int length, float low, int top,
+                                        unsigned long long (*list)[32], unsigned long long* best) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint64_t mine = 0;
+  for_each_candidate<T, kThreads, true>(
+      row, v0, v1, item, items, length, low, [&](float x, int index) {
+        const uint64_t k = order_key(x, index);
+        const uint64_t least = __shfl_sync(kAll, mine, top - 1);
+        unsigned who = __ballot_sync(kAll, k > least);
+        while (who) {
+          const int l = __ffs(who) - 1;
+          who &= who - 1;
+          mine = insert32(mine, __shfl_sync(kAll, k, l));
+        }
+      });
+  list[warp][lane] = mine;
+  for (int step = kThreads / 64; step > 0; step >>= 1) {
+    __syncthreads();
+    if (warp < step) {
+      mine = merge32(mine, list[warp + step][31 - lane]);
+      list[warp][lane] = mine;
+    }
+  }
+  if (warp == 0) best[lane] = mine;
 }
 
 // A row (or, in a cluster of `split` CTAs, 1 / split of it) per CTA, read once.
 // Each thread keeps the running maximum and sums of its vectors in registers;
 // warps, the CTA and the cluster join them in a fixed order.
 //
-// Alternatives need no work in the loop: the `top`-th largest of the threads'
-// maxima is a lower bound of the row's `top`-th largest logit, and the logits
-// above it belong to the `top` threads with the largest maxima. Only those
-// threads' vectors (top / threads of the row, from L2) are read again and
-// filtered by the bound into sorted lists of 32, one key per lane.
+// Alternatives cost the loop one maximum per group and thread. The `top`-th
+// largest of the maxima of kSample sets of threads is a lower bound of the
+// row's `top`-th largest logit (each set holds one at least as large), and of
+// random logits about 64 ln(64 / (64 - top)) are above it, 24 for 20. Only the
+// (segment, thread) pairs whose maximum reaches the bound are read again, and
+// what reaches it there is ranked by counting.
 template <typename T, int kThreads, bool kTop>
 __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a, int split) {
   constexpr int kWarps = kThreads / 32;
-  constexpr int kPer = Vec<T>::kPer;
-  __shared__ Shared<kWarps> sh;
+  extern __shared__ uint4 ring[];  // kStages kUnroll kThreads; after the loop, lists
+  __shared__ Shared<kThreads, kTop> sh;
   const int row_i = split == 1 ? blockIdx.x : blockIdx.x / split;
   const int part = split == 1 ? 0 : blockIdx.x % split;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -451,85 +550,74 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a,
   const int v1 = static_cast<int>(static_cast<int64_t>(row.vectors) * (part + 1) / split);
   const float c = a.scale * kLog2e;
 
-  int best_at = v0 + tid;  // the first vector of the group that brought the maximum
-  Sums s = sums_of<T, kThreads>(row, v0 + tid, v1, c, best_at);
+  const int groups = (v1 - v0 + kUnroll * kThreads - 1) / (kUnroll * kThreads);
+  const int length = max(1, (groups + kSegments - 1) / kSegments);
+  float(*segment)[kThreads] = nullptr;
+  if constexpr (kTop) segment = sh.segment;
+  Sums s = sums_of<T, kThreads>(row, v0 + tid, v1, c, ring, segment, length);
+  if constexpr (kTop) {
+    float m = sh.segment[0][tid];
+#pragma unroll
+    for (int i = 1; i < kSegments; ++i) m = fmaxf(m, sh.segment[i][tid]);
+#pragma unroll
+    for (int o = 1; o < kThreads / kSample; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+    if (tid % (kThreads / kSample) == 0) sh.sample[tid / (kThreads / kSample)] = m;
+    if (tid == 0) sh.items = sh.keys = 0;
+    if (tid < 32) sh.best[tid] = 0;
+  }
   Sums all = join_sums<kWarps>(s, c, sh.warp_sums);
-  const bool near = all.m > kFloor && all.m <= -kFloor;
-  if (!near) {  // nothing left, or a maximum beyond the fast range
-    best_at = v0 + tid;
-    s = sums_of_any<T, kThreads>(row, v0 + tid, v1, c, best_at);
+  if (!(all.m > kFloor && all.m <= -kFloor)) {  // nothing left, or a maximum beyond the fast range
+    s = sums_of_any<T, kThreads>(row, v0 + tid, v1, c);
     __syncthreads();
     all = join_sums<kWarps>(s, c, sh.warp_sums);
   }
 
   uint64_t list = 0;
-  if (kTop && all.s0 == all.s0 && all.m > -inf) {  // the same in every thread
-    // this thread's maximum and its lowest index
-    uint64_t mine = 0;
-    if (near ? s.m > kFloor : s.m > -inf) {
-      uint4 r[kUnroll];
+  if constexpr (kTop) if (all.s0 == all.s0 && all.m > -inf) {  // the same in every thread
+    if (tid < kSample) {
+      const float x = sh.sample[tid];
+      int rank = 0;
+#pragma unroll 16
+      for (int j = 0; j < kSample; ++j) {
+        const float y = sh.sample[j];
+        rank += y > x || (y == x && j < tid);
+      }
+      if (rank == a.top - 1) sh.bound = x;
+    }
+    __syncthreads();
+    const float low = sh.bound;  // -inf: fewer than `top` sets hold anything
+    uint16_t* item = reinterpret_cast<uint16_t*>(ring);
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u)
-        r[u] = best_at + u * kThreads < v1 ? row.load(best_at + u * kThreads) : Row<T>::none();
-#pragma unroll
-      for (int u = kUnroll - 1; u >= 0; --u) {
-        float x[kPer];
-        Vec<T>::unpack(r[u], x);
-#pragma unroll
-        for (int i = kPer - 1; i >= 0; --i)
-          if (x[i] == s.m) mine = order_key(x[i], row.first_of(best_at + u * kThreads) + i);
+    for (int i = 0; i < kSegments; ++i) {
+      const float m = sh.segment[i][tid];
+      if (m >= low && m > -inf)
+        item[atomicAdd(&sh.items, 1)] = static_cast<uint16_t>(i * kThreads + tid);
+    }
+    __syncthreads();
+    // the order of items and keys varies, what is chosen among them does not
+    for_each_candidate<T, kThreads, false>(
+        row, v0, v1, item, sh.items, length, low, [&](float x, int index) {
+          const uint64_t k = order_key(x, index);
+          if (k == 0) return;
+          const int n = atomicAdd(&sh.keys, 1);
+          if (n < kKeys) sh.key[n] = k;
+        });
+    __syncthreads();
+    const int keys = sh.keys;
+    if (keys <= kKeys) {
+      for (int i = tid; i < keys; i += kThreads) {
+        const unsigned long long k = sh.key[i];
+        int rank = 0;
+        for (int j = 0; j < keys; ++j) rank += sh.key[j] > k;
+        if (rank < a.top) sh.best[rank] = k;
       }
     } else {
-      for (int v = v0 + tid; v < v1; v += kThreads) {
-        float x[kPer];
-        Vec<T>::unpack(row.load(v), x);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const uint64_t k = order_key(x[i], row.first_of(v) + i);
-          mine = k > mine ? k : mine;
-        }
-      }
+      select_any<T, kThreads>(row, v0, v1, item, sh.items, length, low, a.top,
+                              reinterpret_cast<unsigned long long(*)[32]>(
+                                  item + kSegments * kThreads), sh.best);
     }
-    join_lists<kWarps>(sort32(mine), sh.list);
-    const uint64_t leader = sh.list[0][lane];  // lane i: the i-th largest of the maxima
-    const uint64_t bound = __shfl_sync(kAll, leader, a.top - 1);
-    const float low = bound ? key_value(bound) : -inf;
-    const int leaders = __popc(__ballot_sync(kAll, lane < a.top && leader != 0));
-    const int owner =
-        ((static_cast<int>(key_index(leader)) + row.head) / kPer - v0) % kThreads;
     __syncthreads();
-    // vector n of leader l as pair l turns + n, kUnroll pairs of a thread under way
-    const int turns = (v1 - v0 + kThreads - 1) / kThreads;
-    const int pairs = leaders * turns;
-    for (int q = tid; q - lane < pairs; q += kUnroll * kThreads) {
-      uint4 r[kUnroll];
-      int at[kUnroll];
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int pair = q + u * kThreads;
-        const int l = min(pair / turns, 31);
-        at[u] = v0 + __shfl_sync(kAll, owner, l) + (pair - l * turns) * kThreads;
-        r[u] = pair < pairs && at[u] < v1 ? row.load(at[u]) : Row<T>::none();
-      }
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        if (!__any_sync(kAll, Vec<T>::max(r[u]) >= low)) continue;
-        float x[kPer];
-        Vec<T>::unpack(r[u], x);
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-          const uint64_t k = order_key(x[e], row.first_of(at[u]) + e);
-          const uint64_t least = __shfl_sync(kAll, list, a.top - 1);
-          unsigned who = __ballot_sync(kAll, k != 0 && k >= bound && k > least);
-          while (who) {
-            const int l = __ffs(who) - 1;
-            who &= who - 1;
-            list = insert32(list, __shfl_sync(kAll, k, l));
-          }
-        }
-      }
-    }
-    list = join_lists<kWarps>(list, sh.list);
+    list = sh.best[lane];
   }
 
   if (split > 1) {
@@ -542,14 +630,14 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a,
         st_cluster_f32(p + 4, all.s0);
         st_cluster_f32(p + 8, all.s1);
       }
-      if (kTop) st_cluster_u64(mapa_shared(smem_u32(&sh.parts[part][lane]), 0), list);
+      if constexpr (kTop) st_cluster_u64(mapa_shared(smem_u32(&sh.parts[part][lane]), 0), list);
     }
     cluster_sync();
     if (part != 0) return;
     if (warp == 0) {
       all = sh.part[0];
       for (int w = 1; w < split; ++w) all = join(all, sh.part[w], c);
-      if (kTop) {
+      if constexpr (kTop) {
         list = sh.parts[0][lane];
         for (int w = 1; w < split; ++w) list = merge32(list, sh.parts[w][31 - lane]);
       }
@@ -587,6 +675,18 @@ cudaError_t launch_logprobs(const LogprobArgs& a, int split, cudaStream_t s) {
   cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * split, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = s;
+  cfg.dynamicSmemBytes = kStages * kUnroll * kThreads * sizeof(uint4);
+  static std::atomic<uint64_t> allowed{0};  // devices where the kernel may use that much
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev > 63 || !(allowed.load() >> dev & 1)) {
+    e = cudaFuncSetAttribute(logprobs_kernel<T, kThreads, kTop>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(cfg.dynamicSmemBytes));
+    if (e != cudaSuccess) return e;
+    if (dev < 64) allowed.fetch_or(uint64_t(1) << dev);
+  }
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = static_cast<unsigned>(split);
@@ -609,8 +709,8 @@ cudaError_t logprobs_of(const LogprobArgs& a, cudaStream_t s) {
   while (split < kMaxSplit && static_cast<int64_t>(a.rows) * split * 2 <= 2 * num_sms() &&
          vectors / (2 * split) >= 512)
     split *= 2;
-  return a.top ? launch_logprobs<T, 512, true>(a, split, s)
-               : launch_logprobs<T, 512, false>(a, split, s);
+  return a.top ? launch_logprobs<T, 256, true>(a, split, s)
+               : launch_logprobs<T, 256, false>(a, split, s);
 }
 
 cudaError_t logprobs(const LogprobArgs& a, int dtype, cudaStream_t s) {

@@ -155,8 +155,14 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+# the current stream's handle without a Stream object (4 us less per call), where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -290,26 +296,35 @@ def gemm_nf4(a, codes, scales, w_rows, w_cols, b_mn, c, a2=None, b2=None, split_
 
 
 # ------------------------------------------------- token log probabilities
-def _here(t, what, dtypes, shape=None):
-    """Checks that t is a tensor the library may be handed: on the current device, of one of
-    the types, and, where a shape is given, of that shape and contiguous."""
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+def _device(t, what) -> int:
+    """The current CUDA device, which t has to be on."""
+    device = t.get_device()
+    if device < 0 or device != torch.cuda.current_device():
+        raise ValueError(f"{what} must be on the current CUDA device")
+    return device
+
+
+def _here(t, what, dtypes, shape, device):
+    """The address of t, after the checks that the library may be handed it: on the device,
+    of one of the types, and, where a shape is given, of that shape and contiguous."""
+    if t.get_device() != device:
         raise ValueError(f"{what} must be on the current CUDA device")
     if t.dtype not in dtypes:
         raise ValueError(f"{what} has type {t.dtype}")
-    if shape is not None and (tuple(t.shape) != shape or not t.is_contiguous()):
+    if shape is not None and (t.shape != shape or not t.is_contiguous()):
         raise ValueError(f"{what} must be contiguous and of shape {shape}")
+    return t.data_ptr()
 
 
 _F32, _I32 = (torch.float32,), (torch.int32,)
 
 
-def _rows_of(logits, what):
-    _here(logits, what, _DTYPE)
+def _rows_of(logits, what, device):
+    ptr = _here(logits, what, _DTYPE, None, device)
     if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
         raise ValueError(f"{what} must be [rows, vocab] with contiguous rows")
     rows, vocab = logits.shape
-    return rows, vocab, logits.stride(0) if rows > 1 else vocab
+    return ptr, rows, vocab, logits.stride(0) if rows > 1 else vocab
 
 
 def token_logprobs(logits, targets=None, logp=None, entropy=None, lse=None, stats=None,
@@ -319,22 +334,22 @@ def token_logprobs(logits, targets=None, logp=None, entropy=None, lse=None, stat
     (rdt_token_logprobs). logits [rows, vocab] fp32, bf16 or fp16, any row stride;
     targets int32 [rows]; logp, entropy, lse fp32 [rows]; stats fp32 [rows, 2] (for the
     gradient); top_ids int32 and top_logp fp32 [rows, k], k <= RDT_MAX_TOP."""
-    rows, vocab, ld = _rows_of(logits, "logits")
-    for t, what, dtype in ((targets, "targets", _I32), (logp, "logp", _F32),
-                           (entropy, "entropy", _F32), (lse, "lse", _F32)):
-        if t is not None:
-            _here(t, what, dtype, (rows,))
-    if stats is not None:
-        _here(stats, "stats", _F32, (rows, 2))
+    dev = _device(logits, "logits")
+    z, rows, vocab, ld = _rows_of(logits, "logits", dev)
+    one = (rows,)
     top = 0 if top_ids is None else top_ids.shape[-1]
-    if top_ids is not None:
-        _here(top_ids, "top_ids", _I32, (rows, top))
-    if top_logp is not None:
-        _here(top_logp, "top_logp", _F32, (rows, top))
-    _check(lib().rdt_token_logprobs(_ptr(logits), _DTYPE[logits.dtype], ld, rows, vocab,
-                                    logit_scale, _ptr(targets), _ptr(logp), _ptr(entropy),
-                                    _ptr(lse), _ptr(stats), top, _ptr(top_ids), _ptr(top_logp),
-                                    _stream(stream)))
+    if top_logp is not None and top_ids is not None and top_logp.shape != top_ids.shape:
+        raise ValueError("top_ids and top_logp must have the same shape")
+    _check(lib().rdt_token_logprobs(
+        z, _DTYPE[logits.dtype], ld, rows, vocab, logit_scale,
+        None if targets is None else _here(targets, "targets", _I32, one, dev),
+        None if logp is None else _here(logp, "logp", _F32, one, dev),
+        None if entropy is None else _here(entropy, "entropy", _F32, one, dev),
+        None if lse is None else _here(lse, "lse", _F32, one, dev),
+        None if stats is None else _here(stats, "stats", _F32, (rows, 2), dev), top,
+        None if top_ids is None else _here(top_ids, "top_ids", _I32, (rows, top), dev),
+        None if top_logp is None else _here(top_logp, "top_logp", _F32, (rows, top), dev),
+        _stream(stream)))
 
 
 def token_logprobs_backward(logits, targets, stats, d_logits, d_logp=None, entropy=None,
@@ -343,21 +358,21 @@ def token_logprobs_backward(logits, targets, stats, d_logits, d_logp=None, entro
     (rdt_token_logprobs_backward): [rows, vocab] of any of the three types, or the logits
     tensor itself. stats and entropy as token_logprobs wrote them; d_logp, d_entropy, d_lse
     fp32 [rows] or None."""
-    rows, vocab, ld = _rows_of(logits, "logits")
-    d_rows, d_vocab, ld_d = _rows_of(d_logits, "d_logits")
+    dev = _device(logits, "logits")
+    z, rows, vocab, ld = _rows_of(logits, "logits", dev)
+    d, d_rows, d_vocab, ld_d = _rows_of(d_logits, "d_logits", dev)
     if (d_rows, d_vocab) != (rows, vocab):
         raise ValueError("d_logits must have the shape of logits")
-    _here(stats, "stats", _F32, (rows, 2))
-    for t, what, dtype in ((targets, "targets", _I32), (entropy, "entropy", _F32),
-                           (d_logp, "d_logp", _F32), (d_entropy, "d_entropy", _F32),
-                           (d_lse, "d_lse", _F32)):
-        if t is not None:
-            _here(t, what, dtype, (rows,))
-    _check(lib().rdt_token_logprobs_backward(_ptr(logits), _DTYPE[logits.dtype], ld, rows, vocab,
-                                             logit_scale, _ptr(targets), _ptr(stats),
-                                             _ptr(entropy), _ptr(d_logp), _ptr(d_entropy),
-                                             _ptr(d_lse), _ptr(d_logits),
-                                             _DTYPE[d_logits.dtype], ld_d, _stream(stream)))
+    one = (rows,)
+    _check(lib().rdt_token_logprobs_backward(
+        z, _DTYPE[logits.dtype], ld, rows, vocab, logit_scale,
+        None if targets is None else _here(targets, "targets", _I32, one, dev),
+        _here(stats, "stats", _F32, (rows, 2), dev),
+        None if entropy is None else _here(entropy, "entropy", _F32, one, dev),
+        None if d_logp is None else _here(d_logp, "d_logp", _F32, one, dev),
+        None if d_entropy is None else _here(d_entropy, "d_entropy", _F32, one, dev),
+        None if d_lse is None else _here(d_lse, "d_lse", _F32, one, dev),
+        d, _DTYPE[d_logits.dtype], ld_d, _stream(stream)))
 
 
 def head_logprobs_workspace_bytes(cfg: Config, tokens: int) -> int:
@@ -369,23 +384,22 @@ def head_logprobs(cfg, h, gamma_f, w_lm, ws, targets=None, logp=None, entropy=No
     """token_logprobs of the LM head's logits for hidden states h fp32 [tokens, hidden]
     (rdt_head_logprobs): final RMSNorm, head, scores; the logits are held a chunk of rows
     at a time in ws."""
+    dev = _device(h, "h")
     tokens = h.shape[0]
+    one = (tokens,)
     top = 0 if top_ids is None else top_ids.shape[-1]
-    _here(h, "h", _F32, (tokens, cfg.hidden))
-    _here(gamma_f, "gamma_f", _F32, (cfg.hidden,))
-    _here(w_lm, "w_lm", (torch.bfloat16,), (cfg.vocab, cfg.hidden))
-    for t, what, dtype in ((targets, "targets", _I32), (logp, "logp", _F32),
-                           (entropy, "entropy", _F32), (lse, "lse", _F32)):
-        if t is not None:
-            _here(t, what, dtype, (tokens,))
-    if top_ids is not None:
-        _here(top_ids, "top_ids", _I32, (tokens, top))
-    if top_logp is not None:
-        _here(top_logp, "top_logp", _F32, (tokens, top))
-    _check(lib().rdt_head_logprobs(ctypes.byref(cfg), tokens, _ptr(h), _ptr(gamma_f), _ptr(w_lm),
-                                   logit_scale, _ptr(targets), _ptr(logp), _ptr(entropy),
-                                   _ptr(lse), top, _ptr(top_ids), _ptr(top_logp), _ptr(ws),
-                                   ws.numel() * ws.element_size(), _stream(stream)))
+    _check(lib().rdt_head_logprobs(
+        ctypes.byref(cfg), tokens, _here(h, "h", _F32, (tokens, cfg.hidden), dev),
+        _here(gamma_f, "gamma_f", _F32, (cfg.hidden,), dev),
+        _here(w_lm, "w_lm", (torch.bfloat16,), (cfg.vocab, cfg.hidden), dev), logit_scale,
+        None if targets is None else _here(targets, "targets", _I32, one, dev),
+        None if logp is None else _here(logp, "logp", _F32, one, dev),
+        None if entropy is None else _here(entropy, "entropy", _F32, one, dev),
+        None if lse is None else _here(lse, "lse", _F32, one, dev), top,
+        None if top_ids is None else _here(top_ids, "top_ids", _I32, (tokens, top), dev),
+        None if top_logp is None else _here(top_logp, "top_logp", _F32, (tokens, top), dev),
+        _here(ws, "ws", (ws.dtype,), None, dev), ws.numel() * ws.element_size(),
+        _stream(stream)))
 
 
 # ------------------------------------------------- many tensors: clip and AdamW
@@ -414,22 +428,25 @@ class OptTensors:
         if moment not in (torch.float32, torch.uint8, torch.float8_e4m3fn):
             raise ValueError(f"moments of type {moment}")
         self.device = g[0].get_device() if count else None
+        self.g_code = _DTYPE.get(self.g_dtype, -1)
         self.entries = (OptTensor * max(count, 1))()
         self.count = count
+        sizes = [t.numel() for t in self.tensors["g"]]
+        runs = [-(-n // STATE_RUN) for n in sizes]
         for name, column in self.tensors.items():
             if len(column) != count:
                 raise ValueError(f"{len(column)} tensors in {name}, {count} in g")
-            for e, t, gi in zip(self.entries, column, self.tensors["g"]):
-                n = gi.numel()
-                want = -(-n // STATE_RUN) if name.endswith("_scale") else n
-                if t.dtype != types[name] or t.numel() != want or not t.is_contiguous():
-                    raise ValueError(f"{name}: want {want} contiguous elements of {types[name]}, "
+            dtype = types[name]
+            for e, t, want in zip(self.entries, column,
+                                  runs if name.endswith("_scale") else sizes):
+                if t.dtype != dtype or t.numel() != want or not t.is_contiguous():
+                    raise ValueError(f"{name}: want {want} contiguous elements of {dtype}, "
                                      f"got {tuple(t.shape)} of {t.dtype}")
-                if not t.is_cuda or t.get_device() != self.device:
+                if t.get_device() != self.device or self.device < 0:
                     raise ValueError(f"{name}: every tensor must be on one CUDA device")
                 setattr(e, name, t.data_ptr())
-        for e, gi in zip(self.entries, self.tensors["g"]):
-            e.n = gi.numel()
+        for e, n in zip(self.entries, sizes):
+            e.n = n
         self.set_lr(lr)
         self.set_weight_decay(weight_decay)
 
@@ -449,8 +466,10 @@ class OptTensors:
         self._fill("weight_decay", weight_decay)
 
     def _on_device(self):
-        if self.device is not None and self.device != torch.cuda.current_device():
+        device = torch.cuda.current_device()
+        if self.device is not None and self.device != device:
             raise ValueError("the tensors are not on the current CUDA device")
+        return device
 
 
 def tensors_sq_sum_workspace_bytes(tensors: OptTensors) -> int:
@@ -459,12 +478,11 @@ def tensors_sq_sum_workspace_bytes(tensors: OptTensors) -> int:
 
 def tensors_sq_sum(tensors: OptTensors, sumsq, ws, stream=None):
     """sumsq (fp64 device scalar) = the squared sum of every gradient of the list."""
-    tensors._on_device()
-    _here(sumsq, "sumsq", (torch.float64,))
-    _here(ws, "ws", (ws.dtype,))
-    _check(lib().rdt_tensors_sq_sum(tensors.entries, tensors.count, _DTYPE[tensors.g_dtype],
-                                    _ptr(sumsq), _ptr(ws), ws.numel() * ws.element_size(),
-                                    _stream(stream)))
+    dev = tensors._on_device()
+    _check(lib().rdt_tensors_sq_sum(tensors.entries, tensors.count, tensors.g_code,
+                                    _here(sumsq, "sumsq", (torch.float64,), None, dev),
+                                    _here(ws, "ws", (ws.dtype,), None, dev),
+                                    ws.numel() * ws.element_size(), _stream(stream)))
 
 
 def tensors_adamw(tensors: OptTensors, step, beta1, beta2, eps, scale=None, skip=None,
@@ -476,15 +494,14 @@ def tensors_adamw(tensors: OptTensors, step, beta1, beta2, eps, scale=None, skip
         raise ValueError("the list has no moments")
     if seed is not None and not 0 <= seed < 1 << 32:
         raise ValueError("seed must be in [0, 2^32)")
-    tensors._on_device()
-    for t, what, dtype in ((scale, "scale", _F32), (skip, "skip", _I32),
-                           (step_dev, "step_dev", _I32)):
-        if t is not None:
-            _here(t, what, dtype)
-    _check(lib().rdt_tensors_adamw(tensors.entries, tensors.count, _DTYPE[tensors.g_dtype],
-                                   tensors.state_bits, -1 if seed is None else seed, _ptr(scale),
-                                   _ptr(skip), int(step or 0), _ptr(step_dev), beta1, beta2, eps,
-                                   _stream(stream)))
+    dev = tensors._on_device()
+    _check(lib().rdt_tensors_adamw(
+        tensors.entries, tensors.count, tensors.g_code, tensors.state_bits,
+        -1 if seed is None else seed,
+        None if scale is None else _here(scale, "scale", _F32, None, dev),
+        None if skip is None else _here(skip, "skip", _I32, None, dev), int(step or 0),
+        None if step_dev is None else _here(step_dev, "step_dev", _I32, None, dev), beta1, beta2,
+        eps, _stream(stream)))
 
 
 # ------------------------------------------------- NF4 + LoRA block
