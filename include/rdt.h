@@ -481,16 +481,18 @@ rdt_status rdt_head_logprobs(const rdt_config* cfg, int32_t tokens, const float*
  * call writes (entries whose w overlap are rejected).
  *
  * rdt_tensors_sq_sum: *sumsq = sum over all g of g^2, relative error
- *   below 1e-12 where the squares lie in [1e-30, 1e38] (they are formed in
- *   fp32, with their rounding errors kept); order of summation fixed by the
- *   sizes. Only g and n of each entry are read. For
+ *   below 1e-12 where each square is 0 or at least 1e-30 and the sum at most
+ *   1e38 (it is formed in fp32 with the rounding errors kept; a larger one may
+ *   come out as not finite); order of summation fixed by the sizes. Only g and n of each entry are read. For
  *   rdt_clip_scale. ws: rdt_tensors_sq_sum_workspace_bytes(tensors, count)
  *   bytes, 8-byte aligned.
  *
  * rdt_tensors_adamw, step t (>= 1, or *step_dev), each operation rounded to
- * fp32 in this order, so the result does not depend on the launch:
+ * fp32 in this order (the quotient by a reciprocal, relative error below
+ * 2^-22):
  *   g' = g scale;  m = b1 m + (1 - b1) g';  v = b2 v + ((1 - b2) g') g'
  *   w = w (1 - lr weight_decay) - (m / (sqrt(v) / sqrt(1 - b2^t) + eps)) (lr / (1 - b1^t))
+ * with b1 and b2 in [0, 1) and eps in [1e-30, 1e30]
  * (1 - b1, 1 - b2, 1 / (1 - b1^t) and 1 / sqrt(1 - b2^t) are formed in double
  * and rounded once; sqrt(v) is multiplied by the last.) w_bf16, where not
  * null, receives the bf16 copy of w. scale, skip_flag and step_dev as in

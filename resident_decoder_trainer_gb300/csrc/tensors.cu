@@ -21,8 +21,10 @@ namespace {
 constexpr int kRun = 256;            // elements that share one scale of an 8-bit state
 constexpr int kThreads = 256;
 constexpr int kTile = 8 * kThreads;  // elements of a CTA's tile: one run per warp, 8 per lane
-// Tensors per launch: the table stays inside the 32,764 bytes of parameters a kernel may have.
+// Tensors per launch: the table stays inside the 32,764 bytes of parameters a
+// kernel may have. Short lists take the short table, whose launch copies less.
 constexpr int kMaxTensors = 400;
+constexpr int kFewTensors = 32;
 
 struct Tensor {
   float* w;
@@ -36,22 +38,68 @@ struct Tensor {
   float lr, wd;
 };
 
+template <int kMax>
 struct Table {
-  Tensor t[kMaxTensors];
-  int32_t end[kMaxTensors];  // tiles up to and including tensor i
-  int32_t first;             // index of t[0] in the caller's list
+  Tensor t[kMax];
+  int32_t end[kMax];  // tiles up to and including tensor i
+  int32_t first;      // index of t[0] in the caller's list
   int32_t count;
 };
-static_assert(sizeof(Table) + 128 <= 32764, "the table must fit the kernel parameters");
+static_assert(sizeof(Table<kMaxTensors>) + 128 <= 32764, "the table must fit the parameters");
 
-// The tensor that owns a tile: the first whose end is above it.
-__device__ __forceinline__ int owner_of(const Table& tab, int tile) {
-  int lo = 0, hi = tab.count - 1;
+// f(tensor, its place in the table, tile within it, tiles) for the tiles of
+// this CTA: a contiguous share of all, tensor after tensor, so the table is
+// searched once (a search for every tile of a grid-wide stride took five times
+// as long on 500 small tensors).
+template <int kMax, typename F>
+__device__ __forceinline__ void for_each_span(const Table<kMax>& tab, int tiles, F f) {
+  int tile = static_cast<int>(static_cast<int64_t>(tiles) * blockIdx.x / gridDim.x);
+  const int last = static_cast<int>(static_cast<int64_t>(tiles) * (blockIdx.x + 1) / gridDim.x);
+  if (tile >= last) return;
+  int lo = 0, hi = tab.count - 1;  // the first tensor whose end is above the tile
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
     if (tab.end[mid] > tile) hi = mid; else lo = mid + 1;
   }
-  return lo;
+  int begin = lo ? tab.end[lo - 1] : 0;
+  for (; tile < last; ++lo) {
+    const int end = tab.end[lo], stop = min(end, last);
+    if (tile < stop) f(tab.t[lo], lo, tile - begin, stop - tile);
+    tile = stop;
+    begin = end;
+  }
+}
+
+// Two fp32 operations, each rounded to nearest, in one instruction.
+__device__ __forceinline__ uint64_t bits2(float2 a) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
+}
+__device__ __forceinline__ float2 floats2(uint64_t a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return floats2(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return floats2(r);
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+// A pair's product and the sum it goes into would be contracted to one fma,
+// the .rn of both notwithstanding; a sum that is an fma itself, with a 1 the
+// compiler does not know, is not.
+__device__ __forceinline__ float2 add2(float2 a, float2 b, float one) {
+  return fma2(a, both(one), b);
+}
+__device__ __forceinline__ float2 sub2(float2 a, float2 b, float one) {
+  return fma2(b, both(-one), a);
 }
 
 // A lane's eight elements of its warp's run are two groups of four, 128
@@ -147,43 +195,62 @@ __device__ __forceinline__ void store8(uint8_t* p, int have, const uint32_t* c) 
   }
 }
 
-// hi + lo += x x, with the rounding errors of the product and of the sum kept
-// in lo: a sum of n squares is right to about n 2^-48. (fp64 has 1/64 of
-// fp32's rate here: the same sum in fp64 took 1.82 ms for 490 M fp32 values.)
-__device__ __forceinline__ void add_square(float x, float& hi, float& lo) {
-  const float p = __fmul_rn(x, x);
-  const float e = __fmaf_rn(x, x, -p);
-  const float t = __fadd_rn(hi, p);
-  const float b = __fsub_rn(t, hi);
-  const float c = __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(p, b));
+// hi + lo += x x for two elements at once, with the rounding errors of the
+// product and of the sum kept in lo: a sum of n squares is right to about
+// n 2^-48. (fp64 has 1/64 of fp32's rate here: the same sum in fp64 took
+// 1.82 ms for 490 M fp32 values.) kExact: x x has no rounding error (bf16).
+template <bool kExact>
+__device__ __forceinline__ void add_squares(float2 x, float2& hi, float2& lo, float one) {
+  const float2 p = mul2(x, x);
+  const float2 t = add2(hi, p, one);
+  const float2 b = sub2(t, hi, one);
+  float2 c = add2(sub2(hi, sub2(t, b, one), one), sub2(p, b, one), one);
+  if (!kExact) c = add2(c, fma2(x, x, make_float2(-p.x, -p.y)), one);
   hi = t;
-  lo = __fadd_rn(lo, __fadd_rn(c, e));
+  lo = add2(lo, c, one);
 }
 
-template <bool kBf16>
+template <bool kBf16, int kMax>
 __global__ void __launch_bounds__(kThreads) tensors_sq_sum_kernel(
-    const __grid_constant__ Table tab, int tiles, double* __restrict__ partials) {
+    const __grid_constant__ Table<kMax> tab, int tiles, float one,
+    double* __restrict__ partials) {
   __shared__ double red[kThreads / 32];
   using G = typename std::conditional<kBf16, bf16, float>::type;
+  constexpr int kAhead = 4;  // tiles whose loads are under way
   const int at = (threadIdx.x >> 5) * kRun + (threadIdx.x & 31) * 4;
-  float hi[4] = {0.f, 0.f, 0.f, 0.f}, lo[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int o = owner_of(tab, tile);
-    const Tensor& t = tab.t[o];
-    const int64_t first = static_cast<int64_t>(tile - (o ? tab.end[o - 1] : 0)) * kTile;
-    const G* g = static_cast<const G*>(t.g) + first + at;
-    const int64_t left = t.n - first;
-    float x[8];
-    if (left >= kTile)
-      load8<true>(g, 0, x);
-    else
-      load8<false>(g, static_cast<int>(left) - at, x);
+  float2 hi[4] = {}, lo[4] = {};
+  auto add = [&](const float* x) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) add_square(x[k], hi[k & 3], lo[k & 3]);
-  }
+    for (int k = 0; k < 4; ++k)
+      add_squares<kBf16>(make_float2(x[2 * k], x[2 * k + 1]), hi[k], lo[k], one);
+  };
+  for_each_span(tab, tiles, [&](const Tensor& t, int, int tile, int count) {
+    int64_t left = t.n - static_cast<int64_t>(tile) * kTile;
+    const G* g = static_cast<const G*>(t.g) + static_cast<int64_t>(tile) * kTile + at;
+    for (; count >= kAhead && left >= kAhead * kTile; count -= kAhead) {
+      float x[kAhead][8];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) load8<true>(g + u * kTile, 0, x[u]);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) add(x[u]);
+      g += kAhead * kTile;
+      left -= kAhead * kTile;
+    }
+    for (; count > 0; --count) {
+      float x[8];
+      if (left >= kTile)
+        load8<true>(g, 0, x);
+      else
+        load8<false>(g, static_cast<int>(left) - at, x);
+      add(x);
+      g += kTile;
+      left -= kTile;
+    }
+  });
   double acc = 0.0;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) acc += static_cast<double>(hi[k]) + static_cast<double>(lo[k]);
+  for (int k = 0; k < 4; ++k)
+    acc += (static_cast<double>(hi[k].x) + hi[k].y) + (static_cast<double>(lo[k].x) + lo[k].y);
   acc = warp_sum_d(acc);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = acc;
   __syncthreads();
@@ -210,7 +277,7 @@ __global__ void __launch_bounds__(kThreads) tensors_sq_final_kernel(
 }
 
 struct AdamArgs {
-  float b1, b2, omb1, omb2, inv_bc1, inv_root_bc2, eps;
+  float b1, b2, omb1, omb2, inv_bc1, inv_root_bc2, eps, one;
   const float* scale;
   const int32_t* skip;
   const int32_t* step_dev;
@@ -254,15 +321,20 @@ __device__ __forceinline__ uint32_t mix(uint32_t x) {
 }
 
 // |x| <= 448 up or down to a neighbouring e4m3 value with the probability of
-// the distance: 20 of fp32's 23 mantissa bits go, so a number of 20 bits, the
-// upper 16 random, is added and the 20 are cut. Below 2^-6 e4m3 has the steps
-// of [2^-6, 2^-5), hence the shift by 2^-6.
-__device__ __forceinline__ float round_random(float x, uint32_t half) {
-  const float a = fabsf(x);
-  const float low = a < 0x1p-6f ? 0x1p-6f : 0.f;
-  const uint32_t b = __float_as_uint(__fadd_rn(a, low)) + half * 16u + 8u;
-  const float r = __fsub_rn(__uint_as_float(b & 0xfff00000u), low);
-  return copysignf(fminf(r, kE4m3Max), x);
+// the distance: 20 of fp32's 23 mantissa bits go, so a number of 20 bits (16
+// random ones, then 1000) is added and the 20 are cut. Below 2^-6 e4m3 has the
+// steps of [2^-6, 2^-5), hence the shift by 2^-6. Not for NaN.
+__device__ __forceinline__ float round_random(float x, uint32_t bits20) {
+  const float low = fabsf(x) < 0x1p-6f ? 0x1p-6f : 0.f;
+  const uint32_t b = __float_as_uint(__fadd_rn(fabsf(x), low)) + bits20;
+  const float r = fminf(__fsub_rn(__uint_as_float(b & 0xfff00000u), low), kE4m3Max);
+  return __uint_as_float(__float_as_uint(r) | (__float_as_uint(x) & 0x80000000u));
+}
+// 1 / x to 1 ulp.
+__device__ __forceinline__ float reciprocal(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 // The run's scale from its largest magnitude, and the factor to code units.
@@ -300,25 +372,34 @@ __device__ __forceinline__ void adamw_run(const Tensor& t, int64_t first, const 
       e4m3_decode4(vc[h], r + 4 * h);
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      m[k] = __fmul_rn(m[k], ms);
-      r[k] = __fmul_rn(r[k], vs);
-      r[k] = __fmul_rn(r[k], r[k]);
+    for (int k = 0; k < 8; k += 2) {
+      const float2 a = mul2(make_float2(m[k], m[k + 1]), both(ms));
+      const float2 b = mul2(make_float2(r[k], r[k + 1]), both(vs));
+      const float2 q = mul2(b, b);
+      m[k] = a.x; m[k + 1] = a.y;
+      r[k] = q.x; r[k + 1] = q.y;
     }
   }
   const float rate = __fmul_rn(t.lr, inv_bc1), keep = __fsub_rn(1.f, __fmul_rn(t.lr, t.wd));
   float big_m = 0.f, big_r = 0.f;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float gs = __fmul_rn(g[k], sc);
-    m[k] = __fadd_rn(__fmul_rn(m[k], p.b1), __fmul_rn(gs, p.omb1));
-    const float v = __fadd_rn(__fmul_rn(r[k], p.b2), __fmul_rn(__fmul_rn(gs, p.omb2), gs));
-    const float root = __fsqrt_rn(v);
-    const float u = __fdiv_rn(m[k], __fadd_rn(__fmul_rn(root, inv_root_bc2), p.eps));
-    w[k] = __fsub_rn(__fmul_rn(w[k], keep), __fmul_rn(u, rate));
-    r[k] = kBits == 32 ? v : root;
-    big_m = fmaxf(big_m, fabsf(m[k]));
-    big_r = fmaxf(big_r, root);
+  for (int k = 0; k < 8; k += 2) {
+    const float2 gs = mul2(make_float2(g[k], g[k + 1]), both(sc));
+    const float2 mm = add2(mul2(make_float2(m[k], m[k + 1]), both(p.b1)),
+                           mul2(gs, both(p.omb1)), p.one);
+    const float2 v = add2(mul2(make_float2(r[k], r[k + 1]), both(p.b2)),
+                          mul2(mul2(gs, both(p.omb2)), gs), p.one);
+    const float2 root = make_float2(__fsqrt_rn(v.x), __fsqrt_rn(v.y));
+    const float2 den = add2(mul2(root, both(inv_root_bc2)), both(p.eps), p.one);
+    const float2 u = mul2(mm, make_float2(reciprocal(den.x), reciprocal(den.y)));
+    const float2 x = sub2(mul2(make_float2(w[k], w[k + 1]), both(keep)), mul2(u, both(rate)),
+                          p.one);
+    w[k] = x.x; w[k + 1] = x.y;
+    m[k] = mm.x; m[k + 1] = mm.y;
+    r[k] = kBits == 32 ? v.x : root.x;
+    r[k + 1] = kBits == 32 ? v.y : root.y;
+    big_m = fmaxf(big_m, fmaxf(fabsf(mm.x), fabsf(mm.y)));
+    big_r = fmaxf(big_r, fmaxf(root.x, root.y));
   }
   store8<kFull>(t.w + i, have, w);
   if (t.wb) store8<kFull>(t.wb + i, have, w);
@@ -333,17 +414,38 @@ __device__ __forceinline__ void adamw_run(const Tensor& t, int64_t first, const 
       t.m_scale[run] = ms;
       t.v_scale[run] = vs;
     }
+    // no sqrt(v) > 0 becomes 0, but in a run that is stored as zeros
+    const float least = uv > 0.f ? kE4m3Tiny : 0.f;
+    bool nan = false;
+    if (kRandom) {
+      // NaN does not go through round_random; a sum shows it (so does one that leaves fp32's
+      // range, which costs the slow way only)
+      float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      float qm = __fmul_rn(m[k], um), qr = __fmul_rn(r[k], uv);
+      for (int k = 0; k < 8; k += 2)
+        sum = fma2(make_float2(m[k], m[k + 1]), make_float2(r[k], r[k + 1]), sum);
+      nan = !(fabsf(sum.x + sum.y) < INFINITY);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+      const float2 qm = mul2(make_float2(m[k], m[k + 1]), both(um));
+      float2 qr = mul2(make_float2(r[k], r[k + 1]), both(uv));
+      m[k] = qm.x; m[k + 1] = qm.y;
+      float2 qx = qr;
       if constexpr (kRandom) {
-        const uint32_t x = mix(static_cast<uint32_t>(i + (k & 3) + 32 * (k & 4)) ^ key);
-        qm = qm != qm ? qm : round_random(fminf(fmaxf(qm, -kE4m3Max), kE4m3Max), x & 0xffffu);
-        qr = qr != qr ? qr : round_random(fminf(qr, kE4m3Max), x >> 16);
+        const uint32_t at = static_cast<uint32_t>(i + (k & 3) + 32 * (k & 4));
+        const uint32_t x0 = mix(at ^ key), x1 = mix((at + 1) ^ key);
+        const float2 rm = make_float2(round_random(qm.x, (x0 << 4 & 0xffff0u) | 8u),
+                                      round_random(qm.y, (x1 << 4 & 0xffff0u) | 8u));
+        const float2 rr = make_float2(round_random(qr.x, (x0 >> 12 & 0xffff0u) | 8u),
+                                      round_random(qr.y, (x1 >> 12 & 0xffff0u) | 8u));
+        if (!nan || qm.x == qm.x) m[k] = rm.x;
+        if (!nan || qm.y == qm.y) m[k + 1] = rm.y;
+        if (!nan || qr.x == qr.x) qx.x = rr.x;
+        if (!nan || qr.y == qr.y) qx.y = rr.y;
       }
-      if (r[k] > 0.f && uv > 0.f && qr < kE4m3Tiny) qr = kE4m3Tiny;
-      m[k] = qm;
-      r[k] = qr;
+      r[k] = r[k] > 0.f ? fmaxf(qx.x, least) : qx.x;
+      r[k + 1] = r[k + 1] > 0.f ? fmaxf(qx.y, least) : qx.y;
     }
     uint32_t mc[2] = {e4m3_encode4(m), e4m3_encode4(m + 4)};
     uint32_t vc[2] = {e4m3_encode4(r), e4m3_encode4(r + 4)};
@@ -352,9 +454,9 @@ __device__ __forceinline__ void adamw_run(const Tensor& t, int64_t first, const 
   }
 }
 
-template <int kBits, bool kBf16, bool kRandom>
+template <int kBits, bool kBf16, bool kRandom, int kMax>
 __global__ void __launch_bounds__(kThreads) tensors_adamw_kernel(
-    const __grid_constant__ Table tab, int tiles, const AdamArgs p) {
+    const __grid_constant__ Table<kMax> tab, int tiles, const AdamArgs p) {
   if (p.skip && *p.skip) return;
   const float sc = p.scale ? *p.scale : 1.f;
   float inv_bc1 = p.inv_bc1, inv_root_bc2 = p.inv_root_bc2;
@@ -366,17 +468,17 @@ __global__ void __launch_bounds__(kThreads) tensors_adamw_kernel(
         1.0 / sqrt(1.0 - pow(static_cast<double>(p.b2), static_cast<double>(step))));
   }
   const uint32_t key0 = mix(mix(static_cast<uint32_t>(step)) + p.seed) + tab.first;
-  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int o = owner_of(tab, tile);
-    const Tensor& t = tab.t[o];
-    const int64_t first = static_cast<int64_t>(tile - (o ? tab.end[o - 1] : 0)) * kTile +
-                          (threadIdx.x >> 5) * kRun;
-    const uint32_t key = mix(key0 + o) ^ static_cast<uint32_t>(first >> 32) * 0x9E3779B1u;
-    if (first + kRun <= t.n)
-      adamw_run<kBits, kBf16, kRandom, true>(t, first, p, sc, inv_bc1, inv_root_bc2, key);
-    else if (first < t.n)
-      adamw_run<kBits, kBf16, kRandom, false>(t, first, p, sc, inv_bc1, inv_root_bc2, key);
-  }
+  for_each_span(tab, tiles, [&](const Tensor& t, int o, int tile, int count) {
+    const uint32_t key_o = mix(key0 + o);
+    int64_t first = static_cast<int64_t>(tile) * kTile + (threadIdx.x >> 5) * kRun;
+    for (; count > 0; --count, first += kTile) {
+      const uint32_t key = key_o ^ static_cast<uint32_t>(first >> 32) * 0x9E3779B1u;
+      if (first + kRun <= t.n)
+        adamw_run<kBits, kBf16, kRandom, true>(t, first, p, sc, inv_bc1, inv_root_bc2, key);
+      else if (first < t.n)
+        adamw_run<kBits, kBf16, kRandom, false>(t, first, p, sc, inv_bc1, inv_root_bc2, key);
+    }
+  });
 }
 
 rdt_status refuse(const char* msg) {
@@ -406,17 +508,19 @@ const char* list_problem(const rdt_opt_tensor* t, int count, int g_dtype) {
 }
 
 // Calls f(table, tiles) for each launch's share of the list.
-template <typename F>
+template <int kMax, typename F>
 cudaError_t each_launch(const rdt_opt_tensor* list, int count, F f) {
-  Table tab;
+  Table<kMax> tab;
   int64_t tiles = 0;
   tab.count = 0;
   tab.first = 0;
   for (int i = 0; i <= count; ++i) {
     const int64_t more = i < count ? tiles_of(list[i].n) : 0;
-    if (tab.count && (i == count || tab.count == kMaxTensors || tiles + more > INT32_MAX)) {
-      const cudaError_t e = f(tab, static_cast<int>(tiles));
-      if (e != cudaSuccess) return e;
+    if (tab.count && (i == count || tab.count == kMax || tiles + more > INT32_MAX)) {
+      if (tiles > 0) {
+        const cudaError_t e = f(tab, static_cast<int>(tiles));
+        if (e != cudaSuccess) return e;
+      }
       tab.count = 0;
       tiles = 0;
     }
@@ -432,8 +536,39 @@ cudaError_t each_launch(const rdt_opt_tensor* list, int count, F f) {
   return cudaSuccess;
 }
 
-int sq_blocks(int64_t tiles) {
-  return static_cast<int>(std::min<int64_t>(std::max<int64_t>(tiles, 1), 4LL * num_sms()));
+// One resident wave of CTAs: 8 of 256 threads an SM at most.
+int wave(int tiles) { return static_cast<int>(std::min<int64_t>(tiles, 8LL * num_sms())); }
+
+constexpr int kMaxPartials = 2048;  // of one launch
+
+template <int kMax>
+cudaError_t sq_sum_launches(const rdt_opt_tensor* list, int count, bool half, double* parts,
+                            int64_t room, int64_t* used, cudaStream_t s) {
+  return each_launch<kMax>(list, count, [&](const Table<kMax>& tab, int tiles) {
+    const int blocks = std::min(wave(tiles), kMaxPartials);
+    if (*used + blocks > room) return cudaErrorInvalidValue;
+    note_launch();
+    auto kernel = half ? tensors_sq_sum_kernel<true, kMax> : tensors_sq_sum_kernel<false, kMax>;
+    kernel<<<blocks, kThreads, 0, s>>>(tab, tiles, 1.f, parts + *used);
+    *used += blocks;
+    return cudaGetLastError();
+  });
+}
+
+template <int kMax>
+cudaError_t adamw_launches(const rdt_opt_tensor* list, int count, bool half, int bits, bool random,
+                           const AdamArgs& a, cudaStream_t s) {
+  return each_launch<kMax>(list, count, [&](const Table<kMax>& tab, int tiles) {
+    note_launch();
+    auto kernel = bits == 32 ? (half ? tensors_adamw_kernel<32, true, false, kMax>
+                                     : tensors_adamw_kernel<32, false, false, kMax>)
+                  : random   ? (half ? tensors_adamw_kernel<8, true, true, kMax>
+                                     : tensors_adamw_kernel<8, false, true, kMax>)
+                             : (half ? tensors_adamw_kernel<8, true, false, kMax>
+                                     : tensors_adamw_kernel<8, false, false, kMax>);
+    kernel<<<wave(tiles), kThreads, 0, s>>>(tab, tiles, a);
+    return cudaGetLastError();
+  });
 }
 
 }  // namespace
@@ -446,8 +581,8 @@ extern "C" {
 
 size_t rdt_tensors_sq_sum_workspace_bytes(const rdt_opt_tensor* tensors, int32_t count) {
   if (list_problem(tensors, count, RDT_F32)) return 0;
-  // one partial sum for each block of each launch (num_sms() is not asked: no device needed)
-  return (static_cast<size_t>(count) / kMaxTensors + 2) * 1024 * sizeof(double);
+  // one partial sum for each block of each launch (no device is asked how many there are)
+  return (static_cast<size_t>(count) / kMaxTensors + 1) * kMaxPartials * sizeof(double);
 }
 
 rdt_status rdt_tensors_sq_sum(const rdt_opt_tensor* tensors, int32_t count, int32_t g_dtype,
@@ -462,18 +597,11 @@ rdt_status rdt_tensors_sq_sum(const rdt_opt_tensor* tensors, int32_t count, int3
   double* parts = static_cast<double*>(ws);
   int64_t used = 0;
   const int64_t room = static_cast<int64_t>(ws_bytes / sizeof(double));
-  cudaError_t e = each_launch(tensors, count, [&](const Table& tab, int tiles) {
-    if (tiles == 0) return cudaSuccess;
-    const int blocks = static_cast<int>(std::min<int64_t>(sq_blocks(tiles), 1024));
-    if (used + blocks > room) return cudaErrorInvalidValue;
-    note_launch();
-    if (g_dtype == RDT_BF16)
-      tensors_sq_sum_kernel<true><<<blocks, kThreads, 0, s>>>(tab, tiles, parts + used);
-    else
-      tensors_sq_sum_kernel<false><<<blocks, kThreads, 0, s>>>(tab, tiles, parts + used);
-    used += blocks;
-    return cudaGetLastError();
-  });
+  const bool half = g_dtype == RDT_BF16;
+  cudaError_t e =
+      count <= kFewTensors
+          ? sq_sum_launches<kFewTensors>(tensors, count, half, parts, room, &used, s)
+          : sq_sum_launches<kMaxTensors>(tensors, count, half, parts, room, &used, s);
   if (e != cudaSuccess) return launched(e);
   note_launch();
   tensors_sq_final_kernel<<<1, kThreads, 0, s>>>(parts, static_cast<int>(used), sumsq);
@@ -488,8 +616,9 @@ rdt_status rdt_tensors_adamw(const rdt_opt_tensor* tensors, int32_t count, int32
   if (state_bits != 32 && state_bits != 8) return refuse("state_bits must be 32 or 8");
   if (seed >= (int64_t(1) << 32)) return refuse("seed must be below 2^32");
   if (!step_dev && step < 1) return refuse("step must be >= 1 (bias correction)");
-  if (!(beta1 >= 0.f && beta1 < 1.f) || !(beta2 >= 0.f && beta2 < 1.f) || !(eps >= 0.f))
-    return refuse("beta1 and beta2 must be in [0, 1) and eps >= 0");
+  if (!(beta1 >= 0.f && beta1 < 1.f) || !(beta2 >= 0.f && beta2 < 1.f) ||
+      !(eps >= 1e-30f && eps <= 1e30f))
+    return refuse("beta1 and beta2 must be in [0, 1) and eps in [1e-30, 1e30]");
   if ((reinterpret_cast<uintptr_t>(scale) | reinterpret_cast<uintptr_t>(skip_flag) |
        reinterpret_cast<uintptr_t>(step_dev)) & 3)
     return refuse("scale, skip_flag and step_dev must be 4-byte aligned");
@@ -537,26 +666,18 @@ rdt_status rdt_tensors_adamw(const rdt_opt_tensor* tensors, int32_t count, int32
   a.inv_root_bc2 =
       static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(static_cast<double>(beta2), a.step)));
   a.eps = eps;
+  a.one = 1.f;
   a.scale = scale;
   a.skip = skip_flag;
   a.step_dev = step_dev;
   a.seed = seed < 0 ? 0u : static_cast<uint32_t>(seed);
   const bool random = seed >= 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return launched(each_launch(tensors, count, [&](const Table& tab, int tiles) {
-    if (tiles == 0) return cudaSuccess;
-    const int blocks = static_cast<int>(std::min<int64_t>(tiles, 8LL * num_sms()));
-    note_launch();
-    const bool half = g_dtype == RDT_BF16;
-    auto kernel = state_bits == 32 ? (half ? tensors_adamw_kernel<32, true, false>
-                                           : tensors_adamw_kernel<32, false, false>)
-                  : random ? (half ? tensors_adamw_kernel<8, true, true>
-                                   : tensors_adamw_kernel<8, false, true>)
-                           : (half ? tensors_adamw_kernel<8, true, false>
-                                   : tensors_adamw_kernel<8, false, false>);
-    kernel<<<blocks, kThreads, 0, s>>>(tab, tiles, a);
-    return cudaGetLastError();
-  }));
+  const bool half = g_dtype == RDT_BF16;
+  return launched(
+      count <= kFewTensors
+          ? adamw_launches<kFewTensors>(tensors, count, half, state_bits, random, a, s)
+          : adamw_launches<kMaxTensors>(tensors, count, half, state_bits, random, a, s));
 }
 
 }  // extern "C"

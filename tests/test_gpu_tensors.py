@@ -141,7 +141,8 @@ def encode(x, half, floor):
 
 
 def by_the_header(old, i, problem, step, scale, seed):
-    """One tensor's step in the documented fp32 operations."""
+    """One tensor's state and bf16 copy after a step of the documented fp32 operations. Checks
+    its w, whose quotient is right to 2^-22 and whose last difference is rounded again."""
     n = problem.sizes[i]
     b1, b2, eps = f32(B1), f32(B2), f32(EPS)
     lr, wd = (torch.tensor(x, dtype=torch.float32, device="cuda") for x in (problem.lr[i],
@@ -156,8 +157,10 @@ def by_the_header(old, i, problem, step, scale, seed):
     m = m * b1 + g * f32(1.0 - b1)
     v = v * b2 + (g * f32(1.0 - b2)) * g
     root = torch.sqrt(v)
-    w = old["w"][i] * keep - (m / (root * f32(1.0 / math.sqrt(1.0 - b2 ** step)) + eps)) * rate
-    out = {"w": w, "wb": w.bfloat16()}
+    move = (m / (root * f32(1.0 / math.sqrt(1.0 - b2 ** step)) + eps)) * rate
+    w = old["w"][i] * keep - move
+    assert_near(problem.w.parts[i], w, 2.0 ** -22 * move.abs().double() + 2 * U * w.abs().double())
+    out = {"wb": problem.w.parts[i].bfloat16()}
     if problem.bits == 32:
         return {**out, "m": m, "v": v}
     up = (None, None)
@@ -167,6 +170,11 @@ def by_the_header(old, i, problem, step, scale, seed):
         up = (x & 0xFFFF, x >> 16)
     (mc, ms), (vc, vs) = encode(m, up[0], False), encode(root, up[1], True)
     return {**out, "m": mc, "ms": ms, "v": vc, "vs": vs}
+
+
+def assert_near(got, want, tol):
+    off = (got.double() - want.double()).abs() - tol
+    assert off.numel() == 0 or off.max() <= 0, float(off.max())
 
 
 def in_64_bits(old, i, problem, step, scale):

@@ -110,7 +110,7 @@ def adamw(lib, e, count, **change):
 @pytest.mark.parametrize("change,text", [
     (dict(g_dtype=2), b"g_dtype"), (dict(bits=16), b"state_bits"), (dict(seed=1 << 32), b"seed"),
     (dict(step=0), b"step"), (dict(b1=1.0), b"beta"), (dict(b2=-0.1), b"beta"),
-    (dict(b2=float("nan")), b"beta"), (dict(eps=-1.0), b"eps"), (dict(scale=P(2)), b"aligned"),
+    (dict(b2=float("nan")), b"beta"), (dict(eps=-1.0), b"eps"), (dict(eps=0.0), b"eps"), (dict(scale=P(2)), b"aligned"),
     (dict(step_dev=P(6)), b"aligned")])
 def test_tensors_adamw_refuses(lib, change, text):
     einval(lib, adamw(lib, entries({}), 1, **change), text)
