@@ -210,6 +210,13 @@ __device__ __forceinline__ void add_squares(float2 x, float2& hi, float2& lo, fl
   lo = add2(lo, c, one);
 }
 
+// hi + lo += h + l, the rounding error of hi + h kept in lo.
+__device__ __forceinline__ void add_pair(float& hi, float& lo, float h, float l) {
+  const float t = __fadd_rn(hi, h), b = __fsub_rn(t, hi);
+  lo += l + __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(h, b));
+  hi = t;
+}
+
 template <bool kBf16, int kMax>
 __global__ void __launch_bounds__(kThreads) tensors_sq_sum_kernel(
     const __grid_constant__ Table<kMax> tab, int tiles, float one,
@@ -247,12 +254,18 @@ __global__ void __launch_bounds__(kThreads) tensors_sq_sum_kernel(
       left -= kTile;
     }
   });
-  double acc = 0.0;
+  // down to one pair a warp in fp32: fp64 additions of every lane took 20 us
+  float h = hi[0].x, l = lo[0].x;
+  add_pair(h, l, hi[0].y, lo[0].y);
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    acc += (static_cast<double>(hi[k].x) + hi[k].y) + (static_cast<double>(lo[k].x) + lo[k].y);
-  acc = warp_sum_d(acc);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = acc;
+  for (int k = 1; k < 4; ++k) {
+    add_pair(h, l, hi[k].x, lo[k].x);
+    add_pair(h, l, hi[k].y, lo[k].y);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    add_pair(h, l, __shfl_xor_sync(0xffffffffu, h, o), __shfl_xor_sync(0xffffffffu, l, o));
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = static_cast<double>(h) + l;
   __syncthreads();
   if (threadIdx.x == 0) {
     double s = 0.0;
