@@ -294,7 +294,7 @@ struct LogprobArgs {
 constexpr int kMaxSplit = 8;  // CTAs that share a row (a cluster of the portable size)
 constexpr int kUnroll = 4;    // vectors a thread works on at once: a group
 constexpr int kStages = 3;    // groups a thread holds in shared memory
-constexpr int kSegments = 8;  // parts of a thread's groups whose maxima are kept
+constexpr int kSegments = 16; // parts of a thread's groups whose maxima are kept
 constexpr int kSample = 64;   // sets of threads whose maxima bound the row's alternatives
 constexpr int kKeys = 256;    // candidates that are ranked by counting
 
@@ -309,11 +309,17 @@ struct Shared<kThreads, true> {
   Sums part[kMaxSplit];
   unsigned long long parts[kMaxSplit][32];
   unsigned long long best[32];
-  unsigned long long key[kKeys];
-  float segment[kSegments][kThreads];
+  bf16 segment[kSegments][kThreads];  // rounded up
   float sample[kSample];
   float bound;
   int items, keys;
+};
+// What lies in the ring once the loop is through.
+template <int kThreads>
+struct Lists {
+  unsigned long long list[kThreads / 32][32];
+  unsigned long long key[kKeys];
+  uint16_t item[kSegments * kThreads];
 };
 
 // The CTA's sums from its threads', in every thread: the maximum first, one
@@ -370,13 +376,12 @@ __device__ __noinline__ Sums sums_of_any(const Row<T>& row, int v, int v1, float
 //
 // The loads run kStages - 1 groups ahead, each thread's into its own part of
 // `ring` (no barrier: a thread reads only what it copied). `segment`, where not
-// null, receives the maxima of kSegments runs of `length` groups (as they
-// are: -inf for none, NaN not seen).
+// null, receives the maxima of kSegments runs of `length` groups (-inf for
+// none, NaN not seen), rounded up to bf16, and `raw` the largest, not rounded.
 template <typename T, int kThreads>
 __device__ __forceinline__ Sums sums_of(const Row<T>& row, int v, int v1, float c, uint4* ring,
-                                        float (*segment)[kThreads], int length) {
+                                        bf16 (*segment)[kThreads], int length, float& raw) {
   constexpr int kPer = Vec<T>::kPer;
-  static_assert(kStages * kUnroll * 16 >= kSegments * 2 + 8, "the ring holds the lists");
   constexpr int kStep = kUnroll * kThreads;
   ring += threadIdx.x;
   auto fetch = [&](int g, int stage) {
@@ -412,7 +417,8 @@ __device__ __forceinline__ Sums sums_of(const Row<T>& row, int v, int v1, float 
     if (segment) {
       segment_m = fmaxf(segment_m, top);
       if (--left == 0) {
-        segment[filled++][threadIdx.x] = segment_m;
+        segment[filled++][threadIdx.x] = __float2bfloat16_ru(segment_m);
+        raw = fmaxf(raw, segment_m);
         segment_m = -INFINITY;
         left = length;
       }
@@ -432,11 +438,13 @@ __device__ __forceinline__ Sums sums_of(const Row<T>& row, int v, int v1, float 
       }
     }
   }
-  if (segment)
+  if (segment) {
+    raw = fmaxf(raw, segment_m);
     for (; filled < kSegments; ++filled) {
-      segment[filled][threadIdx.x] = segment_m;
+      segment[filled][threadIdx.x] = __float2bfloat16_ru(segment_m);
       segment_m = -INFINITY;
     }
+  }
   asm volatile("cp.async.wait_all;" ::: "memory");
   const float2 a = unpack2(s0), b = unpack2(s1);
   return Sums{m, a.x + a.y, b.x + b.y};
@@ -552,13 +560,12 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a,
 
   const int groups = (v1 - v0 + kUnroll * kThreads - 1) / (kUnroll * kThreads);
   const int length = max(1, (groups + kSegments - 1) / kSegments);
-  float(*segment)[kThreads] = nullptr;
+  bf16(*segment)[kThreads] = nullptr;
+  float raw = -inf;
   if constexpr (kTop) segment = sh.segment;
-  Sums s = sums_of<T, kThreads>(row, v0 + tid, v1, c, ring, segment, length);
+  Sums s = sums_of<T, kThreads>(row, v0 + tid, v1, c, ring, segment, length, raw);
   if constexpr (kTop) {
-    float m = sh.segment[0][tid];
-#pragma unroll
-    for (int i = 1; i < kSegments; ++i) m = fmaxf(m, sh.segment[i][tid]);
+    float m = raw;
 #pragma unroll
     for (int o = 1; o < kThreads / kSample; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
     if (tid % (kThreads / kSample) == 0) sh.sample[tid / (kThreads / kSample)] = m;
@@ -586,35 +593,37 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a,
     }
     __syncthreads();
     const float low = sh.bound;  // -inf: fewer than `top` sets hold anything
-    uint16_t* item = reinterpret_cast<uint16_t*>(ring);
+    Lists<kThreads>& lists = *reinterpret_cast<Lists<kThreads>*>(ring);
+    static_assert(sizeof(Lists<kThreads>) <= kStages * kUnroll * kThreads * 16, "fits the ring");
+    if (raw >= low && raw > -inf) {
 #pragma unroll
-    for (int i = 0; i < kSegments; ++i) {
-      const float m = sh.segment[i][tid];
-      if (m >= low && m > -inf)
-        item[atomicAdd(&sh.items, 1)] = static_cast<uint16_t>(i * kThreads + tid);
+      for (int i = 0; i < kSegments; ++i) {
+        const float m = bf16_to_f(sh.segment[i][tid]);
+        if (m >= low && m > -inf)
+          lists.item[atomicAdd(&sh.items, 1)] = static_cast<uint16_t>(i * kThreads + tid);
+      }
     }
     __syncthreads();
     // the order of items and keys varies, what is chosen among them does not
     for_each_candidate<T, kThreads, false>(
-        row, v0, v1, item, sh.items, length, low, [&](float x, int index) {
+        row, v0, v1, lists.item, sh.items, length, low, [&](float x, int index) {
           const uint64_t k = order_key(x, index);
           if (k == 0) return;
           const int n = atomicAdd(&sh.keys, 1);
-          if (n < kKeys) sh.key[n] = k;
+          if (n < kKeys) lists.key[n] = k;
         });
     __syncthreads();
     const int keys = sh.keys;
     if (keys <= kKeys) {
       for (int i = tid; i < keys; i += kThreads) {
-        const unsigned long long k = sh.key[i];
+        const unsigned long long k = lists.key[i];
         int rank = 0;
-        for (int j = 0; j < keys; ++j) rank += sh.key[j] > k;
+        for (int j = 0; j < keys; ++j) rank += lists.key[j] > k;
         if (rank < a.top) sh.best[rank] = k;
       }
     } else {
-      select_any<T, kThreads>(row, v0, v1, item, sh.items, length, low, a.top,
-                              reinterpret_cast<unsigned long long(*)[32]>(
-                                  item + kSegments * kThreads), sh.best);
+      select_any<T, kThreads>(row, v0, v1, lists.item, sh.items, length, low, a.top, lists.list,
+                              sh.best);
     }
     __syncthreads();
     list = sh.best[lane];
@@ -705,11 +714,16 @@ cudaError_t logprobs_of(const LogprobArgs& a, cudaStream_t s) {
   const int vectors = a.vocab / Vec<T>::kPer;
   if (vectors <= 1024)
     return a.top ? launch_logprobs<T, 64, true>(a, 1, s) : launch_logprobs<T, 64, false>(a, 1, s);
+  // Rows are shared by clusters while they are too few for one wave of 4 CTAs an SM.
+  const int sms = num_sms();
   int split = 1;
-  while (split < kMaxSplit && static_cast<int64_t>(a.rows) * split * 2 <= 2 * num_sms() &&
-         vectors / (2 * split) >= 512)
+  while (split < kMaxSplit && static_cast<int64_t>(a.rows) * split <= sms &&
+         vectors / (2 * split) >= 1024)
     split *= 2;
-  return a.top ? launch_logprobs<T, 256, true>(a, split, s)
+  // Alternatives leave a CTA without loads under way for some 5 us a row; smaller and more
+  // CTAs hide more of it (4096 rows of 151,936 bf16 logits, 20 alternatives: 228 us with 128
+  // threads, 240 with 256, 244 with 64; without alternatives 204, 197 and 200).
+  return a.top ? launch_logprobs<T, 128, true>(a, split, s)
                : launch_logprobs<T, 256, false>(a, split, s);
 }
 

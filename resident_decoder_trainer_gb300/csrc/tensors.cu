@@ -3,6 +3,7 @@
 // parameters, every tensor is cut into tiles, and the tiles of all tensors
 // make one launch (one per kMaxTensors tensors).
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cuda_fp8.h>
 #include <new>
@@ -47,27 +48,39 @@ struct Table {
 };
 static_assert(sizeof(Table<kMaxTensors>) + 128 <= 32764, "the table must fit the parameters");
 
-// f(tensor, its place in the table, tile within it, tiles) for the tiles of
-// this CTA: a contiguous share of all, tensor after tensor, so the table is
-// searched once (a search for every tile of a grid-wide stride took five times
-// as long on 500 small tensors).
-template <int kMax, typename F>
-__device__ __forceinline__ void for_each_span(const Table<kMax>& tab, int tiles, F f) {
-  int tile = static_cast<int>(static_cast<int64_t>(tiles) * blockIdx.x / gridDim.x);
-  const int last = static_cast<int>(static_cast<int64_t>(tiles) * (blockIdx.x + 1) / gridDim.x);
-  if (tile >= last) return;
-  int lo = 0, hi = tab.count - 1;  // the first tensor whose end is above the tile
+// The CTA's way through the tiles: chunks of `chunk` neighbours, a grid apart,
+// so that the whole grid works in one window of each array (a contiguous share
+// per CTA, a thousand windows, read DRAM at 0.8 of the speed), and so that
+// only every chunk needs a search of the table.
+struct Walk {
+  int tile, end_of_chunk, o, begin, end;  // tensor o has the tiles [begin, end)
+};
+template <int kMax>
+__device__ __forceinline__ void find_owner(const Table<kMax>& tab, Walk& w) {
+  int lo = w.o, hi = tab.count - 1;  // the first tensor whose end is above the tile
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (tab.end[mid] > tile) hi = mid; else lo = mid + 1;
+    if (tab.end[mid] > w.tile) hi = mid; else lo = mid + 1;
   }
-  int begin = lo ? tab.end[lo - 1] : 0;
-  for (; tile < last; ++lo) {
-    const int end = tab.end[lo], stop = min(end, last);
-    if (tile < stop) f(tab.t[lo], lo, tile - begin, stop - tile);
-    tile = stop;
-    begin = end;
+  w.o = lo;
+  w.begin = lo ? tab.end[lo - 1] : 0;
+  w.end = tab.end[lo];
+}
+template <int kMax>
+__device__ __forceinline__ Walk first_tile(const Table<kMax>& tab, int tiles, int chunk) {
+  Walk w{static_cast<int>(blockIdx.x) * chunk, 0, 0, 0, 0};
+  w.end_of_chunk = min(w.tile + chunk, tiles);
+  if (w.tile < tiles) find_owner(tab, w);
+  return w;
+}
+// The next tile; at or behind `tiles` there is none.
+template <int kMax>
+__device__ __forceinline__ void next_tile(const Table<kMax>& tab, int tiles, int chunk, Walk& w) {
+  if (++w.tile == w.end_of_chunk) {
+    w.tile += chunk * (static_cast<int>(gridDim.x) - 1);
+    w.end_of_chunk = min(w.tile + chunk, tiles);
   }
+  if (w.tile >= w.end && w.tile < tiles) find_owner(tab, w);
 }
 
 // Two fp32 operations, each rounded to nearest, in one instruction.
@@ -217,43 +230,68 @@ __device__ __forceinline__ void add_pair(float& hi, float& lo, float h, float l)
   hi = t;
 }
 
+// Sixteen bytes of g from p on, of which the first `have` elements count.
+template <bool kFull, typename G>
+__device__ __forceinline__ void load16(const G* p, int have, float* x) {
+  constexpr int kPer = 16 / sizeof(G);
+  if (kFull) {
+    const uint4 r = __ldg(reinterpret_cast<const uint4*>(p));
+    if constexpr (sizeof(G) == 4) {
+      x[0] = __uint_as_float(r.x); x[1] = __uint_as_float(r.y);
+      x[2] = __uint_as_float(r.z); x[3] = __uint_as_float(r.w);
+    } else {
+      x[0] = bf16lo(r.x); x[1] = bf16hi(r.x); x[2] = bf16lo(r.y); x[3] = bf16hi(r.y);
+      x[4] = bf16lo(r.z); x[5] = bf16hi(r.z); x[6] = bf16lo(r.w); x[7] = bf16hi(r.w);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) x[k] = k < have ? static_cast<float>(p[k]) : 0.f;
+  }
+}
+
+// A CTA's step is one chunk of kSqChunk tiles: eight 16-byte loads of a thread
+// under way together.
+constexpr int kSqChunk = 4;
 template <bool kBf16, int kMax>
 __global__ void __launch_bounds__(kThreads) tensors_sq_sum_kernel(
     const __grid_constant__ Table<kMax> tab, int tiles, float one,
     double* __restrict__ partials) {
   __shared__ double red[kThreads / 32];
   using G = typename std::conditional<kBf16, bf16, float>::type;
-  constexpr int kAhead = 4;  // tiles whose loads are under way
-  const int at = (threadIdx.x >> 5) * kRun + (threadIdx.x & 31) * 4;
+  constexpr int kPer = 16 / sizeof(G), kStep = kPer * kThreads;  // elements of a load
+  constexpr int kLoads = kSqChunk * kTile / kStep;
   float2 hi[4] = {}, lo[4] = {};
   auto add = [&](const float* x) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      add_squares<kBf16>(make_float2(x[2 * k], x[2 * k + 1]), hi[k], lo[k], one);
+    for (int k = 0; k < kPer / 2; ++k)
+      add_squares<kBf16>(make_float2(x[2 * k], x[2 * k + 1]), hi[k & 3], lo[k & 3], one);
   };
-  for_each_span(tab, tiles, [&](const Tensor& t, int, int tile, int count) {
-    int64_t left = t.n - static_cast<int64_t>(tile) * kTile;
-    const G* g = static_cast<const G*>(t.g) + static_cast<int64_t>(tile) * kTile + at;
-    for (; count >= kAhead && left >= kAhead * kTile; count -= kAhead) {
-      float x[kAhead][8];
+  Walk w = first_tile(tab, tiles, kSqChunk);
+  while (w.tile < tiles) {
+    const Tensor& t = tab.t[w.o];
+    const int64_t at = static_cast<int64_t>(w.tile - w.begin) * kTile;
+    const int count = min(w.end, w.end_of_chunk) - w.tile;  // tiles of this tensor and chunk
+    const G* g = static_cast<const G*>(t.g) + at + threadIdx.x * kPer;
+    if (count == kSqChunk && at + kSqChunk * kTile <= t.n) {
+      float x[kLoads][kPer];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) load8<true>(g + u * kTile, 0, x[u]);
+      for (int u = 0; u < kLoads; ++u) load16<true>(g + u * kStep, 0, x[u]);
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) add(x[u]);
-      g += kAhead * kTile;
-      left -= kAhead * kTile;
+      for (int u = 0; u < kLoads; ++u) add(x[u]);
+    } else {
+      const int left = static_cast<int>(min(t.n - at, static_cast<int64_t>(count) * kTile));
+      for (int e = threadIdx.x * kPer; e < left; e += kStep, g += kStep) {
+        float x[kPer];
+        if (e + kPer <= left)
+          load16<true>(g, 0, x);
+        else
+          load16<false>(g, left - e, x);
+        add(x);
+      }
     }
-    for (; count > 0; --count) {
-      float x[8];
-      if (left >= kTile)
-        load8<true>(g, 0, x);
-      else
-        load8<false>(g, static_cast<int>(left) - at, x);
-      add(x);
-      g += kTile;
-      left -= kTile;
-    }
-  });
+    w.tile += count - 1;
+    next_tile(tab, tiles, kSqChunk, w);
+  }
   // down to one pair a warp in fp32: fp64 additions of every lane took 20 us
   float h = hi[0].x, l = lo[0].x;
   add_pair(h, l, hi[0].y, lo[0].y);
@@ -357,28 +395,96 @@ __device__ __forceinline__ void run_scale(float big, float& scale, float& unit) 
   unit = there ? __fmul_rn(__frcp_rn(big), kE4m3Max) : 0.f;
 }
 
+// A thread's share of a run in shared memory, 16 bytes or less a piece; each
+// thread copies and reads only its own.
+template <int kBits, bool kBf16>
+struct Stage {
+  static constexpr int kG = kBf16 ? 8 : 16, kS = kBits == 32 ? 16 : 4;  // bytes of four elements
+  static constexpr int kW = 0, kGAt = 2 * 16 * kThreads, kM = kGAt + 2 * kG * kThreads,
+                       kV = kM + 2 * kS * kThreads, kBytes = kV + 2 * kS * kThreads;
+};
+template <int kBytes>
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(kBytes)
+                 : "memory");
+}
+// Starts the copies of the whole run at `first`.
+template <int kBits, bool kBf16>
+__device__ __forceinline__ void fetch_run(const Tensor& t, int64_t first, uint32_t stage,
+                                          float& ms, float& vs) {
+  using S = Stage<kBits, kBf16>;
+  const int tid = threadIdx.x;
+  const int64_t i = first + (tid & 31) * 4;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int at = h * kThreads + tid;
+    const int64_t e = i + 128 * h;
+    copy_async<16>(stage + S::kW + at * 16, t.w + e);
+    copy_async<S::kG>(stage + S::kGAt + at * S::kG, static_cast<const uint8_t*>(t.g) + e * (S::kG / 4));
+    copy_async<S::kS>(stage + S::kM + at * S::kS, static_cast<uint8_t*>(t.m) + e * (S::kS / 4));
+    copy_async<S::kS>(stage + S::kV + at * S::kS, static_cast<uint8_t*>(t.v) + e * (S::kS / 4));
+  }
+  if constexpr (kBits == 8) {
+    ms = t.m_scale[first / kRun];
+    vs = t.v_scale[first / kRun];
+  }
+}
+
 // One run of 256 elements of tensor t, `first` its first element's index; the
-// lane's own elements start at first + 4 lane.
+// lane's own elements start at first + 4 lane. A full run is in `stage`.
 template <int kBits, bool kBf16, bool kRandom, bool kFull>
-__device__ __forceinline__ void adamw_run(const Tensor& t, int64_t first, const AdamArgs& p,
-                                          float sc, float inv_bc1, float inv_root_bc2,
-                                          uint32_t key) {
+__device__ __forceinline__ void adamw_run(const Tensor& t, int64_t first, const uint8_t* stage,
+                                          float ms, float vs, const AdamArgs& p, float sc,
+                                          float inv_bc1, float inv_root_bc2, uint32_t key) {
   using G = typename std::conditional<kBf16, bf16, float>::type;
-  const int lane = threadIdx.x & 31;
+  using S = Stage<kBits, kBf16>;
+  const int tid = threadIdx.x, lane = tid & 31;
   const int64_t i = first + lane * 4;
   const int have = kFull ? kRun : static_cast<int>(t.n - i);
   const int64_t run = first / kRun;
   float w[8], g[8], m[8], r[8];
-  load8<kFull>(t.w + i, have, w);
-  load8<kFull>(static_cast<const G*>(t.g) + i, have, g);
-  if constexpr (kBits == 32) {
-    load8<kFull>(static_cast<const float*>(t.m) + i, have, m);
-    load8<kFull>(static_cast<const float*>(t.v) + i, have, r);
+  uint32_t mc[2], vc[2];
+  if constexpr (kFull) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int at = h * kThreads + tid;
+      auto four = [&](int where, float* x) {
+        const float4 a = *reinterpret_cast<const float4*>(stage + where + at * 16);
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+      };
+      four(S::kW, w + 4 * h);
+      if constexpr (kBf16) {
+        const uint2 a = *reinterpret_cast<const uint2*>(stage + S::kGAt + at * 8);
+        g[4 * h] = bf16lo(a.x); g[4 * h + 1] = bf16hi(a.x);
+        g[4 * h + 2] = bf16lo(a.y); g[4 * h + 3] = bf16hi(a.y);
+      } else {
+        four(S::kGAt, g + 4 * h);
+      }
+      if constexpr (kBits == 32) {
+        four(S::kM, m + 4 * h);
+        four(S::kV, r + 4 * h);
+      } else {
+        mc[h] = *reinterpret_cast<const uint32_t*>(stage + S::kM + at * 4);
+        vc[h] = *reinterpret_cast<const uint32_t*>(stage + S::kV + at * 4);
+      }
+    }
   } else {
-    uint32_t mc[2], vc[2];
-    load8<kFull>(static_cast<const uint8_t*>(t.m) + i, have, mc);
-    load8<kFull>(static_cast<const uint8_t*>(t.v) + i, have, vc);
-    const float ms = t.m_scale[run], vs = t.v_scale[run];
+    load8<false>(t.w + i, have, w);
+    load8<false>(static_cast<const G*>(t.g) + i, have, g);
+    if constexpr (kBits == 32) {
+      load8<false>(static_cast<const float*>(t.m) + i, have, m);
+      load8<false>(static_cast<const float*>(t.v) + i, have, r);
+    } else {
+      load8<false>(static_cast<const uint8_t*>(t.m) + i, have, mc);
+      load8<false>(static_cast<const uint8_t*>(t.v) + i, have, vc);
+      ms = t.m_scale[run];
+      vs = t.v_scale[run];
+    }
+  }
+  if constexpr (kBits == 8) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       e4m3_decode4(mc[h], m + 4 * h);
@@ -420,7 +526,7 @@ __device__ __forceinline__ void adamw_run(const Tensor& t, int64_t first, const 
     store8<kFull>(static_cast<float*>(t.m) + i, have, m);
     store8<kFull>(static_cast<float*>(t.v) + i, have, r);
   } else {
-    float ms, vs, um, uv;
+    float um, uv;
     run_scale(warp_max(big_m), ms, um);
     run_scale(warp_max(big_r), vs, uv);
     if (lane == 0) {
@@ -460,13 +566,17 @@ __device__ __forceinline__ void adamw_run(const Tensor& t, int64_t first, const 
       r[k] = r[k] > 0.f ? fmaxf(qx.x, least) : qx.x;
       r[k + 1] = r[k + 1] > 0.f ? fmaxf(qx.y, least) : qx.y;
     }
-    uint32_t mc[2] = {e4m3_encode4(m), e4m3_encode4(m + 4)};
-    uint32_t vc[2] = {e4m3_encode4(r), e4m3_encode4(r + 4)};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      mc[h] = e4m3_encode4(m + 4 * h);
+      vc[h] = e4m3_encode4(r + 4 * h);
+    }
     store8<kFull>(static_cast<uint8_t*>(t.m) + i, have, mc);
     store8<kFull>(static_cast<uint8_t*>(t.v) + i, have, vc);
   }
 }
 
+constexpr int kChunk = 2;  // tiles of a CTA's step
 template <int kBits, bool kBf16, bool kRandom, int kMax>
 __global__ void __launch_bounds__(kThreads) tensors_adamw_kernel(
     const __grid_constant__ Table<kMax> tab, int tiles, const AdamArgs p) {
@@ -481,17 +591,38 @@ __global__ void __launch_bounds__(kThreads) tensors_adamw_kernel(
         1.0 / sqrt(1.0 - pow(static_cast<double>(p.b2), static_cast<double>(step))));
   }
   const uint32_t key0 = mix(mix(static_cast<uint32_t>(step)) + p.seed) + tab.first;
-  for_each_span(tab, tiles, [&](const Tensor& t, int o, int tile, int count) {
-    const uint32_t key_o = mix(key0 + o);
-    int64_t first = static_cast<int64_t>(tile) * kTile + (threadIdx.x >> 5) * kRun;
-    for (; count > 0; --count, first += kTile) {
-      const uint32_t key = key_o ^ static_cast<uint32_t>(first >> 32) * 0x9E3779B1u;
-      if (first + kRun <= t.n)
-        adamw_run<kBits, kBf16, kRandom, true>(t, first, p, sc, inv_bc1, inv_root_bc2, key);
-      else if (first < t.n)
-        adamw_run<kBits, kBf16, kRandom, false>(t, first, p, sc, inv_bc1, inv_root_bc2, key);
-    }
-  });
+  // The next run's copies are under way while one is computed.
+  extern __shared__ __align__(16) uint8_t stages[];
+  constexpr int kBytes = Stage<kBits, kBf16>::kBytes;
+  const uint32_t at = smem_u32(stages);
+  const int part = (threadIdx.x >> 5) * kRun;
+  auto place = [&](const Walk& w) { return static_cast<int64_t>(w.tile - w.begin) * kTile + part; };
+  Walk w = first_tile(tab, tiles, kChunk);
+  float ms = 0.f, vs = 0.f;
+  if (w.tile < tiles && place(w) + kRun <= tab.t[w.o].n)
+    fetch_run<kBits, kBf16>(tab.t[w.o], place(w), at, ms, vs);
+  asm volatile("cp.async.commit_group;" ::: "memory");
+  for (int s = 0; w.tile < tiles; s ^= 1) {
+    Walk n = w;
+    next_tile(tab, tiles, kChunk, n);
+    float next_ms = 0.f, next_vs = 0.f;
+    if (n.tile < tiles && place(n) + kRun <= tab.t[n.o].n)
+      fetch_run<kBits, kBf16>(tab.t[n.o], place(n), at + (s ^ 1) * kBytes, next_ms, next_vs);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    const Tensor& t = tab.t[w.o];
+    const int64_t first = place(w);
+    const uint32_t key = mix(key0 + w.o) ^ static_cast<uint32_t>(first >> 32) * 0x9E3779B1u;
+    if (first + kRun <= t.n)
+      adamw_run<kBits, kBf16, kRandom, true>(t, first, stages + s * kBytes, ms, vs, p, sc, inv_bc1,
+                                             inv_root_bc2, key);
+    else if (first < t.n)
+      adamw_run<kBits, kBf16, kRandom, false>(t, first, nullptr, 0.f, 0.f, p, sc, inv_bc1,
+                                              inv_root_bc2, key);
+    w = n;
+    ms = next_ms;
+    vs = next_vs;
+  }
 }
 
 rdt_status refuse(const char* msg) {
@@ -549,8 +680,11 @@ cudaError_t each_launch(const rdt_opt_tensor* list, int count, F f) {
   return cudaSuccess;
 }
 
-// One resident wave of CTAs: 8 of 256 threads an SM at most.
-int wave(int tiles) { return static_cast<int>(std::min<int64_t>(tiles, 8LL * num_sms())); }
+// At most one resident wave of CTAs.
+int wave(int tiles, int chunk, int per_sm) {
+  return static_cast<int>(std::min<int64_t>((tiles + chunk - 1) / chunk,
+                                            static_cast<int64_t>(per_sm) * num_sms()));
+}
 
 constexpr int kMaxPartials = 2048;  // of one launch
 
@@ -558,7 +692,7 @@ template <int kMax>
 cudaError_t sq_sum_launches(const rdt_opt_tensor* list, int count, bool half, double* parts,
                             int64_t room, int64_t* used, cudaStream_t s) {
   return each_launch<kMax>(list, count, [&](const Table<kMax>& tab, int tiles) {
-    const int blocks = std::min(wave(tiles), kMaxPartials);
+    const int blocks = std::min(wave(tiles, kSqChunk, 5), kMaxPartials);
     if (*used + blocks > room) return cudaErrorInvalidValue;
     note_launch();
     auto kernel = half ? tensors_sq_sum_kernel<true, kMax> : tensors_sq_sum_kernel<false, kMax>;
@@ -568,19 +702,36 @@ cudaError_t sq_sum_launches(const rdt_opt_tensor* list, int count, bool half, do
   });
 }
 
+template <int kBits, bool kBf16, bool kRandom, int kMax>
+cudaError_t launch_adamw(const Table<kMax>& tab, int tiles, const AdamArgs& a, cudaStream_t s) {
+  constexpr int kBytes = 2 * Stage<kBits, kBf16>::kBytes;
+  auto kernel = tensors_adamw_kernel<kBits, kBf16, kRandom, kMax>;
+  static std::atomic<uint64_t> allowed{0};  // devices where the kernel may use kBytes
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev > 63 || !(allowed.load() >> dev & 1)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) allowed.fetch_or(uint64_t(1) << dev);
+  }
+  note_launch();
+  kernel<<<wave(tiles, kChunk, kBits == 32 ? 3 : 4), kThreads, kBytes, s>>>(tab, tiles, a);
+  return cudaGetLastError();
+}
+
 template <int kMax>
 cudaError_t adamw_launches(const rdt_opt_tensor* list, int count, bool half, int bits, bool random,
                            const AdamArgs& a, cudaStream_t s) {
   return each_launch<kMax>(list, count, [&](const Table<kMax>& tab, int tiles) {
-    note_launch();
-    auto kernel = bits == 32 ? (half ? tensors_adamw_kernel<32, true, false, kMax>
-                                     : tensors_adamw_kernel<32, false, false, kMax>)
-                  : random   ? (half ? tensors_adamw_kernel<8, true, true, kMax>
-                                     : tensors_adamw_kernel<8, false, true, kMax>)
-                             : (half ? tensors_adamw_kernel<8, true, false, kMax>
-                                     : tensors_adamw_kernel<8, false, false, kMax>);
-    kernel<<<wave(tiles), kThreads, 0, s>>>(tab, tiles, a);
-    return cudaGetLastError();
+    if (bits == 32)
+      return half ? launch_adamw<32, true, false>(tab, tiles, a, s)
+                  : launch_adamw<32, false, false>(tab, tiles, a, s);
+    if (random)
+      return half ? launch_adamw<8, true, true>(tab, tiles, a, s)
+                  : launch_adamw<8, false, true>(tab, tiles, a, s);
+    return half ? launch_adamw<8, true, false>(tab, tiles, a, s)
+                : launch_adamw<8, false, false>(tab, tiles, a, s);
   });
 }
 
