@@ -374,12 +374,15 @@ __device__ __forceinline__ uint32_t mix(uint32_t x) {
 // |x| <= 448 up or down to a neighbouring e4m3 value with the probability of
 // the distance: 20 of fp32's 23 mantissa bits go, so a number of 20 bits (16
 // random ones, then 1000) is added and the 20 are cut. Below 2^-6 e4m3 has the
-// steps of [2^-6, 2^-5), hence the shift by 2^-6. Not for NaN.
+// steps of [2^-6, 2^-5), hence the shift by 2^-6. Not for NaN; what is rounded
+// beyond 448 saturates when it is encoded.
+template <bool kSigned>
 __device__ __forceinline__ float round_random(float x, uint32_t bits20) {
-  const float low = fabsf(x) < 0x1p-6f ? 0x1p-6f : 0.f;
-  const uint32_t b = __float_as_uint(__fadd_rn(fabsf(x), low)) + bits20;
-  const float r = fminf(__fsub_rn(__uint_as_float(b & 0xfff00000u), low), kE4m3Max);
-  return __uint_as_float(__float_as_uint(r) | (__float_as_uint(x) & 0x80000000u));
+  const float a = kSigned ? fabsf(x) : x;
+  const float low = a < 0x1p-6f ? 0x1p-6f : 0.f;
+  const uint32_t b = __float_as_uint(__fadd_rn(a, low)) + bits20;
+  const float r = __fsub_rn(__uint_as_float(b & 0xfff00000u), low);
+  return kSigned ? __uint_as_float(__float_as_uint(r) | (__float_as_uint(x) & 0x80000000u)) : r;
 }
 // 1 / x to 1 ulp.
 __device__ __forceinline__ float reciprocal(float x) {
@@ -395,11 +398,13 @@ __device__ __forceinline__ void run_scale(float big, float& scale, float& unit) 
   unit = there ? __fmul_rn(__frcp_rn(big), kE4m3Max) : 0.f;
 }
 
-// A thread's share of a run in shared memory, 16 bytes or less a piece; each
-// thread copies and reads only its own.
-template <int kBits, bool kBf16>
+// A thread's share of a run with 8-bit states in shared memory, 16 bytes or
+// less a piece; each thread copies and reads only its own. (32-bit states are
+// loaded directly: their arithmetic is short enough beside their bytes, and
+// 479 us a q4b block through shared memory stood against 466.)
+template <bool kBf16>
 struct Stage {
-  static constexpr int kG = kBf16 ? 8 : 16, kS = kBits == 32 ? 16 : 4;  // bytes of four elements
+  static constexpr int kG = kBf16 ? 8 : 16, kS = 4;  // bytes of four elements
   static constexpr int kW = 0, kGAt = 2 * 16 * kThreads, kM = kGAt + 2 * kG * kThreads,
                        kV = kM + 2 * kS * kThreads, kBytes = kV + 2 * kS * kThreads;
 };
@@ -412,10 +417,10 @@ __device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
                  : "memory");
 }
 // Starts the copies of the whole run at `first`.
-template <int kBits, bool kBf16>
+template <bool kBf16>
 __device__ __forceinline__ void fetch_run(const Tensor& t, int64_t first, uint32_t stage,
                                           float& ms, float& vs) {
-  using S = Stage<kBits, kBf16>;
+  using S = Stage<kBf16>;
   const int tid = threadIdx.x;
   const int64_t i = first + (tid & 31) * 4;
 #pragma unroll
@@ -427,27 +432,25 @@ __device__ __forceinline__ void fetch_run(const Tensor& t, int64_t first, uint32
     copy_async<S::kS>(stage + S::kM + at * S::kS, static_cast<uint8_t*>(t.m) + e * (S::kS / 4));
     copy_async<S::kS>(stage + S::kV + at * S::kS, static_cast<uint8_t*>(t.v) + e * (S::kS / 4));
   }
-  if constexpr (kBits == 8) {
-    ms = t.m_scale[first / kRun];
-    vs = t.v_scale[first / kRun];
-  }
+  ms = t.m_scale[first / kRun];
+  vs = t.v_scale[first / kRun];
 }
 
 // One run of 256 elements of tensor t, `first` its first element's index; the
-// lane's own elements start at first + 4 lane. A full run is in `stage`.
+// lane's own elements start at first + 4 lane. A full run of 8 bits is in `stage`.
 template <int kBits, bool kBf16, bool kRandom, bool kFull>
 __device__ __forceinline__ void adamw_run(const Tensor& t, int64_t first, const uint8_t* stage,
                                           float ms, float vs, const AdamArgs& p, float sc,
                                           float inv_bc1, float inv_root_bc2, uint32_t key) {
   using G = typename std::conditional<kBf16, bf16, float>::type;
-  using S = Stage<kBits, kBf16>;
+  using S = Stage<kBf16>;
   const int tid = threadIdx.x, lane = tid & 31;
   const int64_t i = first + lane * 4;
   const int have = kFull ? kRun : static_cast<int>(t.n - i);
   const int64_t run = first / kRun;
   float w[8], g[8], m[8], r[8];
   uint32_t mc[2], vc[2];
-  if constexpr (kFull) {
+  if constexpr (kFull && kBits == 8) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int at = h * kThreads + tid;
@@ -463,20 +466,15 @@ __device__ __forceinline__ void adamw_run(const Tensor& t, int64_t first, const 
       } else {
         four(S::kGAt, g + 4 * h);
       }
-      if constexpr (kBits == 32) {
-        four(S::kM, m + 4 * h);
-        four(S::kV, r + 4 * h);
-      } else {
-        mc[h] = *reinterpret_cast<const uint32_t*>(stage + S::kM + at * 4);
-        vc[h] = *reinterpret_cast<const uint32_t*>(stage + S::kV + at * 4);
-      }
+      mc[h] = *reinterpret_cast<const uint32_t*>(stage + S::kM + at * 4);
+      vc[h] = *reinterpret_cast<const uint32_t*>(stage + S::kV + at * 4);
     }
   } else {
-    load8<false>(t.w + i, have, w);
-    load8<false>(static_cast<const G*>(t.g) + i, have, g);
+    load8<kFull>(t.w + i, have, w);
+    load8<kFull>(static_cast<const G*>(t.g) + i, have, g);
     if constexpr (kBits == 32) {
-      load8<false>(static_cast<const float*>(t.m) + i, have, m);
-      load8<false>(static_cast<const float*>(t.v) + i, have, r);
+      load8<kFull>(static_cast<const float*>(t.m) + i, have, m);
+      load8<kFull>(static_cast<const float*>(t.v) + i, have, r);
     } else {
       load8<false>(static_cast<const uint8_t*>(t.m) + i, have, mc);
       load8<false>(static_cast<const uint8_t*>(t.v) + i, have, vc);
@@ -535,36 +533,39 @@ __device__ __forceinline__ void adamw_run(const Tensor& t, int64_t first, const 
     }
     // no sqrt(v) > 0 becomes 0, but in a run that is stored as zeros
     const float least = uv > 0.f ? kE4m3Tiny : 0.f;
-    bool nan = false;
-    if (kRandom) {
-      // NaN does not go through round_random; a sum shows it (so does one that leaves fp32's
-      // range, which costs the slow way only)
+    auto codes = [&](auto careful) {
+#pragma unroll
+      for (int k = 0; k < 8; k += 2) {
+        float2 qm = mul2(make_float2(m[k], m[k + 1]), both(um));
+        float2 qr = mul2(make_float2(r[k], r[k + 1]), both(uv));
+        if constexpr (kRandom) {
+          const uint32_t at = static_cast<uint32_t>(i + (k & 3) + 32 * (k & 4));
+          const uint32_t x = mix(at ^ key), y = mix((at + 1) ^ key);
+          auto up = [&](float& q, float& p, uint32_t z) {
+            if (!careful.value || q == q) q = round_random<true>(q, (z << 4 & 0xffff0u) | 8u);
+            if (!careful.value || p == p) p = round_random<false>(p, (z >> 12 & 0xffff0u) | 8u);
+          };
+          up(qm.x, qr.x, x);
+          up(qm.y, qr.y, y);
+        }
+        m[k] = qm.x; m[k + 1] = qm.y;
+        r[k] = r[k] > 0.f ? fmaxf(qr.x, least) : qr.x;
+        r[k + 1] = r[k + 1] > 0.f ? fmaxf(qr.y, least) : qr.y;
+      }
+    };
+    if constexpr (kRandom) {
+      // NaN must not go through round_random; a sum shows it (so does one that leaves fp32's
+      // range, which only costs the careful way)
       float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
       for (int k = 0; k < 8; k += 2)
         sum = fma2(make_float2(m[k], m[k + 1]), make_float2(r[k], r[k + 1]), sum);
-      nan = !(fabsf(sum.x + sum.y) < INFINITY);
-    }
-#pragma unroll
-    for (int k = 0; k < 8; k += 2) {
-      const float2 qm = mul2(make_float2(m[k], m[k + 1]), both(um));
-      float2 qr = mul2(make_float2(r[k], r[k + 1]), both(uv));
-      m[k] = qm.x; m[k + 1] = qm.y;
-      float2 qx = qr;
-      if constexpr (kRandom) {
-        const uint32_t at = static_cast<uint32_t>(i + (k & 3) + 32 * (k & 4));
-        const uint32_t x0 = mix(at ^ key), x1 = mix((at + 1) ^ key);
-        const float2 rm = make_float2(round_random(qm.x, (x0 << 4 & 0xffff0u) | 8u),
-                                      round_random(qm.y, (x1 << 4 & 0xffff0u) | 8u));
-        const float2 rr = make_float2(round_random(qr.x, (x0 >> 12 & 0xffff0u) | 8u),
-                                      round_random(qr.y, (x1 >> 12 & 0xffff0u) | 8u));
-        if (!nan || qm.x == qm.x) m[k] = rm.x;
-        if (!nan || qm.y == qm.y) m[k + 1] = rm.y;
-        if (!nan || qr.x == qr.x) qx.x = rr.x;
-        if (!nan || qr.y == qr.y) qx.y = rr.y;
-      }
-      r[k] = r[k] > 0.f ? fmaxf(qx.x, least) : qx.x;
-      r[k + 1] = r[k + 1] > 0.f ? fmaxf(qx.y, least) : qx.y;
+      if (fabsf(sum.x + sum.y) < INFINITY)
+        codes(std::false_type{});
+      else
+        codes(std::true_type{});
+    } else {
+      codes(std::false_type{});
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -576,7 +577,7 @@ __device__ __forceinline__ void adamw_run(const Tensor& t, int64_t first, const 
   }
 }
 
-constexpr int kChunk = 2;  // tiles of a CTA's step
+constexpr int kChunk = 2;  // tiles of a CTA's step of tensors_adamw_kernel
 template <int kBits, bool kBf16, bool kRandom, int kMax>
 __global__ void __launch_bounds__(kThreads) tensors_adamw_kernel(
     const __grid_constant__ Table<kMax> tab, int tiles, const AdamArgs p) {
@@ -591,37 +592,51 @@ __global__ void __launch_bounds__(kThreads) tensors_adamw_kernel(
         1.0 / sqrt(1.0 - pow(static_cast<double>(p.b2), static_cast<double>(step))));
   }
   const uint32_t key0 = mix(mix(static_cast<uint32_t>(step)) + p.seed) + tab.first;
-  // The next run's copies are under way while one is computed.
-  extern __shared__ __align__(16) uint8_t stages[];
-  constexpr int kBytes = Stage<kBits, kBf16>::kBytes;
-  const uint32_t at = smem_u32(stages);
   const int part = (threadIdx.x >> 5) * kRun;
   auto place = [&](const Walk& w) { return static_cast<int64_t>(w.tile - w.begin) * kTile + part; };
+  auto key_of = [&](const Walk& w) {
+    return mix(key0 + w.o) ^ static_cast<uint32_t>(place(w) >> 32) * 0x9E3779B1u;
+  };
   Walk w = first_tile(tab, tiles, kChunk);
-  float ms = 0.f, vs = 0.f;
-  if (w.tile < tiles && place(w) + kRun <= tab.t[w.o].n)
-    fetch_run<kBits, kBf16>(tab.t[w.o], place(w), at, ms, vs);
-  asm volatile("cp.async.commit_group;" ::: "memory");
-  for (int s = 0; w.tile < tiles; s ^= 1) {
-    Walk n = w;
-    next_tile(tab, tiles, kChunk, n);
-    float next_ms = 0.f, next_vs = 0.f;
-    if (n.tile < tiles && place(n) + kRun <= tab.t[n.o].n)
-      fetch_run<kBits, kBf16>(tab.t[n.o], place(n), at + (s ^ 1) * kBytes, next_ms, next_vs);
+  if constexpr (kBits == 32) {
+    while (w.tile < tiles) {
+      const Tensor& t = tab.t[w.o];
+      const int64_t first = place(w);
+      next_tile(tab, tiles, kChunk, w);
+      if (first + kRun <= t.n)
+        adamw_run<32, kBf16, false, true>(t, first, nullptr, 0.f, 0.f, p, sc, inv_bc1, inv_root_bc2, 0);
+      else if (first < t.n)
+        adamw_run<32, kBf16, false, false>(t, first, nullptr, 0.f, 0.f, p, sc, inv_bc1, inv_root_bc2, 0);
+    }
+  } else {
+    // the next run's copies are under way while one is computed
+    extern __shared__ __align__(16) uint8_t stages[];
+    constexpr int kBytes = Stage<kBf16>::kBytes;
+    const uint32_t at = smem_u32(stages);
+    float ms = 0.f, vs = 0.f;
+    if (w.tile < tiles && place(w) + kRun <= tab.t[w.o].n)
+      fetch_run<kBf16>(tab.t[w.o], place(w), at, ms, vs);
     asm volatile("cp.async.commit_group;" ::: "memory");
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
-    const Tensor& t = tab.t[w.o];
-    const int64_t first = place(w);
-    const uint32_t key = mix(key0 + w.o) ^ static_cast<uint32_t>(first >> 32) * 0x9E3779B1u;
-    if (first + kRun <= t.n)
-      adamw_run<kBits, kBf16, kRandom, true>(t, first, stages + s * kBytes, ms, vs, p, sc, inv_bc1,
-                                             inv_root_bc2, key);
-    else if (first < t.n)
-      adamw_run<kBits, kBf16, kRandom, false>(t, first, nullptr, 0.f, 0.f, p, sc, inv_bc1,
-                                              inv_root_bc2, key);
-    w = n;
-    ms = next_ms;
-    vs = next_vs;
+    for (int s = 0; w.tile < tiles; s ^= 1) {
+      Walk n = w;
+      next_tile(tab, tiles, kChunk, n);
+      float next_ms = 0.f, next_vs = 0.f;
+      if (n.tile < tiles && place(n) + kRun <= tab.t[n.o].n)
+        fetch_run<kBf16>(tab.t[n.o], place(n), at + (s ^ 1) * kBytes, next_ms, next_vs);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      const Tensor& t = tab.t[w.o];
+      const int64_t first = place(w);
+      if (first + kRun <= t.n)
+        adamw_run<8, kBf16, kRandom, true>(t, first, stages + s * kBytes, ms, vs, p, sc, inv_bc1,
+                                           inv_root_bc2, key_of(w));
+      else if (first < t.n)
+        adamw_run<8, kBf16, kRandom, false>(t, first, nullptr, 0.f, 0.f, p, sc, inv_bc1,
+                                            inv_root_bc2, key_of(w));
+      w = n;
+      ms = next_ms;
+      vs = next_vs;
+    }
   }
 }
 
@@ -704,7 +719,7 @@ cudaError_t sq_sum_launches(const rdt_opt_tensor* list, int count, bool half, do
 
 template <int kBits, bool kBf16, bool kRandom, int kMax>
 cudaError_t launch_adamw(const Table<kMax>& tab, int tiles, const AdamArgs& a, cudaStream_t s) {
-  constexpr int kBytes = 2 * Stage<kBits, kBf16>::kBytes;
+  constexpr int kBytes = kBits == 8 ? 2 * Stage<kBf16>::kBytes : 0;
   auto kernel = tensors_adamw_kernel<kBits, kBf16, kRandom, kMax>;
   static std::atomic<uint64_t> allowed{0};  // devices where the kernel may use kBytes
   int dev = 0;
@@ -716,7 +731,7 @@ cudaError_t launch_adamw(const Table<kMax>& tab, int tiles, const AdamArgs& a, c
     if (dev < 64) allowed.fetch_or(uint64_t(1) << dev);
   }
   note_launch();
-  kernel<<<wave(tiles, kChunk, kBits == 32 ? 3 : 4), kThreads, kBytes, s>>>(tab, tiles, a);
+  kernel<<<wave(tiles, kChunk, kBits == 32 ? 8 : 4), kThreads, kBytes, s>>>(tab, tiles, a);
   return cudaGetLastError();
 }
 
