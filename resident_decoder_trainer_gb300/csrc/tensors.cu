@@ -249,9 +249,13 @@ __device__ __forceinline__ void load16(const G* p, int have, float* x) {
   }
 }
 
-// A CTA's step is one chunk of kSqChunk tiles: eight 16-byte loads of a thread
-// under way together.
-constexpr int kSqChunk = 4;
+// A CTA's step is one chunk of two tiles: two (bf16) or four (fp32) 16-byte
+// loads of a thread under way together. 268 M values: fp32 162 us (0.98 of
+// measured HBM) with 4 loads and 6 CTAs an SM, 188 with 8 and 8; bf16 101 us
+// (0.78; the additions bound it) with 2 and 5, 106 with 4, 150 with 1.
+template <bool kBf16> constexpr int kSqLoads = kBf16 ? 2 : 4;
+template <bool kBf16>
+constexpr int kSqTiles = kSqLoads<kBf16> * (kBf16 ? 8 : 4) * kThreads / kTile;
 template <bool kBf16, int kMax>
 __global__ void __launch_bounds__(kThreads) tensors_sq_sum_kernel(
     const __grid_constant__ Table<kMax> tab, int tiles, float one,
@@ -259,7 +263,7 @@ __global__ void __launch_bounds__(kThreads) tensors_sq_sum_kernel(
   __shared__ double red[kThreads / 32];
   using G = typename std::conditional<kBf16, bf16, float>::type;
   constexpr int kPer = 16 / sizeof(G), kStep = kPer * kThreads;  // elements of a load
-  constexpr int kLoads = kSqChunk * kTile / kStep;
+  constexpr int kLoads = kSqLoads<kBf16>, kSqChunk = kSqTiles<kBf16>;
   float2 hi[4] = {}, lo[4] = {};
   auto add = [&](const float* x) {
 #pragma unroll
@@ -695,10 +699,15 @@ cudaError_t each_launch(const rdt_opt_tensor* list, int count, F f) {
   return cudaSuccess;
 }
 
-// At most one resident wave of CTAs.
-int wave(int tiles, int chunk, int per_sm) {
-  return static_cast<int>(std::min<int64_t>((tiles + chunk - 1) / chunk,
-                                            static_cast<int64_t>(per_sm) * num_sms()));
+// CTAs for `tiles`: a resident wave at most, or, with `share`, one per `share`
+// tiles if that is more. CTAs that come and go in order keep the grid's
+// window of the arrays narrow: 268 M parameters with 8-bit states took 823 us
+// in one wave, 702 with 12 tiles a CTA, 693 with 6 and 685 with 2 (776 for
+// random rounding, against 730 with 6, by each CTA's start). The squared sum,
+// one array, loses: 166 us in a wave, 168 with 16 tiles a CTA.
+int ctas(int tiles, int chunk, int per_sm, int share = INT32_MAX) {
+  const int all = (tiles + chunk - 1) / chunk;
+  return std::min(all, std::max(per_sm * num_sms(), tiles / share));
 }
 
 constexpr int kMaxPartials = 2048;  // of one launch
@@ -707,7 +716,7 @@ template <int kMax>
 cudaError_t sq_sum_launches(const rdt_opt_tensor* list, int count, bool half, double* parts,
                             int64_t room, int64_t* used, cudaStream_t s) {
   return each_launch<kMax>(list, count, [&](const Table<kMax>& tab, int tiles) {
-    const int blocks = std::min(wave(tiles, kSqChunk, 5), kMaxPartials);
+    const int blocks = std::min(half ? ctas(tiles, kSqTiles<true>, 5) : ctas(tiles, kSqTiles<false>, 6), kMaxPartials);
     if (*used + blocks > room) return cudaErrorInvalidValue;
     note_launch();
     auto kernel = half ? tensors_sq_sum_kernel<true, kMax> : tensors_sq_sum_kernel<false, kMax>;
@@ -731,7 +740,7 @@ cudaError_t launch_adamw(const Table<kMax>& tab, int tiles, const AdamArgs& a, c
     if (dev < 64) allowed.fetch_or(uint64_t(1) << dev);
   }
   note_launch();
-  kernel<<<wave(tiles, kChunk, kBits == 32 ? 8 : 4), kThreads, kBytes, s>>>(tab, tiles, a);
+  kernel<<<ctas(tiles, kChunk, kBits == 32 ? 8 : 4, 6), kThreads, kBytes, s>>>(tab, tiles, a);
   return cudaGetLastError();
 }
 
