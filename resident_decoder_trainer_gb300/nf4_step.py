@@ -11,6 +11,10 @@ cuda_block.rs page, with lora_scale = alpha / rank as in cuda_trainer.rs).
   ``shadow`` their bf16 operand copy, ``g``, ``m``, ``v`` the adapter
   gradients and AdamW moments.
 
+``state_bits=8`` keeps ``m`` and ``v`` as e4m3 codes with one scale per 256
+elements (``rdt_tensors_adamw`` over the fourteen adapter tensors), rounded up
+or down at random from ``state_seed`` and the step (None: to nearest).
+
 A step is the block forward, the block backward (adapter gradients only), the
 squared sum of the adapter gradients, the clip scale, AdamW over the adapters
 and the shadow refresh. Every launch is a librdt kernel; torch only allocates
@@ -25,8 +29,12 @@ from .synth import LORA, NF4_PROJECTIONS, OPTIM, DecoderShape
 
 
 class Nf4LoraTrainer:
-    def __init__(self, shape: DecoderShape, rank=None, alpha=None, device="cuda", optim=None):
+    def __init__(self, shape: DecoderShape, rank=None, alpha=None, device="cuda", optim=None,
+                 state_bits=32, state_seed=0):
         self.shape = s = shape
+        if state_bits not in (32, 8):
+            raise ValueError("state_bits must be 32 or 8")
+        self.state_bits, self.state_seed = state_bits, state_seed
         self.rank = int(rank or LORA["rank"])
         self.alpha = float(alpha if alpha is not None else LORA["alpha"])
         self.device = dev = torch.device(device)
@@ -45,8 +53,15 @@ class Nf4LoraTrainer:
         self.shadow = torch.zeros(rdt.lora_shadow_count(self.cfg, self.rank),
                                   dtype=torch.bfloat16, device=dev)
         self.g = torch.zeros(self.n_params, **f32)
-        self.m = torch.zeros(self.n_params, **f32)
-        self.v = torch.zeros(self.n_params, **f32)
+        state = dict(dtype=torch.float32 if state_bits == 32 else torch.uint8, device=dev)
+        self.m = torch.zeros(self.n_params, **state)
+        self.v = torch.zeros(self.n_params, **state)
+        if state_bits == 8:
+            spans = list(self.lora_offsets.values())
+            cut = lambda buf: [buf[a:a + n] for a, n in spans]  # noqa: E731
+            scales = lambda: [torch.zeros(-(-n // rdt.STATE_RUN), **f32) for _, n in spans]  # noqa: E731
+            self.opt = rdt.OptTensors(g=cut(self.g), w=cut(self.lora), m=cut(self.m),
+                                      v=cut(self.v), m_scale=scales(), v_scale=scales())
         self.saved = torch.empty(rdt.nf4_saved_bytes(self.cfg, self.rank, s.batch, s.seq),
                                  dtype=torch.uint8, device=dev)
         self.ws = torch.empty(rdt.nf4_workspace_bytes(self.cfg, self.rank, s.batch, s.seq),
@@ -134,9 +149,15 @@ class Nf4LoraTrainer:
         rdt.sq_sum_noalloc([self.g], self.sumsq)
         rdt.clip_scale(self.sumsq, o["max_norm"], self.scale, self.nonfinite)
         rdt.step_advance(self.step_dev)
-        rdt.adamw_step(self.lora, self.g, self.m, self.v, None, o["lr"], o["beta1"],
-                       o["beta2"], o["eps"], o["weight_decay"], scale=self.scale,
-                       skip=self.nonfinite, step_dev=self.step_dev)
+        if self.state_bits == 8:
+            self.opt.set_lr(o["lr"])
+            self.opt.set_weight_decay(o["weight_decay"])
+            rdt.tensors_adamw(self.opt, None, o["beta1"], o["beta2"], o["eps"], scale=self.scale,
+                              skip=self.nonfinite, step_dev=self.step_dev, seed=self.state_seed)
+        else:
+            rdt.adamw_step(self.lora, self.g, self.m, self.v, None, o["lr"], o["beta1"],
+                           o["beta2"], o["eps"], o["weight_decay"], scale=self.scale,
+                           skip=self.nonfinite, step_dev=self.step_dev)
         self.refresh_shadow()
 
     def train_step(self, x, dy):

@@ -37,6 +37,14 @@ leaving the first block is clipped by its own norm and scatter-added into the
 table's gradient (deterministically, in token order); the table has its own
 AdamW, outside the global clip.
 
+8-bit optimizer states (``state_bits=8``): ``m`` and ``v`` hold e4m3 codes with one scale
+per 256 elements (``rdt_tensors_adamw``: 2.03 bytes a parameter instead of 8), updated
+tensor by tensor in one call, rounded up or down at random from ``state_seed`` and the
+step (``state_seed=None``: to nearest). Everything else is as with 32-bit states.
+
+Scoring (``score``): the forward pass, then log probabilities of given tokens, entropies
+and the most likely alternatives of the LM head (``rdt_head_logprobs``), without gradients.
+
 CUDA graph (``train_step_graph``): the whole step (every micro-batch, the clip
 and AdamW) is captured once into one graph that reads its inputs from the
 trainer's staging buffers and is replayed each step; the optimizer's step
@@ -59,8 +67,11 @@ def _align(n: int, a: int = 64) -> int:
 
 class DecoderTrainer:
     def __init__(self, shape: DecoderShape, device="cuda", optim=None, checkpoint_segments=0,
-                 accumulation_steps=1, embedding=False):
+                 accumulation_steps=1, embedding=False, state_bits=32, state_seed=0):
         self.shape = s = shape
+        if state_bits not in (32, 8):
+            raise ValueError("state_bits must be 32 or 8")
+        self.state_bits, self.state_seed = state_bits, state_seed
         self.accumulation_steps = n_acc = max(1, int(accumulation_steps))
         self.device = torch.device(device)
         self.optim = dict(OPTIM if optim is None else optim)
@@ -77,8 +88,9 @@ class DecoderTrainer:
         self.w = torch.zeros(self.n_params, **f32)
         self.wb = torch.zeros(self.n_params, dtype=torch.bfloat16, device=dev)
         self.g = torch.zeros(self.n_params, **f32)
-        self.m = torch.zeros(self.n_params, **f32)
-        self.v = torch.zeros(self.n_params, **f32)
+        state = dict(dtype=torch.float32 if state_bits == 32 else torch.uint8, device=dev)
+        self.m = torch.zeros(self.n_params, **state)
+        self.v = torch.zeros(self.n_params, **state)
         self.saved_bytes = rdt.block_saved_bytes(self.cfg, s.batch, s.seq)
         self.checkpoint_segments = int(checkpoint_segments)
         if self.checkpoint_segments > 0:
@@ -100,14 +112,15 @@ class DecoderTrainer:
         self.nonfinite = torch.zeros(1, dtype=torch.int32, device=dev)
         self.step_dev = torch.zeros(1, dtype=torch.int32, device=dev)  # AdamW's step count
         self.graph = None
+        self.score_ws = None
         self.loss_partials = torch.zeros(n_acc * T, **f32)
         self.targets = torch.zeros(T, dtype=torch.int32, device=dev)
         self.embedding = bool(embedding)
         if self.embedding:
             self.emb = torch.zeros((V, H), **f32)
             self.emb_g = torch.zeros((V, H), **f32)
-            self.emb_m = torch.zeros((V, H), **f32)
-            self.emb_v = torch.zeros((V, H), **f32)
+            self.emb_m = torch.zeros((V, H), **state)
+            self.emb_v = torch.zeros((V, H), **state)
             self.ids = torch.zeros(n_acc * T, dtype=torch.int32, device=dev)
             self.emb_ws = torch.empty(rdt.embedding_workspace_bytes(T), dtype=torch.uint8,
                                       device=dev)
@@ -120,7 +133,29 @@ class DecoderTrainer:
             # does it
             with torch.cuda.device(dev):
                 rdt.sq_sum_noalloc([self.emb_scale], self.emb_sumsq)
+        if state_bits == 8:
+            spans = [(li * self.per_block + off, cnt) for li in range(L)
+                     for off, cnt in self.offsets.values()]
+            self.opt = self._opt_list(spans + [(self.off_gf, H), (self.off_lm, V * H)], self.g,
+                                      self.w, self.m, self.v, self.wb)
+            if self.embedding:
+                self.emb_opt = self._opt_list([(0, V * H)], self.emb_g.view(-1),
+                                              self.emb.view(-1), self.emb_m.view(-1),
+                                              self.emb_v.view(-1), None)
         self.step_count = 0
+
+    def _opt_list(self, spans, g, w, m, v, wb):
+        """rdt.OptTensors of the tensors at (offset, count) of flat buffers, with new scales."""
+        def cut(buf):
+            return [buf[a:a + n] for a, n in spans]
+
+        def scales():
+            return [torch.zeros(-(-n // rdt.STATE_RUN), dtype=torch.float32, device=self.device)
+                    for _, n in spans]
+
+        return rdt.OptTensors(g=cut(g), w=cut(w), m=cut(m), v=cut(v), m_scale=scales(),
+                              v_scale=scales(), w_bf16=None if wb is None else cut(wb),
+                              lr=self.optim["lr"], weight_decay=self.optim["weight_decay"])
 
     # -------------------------------------------------------------- views
     def block_slice(self, buf, layer):
@@ -189,6 +224,10 @@ class DecoderTrainer:
         if self.embedding:
             self.emb_m.zero_()
             self.emb_v.zero_()
+        if self.state_bits == 8:
+            for opt in [self.opt] + ([self.emb_opt] if self.embedding else []):
+                for scale in opt.tensors["m_scale"] + opt.tensors["v_scale"]:
+                    scale.zero_()
         self.step_count = 0
 
     # --------------------------------------------------------------- step
@@ -254,6 +293,11 @@ class DecoderTrainer:
         rdt.clip_scale(self.sumsq, o["max_norm"], self.scale, self.nonfinite)
         self.step_count += 1
         rdt.step_advance(self.step_dev)
+        if self.state_bits == 8:
+            self._update_8_bit(self.opt, self.scale, self.nonfinite)
+            if self.embedding:
+                self._update_8_bit(self.emb_opt, None, self.emb_nonfinite)
+            return
         rdt.adamw_step(self.w, self.g, self.m, self.v, None, o["lr"], o["beta1"], o["beta2"],
                        o["eps"], o["weight_decay"], scale=self.scale, skip=self.nonfinite,
                        w_bf16=self.wb, step_dev=self.step_dev)
@@ -261,6 +305,46 @@ class DecoderTrainer:
             rdt.adamw_step(self.emb, self.emb_g, self.emb_m, self.emb_v, None, o["lr"],
                            o["beta1"], o["beta2"], o["eps"], o["weight_decay"],
                            skip=self.emb_nonfinite, step_dev=self.step_dev)
+
+    def _update_8_bit(self, opt, scale, skip):
+        o = self.optim
+        opt.set_lr(o["lr"])
+        opt.set_weight_decay(o["weight_decay"])
+        rdt.tensors_adamw(opt, None, o["beta1"], o["beta2"], o["eps"], scale=scale, skip=skip,
+                          step_dev=self.step_dev, seed=self.state_seed)
+
+    # -------------------------------------------------------------- scoring
+    def score(self, x=None, targets=None, ids=None, top=0, logit_scale=1.0):
+        """Scores one batch of T tokens with the current weights: a dict of device tensors
+        ``entropy``, ``lse`` [T], with targets (int32 [T], negative: not scored) ``logp``
+        [T], with top > 0 ``top_ids``, ``top_logp`` [T, top] (rdt_head_logprobs). x, ids as
+        for train_step. The activations kept for a backward pass are overwritten."""
+        s, cfg, T = self.shape, self.cfg, self.shape.tokens
+        if ids is not None:
+            self.ids[:T].copy_(ids)
+        if self.embedding:
+            rdt.embedding_forward(self.emb, self.ids[:T], self.h[0])
+        elif x is not None:
+            self.h[0].copy_(x)
+        for li in range(s.layers):
+            rdt.block_forward(cfg, s.batch, s.seq, self.block_slice(self.w, li),
+                              self.block_slice(self.wb, li), self.h[li], self.h[li + 1],
+                              self.saved_slice(li), self.block_ws)
+        if self.score_ws is None:
+            self.score_ws = torch.empty(rdt.head_logprobs_workspace_bytes(cfg, T),
+                                        dtype=torch.uint8, device=self.device)
+        f32 = dict(dtype=torch.float32, device=self.device)
+        out = {"entropy": torch.empty(T, **f32), "lse": torch.empty(T, **f32)}
+        if targets is not None:
+            out["logp"] = torch.empty(T, **f32)
+            targets = targets.to(device=self.device, dtype=torch.int32)
+        if top:
+            out["top_ids"] = torch.empty((T, top), dtype=torch.int32, device=self.device)
+            out["top_logp"] = torch.empty((T, top), **f32)
+        rdt.head_logprobs(cfg, self.h[s.layers], self.tensor(self.w, "head", "g_final"),
+                          self.tensor(self.wb, "head", "w_lm"), self.score_ws, targets=targets,
+                          logit_scale=logit_scale, **out)
+        return out
 
     def train_step(self, x=None, targets=None, ids=None):
         """One full step; returns the device tensor of per-token loss partials.
