@@ -41,11 +41,6 @@ __device__ __forceinline__ float keep_finite(float x) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(kLowest));
   return r;
 }
-// In a row whose maximum is above it, a logit of kFloor or less has
-// probability 0 for every logit_scale; raised to it, it needs no case of its
-// own (c (z - m) stays finite).
-constexpr float kFloor = -0x1p100f;
-
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
   uint64_t r;
@@ -97,8 +92,14 @@ __device__ __forceinline__ uint32_t key_index(uint64_t key) {
 
 // ------------------------------------------------------------ 16-byte vectors
 // kPer elements of a row, as loaded; filled with -inf where the row has none.
+//
+// kFloor: in a row whose maximum is `near`, a logit of kFloor or less has
+// probability 0; raised to it, masked tokens need no case of their own.
 template <typename T> struct Vec;
 template <> struct Vec<float> {
+  static constexpr float kFloor = -0x1p100f;
+  // For every logit_scale; c (z - m) stays finite.
+  static __device__ __forceinline__ bool near(float m, float) { return m > kFloor && m <= -kFloor; }
   static constexpr int kPer = 4;
   static constexpr uint32_t kNone = 0xff800000u;
   static __device__ __forceinline__ void unpack(const uint4& r, float* x) {
@@ -117,6 +118,8 @@ template <> struct Vec<float> {
   }
 };
 template <> struct Vec<bf16> {
+  static constexpr float kFloor = -0x1p100f;
+  static __device__ __forceinline__ bool near(float m, float) { return m > kFloor && m <= -kFloor; }
   static constexpr int kPer = 8;
   static constexpr uint32_t kNone = 0xff80ff80u;
   static __device__ __forceinline__ void unpack(const uint4& r, float* x) {
@@ -128,7 +131,7 @@ template <> struct Vec<bf16> {
     const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
     return fmaxf(__low2float(m), __high2float(m));
   }
-  // A power of 2 is a bf16 value: two elements are raised at once.
+  // kFloor is a bf16 value: two elements are raised at once.
   static __device__ __forceinline__ void raised(const uint4& r, float* x) {
     const __nv_bfloat162 low = __float2bfloat162_rn(kFloor);
     uint4 q = r;
@@ -139,6 +142,8 @@ template <> struct Vec<bf16> {
   }
 };
 template <> struct Vec<__half> {
+  static constexpr float kFloor = -65504.f;  // the lowest finite one
+  static __device__ __forceinline__ bool near(float m, float c) { return (m - kFloor) * c > 160.f; }
   static constexpr int kPer = 8;
   static constexpr uint32_t kNone = 0xfc00fc00u;
   static __device__ __forceinline__ void unpack(const uint4& r, float* x) {
@@ -155,11 +160,13 @@ template <> struct Vec<__half> {
     const __half2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
     return fmaxf(__low2float(m), __high2float(m));
   }
-  // In fp32: kFloor is below every fp16 value.
   static __device__ __forceinline__ void raised(const uint4& r, float* x) {
-    unpack(r, x);
+    const __half2 low = __float2half2_rn(kFloor);
+    uint4 q = r;
+    __half2* h = reinterpret_cast<__half2*>(&q);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) x[i] = max_nan(x[i], kFloor);
+    for (int i = 0; i < 4; ++i) h[i] = __hmax2_nan(h[i], low);
+    unpack(q, x);
   }
 };
 
@@ -237,13 +244,6 @@ __device__ __forceinline__ void rebase(Sums& a, float m, float c) {
   a.s0 = f * a.s0;
   a.m = m;
 }
-__device__ __forceinline__ Sums join(Sums a, Sums b, float c) {
-  const float m = fmaxf(a.m, b.m);
-  rebase(a, m, c);
-  rebase(b, m, c);
-  return Sums{m, a.s0 + b.s0, a.s1 + b.s1};
-}
-
 // ------------------------------------------------------- lists of 32, by lane
 // A warp holds a list of 32 keys, one per lane, largest in lane 0.
 constexpr unsigned kAll = 0xffffffffu;
@@ -292,9 +292,17 @@ struct LogprobArgs {
 };
 
 constexpr int kMaxSplit = 8;  // CTAs that share a row (a cluster of the portable size)
-constexpr int kUnroll = 4;    // vectors a thread works on at once: a group
-constexpr int kStages = 3;    // groups a thread holds in shared memory
-constexpr int kSegments = 16; // parts of a thread's groups whose maxima are kept
+// A group: the vectors a thread works on at once. A thread holds `stages`
+// groups in shared memory, all but one of them under way.
+template <int kThreads, bool kTop>
+struct Ring {
+  static constexpr int unroll = 4;
+  static constexpr int stages = kThreads == 512 ? 2 : 3;
+  static constexpr int bytes = unroll * stages * kThreads * 16;
+};
+// Parts of a thread's groups whose maxima are kept (8 for 256 threads: 16 would leave an SM a
+// CTA less).
+constexpr int segments_of(int threads) { return threads == 256 ? 8 : 16; }
 constexpr int kSample = 64;   // sets of threads whose maxima bound the row's alternatives
 constexpr int kKeys = 256;    // candidates that are ranked by counting
 
@@ -307,9 +315,9 @@ template <int kThreads>
 struct Shared<kThreads, true> {
   Sums warp_sums[kThreads / 32];
   Sums part[kMaxSplit];
-  unsigned long long parts[kMaxSplit][32];
-  unsigned long long best[32];
-  bf16 segment[kSegments][kThreads];  // rounded up
+  unsigned long long parts[kThreads < 256 ? 1 : kMaxSplit][32];  // smaller CTAs share no row
+  unsigned long long best[32], merged[32];
+  bf16 segment[segments_of(kThreads)][kThreads];  // rounded up
   float sample[kSample];
   float bound;
   int items, keys;
@@ -319,8 +327,23 @@ template <int kThreads>
 struct Lists {
   unsigned long long list[kThreads / 32][32];
   unsigned long long key[kKeys];
-  uint16_t item[kSegments * kThreads];
+  uint16_t item[segments_of(kThreads) * kThreads];
 };
+
+// The sums of kLanes (a power of 2) neighbouring lanes, in each of them.
+template <int kLanes>
+__device__ __forceinline__ Sums join_lanes(Sums s, float c) {
+  float m = s.m;
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+  rebase(s, m, c);
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) {
+    s.s0 += __shfl_xor_sync(kAll, s.s0, o);
+    s.s1 += __shfl_xor_sync(kAll, s.s1, o);
+  }
+  return s;
+}
 
 // The CTA's sums from its threads', in every thread: the maximum first, one
 // rebase, then plain sums, within warps and then between them.
@@ -332,17 +355,7 @@ __device__ __forceinline__ Sums join_sums(Sums s, float c, Sums* warp_sums) {
   s.s1 = warp_sum(s.s1);
   if (lane == 0) warp_sums[warp] = s;
   __syncthreads();
-  s = warp_sums[lane % kWarps];
-  float m = s.m;
-#pragma unroll
-  for (int o = kWarps / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
-  rebase(s, m, c);
-#pragma unroll
-  for (int o = kWarps / 2; o > 0; o >>= 1) {
-    s.s0 += __shfl_xor_sync(kAll, s.s0, o);
-    s.s1 += __shfl_xor_sync(kAll, s.s1, o);
-  }
-  return s;
+  return join_lanes<kWarps>(warp_sums[lane % kWarps], c);
 }
 
 // A thread's vectors v, v + kThreads, ... below v1, whatever they hold.
@@ -369,19 +382,20 @@ __device__ __noinline__ Sums sums_of_any(const Row<T>& row, int v, int v1, float
   return s;
 }
 
-// The same for values whose maximum (over the CTA) is in (kFloor, -kFloor],
-// without special values but NaN and with two elements to an instruction. A
+// The same for values whose maximum (over the CTA) is `near`, without special
+// values but NaN and with two elements to an instruction. A
 // thread with nothing above kFloor returns m = kFloor. t is 0 and 2^t 1 at the
 // maximum itself, so a row with one token left has ln p = 0.
 //
-// The loads run kStages - 1 groups ahead, each thread's into its own part of
+// The loads run Ring::stages - 1 groups ahead, each thread's into its own part of
 // `ring` (no barrier: a thread reads only what it copied). `segment`, where not
-// null, receives the maxima of kSegments runs of `length` groups (-inf for
+// null, receives the maxima of segments_of() runs of `length` groups (-inf for
 // none, NaN not seen), rounded up to bf16, and `raw` the largest, not rounded.
-template <typename T, int kThreads>
+template <typename T, int kThreads, bool kTop>
 __device__ __forceinline__ Sums sums_of(const Row<T>& row, int v, int v1, float c, uint4* ring,
                                         bf16 (*segment)[kThreads], int length, float& raw) {
   constexpr int kPer = Vec<T>::kPer;
+  constexpr int kUnroll = Ring<kThreads, kTop>::unroll, kStages = Ring<kThreads, kTop>::stages;
   constexpr int kStep = kUnroll * kThreads;
   ring += threadIdx.x;
   auto fetch = [&](int g, int stage) {
@@ -392,7 +406,7 @@ __device__ __forceinline__ Sums sums_of(const Row<T>& row, int v, int v1, float 
   };
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) fetch(v + i * kStep, i);
-  float m = kFloor, segment_m = -INFINITY;
+  float m = Vec<T>::kFloor, segment_m = -INFINITY;
   int left = length, filled = 0;
   uint64_t s0 = 0, s1 = 0;
   const uint64_t cc = pack2(c, c);
@@ -440,7 +454,7 @@ __device__ __forceinline__ Sums sums_of(const Row<T>& row, int v, int v1, float 
   }
   if (segment) {
     raw = fmaxf(raw, segment_m);
-    for (; filled < kSegments; ++filled) {
+    for (; filled < segments_of(kThreads); ++filled) {
       segment[filled][threadIdx.x] = __float2bfloat16_ru(segment_m);
       segment_m = -INFINITY;
     }
@@ -451,21 +465,22 @@ __device__ __forceinline__ Sums sums_of(const Row<T>& row, int v, int v1, float 
 }
 
 // f(element, index) for the elements of the listed (segment, thread) pairs'
-// vectors whose maximum is at least `low`; the vectors are spread over the
-// threads, kUnroll of each under way. With kWhole f is called by whole warps,
+// vectors (`length` each) whose maximum is at least `low`; they are spread
+// over the threads, kReread of each under way. With kWhole f is called by whole warps,
 // with -inf where a lane has no such element.
 template <typename T, int kThreads, bool kWhole, typename F>
 __device__ __forceinline__ void for_each_candidate(const Row<T>& row, int v0, int v1,
                                                    const uint16_t* item, int items, int length,
                                                    float low, F f) {
   constexpr int kPer = Vec<T>::kPer;
+  constexpr int kReread = kThreads == 128 ? 8 : 4;  // (more registers leave 256 threads a CTA less)
   const int lane = threadIdx.x & 31;
-  const int each = length * kUnroll, pairs = items * each;
-  for (int q = threadIdx.x; q - lane < pairs; q += kUnroll * kThreads) {
-    uint4 r[kUnroll];
-    int at[kUnroll];
+  const int each = length, pairs = items * each;
+  for (int q = threadIdx.x; q - lane < pairs; q += kReread * kThreads) {
+    uint4 r[kReread];
+    int at[kReread];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < kReread; ++u) {
       const int pair = q + u * kThreads;
       r[u] = Row<T>::none();
       at[u] = v0;
@@ -476,7 +491,7 @@ __device__ __forceinline__ void for_each_candidate(const Row<T>& row, int v0, in
       }
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < kReread; ++u) {
       const bool some = Vec<T>::max(r[u]) >= low;
       if (kWhole ? !__any_sync(kAll, some) : !some) continue;
       float x[kPer];
@@ -530,7 +545,7 @@ __device__ __noinline__ void select_any(const Row<T>& row, int v0, int v1, const
 template <typename T, int kThreads, bool kTop>
 __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a, int split) {
   constexpr int kWarps = kThreads / 32;
-  extern __shared__ uint4 ring[];  // kStages kUnroll kThreads; after the loop, lists
+  extern __shared__ uint4 ring[];  // Ring::bytes; after the loop, lists
   __shared__ Shared<kThreads, kTop> sh;
   const int row_i = split == 1 ? blockIdx.x : blockIdx.x / split;
   const int part = split == 1 ? 0 : blockIdx.x % split;
@@ -552,28 +567,31 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a,
   }
   // shared memory of another CTA may be written once that CTA runs: every CTA says so here and
   // waits for the others only before its stores
-  if (split > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+  if (kThreads >= 256 && split > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
   const Row<T> row(static_cast<const T*>(a.logits) + static_cast<int64_t>(row_i) * a.ld, a.vocab);
   const int v0 = static_cast<int>(static_cast<int64_t>(row.vectors) * part / split);
   const int v1 = static_cast<int>(static_cast<int64_t>(row.vectors) * (part + 1) / split);
   const float c = a.scale * kLog2e;
+  float target_z = 0.f;  // long before it is needed
+  if (tid == 0 && part == 0 && a.logp && target < a.vocab) target_z = to_f(row.z[target]);
 
+  constexpr int kUnroll = Ring<kThreads, kTop>::unroll;
   const int groups = (v1 - v0 + kUnroll * kThreads - 1) / (kUnroll * kThreads);
-  const int length = max(1, (groups + kSegments - 1) / kSegments);
+  const int length = max(1, (groups + segments_of(kThreads) - 1) / segments_of(kThreads));
   bf16(*segment)[kThreads] = nullptr;
   float raw = -inf;
   if constexpr (kTop) segment = sh.segment;
-  Sums s = sums_of<T, kThreads>(row, v0 + tid, v1, c, ring, segment, length, raw);
+  Sums s = sums_of<T, kThreads, kTop>(row, v0 + tid, v1, c, ring, segment, length, raw);
   if constexpr (kTop) {
     float m = raw;
 #pragma unroll
     for (int o = 1; o < kThreads / kSample; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
     if (tid % (kThreads / kSample) == 0) sh.sample[tid / (kThreads / kSample)] = m;
     if (tid == 0) sh.items = sh.keys = 0;
-    if (tid < 32) sh.best[tid] = 0;
+    if (tid < 32) sh.best[tid] = sh.merged[tid] = 0;
   }
   Sums all = join_sums<kWarps>(s, c, sh.warp_sums);
-  if (!(all.m > kFloor && all.m <= -kFloor)) {  // nothing left, or a maximum beyond the fast range
+  if (!Vec<T>::near(all.m, c)) {  // nothing left, or a maximum outside the fast range
     s = sums_of_any<T, kThreads>(row, v0 + tid, v1, c);
     __syncthreads();
     all = join_sums<kWarps>(s, c, sh.warp_sums);
@@ -594,19 +612,36 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a,
     __syncthreads();
     const float low = sh.bound;  // -inf: fewer than `top` sets hold anything
     Lists<kThreads>& lists = *reinterpret_cast<Lists<kThreads>*>(ring);
-    static_assert(sizeof(Lists<kThreads>) <= kStages * kUnroll * kThreads * 16, "fits the ring");
+    static_assert(sizeof(Lists<kThreads>) <= Ring<kThreads, kTop>::bytes, "fits the ring");
+    unsigned mask = 0;  // the thread's segments that reach the bound
     if (raw >= low && raw > -inf) {
 #pragma unroll
-      for (int i = 0; i < kSegments; ++i) {
+      for (int i = 0; i < segments_of(kThreads); ++i) {
         const float m = bf16_to_f(sh.segment[i][tid]);
-        if (m >= low && m > -inf)
-          lists.item[atomicAdd(&sh.items, 1)] = static_cast<uint16_t>(i * kThreads + tid);
+        mask |= static_cast<unsigned>(m >= low && m > -inf) << i;
+      }
+    }
+    if (__any_sync(kAll, mask)) {  // one place for the warp's
+      const int n = __popc(mask);
+      int before = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(kAll, before, o);
+        if (lane >= o) before += x;
+      }
+      int at = 0;
+      if (lane == 31) at = atomicAdd(&sh.items, before);
+      at = __shfl_sync(kAll, at, 31) + before - n;
+      while (mask) {
+        const int i = __ffs(mask) - 1;
+        mask &= mask - 1;
+        lists.item[at++] = static_cast<uint16_t>(i * kThreads + tid);
       }
     }
     __syncthreads();
     // the order of items and keys varies, what is chosen among them does not
     for_each_candidate<T, kThreads, false>(
-        row, v0, v1, lists.item, sh.items, length, low, [&](float x, int index) {
+        row, v0, v1, lists.item, sh.items, length * kUnroll, low, [&](float x, int index) {
           const uint64_t k = order_key(x, index);
           if (k == 0) return;
           const int n = atomicAdd(&sh.keys, 1);
@@ -618,18 +653,19 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a,
       for (int i = tid; i < keys; i += kThreads) {
         const unsigned long long k = lists.key[i];
         int rank = 0;
+#pragma unroll 8
         for (int j = 0; j < keys; ++j) rank += lists.key[j] > k;
         if (rank < a.top) sh.best[rank] = k;
       }
     } else {
-      select_any<T, kThreads>(row, v0, v1, lists.item, sh.items, length, low, a.top, lists.list,
+      select_any<T, kThreads>(row, v0, v1, lists.item, sh.items, length * kUnroll, low, a.top, lists.list,
                               sh.best);
     }
     __syncthreads();
     list = sh.best[lane];
   }
 
-  if (split > 1) {
+  if constexpr (kThreads >= 256) if (split > 1) {
     // every part to the cluster's first CTA; it joins them in order
     asm volatile("barrier.cluster.wait;" ::: "memory");
     if (warp == 0) {
@@ -643,13 +679,30 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a,
     }
     cluster_sync();
     if (part != 0) return;
-    if (warp == 0) {
-      all = sh.part[0];
-      for (int w = 1; w < split; ++w) all = join(all, sh.part[w], c);
-      if constexpr (kTop) {
-        list = sh.parts[0][lane];
-        for (int w = 1; w < split; ++w) list = merge32(list, sh.parts[w][31 - lane]);
+    if constexpr (kTop) {
+      // a key's place: its place in its own list, and in the others by halving them
+      for (int i = tid; i < split * 32; i += kThreads) {
+        const unsigned long long k = sh.parts[i >> 5][i & 31];
+        int rank = i & 31;
+        int n[kMaxSplit] = {};  // keys of list q above k, the lists side by side
+#pragma unroll
+        for (int step = 16; step > 0; step >>= 1)
+#pragma unroll
+          for (int q = 0; q < kMaxSplit; ++q)
+            if (q < split && sh.parts[q][n[q] + step - 1] > k) n[q] += step;
+#pragma unroll
+        for (int q = 0; q < kMaxSplit; ++q) {
+          if (q < split && n[q] == 31 && sh.parts[q][31] > k) n[q] = 32;
+          if (q != i >> 5) rank += n[q];
+        }
+        if (k != 0 && rank < 32) sh.merged[rank] = k;
       }
+      __syncthreads();
+      list = sh.merged[lane];
+    }
+    if (warp == 0) {
+      all = lane % kMaxSplit < split ? sh.part[lane % kMaxSplit] : Sums{-inf, 0.f, 0.f};
+      all = join_lanes<kMaxSplit>(all, c);
     }
   }
   if (warp != 0) return;
@@ -659,7 +712,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a,
     if (a.logp) {
       float lp = nan_f();
       if (live && target < a.vocab)
-        lp = some ? (to_f(row.z[target]) - all.m) * a.scale - log_sum : -inf;
+        lp = some ? (target_z - all.m) * a.scale - log_sum : -inf;
       a.logp[row_i] = lp;
     }
     if (a.entropy)
@@ -684,7 +737,7 @@ cudaError_t launch_logprobs(const LogprobArgs& a, int split, cudaStream_t s) {
   cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * split, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = s;
-  cfg.dynamicSmemBytes = kStages * kUnroll * kThreads * sizeof(uint4);
+  cfg.dynamicSmemBytes = Ring<kThreads, kTop>::bytes;
   static std::atomic<uint64_t> allowed{0};  // devices where the kernel may use that much
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -714,17 +767,22 @@ cudaError_t logprobs_of(const LogprobArgs& a, cudaStream_t s) {
   const int vectors = a.vocab / Vec<T>::kPer;
   if (vectors <= 1024)
     return a.top ? launch_logprobs<T, 64, true>(a, 1, s) : launch_logprobs<T, 64, false>(a, 1, s);
-  // Rows are shared by clusters while they are too few for one wave of 4 CTAs an SM.
+  // At most a row an SM: a cluster a row, as long as each thread has four vectors (152 fp32
+  // rows of 151,936, 20 alternatives: 27 us with 256 threads, 33 with 512, 39 with 128 and no
+  // cluster; without alternatives 21 us with 512, 23 with 256).
   const int sms = num_sms();
-  int split = 1;
-  while (split < kMaxSplit && static_cast<int64_t>(a.rows) * split <= sms &&
-         vectors / (2 * split) >= 1024)
-    split *= 2;
+  if (a.rows <= sms) {
+    int split = 1;
+    while (split < kMaxSplit && a.rows * split <= sms && vectors >= 4 * 1024 * split) split *= 2;
+    return a.top ? launch_logprobs<T, 256, true>(a, split, s)
+                 : launch_logprobs<T, 512, false>(a, split, s);
+  }
   // Alternatives leave a CTA without loads under way for some 5 us a row; smaller and more
-  // CTAs hide more of it (4096 rows of 151,936 bf16 logits, 20 alternatives: 228 us with 128
-  // threads, 240 with 256, 244 with 64; without alternatives 204, 197 and 200).
-  return a.top ? launch_logprobs<T, 128, true>(a, split, s)
-               : launch_logprobs<T, 256, false>(a, split, s);
+  // CTAs hide more of it once there are rows for them (20 alternatives, 151,936 logits: 608
+  // fp32 rows 69 us with 128 threads, 88 with 256, but 304 rows 47 and 43; 4096 bf16 rows 229
+  // and 238, without alternatives 204 and 197).
+  if (a.top && a.rows > 2 * sms) return launch_logprobs<T, 128, true>(a, 1, s);
+  return a.top ? launch_logprobs<T, 256, true>(a, 1, s) : launch_logprobs<T, 256, false>(a, 1, s);
 }
 
 cudaError_t logprobs(const LogprobArgs& a, int dtype, cudaStream_t s) {
