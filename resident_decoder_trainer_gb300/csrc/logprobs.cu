@@ -362,21 +362,27 @@ __device__ __forceinline__ Sums join_sums(Sums s, float c, Sums* warp_sums) {
 template <typename T, int kThreads>
 __device__ __noinline__ Sums sums_of_any(const Row<T>& row, int v, int v1, float c) {
   constexpr int kPer = Vec<T>::kPer;
+  constexpr int kAhead = 4;
   Sums s{-INFINITY, 0.f, 0.f};
-#pragma unroll 1
-  for (; v < v1; v += kThreads) {
-    const uint4 r = row.load(v);
-    const float m = Vec<T>::max(r);
-    if (m > s.m) rebase(s, m, c);
-    const float base = base_of(s.m);
-    float x[kPer];
-    Vec<T>::unpack(r, x);
+  for (; v < v1; v += kAhead * kThreads) {
+    uint4 r[kAhead];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const float t = keep_finite((x[i] - base) * c);
-      const float e = exp2_fast(t);
-      s.s0 += e;
-      s.s1 = fmaf(e, t, s.s1);
+    for (int u = 0; u < kAhead; ++u)
+      r[u] = v + u * kThreads < v1 ? row.load(v + u * kThreads) : Row<T>::none();
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const float m = Vec<T>::max(r[u]);
+      if (m > s.m) rebase(s, m, c);
+      const float base = base_of(s.m);
+      float x[kPer];
+      Vec<T>::unpack(r[u], x);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const float t = keep_finite((x[i] - base) * c);
+        const float e = exp2_fast(t);
+        s.s0 += e;
+        s.s1 = fmaf(e, t, s.s1);
+      }
     }
   }
   return s;
@@ -384,13 +390,14 @@ __device__ __noinline__ Sums sums_of_any(const Row<T>& row, int v, int v1, float
 
 // The same for values whose maximum (over the CTA) is `near`, without special
 // values but NaN and with two elements to an instruction. A
-// thread with nothing above kFloor returns m = kFloor. t is 0 and 2^t 1 at the
-// maximum itself, so a row with one token left has ln p = 0.
+// thread with nothing above kFloor returns m = kFloor, with nothing but -inf
+// what an empty set has. t is 0 and 2^t 1 at the maximum itself, so a row with
+// one token left has ln p = 0.
 //
 // The loads run Ring::stages - 1 groups ahead, each thread's into its own part of
 // `ring` (no barrier: a thread reads only what it copied). `segment`, where not
 // null, receives the maxima of segments_of() runs of `length` groups (-inf for
-// none, NaN not seen), rounded up to bf16, and `raw` the largest, not rounded.
+// none, NaN not seen), rounded up to bf16; `raw` receives the largest of all.
 template <typename T, int kThreads, bool kTop>
 __device__ __forceinline__ Sums sums_of(const Row<T>& row, int v, int v1, float c, uint4* ring,
                                         bf16 (*segment)[kThreads], int length, float& raw) {
@@ -421,6 +428,7 @@ __device__ __forceinline__ Sums sums_of(const Row<T>& row, int v, int v1, float 
     float top = Vec<T>::max(r[0]);
 #pragma unroll
     for (int u = 1; u < kUnroll; ++u) top = fmaxf(top, Vec<T>::max(r[u]));
+    raw = fmaxf(raw, top);
     if (top > m) {
       const float t = keep_finite((m - top) * c), f = exp2_fast(t);
       const uint64_t ff = pack2(f, f), tt = pack2(t, t);
@@ -432,7 +440,6 @@ __device__ __forceinline__ Sums sums_of(const Row<T>& row, int v, int v1, float 
       segment_m = fmaxf(segment_m, top);
       if (--left == 0) {
         segment[filled++][threadIdx.x] = __float2bfloat16_ru(segment_m);
-        raw = fmaxf(raw, segment_m);
         segment_m = -INFINITY;
         left = length;
       }
@@ -453,7 +460,6 @@ __device__ __forceinline__ Sums sums_of(const Row<T>& row, int v, int v1, float 
     }
   }
   if (segment) {
-    raw = fmaxf(raw, segment_m);
     for (; filled < segments_of(kThreads); ++filled) {
       segment[filled][threadIdx.x] = __float2bfloat16_ru(segment_m);
       segment_m = -INFINITY;
@@ -461,7 +467,9 @@ __device__ __forceinline__ Sums sums_of(const Row<T>& row, int v, int v1, float 
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   const float2 a = unpack2(s0), b = unpack2(s1);
-  return Sums{m, a.x + a.y, b.x + b.y};
+  const float sum = a.x + a.y;
+  if (raw == -INFINITY && sum == sum) return Sums{-INFINITY, 0.f, 0.f};
+  return Sums{m, sum, b.x + b.y};
 }
 
 // f(element, index) for the elements of the listed (segment, thread) pairs'
@@ -591,7 +599,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a,
     if (tid < 32) sh.best[tid] = sh.merged[tid] = 0;
   }
   Sums all = join_sums<kWarps>(s, c, sh.warp_sums);
-  if (!Vec<T>::near(all.m, c)) {  // nothing left, or a maximum outside the fast range
+  if (!Vec<T>::near(all.m, c) && all.m > -inf) {  // a maximum outside the fast range
     s = sums_of_any<T, kThreads>(row, v0 + tid, v1, c);
     __syncthreads();
     all = join_sums<kWarps>(s, c, sh.warp_sums);
@@ -806,8 +814,7 @@ struct GradArgs {
 };
 
 constexpr int kGradThreads = 256;
-constexpr int kGradPer = 8;     // elements of a thread's piece: 16 bytes of a 16-bit type
-constexpr int kGradUnroll = 2;  // pieces a thread has under way
+constexpr int kGradPer = 8;  // elements of a thread's piece: 16 bytes of a 16-bit type
 
 // Eight elements; inside: all of them in the row and p 16-byte aligned.
 template <typename T>
@@ -868,35 +875,47 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const GradA
   const int pieces = static_cast<int>((static_cast<int64_t>(head) + a.vocab + kGradPer - 1) / kGradPer);
   const bool same = (reinterpret_cast<uintptr_t>(z - head) & 15) == 0;
   const int stride = a.pieces * kGradThreads;
-  for (int q = part * kGradThreads + threadIdx.x; q < pieces; q += kGradUnroll * stride) {
-    float x[kGradUnroll][kGradPer];
-#pragma unroll
-    for (int u = 0; u < kGradUnroll; ++u) {
-      const int j = (q + u * stride) * kGradPer - head;
-      if (q + u * stride < pieces && !none)
-        load_piece(z, j, a.vocab, same && j >= 0 && j <= a.vocab - kGradPer, x[u]);
+  int q = part * kGradThreads + threadIdx.x;
+  if (none) {
+    const float zero[kGradPer] = {};
+    for (; q < pieces; q += stride) {
+      const int j = q * kGradPer - head;
+      store_piece(out, j, a.vocab, j >= 0 && j <= a.vocab - kGradPer, zero);
     }
+    return;
+  }
+  const uint64_t mm = pack2(-st.x, -st.x), cc = pack2(c, c), ss = pack2(-shift, -shift),
+                 aa = pack2(big_a, big_a), bb = pack2(-big_b, -big_b);
+  for (; q < pieces; q += stride) {
+    const int j = q * kGradPer - head, hit = target - j;
+    const bool inside = j >= 0 && j <= a.vocab - kGradPer;
+    float x[kGradPer];
+    load_piece(z, j, a.vocab, same && inside, x);
 #pragma unroll
-    for (int u = 0; u < kGradUnroll; ++u) {
-      if (q + u * stride >= pieces) break;
-      const int j = (q + u * stride) * kGradPer - head;
-#pragma unroll
-      for (int i = 0; i < kGradPer; ++i) {
-        const float t = keep_finite(fmaf(x[u][i] - st.x, c, -shift));
-        float r = exp2_fast(t) * fmaf(-big_b, t, big_a);
-        if (a.d_logp && j + i == target) r = fmaf(a.scale, g, r);
-        x[u][i] = none ? 0.f : r;
-      }
-      store_piece(out, j, a.vocab, j >= 0 && j <= a.vocab - kGradPer, x[u]);
+    for (int i = 0; i < kGradPer; i += 2) {
+      const float2 t = unpack2(fma2(add2(pack2(x[i], x[i + 1]), mm), cc, ss));
+      const float2 k = make_float2(keep_finite(t.x), keep_finite(t.y));
+      const uint64_t e = pack2(exp2_fast(k.x), exp2_fast(k.y));
+      const float2 r = unpack2(mul2(e, fma2(bb, pack2(k.x, k.y), aa)));
+      x[i] = r.x;
+      x[i + 1] = r.y;
     }
+    if (a.d_logp && static_cast<unsigned>(hit) < static_cast<unsigned>(kGradPer)) {
+#pragma unroll
+      for (int i = 0; i < kGradPer; ++i)
+        if (i == hit) x[i] = fmaf(a.scale, g, x[i]);
+    }
+    store_piece(out, j, a.vocab, inside, x);
   }
 }
 
 template <typename T>
 void launch_grad(GradArgs a, int d_dtype, cudaStream_t s) {
   const int pieces = (a.vocab + kGradPer - 1) / kGradPer;
-  a.pieces = (pieces + kGradThreads * kGradUnroll - 1) / (kGradThreads * kGradUnroll);
-  // a CTA per piece of the row while there are few rows, else a few per row
+  a.pieces = (pieces + 2 * kGradThreads - 1) / (2 * kGradThreads);  // two pieces a thread
+  // ... while there are few rows, else four CTAs a row: its stats and gradients are read by
+  // each (4096 bf16 rows of 151,936: 370 us; with two pieces of a thread under way at once
+  // 410, the bytes in flight do not need it and the window of rows grows)
   const int64_t enough = 16LL * num_sms();
   if (static_cast<int64_t>(a.rows) * a.pieces > enough)
     a.pieces = static_cast<int>(std::max<int64_t>(
