@@ -83,6 +83,22 @@ __device__ __forceinline__ void next_tile(const Table<kMax>& tab, int tiles, int
   if (w.tile >= w.end && w.tile < tiles) find_owner(tab, w);
 }
 
+// The launches of one call. They touch no common memory but the final sum's
+// partials, so a later one may start as soon as the one before has all its
+// CTAs running (launches_may_follow) and only has to end after it
+// (end_after_previous, in one thread; the first launch of a call has no
+// previous one to wait for and returns at once). What follows the call in the
+// stream waits for its last launch, and so for all.
+__device__ __forceinline__ void launches_may_follow() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void end_after_previous() {
+  if (blockIdx.x == 0 && threadIdx.x == 0) wait_for_previous();
+}
+
 // Two fp32 operations, each rounded to nearest, in one instruction.
 __device__ __forceinline__ uint64_t bits2(float2 a) {
   uint64_t r;
@@ -230,22 +246,15 @@ __device__ __forceinline__ void add_pair(float& hi, float& lo, float h, float l)
   hi = t;
 }
 
-// Sixteen bytes of g from p on, of which the first `have` elements count.
-template <bool kFull, typename G>
-__device__ __forceinline__ void load16(const G* p, int have, float* x) {
-  constexpr int kPer = 16 / sizeof(G);
-  if (kFull) {
-    const uint4 r = __ldg(reinterpret_cast<const uint4*>(p));
-    if constexpr (sizeof(G) == 4) {
-      x[0] = __uint_as_float(r.x); x[1] = __uint_as_float(r.y);
-      x[2] = __uint_as_float(r.z); x[3] = __uint_as_float(r.w);
-    } else {
-      x[0] = bf16lo(r.x); x[1] = bf16hi(r.x); x[2] = bf16lo(r.y); x[3] = bf16hi(r.y);
-      x[4] = bf16lo(r.z); x[5] = bf16hi(r.z); x[6] = bf16lo(r.w); x[7] = bf16hi(r.w);
-    }
+// Sixteen bytes of gradients to fp32.
+template <bool kBf16>
+__device__ __forceinline__ void unpack16(const uint4& r, float* x) {
+  if constexpr (!kBf16) {
+    x[0] = __uint_as_float(r.x); x[1] = __uint_as_float(r.y);
+    x[2] = __uint_as_float(r.z); x[3] = __uint_as_float(r.w);
   } else {
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) x[k] = k < have ? static_cast<float>(p[k]) : 0.f;
+    x[0] = bf16lo(r.x); x[1] = bf16hi(r.x); x[2] = bf16lo(r.y); x[3] = bf16hi(r.y);
+    x[4] = bf16lo(r.z); x[5] = bf16hi(r.z); x[6] = bf16lo(r.w); x[7] = bf16hi(r.w);
   }
 }
 
@@ -260,6 +269,7 @@ template <bool kBf16, int kMax>
 __global__ void __launch_bounds__(kThreads) tensors_sq_sum_kernel(
     const __grid_constant__ Table<kMax> tab, int tiles, float one,
     double* __restrict__ partials) {
+  launches_may_follow();
   __shared__ double red[kThreads / 32];
   using G = typename std::conditional<kBf16, bf16, float>::type;
   constexpr int kPer = 16 / sizeof(G), kStep = kPer * kThreads;  // elements of a load
@@ -270,31 +280,60 @@ __global__ void __launch_bounds__(kThreads) tensors_sq_sum_kernel(
     for (int k = 0; k < kPer / 2; ++k)
       add_squares<kBf16>(make_float2(x[2 * k], x[2 * k + 1]), hi[k & 3], lo[k & 3], one);
   };
+  // The tiles of the walk's tensor and chunk from its tile on, and whether they are a whole
+  // chunk of whole tiles.
+  auto count_of = [&](const Walk& w) { return min(w.end, w.end_of_chunk) - w.tile; };
+  auto whole = [&](const Walk& w) {
+    return w.tile < tiles && count_of(w) == kSqChunk &&
+           static_cast<int64_t>(w.tile - w.begin + kSqChunk) * kTile <= tab.t[w.o].n;
+  };
+  auto first_of = [&](const Walk& w) {
+    return static_cast<const G*>(tab.t[w.o].g) + static_cast<int64_t>(w.tile - w.begin) * kTile;
+  };
+  auto load = [&](const Walk& w, uint4* r) {
+    const uint4* g = reinterpret_cast<const uint4*>(first_of(w)) + threadIdx.x;
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) r[u] = __ldg(g + u * kThreads);
+  };
   Walk w = first_tile(tab, tiles, kSqChunk);
+  uint4 r[kLoads];
+  bool full = whole(w);
+  if (full) load(w, r);
   while (w.tile < tiles) {
-    const Tensor& t = tab.t[w.o];
-    const int64_t at = static_cast<int64_t>(w.tile - w.begin) * kTile;
-    const int count = min(w.end, w.end_of_chunk) - w.tile;  // tiles of this tensor and chunk
-    const G* g = static_cast<const G*>(t.g) + at + threadIdx.x * kPer;
-    if (count == kSqChunk && at + kSqChunk * kTile <= t.n) {
-      float x[kLoads][kPer];
+    // the next chunk is looked up and its loads started before this one is added
+    Walk n = w;
+    n.tile += count_of(w) - 1;
+    next_tile(tab, tiles, kSqChunk, n);
+    uint4 next_r[kLoads];
+    const bool next_full = whole(n);
+    if (next_full) load(n, next_r);
+    if (full) {
 #pragma unroll
-      for (int u = 0; u < kLoads; ++u) load16<true>(g + u * kStep, 0, x[u]);
-#pragma unroll
-      for (int u = 0; u < kLoads; ++u) add(x[u]);
-    } else {
-      const int left = static_cast<int>(min(t.n - at, static_cast<int64_t>(count) * kTile));
-      for (int e = threadIdx.x * kPer; e < left; e += kStep, g += kStep) {
+      for (int u = 0; u < kLoads; ++u) {
         float x[kPer];
-        if (e + kPer <= left)
-          load16<true>(g, 0, x);
-        else
-          load16<false>(g, left - e, x);
+        unpack16<kBf16>(r[u], x);
+        add(x);
+      }
+    } else {
+      const G* g = first_of(w);
+      const int left =
+          static_cast<int>(min(tab.t[w.o].n - static_cast<int64_t>(w.tile - w.begin) * kTile,
+                               static_cast<int64_t>(count_of(w)) * kTile));
+      for (int e = threadIdx.x * kPer; e < left; e += kStep) {
+        float x[kPer];
+        if (e + kPer <= left) {
+          unpack16<kBf16>(__ldg(reinterpret_cast<const uint4*>(g + e)), x);
+        } else {
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) x[k] = e + k < left ? static_cast<float>(g[e + k]) : 0.f;
+        }
         add(x);
       }
     }
-    w.tile += count - 1;
-    next_tile(tab, tiles, kSqChunk, w);
+    w = n;
+    full = next_full;
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) r[u] = next_r[u];
   }
   // down to one pair a warp in fp32: fp64 additions of every lane took 20 us
   float h = hi[0].x, l = lo[0].x;
@@ -314,10 +353,12 @@ __global__ void __launch_bounds__(kThreads) tensors_sq_sum_kernel(
     for (int w = 0; w < kThreads / 32; ++w) s += red[w];
     partials[blockIdx.x] = s;
   }
+  end_after_previous();
 }
 
 __global__ void __launch_bounds__(kThreads) tensors_sq_final_kernel(
     const double* __restrict__ partials, int n, double* __restrict__ out) {
+  wait_for_previous();
   __shared__ double red[kThreads / 32];
   double s = 0.0;
   for (int i = threadIdx.x; i < n; i += kThreads) s += partials[i];
@@ -585,7 +626,11 @@ constexpr int kChunk = 2;  // tiles of a CTA's step of tensors_adamw_kernel
 template <int kBits, bool kBf16, bool kRandom, int kMax>
 __global__ void __launch_bounds__(kThreads) tensors_adamw_kernel(
     const __grid_constant__ Table<kMax> tab, int tiles, const AdamArgs p) {
-  if (p.skip && *p.skip) return;
+  launches_may_follow();
+  if (p.skip && *p.skip) {
+    end_after_previous();
+    return;
+  }
   const float sc = p.scale ? *p.scale : 1.f;
   float inv_bc1 = p.inv_bc1, inv_root_bc2 = p.inv_root_bc2;
   int step = p.step;
@@ -642,6 +687,7 @@ __global__ void __launch_bounds__(kThreads) tensors_adamw_kernel(
       vs = next_vs;
     }
   }
+  end_after_previous();
 }
 
 rdt_status refuse(const char* msg) {
@@ -712,22 +758,40 @@ int ctas(int tiles, int chunk, int per_sm, int share = INT32_MAX) {
 
 constexpr int kMaxPartials = 2048;  // of one launch
 
+// `follows`: not the call's first launch.
+template <typename K, typename... A>
+cudaError_t launch(K kernel, int grid, size_t smem, cudaStream_t s, bool follows, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = follows ? 1 : 0;
+  note_launch();
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <int kMax>
 cudaError_t sq_sum_launches(const rdt_opt_tensor* list, int count, bool half, double* parts,
                             int64_t room, int64_t* used, cudaStream_t s) {
   return each_launch<kMax>(list, count, [&](const Table<kMax>& tab, int tiles) {
-    const int blocks = std::min(half ? ctas(tiles, kSqTiles<true>, 5) : ctas(tiles, kSqTiles<false>, 6), kMaxPartials);
+    const int blocks = std::min(ctas(tiles, half ? kSqTiles<true> : kSqTiles<false>, 4), kMaxPartials);
     if (*used + blocks > room) return cudaErrorInvalidValue;
-    note_launch();
     auto kernel = half ? tensors_sq_sum_kernel<true, kMax> : tensors_sq_sum_kernel<false, kMax>;
-    kernel<<<blocks, kThreads, 0, s>>>(tab, tiles, 1.f, parts + *used);
+    double* to = parts + *used;
+    const bool follows = *used > 0;
     *used += blocks;
-    return cudaGetLastError();
+    return launch(kernel, blocks, 0, s, follows, tab, tiles, 1.f, to);
   });
 }
 
 template <int kBits, bool kBf16, bool kRandom, int kMax>
-cudaError_t launch_adamw(const Table<kMax>& tab, int tiles, const AdamArgs& a, cudaStream_t s) {
+cudaError_t launch_adamw(const Table<kMax>& tab, int tiles, const AdamArgs& a, bool follows,
+                         cudaStream_t s) {
   constexpr int kBytes = kBits == 8 ? 2 * Stage<kBf16>::kBytes : 0;
   auto kernel = tensors_adamw_kernel<kBits, kBf16, kRandom, kMax>;
   static std::atomic<uint64_t> allowed{0};  // devices where the kernel may use kBytes
@@ -739,23 +803,25 @@ cudaError_t launch_adamw(const Table<kMax>& tab, int tiles, const AdamArgs& a, c
     if (e != cudaSuccess) return e;
     if (dev < 64) allowed.fetch_or(uint64_t(1) << dev);
   }
-  note_launch();
-  kernel<<<ctas(tiles, kChunk, kBits == 32 ? 8 : 4, 6), kThreads, kBytes, s>>>(tab, tiles, a);
-  return cudaGetLastError();
+  return launch(kernel, ctas(tiles, kChunk, kBits == 32 ? 8 : 4, 6), kBytes, s, follows, tab, tiles,
+                a);
 }
 
 template <int kMax>
 cudaError_t adamw_launches(const rdt_opt_tensor* list, int count, bool half, int bits, bool random,
                            const AdamArgs& a, cudaStream_t s) {
+  bool follows = false;
   return each_launch<kMax>(list, count, [&](const Table<kMax>& tab, int tiles) {
+    const bool f = follows;
+    follows = true;
     if (bits == 32)
-      return half ? launch_adamw<32, true, false>(tab, tiles, a, s)
-                  : launch_adamw<32, false, false>(tab, tiles, a, s);
+      return half ? launch_adamw<32, true, false>(tab, tiles, a, f, s)
+                  : launch_adamw<32, false, false>(tab, tiles, a, f, s);
     if (random)
-      return half ? launch_adamw<8, true, true>(tab, tiles, a, s)
-                  : launch_adamw<8, false, true>(tab, tiles, a, s);
-    return half ? launch_adamw<8, true, false>(tab, tiles, a, s)
-                : launch_adamw<8, false, false>(tab, tiles, a, s);
+      return half ? launch_adamw<8, true, true>(tab, tiles, a, f, s)
+                  : launch_adamw<8, false, true>(tab, tiles, a, f, s);
+    return half ? launch_adamw<8, true, false>(tab, tiles, a, f, s)
+                : launch_adamw<8, false, false>(tab, tiles, a, f, s);
   });
 }
 
@@ -791,9 +857,8 @@ rdt_status rdt_tensors_sq_sum(const rdt_opt_tensor* tensors, int32_t count, int3
           ? sq_sum_launches<kFewTensors>(tensors, count, half, parts, room, &used, s)
           : sq_sum_launches<kMaxTensors>(tensors, count, half, parts, room, &used, s);
   if (e != cudaSuccess) return launched(e);
-  note_launch();
-  tensors_sq_final_kernel<<<1, kThreads, 0, s>>>(parts, static_cast<int>(used), sumsq);
-  return launched(cudaGetLastError());
+  return launched(launch(tensors_sq_final_kernel, 1, 0, s, used > 0, parts,
+                         static_cast<int>(used), sumsq));
 }
 
 rdt_status rdt_tensors_adamw(const rdt_opt_tensor* tensors, int32_t count, int32_t g_dtype,

@@ -338,10 +338,11 @@ def test_step_on_the_device(bits, step):
     check_step(p, step=step, seed=8, step_arg=None, step_dev=at)
 
 
-def test_captured_and_replayed():
+@pytest.mark.parametrize("sizes", [SIZES, [300, 5, 2048] * 280], ids=["one launch", "three"])
+def test_captured_and_replayed(sizes):
     """A graph of squared sum, clip scale, step count and update; each replay is the next
     step, with rounding numbers of its own. Two graphs with one workspace, in turn."""
-    p, q = Problem(SIZES, 8, seed=7), Problem(SIZES, 8, seed=7)
+    p, q = Problem(sizes, 8, seed=7), Problem(sizes, 8, seed=7)
     sumsq = torch.zeros(1, dtype=torch.float64, device="cuda")
     scale = torch.ones(1, device="cuda")
     bad = torch.zeros(1, dtype=torch.int32, device="cuda")
