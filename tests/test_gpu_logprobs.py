@@ -121,6 +121,8 @@ def check(z, targets, top=0, scale=1.0, out=None):
             assert torch.equal(got, want[k]), k
             continue
         w, g = want[k], got.double()
+        beyond = w.abs() > torch.finfo(torch.float32).max  # what fp32 rounds to infinity
+        w = torch.where(beyond, torch.copysign(torch.full_like(w, INF), w), w)
         fine = w.isfinite()
         assert torch.equal(g.isnan(), w.isnan()), k
         assert torch.equal(g[~fine & ~w.isnan()], w[~fine & ~w.isnan()]), k
@@ -228,6 +230,43 @@ def test_large_logits_keep_their_digits():
     again = check(z - 1e6, torch.zeros(4, dtype=torch.int32, device="cuda"), top=5)
     for k in ("logp", "entropy", "top_ids", "top_logp"):
         assert torch.equal(out[k], again[k]), k
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("scale", [1e-6, 1e-3, 30.0, 1e6])
+@pytest.mark.parametrize("vocab", [600, 40001])
+def test_temperatures(vocab, scale, dtype):
+    """From nearly uniform to one token only, with masked tokens (for fp16 at low scales the
+    floor is not clear of the maximum, and a masked token still has probability 0)."""
+    z, t = random_logits(5, vocab, dtype, 31, mask=0.4)
+    z[1] = -INF
+    z[2, ::3] = torch.finfo(dtype).min
+    z[3] = torch.finfo(dtype).min
+    z[3, 5:9] = torch.finfo(dtype).min * 0.999
+    check(z, t, top=6, scale=scale)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows", [5, 40, 100])
+def test_rows_shared_by_a_cluster(rows, dtype):
+    """Few long rows: parts of a row that hold nothing, everything, the NaN, or equal values."""
+    vocab = 151936
+    z, t = random_logits(rows, vocab, dtype, 32)
+    part = vocab // 8
+    z[0, :-part] = -INF                   # only the last part holds anything
+    z[1, part:] = -INF                    # only the first
+    z[2] = -INF
+    z[2, torch.arange(5) * part + 17] = torch.arange(5, device="cuda").to(dtype)
+    z[3, 3 * part + 5] = math.nan         # one part's NaN is the row's
+    z[4] = -INF
+    z[4, 7 * part + 3] = torch.finfo(dtype).min
+    if rows > 5:
+        z[5] = 1.5                        # ties across the parts
+        z[6, -20:] = 50                   # the best all in the last part
+        z[7] = -INF
+        t[8] = -1
+    check(z, t, top=20)
+    check(z, t, top=0)
 
 
 @pytest.mark.parametrize("keep", ["logp", "entropy", "lse", "stats", "top"])

@@ -470,6 +470,47 @@ def test_eight_bit_states_follow_thirty_two():
         assert float((way - ways[0]).norm() / ways[0].norm()) < 1 / 3
 
 
+def test_a_tensor_of_more_than_32_bits_of_elements():
+    """2^32 + 1000 elements: addresses, scales and rounding numbers behind 2^32, against the
+    same step of a short tensor (whose rounding goes by its own indexes: states to one code)."""
+    n, tail = (1 << 32) + 1000, 5 * RUN + 1000
+    a = n - tail
+    gen = torch.Generator(device="cuda").manual_seed(15)
+    big, short = {}, {}
+    for k, dtype in (("g", torch.bfloat16), ("w", torch.float32), ("m", torch.uint8),
+                     ("v", torch.uint8)):
+        big[k] = torch.zeros(n, dtype=dtype, device="cuda")
+        if k in "gw":
+            big[k][a:] = torch.randn(tail, generator=gen, device="cuda").to(dtype)
+        short[k] = big[k][a:].clone()
+    for x, size in ((big, n), (short, tail)):
+        for k in ("m_scale", "v_scale"):
+            x[k] = torch.zeros(-(-size // RUN), device="cuda")
+    for x in (big, short):
+        lst = rdt.OptTensors(**{k: [t] for k, t in x.items()}, lr=1e-3)
+        rdt.tensors_adamw(lst, 1, B1, B2, EPS, seed=3)
+    assert torch.equal(big["w"][a:], short["w"]) and int(big["w"][:a].count_nonzero()) == 0
+    for k in "mv":
+        assert torch.equal(big[k + "_scale"][a // RUN:], short[k + "_scale"])
+        x, y = (decode(c, s, tail).double() for c, s in (
+            (big[k][a:], short[k + "_scale"]), (short[k], short[k + "_scale"])))
+        unit = short[k + "_scale"].double().repeat_interleave(RUN)[:tail]
+        assert ((x - y).abs() <= 2.0 ** -3 * 1.001 * torch.maximum(x.abs(), y.abs()) +
+                2.0 ** -9 * unit).all()
+    # the documented numbers there: the low 32 bits of the index, the key folded with the rest
+    key = mix((mix((mix(1) + 3) & 0xFFFFFFFF) + 0) & 0xFFFFFFFF) ^ 0x9E3779B1
+    at = torch.arange(1000, device="cuda")
+    x = mix(at ^ key)
+    g = big["g"][1 << 32:].float()
+    m = g * f32(1.0 - f32(B1))
+    root = torch.sqrt((g * f32(1.0 - f32(B2))) * g)
+    for k, value, half, low in (("m", m, x & 0xFFFF, False), ("v", root, x >> 16, True)):
+        codes, _ = encode(value, half, low)
+        assert torch.equal(big[k][1 << 32:], codes), k
+    want = float(big["g"][a:].double().square().sum())
+    assert abs(sq_sum([big["g"]]) - want) <= 1e-12 * want
+
+
 # --------------------------------------------------------------- squared sum
 def sq_sum(parts):
     lst = rdt.OptTensors(g=parts)
