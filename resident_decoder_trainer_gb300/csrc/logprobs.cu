@@ -300,11 +300,13 @@ struct Ring {
   static constexpr int stages = kThreads == 512 ? 2 : 3;
   static constexpr int bytes = unroll * stages * kThreads * 16;
 };
-// Parts of a thread's groups whose maxima are kept (8 for 256 threads: 16 would leave an SM a
+// A thread's first groups, whose maxima are all kept (8 for 256 threads: 16 would leave an SM a
 // CTA less).
-constexpr int segments_of(int threads) { return threads == 256 ? 8 : 16; }
-constexpr int kSample = 64;   // sets of threads whose maxima bound the row's alternatives
-constexpr int kKeys = 256;    // candidates that are ranked by counting
+constexpr int first_of(int threads) { return threads == 256 ? 8 : 16; }
+constexpr int kSample = 64;  // sets of threads whose maxima bound the row's alternatives
+// Later groups that reached the bound of their time, at most.
+constexpr int seen_of(int threads) { return threads == 256 ? 160 : 320; }
+constexpr int kKeys = 256;   // candidates that are ranked by counting
 
 template <int kThreads, bool kTop>
 struct Shared {
@@ -317,17 +319,19 @@ struct Shared<kThreads, true> {
   Sums part[kMaxSplit];
   unsigned long long parts[kThreads < 256 ? 1 : kMaxSplit][32];  // smaller CTAs share no row
   unsigned long long best[32], merged[32];
-  bf16 segment[segments_of(kThreads)][kThreads];  // rounded up
+  bf16 first[first_of(kThreads)][kThreads];  // maxima, rounded up
+  bf16 seen_max[seen_of(kThreads)];          // the same of the groups in seen_group
+  uint32_t seen_group[seen_of(kThreads)];                // group kThreads + thread
   float sample[kSample];
   float bound;
-  int items, keys;
+  int seen, items, keys;
 };
 // What lies in the ring once the loop is through.
 template <int kThreads>
 struct Lists {
   unsigned long long list[kThreads / 32][32];
   unsigned long long key[kKeys];
-  uint16_t item[segments_of(kThreads) * kThreads];
+  uint32_t item[first_of(kThreads) * kThreads + seen_of(kThreads)];  // group kThreads + thread
 };
 
 // The sums of kLanes (a power of 2) neighbouring lanes, in each of them.
@@ -343,6 +347,29 @@ __device__ __forceinline__ Sums join_lanes(Sums s, float c) {
     s.s1 += __shfl_xor_sync(kAll, s.s1, o);
   }
   return s;
+}
+
+// Notes the threads' maxima for the bound below.
+template <int kThreads>
+__device__ __forceinline__ void put_sample(float m, float* sample) {
+#pragma unroll
+  for (int o = 1; o < kThreads / kSample; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+  if (threadIdx.x % (kThreads / kSample) == 0) sample[threadIdx.x / (kThreads / kSample)] = m;
+}
+// The `top`-th largest of the samples: a lower bound of the `top`-th largest
+// logit so far, for each set holds one at least as large. Called by all
+// threads after a barrier; the bound is there after the next one.
+__device__ __forceinline__ void put_bound(const float* sample, int top, float* bound) {
+  if (threadIdx.x < kSample) {
+    const float x = sample[threadIdx.x];
+    int rank = 0;
+#pragma unroll 16
+    for (int j = 0; j < kSample; ++j) {
+      const float y = sample[j];
+      rank += y > x || (y == x && j < static_cast<int>(threadIdx.x));
+    }
+    if (rank == top - 1) *bound = x;
+  }
 }
 
 // The CTA's sums from its threads', in every thread: the maximum first, one
@@ -395,12 +422,17 @@ __device__ __noinline__ Sums sums_of_any(const Row<T>& row, int v, int v1, float
 // one token left has ln p = 0.
 //
 // The loads run Ring::stages - 1 groups ahead, each thread's into its own part of
-// `ring` (no barrier: a thread reads only what it copied). `segment`, where not
-// null, receives the maxima of segments_of() runs of `length` groups (-inf for
-// none, NaN not seen), rounded up to bf16; `raw` receives the largest of all.
+// `ring` (no barrier: a thread reads only what it copied). `raw` receives the
+// thread's maximum (-inf for none, NaN not seen).
+//
+// For alternatives the maxima of the first groups are kept; then, and at each
+// doubling of the groups, the row so far bounds its `top`-th largest logit, and
+// later groups are kept if they reach that bound: some 24 for 20 alternatives
+// and doubling of a row of random logits. All threads make `groups` turns.
 template <typename T, int kThreads, bool kTop>
-__device__ __forceinline__ Sums sums_of(const Row<T>& row, int v, int v1, float c, uint4* ring,
-                                        bf16 (*segment)[kThreads], int length, float& raw) {
+__device__ __forceinline__ Sums sums_of(const Row<T>& row, int v, int v1, int groups, float c,
+                                        uint4* ring, Shared<kThreads, kTop>& sh, int alternatives,
+                                        float& raw) {
   constexpr int kPer = Vec<T>::kPer;
   constexpr int kUnroll = Ring<kThreads, kTop>::unroll, kStages = Ring<kThreads, kTop>::stages;
   constexpr int kStep = kUnroll * kThreads;
@@ -413,11 +445,21 @@ __device__ __forceinline__ Sums sums_of(const Row<T>& row, int v, int v1, float 
   };
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) fetch(v + i * kStep, i);
-  float m = Vec<T>::kFloor, segment_m = -INFINITY;
-  int left = length, filled = 0;
+  float m = Vec<T>::kFloor, bound = INFINITY;
+  int renew = first_of(kThreads);
   uint64_t s0 = 0, s1 = 0;
   const uint64_t cc = pack2(c, c);
-  for (int stage = 0; v < v1; v += kStep) {
+  for (int group = 0, stage = 0; group < groups; ++group, v += kStep) {
+    if constexpr (kTop) {
+      if (group == renew) {
+        put_sample<kThreads>(raw, sh.sample);
+        __syncthreads();
+        put_bound(sh.sample, alternatives, &sh.bound);
+        __syncthreads();
+        bound = sh.bound;
+        renew *= 2;
+      }
+    }
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
     uint4 r[kUnroll];
 #pragma unroll
@@ -436,12 +478,15 @@ __device__ __forceinline__ Sums sums_of(const Row<T>& row, int v, int v1, float 
       s0 = mul2(ff, s0);
       m = top;
     }
-    if (segment) {
-      segment_m = fmaxf(segment_m, top);
-      if (--left == 0) {
-        segment[filled++][threadIdx.x] = __float2bfloat16_ru(segment_m);
-        segment_m = -INFINITY;
-        left = length;
+    if constexpr (kTop) {
+      if (group < first_of(kThreads)) {
+        sh.first[group][threadIdx.x] = __float2bfloat16_ru(top);
+      } else if (top >= bound && top > -INFINITY) {
+        const int at = atomicAdd(&sh.seen, 1);
+        if (at < seen_of(kThreads)) {
+          sh.seen_group[at] = static_cast<uint32_t>(group) * kThreads + threadIdx.x;
+          sh.seen_max[at] = __float2bfloat16_ru(top);
+        }
       }
     }
     const uint64_t mm = pack2(-m, -m);
@@ -459,12 +504,6 @@ __device__ __forceinline__ Sums sums_of(const Row<T>& row, int v, int v1, float 
       }
     }
   }
-  if (segment) {
-    for (; filled < segments_of(kThreads); ++filled) {
-      segment[filled][threadIdx.x] = __float2bfloat16_ru(segment_m);
-      segment_m = -INFINITY;
-    }
-  }
   asm volatile("cp.async.wait_all;" ::: "memory");
   const float2 a = unpack2(s0), b = unpack2(s1);
   const float sum = a.x + a.y;
@@ -472,18 +511,18 @@ __device__ __forceinline__ Sums sums_of(const Row<T>& row, int v, int v1, float 
   return Sums{m, sum, b.x + b.y};
 }
 
-// f(element, index) for the elements of the listed (segment, thread) pairs'
-// vectors (`length` each) whose maximum is at least `low`; they are spread
-// over the threads, kReread of each under way. With kWhole f is called by whole warps,
+// f(element, index) for the elements of the listed groups that are at least
+// `low` (all groups where item is null); the vectors are spread over the
+// threads, kReread of each under way. With kWhole f is called by whole warps,
 // with -inf where a lane has no such element.
-template <typename T, int kThreads, bool kWhole, typename F>
+template <typename T, int kThreads, int kUnroll, bool kWhole, typename F>
 __device__ __forceinline__ void for_each_candidate(const Row<T>& row, int v0, int v1,
-                                                   const uint16_t* item, int items, int length,
-                                                   float low, F f) {
+                                                   const uint32_t* item, int items, float low,
+                                                   F f) {
   constexpr int kPer = Vec<T>::kPer;
-  constexpr int kReread = kThreads == 128 ? 8 : 4;  // (more registers leave 256 threads a CTA less)
+  constexpr int kReread = 2;
   const int lane = threadIdx.x & 31;
-  const int each = length, pairs = items * each;
+  const int pairs = items * kUnroll;
   for (int q = threadIdx.x; q - lane < pairs; q += kReread * kThreads) {
     uint4 r[kReread];
     int at[kReread];
@@ -493,8 +532,8 @@ __device__ __forceinline__ void for_each_candidate(const Row<T>& row, int v0, in
       r[u] = Row<T>::none();
       at[u] = v0;
       if (pair < pairs) {
-        const int i = pair / each, n = pair - i * each, id = item[i];
-        at[u] = v0 + id % kThreads + (id / kThreads * each + n) * kThreads;
+        const int id = item ? static_cast<int>(item[pair / kUnroll]) : pair / kUnroll;
+        at[u] = v0 + id % kThreads + (id / kThreads * kUnroll + pair % kUnroll) * kThreads;
         if (at[u] < v1) r[u] = row.load(at[u]);
       }
     }
@@ -512,14 +551,14 @@ __device__ __forceinline__ void for_each_candidate(const Row<T>& row, int v0, in
 
 // The CTA's 32 largest elements among the candidates, to best[]: for any
 // number of them (ties, or few finite logits). list: scratch, 32 keys a warp.
-template <typename T, int kThreads>
-__device__ __noinline__ void select_any(const Row<T>& row, int v0, int v1, const uint16_t* item,
-                                        int items, int length, float low, int top,
+template <typename T, int kThreads, int kUnroll>
+__device__ __noinline__ void select_any(const Row<T>& row, int v0, int v1, const uint32_t* item,
+                                        int items, float low, int top,
                                         unsigned long long (*list)[32], unsigned long long* best) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint64_t mine = 0;
-  for_each_candidate<T, kThreads, true>(
-      row, v0, v1, item, items, length, low, [&](float x, int index) {
+  for_each_candidate<T, kThreads, kUnroll, true>(
+      row, v0, v1, item, items, low, [&](float x, int index) {
         const uint64_t k = order_key(x, index);
         const uint64_t least = __shfl_sync(kAll, mine, top - 1);
         unsigned who = __ballot_sync(kAll, k > least);
@@ -544,12 +583,10 @@ __device__ __noinline__ void select_any(const Row<T>& row, int v0, int v1, const
 // Each thread keeps the running maximum and sums of its vectors in registers;
 // warps, the CTA and the cluster join them in a fixed order.
 //
-// Alternatives cost the loop one maximum per group and thread. The `top`-th
-// largest of the maxima of kSample sets of threads is a lower bound of the
-// row's `top`-th largest logit (each set holds one at least as large), and of
-// random logits about 64 ln(64 / (64 - top)) are above it, 24 for 20. Only the
-// (segment, thread) pairs whose maximum reaches the bound are read again, and
-// what reaches it there is ranked by counting.
+// Alternatives: the groups that the loop kept and whose maximum reaches the
+// whole row's bound are read again (of random logits about 64 ln(64 / (64 -
+// top)) elements are above it, 24 for 20), and what reaches it there is ranked
+// by counting.
 template <typename T, int kThreads, bool kTop>
 __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a, int split) {
   constexpr int kWarps = kThreads / 32;
@@ -585,19 +622,14 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a,
 
   constexpr int kUnroll = Ring<kThreads, kTop>::unroll;
   const int groups = (v1 - v0 + kUnroll * kThreads - 1) / (kUnroll * kThreads);
-  const int length = max(1, (groups + segments_of(kThreads) - 1) / segments_of(kThreads));
-  bf16(*segment)[kThreads] = nullptr;
   float raw = -inf;
-  if constexpr (kTop) segment = sh.segment;
-  Sums s = sums_of<T, kThreads, kTop>(row, v0 + tid, v1, c, ring, segment, length, raw);
   if constexpr (kTop) {
-    float m = raw;
-#pragma unroll
-    for (int o = 1; o < kThreads / kSample; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
-    if (tid % (kThreads / kSample) == 0) sh.sample[tid / (kThreads / kSample)] = m;
-    if (tid == 0) sh.items = sh.keys = 0;
+    if (tid == 0) sh.seen = sh.items = sh.keys = 0;
     if (tid < 32) sh.best[tid] = sh.merged[tid] = 0;
+    __syncthreads();
   }
+  Sums s = sums_of<T, kThreads, kTop>(row, v0 + tid, v1, groups, c, ring, sh, a.top, raw);
+  if constexpr (kTop) put_sample<kThreads>(raw, sh.sample);
   Sums all = join_sums<kWarps>(s, c, sh.warp_sums);
   if (!Vec<T>::near(all.m, c) && all.m > -inf) {  // a maximum outside the fast range
     s = sums_of_any<T, kThreads>(row, v0 + tid, v1, c);
@@ -607,49 +639,49 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a,
 
   uint64_t list = 0;
   if constexpr (kTop) if (all.s0 == all.s0 && all.m > -inf) {  // the same in every thread
-    if (tid < kSample) {
-      const float x = sh.sample[tid];
-      int rank = 0;
-#pragma unroll 16
-      for (int j = 0; j < kSample; ++j) {
-        const float y = sh.sample[j];
-        rank += y > x || (y == x && j < tid);
-      }
-      if (rank == a.top - 1) sh.bound = x;
-    }
+    put_bound(sh.sample, a.top, &sh.bound);
     __syncthreads();
     const float low = sh.bound;  // -inf: fewer than `top` sets hold anything
     Lists<kThreads>& lists = *reinterpret_cast<Lists<kThreads>*>(ring);
     static_assert(sizeof(Lists<kThreads>) <= Ring<kThreads, kTop>::bytes, "fits the ring");
-    unsigned mask = 0;  // the thread's segments that reach the bound
-    if (raw >= low && raw > -inf) {
+    const int seen = sh.seen;
+    const bool lost = seen > seen_of(kThreads);  // rising rows: every group is looked at again
+    if (!lost) {
+      unsigned mask = 0;  // the thread's first groups that reach the bound
+      if (raw >= low && raw > -inf) {
 #pragma unroll
-      for (int i = 0; i < segments_of(kThreads); ++i) {
-        const float m = bf16_to_f(sh.segment[i][tid]);
-        mask |= static_cast<unsigned>(m >= low && m > -inf) << i;
+        for (int i = 0; i < first_of(kThreads); ++i) {
+          const float m = i < groups ? bf16_to_f(sh.first[i][tid]) : -inf;
+          mask |= static_cast<unsigned>(m >= low && m > -inf) << i;
+        }
       }
-    }
-    if (__any_sync(kAll, mask)) {  // one place for the warp's
-      const int n = __popc(mask);
-      int before = n;
+      if (__any_sync(kAll, mask)) {  // one place for the warp's
+        const int n = __popc(mask);
+        int before = n;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(kAll, before, o);
-        if (lane >= o) before += x;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(kAll, before, o);
+          if (lane >= o) before += x;
+        }
+        int at = 0;
+        if (lane == 31) at = atomicAdd(&sh.items, before);
+        at = __shfl_sync(kAll, at, 31) + before - n;
+        while (mask) {
+          const int i = __ffs(mask) - 1;
+          mask &= mask - 1;
+          lists.item[at++] = static_cast<uint32_t>(i * kThreads + tid);
+        }
       }
-      int at = 0;
-      if (lane == 31) at = atomicAdd(&sh.items, before);
-      at = __shfl_sync(kAll, at, 31) + before - n;
-      while (mask) {
-        const int i = __ffs(mask) - 1;
-        mask &= mask - 1;
-        lists.item[at++] = static_cast<uint16_t>(i * kThreads + tid);
-      }
+      for (int i = tid; i < seen; i += kThreads)
+        if (bf16_to_f(sh.seen_max[i]) >= low)
+          lists.item[atomicAdd(&sh.items, 1)] = sh.seen_group[i];
     }
     __syncthreads();
     // the order of items and keys varies, what is chosen among them does not
-    for_each_candidate<T, kThreads, false>(
-        row, v0, v1, lists.item, sh.items, length * kUnroll, low, [&](float x, int index) {
+    const uint32_t* item = lost ? nullptr : lists.item;
+    const int items = lost ? groups * kThreads : sh.items;
+    for_each_candidate<T, kThreads, kUnroll, false>(
+        row, v0, v1, item, items, low, [&](float x, int index) {
           const uint64_t k = order_key(x, index);
           if (k == 0) return;
           const int n = atomicAdd(&sh.keys, 1);
@@ -666,8 +698,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a,
         if (rank < a.top) sh.best[rank] = k;
       }
     } else {
-      select_any<T, kThreads>(row, v0, v1, lists.item, sh.items, length * kUnroll, low, a.top, lists.list,
-                              sh.best);
+      select_any<T, kThreads, kUnroll>(row, v0, v1, item, items, low, a.top, lists.list, sh.best);
     }
     __syncthreads();
     list = sh.best[lane];

@@ -183,6 +183,7 @@ def test_ties_go_to_the_lowest_id(vocab, dtype):
     z[3] = z[2].flip(0)                                     # falling
     z[4] = (torch.arange(vocab, device="cuda") % 7).to(dtype)
     z[5, vocab // 2:] = 1
+    check(z.repeat(200, 1)[:700], None, top=32)  # more rows than SMs: whole rows to a CTA
     out = check(z, None, top=32)
     first = torch.arange(32, dtype=torch.int32, device="cuda")
     assert torch.equal(out["top_ids"][0], first) and torch.equal(out["top_ids"][1], first)
