@@ -292,14 +292,11 @@ struct LogprobArgs {
 };
 
 constexpr int kMaxSplit = 8;  // CTAs that share a row (a cluster of the portable size)
-// A group: the vectors a thread works on at once. A thread holds `stages`
+// A group: the vectors a thread works on at once. A thread holds kStages
 // groups in shared memory, all but one of them under way.
-template <int kThreads, bool kTop>
-struct Ring {
-  static constexpr int unroll = 4;
-  static constexpr int stages = kThreads == 512 ? 2 : 3;
-  static constexpr int bytes = unroll * stages * kThreads * 16;
-};
+constexpr int kUnroll = 4;
+template <int kThreads, int kStages>
+constexpr int kRingBytes = kUnroll * kStages * kThreads * 16;
 // A thread's first groups, whose maxima are all kept (8 for 256 threads: 16 would leave an SM a
 // CTA less).
 constexpr int first_of(int threads) { return threads == 256 ? 8 : 16; }
@@ -421,7 +418,7 @@ __device__ __noinline__ Sums sums_of_any(const Row<T>& row, int v, int v1, float
 // what an empty set has. t is 0 and 2^t 1 at the maximum itself, so a row with
 // one token left has ln p = 0.
 //
-// The loads run Ring::stages - 1 groups ahead, each thread's into its own part of
+// The loads run kStages - 1 groups ahead, each thread's into its own part of
 // `ring` (no barrier: a thread reads only what it copied). `raw` receives the
 // thread's maximum (-inf for none, NaN not seen).
 //
@@ -429,12 +426,11 @@ __device__ __noinline__ Sums sums_of_any(const Row<T>& row, int v, int v1, float
 // doubling of the groups, the row so far bounds its `top`-th largest logit, and
 // later groups are kept if they reach that bound: some 24 for 20 alternatives
 // and doubling of a row of random logits. All threads make `groups` turns.
-template <typename T, int kThreads, bool kTop>
+template <typename T, int kThreads, int kStages, bool kTop>
 __device__ __forceinline__ Sums sums_of(const Row<T>& row, int v, int v1, int groups, float c,
                                         uint4* ring, Shared<kThreads, kTop>& sh, int alternatives,
                                         float& raw) {
   constexpr int kPer = Vec<T>::kPer;
-  constexpr int kUnroll = Ring<kThreads, kTop>::unroll, kStages = Ring<kThreads, kTop>::stages;
   constexpr int kStep = kUnroll * kThreads;
   ring += threadIdx.x;
   auto fetch = [&](int g, int stage) {
@@ -515,7 +511,7 @@ __device__ __forceinline__ Sums sums_of(const Row<T>& row, int v, int v1, int gr
 // `low` (all groups where item is null); the vectors are spread over the
 // threads, kReread of each under way. With kWhole f is called by whole warps,
 // with -inf where a lane has no such element.
-template <typename T, int kThreads, int kUnroll, bool kWhole, typename F>
+template <typename T, int kThreads, bool kWhole, typename F>
 __device__ __forceinline__ void for_each_candidate(const Row<T>& row, int v0, int v1,
                                                    const uint32_t* item, int items, float low,
                                                    F f) {
@@ -551,13 +547,13 @@ __device__ __forceinline__ void for_each_candidate(const Row<T>& row, int v0, in
 
 // The CTA's 32 largest elements among the candidates, to best[]: for any
 // number of them (ties, or few finite logits). list: scratch, 32 keys a warp.
-template <typename T, int kThreads, int kUnroll>
+template <typename T, int kThreads>
 __device__ __noinline__ void select_any(const Row<T>& row, int v0, int v1, const uint32_t* item,
                                         int items, float low, int top,
                                         unsigned long long (*list)[32], unsigned long long* best) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint64_t mine = 0;
-  for_each_candidate<T, kThreads, kUnroll, true>(
+  for_each_candidate<T, kThreads, true>(
       row, v0, v1, item, items, low, [&](float x, int index) {
         const uint64_t k = order_key(x, index);
         const uint64_t least = __shfl_sync(kAll, mine, top - 1);
@@ -587,10 +583,10 @@ __device__ __noinline__ void select_any(const Row<T>& row, int v0, int v1, const
 // whole row's bound are read again (of random logits about 64 ln(64 / (64 -
 // top)) elements are above it, 24 for 20), and what reaches it there is ranked
 // by counting.
-template <typename T, int kThreads, bool kTop>
+template <typename T, int kThreads, int kStages, bool kTop>
 __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a, int split) {
   constexpr int kWarps = kThreads / 32;
-  extern __shared__ uint4 ring[];  // Ring::bytes; after the loop, lists
+  extern __shared__ uint4 ring[];  // kRingBytes; after the loop, lists
   __shared__ Shared<kThreads, kTop> sh;
   const int row_i = split == 1 ? blockIdx.x : blockIdx.x / split;
   const int part = split == 1 ? 0 : blockIdx.x % split;
@@ -620,7 +616,6 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a,
   float target_z = 0.f;  // long before it is needed
   if (tid == 0 && part == 0 && a.logp && target < a.vocab) target_z = to_f(row.z[target]);
 
-  constexpr int kUnroll = Ring<kThreads, kTop>::unroll;
   const int groups = (v1 - v0 + kUnroll * kThreads - 1) / (kUnroll * kThreads);
   float raw = -inf;
   if constexpr (kTop) {
@@ -628,7 +623,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a,
     if (tid < 32) sh.best[tid] = sh.merged[tid] = 0;
     __syncthreads();
   }
-  Sums s = sums_of<T, kThreads, kTop>(row, v0 + tid, v1, groups, c, ring, sh, a.top, raw);
+  Sums s = sums_of<T, kThreads, kStages, kTop>(row, v0 + tid, v1, groups, c, ring, sh, a.top, raw);
   if constexpr (kTop) put_sample<kThreads>(raw, sh.sample);
   Sums all = join_sums<kWarps>(s, c, sh.warp_sums);
   if (!Vec<T>::near(all.m, c) && all.m > -inf) {  // a maximum outside the fast range
@@ -643,7 +638,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a,
     __syncthreads();
     const float low = sh.bound;  // -inf: fewer than `top` sets hold anything
     Lists<kThreads>& lists = *reinterpret_cast<Lists<kThreads>*>(ring);
-    static_assert(sizeof(Lists<kThreads>) <= Ring<kThreads, kTop>::bytes, "fits the ring");
+    static_assert(sizeof(Lists<kThreads>) <= kRingBytes<kThreads, kStages>, "fits the ring");
     const int seen = sh.seen;
     const bool lost = seen > seen_of(kThreads);  // rising rows: every group is looked at again
     if (!lost) {
@@ -680,7 +675,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a,
     // the order of items and keys varies, what is chosen among them does not
     const uint32_t* item = lost ? nullptr : lists.item;
     const int items = lost ? groups * kThreads : sh.items;
-    for_each_candidate<T, kThreads, kUnroll, false>(
+    for_each_candidate<T, kThreads, false>(
         row, v0, v1, item, items, low, [&](float x, int index) {
           const uint64_t k = order_key(x, index);
           if (k == 0) return;
@@ -698,7 +693,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a,
         if (rank < a.top) sh.best[rank] = k;
       }
     } else {
-      select_any<T, kThreads, kUnroll>(row, v0, v1, item, items, low, a.top, lists.list, sh.best);
+      select_any<T, kThreads>(row, v0, v1, item, items, low, a.top, lists.list, sh.best);
     }
     __syncthreads();
     list = sh.best[lane];
@@ -770,19 +765,19 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a,
   }
 }
 
-template <typename T, int kThreads, bool kTop>
+template <typename T, int kThreads, int kStages, bool kTop>
 cudaError_t launch_logprobs(const LogprobArgs& a, int split, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * split, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = s;
-  cfg.dynamicSmemBytes = Ring<kThreads, kTop>::bytes;
+  cfg.dynamicSmemBytes = kRingBytes<kThreads, kStages>;
   static std::atomic<uint64_t> allowed{0};  // devices where the kernel may use that much
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev > 63 || !(allowed.load() >> dev & 1)) {
-    e = cudaFuncSetAttribute(logprobs_kernel<T, kThreads, kTop>,
+    e = cudaFuncSetAttribute(logprobs_kernel<T, kThreads, kStages, kTop>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(cfg.dynamicSmemBytes));
     if (e != cudaSuccess) return e;
@@ -796,7 +791,7 @@ cudaError_t launch_logprobs(const LogprobArgs& a, int split, cudaStream_t s) {
   cfg.attrs = at;
   cfg.numAttrs = split > 1 ? 1 : 0;
   note_launch();
-  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, kThreads, kTop>, a, split);
+  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, kThreads, kStages, kTop>, a, split);
 }
 
 // Threads by the row's vectors (a thread should have a few), CTAs per row by
@@ -805,7 +800,7 @@ template <typename T>
 cudaError_t logprobs_of(const LogprobArgs& a, cudaStream_t s) {
   const int vectors = a.vocab / Vec<T>::kPer;
   if (vectors <= 1024)
-    return a.top ? launch_logprobs<T, 64, true>(a, 1, s) : launch_logprobs<T, 64, false>(a, 1, s);
+    return a.top ? launch_logprobs<T, 64, 3, true>(a, 1, s) : launch_logprobs<T, 64, 3, false>(a, 1, s);
   // At most a row an SM: a cluster a row, as long as each thread has four vectors (152 fp32
   // rows of 151,936, 20 alternatives: 27 us with 256 threads, 33 with 512, 39 with 128 and no
   // cluster; without alternatives 21 us with 512, 23 with 256).
@@ -813,15 +808,22 @@ cudaError_t logprobs_of(const LogprobArgs& a, cudaStream_t s) {
   if (a.rows <= sms) {
     int split = 1;
     while (split < kMaxSplit && a.rows * split <= sms && vectors >= 4 * 1024 * split) split *= 2;
-    return a.top ? launch_logprobs<T, 256, true>(a, split, s)
-                 : launch_logprobs<T, 512, false>(a, split, s);
+    return a.top ? launch_logprobs<T, 256, 3, true>(a, split, s)
+                 : launch_logprobs<T, 512, 2, false>(a, split, s);
   }
-  // Alternatives leave a CTA without loads under way for some 5 us a row; smaller and more
-  // CTAs hide more of it once there are rows for them (20 alternatives, 151,936 logits: 608
-  // fp32 rows 69 us with 128 threads, 88 with 256, but 304 rows 47 and 43; 4096 bf16 rows 229
-  // and 238, without alternatives 204 and 197).
-  if (a.top && a.rows > 2 * sms) return launch_logprobs<T, 128, true>(a, 1, s);
-  return a.top ? launch_logprobs<T, 256, true>(a, 1, s) : launch_logprobs<T, 256, false>(a, 1, s);
+  if (!a.top) return launch_logprobs<T, 256, 3, false>(a, 1, s);
+  // Alternatives leave a CTA without loads under way for some microseconds a row; smaller and
+  // more CTAs hide more of it once there are rows for them (20 alternatives, 151,936 logits: 608
+  // fp32 rows 66 us with 128 threads, 75 with 256, but 304 rows 47 and 39; 4096 bf16 rows 221 and
+  // 232, without alternatives 204 and 197).
+  if (a.rows <= 2 * sms) return launch_logprobs<T, 256, 3, true>(a, 1, s);
+  // Of 128 threads an SM holds 7 CTAs with three groups in shared memory and 9 with two. Up to 6
+  // rows an SM want the three (760 fp32 rows: 81 us, 86 with two), one wave of more the two (1024
+  // rows: 106, 113 with three; 1216 rows: 121 and 153), and several waves whichever leaves less of
+  // the last one empty (2048 rows: 226 and 205; 2432 rows: 234 and 252).
+  const int deep = (a.rows - 1) / sms + 1;  // rows an SM
+  const bool two = deep > 6 && (deep <= 9 || (deep + 8) / 9 * 9 <= (deep + 6) / 7 * 7);
+  return two ? launch_logprobs<T, 128, 2, true>(a, 1, s) : launch_logprobs<T, 128, 3, true>(a, 1, s);
 }
 
 cudaError_t logprobs(const LogprobArgs& a, int dtype, cudaStream_t s) {
