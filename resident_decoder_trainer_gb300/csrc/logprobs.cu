@@ -96,6 +96,15 @@ __device__ __forceinline__ uint32_t key_index(uint64_t key) {
 // kFloor: in a row whose maximum is `near`, a logit of kFloor or less has
 // probability 0; raised to it, masked tokens need no case of their own.
 template <typename T> struct Vec;
+// The maximum of n vectors of 16-bit elements, two elements to an instruction.
+template <typename H2, int n>
+__device__ __forceinline__ float max_of_halves(const uint4* r) {
+  const H2* h = reinterpret_cast<const H2*>(r);
+  H2 m = h[0];
+#pragma unroll
+  for (int i = 1; i < 4 * n; ++i) m = __hmax2(m, h[i]);
+  return fmaxf(__low2float(m), __high2float(m));
+}
 template <> struct Vec<float> {
   static constexpr float kFloor = -0x1p100f;
   // For every logit_scale; c (z - m) stays finite.
@@ -106,9 +115,14 @@ template <> struct Vec<float> {
     x[0] = __uint_as_float(r.x); x[1] = __uint_as_float(r.y);
     x[2] = __uint_as_float(r.z); x[3] = __uint_as_float(r.w);
   }
-  static __device__ __forceinline__ float max(const uint4& r) {
-    return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)),
-                 fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+  template <int n = 1>
+  static __device__ __forceinline__ float max(const uint4* r) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < n; ++i)
+      m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(r[i].x), __uint_as_float(r[i].y)),
+                         fmaxf(__uint_as_float(r[i].z), __uint_as_float(r[i].w))));
+    return m;
   }
   // The elements, raised to kFloor (NaN stays).
   static __device__ __forceinline__ void raised(const uint4& r, float* x) {
@@ -126,10 +140,9 @@ template <> struct Vec<bf16> {
     x[0] = bf16lo(r.x); x[1] = bf16hi(r.x); x[2] = bf16lo(r.y); x[3] = bf16hi(r.y);
     x[4] = bf16lo(r.z); x[5] = bf16hi(r.z); x[6] = bf16lo(r.w); x[7] = bf16hi(r.w);
   }
-  static __device__ __forceinline__ float max(const uint4& r) {
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&r);
-    const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
-    return fmaxf(__low2float(m), __high2float(m));
+  template <int n = 1>
+  static __device__ __forceinline__ float max(const uint4* r) {
+    return max_of_halves<__nv_bfloat162, n>(r);
   }
   // kFloor is a bf16 value: two elements are raised at once.
   static __device__ __forceinline__ void raised(const uint4& r, float* x) {
@@ -155,10 +168,9 @@ template <> struct Vec<__half> {
       x[2 * i + 1] = f.y;
     }
   }
-  static __device__ __forceinline__ float max(const uint4& r) {
-    const __half2* h = reinterpret_cast<const __half2*>(&r);
-    const __half2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
-    return fmaxf(__low2float(m), __high2float(m));
+  template <int n = 1>
+  static __device__ __forceinline__ float max(const uint4* r) {
+    return max_of_halves<__half2, n>(r);
   }
   static __device__ __forceinline__ void raised(const uint4& r, float* x) {
     const __half2 low = __float2half2_rn(kFloor);
@@ -179,30 +191,27 @@ struct Row {
   const uint4* v0; // the vector that holds it
   int head, vocab;
   int vectors;
+  int whole0, whole1;  // the vectors that lie in the row as a whole: [whole0, whole1)
   __device__ __forceinline__ Row(const T* row, int n) : z(row), vocab(n) {
     const uintptr_t at = reinterpret_cast<uintptr_t>(row);
     v0 = reinterpret_cast<const uint4*>(at & ~static_cast<uintptr_t>(15));
     head = static_cast<int>((at & 15) / sizeof(T));
     vectors = static_cast<int>((static_cast<int64_t>(head) + n + Vec<T>::kPer - 1) / Vec<T>::kPer);
+    whole0 = head > 0;
+    whole1 = (head + n) / Vec<T>::kPer;
   }
   __device__ __forceinline__ int first_of(int v) const { return v * Vec<T>::kPer - head; }
-  __device__ __forceinline__ bool whole(int v) const {
-    const int j = first_of(v);
-    return j >= 0 && j <= vocab - Vec<T>::kPer;
-  }
+  __device__ __forceinline__ bool whole(int v) const { return v >= whole0 && v < whole1; }
   // v in [0, vectors)
   __device__ __forceinline__ uint4 load(int v) const {
     return whole(v) ? __ldg(v0 + v) : load_part(first_of(v));
   }
-  // Starts to copy vector v to shared memory; the thread that called finds it there after a
-  // wait for its copies.
+  // Starts to copy whole vector v to shared memory; the thread that called finds it there
+  // after a wait for its copies.
   __device__ __forceinline__ void fetch(int v, uint4* to) const {
-    if (whole(v))
-      asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(smem_u32(to)),
-                   "l"(v0 + v)
-                   : "memory");
-    else
-      *to = load_part(first_of(v));
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(smem_u32(to)),
+                 "l"(v0 + v)
+                 : "memory");
   }
   __device__ __noinline__ uint4 load_part(int j) const {
     uint32_t w[4];
@@ -395,7 +404,7 @@ __device__ __noinline__ Sums sums_of_any(const Row<T>& row, int v, int v1, float
       r[u] = v + u * kThreads < v1 ? row.load(v + u * kThreads) : Row<T>::none();
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const float m = Vec<T>::max(r[u]);
+      const float m = Vec<T>::max(&r[u]);
       if (m > s.m) rebase(s, m, c);
       const float base = base_of(s.m);
       float x[kPer];
@@ -433,10 +442,23 @@ __device__ __forceinline__ Sums sums_of(const Row<T>& row, int v, int v1, int gr
   constexpr int kPer = Vec<T>::kPer;
   constexpr int kStep = kUnroll * kThreads;
   ring += threadIdx.x;
+  const int whole1 = min(v1, row.whole1);
   auto fetch = [&](int g, int stage) {
+    uint4* to = ring + stage * kUnroll * kThreads;
+    if (g >= row.whole0 && g + (kUnroll - 1) * kThreads < whole1) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (g + u * kThreads < v1) row.fetch(g + u * kThreads, ring + (stage * kUnroll + u) * kThreads);
+      for (int u = 0; u < kUnroll; ++u) row.fetch(g + u * kThreads, to + u * kThreads);
+    } else {
+#pragma unroll 1
+      for (int u = 0; u < kUnroll; ++u) {
+        const int at = g + u * kThreads;
+        if (at >= v1) break;
+        if (row.whole(at))
+          row.fetch(at, to + u * kThreads);
+        else
+          to[u * kThreads] = row.load_part(row.first_of(at));
+      }
+    }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
@@ -458,14 +480,17 @@ __device__ __forceinline__ Sums sums_of(const Row<T>& row, int v, int v1, int gr
     }
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
     uint4 r[kUnroll];
+    if (v + (kUnroll - 1) * kThreads < v1) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      r[u] = v + u * kThreads < v1 ? ring[(stage * kUnroll + u) * kThreads] : Row<T>::none();
+      for (int u = 0; u < kUnroll; ++u) r[u] = ring[(stage * kUnroll + u) * kThreads];
+    } else {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        r[u] = v + u * kThreads < v1 ? ring[(stage * kUnroll + u) * kThreads] : Row<T>::none();
+    }
     fetch(v + (kStages - 1) * kStep, stage == 0 ? kStages - 1 : stage - 1);
     stage = stage == kStages - 1 ? 0 : stage + 1;
-    float top = Vec<T>::max(r[0]);
-#pragma unroll
-    for (int u = 1; u < kUnroll; ++u) top = fmaxf(top, Vec<T>::max(r[u]));
+    const float top = Vec<T>::template max<kUnroll>(r);
     raw = fmaxf(raw, top);
     if (top > m) {
       const float t = keep_finite((m - top) * c), f = exp2_fast(t);
@@ -535,7 +560,7 @@ __device__ __forceinline__ void for_each_candidate(const Row<T>& row, int v0, in
     }
 #pragma unroll
     for (int u = 0; u < kReread; ++u) {
-      const bool some = Vec<T>::max(r[u]) >= low;
+      const bool some = Vec<T>::max(&r[u]) >= low;
       if (kWhole ? !__any_sync(kAll, some) : !some) continue;
       float x[kPer];
       Vec<T>::unpack(r[u], x);
