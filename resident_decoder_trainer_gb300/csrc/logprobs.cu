@@ -1,6 +1,11 @@
 // Token log probabilities with entropy, log-sum-exp and top alternatives from
 // logits, their gradient, and the scoring head that calls them
 // (rdt_token_logprobs, rdt_token_logprobs_backward, rdt_head_logprobs).
+//
+// Bound by DRAM where rows are many: the logits are read once, in the gradient
+// written once. Measured, of the copy bandwidth: 4096 bf16 rows of 151,936
+// 193 us (0.95), 1024 fp32 rows with 20 alternatives 101 us (0.90), gradient of
+// 4096 bf16 rows 369 us (0.99). One row is bound by latency: 10 us.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -422,10 +427,10 @@ __device__ __noinline__ Sums sums_of_any(const Row<T>& row, int v, int v1, float
 }
 
 // The same for values whose maximum (over the CTA) is `near`, without special
-// values but NaN and with two elements to an instruction. A
-// thread with nothing above kFloor returns m = kFloor, with nothing but -inf
-// what an empty set has. t is 0 and 2^t 1 at the maximum itself, so a row with
-// one token left has ln p = 0.
+// values but NaN and with two elements to an instruction (256 us for 4096 bf16
+// rows with one, at 0.7 of the issue slots). A thread with nothing above
+// kFloor returns m = kFloor, with nothing but -inf what an empty set has. t is
+// 0 and 2^t 1 at the maximum itself, so a row with one token left has ln p = 0.
 //
 // The loads run kStages - 1 groups ahead, each thread's into its own part of
 // `ring` (no barrier: a thread reads only what it copied). `raw` receives the
@@ -999,6 +1004,7 @@ rdt_status refuse(const char* msg) {
 }
 rdt_status launched(cudaError_t e) {
   if (e == cudaSuccess) return RDT_OK;
+  cudaGetLastError();  // not left for the next call to find
   set_last_error(cudaGetErrorString(e));
   return RDT_ECUDA;
 }
