@@ -303,6 +303,7 @@ struct LogprobArgs {
   int top;
   int32_t* top_ids;
   float* top_logp;
+  bool early;
 };
 
 constexpr int kMaxSplit = 8;  // CTAs that share a row (a cluster of the portable size)
@@ -426,13 +427,42 @@ __device__ __noinline__ Sums sums_of_any(const Row<T>& row, int v, int v1, float
   return s;
 }
 
+// Starts the copies of a thread's group at vector g, below v1, to its part of a
+// ring's stage.
+template <typename T, int kThreads>
+__device__ __forceinline__ void fetch_group(const Row<T>& row, int g, int v1, uint4* to) {
+  if (g >= row.whole0 && g + (kUnroll - 1) * kThreads < min(v1, row.whole1)) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) row.fetch(g + u * kThreads, to + u * kThreads);
+  } else {
+#pragma unroll 1
+    for (int u = 0; u < kUnroll; ++u) {
+      const int at = g + u * kThreads;
+      if (at >= v1) break;
+      if (row.whole(at))
+        row.fetch(at, to + u * kThreads);
+      else
+        to[u * kThreads] = row.load_part(row.first_of(at));
+    }
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// The first groups, before sums_of.
+template <typename T, int kThreads, int kStages>
+__device__ __forceinline__ void fetch_first(const Row<T>& row, int v, int v1, uint4* ring) {
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i)
+    fetch_group<T, kThreads>(row, v + i * kUnroll * kThreads, v1,
+                             ring + i * kUnroll * kThreads + threadIdx.x);
+}
+
 // The same for values whose maximum (over the CTA) is `near`, without special
 // values but NaN and with two elements to an instruction (256 us for 4096 bf16
 // rows with one, at 0.7 of the issue slots). A thread with nothing above
 // kFloor returns m = kFloor, with nothing but -inf what an empty set has. t is
 // 0 and 2^t 1 at the maximum itself, so a row with one token left has ln p = 0.
 //
-// The loads run kStages - 1 groups ahead, each thread's into its own part of
+// The loads run kStages - 1 groups ahead (fetch_first), each thread's into its own part of
 // `ring` (no barrier: a thread reads only what it copied). `raw` receives the
 // thread's maximum (-inf for none, NaN not seen).
 //
@@ -447,27 +477,6 @@ __device__ __forceinline__ Sums sums_of(const Row<T>& row, int v, int v1, int gr
   constexpr int kPer = Vec<T>::kPer;
   constexpr int kStep = kUnroll * kThreads;
   ring += threadIdx.x;
-  const int whole1 = min(v1, row.whole1);
-  auto fetch = [&](int g, int stage) {
-    uint4* to = ring + stage * kUnroll * kThreads;
-    if (g >= row.whole0 && g + (kUnroll - 1) * kThreads < whole1) {
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) row.fetch(g + u * kThreads, to + u * kThreads);
-    } else {
-#pragma unroll 1
-      for (int u = 0; u < kUnroll; ++u) {
-        const int at = g + u * kThreads;
-        if (at >= v1) break;
-        if (row.whole(at))
-          row.fetch(at, to + u * kThreads);
-        else
-          to[u * kThreads] = row.load_part(row.first_of(at));
-      }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) fetch(v + i * kStep, i);
   float m = Vec<T>::kFloor, bound = INFINITY;
   int renew = first_of(kThreads);
   uint64_t s0 = 0, s1 = 0;
@@ -493,7 +502,8 @@ __device__ __forceinline__ Sums sums_of(const Row<T>& row, int v, int v1, int gr
       for (int u = 0; u < kUnroll; ++u)
         r[u] = v + u * kThreads < v1 ? ring[(stage * kUnroll + u) * kThreads] : Row<T>::none();
     }
-    fetch(v + (kStages - 1) * kStep, stage == 0 ? kStages - 1 : stage - 1);
+    fetch_group<T, kThreads>(row, v + (kStages - 1) * kStep, v1,
+                             ring + (stage == 0 ? kStages - 1 : stage - 1) * kStep);
     stage = stage == kStages - 1 ? 0 : stage + 1;
     const float top = Vec<T>::template max<kUnroll>(r);
     raw = fmaxf(raw, top);
@@ -621,8 +631,13 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a,
   const int row_i = split == 1 ? blockIdx.x : blockIdx.x / split;
   const int part = split == 1 ? 0 : blockIdx.x % split;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int target = a.targets ? a.targets[row_i] : 0;
   const float inf = INFINITY;
+  const Row<T> row(static_cast<const T*>(a.logits) + static_cast<int64_t>(row_i) * a.ld, a.vocab);
+  const int v0 = static_cast<int>(static_cast<int64_t>(row.vectors) * part / split);
+  const int v1 = static_cast<int>(static_cast<int64_t>(row.vectors) * (part + 1) / split);
+  // few rows: their loads start before it is known whether they are scored
+  if (a.early) fetch_first<T, kThreads, kStages>(row, v0 + tid, v1, ring);
+  const int target = a.targets ? a.targets[row_i] : 0;
   if (target < 0) {  // not scored (the same in every CTA of the cluster)
     if (part == 0 && tid == 0) {
       if (a.logp) a.logp[row_i] = 0.f;
@@ -634,14 +649,13 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a,
       a.top_ids[static_cast<int64_t>(row_i) * a.top + tid] = -1;
       a.top_logp[static_cast<int64_t>(row_i) * a.top + tid] = 0.f;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     return;
   }
+  if (!a.early) fetch_first<T, kThreads, kStages>(row, v0 + tid, v1, ring);
   // shared memory of another CTA may be written once that CTA runs: every CTA says so here and
   // waits for the others only before its stores
   if (kThreads >= 256 && split > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
-  const Row<T> row(static_cast<const T*>(a.logits) + static_cast<int64_t>(row_i) * a.ld, a.vocab);
-  const int v0 = static_cast<int>(static_cast<int64_t>(row.vectors) * part / split);
-  const int v1 = static_cast<int>(static_cast<int64_t>(row.vectors) * (part + 1) / split);
   const float c = a.scale * kLog2e;
   float target_z = 0.f;  // long before it is needed
   if (tid == 0 && part == 0 && a.logp && target < a.vocab) target_z = to_f(row.z[target]);
@@ -827,7 +841,7 @@ cudaError_t launch_logprobs(const LogprobArgs& a, int split, cudaStream_t s) {
 // Threads by the row's vectors (a thread should have a few), CTAs per row by
 // how many rows there are to fill the GPU with.
 template <typename T>
-cudaError_t logprobs_of(const LogprobArgs& a, cudaStream_t s) {
+cudaError_t logprobs_of(LogprobArgs a, cudaStream_t s) {
   const int vectors = a.vocab / Vec<T>::kPer;
   if (vectors <= 1024)
     return a.top ? launch_logprobs<T, 64, 3, true>(a, 1, s) : launch_logprobs<T, 64, 3, false>(a, 1, s);
@@ -838,7 +852,8 @@ cudaError_t logprobs_of(const LogprobArgs& a, cudaStream_t s) {
   if (a.rows <= sms) {
     int split = 1;
     while (split < kMaxSplit && a.rows * split <= sms && vectors >= 4 * 1024 * split) split *= 2;
-    return a.top ? launch_logprobs<T, 256, 3, true>(a, split, s)
+    a.early = true;
+    return a.top ? launch_logprobs<T, 256, 4, true>(a, split, s)
                  : launch_logprobs<T, 512, 2, false>(a, split, s);
   }
   if (!a.top) return launch_logprobs<T, 256, 3, false>(a, 1, s);
@@ -1086,7 +1101,7 @@ rdt_status rdt_token_logprobs(const void* logits, int32_t dtype, int64_t ld, int
     return refuse("targets and outputs must be 4-byte aligned (stats 8-byte)");
   LogprobArgs a{logits,  ld,   rows,    vocab, logit_scale,
                 targets, logp, entropy, lse,   reinterpret_cast<float2*>(stats),
-                top,     top_ids, top_logp};
+                top,     top_ids, top_logp, false};
   return launched(rdt::logprobs(a, dtype, static_cast<cudaStream_t>(stream)));
 }
 
