@@ -420,8 +420,8 @@ rdt_status rdt_embedding_backward(const int32_t* ids, int32_t tokens, const floa
  * Each output may be null (logp needs targets; top_ids and top_logp go
  * together, with top >= 1); at least one is given.
  *  - targets int32 [rows], or null: no logp, every row is computed. A row with
- *    targets[t] < 0 is not scored and its logits are not read: its outputs
- *    are 0 and its ids -1. targets[t] >= vocab gives logp NaN.
+ *    targets[t] < 0 is not scored, whatever its logits (where rows are many
+ *    they are not even read): its outputs are 0 and its ids -1. targets[t] >= vocab gives logp NaN.
  *  - A logit of -inf is a masked token: p = 0, never an alternative; a masked
  *    target has logp -inf. Where fewer than `top` tokens are left, the rest
  *    has id -1 and ln p -inf. A row with every token masked has lse, logp,

@@ -292,6 +292,20 @@ __device__ __forceinline__ void st_cluster_u64(uint32_t at, uint64_t x) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(x) : "memory");
 }
 
+// Each kernel of this file may be launched while the one before it in the
+// stream still runs, and waits here for its end before it touches memory: of
+// two calls in a row the second's launch is hidden (programmatic launch; after
+// a kernel that does not take part the launch is an ordinary one).
+__device__ __forceinline__ void after_previous_kernel() {
+  asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+}
+inline cudaLaunchAttribute overlapping_launch(bool yes = true) {
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = yes;
+  return at;
+}
+
 struct LogprobArgs {
   const void* logits;
   int64_t ld;
@@ -628,6 +642,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a,
   constexpr int kWarps = kThreads / 32;
   extern __shared__ uint4 ring[];  // kRingBytes; after the loop, lists
   __shared__ Shared<kThreads, kTop> sh;
+  after_previous_kernel();
   const int row_i = split == 1 ? blockIdx.x : blockIdx.x / split;
   const int part = split == 1 ? 0 : blockIdx.x % split;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -827,13 +842,18 @@ cudaError_t launch_logprobs(const LogprobArgs& a, int split, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev < 64) allowed.fetch_or(uint64_t(1) << dev);
   }
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = static_cast<unsigned>(split);
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2];
+  // CTAs that wait already sit where there was room, some SMs full and some not; long rows in
+  // one or two waves lose by that (1024 fp32 rows of 151,936: 105 us for 101) what small calls
+  // and many waves win (2 us).
+  const int64_t bytes = static_cast<int64_t>(a.rows) * a.vocab * sizeof(T);
+  at[0] = overlapping_launch(bytes <= (64 << 20) || a.rows >= 24 * num_sms());
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = static_cast<unsigned>(split);
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = split > 1 ? 1 : 0;
+  cfg.numAttrs = split > 1 ? 2 : 1;
   note_launch();
   return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, kThreads, kStages, kTop>, a, split);
 }
@@ -937,6 +957,7 @@ __device__ __forceinline__ void store_piece(T* p, int j, int vocab, bool inside,
 // another phase there loads them one by one.
 template <typename T, typename O>
 __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const GradArgs a) {
+  after_previous_kernel();
   const int row = blockIdx.x / a.pieces, part = blockIdx.x % a.pieces;
   const T* z = static_cast<const T*>(a.logits) + static_cast<int64_t>(row) * a.ld;
   O* out = static_cast<O*>(a.out) + static_cast<int64_t>(row) * a.ld_out;
@@ -988,7 +1009,7 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const GradA
 }
 
 template <typename T>
-void launch_grad(GradArgs a, int d_dtype, cudaStream_t s) {
+cudaError_t launch_grad(GradArgs a, int d_dtype, cudaStream_t s) {
   const int pieces = (a.vocab + kGradPer - 1) / kGradPer;
   a.pieces = (pieces + 2 * kGradThreads - 1) / (2 * kGradThreads);  // two pieces a thread
   // ... while there are few rows, else four CTAs a row: its stats and gradients are read by
@@ -999,13 +1020,17 @@ void launch_grad(GradArgs a, int d_dtype, cudaStream_t s) {
     a.pieces = static_cast<int>(std::max<int64_t>(
         std::min<int64_t>(a.pieces, 4), enough / a.rows));
   if (static_cast<int64_t>(a.rows) * a.pieces > INT32_MAX) a.pieces = 1;
-  const unsigned grid = static_cast<unsigned>(a.rows) * a.pieces;
-  if (d_dtype == RDT_F32)
-    logprobs_grad_kernel<T, float><<<grid, kGradThreads, 0, s>>>(a);
-  else if (d_dtype == RDT_BF16)
-    logprobs_grad_kernel<T, bf16><<<grid, kGradThreads, 0, s>>>(a);
-  else
-    logprobs_grad_kernel<T, __half><<<grid, kGradThreads, 0, s>>>(a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * a.pieces, 1, 1);
+  cfg.blockDim = dim3(kGradThreads, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute at = overlapping_launch();
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  note_launch();
+  return d_dtype == RDT_F32    ? cudaLaunchKernelEx(&cfg, logprobs_grad_kernel<T, float>, a)
+         : d_dtype == RDT_BF16 ? cudaLaunchKernelEx(&cfg, logprobs_grad_kernel<T, bf16>, a)
+                               : cudaLaunchKernelEx(&cfg, logprobs_grad_kernel<T, __half>, a);
 }
 
 constexpr int kMaxVocab = 1 << 30;  // indexes of a row's elements stay inside 32 bits
@@ -1135,14 +1160,9 @@ rdt_status rdt_token_logprobs_backward(const void* logits, int32_t dtype, int64_
              reinterpret_cast<const float2*>(stats),
              entropy, d_logp, d_entropy, d_lse, d_logits,    ld_d, 1};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  note_launch();
-  if (dtype == RDT_F32)
-    launch_grad<float>(a, d_dtype, s);
-  else if (dtype == RDT_BF16)
-    launch_grad<bf16>(a, d_dtype, s);
-  else
-    launch_grad<__half>(a, d_dtype, s);
-  return launched(cudaGetLastError());
+  return launched(dtype == RDT_F32    ? launch_grad<float>(a, d_dtype, s)
+                  : dtype == RDT_BF16 ? launch_grad<bf16>(a, d_dtype, s)
+                                      : launch_grad<__half>(a, d_dtype, s));
 }
 
 size_t rdt_head_logprobs_workspace_bytes(const rdt_config* cfg, int32_t tokens) {

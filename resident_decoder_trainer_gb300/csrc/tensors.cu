@@ -89,17 +89,20 @@ __device__ __forceinline__ void next_tile(const Table<kMax>& tab, int tiles, int
   if (w.tile >= w.end && w.tile < tiles) find_owner(tab, w);
 }
 
-// The launches of one call. They touch no common memory but the final sum's
-// partials, so a later one may start as soon as the one before has all its
-// CTAs running (launches_may_follow) and only has to end after it
-// (end_after_previous, in one thread; the first launch of a call has no
-// previous one to wait for and returns at once). What follows the call in the
-// stream waits for its last launch, and so for all.
-__device__ __forceinline__ void launches_may_follow() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
+// Launches overlap (programmatic launch: one may start when all CTAs of the
+// one before it have said launches_may_follow). The first of a call waits for
+// the end of what is before it in the stream, and only then lets the next one
+// come: two calls in a row hide the second's launch. The later launches of a
+// call touch no memory in common with the first but the partial sums' array,
+// each its own part; they start at once and end after the one before
+// (end_after_previous, in one thread), so that the end of a call's last launch
+// is the end of all.
 __device__ __forceinline__ void wait_for_previous() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void launches_may_follow(bool first) {
+  if (first) wait_for_previous();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 __device__ __forceinline__ void end_after_previous() {
   if (blockIdx.x == 0 && threadIdx.x == 0) wait_for_previous();
@@ -274,9 +277,9 @@ template <bool kBf16>
 constexpr int kSqTiles = kSqLoads<kBf16> * (kBf16 ? 8 : 4) * kThreads / kTile;
 template <bool kBf16, int kMax>
 __global__ void __launch_bounds__(kThreads) tensors_sq_sum_kernel(
-    const __grid_constant__ Table<kMax> tab, int tiles, float one,
+    const __grid_constant__ Table<kMax> tab, int tiles, bool first, float one,
     double* __restrict__ partials) {
-  launches_may_follow();
+  launches_may_follow(first);
   __shared__ double red[kThreads / 32];
   using G = typename std::conditional<kBf16, bf16, float>::type;
   constexpr int kPer = 16 / sizeof(G), kStep = kPer * kThreads;  // elements of a load
@@ -365,7 +368,7 @@ __global__ void __launch_bounds__(kThreads) tensors_sq_sum_kernel(
 
 __global__ void __launch_bounds__(kThreads) tensors_sq_final_kernel(
     const double* __restrict__ partials, int n, double* __restrict__ out) {
-  wait_for_previous();
+  launches_may_follow(true);
   __shared__ double red[kThreads / 32];
   double s = 0.0;
   for (int i = threadIdx.x; i < n; i += kThreads) s += partials[i];
@@ -632,8 +635,8 @@ __device__ __forceinline__ void adamw_run(const Tensor& t, int64_t first, const 
 constexpr int kChunk = 2;  // tiles of a CTA's step of tensors_adamw_kernel
 template <int kBits, bool kBf16, bool kRandom, int kMax>
 __global__ void __launch_bounds__(kThreads) tensors_adamw_kernel(
-    const __grid_constant__ Table<kMax> tab, int tiles, const AdamArgs p) {
-  launches_may_follow();
+    const __grid_constant__ Table<kMax> tab, int tiles, bool first, const AdamArgs p) {
+  launches_may_follow(first);
   if (p.skip && *p.skip) {
     end_after_previous();
     return;
@@ -766,9 +769,8 @@ int ctas(int tiles, int chunk, int per_sm, int share = INT32_MAX) {
 
 constexpr int kMaxPartials = 2048;  // of one launch
 
-// `follows`: not the call's first launch.
 template <typename K, typename... A>
-cudaError_t launch(K kernel, int grid, size_t smem, cudaStream_t s, bool follows, A... args) {
+cudaError_t launch(K kernel, int grid, size_t smem, cudaStream_t s, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
@@ -778,7 +780,7 @@ cudaError_t launch(K kernel, int grid, size_t smem, cudaStream_t s, bool follows
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = follows ? 1 : 0;
+  cfg.numAttrs = 1;
   note_launch();
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
@@ -791,14 +793,14 @@ cudaError_t sq_sum_launches(const rdt_opt_tensor* list, int count, bool half, do
     if (*used + blocks > room) return cudaErrorInvalidValue;
     auto kernel = half ? tensors_sq_sum_kernel<true, kMax> : tensors_sq_sum_kernel<false, kMax>;
     double* to = parts + *used;
-    const bool follows = *used > 0;
+    const bool first = *used == 0;
     *used += blocks;
-    return launch(kernel, blocks, 0, s, follows, tab, tiles, 1.f, to);
+    return launch(kernel, blocks, 0, s, tab, tiles, first, 1.f, to);
   });
 }
 
 template <int kBits, bool kBf16, bool kRandom, int kMax>
-cudaError_t launch_adamw(const Table<kMax>& tab, int tiles, const AdamArgs& a, bool follows,
+cudaError_t launch_adamw(const Table<kMax>& tab, int tiles, const AdamArgs& a, bool first,
                          cudaStream_t s) {
   constexpr int kBytes = kBits == 8 ? 2 * Stage<kBf16>::kBytes : 0;
   auto kernel = tensors_adamw_kernel<kBits, kBf16, kRandom, kMax>;
@@ -811,17 +813,17 @@ cudaError_t launch_adamw(const Table<kMax>& tab, int tiles, const AdamArgs& a, b
     if (e != cudaSuccess) return e;
     if (dev < 64) allowed.fetch_or(uint64_t(1) << dev);
   }
-  return launch(kernel, ctas(tiles, kChunk, kBits == 32 ? 8 : 4, 6), kBytes, s, follows, tab, tiles,
+  return launch(kernel, ctas(tiles, kChunk, kBits == 32 ? 8 : 4, 6), kBytes, s, tab, tiles, first,
                 a);
 }
 
 template <int kMax>
 cudaError_t adamw_launches(const rdt_opt_tensor* list, int count, bool half, int bits, bool random,
                            const AdamArgs& a, cudaStream_t s) {
-  bool follows = false;
+  bool first = true;
   return each_launch<kMax>(list, count, [&](const Table<kMax>& tab, int tiles) {
-    const bool f = follows;
-    follows = true;
+    const bool f = first;
+    first = false;
     if (bits == 32)
       return half ? launch_adamw<32, true, false>(tab, tiles, a, f, s)
                   : launch_adamw<32, false, false>(tab, tiles, a, f, s);
@@ -865,8 +867,7 @@ rdt_status rdt_tensors_sq_sum(const rdt_opt_tensor* tensors, int32_t count, int3
           ? sq_sum_launches<kFewTensors>(tensors, count, half, parts, room, &used, s)
           : sq_sum_launches<kMaxTensors>(tensors, count, half, parts, room, &used, s);
   if (e != cudaSuccess) return launched(e);
-  return launched(launch(tensors_sq_final_kernel, 1, 0, s, used > 0, parts,
-                         static_cast<int>(used), sumsq));
+  return launched(launch(tensors_sq_final_kernel, 1, 0, s, parts, static_cast<int>(used), sumsq));
 }
 
 rdt_status rdt_tensors_adamw(const rdt_opt_tensor* tensors, int32_t count, int32_t g_dtype,
