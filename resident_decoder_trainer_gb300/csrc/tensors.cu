@@ -4,8 +4,8 @@
 // make one launch (one per kMaxTensors tensors).
 //
 // Both are bound by DRAM: each value is read and written once. Measured, of the
-// copy bandwidth: squared sum of 490 M fp32 gradients 277 us (1.04), AdamW with
-// 32-bit states of a 101 M block 440 us (1.01), with 8-bit states of 490 M
+// copy bandwidth: squared sum of 490 M fp32 gradients 275 us (1.05), AdamW with
+// 32-bit states of a 101 M block 437 us (1.02), with 8-bit states of 490 M
 // 1345 us rounded at random (0.97; 0.86 with bf16 gradients, where the 91
 // instructions an element weigh more).
 #include <algorithm>
