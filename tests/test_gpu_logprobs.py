@@ -356,6 +356,45 @@ def test_captured_and_replayed():
         assert torch.equal(d, eager)
 
 
+@pytest.mark.parametrize("rows,vocab", [(1, 151936), (64, 32000), (4000, 4096), (600, 40000)])
+def test_overlapping_launches_keep_the_order_of_the_stream(rows, vocab):
+    """Copies, other kernels and calls in turn, nothing waited for in between: every call sees
+    what was written before it and none of what is written after it."""
+    values = [random_logits(rows, vocab, torch.bfloat16, 40 + i)[0] for i in range(4)]
+    t = random_logits(rows, vocab, torch.bfloat16, 40)[1]
+    up = torch.ones(rows, device="cuda")
+    alone = []
+    for z in values:
+        out, d = outputs(rows, 4), torch.empty_like(z)
+        rdt.token_logprobs(z, targets=t, **out)
+        rdt.token_logprobs_backward(z, t, out["stats"], d, d_logp=up)
+        torch.cuda.synchronize()
+        alone.append({**out, "d": d})
+    z, d, out = torch.empty_like(values[0]), torch.empty_like(values[0]), outputs(rows, 4)
+    got = []
+    for i in range(12):
+        source = values[i % 4]
+        if i % 3 == 0:
+            z.copy_(source)                # a copy without a kernel
+        elif i % 3 == 1:
+            torch.add(source, 0.0, out=z)  # a kernel
+        else:
+            z.zero_()
+            z.copy_(source.clone())
+        rdt.token_logprobs(z, targets=t, **out)
+        rdt.token_logprobs_backward(z, t, out["stats"], d, d_logp=up)
+        got.append({k: v.clone() for k, v in out.items()})
+        got[-1]["d"] = d.clone()
+        z.fill_(float("nan"))
+        for v in out.values():
+            v.fill_(-5)
+        d.fill_(-5)
+    torch.cuda.synchronize()
+    for i, one in enumerate(got):
+        for k, v in one.items():
+            assert torch.equal(v, alone[i % 4][k]), (i, k)
+
+
 def test_refusals_of_the_binding():
     z, t = random_logits(4, 64, torch.float32, 1)
     e = torch.empty(4, device="cuda")

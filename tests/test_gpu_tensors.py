@@ -375,6 +375,45 @@ def test_captured_and_replayed(sizes):
         assert all(torch.equal(a, b) for a, b in zip(parts, q.snapshot()[k])), k
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("sizes", [[300, 5, 2048] * 280, [3_000_000, 17]], ids=["three", "one"])
+def test_overlapping_launches_keep_the_order_of_the_stream(sizes, bits):
+    """Gradients written by a copy or a kernel, clip, step, gradients overwritten, step after
+    step without a wait: the same as with one after every call."""
+    ways = []
+    for wait in (True, False):
+        p = Problem(sizes, bits, seed=14)
+        lst = p.list()
+        ws = torch.empty(rdt.tensors_sq_sum_workspace_bytes(lst), dtype=torch.uint8, device="cuda")
+        sumsq = torch.zeros(1, dtype=torch.float64, device="cuda")
+        scale, bad = torch.ones(1, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+        gen = torch.Generator(device="cuda").manual_seed(2)
+        grads = [torch.randn(p.g.buf.numel(), generator=gen, device="cuda") for _ in range(3)]
+        sums = []
+        torch.cuda.synchronize()
+        for step in range(1, 10):
+            if step % 2:
+                p.g.buf.copy_(grads[step % 3])
+            else:
+                torch.mul(grads[step % 3], 0.5, out=p.g.buf)
+            for call in (lambda: rdt.tensors_sq_sum(lst, sumsq, ws),
+                         lambda: rdt.clip_scale(sumsq, 1.0, scale, bad),
+                         lambda: rdt.tensors_adamw(lst, step, B1, B2, EPS, scale=scale, skip=bad,
+                                                   seed=1),
+                         lambda: rdt.tensors_adamw(lst, step, B1, B2, EPS, seed=2)):
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+            sums.append(sumsq.clone())
+            p.g.buf.fill_(float("nan"))
+        torch.cuda.synchronize()
+        ways.append((p.snapshot(), torch.cat(sums)))
+    assert torch.equal(ways[0][1], ways[1][1])
+    for k, parts in ways[0][0].items():
+        if k != "g":
+            assert all(torch.equal(a, b) for a, b in zip(parts, ways[1][0][k])), k
+
+
 def test_another_stream():
     p = Problem(SIZES, 8, seed=8)
     s = torch.cuda.Stream()
