@@ -327,11 +327,11 @@ constexpr int kUnroll = 4;
 template <int kThreads, int kStages>
 constexpr int kRingBytes = kUnroll * kStages * kThreads * 16;
 // A thread's first groups, whose maxima are all kept (8 for 256 threads: 16 would leave an SM a
-// CTA less).
-constexpr int first_of(int threads) { return threads == 256 ? 8 : 16; }
+// CTA less; rows for 64 threads have at most 5).
+constexpr int first_of(int threads) { return threads == 128 ? 16 : 8; }
 constexpr int kSample = 64;  // sets of threads whose maxima bound the row's alternatives
-// Later groups that reached the bound of their time, at most.
-constexpr int seen_of(int threads) { return threads == 256 ? 160 : 320; }
+// Later groups that reached the bound of their time, at most (for 64 threads there are none).
+constexpr int seen_of(int threads) { return threads == 64 ? 1 : threads == 256 ? 160 : 320; }
 constexpr int kKeys = 256;   // candidates that are ranked by counting
 
 template <int kThreads, bool kTop>
@@ -863,8 +863,10 @@ cudaError_t launch_logprobs(const LogprobArgs& a, int split, cudaStream_t s) {
 template <typename T>
 cudaError_t logprobs_of(LogprobArgs a, cudaStream_t s) {
   const int vectors = a.vocab / Vec<T>::kPer;
+  // Short rows: 64 threads, and two groups in shared memory so that more CTAs fit (8192 bf16
+  // rows of 4096, 20 alternatives: 39 us, 44 with three).
   if (vectors <= 1024)
-    return a.top ? launch_logprobs<T, 64, 3, true>(a, 1, s) : launch_logprobs<T, 64, 3, false>(a, 1, s);
+    return a.top ? launch_logprobs<T, 64, 2, true>(a, 1, s) : launch_logprobs<T, 64, 2, false>(a, 1, s);
   // At most a row an SM: a cluster a row, as long as each thread has four vectors (152 fp32
   // rows of 151,936, 20 alternatives: 27 us with 256 threads, 33 with 512, 39 with 128 and no
   // cluster; without alternatives 21 us with 512, 23 with 256).
