@@ -234,9 +234,18 @@ __device__ __forceinline__ void store8(uint8_t* p, int have, const uint32_t* c) 
 }
 
 // hi + lo += x x for two elements at once, with the rounding errors of the
-// product and of the sum kept in lo: a sum of n squares is right to about
-// n 2^-48. (fp64 has 1/64 of fp32's rate here: the same sum in fp64 took
-// 1.82 ms for 490 M fp32 values.) kExact: x x has no rounding error (bf16).
+// product and of the sum kept in lo. (fp64 has 1/64 of fp32's rate here: the
+// same sum in fp64 took 1.82 ms for 490 M fp32 values.) kExact: x x has no
+// rounding error (bf16).
+//
+// lo is a plain fp32 sum that grows with the number n of additions: with u =
+// 2^-24 its own roundings come to (n^2 / 2) u^2 of the sum, and equal values
+// give them all one sign. So after every 8 additions lo is taken into hi
+// (tidy; 52 u^2 for the eight), and after every 24 the pairs go into an fp64
+// sum. Adding up every rounding that can occur, with the joins of a thread's
+// pairs (25 u^2) and of a warp's lanes (41 u^2, or 80 u^2 where there was no
+// fp64 sum to start from), the result is within 270 u^2 = 9.6e-13 of the sum
+// for any number of values.
 template <bool kExact>
 __device__ __forceinline__ void add_squares(float2 x, float2& hi, float2& lo, float one) {
   const float2 p = mul2(x, x);
@@ -255,6 +264,14 @@ __device__ __forceinline__ void add_pair(float& hi, float& lo, float h, float l)
   hi = t;
 }
 
+// The same for two pairs at once.
+__device__ __forceinline__ void add_pair2(float2& hi, float2& lo, float2 h, float2 l, float one) {
+  const float2 t = add2(hi, h, one), b = sub2(t, hi, one);
+  const float2 e = add2(sub2(hi, sub2(t, b, one), one), sub2(h, b, one), one);
+  lo = add2(lo, add2(l, e, one), one);
+  hi = t;
+}
+
 // Sixteen bytes of gradients to fp32.
 template <bool kBf16>
 __device__ __forceinline__ void unpack16(const uint4& r, float* x) {
@@ -269,12 +286,15 @@ __device__ __forceinline__ void unpack16(const uint4& r, float* x) {
 
 // A CTA's step is one chunk of two tiles: two (bf16) or four (fp32) 16-byte
 // loads of a thread, those of the next step under way with them. 268 M values,
-// 4 CTAs an SM: fp32 157 us (1.00 of measured HBM; 173 with 6 CTAs), bf16 98 us
-// (0.80: the additions bound it; without looking ahead 101 with two loads, 106
-// with four, 150 with one).
+// 4 CTAs an SM: fp32 154 us (1.03 of the copy bandwidth; 173 with 6 CTAs), bf16
+// 101 us (0.78: the additions bound it; without the next step's loads 4 to 9 us
+// more).
 template <bool kBf16> constexpr int kSqLoads = kBf16 ? 2 : 4;
 template <bool kBf16>
 constexpr int kSqTiles = kSqLoads<kBf16> * (kBf16 ? 8 : 4) * kThreads / kTile;
+// A chunk makes two additions to each pair of a thread: chunks before a tidy, and tidies before
+// the pairs go to fp64. 490 M bf16 values: 178 us; 189 with fp64 every 4 chunks, 165 with neither.
+constexpr int kSqTidy = 4, kSqFold = 3;
 template <bool kBf16, int kMax>
 __global__ void __launch_bounds__(kThreads) tensors_sq_sum_kernel(
     const __grid_constant__ Table<kMax> tab, int tiles, bool first, float one,
@@ -284,11 +304,42 @@ __global__ void __launch_bounds__(kThreads) tensors_sq_sum_kernel(
   using G = typename std::conditional<kBf16, bf16, float>::type;
   constexpr int kPer = 16 / sizeof(G), kStep = kPer * kThreads;  // elements of a load
   constexpr int kLoads = kSqLoads<kBf16>, kSqChunk = kSqTiles<kBf16>;
+  static_assert(kLoads * kPer / 2 == 2 * 4 && kLoads * kStep == kSqChunk * kTile,
+                "two additions to each pair a chunk");
   float2 hi[4] = {}, lo[4] = {};
-  auto add = [&](const float* x) {
+  double total = 0.0;
+  bool folded = false;
+  // the u-th of a thread's loads of a chunk
+  auto add = [&](const float* x, int u) {
 #pragma unroll
-    for (int k = 0; k < kPer / 2; ++k)
-      add_squares<kBf16>(make_float2(x[2 * k], x[2 * k + 1]), hi[k & 3], lo[k & 3], one);
+    for (int k = 0; k < kPer / 2; ++k) {
+      const int i = (u * (kPer / 2) + k) & 3;
+      add_squares<kBf16>(make_float2(x[2 * k], x[2 * k + 1]), hi[i], lo[i], one);
+    }
+  };
+  auto tidy = [&]() {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 t = add2(hi[k], lo[k], one);
+      lo[k] = sub2(lo[k], sub2(t, hi[k], one), one);
+      hi[k] = t;
+    }
+  };
+  // The thread's pairs joined to one.
+  auto join = [&]() {
+    float2 h2 = hi[0], l2 = lo[0];
+#pragma unroll
+    for (int k = 1; k < 4; ++k) add_pair2(h2, l2, hi[k], lo[k], one);
+    float h = h2.x, l = l2.x;
+    add_pair(h, l, h2.y, l2.y);
+    return make_float2(h, l);
+  };
+  auto fold = [&]() {
+    const float2 a = join();
+    total += static_cast<double>(a.x) + a.y;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) hi[k] = lo[k] = make_float2(0.f, 0.f);
+    folded = true;
   };
   // The tiles of the walk's tensor and chunk from its tile on, and whether they are a whole
   // chunk of whole tiles.
@@ -310,48 +361,54 @@ __global__ void __launch_bounds__(kThreads) tensors_sq_sum_kernel(
   bool full = whole(w);
   if (full) load(w, r);
   while (w.tile < tiles) {
-    // the next chunk is looked up and its loads started before this one is added
-    Walk n = w;
-    n.tile += count_of(w) - 1;
-    next_tile(tab, tiles, kSqChunk, n);
-    uint4 next_r[kLoads];
-    const bool next_full = whole(n);
-    if (next_full) load(n, next_r);
-    if (full) {
+    for (int f = 0; f < kSqFold && w.tile < tiles; ++f) {
+      for (int c = 0; c < kSqTidy && w.tile < tiles; ++c) {
+        // the next chunk is looked up and its loads started before this one is added
+        Walk n = w;
+        n.tile += count_of(w) - 1;
+        next_tile(tab, tiles, kSqChunk, n);
+        uint4 next_r[kLoads];
+        const bool next_full = whole(n);
+        if (next_full) load(n, next_r);
+        if (full) {
 #pragma unroll
-      for (int u = 0; u < kLoads; ++u) {
-        float x[kPer];
-        unpack16<kBf16>(r[u], x);
-        add(x);
-      }
-    } else {
-      const G* g = first_of(w);
-      const int left =
-          static_cast<int>(min(tab.t[w.o].n - static_cast<int64_t>(w.tile - w.begin) * kTile,
-                               static_cast<int64_t>(count_of(w)) * kTile));
-      for (int e = threadIdx.x * kPer; e < left; e += kStep) {
-        float x[kPer];
-        if (e + kPer <= left) {
-          unpack16<kBf16>(__ldg(reinterpret_cast<const uint4*>(g + e)), x);
+          for (int u = 0; u < kLoads; ++u) {
+            float x[kPer];
+            unpack16<kBf16>(r[u], x);
+            add(x, u);
+          }
         } else {
+          const G* g = first_of(w);
+          const int left =
+              static_cast<int>(min(tab.t[w.o].n - static_cast<int64_t>(w.tile - w.begin) * kTile,
+                                   static_cast<int64_t>(count_of(w)) * kTile));
+#pragma unroll 1
+          for (int u = 0, e = threadIdx.x * kPer; e < left; e += kStep, ++u) {
+            float x[kPer];
+            if (e + kPer <= left) {
+              unpack16<kBf16>(__ldg(reinterpret_cast<const uint4*>(g + e)), x);
+            } else {
 #pragma unroll
-          for (int k = 0; k < kPer; ++k) x[k] = e + k < left ? static_cast<float>(g[e + k]) : 0.f;
+              for (int k = 0; k < kPer; ++k) x[k] = e + k < left ? static_cast<float>(g[e + k]) : 0.f;
+            }
+            if (kBf16 || u & 1) add(x, 1); else add(x, 0);
+          }
         }
-        add(x);
+        w = n;
+        full = next_full;
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) r[u] = next_r[u];
       }
+      tidy();
     }
-    w = n;
-    full = next_full;
-#pragma unroll
-    for (int u = 0; u < kLoads; ++u) r[u] = next_r[u];
+    if (w.tile < tiles) fold();  // short lists do without fp64 (1.2 us)
   }
-  // down to one pair a warp in fp32: fp64 additions of every lane took 20 us
-  float h = hi[0].x, l = lo[0].x;
-  add_pair(h, l, hi[0].y, lo[0].y);
-#pragma unroll
-  for (int k = 1; k < 4; ++k) {
-    add_pair(h, l, hi[k].x, lo[k].x);
-    add_pair(h, l, hi[k].y, lo[k].y);
+  const float2 rest = join();
+  float h = rest.x, l = rest.y;
+  if (folded) {
+    total += static_cast<double>(h) + l;
+    h = static_cast<float>(total);
+    l = static_cast<float>(total - h);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)

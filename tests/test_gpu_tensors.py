@@ -578,6 +578,23 @@ def test_squared_sum_of_one_large_and_many_small_values():
     assert abs(sq_sum([g]) - want) <= 1e-12 * want
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("first,rest", [(0.3, 0.3), (1e-3, 1e-3), (0.7, 0.7), (1.0, 1.7e-4),
+                                        (1.0, 1.21e-4)])
+def test_squared_sum_of_many_alike(first, rest, dtype):
+    """Half a billion values whose additions round alike, so that nothing averages out; or a few
+    thousand large values in front of ones whose squares are below half a step of the sum."""
+    n, head = 500_000_000, 3_000_000
+    g = torch.full((n,), rest, dtype=dtype, device="cuda")
+    g[:head] = first
+    a, b = float(g[0].double()) ** 2, float(g[-1].double()) ** 2
+    want = head * a + (n - head) * b  # each square is exact in fp64
+    assert abs(sq_sum([g]) - want) <= 1e-12 * want
+    cut = list(g[: n // 8 * 8].view(8, -1)[:, :-16].unbind())  # rows of 62,499,984: ragged ends
+    a8 = head * a + sum(c.numel() for c in cut) * b - head * b
+    assert abs(sq_sum(cut) - a8) <= 1e-12 * a8
+
+
 def test_squared_sum_of_nothing_and_of_what_is_not_finite():
     assert sq_sum([]) == 0.0
     assert sq_sum([torch.zeros(100, device="cuda")]) == 0.0
