@@ -317,19 +317,24 @@ class DecoderTrainer:
     def score(self, x=None, targets=None, ids=None, top=0, logit_scale=1.0):
         """Scores one batch of T tokens with the current weights: a dict of device tensors
         ``entropy``, ``lse`` [T], with targets (int32 [T], negative: not scored) ``logp``
-        [T], with top > 0 ``top_ids``, ``top_logp`` [T, top] (rdt_head_logprobs). x, ids as
-        for train_step. The activations kept for a backward pass are overwritten."""
+        [T], with top > 0 ``top_ids``, ``top_logp`` [T, top] (rdt_head_logprobs). x, ids: the
+        batch's T tokens; None scores the inputs staged for training (with accumulation the
+        first micro-batch's ids). Staged inputs stay as they are: a later step without inputs
+        trains on them. The activations kept for a backward pass are overwritten."""
         s, cfg, T = self.shape, self.cfg, self.shape.tokens
-        if ids is not None:
-            self.ids[:T].copy_(ids)
+        if ids is not None and not self.embedding:
+            raise ValueError("ids need the device embedding")
+        h = self.h[0]
         if self.embedding:
-            rdt.embedding_forward(self.emb, self.ids[:T], self.h[0])
+            mine = self.ids[:T] if ids is None else torch.empty_like(self.ids[:T]).copy_(ids)
+            rdt.embedding_forward(self.emb, mine, h)  # every pass writes h[0] from its ids
         elif x is not None:
-            self.h[0].copy_(x)
+            h = torch.empty_like(h).copy_(x)
         for li in range(s.layers):
             rdt.block_forward(cfg, s.batch, s.seq, self.block_slice(self.w, li),
-                              self.block_slice(self.wb, li), self.h[li], self.h[li + 1],
+                              self.block_slice(self.wb, li), h, self.h[li + 1],
                               self.saved_slice(li), self.block_ws)
+            h = self.h[li + 1]
         if self.score_ws is None:
             self.score_ws = torch.empty(rdt.head_logprobs_workspace_bytes(cfg, T),
                                         dtype=torch.uint8, device=self.device)
@@ -341,7 +346,7 @@ class DecoderTrainer:
         if top:
             out["top_ids"] = torch.empty((T, top), dtype=torch.int32, device=self.device)
             out["top_logp"] = torch.empty((T, top), **f32)
-        rdt.head_logprobs(cfg, self.h[s.layers], self.tensor(self.w, "head", "g_final"),
+        rdt.head_logprobs(cfg, h, self.tensor(self.w, "head", "g_final"),
                           self.tensor(self.wb, "head", "w_lm"), self.score_ws, targets=targets,
                           logit_scale=logit_scale, **out)
         return out

@@ -63,6 +63,43 @@ def test_scoring_leaves_training_alone():
         assert torch.equal(getattr(a, name), getattr(b, name)), name
 
 
+@pytest.mark.parametrize("kw", [dict(embedding=True), dict(embedding=True, accumulation_steps=2),
+                                dict(), dict(checkpoint_segments=2)])
+@pytest.mark.parametrize("graph", [False, True])
+def test_scoring_leaves_the_staged_inputs_alone(kw, graph):
+    """Steps without inputs train on the batch staged before, whatever was scored in between."""
+    shape = ragged_shape()
+    n, T = kw.get("accumulation_steps", 1), shape.tokens
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    ids, other = (torch.randint(0, shape.vocab, (n * T,), dtype=torch.int32, device="cuda",
+                                generator=gen) for _ in range(2))
+    x, y = (torch.randn(n * T, shape.hidden, device="cuda", generator=gen) for _ in range(2))
+    one = dict(ids=ids) if kw.get("embedding") else dict(x=x)
+    two = dict(ids=other[:T]) if kw.get("embedding") else dict(x=y[:T])
+    ways = []
+    for scores in (False, True):
+        tr = DecoderTrainer(shape, **kw)
+        tr.init_random(4)
+        tr.train_step(targets=ids.roll(-1), **one)
+        if graph:
+            tr.train_step_graph(targets=ids.roll(-1), **one)
+        for _ in range(2):
+            if scores:
+                tr.score(targets=other[:T].roll(-1), top=3, **two)
+            tr.train_step_graph() if graph else tr.train_step()
+        torch.cuda.synchronize()
+        ways.append(tr)
+    for name in ("w", "m", "v") + (("emb", "emb_m") if kw.get("embedding") else ()):
+        assert torch.equal(getattr(ways[0], name), getattr(ways[1], name)), name
+
+
+def test_scoring_takes_ids_with_the_device_embedding_only():
+    shape = ragged_shape()
+    tr = DecoderTrainer(shape)
+    with pytest.raises(ValueError, match="embedding"):
+        tr.score(ids=torch.zeros(shape.tokens, dtype=torch.int32, device="cuda"))
+
+
 def test_scoring_with_the_device_embedding():
     shape = ragged_shape()
     tr = DecoderTrainer(shape, embedding=True)
