@@ -90,22 +90,13 @@ __device__ __forceinline__ void next_tile(const Table<kMax>& tab, int tiles, int
 }
 
 // Launches overlap (programmatic launch: one may start when all CTAs of the
-// one before it have said launches_may_follow). The first of a call waits for
-// the end of what is before it in the stream, and only then lets the next one
-// come: two calls in a row hide the second's launch. The later launches of a
-// call touch no memory in common with the first but the partial sums' array,
-// each its own part; they start at once and end after the one before
-// (end_after_previous, in one thread), so that the end of a call's last launch
-// is the end of all.
-__device__ __forceinline__ void wait_for_previous() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-__device__ __forceinline__ void launches_may_follow(bool first) {
-  if (first) wait_for_previous();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void end_after_previous() {
-  if (blockIdx.x == 0 && threadIdx.x == 0) wait_for_previous();
+// one before it have come here). Each waits for the end of what is before it
+// in the stream ahead of its first access to memory, the later launches of one
+// call as well as its first: nothing but that wait orders their reads after
+// the writes of earlier kernels. What overlaps is a launch's own start and its
+// first look at the table.
+__device__ __forceinline__ void after_previous_kernel() {
+  asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // Two fp32 operations, each rounded to nearest, in one instruction.
@@ -297,9 +288,7 @@ constexpr int kSqTiles = kSqLoads<kBf16> * (kBf16 ? 8 : 4) * kThreads / kTile;
 constexpr int kSqTidy = 4, kSqFold = 3;
 template <bool kBf16, int kMax>
 __global__ void __launch_bounds__(kThreads) tensors_sq_sum_kernel(
-    const __grid_constant__ Table<kMax> tab, int tiles, bool first, float one,
-    double* __restrict__ partials) {
-  launches_may_follow(first);
+    const __grid_constant__ Table<kMax> tab, int tiles, float one, double* __restrict__ partials) {
   __shared__ double red[kThreads / 32];
   using G = typename std::conditional<kBf16, bf16, float>::type;
   constexpr int kPer = 16 / sizeof(G), kStep = kPer * kThreads;  // elements of a load
@@ -359,6 +348,7 @@ __global__ void __launch_bounds__(kThreads) tensors_sq_sum_kernel(
   Walk w = first_tile(tab, tiles, kSqChunk);
   uint4 r[kLoads];
   bool full = whole(w);
+  after_previous_kernel();
   if (full) load(w, r);
   while (w.tile < tiles) {
     for (int f = 0; f < kSqFold && w.tile < tiles; ++f) {
@@ -420,12 +410,11 @@ __global__ void __launch_bounds__(kThreads) tensors_sq_sum_kernel(
     for (int w = 0; w < kThreads / 32; ++w) s += red[w];
     partials[blockIdx.x] = s;
   }
-  end_after_previous();
 }
 
 __global__ void __launch_bounds__(kThreads) tensors_sq_final_kernel(
     const double* __restrict__ partials, int n, double* __restrict__ out) {
-  launches_may_follow(true);
+  after_previous_kernel();
   __shared__ double red[kThreads / 32];
   double s = 0.0;
   for (int i = threadIdx.x; i < n; i += kThreads) s += partials[i];
@@ -698,12 +687,10 @@ __device__ __forceinline__ void adamw_run(const Tensor& t, int64_t first, const 
 constexpr int kChunk = 2;  // tiles of a CTA's step of tensors_adamw_kernel
 template <int kBits, bool kBf16, bool kRandom, int kMax>
 __global__ void __launch_bounds__(kThreads) tensors_adamw_kernel(
-    const __grid_constant__ Table<kMax> tab, int tiles, bool first, const AdamArgs p) {
-  launches_may_follow(first);
-  if (p.skip && *p.skip) {
-    end_after_previous();
-    return;
-  }
+    const __grid_constant__ Table<kMax> tab, int tiles, const AdamArgs p) {
+  Walk w = first_tile(tab, tiles, kChunk);
+  after_previous_kernel();
+  if (p.skip && *p.skip) return;
   const float sc = p.scale ? *p.scale : 1.f;
   float inv_bc1 = p.inv_bc1, inv_root_bc2 = p.inv_root_bc2;
   int step = p.step;
@@ -719,7 +706,6 @@ __global__ void __launch_bounds__(kThreads) tensors_adamw_kernel(
   auto key_of = [&](const Walk& w) {
     return mix(key0 + w.o) ^ static_cast<uint32_t>(place(w) >> 32) * 0x9E3779B1u;
   };
-  Walk w = first_tile(tab, tiles, kChunk);
   if constexpr (kBits == 32) {
     while (w.tile < tiles) {
       const Tensor& t = tab.t[w.o];
@@ -760,7 +746,6 @@ __global__ void __launch_bounds__(kThreads) tensors_adamw_kernel(
       vs = next_vs;
     }
   }
-  end_after_previous();
 }
 
 rdt_status refuse(const char* msg) {
@@ -856,15 +841,13 @@ cudaError_t sq_sum_launches(const rdt_opt_tensor* list, int count, bool half, do
     if (*used + blocks > room) return cudaErrorInvalidValue;
     auto kernel = half ? tensors_sq_sum_kernel<true, kMax> : tensors_sq_sum_kernel<false, kMax>;
     double* to = parts + *used;
-    const bool first = *used == 0;
     *used += blocks;
-    return launch(kernel, blocks, 0, s, tab, tiles, first, 1.f, to);
+    return launch(kernel, blocks, 0, s, tab, tiles, 1.f, to);
   });
 }
 
 template <int kBits, bool kBf16, bool kRandom, int kMax>
-cudaError_t launch_adamw(const Table<kMax>& tab, int tiles, const AdamArgs& a, bool first,
-                         cudaStream_t s) {
+cudaError_t launch_adamw(const Table<kMax>& tab, int tiles, const AdamArgs& a, cudaStream_t s) {
   constexpr int kBytes = kBits == 8 ? 2 * Stage<kBf16>::kBytes : 0;
   auto kernel = tensors_adamw_kernel<kBits, kBf16, kRandom, kMax>;
   static std::atomic<uint64_t> allowed{0};  // devices where the kernel may use kBytes
@@ -876,25 +859,21 @@ cudaError_t launch_adamw(const Table<kMax>& tab, int tiles, const AdamArgs& a, b
     if (e != cudaSuccess) return e;
     if (dev < 64) allowed.fetch_or(uint64_t(1) << dev);
   }
-  return launch(kernel, ctas(tiles, kChunk, kBits == 32 ? 8 : 4, 6), kBytes, s, tab, tiles, first,
-                a);
+  return launch(kernel, ctas(tiles, kChunk, kBits == 32 ? 8 : 4, 6), kBytes, s, tab, tiles, a);
 }
 
 template <int kMax>
 cudaError_t adamw_launches(const rdt_opt_tensor* list, int count, bool half, int bits, bool random,
                            const AdamArgs& a, cudaStream_t s) {
-  bool first = true;
   return each_launch<kMax>(list, count, [&](const Table<kMax>& tab, int tiles) {
-    const bool f = first;
-    first = false;
     if (bits == 32)
-      return half ? launch_adamw<32, true, false>(tab, tiles, a, f, s)
-                  : launch_adamw<32, false, false>(tab, tiles, a, f, s);
+      return half ? launch_adamw<32, true, false>(tab, tiles, a, s)
+                  : launch_adamw<32, false, false>(tab, tiles, a, s);
     if (random)
-      return half ? launch_adamw<8, true, true>(tab, tiles, a, f, s)
-                  : launch_adamw<8, false, true>(tab, tiles, a, f, s);
-    return half ? launch_adamw<8, true, false>(tab, tiles, a, f, s)
-                : launch_adamw<8, false, false>(tab, tiles, a, f, s);
+      return half ? launch_adamw<8, true, true>(tab, tiles, a, s)
+                  : launch_adamw<8, false, true>(tab, tiles, a, s);
+    return half ? launch_adamw<8, true, false>(tab, tiles, a, s)
+                : launch_adamw<8, false, false>(tab, tiles, a, s);
   });
 }
 
