@@ -209,7 +209,7 @@ struct Row {
   __device__ __forceinline__ bool whole(int v) const { return v >= whole0 && v < whole1; }
   // v in [0, vectors)
   __device__ __forceinline__ uint4 load(int v) const {
-    return whole(v) ? __ldg(v0 + v) : load_part(first_of(v));
+    return whole(v) ? v0[v] : load_part(first_of(v));
   }
   // Starts to copy whole vector v to shared memory; the thread that called finds it there
   // after a wait for its copies.
@@ -295,7 +295,10 @@ __device__ __forceinline__ void st_cluster_u64(uint32_t at, uint64_t x) {
 // Each kernel of this file may be launched while the one before it in the
 // stream still runs, and waits here for its end before it touches memory: of
 // two calls in a row the second's launch is hidden (programmatic launch; after
-// a kernel that does not take part the launch is an ordinary one).
+// a kernel that does not take part the launch is an ordinary one). Nothing is
+// read through the read-only path (__ldg, const __restrict__): that is for
+// memory nobody writes while the kernel is there, and this one may be there
+// while the kernel before it writes.
 __device__ __forceinline__ void after_previous_kernel() {
   asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
 }

@@ -94,7 +94,9 @@ __device__ __forceinline__ void next_tile(const Table<kMax>& tab, int tiles, int
 // in the stream ahead of its first access to memory, the later launches of one
 // call as well as its first: nothing but that wait orders their reads after
 // the writes of earlier kernels. What overlaps is a launch's own start and its
-// first look at the table.
+// first look at the table. For the same reason nothing is read through the
+// read-only path (__ldg, const __restrict__), which is for memory nobody writes
+// while the kernel is there.
 __device__ __forceinline__ void after_previous_kernel() {
   asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
 }
@@ -277,18 +279,18 @@ __device__ __forceinline__ void unpack16(const uint4& r, float* x) {
 
 // A CTA's step is one chunk of two tiles: two (bf16) or four (fp32) 16-byte
 // loads of a thread, those of the next step under way with them. 268 M values,
-// 4 CTAs an SM: fp32 154 us (1.03 of the copy bandwidth; 173 with 6 CTAs), bf16
-// 101 us (0.78: the additions bound it; without the next step's loads 4 to 9 us
-// more).
+// 4 CTAs an SM: fp32 152 us (1.04 of the copy bandwidth; 173 with 6 CTAs), bf16
+// 100 us (0.79: the additions bound it; without the next step's loads 4 to 9 us
+// more). Left to itself the compiler takes 48 registers for bf16 and spills.
 template <bool kBf16> constexpr int kSqLoads = kBf16 ? 2 : 4;
 template <bool kBf16>
 constexpr int kSqTiles = kSqLoads<kBf16> * (kBf16 ? 8 : 4) * kThreads / kTile;
 // A chunk makes two additions to each pair of a thread: chunks before a tidy, and tidies before
-// the pairs go to fp64. 490 M bf16 values: 178 us; 189 with fp64 every 4 chunks, 165 with neither.
+// the pairs go to fp64. 490 M bf16 values: 176 us; 189 with fp64 every 4 chunks, 165 with neither.
 constexpr int kSqTidy = 4, kSqFold = 3;
 template <bool kBf16, int kMax>
-__global__ void __launch_bounds__(kThreads) tensors_sq_sum_kernel(
-    const __grid_constant__ Table<kMax> tab, int tiles, float one, double* __restrict__ partials) {
+__global__ void __launch_bounds__(kThreads, 4) tensors_sq_sum_kernel(
+    const __grid_constant__ Table<kMax> tab, int tiles, float one, double* partials) {
   __shared__ double red[kThreads / 32];
   using G = typename std::conditional<kBf16, bf16, float>::type;
   constexpr int kPer = 16 / sizeof(G), kStep = kPer * kThreads;  // elements of a load
@@ -343,7 +345,7 @@ __global__ void __launch_bounds__(kThreads) tensors_sq_sum_kernel(
   auto load = [&](const Walk& w, uint4* r) {
     const uint4* g = reinterpret_cast<const uint4*>(first_of(w)) + threadIdx.x;
 #pragma unroll
-    for (int u = 0; u < kLoads; ++u) r[u] = __ldg(g + u * kThreads);
+    for (int u = 0; u < kLoads; ++u) r[u] = __ldcg(g + u * kThreads);  // (plain: 352 us for 275)
   };
   Walk w = first_tile(tab, tiles, kSqChunk);
   uint4 r[kLoads];
@@ -376,7 +378,7 @@ __global__ void __launch_bounds__(kThreads) tensors_sq_sum_kernel(
           for (int u = 0, e = threadIdx.x * kPer; e < left; e += kStep, ++u) {
             float x[kPer];
             if (e + kPer <= left) {
-              unpack16<kBf16>(__ldg(reinterpret_cast<const uint4*>(g + e)), x);
+              unpack16<kBf16>(__ldcg(reinterpret_cast<const uint4*>(g + e)), x);
             } else {
 #pragma unroll
               for (int k = 0; k < kPer; ++k) x[k] = e + k < left ? static_cast<float>(g[e + k]) : 0.f;
@@ -413,7 +415,7 @@ __global__ void __launch_bounds__(kThreads) tensors_sq_sum_kernel(
 }
 
 __global__ void __launch_bounds__(kThreads) tensors_sq_final_kernel(
-    const double* __restrict__ partials, int n, double* __restrict__ out) {
+    const double* partials, int n, double* out) {
   after_previous_kernel();
   __shared__ double red[kThreads / 32];
   double s = 0.0;

@@ -526,6 +526,39 @@ def test_gradient_in_place(dtype, pad, shift):
     assert torch.equal(z, d)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gradient_in_place_is_read_at_once(dtype):
+    """Rows that share cache lines, their gradient written over them, and its squared sum, its
+    own log probabilities and one more gradient taken without a wait: as with waits."""
+    rows, vocab = 301, 4099
+    z0, t = random_logits(rows, vocab, dtype, 61)
+    up = torch.full((rows,), 0.5, device="cuda")
+    ways = []
+    for wait in (True, False):
+        z = torch.empty_like(z0)
+        lst = rdt.OptTensors(g=[z])
+        ws = torch.empty(rdt.tensors_sq_sum_workspace_bytes(lst), dtype=torch.uint8, device="cuda")
+        sums = torch.zeros(8, dtype=torch.float64, device="cuda")
+        out, again = outputs(rows, 3), outputs(rows, 3)
+        kept_out = []
+        for i in range(8):
+            z.copy_(z0 * (1 + i / 4))
+            for call in (lambda: rdt.token_logprobs(z, targets=t, **out),
+                         lambda: rdt.token_logprobs_backward(z, t, out["stats"], z, d_logp=up),
+                         lambda: rdt.tensors_sq_sum(lst, sums[i:i + 1], ws),
+                         lambda: rdt.token_logprobs(z, targets=t, **again),
+                         lambda: rdt.token_logprobs_backward(z, t, again["stats"], z, d_logp=up)):
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+            kept_out.append([z.clone()] + [x.clone() for x in again.values()])
+        torch.cuda.synchronize()
+        ways.append((sums.clone(), kept_out))
+    assert torch.equal(ways[0][0], ways[1][0]) and (ways[0][0] > 0).all()
+    for a, b in zip(ways[0][1], ways[1][1]):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_gradient_of_masked_empty_and_broken_rows(dtype):
     vocab = 1201
