@@ -762,6 +762,9 @@ rdt_status launched(cudaError_t e) {
 }
 
 constexpr int kMaxCount = 1000000;
+// Tiles of a launch: a CTA's next tile, up to a grid's chunks further on, stays inside 32 bits.
+// More than memory holds, but a list for the squared sum may name a tensor again and again.
+constexpr int64_t kMaxTiles = int64_t(1) << 30;
 
 int64_t tiles_of(int64_t n) { return (n + kTile - 1) / kTile; }
 
@@ -786,7 +789,7 @@ cudaError_t each_launch(const rdt_opt_tensor* list, int count, F f) {
   tab.first = 0;
   for (int i = 0; i <= count; ++i) {
     const int64_t more = i < count ? tiles_of(list[i].n) : 0;
-    if (tab.count && (i == count || tab.count == kMax || tiles + more > INT32_MAX)) {
+    if (tab.count && (i == count || tab.count == kMax || tiles + more > kMaxTiles)) {
       if (tiles > 0) {
         const cudaError_t e = f(tab, static_cast<int>(tiles));
         if (e != cudaSuccess) return e;
@@ -889,8 +892,12 @@ extern "C" {
 
 size_t rdt_tensors_sq_sum_workspace_bytes(const rdt_opt_tensor* tensors, int32_t count) {
   if (list_problem(tensors, count, RDT_F32)) return 0;
-  // one partial sum for each block of each launch (no device is asked how many there are)
-  return (static_cast<size_t>(count) / kMaxTensors + 1) * kMaxPartials * sizeof(double);
+  // one partial sum for each block of each launch (no device is asked how many there are); two
+  // launches that end for their tiles have more than kMaxTiles together
+  int64_t tiles = 0;
+  for (int i = 0; i < count; ++i) tiles += tiles_of(tensors[i].n);
+  const size_t launches = count / kMaxTensors + 1 + 2 * (tiles / kMaxTiles);
+  return launches * kMaxPartials * sizeof(double);
 }
 
 rdt_status rdt_tensors_sq_sum(const rdt_opt_tensor* tensors, int32_t count, int32_t g_dtype,

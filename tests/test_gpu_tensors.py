@@ -595,6 +595,17 @@ def test_squared_sum_of_many_alike(first, rest, dtype):
     assert abs(sq_sum(cut) - a8) <= 1e-12 * a8
 
 
+def test_squared_sum_of_a_list_with_more_tiles_than_32_bits_count():
+    """2^31 - 1 tiles of 2048: one tensor of 2^34 elements named 256 times, once a tile shorter."""
+    n = 1 << 34
+    g = torch.full((n,), 0.5, dtype=torch.bfloat16, device="cuda")
+    g[-2048:] = 2.0
+    g[0] = 4.0
+    one = 0.25 * (n - 2049) + 4.0 * 2048 + 16.0
+    want = 256 * one - 4.0 * 2048
+    assert abs(sq_sum([g] * 255 + [g[:-2048]]) - want) <= 1e-12 * want
+
+
 def test_squared_sum_of_nothing_and_of_what_is_not_finite():
     assert sq_sum([]) == 0.0
     assert sq_sum([torch.zeros(100, device="cuda")]) == 0.0

@@ -157,6 +157,25 @@ def test_tensors_sq_sum_refuses(lib):
     assert lib.rdt_tensors_sq_sum_workspace_bytes(entries(dict(n=-1)), 1) == 0
 
 
+@pytest.mark.parametrize("sizes", [[1 << 40] * 400, [(1 << 40) - 5, 3] * 900, [1 << 33] * 32,
+                                   [1 << 39, 1 << 40] * 16, [300] * 1203, [(1 << 40) + 0] * 3])
+def test_the_workspace_of_the_squared_sum_has_room_for_every_launch(lib, sizes):
+    """A launch ends at 400 entries (32 for short lists) or where the next entry's tiles of 2048
+    would make it more than 2^30: then a CTA's next tile (its own, and at most 4 x 2048 chunks of
+    two behind) fits 32 bits. Each launch has up to 2048 partial sums."""
+    most, launches, held, tiles = 32 if len(sizes) <= 32 else 400, 1, 0, 0
+    for n in sizes:
+        more = -(-n // 2048)
+        if held and (held == most or tiles + more > 1 << 30):
+            launches, held, tiles = launches + 1, 0, 0
+        held, tiles = held + 1, tiles + more
+        assert tiles <= 1 << 30
+    e = entries(*[dict(n=n) for n in sizes])
+    size = lib.rdt_tensors_sq_sum_workspace_bytes(e, len(sizes))
+    assert size >= launches * 2048 * 8
+    assert size <= (3 * launches + 1) * 2048 * 8
+
+
 def test_bindings_refuse_tensors_the_device_cannot_read():
     z = torch.zeros(2, 8)
     with pytest.raises(ValueError, match="CUDA"):
