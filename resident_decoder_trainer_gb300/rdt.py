@@ -316,6 +316,21 @@ def _here(t, what, dtypes, shape, device):
     return t.data_ptr()
 
 
+def _scalar(t, what, dtypes, device):
+    """The address of a tensor whose first element a kernel reads or writes."""
+    if t.numel() < 1:
+        raise ValueError(f"{what} has no element")
+    return _here(t, what, dtypes, None, device)
+
+
+def _scratch(t, what, device):
+    """Address and bytes of a workspace. An expanded or strided view has fewer bytes than its
+    elements come to."""
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return _here(t, what, (t.dtype,), None, device), t.numel() * t.element_size()
+
+
 _F32, _I32 = (torch.float32,), (torch.int32,)
 
 
@@ -398,8 +413,7 @@ def head_logprobs(cfg, h, gamma_f, w_lm, ws, targets=None, logp=None, entropy=No
         None if lse is None else _here(lse, "lse", _F32, one, dev), top,
         None if top_ids is None else _here(top_ids, "top_ids", _I32, (tokens, top), dev),
         None if top_logp is None else _here(top_logp, "top_logp", _F32, (tokens, top), dev),
-        _here(ws, "ws", (ws.dtype,), None, dev), ws.numel() * ws.element_size(),
-        _stream(stream)))
+        *_scratch(ws, "ws", dev), _stream(stream)))
 
 
 # ------------------------------------------------- many tensors: clip and AdamW
@@ -480,9 +494,8 @@ def tensors_sq_sum(tensors: OptTensors, sumsq, ws, stream=None):
     """sumsq (fp64 device scalar) = the squared sum of every gradient of the list."""
     dev = tensors._on_device()
     _check(lib().rdt_tensors_sq_sum(tensors.entries, tensors.count, tensors.g_code,
-                                    _here(sumsq, "sumsq", (torch.float64,), None, dev),
-                                    _here(ws, "ws", (ws.dtype,), None, dev),
-                                    ws.numel() * ws.element_size(), _stream(stream)))
+                                    _scalar(sumsq, "sumsq", (torch.float64,), dev),
+                                    *_scratch(ws, "ws", dev), _stream(stream)))
 
 
 def tensors_adamw(tensors: OptTensors, step, beta1, beta2, eps, scale=None, skip=None,
@@ -498,10 +511,10 @@ def tensors_adamw(tensors: OptTensors, step, beta1, beta2, eps, scale=None, skip
     _check(lib().rdt_tensors_adamw(
         tensors.entries, tensors.count, tensors.g_code, tensors.state_bits,
         -1 if seed is None else seed,
-        None if scale is None else _here(scale, "scale", _F32, None, dev),
-        None if skip is None else _here(skip, "skip", _I32, None, dev), int(step or 0),
-        None if step_dev is None else _here(step_dev, "step_dev", _I32, None, dev), beta1, beta2,
-        eps, _stream(stream)))
+        None if scale is None else _scalar(scale, "scale", _F32, dev),
+        None if skip is None else _scalar(skip, "skip", _I32, dev), int(step or 0),
+        None if step_dev is None else _scalar(step_dev, "step_dev", _I32, dev), beta1, beta2, eps,
+        _stream(stream)))
 
 
 # ------------------------------------------------- NF4 + LoRA block

@@ -651,6 +651,22 @@ def test_refusals_of_the_list():
         rdt.tensors_adamw(rdt.OptTensors(**ok), 0, B1, B2, EPS)
 
 
+def test_refusals_of_workspaces_and_scalars():
+    def t(n, dtype=torch.float32):
+        return torch.zeros(n, dtype=dtype, device="cuda")
+
+    lst = rdt.OptTensors(g=[t(300)], w=[t(300)], m=[t(300)], v=[t(300)])
+    size = rdt.tensors_sq_sum_workspace_bytes(lst)
+    sumsq = t(1, torch.float64)
+    with pytest.raises(ValueError, match="contiguous"):
+        rdt.tensors_sq_sum(lst, sumsq, t(1, torch.uint8).expand(size))
+    with pytest.raises(ValueError, match="sumsq"):
+        rdt.tensors_sq_sum(lst, sumsq[:0], t(size, torch.uint8))
+    for kw in (dict(scale=t(0)), dict(skip=t(0, torch.int32)), dict(step_dev=t(0, torch.int32))):
+        with pytest.raises(ValueError, match="no element"):
+            rdt.tensors_adamw(lst, 1, B1, B2, EPS, **kw)
+
+
 def test_rates_can_change_between_steps():
     p = Problem([500, 300], 32, seed=12)
     old = p.snapshot()

@@ -189,6 +189,23 @@ def test_bindings_refuse_tensors_the_device_cannot_read():
         rdt.tensors_adamw(empty, 1, 0.9, 0.95, 1e-8, seed=-1)
 
 
+def test_bindings_refuse_workspaces_and_scalars_that_hold_less_than_they_seem():
+    """The checks alone, on CPU tensors (device -1): an expanded workspace of one byte that
+    claims a million, an empty scale that would count as none."""
+    for t in (torch.empty(1, dtype=torch.uint8).expand(1 << 20),
+              torch.empty(100, dtype=torch.uint8)[::2], torch.empty(4, 6).t()):
+        with pytest.raises(ValueError, match="contiguous"):
+            rdt._scratch(t, "ws", -1)
+    ws = torch.empty(4, 6)
+    assert rdt._scratch(ws, "ws", -1) == (ws.data_ptr(), 96)
+    with pytest.raises(ValueError, match="no element"):
+        rdt._scalar(torch.empty(0), "scale", (torch.float32,), -1)
+    with pytest.raises(ValueError, match="type"):
+        rdt._scalar(torch.empty(1), "skip", (torch.int32,), -1)
+    one = torch.ones(1)
+    assert rdt._scalar(one, "scale", (torch.float32,), -1) == one.data_ptr()
+
+
 def test_the_random_rounding_numbers_are_uniform():
     """The 16-bit halves that decide the rounding (the header's function of seed, step,
     entry and element, restated here): uniform, and independent of their neighbours."""
