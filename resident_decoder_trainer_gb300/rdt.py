@@ -339,6 +339,8 @@ def _rows_of(logits, what, device):
     if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
         raise ValueError(f"{what} must be [rows, vocab] with contiguous rows")
     rows, vocab = logits.shape
+    if rows >= 1 << 31 or vocab > 1 << 30:  # ctypes would cut them to 32 bits
+        raise ValueError(f"{what} has more than 2^31 - 1 rows or 2^30 columns")
     return ptr, rows, vocab, logits.stride(0) if rows > 1 else vocab
 
 

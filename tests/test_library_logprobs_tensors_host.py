@@ -206,6 +206,14 @@ def test_bindings_refuse_workspaces_and_scalars_that_hold_less_than_they_seem():
     assert rdt._scalar(one, "scale", (torch.float32,), -1) == one.data_ptr()
 
 
+@pytest.mark.parametrize("rows,vocab", [((1 << 32) + 1, 8), (1 << 31, 8), (1, (1 << 32) + 8),
+                                        (3, (1 << 30) + 1)])
+def test_bindings_refuse_sizes_that_do_not_fit_the_call(rows, vocab):
+    """The C call takes 32-bit sizes: 2^32 + 1 rows must not become one."""
+    with pytest.raises(ValueError, match="rows"):
+        rdt._rows_of(torch.empty(rows, vocab, device="meta"), "logits", -1)
+
+
 def test_the_random_rounding_numbers_are_uniform():
     """The 16-bit halves that decide the rounding (the header's function of seed, step,
     entry and element, restated here): uniform, and independent of their neighbours."""
