@@ -9,6 +9,7 @@ from resident_decoder_trainer_gb300 import rdt, synth
 from resident_decoder_trainer_gb300.nf4_step import Nf4LoraTrainer
 from resident_decoder_trainer_gb300.step import DecoderTrainer
 
+import test_gpu_tensors as tensors
 from gpu_helpers import LOSS_REL, ensure_built, ragged_shape, rel_l2, to_np
 
 pytestmark = pytest.mark.gpu
@@ -275,3 +276,47 @@ def test_a_policy_step_of_a_linear_head(bits):
             want = before[2] - 1e-3 * (g / (g.abs() + 1e-8) + 0.1 * before[2])
             assert (w.double() - want).abs().max() < 1e-3 * 2.0 ** -18 + 2.0 ** -22
         assert torch.equal(wb, w.bfloat16())
+
+
+@pytest.mark.parametrize("bits,seed", [(32, None), (8, None), (8, 9)])
+def test_the_updates_of_three_policy_steps(bits, seed):
+    """The steps above, with every update checked: weight and bias, their moments (codes and
+    scales), the bf16 copies, at the first step from zero states and at the next ones from the
+    states the last one left; bit for bit by the documented operations and, with the tolerances
+    of the many-tensor tests, in 64 bits. The bias has a rate and a decay of its own."""
+    T, V, H = 192, 2048, 128
+    gen = torch.Generator(device="cuda").manual_seed(16)
+    x = torch.randn(T, H, generator=gen, device="cuda").bfloat16()
+    tg = torch.randint(0, V, (T,), generator=gen, device="cuda", dtype=torch.int32)
+    tg[:T // 4] = -1
+    up = torch.randn(T, generator=gen, device="cuda") / T
+    h_up = torch.full((T,), -0.01 / T, device="cuda")
+    p = tensors.Problem([V * H, V], bits, seed=17)
+    p.lr, p.wd = [1e-3, 2e-2], [0.1, 0.0]
+    for arena in (p.m, p.v, p.ms, p.vs):
+        for part in arena.parts:
+            part.zero_()
+    for w, wb in zip(p.w.parts, p.wb.parts):
+        wb.copy_(w)
+    z = torch.empty(T, V, device="cuda")
+    dz = torch.empty(T, V, device="cuda", dtype=torch.bfloat16)
+    f = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
+    logp, ent, stats = f(T), f(T), f(T, 2)
+    lst = p.list()
+    ws = torch.empty(rdt.tensors_sq_sum_workspace_bytes(lst), dtype=torch.uint8, device="cuda")
+    sumsq = torch.zeros(1, dtype=torch.float64, device="cuda")
+    scale, bad = torch.ones(1, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    for step in (1, 2, 3):
+        rdt.gemm(x, 0, p.wb.parts[0].view(V, H), 0, T, V, H, z)
+        z += p.w.parts[1]
+        rdt.token_logprobs(z, targets=tg, logp=logp, entropy=ent, stats=stats)
+        rdt.token_logprobs_backward(z, tg, stats, dz, d_logp=up, entropy=ent, d_entropy=h_up)
+        rdt.gemm(dz, 1, x, 1, V, H, T, p.g.parts[0].view(V, H))
+        torch.sum(dz.float(), 0, out=p.g.parts[1])
+        rdt.tensors_sq_sum(lst, sumsq, ws)
+        rdt.clip_scale(sumsq, 0.05, scale, bad)
+        assert 0 < float(scale) <= 1 and int(bad) == 0
+        assert all(int(part.count_nonzero()) > part.numel() // 2 for part in p.g.parts)
+        before = [w.clone() for w in p.w.parts]
+        tensors.check_step(p, step, scale=float(scale), seed=seed, skip=bad)
+        assert all(not torch.equal(a, b) for a, b in zip(before, p.w.parts))
