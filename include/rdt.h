@@ -510,9 +510,11 @@ rdt_status rdt_head_logprobs(const rdt_config* cfg, int32_t tokens, const float*
  *   Zeroed codes and scales are the initial state.
  *   seed < 0: codes are rounded to nearest even. seed in [0, 2^32): rounded up
  *   or down with the probability of the distance, from 16 bits that are a
- *   function of (seed, step, index of the entry, index of the element): the
- *   expected state is exact, so that changes smaller than half a code (a decay
- *   of v by 1 - b2) are not lost. Ignored for 32 bits.
+ *   function of (seed, step, index of the entry, index of the element): on
+ *   average the state is the value itself, to 2^-16 of a code's step, so that
+ *   changes smaller than half a code (a decay of v by 1 - b2) are not lost. A
+ *   sqrt(v) below the smallest code (2^-9) is stored as that code each time.
+ *   Ignored for 32 bits.
  *   A NaN in g makes its element NaN; an infinite g makes its run of 256 NaN
  *   (rdt_clip_scale's nonfinite flag, passed as skip_flag, prevents both).
  * ------------------------------------------------------------------------- */

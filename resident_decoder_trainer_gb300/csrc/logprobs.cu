@@ -1088,8 +1088,7 @@ int head_rows(int64_t tokens, int64_t vocab) {
 
 struct HeadScratch {
   bf16* hn;
-  float *rstd, *logits, *split;
-  int64_t split_floats;
+  float *rstd, *logits;
   size_t bytes;
 };
 HeadScratch head_scratch(const rdt_config* c, int tokens, void* ws) {
