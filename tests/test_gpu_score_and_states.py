@@ -278,6 +278,88 @@ def test_a_policy_step_of_a_linear_head(bits):
         assert torch.equal(wb, w.bfloat16())
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_behind_events_of_another_stream(captured):
+    """Each call follows one of its own kind in its stream and an event of a second stream, whose
+    kernels, still running when the call is launched, write what it reads; eager and captured."""
+    rows, vocab, sizes = 200, 5003, [300, 5, 2048] * 140
+    gen = torch.Generator(device="cuda").manual_seed(20)
+    z0 = torch.randn(rows, vocab, generator=gen, device="cuda")
+    tg = torch.randint(0, vocab, (rows,), generator=gen, device="cuda", dtype=torch.int32)
+    big = torch.randn(4096, 4096, generator=gen, device="cuda")
+    p = tensors.Problem(sizes, 8, seed=21)
+    g0 = p.g.buf.clone()
+    lst, f = p.list(), lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
+    ws = torch.empty(rdt.tensors_sq_sum_workspace_bytes(lst), dtype=torch.uint8, device="cuda")
+    sumsq, scale = torch.zeros(1, dtype=torch.float64, device="cuda"), f(1)
+    z, d, slow = f(rows, vocab), f(rows, vocab), f(4096, 4096)
+    out = dict(logp=f(rows), entropy=f(rows), lse=f(rows), stats=f(rows, 2))
+    up, side = torch.ones(rows, device="cuda"), torch.cuda.Stream()
+
+    def behind(write):
+        """Runs `write` on the second stream behind a long kernel; this stream waits for it."""
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.mm(big, big, out=slow)
+            write()
+        torch.cuda.current_stream().wait_stream(side)
+
+    def calls():
+        rdt.token_logprobs(z, targets=tg, **out)
+        behind(lambda: torch.mul(z0, 2.0, out=z))
+        rdt.token_logprobs(z, targets=tg, **out)
+        behind(lambda: torch.mul(out["logp"], -0.1, out=up))
+        rdt.token_logprobs_backward(z, tg, out["stats"], d, d_logp=up)
+        behind(lambda: torch.mul(g0, 0.5, out=p.g.buf))
+        rdt.tensors_sq_sum(lst, sumsq, ws)
+        behind(lambda: torch.rsqrt(sumsq, out=sumsq))
+        scale.copy_(sumsq)
+        rdt.tensors_adamw(lst, 2, 0.9, 0.95, 1e-8, scale=scale, seed=1)
+        behind(lambda: scale.mul_(0.5))
+        rdt.tensors_adamw(lst, 3, 0.9, 0.95, 1e-8, scale=scale, seed=1)
+
+    old = p.snapshot()
+    calls()
+    torch.cuda.synchronize()
+    # one by one, with nothing under way
+    ref = {k: torch.zeros_like(x) for k, x in out.items()}
+    d_ref = f(rows, vocab)
+    rdt.token_logprobs(z0 * 2.0, targets=tg, **ref)
+    torch.cuda.synchronize()
+    rdt.token_logprobs_backward(z0 * 2.0, tg, ref["stats"], d_ref, d_logp=ref["logp"] * -0.1)
+    q = tensors.Problem(sizes, 8, seed=21)
+    q.g.buf.copy_(g0 * 0.5)
+    total = torch.zeros(1, dtype=torch.float64, device="cuda")
+    torch.cuda.synchronize()
+    rdt.tensors_sq_sum(q.list(), total, ws)
+    torch.cuda.synchronize()
+    s1 = total.rsqrt().float()
+    for step, s in ((2, s1), (3, s1 * 0.5)):
+        rdt.tensors_adamw(q.list(), step, 0.9, 0.95, 1e-8, scale=s, seed=1)
+        torch.cuda.synchronize()
+
+    def check():
+        assert all(torch.equal(out[k], ref[k]) for k in ref) and torch.equal(d, d_ref)
+        for k in ("w", "m", "v", "ms", "vs", "wb"):
+            assert torch.equal(getattr(p, k).buf, getattr(q, k).buf), k
+
+    check()
+    if not captured:
+        return
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for _ in range(2):
+        for k, parts in old.items():
+            for a, b in zip(getattr(p, k).parts, parts):
+                a.copy_(b)
+        for x in (z, d, p.g.buf, *out.values()):
+            x.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        check()
+
+
 @pytest.mark.parametrize("bits,seed", [(32, None), (8, None), (8, 9)])
 def test_the_updates_of_three_policy_steps(bits, seed):
     """The steps above, with every update checked: weight and bias, their moments (codes and
