@@ -481,11 +481,12 @@ rdt_status rdt_head_logprobs(const rdt_config* cfg, int32_t tokens, const float*
  * call writes (entries whose w overlap are rejected).
  *
  * rdt_tensors_sq_sum: *sumsq = sum over all g of g^2, relative error
- *   below 1e-12 where each square is 0 or at least 1e-30 and the sum at most
- *   1e38 (it is formed in fp32 with the rounding errors kept; a larger one may
- *   come out as not finite); order of summation fixed by the sizes. Only g and n of each entry are read. For
- *   rdt_clip_scale. ws: rdt_tensors_sq_sum_workspace_bytes(tensors, count)
- *   bytes, 8-byte aligned.
+ *   below 1e-12, for any number of values, where each square is 0 or at least
+ *   1e-30 and the sum at most 1e38 (it is formed in fp32 with the rounding
+ *   errors kept; a larger one may come out as not finite); order of summation
+ *   fixed by the sizes. Only g and n of each entry are read, so entries may
+ *   share memory here. For rdt_clip_scale. ws:
+ *   rdt_tensors_sq_sum_workspace_bytes(tensors, count) bytes, 8-byte aligned.
  *
  * rdt_tensors_adamw, step t (>= 1, or *step_dev), each operation rounded to
  * fp32 in this order (the quotient by a reciprocal, relative error below

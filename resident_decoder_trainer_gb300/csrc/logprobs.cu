@@ -4,8 +4,10 @@
 //
 // Bound by DRAM where rows are many: the logits are read once, in the gradient
 // written once. Measured, of the copy bandwidth: 4096 bf16 rows of 151,936
-// 191 us (0.96), 1024 fp32 rows with 20 alternatives 99 us (0.92), gradient of
-// 4096 bf16 rows 367 us (1.00). One row is bound by latency and the host: 9 us.
+// 193 us (0.95), 1024 fp32 rows with 20 alternatives 101 us (0.91), gradient of
+// 4096 bf16 rows 366 us (1.00). One row is bound by latency and the host: 9 us;
+// rows of a few thousand logits by each CTA's start, joins and selection (8192
+// bf16 rows of 4096: 17 us, 40 with 20 alternatives, 9.9 for the bytes).
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -847,8 +849,9 @@ cudaError_t launch_logprobs(const LogprobArgs& a, int split, cudaStream_t s) {
   }
   cudaLaunchAttribute at[2];
   // CTAs that wait already sit where there was room, some SMs full and some not; long rows in
-  // one or two waves lose by that (1024 fp32 rows of 151,936: 105 us for 101) what small calls
-  // and many waves win (2 us).
+  // one or two waves lose by that (1024 rows of 151,936, 20 alternatives: fp32 105 us for 101,
+  // bf16 71 for 64) what small calls and many waves win (2 us). Some that the rule leaves out
+  // would win as well (2048 bf16 rows of 32,000: 35 us for 38).
   const int64_t bytes = static_cast<int64_t>(a.rows) * a.vocab * sizeof(T);
   at[0] = overlapping_launch(bytes <= (64 << 20) || a.rows >= 24 * num_sms());
   at[1].id = cudaLaunchAttributeClusterDimension;
@@ -890,7 +893,10 @@ cudaError_t logprobs_of(LogprobArgs a, cudaStream_t s) {
   // Of 128 threads an SM holds 7 CTAs with three groups in shared memory and 9 with two. Up to 6
   // rows an SM want the three (760 fp32 rows: 81 us, 86 with two), one wave of more the two (1024
   // rows: 106, 113 with three; 1216 rows: 121 and 153), and several waves whichever leaves less of
-  // the last one empty (2048 rows: 226 and 205; 2432 rows: 234 and 252).
+  // the last one empty (2048 rows: 226 and 205; 2432 rows: 234 and 252). bf16 rows of 151,936, two
+  // and three: 760 rows 51 and 48, 1024 rows 63 and 67, 1216 rows 72 and 86, 2048 rows 122 and 116,
+  // 2432 rows 132 and 135, but 4096 rows 212 and 204; of 32,000: 760 rows 22 and 19, 1216 rows 24
+  // and 29, but 1024 rows 23 and 20.
   const int deep = (a.rows - 1) / sms + 1;  // rows an SM
   const bool two = deep > 6 && (deep <= 9 || (deep + 8) / 9 * 9 <= (deep + 6) / 7 * 7);
   return two ? launch_logprobs<T, 128, 2, true>(a, 1, s) : launch_logprobs<T, 128, 3, true>(a, 1, s);

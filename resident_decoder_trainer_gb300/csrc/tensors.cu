@@ -6,8 +6,8 @@
 // Both are bound by DRAM: each value is read and written once. Measured, of the
 // copy bandwidth: squared sum of 490 M fp32 gradients 275 us (1.05), AdamW with
 // 32-bit states of a 101 M block 437 us (1.02), with 8-bit states of 490 M
-// 1317 us rounded at random (0.99; 0.88 with bf16 gradients, where the 91
-// instructions an element weigh more).
+// 1326 us rounded at random (0.98; 0.88 with bf16 gradients, where the 91
+// instructions an element weigh more), 1360 us with the step on the device.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
