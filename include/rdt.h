@@ -540,6 +540,106 @@ rdt_status rdt_tensors_adamw(const rdt_opt_tensor* tensors, int32_t count, int32
                              const int32_t* skip_flag, int32_t step, const int32_t* step_dev,
                              float beta1, float beta2, float eps, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Attention for packed documents, prompts, windows and single tokens, and the
+ * per-head norm with rotation that feeds it. The block calls above do both for
+ * a dense batch of causal sequences of equal length, at positions 0, 1, ...;
+ * here every token has positions of its own and every query a span of keys.
+ *
+ * A tensor of heads is [tokens, heads, head_dim] with the head_dim values
+ * contiguous: element (t, h, i) at data + t token_stride + h head_stride + i,
+ * strides in elements, at least head_dim, multiples of 16 bytes, data 16-byte
+ * aligned. So q, k and v may lie together as a projection wrote them, or head
+ * by head. The stride of an axis with one element is not looked at.
+ * ------------------------------------------------------------------------- */
+typedef struct rdt_heads {
+  void* data;
+  int64_t token_stride;
+  int64_t head_stride;
+} rdt_heads;
+
+/* rdt_qk_norm_rope: for every head of q and k, with x its head_dim values,
+ *   n = x / sqrt(mean(x^2) + eps) gain                 (gain null: n = x)
+ *   out_i = n_i cos a - n_{i+d/2} sin a,  out_{i+d/2} = n_{i+d/2} cos a + n_i sin a,
+ *   a = positions[axis(i)][t] theta^(-2i / head_dim)    (positions null: out = n)
+ * in fp32, rounded once to out_dtype. positions int32 [axes, tokens], any
+ * value; axes in [1, 4]. sections is a HOST array of `axes` counts that add up
+ * to head_dim / 2: the first sections[0] pairs turn by axis 0, the next
+ * sections[1] by axis 1, and so on; null with one axis. Angles are exact to
+ * 2^-31 of a half turn, however far the position.
+ * head_dim a multiple of 16 in [16, 256]; n_heads and n_kv_heads in [0, 4096],
+ * not both 0 (a tensor without heads is not looked at and may be null);
+ * gain_q, gain_k fp32 [head_dim]; eps >= 0; theta > 0. tokens may be 0.
+ * An output may be its input itself (same address, type and strides), else
+ * outputs overlap neither inputs nor each other.
+ *
+ * rdt_qk_norm_rope_backward: gradients with respect to q, k and the gains from
+ * d_q_out and d_k_out (of type d_dtype); q and k are the forward's inputs. dq
+ * and dk of type out_dtype; they may be q and k, or d_q_out and d_k_out,
+ * themselves. d_gain_q and d_gain_k fp32 [head_dim], each may be null, = or
+ * (accumulate != 0) += the sum over tokens and heads, its order fixed by the
+ * sizes. ws: rdt_qk_norm_rope_backward_workspace_bytes() bytes, 256-byte
+ * aligned; not looked at when neither gain gradient is wanted. */
+rdt_status rdt_qk_norm_rope(int32_t tokens, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                            const rdt_heads* q, const rdt_heads* k, int32_t dtype,
+                            const float* gain_q, const float* gain_k, float eps,
+                            const int32_t* positions, int32_t axes, const int32_t* sections,
+                            float theta, const rdt_heads* q_out, const rdt_heads* k_out,
+                            int32_t out_dtype, void* stream);
+size_t rdt_qk_norm_rope_backward_workspace_bytes(int32_t tokens, int32_t n_heads,
+                                                 int32_t n_kv_heads, int32_t head_dim);
+rdt_status rdt_qk_norm_rope_backward(int32_t tokens, int32_t n_heads, int32_t n_kv_heads,
+                                     int32_t head_dim, const rdt_heads* q, const rdt_heads* k,
+                                     int32_t dtype, const float* gain_q, const float* gain_k,
+                                     float eps, const int32_t* positions, int32_t axes,
+                                     const int32_t* sections, float theta,
+                                     const rdt_heads* d_q_out, const rdt_heads* d_k_out,
+                                     int32_t d_dtype, const rdt_heads* dq, const rdt_heads* dk,
+                                     int32_t out_dtype, float* d_gain_q, float* d_gain_k,
+                                     int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/* rdt_attention: query t sees the keys j with lo[t] <= j < hi[t] (and
+ * 0 <= j < keys). For every query head h, which reads kv head h / (n_heads /
+ * n_kv_heads),
+ *   s_j = scale q_t . k_j,  and with softcap > 0  s_j = softcap tanh(s_j / softcap)
+ *   o_t = sum_j p_j v_j,  p = softmax of the s_j it sees,  lse_t = ln sum_j exp(s_j).
+ * A query that sees nothing has o = 0 and lse = -inf. Spans give a causal
+ * batch, packed documents, a prompt that is seen whole, a sliding window, or
+ * new tokens against a cache: any mask in which a query sees a run of keys.
+ * lo and hi int32 [queries], device memory; lo null: 0, hi null: keys.
+ * What a query does not see does not reach its results, whatever it holds.
+ * The cost goes by the keys between the least lo and the largest hi of
+ * neighbouring queries, so queries of one document belong together.
+ *
+ * q, k, v, o bf16, head_dim a multiple of 16 in [16, 128]; n_heads a multiple
+ * of n_kv_heads, at most 128 times it, at most 4096; queries and keys in
+ * [0, 2^30]; scale > 0, softcap >= 0 (0: none), both finite. Scores, softmax
+ * and sums are fp32, p is rounded to bf16 for its product with v. lse fp32
+ * [queries, n_heads], natural logarithm; may be null. Outputs overlap nothing
+ * else. ws: rdt_attention_workspace_bytes(..., 0) bytes, 256-byte aligned (may
+ * be 0 bytes). Results do not depend on scheduling.
+ *
+ * rdt_attention_backward: gradients of sum(d_o o) + sum(d_lse lse) with
+ * respect to q, k and v, those of k and v summed over the query heads that
+ * share them, each rounded once to bf16. o and lse as rdt_attention wrote
+ * them; d_o bf16, d_lse fp32 [queries, n_heads] or null. Rows that nothing
+ * sees or that see nothing get zeros. ws:
+ * rdt_attention_workspace_bytes(..., 1) bytes, 256-byte aligned. */
+size_t rdt_attention_workspace_bytes(int32_t queries, int32_t keys, int32_t n_heads,
+                                     int32_t n_kv_heads, int32_t head_dim, int32_t backward);
+rdt_status rdt_attention(int32_t queries, int32_t keys, int32_t n_heads, int32_t n_kv_heads,
+                         int32_t head_dim, const rdt_heads* q, const rdt_heads* k,
+                         const rdt_heads* v, const int32_t* lo, const int32_t* hi, float scale,
+                         float softcap, const rdt_heads* o, float* lse, void* ws, size_t ws_bytes,
+                         void* stream);
+rdt_status rdt_attention_backward(int32_t queries, int32_t keys, int32_t n_heads,
+                                  int32_t n_kv_heads, int32_t head_dim, const rdt_heads* q,
+                                  const rdt_heads* k, const rdt_heads* v, const rdt_heads* o,
+                                  const float* lse, const rdt_heads* d_o, const float* d_lse,
+                                  const int32_t* lo, const int32_t* hi, float scale, float softcap,
+                                  const rdt_heads* dq, const rdt_heads* dk, const rdt_heads* dv,
+                                  void* ws, size_t ws_bytes, void* stream);
+
 /* Thread-local description of the last failure on this thread ("" if none). */
 const char* rdt_last_error(void);
 

@@ -1,0 +1,135 @@
+// What the per-head norm with rotation and the attention over spans share:
+// the checks of a [tokens, heads, head_dim] tensor, launches that overlap, and
+// eight values of any of the three types.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "../../include/rdt.h"
+#include "common.cuh"
+#include "internal.h"
+
+namespace rdt {
+
+// Each kernel of these files may be launched while the one before it in the
+// stream still runs, and waits here for its end before it touches memory
+// (programmatic launch). Nothing is read through the read-only path (__ldg,
+// const __restrict__): that is for memory nobody writes while the kernel is
+// there, and this one may be there while the kernel before it writes.
+__device__ __forceinline__ void after_previous_kernel() {
+  asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Launches `kernel` so that it may start while the stream's previous one ends.
+template <typename... P, typename... A>
+cudaError_t launch_overlapping(void (*kernel)(P...), int64_t grid, int threads, size_t smem,
+                               cudaStream_t s, A... args) {
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  note_launch();
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+inline rdt_status refuse(const char* msg) {
+  set_last_error(msg);
+  return RDT_EINVAL;
+}
+inline rdt_status launched(cudaError_t e) {
+  if (e == cudaSuccess) return RDT_OK;
+  cudaGetLastError();  // not left for the next call to find
+  set_last_error(cudaGetErrorString(e));
+  return RDT_ECUDA;
+}
+
+inline bool dtype_ok(int dtype) {
+  return dtype == RDT_F32 || dtype == RDT_BF16 || dtype == RDT_F16;
+}
+inline int dtype_bytes(int dtype) { return dtype == RDT_F32 ? 4 : 2; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
+// What is wrong with x as a [tokens, heads, d] tensor; null if nothing is. A
+// stride along an axis of one element is not looked at.
+inline const char* heads_problem(const rdt_heads* x, int64_t tokens, int64_t heads, int64_t d,
+                                 int bytes, bool written) {
+  if (!x || !x->data) return "null pointer";
+  const int64_t ts = x->token_stride, hs = x->head_stride;
+  if (reinterpret_cast<uintptr_t>(x->data) & 15) return "tensors must be 16-byte aligned";
+  const int64_t most = (int64_t{1} << 39) / bytes;
+  if ((tokens > 1 && (ts < d || ts > most)) || (heads > 1 && (hs < d || hs > most)))
+    return "strides must be at least head_dim and below 2^39 bytes";
+  if ((tokens > 1 && ts * bytes % 16) || (heads > 1 && hs * bytes % 16))
+    return "strides must be multiples of 16 bytes";
+  if (written && tokens > 1 && heads > 1) {
+    const bool apart = ts >= hs ? ts >= (heads - 1) * hs + d : hs >= (tokens - 1) * ts + d;
+    if (!apart) return "a written tensor overlaps itself";
+  }
+  return nullptr;
+}
+
+// Eight consecutive values, as loaded: 16 bytes of a 16-bit type, 32 of fp32.
+template <typename T>
+struct Eight {
+  uint4 a;
+  __device__ __forceinline__ void load(const T* p) { a = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 2 && !std::is_same<T, __half>::value) {
+        x[2 * i] = bf16lo(w[i]);
+        x[2 * i + 1] = bf16hi(w[i]);
+      } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+      }
+    }
+  }
+};
+template <>
+struct Eight<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+};
+
+// Rounds eight values to the type and stores them at element `at` of `base`.
+__device__ __forceinline__ void store_eight(void* base, int dtype, int64_t at, const float (&x)[8]) {
+  if (dtype == RDT_F32) {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
+    p[0] = make_float4(x[0], x[1], x[2], x[3]);
+    p[1] = make_float4(x[4], x[5], x[6], x[7]);
+    return;
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (dtype == RDT_BF16) {
+      w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+    } else {
+      const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  *reinterpret_cast<uint4*>(static_cast<bf16*>(base) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+}  // namespace rdt

@@ -35,7 +35,9 @@ EXPORTS = (
     "rdt_embedding_forward", "rdt_embedding_backward", "rdt_step_advance", "rdt_wait_probe",
     "rdt_token_logprobs", "rdt_token_logprobs_backward", "rdt_head_logprobs_workspace_bytes",
     "rdt_head_logprobs", "rdt_tensors_sq_sum_workspace_bytes", "rdt_tensors_sq_sum",
-    "rdt_tensors_adamw",
+    "rdt_tensors_adamw", "rdt_qk_norm_rope", "rdt_qk_norm_rope_backward_workspace_bytes",
+    "rdt_qk_norm_rope_backward", "rdt_attention_workspace_bytes", "rdt_attention",
+    "rdt_attention_backward",
 )
 RDT_MAX_TOP = 32  # alternatives per row of token_logprobs
 STATE_RUN = 256  # elements that share one scale of an 8-bit AdamW state
@@ -69,6 +71,12 @@ class OptTensor(ctypes.Structure):
                 ("weight_decay", ctypes.c_float)]
 
 
+class Heads(ctypes.Structure):
+    """rdt_heads: a [tokens, heads, head_dim] tensor by address and strides."""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with "
@@ -76,7 +84,7 @@ def _load() -> ctypes.CDLL:
     lib = ctypes.CDLL(LIB_PATH)
     P, I32, I64, F32, SZ = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float,
                             ctypes.c_size_t)
-    CP = ctypes.POINTER(Config)
+    CP, HP = ctypes.POINTER(Config), ctypes.POINTER(Heads)
     sig = {
         "rdt_check_config": (I32, [CP]),
         "rdt_block_param_count": (I64, [CP]),
@@ -129,6 +137,16 @@ def _load() -> ctypes.CDLL:
         "rdt_tensors_sq_sum_workspace_bytes": (SZ, [P, I32]),
         "rdt_tensors_sq_sum": (I32, [P, I32, I32, P, P, SZ, P]),
         "rdt_tensors_adamw": (I32, [P, I32, I32, I32, I64, P, P, I32, P, F32, F32, F32, P]),
+        "rdt_qk_norm_rope": (I32, [I32, I32, I32, I32, HP, HP, I32, P, P, F32, P, I32, P, F32, HP,
+                                   HP, I32, P]),
+        "rdt_qk_norm_rope_backward_workspace_bytes": (SZ, [I32, I32, I32, I32]),
+        "rdt_qk_norm_rope_backward": (I32, [I32, I32, I32, I32, HP, HP, I32, P, P, F32, P, I32, P,
+                                            F32, HP, HP, I32, HP, HP, I32, P, P, I32, P, SZ, P]),
+        "rdt_attention_workspace_bytes": (SZ, [I32, I32, I32, I32, I32, I32]),
+        "rdt_attention": (I32, [I32, I32, I32, I32, I32, HP, HP, HP, P, P, F32, F32, HP, P, P, SZ,
+                                P]),
+        "rdt_attention_backward": (I32, [I32, I32, I32, I32, I32, HP, HP, HP, HP, P, HP, P, P, P,
+                                         F32, F32, HP, HP, HP, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -416,6 +434,161 @@ def head_logprobs(cfg, h, gamma_f, w_lm, ws, targets=None, logp=None, entropy=No
         None if top_ids is None else _here(top_ids, "top_ids", _I32, (tokens, top), dev),
         None if top_logp is None else _here(top_logp, "top_logp", _F32, (tokens, top), dev),
         *_scratch(ws, "ws", dev), _stream(stream)))
+
+
+# ------------------------------------- per-head norm with rotation, attention over spans
+def _heads(t, what, dtype, shape, device):
+    """rdt_heads of a [tokens, heads, head_dim] tensor, after the checks that the library may
+    be handed it; its own checks of strides and alignment follow there."""
+    if t.get_device() != device:
+        raise ValueError(f"{what} must be on the current CUDA device")
+    if t.dtype != dtype:
+        raise ValueError(f"{what} has type {t.dtype}, not {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    ts, hs, one = t.stride()
+    if one != 1 and shape[2] > 1:
+        raise ValueError(f"the values of a head of {what} must be contiguous")
+    return Heads(t.data_ptr(), ts, hs)
+
+
+def _qk_shapes(q, k):
+    """(tokens, heads, kv heads, head_dim) of the q and k of a norm; one of them may be None."""
+    for t, what in ((q, "q"), (k, "k")):
+        if t is not None and t.dim() != 3:
+            raise ValueError(f"{what} must be [tokens, heads, head_dim]")
+    some = q if q is not None else k
+    if some is None:
+        raise ValueError("neither q nor k is given")
+    tokens, _, d = some.shape
+    if tokens >= 1 << 31:
+        raise ValueError("more than 2^31 - 1 tokens")
+    return tokens, 0 if q is None else q.shape[1], 0 if k is None else k.shape[1], d
+
+
+def _rotation(positions, sections, tokens, device):
+    """Address of positions, number of axes, and the C array of the sections."""
+    if positions is None:
+        return None, 0, None
+    axes = positions.shape[0] if positions.dim() == 2 else 1
+    shape = (axes, tokens) if positions.dim() == 2 else (tokens,)
+    ptr = _here(positions, "positions", _I32, shape, device)
+    if sections is None:
+        return ptr, axes, None
+    if len(sections) != axes:
+        raise ValueError(f"{len(sections)} sections for {axes} axes")
+    return ptr, axes, (ctypes.c_int32 * axes)(*sections)
+
+
+def _gain(t, what, d, device):
+    return None if t is None else _here(t, what, _F32, (d,), device)
+
+
+def qk_norm_rope(q, k, q_out, k_out, gain_q=None, gain_k=None, eps=1e-6, positions=None,
+                 sections=None, theta=1e6, stream=None):
+    """RMSNorm of every head of q and k and the rotation at given positions, in one pass
+    (rdt_qk_norm_rope). q [tokens, heads, head_dim], k [tokens, kv heads, head_dim], fp32, bf16
+    or fp16, any strides of tokens and heads that are multiples of 16 bytes; q_out and k_out
+    likewise, of a type of their own, or q and k themselves. q with q_out, or k with k_out, may
+    be None. gain fp32 [head_dim], None: no norm. positions int32 [tokens] or [axes, tokens],
+    None: no rotation; sections: pairs of each axis."""
+    tokens, nh, nkv, d = _qk_shapes(q, k)
+    some, some_out = (q, q_out) if q is not None else (k, k_out)
+    dev = _device(some, "q" if q is not None else "k")
+    pos, axes, sec = _rotation(positions, sections, tokens, dev)
+    ins = [None if t is None else _heads(t, n, some.dtype, (tokens, h, d), dev)
+           for t, n, h in ((q, "q", nh), (k, "k", nkv))]
+    outs = [None if src is None else _heads(t, n, some_out.dtype, (tokens, h, d), dev)
+            for src, t, n, h in ((q, q_out, "q_out", nh), (k, k_out, "k_out", nkv))]
+    _check(lib().rdt_qk_norm_rope(
+        tokens, nh, nkv, d, *ins, _DTYPE.get(some.dtype, -1), _gain(gain_q, "gain_q", d, dev),
+        _gain(gain_k, "gain_k", d, dev), eps, pos, axes, sec, theta, *outs,
+        _DTYPE.get(some_out.dtype, -1), _stream(stream)))
+
+
+def qk_norm_rope_backward_workspace_bytes(tokens, n_heads, n_kv_heads, head_dim) -> int:
+    return lib().rdt_qk_norm_rope_backward_workspace_bytes(tokens, n_heads, n_kv_heads, head_dim)
+
+
+def qk_norm_rope_backward(q, k, d_q_out, d_k_out, dq, dk, ws=None, gain_q=None, gain_k=None,
+                          d_gain_q=None, d_gain_k=None, eps=1e-6, positions=None, sections=None,
+                          theta=1e6, accumulate=False, stream=None):
+    """Gradients of qk_norm_rope (rdt_qk_norm_rope_backward): dq and dk, of one type of their
+    own, written over whatever they hold (they may be q and k or d_q_out and d_k_out), and
+    d_gain_q and d_gain_k fp32 [head_dim] where given, overwritten or (accumulate) added to.
+    ws: scratch for the gains' gradients."""
+    tokens, nh, nkv, d = _qk_shapes(q, k)
+    some, grad, out = (q, d_q_out, dq) if q is not None else (k, d_k_out, dk)
+    dev = _device(some, "q" if q is not None else "k")
+    pos, axes, sec = _rotation(positions, sections, tokens, dev)
+
+    def pair(tq, tk, nq, nk, dtype):
+        return [None if src is None else _heads(t, n, dtype, (tokens, h, d), dev)
+                for src, t, n, h in ((q, tq, nq, nh), (k, tk, nk, nkv))]
+
+    _check(lib().rdt_qk_norm_rope_backward(
+        tokens, nh, nkv, d, *pair(q, k, "q", "k", some.dtype), _DTYPE.get(some.dtype, -1),
+        _gain(gain_q, "gain_q", d, dev), _gain(gain_k, "gain_k", d, dev), eps, pos, axes, sec,
+        theta, *pair(d_q_out, d_k_out, "d_q_out", "d_k_out", grad.dtype),
+        _DTYPE.get(grad.dtype, -1), *pair(dq, dk, "dq", "dk", out.dtype),
+        _DTYPE.get(out.dtype, -1), _gain(d_gain_q, "d_gain_q", d, dev),
+        _gain(d_gain_k, "d_gain_k", d, dev), int(bool(accumulate)),
+        *((None, 0) if ws is None else _scratch(ws, "ws", dev)), _stream(stream)))
+
+
+def attention_workspace_bytes(queries, keys, n_heads, n_kv_heads, head_dim, backward=False) -> int:
+    return lib().rdt_attention_workspace_bytes(queries, keys, n_heads, n_kv_heads, head_dim,
+                                               int(bool(backward)))
+
+
+_BF16 = torch.bfloat16
+
+
+def _attention_shapes(q, k):
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k and v must be [tokens, heads, head_dim]")
+    if q.shape[0] >= 1 << 31 or k.shape[0] >= 1 << 31:
+        raise ValueError("more than 2^31 - 1 queries or keys")
+    return q.shape[0], k.shape[0], q.shape[1], k.shape[1], q.shape[2]
+
+
+def attention(q, k, v, o, ws=None, lse=None, lo=None, hi=None, scale=None, softcap=0.0,
+              stream=None):
+    """Attention in which query t sees the keys lo[t] <= j < hi[t] (rdt_attention), written to
+    o and, where given, lse (fp32 [queries, heads]). q, o [queries, heads, head_dim], k, v
+    [keys, kv heads, head_dim], bf16, any strides of tokens and heads that are multiples of 16
+    bytes; lo, hi int32 [queries], None: 0 and keys. scale None: 1 / sqrt(head_dim). softcap >
+    0: scores become softcap tanh(score / softcap). ws: attention_workspace_bytes of scratch."""
+    t, n, nh, nkv, d = _attention_shapes(q, k)
+    dev = _device(q, "q")
+    _check(lib().rdt_attention(
+        t, n, nh, nkv, d, _heads(q, "q", _BF16, (t, nh, d), dev),
+        _heads(k, "k", _BF16, (n, nkv, d), dev), _heads(v, "v", _BF16, (n, nkv, d), dev),
+        None if lo is None else _here(lo, "lo", _I32, (t,), dev),
+        None if hi is None else _here(hi, "hi", _I32, (t,), dev),
+        d ** -0.5 if scale is None else scale, softcap, _heads(o, "o", _BF16, (t, nh, d), dev),
+        None if lse is None else _here(lse, "lse", _F32, (t, nh), dev),
+        *((None, 0) if ws is None else _scratch(ws, "ws", dev)), _stream(stream)))
+
+
+def attention_backward(q, k, v, o, lse, d_o, dq, dk, dv, ws=None, d_lse=None, lo=None, hi=None,
+                       scale=None, softcap=0.0, stream=None):
+    """Gradients of attention with respect to q, k and v, written to dq, dk and dv
+    (rdt_attention_backward); o and lse as attention wrote them, d_lse fp32 [queries, heads] or
+    None, the rest as given there. ws: attention_workspace_bytes(..., backward=True)."""
+    t, n, nh, nkv, d = _attention_shapes(q, k)
+    dev = _device(q, "q")
+    qs, ks = (t, nh, d), (n, nkv, d)
+    _check(lib().rdt_attention_backward(
+        t, n, nh, nkv, d, _heads(q, "q", _BF16, qs, dev), _heads(k, "k", _BF16, ks, dev),
+        _heads(v, "v", _BF16, ks, dev), _heads(o, "o", _BF16, qs, dev),
+        _here(lse, "lse", _F32, (t, nh), dev), _heads(d_o, "d_o", _BF16, qs, dev),
+        None if d_lse is None else _here(d_lse, "d_lse", _F32, (t, nh), dev),
+        None if lo is None else _here(lo, "lo", _I32, (t,), dev),
+        None if hi is None else _here(hi, "hi", _I32, (t,), dev),
+        d ** -0.5 if scale is None else scale, softcap, _heads(dq, "dq", _BF16, qs, dev),
+        _heads(dk, "dk", _BF16, ks, dev), _heads(dv, "dv", _BF16, ks, dev),
+        *((None, 0) if ws is None else _scratch(ws, "ws", dev)), _stream(stream)))
 
 
 # ------------------------------------------------- many tensors: clip and AdamW
