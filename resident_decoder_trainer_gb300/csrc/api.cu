@@ -32,7 +32,9 @@ rdt_status fail(rdt_status st, const char* fmt, ...) {
 // Device error word: bounded waits that give up record a code here.
 __device__ int g_device_error;
 
-int* device_error_ptr() {
+}  // namespace
+
+int* rdt::device_error_ptr() {
   static int* ptrs[64] = {};
   static std::mutex mu;
   int dev = 0;
@@ -45,6 +47,8 @@ int* device_error_ptr() {
   }
   return ptrs[dev];
 }
+
+namespace {
 
 // ---------------------------------------------------------- measurement hooks
 std::atomic<int64_t> g_launches{0};

@@ -1576,6 +1576,23 @@ bool make_tma_2d(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols, in
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_tma_heads(CUtensorMap* m, const void* ptr, int64_t tokens, int64_t heads, int64_t d,
+                    int64_t token_stride, int64_t head_stride, int box_heads, int box_tokens) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  if (heads == 1) head_stride = d;
+  if (tokens == 1) token_stride = d;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads),
+                        static_cast<cuuint64_t>(tokens)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_stride) * 2,
+                           static_cast<cuuint64_t>(token_stride) * 2};
+  cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_tokens)};
+  cuuint32_t es[3] = {1u, 1u, 1u};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box,
+             es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 static bool make_map(CUtensorMap* m, const Mat& x, int box_rows) {
   return make_tma_2d(m, x.ptr, x.rows, x.cols, x.ld, box_rows);
 }

@@ -40,6 +40,13 @@ cudaError_t launch_overlapping(void (*kernel)(P...), int64_t grid, int threads, 
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
+// Lets a kernel have `smem` bytes of dynamic shared memory on the current device.
+template <typename... P>
+cudaError_t allow_smem(void (*kernel)(P...), size_t smem) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(smem));
+}
+
 inline rdt_status refuse(const char* msg) {
   set_last_error(msg);
   return RDT_EINVAL;

@@ -101,6 +101,15 @@ int num_sms();
 bool make_tma_2d(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, int64_t ld,
                  int box_rows);
 
+// 3-D bf16 TMA map over a [tokens, heads, d] tensor (strides in elements; that
+// of an axis with one element is not looked at) with a box of 64 columns x
+// box_heads x box_tokens and 128-byte swizzle. What lies outside reads as 0.
+bool make_tma_heads(CUtensorMap* map, const void* ptr, int64_t tokens, int64_t heads, int64_t d,
+                    int64_t token_stride, int64_t head_stride, int box_heads, int box_tokens);
+
+// The current device's error word; null where it cannot be had.
+int* device_error_ptr();
+
 // Sets the thread-local message returned by rdt_last_error().
 void set_last_error(const char* msg);
 

@@ -1,0 +1,570 @@
+// Forward pass of the attention over spans of keys on the 5th-generation
+// tensor cores: S = Q K^T and O += P V by tcgen05.mma with accumulators in
+// TMEM, operands by TMA, softmax in registers.
+//
+// A CTA walks work items, one item being two tiles (A, B) of 128 rows of one
+// key head (spans.cuh) that share their K and V tiles of 128 keys. The key
+// tiles start at the least key that a row of the item sees, wherever that is.
+// Warps: 0 loads (and finds each item's spans, a few items ahead of the
+// others), 1 issues the MMAs, 4-7 and 8-11 are the softmax of tile A and B,
+// one thread a row. The MMA warp interleaves
+//   S_A(0) S_B(0) | PV_A(0) S_A(1) | PV_B(0) S_B(1) | PV_A(1) ...
+// so that one tile's products run while the other's softmax does. P (bf16) is
+// written over its S in TMEM and read from there; its first 64 keys are handed
+// over while the exponentials of the others are formed. O is rescaled only
+// when a row's maximum grows by more than 2^8.
+//
+// A row whose O is not finite is computed again key by key (row_forward): a NaN
+// or infinity in a value that the row does not see, times p = 0, would reach it.
+#include <algorithm>
+#include <atomic>
+
+#include "spans.cuh"
+
+namespace rdt {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kThreads = 384;
+constexpr float kRescaleLog2 = 8.f;
+constexpr int kItemRing = 4;
+constexpr int kItemReaders = 1 + 8;  // MMA thread, softmax warps
+
+// What the loading warp found out about an item.
+struct Item {
+  int first;     // first key of key tile 0
+  int n;         // key tiles, of both row tiles together
+  int begin[2];  // key tiles [begin, end) of each row tile; begin == end: none
+  int end[2];
+};
+
+struct Args {
+  SpanArgs a;
+  Tiling tl;
+  int pairs, splits;
+  int64_t items;
+  float to_tanh;     // scale / cap
+  float scale_log2;  // of what is exponentiated: scale log2 e, or cap log2 e
+  float* part_o;     // splits > 1: fp32 [splits][queries][nh][d] and lse (base 2)
+  float* part_lse;
+  int* err;
+};
+
+template <int D>
+struct Cfg {
+  static constexpr int BM = 128, BN = 128;
+  static constexpr uint32_t CHUNK = 128 * 128;  // 64 columns x 128 rows of bf16
+  static constexpr uint32_t TILE = 128 * D * 2;
+  static constexpr int KS = D == 128 ? 2 : 4, VS = KS;
+  static constexpr uint32_t OFF_Q = 0, OFF_K = OFF_Q + 2 * TILE, OFF_V = OFF_K + KS * TILE,
+                            OFF_MEM = OFF_V + VS * TILE,  // 8 warps x kMaxDim floats
+      OFF_ITEM = OFF_MEM + 8 * kMaxDim * 4, OFF_BAR = OFF_ITEM + kItemRing * sizeof(Item);
+  static constexpr size_t SMEM = OFF_BAR + 512 + 1024;
+  static constexpr uint32_t TMEM_S = 0, TMEM_O = 256, TMEM_COLS = 512;
+  static_assert(TMEM_O + 2 * D <= TMEM_COLS && SMEM <= 232448 && OFF_BAR % 8 == 0, "");
+};
+
+// sv = tanh(to_tanh sv) of 1 - 2 / (1 + e^2x): off by a few 2^-23.
+__device__ __forceinline__ void tanh_all(uint32_t (&sv)[128], float to_tanh) {
+  const float w = 2.f * kLog2e * to_tanh;
+#pragma unroll
+  for (int c = 0; c < 128; ++c)
+    sv[c] = __float_as_uint(
+        fmaf(-2.f, rcp_approx(1.f + ex2_approx(__uint_as_float(sv[c]) * w)), 1.f));
+}
+
+template <int D, bool CAP>
+__global__ void __launch_bounds__(kThreads, 1)
+    spans_forward_kernel(const __grid_constant__ CUtensorMap tq,
+                         const __grid_constant__ CUtensorMap tk,
+                         const __grid_constant__ CUtensorMap tv, const __grid_constant__ Args ar) {
+  using C = Cfg<D>;
+  constexpr int BM = C::BM, BN = C::BN, KS = C::KS, VS = C::VS;
+  const SpanArgs& a = ar.a;
+  int* err = ar.err;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + C::OFF_BAR;
+  const uint32_t q_full = bar0, q_empty = bar0 + 8, k_full = bar0 + 16, k_empty = k_full + 8 * KS,
+                 v_full = k_empty + 8 * KS, v_empty = v_full + 8 * VS, s_full = v_empty + 8 * VS,
+                 p_full = s_full + 16,  // [tile][half]
+      o_done = p_full + 32, o_free = o_done + 16, item_full = o_free + 16,
+                 item_empty = item_full + 8 * kItemRing, drain = item_empty + 8 * kItemRing;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 448);
+  static_assert(8 * (2 + 2 * KS + 2 * VS + 2 + 4 + 2 + 2 + 2 * kItemRing + 1) <= 448, "");
+  Item* ring = reinterpret_cast<Item*>(smem + C::OFF_ITEM);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int chunks = (a.d + 63) / 64;
+  // item -> pair (the last queries, whose spans are often the longest, first), key head, split
+  auto place = [&](int64_t item, int& t0, int& g, int& split) {
+    split = static_cast<int>(item % ar.splits);
+    const int64_t x = item / ar.splits;
+    g = static_cast<int>(x % a.nkv);
+    t0 = (ar.pairs - 1 - static_cast<int>(x / a.nkv)) * 2 * ar.tl.per;
+  };
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int x = 0; x < KS; ++x) {
+      mbar_init(k_full + 8 * x, 1);
+      mbar_init(k_empty + 8 * x, 1);
+      mbar_init(v_full + 8 * x, 1);
+      mbar_init(v_empty + 8 * x, 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(s_full + 8 * x, 1);
+      mbar_init(p_full + 16 * x, 128);
+      mbar_init(p_full + 16 * x + 8, 128);
+      mbar_init(o_done + 8 * x, 1);
+      mbar_init(o_free + 8 * x, 128);
+    }
+    for (int x = 0; x < kItemRing; ++x) {
+      mbar_init(item_full + 8 * x, 1);
+      mbar_init(item_empty + 8 * x, kItemReaders);
+    }
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tq);
+    tma_prefetch_desc(&tk);
+    tma_prefetch_desc(&tv);
+  }
+  if (warp == 1) tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  after_previous_kernel();
+
+  if (warp < 4) {
+    regs_dec<88>();
+    if (warp == 0) {
+      // ------------------------------------------------------- producer
+      bool ok = true;
+      int jg = 0, loaded = 0;  // key tiles and items with any so far
+      int it = 0;
+      for (int64_t item = blockIdx.x; item < ar.items && ok; item += gridDim.x, ++it) {
+        int t0, g, split;
+        place(item, t0, g, split);
+        int lo[2], hi[2];
+        span_of_queries(a, t0, t0 + ar.tl.per, lo[0], hi[0]);
+        span_of_queries(a, t0 + ar.tl.per, t0 + 2 * ar.tl.per, lo[1], hi[1]);
+        Item d;
+        d.first = lo[0] >= hi[0] ? lo[1] : lo[1] >= hi[1] ? lo[0] : min(lo[0], lo[1]);
+        const int all = (max(hi[0], hi[1]) - d.first + BN - 1) / BN;
+        const int from = static_cast<int>(static_cast<int64_t>(all) * split / ar.splits);
+        const int to = static_cast<int>(static_cast<int64_t>(all) * (split + 1) / ar.splits);
+        d.first += from * BN;
+        d.n = to - from;
+        for (int x = 0; x < 2; ++x) {
+          d.begin[x] = max(0, (lo[x] - d.first) / BN);
+          d.end[x] = min(d.n, (hi[x] - d.first + BN - 1) / BN);
+          if (lo[x] >= hi[x] || hi[x] <= d.first || d.begin[x] >= d.end[x])
+            d.begin[x] = d.end[x] = 0;
+        }
+        if (d.end[0] == 0 && d.end[1] == 0) d.n = 0;
+        const int slot = it % kItemRing;
+        ok = warp_wait(item_empty + 8 * slot, ((it / kItemRing) & 1) ^ 1, err);
+        if (!ok) break;
+        if (lane == 0) {
+          ring[slot] = d;
+          mbar_arrive(item_full + 8 * slot);
+        }
+        if (d.n == 0) continue;
+        if (lane == 0) {
+          ok = mbar_wait(q_empty, (loaded & 1) ^ 1, err);
+          if (ok) {
+            mbar_arrive_expect_tx(q_full, 2 * chunks * (ar.tl.per * a.rep * 128));
+            for (int x = 0; x < 2; ++x)
+              for (int c = 0; c < chunks; ++c)
+                tma_load_3d(sbase + C::OFF_Q + x * C::TILE + c * C::CHUNK, &tq, q_full, c * 64,
+                            g * a.rep, t0 + x * ar.tl.per);
+          }
+          auto load = [&](int j, uint32_t full, uint32_t empty, int stages, uint32_t off,
+                          const CUtensorMap* map) -> bool {
+            const int jj = jg + j, st = jj % stages;
+            if (!mbar_wait(empty + 8 * st, ((jj / stages) & 1) ^ 1, err)) return false;
+            mbar_arrive_expect_tx(full + 8 * st, chunks * C::CHUNK);
+            for (int c = 0; c < chunks; ++c)
+              tma_load_3d(sbase + off + st * C::TILE + c * C::CHUNK, map, full + 8 * st, c * 64, g,
+                          d.first + j * BN);
+            return true;
+          };
+          for (int j = 0; j < KS - 1 && j < d.n && ok; ++j)
+            ok = load(j, k_full, k_empty, KS, C::OFF_K, &tk);
+          for (int j = 0; j < d.n && ok; ++j) {
+            if (j + KS - 1 < d.n) ok = load(j + KS - 1, k_full, k_empty, KS, C::OFF_K, &tk);
+            if (ok) ok = load(j, v_full, v_empty, VS, C::OFF_V, &tv);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0);
+        jg += d.n;
+        ++loaded;
+      }
+    } else if (warp == 1 && lane == 0) {
+      // ------------------------------------------------------------ MMA
+      constexpr uint32_t idesc_s = idesc_bf16_f32(BM, BN, 0, 0);
+      const uint32_t idesc_o = idesc_bf16_f32(BM, a.d, 0, 1);
+      const int ksteps = a.d / 16;
+      bool ok = true;
+      int jg = 0, loaded = 0, it = 0;
+      int pv[2] = {0, 0}, rounds[2] = {0, 0};  // P V issued; items with any, of each tile
+      for (int64_t item = blockIdx.x; item < ar.items && ok; item += gridDim.x, ++it) {
+        const int slot = it % kItemRing;
+        if (!mbar_wait(item_full + 8 * slot, (it / kItemRing) & 1, err)) break;
+        const Item d = ring[slot];
+        mbar_arrive(item_empty + 8 * slot);
+        if (d.n == 0) continue;
+        auto active = [&](int x, int j) { return j >= d.begin[x] && j < d.end[x]; };
+        auto issue_s = [&](int x, int j) {
+          const uint32_t kb = sbase + C::OFF_K + ((jg + j) % KS) * C::TILE;
+          const uint32_t qb = sbase + C::OFF_Q + x * C::TILE;
+          const uint64_t kd = sdesc_sw128(kb, 16, 1024), qd = sdesc_sw128(qb, 16, 1024);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            if (k >= ksteps) break;
+            const uint32_t off = ((k >> 2) * C::CHUNK + (k & 3) * 32) >> 4;
+            tc_mma_bf16(tmem + C::TMEM_S + x * BN, qd + off, kd + off, idesc_s, k > 0);
+          }
+          tc_commit(s_full + 8 * x);
+        };
+        auto wait_k = [&](int j) -> bool {
+          const int jj = jg + j;
+          if (!mbar_wait(k_full + 8 * (jj % KS), (jj / KS) & 1, err)) return false;
+          tc_fence_after();
+          return true;
+        };
+        auto issue_pv = [&](int x, int j) -> bool {
+          const int jj = jg + j, vs = jj % VS;
+          if (j == d.begin[x] && !mbar_wait(o_free + 8 * x, (rounds[x] & 1) ^ 1, err))
+            return false;
+          const uint64_t vd = sdesc_sw128(sbase + C::OFF_V + vs * C::TILE, C::CHUNK, 1024);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            if (!mbar_wait(p_full + 16 * x + 8 * half, pv[x] & 1, err)) return false;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 4 * half; k < 4 * half + 4; ++k)
+              tc_mma_bf16_ts(tmem + C::TMEM_O + x * D, tmem + C::TMEM_S + x * BN + k * 8,
+                             vd + k * 128, idesc_o, j > d.begin[x] || k > 0);
+          }
+          ++pv[x];
+          if (j + 1 == d.end[x]) {
+            tc_commit(o_done + 8 * x);
+            ++rounds[x];
+          }
+          return true;
+        };
+        ok = mbar_wait(q_full, loaded & 1, err) && wait_k(0);
+        if (!ok) break;
+        for (int x = 0; x < 2; ++x)
+          if (active(x, 0)) issue_s(x, 0);
+        tc_commit(k_empty + 8 * (jg % KS));
+        if (d.n == 1) tc_commit(q_empty);
+        for (int j = 0; j < d.n && ok; ++j) {
+          // waited for even where no row tile reads it: its place is free only once it is there
+          ok = mbar_wait(v_full + 8 * ((jg + j) % VS), ((jg + j) / VS) & 1, err);
+          for (int x = 0; x < 2 && ok; ++x) {
+            if (active(x, j)) ok = issue_pv(x, j);
+            if (ok && j + 1 < d.n) {
+              if (x == 0) ok = wait_k(j + 1);
+              if (ok && active(x, j + 1)) issue_s(x, j + 1);
+            }
+          }
+          if (!ok) break;
+          tc_commit(v_empty + 8 * ((jg + j) % VS));
+          if (j + 1 < d.n) {
+            tc_commit(k_empty + 8 * ((jg + j + 1) % KS));
+            if (j + 2 == d.n) tc_commit(q_empty);  // the item's last Q K^T
+          }
+        }
+        jg += d.n;
+        ++loaded;
+      }
+      tc_commit(drain);
+      mbar_wait(drain, 0, nullptr);
+    }
+  } else {
+    regs_inc<208>();
+    // --------------------------------- softmax: one row a thread
+    const int x = (warp - 4) >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lane_base + C::TMEM_S + x * BN;
+    const uint32_t t_o = tmem + lane_base + C::TMEM_O + x * D;
+    float* mem = reinterpret_cast<float*>(smem + C::OFF_MEM) + (warp - 4) * kMaxDim;
+    const int row_t = row / a.rep, row_h = row % a.rep;
+    const float2 sc2 = make_float2(ar.scale_log2, ar.scale_log2);
+    bool ok = true;
+    int jx = 0, rounds = 0, it = 0;
+    for (int64_t item = blockIdx.x; item < ar.items && ok; item += gridDim.x, ++it) {
+      int t0, g, split;
+      place(item, t0, g, split);
+      const int t = t0 + x * ar.tl.per + row_t, h = g * a.rep + row_h;
+      const bool real = row_t < ar.tl.per && t < a.queries;
+      int lo = 0, hi = INT32_MAX;  // a row that is none needs no mask
+      if (real) a.span(t, lo, hi);
+      const int slot = it % kItemRing;
+      if (!warp_wait(item_full + 8 * slot, (it / kItemRing) & 1, err)) break;
+      const int first = ring[slot].first, begin = ring[slot].begin[x], end = ring[slot].end[x];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(item_empty + 8 * slot);
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int j = begin; j < end; ++j, ++jx) {
+        if (!warp_wait(s_full + 8 * x, jx & 1, err)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t sv[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          tmem_ld32(ts + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * c]));
+        tmem_ld_wait();
+        if constexpr (CAP) tanh_all(sv, ar.to_tanh);
+        // columns l <= c < r are seen by this row
+        const int base = first + j * BN;
+        const int l = lo - base, r = hi - base;
+        if (__any_sync(0xffffffffu, l > 0 || r < BN)) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c < l || c >= r) sv[c] = __float_as_uint(-INFINITY);
+        }
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 128; c += 2)
+          m4[(c >> 1) & 3] =
+              max3(m4[(c >> 1) & 3], __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+        const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * ar.scale_log2;
+        float alpha = 1.f;
+        if (mx > m_run + kRescaleLog2) {
+          alpha = m_run == -INFINITY ? 1.f : ex2_approx(m_run - mx);  // nothing summed: as it is
+          m_run = mx;
+        }
+        if (__any_sync(0xffffffffu, alpha != 1.f)) {
+          // the products so far have completed: the scores were issued after them
+#pragma unroll 1
+          for (int c = 0; c < a.d; c += 16) {
+            uint32_t ov[16];
+            tmem_ld16(t_o + c, ov);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+            tmem_st16(t_o + c, ov);
+          }
+        }
+        const float nm = m_run == -INFINITY ? 0.f : -m_run;
+        const float2 nm2 = make_float2(nm, nm);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+          for (int c = 64 * half; c < 64 * half + 64; c += 2) {
+            float2 p = fma2(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), sc2,
+                            nm2);
+            p.x = ex2_approx(p.x);
+            p.y = ex2_approx(p.y);
+            sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], p);
+            sv[c / 2] = pack_bf16x2(p.x, p.y);
+          }
+          // 64 keys as 32 bf16 pairs over the first columns of S
+          tmem_st32(ts + 32 * half, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * half]));
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(p_full + 16 * x + 8 * half);
+        }
+        const float2 two = add2(sum[0], sum[1]);
+        l_run = l_run * alpha + (two.x + two.y);
+      }
+      if (!ok) break;
+      if (begin < end) {
+        if (!warp_wait(o_done + 8 * x, rounds & 1, err)) break;
+        tc_fence_after();
+        ++rounds;
+      }
+      const int64_t th = static_cast<int64_t>(t) * a.nh + h;
+      const float inv = l_run != 0.f ? 1.f / l_run : 0.f;
+      float bad = 0.f;
+#pragma unroll 1
+      for (int c = 0; c < a.d; c += 16) {
+        uint32_t ov[16];
+        if (begin < end) {
+          tmem_ld16(t_o + c, ov);
+          tmem_ld_wait();
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          // a row that saw nothing has p = 0 throughout, but 0 times what was not seen
+          const float v = l_run != 0.f ? __uint_as_float(ov[e]) * inv : 0.f;
+          bad = fmaf(v, 0.f, bad);
+          ov[e] = __float_as_uint(v);
+        }
+        if (real && ar.splits > 1) {
+          float* out = ar.part_o + (static_cast<int64_t>(split) * a.queries * a.nh + th) * a.d + c;
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<uint4*>(out + e) = make_uint4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+        } else if (real) {
+          bf16* out = a.o.at(t, h) + c;
+#pragma unroll
+          for (int e = 0; e < 16; e += 8)
+            *reinterpret_cast<uint4*>(out + e) = make_uint4(
+                pack_bf16x2(__uint_as_float(ov[e]), __uint_as_float(ov[e + 1])),
+                pack_bf16x2(__uint_as_float(ov[e + 2]), __uint_as_float(ov[e + 3])),
+                pack_bf16x2(__uint_as_float(ov[e + 4]), __uint_as_float(ov[e + 5])),
+                pack_bf16x2(__uint_as_float(ov[e + 6]), __uint_as_float(ov[e + 7])));
+        }
+      }
+      if (begin < end) {  // this O is free for the next item
+        tc_fence_before();
+        mbar_arrive(o_free + 8 * x);
+      }
+      const float lse2 = l_run != 0.f ? m_run + log2f(l_run) : -INFINITY;
+      if (real) {
+        if (ar.splits > 1)
+          ar.part_lse[static_cast<int64_t>(split) * a.queries * a.nh + th] = lse2;
+        else if (a.lse)
+          a.lse[th] = lse2 * kLn2;
+      }
+      if (ar.splits == 1) {
+        for (unsigned again = __ballot_sync(0xffffffffu, real && bad != 0.f); again;
+             again &= again - 1) {
+          const int from = __ffs(again) - 1;
+          row_forward(a, mem, __shfl_sync(0xffffffffu, t, from),
+                      __shfl_sync(0xffffffffu, h, from), false);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (err && *reinterpret_cast<volatile int*>(err) != 0) {
+    // after a timed-out wait, copies issued just before may still be landing
+    // in this CTA's shared memory: let them finish before it exits
+    const uint64_t w0 = global_timer_ns();
+    while (global_timer_ns() - w0 < 200000ull) {
+    }
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// Joins the splits of a row: o = sum_s w_s o_s, w_s = 2^(lse_s - lse). One CTA a
+// row, its warps share the splits, a lane has four columns; fixed order.
+constexpr int kJoinWarps = 4;
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ Args ar) {
+  __shared__ float sums[kJoinWarps][kMaxDim];
+  __shared__ float weight[1024];
+  const SpanArgs& a = ar.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t rows = static_cast<int64_t>(a.queries) * a.nh, th = blockIdx.x;
+  after_previous_kernel();
+  float top = -INFINITY;
+  for (int s = lane; s < ar.splits; s += 32) top = fmaxf(top, ar.part_lse[s * rows + th]);
+  top = warp_max(top);
+  float total = 0.f;
+  for (int s = lane; s < ar.splits; s += 32) {
+    const float lse = ar.part_lse[s * rows + th];
+    const float w = lse == -INFINITY ? 0.f : ex2_approx(lse - top);
+    if (warp == 0) weight[s] = w;
+    total += w;
+  }
+  total = warp_sum(total);
+  __syncthreads();
+  float acc[4] = {};
+  if (4 * lane < a.d) {
+    for (int s = warp; s < ar.splits; s += kJoinWarps) {
+      const float w = weight[s];
+      if (w == 0.f) continue;
+      const float4 o =
+          *reinterpret_cast<const float4*>(ar.part_o + (s * rows + th) * a.d + 4 * lane);
+      acc[0] = fmaf(w, o.x, acc[0]);
+      acc[1] = fmaf(w, o.y, acc[1]);
+      acc[2] = fmaf(w, o.z, acc[2]);
+      acc[3] = fmaf(w, o.w, acc[3]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sums[warp][4 * lane + i] = acc[i];
+  }
+  __syncthreads();
+  const int t = static_cast<int>(th / a.nh), h = static_cast<int>(th % a.nh);
+  if (warp) return;
+  bool bad = false;
+  if (4 * lane < a.d) {
+    float o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o[i] = sums[0][4 * lane + i];
+#pragma unroll
+      for (int w = 1; w < kJoinWarps; ++w) o[i] += sums[w][4 * lane + i];
+      o[i] = total != 0.f ? o[i] / total : 0.f;
+      bad |= !(fabsf(o[i]) <= 3e38f);
+    }
+    *reinterpret_cast<uint2*>(a.o.at(t, h) + 4 * lane) =
+        make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+  }
+  if (lane == 0 && a.lse) a.lse[th] = total != 0.f ? (top + log2f(total)) * kLn2 : -INFINITY;
+  if (__any_sync(0xffffffffu, bad)) row_forward(a, sums[1], t, h, false);
+}
+
+constexpr int kMinKeysOfSplit = 256;
+
+template <int D, bool CAP>
+cudaError_t launch(const Args& ar, cudaStream_t s) {
+  const SpanArgs& a = ar.a;
+  CUtensorMap tq, tk, tv;
+  if (!make_tma_heads(&tq, a.q.p, a.queries, a.nh, a.d, a.q.ts, a.q.hs, a.rep, ar.tl.per) ||
+      !make_tma_heads(&tk, a.k.p, a.keys, a.nkv, a.d, a.k.ts, a.k.hs, 1, 128) ||
+      !make_tma_heads(&tv, a.v.p, a.keys, a.nkv, a.d, a.v.ts, a.v.hs, 1, 128))
+    return cudaErrorInvalidValue;
+  const cudaError_t e = allow_smem(spans_forward_kernel<D, CAP>, Cfg<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_overlapping(spans_forward_kernel<D, CAP>, std::min<int64_t>(ar.items, num_sms()),
+                            kThreads, Cfg<D>::SMEM, s, tq, tk, tv, ar);
+}
+
+}  // namespace
+
+int forward_splits(int queries, int keys, int nkv, int rep) {
+  const Tiling tl = Tiling::of(queries, rep);
+  const int64_t items = static_cast<int64_t>((tl.tiles + 1) / 2) * nkv;
+  if (items < 1) return 1;
+  return static_cast<int>(
+      std::max<int64_t>(1, std::min<int64_t>(num_sms() / items, keys / kMinKeysOfSplit)));
+}
+
+size_t forward_workspace(int queries, int keys, int nh, int nkv, int d) {
+  const int splits = forward_splits(queries, keys, nkv, nh / nkv);
+  return splits == 1 ? 0 : static_cast<size_t>(splits) * queries * nh * (d + 1) * sizeof(float);
+}
+
+cudaError_t forward_tiles(const SpanArgs& a, void* ws, cudaStream_t s) {
+  Args ar = {};
+  ar.a = a;
+  ar.tl = Tiling::of(a.queries, a.rep);
+  ar.pairs = (ar.tl.tiles + 1) / 2;
+  ar.splits = forward_splits(a.queries, a.keys, a.nkv, a.rep);
+  ar.items = static_cast<int64_t>(ar.pairs) * a.nkv * ar.splits;
+  ar.to_tanh = a.cap > 0.f ? a.scale / a.cap : 0.f;
+  ar.scale_log2 = (a.cap > 0.f ? a.cap : a.scale) * kLog2e;
+  const int64_t rows = static_cast<int64_t>(a.queries) * a.nh;
+  ar.part_o = static_cast<float*>(ws);
+  ar.part_lse = ar.part_o + ar.splits * rows * a.d;
+  ar.err = device_error_ptr();
+  cudaError_t e;
+  if (a.d <= 64)
+    e = a.cap > 0.f ? launch<64, true>(ar, s) : launch<64, false>(ar, s);
+  else
+    e = a.cap > 0.f ? launch<128, true>(ar, s) : launch<128, false>(ar, s);
+  if (e != cudaSuccess || ar.splits == 1) return e;
+  return launch_overlapping(join_kernel, rows, 32 * kJoinWarps, 0, s, ar);
+}
+
+}  // namespace rdt
