@@ -21,7 +21,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "librdt.so")
 SOURCES = ["api.cu", "gemm.cu", "attention.cu", "attention_tc.cu", "elementwise.cu",
            "sq_sum_static.cu", "embedding.cu", "logprobs.cu", "tensors.cu",
-           "qk_norm_rope.cu", "attention_spans.cu", "spans_forward.cu"]
+           "qk_norm_rope.cu", "attention_spans.cu", "spans_forward.cu", "spans_backward.cu"]
 HEADERS = ["common.cuh", "internal.h", "heads.cuh", "spans.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",

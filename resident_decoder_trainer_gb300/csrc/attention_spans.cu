@@ -18,18 +18,16 @@ namespace {
 constexpr int kRowWarps = 8, kRowThreads = 32 * kRowWarps;
 
 __global__ void __launch_bounds__(kRowThreads) rows_forward_kernel(const SpanArgs a) {
-  __shared__ float mem[kRowWarps][kMaxDim];
   after_previous_kernel();
   const int warp = threadIdx.x >> 5;
   const int64_t rows = static_cast<int64_t>(a.queries) * a.nh;
   for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRowWarps + warp; r < rows;
        r += static_cast<int64_t>(gridDim.x) * kRowWarps)
-    row_forward(a, mem[warp], static_cast<int>(r / a.nh), static_cast<int>(r % a.nh), true);
+    row_forward(a, static_cast<int>(r / a.nh), static_cast<int>(r % a.nh), true);
 }
 
 // The rows of dq, then those of dk and dv, in one grid.
 __global__ void __launch_bounds__(kRowThreads) rows_backward_kernel(const SpanArgs a) {
-  __shared__ float mem[kRowWarps][2 * kMaxDim];
   after_previous_kernel();
   const int warp = threadIdx.x >> 5;
   const int64_t dq_rows = static_cast<int64_t>(a.queries) * a.nh;
@@ -37,11 +35,10 @@ __global__ void __launch_bounds__(kRowThreads) rows_backward_kernel(const SpanAr
   for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRowWarps + warp; r < rows;
        r += static_cast<int64_t>(gridDim.x) * kRowWarps) {
     if (r < dq_rows) {
-      row_dq(a, mem[warp], static_cast<int>(r / a.nh), static_cast<int>(r % a.nh));
+      row_dq(a, static_cast<int>(r / a.nh), static_cast<int>(r % a.nh), 0, a.d);
     } else {
       const int64_t x = r - dq_rows;
-      row_dkdv(a, mem[warp], static_cast<int>(x / a.nkv), static_cast<int>(x % a.nkv), 0,
-               a.queries);
+      row_dkdv(a, static_cast<int>(x / a.nkv), static_cast<int>(x % a.nkv), 0, a.d);
     }
   }
 }
@@ -52,7 +49,7 @@ int64_t row_grid(int64_t rows) {
 }
 
 // A problem without keys has no tensors to load tiles from.
-bool forward_in_tiles(int queries, int keys) { return queries > 0 && keys > 0; }
+bool in_tiles(int queries, int keys) { return queries > 0 && keys > 0; }
 
 const char* shape_problem(int queries, int keys, int nh, int nkv, int d) {
   if (queries < 0 || keys < 0 || queries > 1 << 30 || keys > 1 << 30)
@@ -102,8 +99,11 @@ extern "C" {
 size_t rdt_attention_workspace_bytes(int32_t queries, int32_t keys, int32_t n_heads,
                                      int32_t n_kv_heads, int32_t head_dim, int32_t backward) {
   if (shape_problem(queries, keys, n_heads, n_kv_heads, head_dim)) return 0;
-  if (backward || !forward_in_tiles(queries, keys)) return 0;
-  return (forward_workspace(queries, keys, n_heads, n_kv_heads, head_dim) + 255) / 256 * 256;
+  if (!in_tiles(queries, keys)) return 0;
+  const size_t n = backward
+                       ? backward_workspace(queries, n_heads, n_kv_heads)
+                       : forward_workspace(queries, keys, n_heads, n_kv_heads, head_dim);
+  return (n + 255) / 256 * 256;
 }
 
 rdt_status rdt_attention(int32_t queries, int32_t keys, int32_t n_heads, int32_t n_kv_heads,
@@ -136,7 +136,7 @@ rdt_status rdt_attention(int32_t queries, int32_t keys, int32_t n_heads, int32_t
   a.v = view_of(v);
   a.o = view_of(o);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (forward_in_tiles(queries, keys)) return launched(forward_tiles(a, ws, s));
+  if (in_tiles(queries, keys)) return launched(forward_tiles(a, ws, s));
   return launched(launch_overlapping(rows_forward_kernel, row_grid(int64_t{queries} * n_heads),
                                      kRowThreads, 0, s, a));
 }
@@ -186,6 +186,7 @@ rdt_status rdt_attention_backward(int32_t queries, int32_t keys, int32_t n_heads
   a.dk = view_of(dk);
   a.dv = view_of(dv);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (in_tiles(queries, keys)) return launched(backward_tiles(a, ws, s));
   const int64_t rows = int64_t{queries} * n_heads + int64_t{keys} * n_kv_heads;
   return launched(
       launch_overlapping(rows_backward_kernel, row_grid(rows), kRowThreads, 0, s, a));

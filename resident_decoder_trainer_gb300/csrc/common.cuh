@@ -370,6 +370,40 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int m, int n, int a_mn, in
          (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
+// The low word of a shared-memory matrix descriptor (sdesc_sw128) whose SBO is
+// 1024: start >> 4 and LBO >> 4. Steps inside a tile are added to it. The
+// high word is a constant.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t lbo) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
+}
+// Keeps what is computed from x where it is: descriptors of every step of every
+// tile, held over a loop, take more registers than there are.
+__device__ __forceinline__ uint32_t not_hoisted(uint32_t x) {
+  asm volatile("" : "+r"(x));
+  return x;
+}
+__device__ __forceinline__ void tc_mma_low(uint32_t d_tmem, uint32_t alow, uint32_t blow,
+                                           uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(alow), "r"(blow), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "n"(kDescHigh)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts_low(uint32_t d_tmem, uint32_t a_tmem, uint32_t blow,
+                                              uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(blow), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "n"(kDescHigh)
+      : "memory");
+}
+
 // ------------------------------------------------------- CTA pairs (clusters)
 // Rank of this CTA in its cluster.
 __device__ __forceinline__ uint32_t cluster_ctarank() {

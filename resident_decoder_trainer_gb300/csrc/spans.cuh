@@ -30,35 +30,11 @@ constexpr int kMaxDim = 128;  // of a head
 
 // ------------------------------------------------- one warp per row of an output
 // Lanes take 32 keys (or queries) at a time for the scores, and four columns
-// each for the sums. All in fp32.
-
-// Copies a head's values to shared memory as fp32; whole warp.
-__device__ __forceinline__ void stage_row(float* dst, const bf16* src, int d) {
-  for (int c = 2 * (threadIdx.x & 31); c < d; c += 64) {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(src + c);
-    dst[c] = bf16lo(w);
-    dst[c + 1] = bf16hi(w);
-  }
-}
-
-__device__ __forceinline__ float dot_row(const float* a, const bf16* b, int d) {
-  float s0 = 0.f, s1 = 0.f;
-  for (int c = 0; c < d; c += 8) {
-    Eight<bf16> e;
-    float x[8];
-    e.load(b + c);
-    e.get(x);
-#pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      s0 = fmaf(a[c + i], x[i], s0);
-      s1 = fmaf(a[c + i + 1], x[i + 1], s1);
-    }
-  }
-  return s0 + s1;
-}
+// each for the sums. All in fp32. Columns [c0, c1) are written.
 
 __device__ __forceinline__ float dot_rows(const bf16* a, const bf16* b, int d) {
-  float s = 0.f;
+  float s0 = 0.f, s1 = 0.f;
+#pragma unroll 4
   for (int c = 0; c < d; c += 8) {
     Eight<bf16> e, f;
     float x[8], y[8];
@@ -67,9 +43,12 @@ __device__ __forceinline__ float dot_rows(const bf16* a, const bf16* b, int d) {
     e.get(x);
     f.get(y);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s = fmaf(x[i], y[i], s);
+    for (int i = 0; i < 8; i += 2) {
+      s0 = fmaf(x[i], y[i], s0);
+      s1 = fmaf(x[i + 1], y[i + 1], s1);
+    }
   }
-  return s;
+  return s0 + s1;
 }
 
 // Score of a product q . k, and what its cap's derivative is.
@@ -93,34 +72,30 @@ __device__ __forceinline__ void add_row(float (&acc)[4], float w, const bf16* sr
     acc[2 * x + 1] = fmaf(w, bf16hi(two), acc[2 * x + 1]);
   }
 }
-__device__ __forceinline__ void put_row(bf16* dst, const float (&acc)[4], float w, int d) {
+__device__ __forceinline__ void put_row(bf16* dst, const float (&acc)[4], float w, int c0, int c1) {
   const int c = 2 * (threadIdx.x & 31);
 #pragma unroll
   for (int x = 0; x < 2; ++x)
-    if (c + 64 * x < d)
+    if (c + 64 * x >= c0 && c + 64 * x < c1)
       *reinterpret_cast<uint32_t*>(dst + c + 64 * x) =
           pack_bf16x2(acc[2 * x] * w, acc[2 * x + 1] * w);
 }
 
-// o of query t, head h, and its lse where `with_lse`. `mem` is kMaxDim floats of
-// the warp's own.
-__device__ __noinline__ static void row_forward(const SpanArgs& a, float* mem, int t, int h,
-                                              bool with_lse) {
+// o of query t, head h, and its lse where `with_lse`.
+__device__ __noinline__ static void row_forward(const SpanArgs& a, int t, int h, bool with_lse) {
   const int lane = threadIdx.x & 31, g = h / a.rep;
   int first, end;
   a.span(t, first, end);
-  __syncwarp();
-  stage_row(mem, a.q.at(t, h), a.d);
-  __syncwarp();
   float m = -INFINITY, l = 0.f, acc[4] = {};
   for (int64_t base = first; base < end; base += 32) {
     const int64_t j = base + lane;
     float s = -INFINITY, slope;
-    if (j < end) s = score_of(a, dot_row(mem, a.k.at(j, g), a.d), slope);
+    if (j < end) s = score_of(a, dot_rows(a.q.at(t, h), a.k.at(j, g), a.d), slope);
     // fmaxf passes over a NaN; exp(s - m) below does not
     const float top = fmaxf(m, warp_max(s));
-    const float alpha = m == top ? 1.f : expf(m - top);
-    const float p = j < end ? expf(s - top) : 0.f;
+    const float base_of = top == -INFINITY ? 0.f : top;
+    const float alpha = m == -INFINITY ? 1.f : expf(m - base_of);
+    const float p = j < end ? expf(s - base_of) : 0.f;
     m = top;
     l = l * alpha + warp_sum(p);
 #pragma unroll
@@ -129,54 +104,47 @@ __device__ __noinline__ static void row_forward(const SpanArgs& a, float* mem, i
     for (int i = 0; i < n; ++i)
       add_row(acc, __shfl_sync(0xffffffffu, p, i), a.v.at(base + i, g), a.d);
   }
-  const bool any = first < end;
-  put_row(a.o.at(t, h), acc, any ? 1.f / l : 0.f, a.d);
+  put_row(a.o.at(t, h), acc, l != 0.f ? 1.f / l : 0.f, 0, a.d);
   if (with_lse && a.lse && lane == 0)
-    a.lse[static_cast<int64_t>(t) * a.nh + h] = any ? m + logf(l) : -INFINITY;
+    a.lse[static_cast<int64_t>(t) * a.nh + h] = l != 0.f ? m + logf(l) : -INFINITY;
 }
 
-// dq of query t, head h. `mem` is 2 kMaxDim floats of the warp's own.
-__device__ __noinline__ static void row_dq(const SpanArgs& a, float* mem, int t, int h) {
+// dq of query t, head h.
+__device__ __noinline__ static void row_dq(const SpanArgs& a, int t, int h, int c0, int c1) {
   const int lane = threadIdx.x & 31, g = h / a.rep;
   int first, end;
   a.span(t, first, end);
   float acc[4] = {};
   if (first < end) {
-    __syncwarp();
-    stage_row(mem, a.q.at(t, h), a.d);
-    stage_row(mem + kMaxDim, a.d_o.at(t, h), a.d);
-    __syncwarp();
     const int64_t th = static_cast<int64_t>(t) * a.nh + h;
     const float lse = a.lse[th];
-    const float own = dot_row(mem + kMaxDim, a.o.at(t, h), a.d) - (a.d_lse ? a.d_lse[th] : 0.f);
+    const float own =
+        dot_rows(a.d_o.at(t, h), a.o.at(t, h), a.d) - (a.d_lse ? a.d_lse[th] : 0.f);
     for (int64_t base = first; base < end; base += 32) {
       const int64_t j = base + lane;
       float ds = 0.f;
       if (j < end) {
         float slope;
-        const float p = expf(score_of(a, dot_row(mem, a.k.at(j, g), a.d), slope) - lse);
-        ds = p * (dot_row(mem + kMaxDim, a.v.at(j, g), a.d) - own) * slope;
+        const float p =
+            expf(score_of(a, dot_rows(a.q.at(t, h), a.k.at(j, g), a.d), slope) - lse);
+        ds = p * (dot_rows(a.d_o.at(t, h), a.v.at(j, g), a.d) - own) * slope;
       }
       const int n = static_cast<int>(min(static_cast<int64_t>(32), end - base));
       for (int i = 0; i < n; ++i)
         add_row(acc, __shfl_sync(0xffffffffu, ds, i), a.k.at(base + i, g), a.d);
     }
   }
-  put_row(a.dq.at(t, h), acc, a.scale, a.d);
+  put_row(a.dq.at(t, h), acc, a.scale, c0, c1);
 }
 
-// dk and dv of key j, kv head g, from queries [t0, t1). `mem` as for row_dq.
-__device__ __noinline__ static void row_dkdv(const SpanArgs& a, float* mem, int j, int g, int t0, int t1) {
+// dk and dv of key j, kv head g.
+__device__ __noinline__ static void row_dkdv(const SpanArgs& a, int j, int g, int c0, int c1) {
   const int lane = threadIdx.x & 31;
-  __syncwarp();
-  stage_row(mem, a.k.at(j, g), a.d);
-  stage_row(mem + kMaxDim, a.v.at(j, g), a.d);
-  __syncwarp();
   float ak[4] = {}, av[4] = {};
-  for (int64_t base = t0; base < t1; base += 32) {
+  for (int64_t base = 0; base < a.queries; base += 32) {
     const int64_t t = base + lane;
     bool sees = false;
-    if (t < t1) {
+    if (t < a.queries) {
       int first, end;
       a.span(static_cast<int>(t), first, end);
       sees = first <= j && j < end;
@@ -189,10 +157,10 @@ __device__ __noinline__ static void row_dkdv(const SpanArgs& a, float* mem, int 
       if (sees) {
         const int64_t th = t * a.nh + h;
         float slope;
-        p = expf(score_of(a, dot_row(mem, a.q.at(t, h), a.d), slope) - a.lse[th]);
+        p = expf(score_of(a, dot_rows(a.q.at(t, h), a.k.at(j, g), a.d), slope) - a.lse[th]);
         const float own =
             dot_rows(a.d_o.at(t, h), a.o.at(t, h), a.d) - (a.d_lse ? a.d_lse[th] : 0.f);
-        ds = p * (dot_row(mem + kMaxDim, a.d_o.at(t, h), a.d) - own) * slope;
+        ds = p * (dot_rows(a.d_o.at(t, h), a.v.at(j, g), a.d) - own) * slope;
       }
       for (unsigned left = who; left; left &= left - 1) {
         const int i = __ffs(left) - 1;
@@ -201,8 +169,8 @@ __device__ __noinline__ static void row_dkdv(const SpanArgs& a, float* mem, int 
       }
     }
   }
-  put_row(a.dk.at(j, g), ak, a.scale, a.d);
-  put_row(a.dv.at(j, g), av, 1.f, a.d);
+  put_row(a.dk.at(j, g), ak, a.scale, c0, c1);
+  put_row(a.dv.at(j, g), av, 1.f, c0, c1);
 }
 
 // ------------------------------------------------- tiles of the tensor-core kernels
@@ -246,5 +214,8 @@ __device__ __forceinline__ void span_of_queries(const SpanArgs& a, int t0, int t
 int forward_splits(int queries, int keys, int nkv, int rep);
 size_t forward_workspace(int queries, int keys, int nh, int nkv, int d);
 cudaError_t forward_tiles(const SpanArgs& a, void* ws, cudaStream_t s);
+
+size_t backward_workspace(int queries, int nh, int nkv);
+cudaError_t backward_tiles(const SpanArgs& a, void* ws, cudaStream_t s);
 
 }  // namespace rdt

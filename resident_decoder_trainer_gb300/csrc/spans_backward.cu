@@ -1,0 +1,924 @@
+// Backward pass of the attention over spans of keys on the 5th-generation
+// tensor cores, in three kernels, none of which adds into memory another one
+// writes, so that results do not depend on scheduling:
+//  * prepare: D = d_o . o - d_lse and the base-2 log-sum-exp of every row, tile
+//    by tile (spans.cuh), both negated; the spans of tiles and of groups of 32
+//    tiles, by which the others find what meets what;
+//  * dK/dV: one CTA per (128 keys, key head) walks the row tiles that see any
+//    of its keys. S^T = K Q^T, P^T, dV += P^T dO; dP^T = V dO^T,
+//    dS^T = P^T o (dP^T - D) slope, dK += dS^T Q. P^T and dS^T are written over
+//    their scores in TMEM as bf16 and read from there; dK and dV stay in TMEM;
+//  * dQ: a CTA walks (row tile, key head) items; S and dP once more,
+//    dQ += dS K.
+// In both, warp 0 loads by TMA, warp 1 issues the MMAs, and warps 4-19 do the
+// elementwise work: TMEM lanes 32 (w mod 4) on, columns 32 (w / 4 - 1) on.
+//
+// Rows of dq, dk and dv that are not finite are computed again one by one
+// (row_dq, row_dkdv): a NaN or infinity where a query does not see a key, times
+// 0, would reach them.
+#include <algorithm>
+
+#include "spans.cuh"
+
+namespace rdt {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kThreads = 640, kEltThreads = 512;
+constexpr int kGroup = 32;  // row tiles of a group
+constexpr float kNoRow = -1e30f;  // negated lse of a row that sees nothing: p = 0
+
+// Spans of a row tile: keys any of its rows sees, keys all of them see. Rows
+// that see nothing (or are none) are left out of both: their p is 0 unmasked.
+struct TileSpan {
+  int first, end;          // any
+  int all_first, all_end;  // all
+};
+
+struct Args {
+  SpanArgs a;
+  Tiling tl;
+  int groups;
+  float to_tanh, scale_log2;
+  float *neg_lse, *neg_d;  // [nkv][tiles][128]
+  int *lo, *len;           // [tiles][128]
+  TileSpan* tiles;
+  int2* group;  // first, end
+  int* err;
+};
+
+// ---------------------------------------------------------------- prepare
+constexpr int kPrepThreads = 256;
+
+// Blocks [0, groups) find the spans, the others the rows' D and lse.
+__global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_constant__ Args ar) {
+  const SpanArgs& a = ar.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  after_previous_kernel();
+  if (static_cast<int>(blockIdx.x) < ar.groups) {
+    __shared__ int2 mine[kPrepThreads / 32];
+    int lo_all = INT32_MAX, hi_all = 0;
+    for (int i = warp; i < kGroup; i += kPrepThreads / 32) {
+      const int tile = blockIdx.x * kGroup + i;
+      if (tile >= ar.tl.tiles) break;
+      TileSpan s = {INT32_MAX, 0, 0, INT32_MAX};
+      for (int row = lane; row < 128; row += 32) {
+        const int in = row / a.rep, t = tile * ar.tl.per + in;
+        int x = 0, y = 0;
+        if (in < ar.tl.per && t < a.queries) a.span(t, x, y);
+        if (x < y) {
+          s.first = min(s.first, x);
+          s.end = max(s.end, y);
+          s.all_first = max(s.all_first, x);
+          s.all_end = min(s.all_end, y);
+        } else {
+          x = y = 0;
+        }
+        ar.lo[tile * int64_t{128} + row] = x;
+        ar.len[tile * int64_t{128} + row] = y - x;
+      }
+      s.first = __reduce_min_sync(0xffffffffu, s.first);
+      s.end = __reduce_max_sync(0xffffffffu, s.end);
+      s.all_first = __reduce_max_sync(0xffffffffu, s.all_first);
+      s.all_end = __reduce_min_sync(0xffffffffu, s.all_end);
+      if (s.first >= s.end) s.first = s.end = 0;
+      if (lane == 0) ar.tiles[tile] = s;
+      if (s.first < s.end) {
+        lo_all = min(lo_all, s.first);
+        hi_all = max(hi_all, s.end);
+      }
+    }
+    if (lane == 0) mine[warp] = make_int2(lo_all, hi_all);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int w = 1; w < kPrepThreads / 32; ++w) {
+        lo_all = min(lo_all, mine[w].x);
+        hi_all = max(hi_all, mine[w].y);
+      }
+      ar.group[blockIdx.x] = lo_all < hi_all ? make_int2(lo_all, hi_all) : make_int2(0, 0);
+    }
+    return;
+  }
+  // a row is `lanes` lanes of eight columns
+  int lanes = 2;
+  while (lanes * 8 < a.d) lanes *= 2;
+  const int per_warp = 32 / lanes, c = 8 * (lane & (lanes - 1));
+  const int64_t rows = static_cast<int64_t>(a.nkv) * ar.tl.tiles * 128;
+  const int64_t step = static_cast<int64_t>(gridDim.x - ar.groups) * (kPrepThreads / 32) * per_warp;
+  for (int64_t base = (static_cast<int64_t>(blockIdx.x - ar.groups) * (kPrepThreads / 32) + warp) *
+                      per_warp;
+       base < rows; base += step) {
+    const int64_t at = base + lane / lanes;  // rows is a multiple of per_warp
+    const int row = static_cast<int>(at & 127);
+    const int tile = static_cast<int>((at >> 7) % ar.tl.tiles);
+    const int g = static_cast<int>((at >> 7) / ar.tl.tiles);
+    const int in = row / a.rep, t = tile * ar.tl.per + in, h = g * a.rep + row % a.rep;
+    const bool real = in < ar.tl.per && t < a.queries;
+    float own = 0.f;
+    if (real && c < a.d) {
+      Eight<bf16> x, y;
+      float u[8], v[8];
+      x.load(a.d_o.at(t, h) + c);
+      y.load(a.o.at(t, h) + c);
+      x.get(u);
+      y.get(v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) own = fmaf(u[i], v[i], own);
+    }
+    for (int o = lanes >> 1; o > 0; o >>= 1) own += __shfl_xor_sync(0xffffffffu, own, o);
+    if (lane & (lanes - 1)) continue;
+    float neg_lse = kNoRow, neg_d = 0.f;
+    if (real) {
+      const int64_t th = static_cast<int64_t>(t) * a.nh + h;
+      int x, y;
+      a.span(t, x, y);
+      if (x < y) {
+        neg_lse = -a.lse[th] * kLog2e;
+        neg_d = (a.d_lse ? a.d_lse[th] : 0.f) - own;
+      }
+    }
+    ar.neg_lse[at] = neg_lse;
+    ar.neg_d[at] = neg_d;
+  }
+}
+
+// ------------------------------------------------------------ elementwise
+// p = 2^(score + neg_lse) of two scores; with a cap the score is its tanh, and
+// the slope 1 - tanh^2 is left in `slope`.
+template <bool CAP>
+__device__ __forceinline__ float2 p_of(float2 s, const Args& ar, float2 neg_lse, float2& slope) {
+  const float2 k = make_float2(ar.scale_log2, ar.scale_log2);
+  if constexpr (CAP) {
+    const float w = 2.f * kLog2e * ar.to_tanh;
+    s.x = fmaf(-2.f, rcp_approx(1.f + ex2_approx(s.x * w)), 1.f);
+    s.y = fmaf(-2.f, rcp_approx(1.f + ex2_approx(s.y * w)), 1.f);
+    slope = fma2(make_float2(-s.x, -s.y), s, make_float2(1.f, 1.f));
+  }
+  float2 p = fma2(s, k, neg_lse);
+  p.x = ex2_approx(p.x);
+  p.y = ex2_approx(p.y);
+  return p;
+}
+
+// Rows of 32 columns, bf16, of which those below `d` exist.
+__device__ __forceinline__ void put_columns(bf16* dst, const uint32_t (&r)[32], float w, int left) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (8 * e >= left) break;
+    reinterpret_cast<uint4*>(dst)[e] = make_uint4(
+        pack_bf16x2(__uint_as_float(r[8 * e]) * w, __uint_as_float(r[8 * e + 1]) * w),
+        pack_bf16x2(__uint_as_float(r[8 * e + 2]) * w, __uint_as_float(r[8 * e + 3]) * w),
+        pack_bf16x2(__uint_as_float(r[8 * e + 4]) * w, __uint_as_float(r[8 * e + 5]) * w),
+        pack_bf16x2(__uint_as_float(r[8 * e + 6]) * w, __uint_as_float(r[8 * e + 7]) * w));
+  }
+}
+__device__ __forceinline__ bool all_finite(const uint32_t (&r)[32], int left) {
+  float bad = 0.f;
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    if (e < left) bad = fmaf(__uint_as_float(r[e]), 0.f, bad);
+  return bad == 0.f;
+}
+
+__device__ __forceinline__ void settle(int* err) {
+  if (err && *reinterpret_cast<volatile int*>(err) != 0) {
+    // after a timed-out wait, copies issued just before may still be landing
+    // in this CTA's shared memory: let them finish before it exits
+    const uint64_t w0 = global_timer_ns();
+    while (global_timer_ns() - w0 < 200000ull) {
+    }
+  }
+}
+
+// ------------------------------------------------------------------ dK, dV
+struct Meta {
+  int tile;  // -1: no more
+  int full;  // every row that sees anything sees all of the CTA's keys
+};
+
+template <int D>
+struct KvCfg {
+  static constexpr uint32_t CHUNK = 128 * 128, TILE = 128 * D * 2;
+  static constexpr int ST = D == 128 ? 2 : 4;  // stages of Q and of dO
+  static constexpr uint32_t OFF_K = 0, OFF_V = TILE, OFF_Q = 2 * TILE, OFF_DO = OFF_Q + ST * TILE,
+                            OFF_ROW = OFF_DO + ST * TILE,  // [ST][neg_lse, neg_d, lo, len][128]
+      OFF_META = OFF_ROW + ST * 2048, OFF_BAR = OFF_META + ST * sizeof(Meta);
+  static constexpr size_t SMEM = OFF_BAR + 256 + 1024;
+  static constexpr uint32_t T_DK = 0, T_DV = 128, T_S = 256, T_DP = 384, TMEM_COLS = 512;
+  static_assert(SMEM <= 232448 && OFF_BAR % 8 == 0, "");
+};
+
+// TMEM column, relative to a block of 128, of the packed bf16 A operand for K
+// step kk (16 rows): 32 columns' pairs lie in the first 16 of their place.
+__device__ __forceinline__ uint32_t packed_col(int kk) { return (kk >> 1) * 32 + (kk & 1) * 8; }
+
+template <int D, bool CAP>
+__global__ void __launch_bounds__(kThreads, 1)
+    spans_dkdv_kernel(const __grid_constant__ CUtensorMap tq,
+                      const __grid_constant__ CUtensorMap tdo,
+                      const __grid_constant__ CUtensorMap tk,
+                      const __grid_constant__ CUtensorMap tv, const __grid_constant__ Args ar) {
+  using C = KvCfg<D>;
+  constexpr int ST = C::ST;
+  const SpanArgs& a = ar.a;
+  int* err = ar.err;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + C::OFF_BAR;
+  const uint32_t kv_full = bar0, q_full = bar0 + 8, q_empty = q_full + 8 * ST,
+                 o_full = q_empty + 8 * ST, o_empty = o_full + 8 * ST, s_full = o_empty + 8 * ST,
+                 dp_full = s_full + 8, p_ready = dp_full + 8, ds_ready = p_ready + 8,
+                 fin = ds_ready + 8, drain = fin + 8;
+  static_assert(8 * (1 + 4 * ST + 6) <= 248, "");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 248);
+  Meta* meta = reinterpret_cast<Meta*>(smem + C::OFF_META);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int chunks = (a.d + 63) / 64, used = ar.tl.per * a.rep;
+  const int n0 = static_cast<int>(blockIdx.x / a.nkv) * 128;
+  const int g = static_cast<int>(blockIdx.x % a.nkv);
+
+  if (threadIdx.x == 0) {
+    mbar_init(kv_full, 1);
+    for (int x = 0; x < ST; ++x) {
+      mbar_init(q_full + 8 * x, 1);
+      mbar_init(q_empty + 8 * x, 1);
+      mbar_init(o_full + 8 * x, 1);
+      mbar_init(o_empty + 8 * x, 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(dp_full, 1);
+    mbar_init(p_ready, kEltThreads);
+    mbar_init(ds_ready, kEltThreads);
+    mbar_init(fin, 1);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tq);
+    tma_prefetch_desc(&tdo);
+    tma_prefetch_desc(&tk);
+    tma_prefetch_desc(&tv);
+  }
+  if (used < 128) {
+    // rows past a tile's last are never loaded, and p = 0 does not clear a NaN
+    const int words = (128 - used) * 32;
+    for (int i = threadIdx.x; i < 2 * ST * chunks * words; i += kThreads) {
+      const int w = i % words, block = i / words;
+      const uint32_t base = C::OFF_Q + (block / chunks) * C::TILE + (block % chunks) * C::CHUNK;
+      *reinterpret_cast<uint32_t*>(smem + base + used * 128 + 4 * w) = 0u;
+    }
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  after_previous_kernel();
+
+  if (warp == 0) {
+    // --------------------------------------------------------- producer
+    if (lane == 0) {
+      mbar_arrive_expect_tx(kv_full, 2 * chunks * C::CHUNK);
+      for (int c = 0; c < chunks; ++c) {
+        tma_load_3d(sbase + C::OFF_K + c * C::CHUNK, &tk, kv_full, c * 64, g, n0);
+        tma_load_3d(sbase + C::OFF_V + c * C::CHUNK, &tv, kv_full, c * 64, g, n0);
+      }
+    }
+    const int n1 = min(n0 + 128, a.keys);
+    bool ok = true;
+    int it = 0;
+    // one row tile, or the end of them
+    auto send = [&](int tile, int full) {
+      const int st = it % ST;
+      const uint32_t ph = ((it / ST) & 1) ^ 1;
+      ++it;
+      if (lane == 0) {
+        ok = mbar_wait(q_empty + 8 * st, ph, err);
+        if (ok) {
+          meta[st] = Meta{tile, full};
+          if (tile < 0) {
+            mbar_arrive(q_full + 8 * st);
+          } else {
+            const uint32_t q = sbase + C::OFF_Q + st * C::TILE, o = sbase + C::OFF_DO + st * C::TILE;
+            const uint32_t row = sbase + C::OFF_ROW + st * 2048;
+            const int64_t at = (static_cast<int64_t>(g) * ar.tl.tiles + tile) * 128;
+            mbar_arrive_expect_tx(q_full + 8 * st, chunks * used * 128 + 2048);
+            for (int c = 0; c < chunks; ++c)
+              tma_load_3d(q + c * C::CHUNK, &tq, q_full + 8 * st, c * 64, g * a.rep,
+                          tile * ar.tl.per);
+            bulk_load_1d(row, ar.neg_lse + at, 512, q_full + 8 * st);
+            bulk_load_1d(row + 512, ar.neg_d + at, 512, q_full + 8 * st);
+            bulk_load_1d(row + 1024, ar.lo + tile * int64_t{128}, 512, q_full + 8 * st);
+            bulk_load_1d(row + 1536, ar.len + tile * int64_t{128}, 512, q_full + 8 * st);
+            ok = mbar_wait(o_empty + 8 * st, ph, err);
+            if (ok) {
+              mbar_arrive_expect_tx(o_full + 8 * st, chunks * used * 128);
+              for (int c = 0; c < chunks; ++c)
+                tma_load_3d(o + c * C::CHUNK, &tdo, o_full + 8 * st, c * 64, g * a.rep,
+                            tile * ar.tl.per);
+            }
+          }
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0);
+    };
+    for (int g0 = 0; g0 < ar.groups && ok; g0 += 32) {
+      const int2 span = g0 + lane < ar.groups ? ar.group[g0 + lane] : make_int2(0, 0);
+      unsigned some = __ballot_sync(0xffffffffu, span.x < n1 && span.y > n0);
+      for (; some && ok; some &= some - 1) {
+        const int first = (g0 + __ffs(some) - 1) * kGroup, tile = first + lane;
+        TileSpan s = {0, 0, 0, 0};
+        if (tile < ar.tl.tiles) s = ar.tiles[tile];
+        unsigned meets = __ballot_sync(0xffffffffu, s.first < n1 && s.end > n0);
+        const unsigned full =
+            __ballot_sync(0xffffffffu, s.all_first <= n0 && s.all_end >= n1);
+        for (; meets && ok; meets &= meets - 1) {
+          const int i = __ffs(meets) - 1;
+          send(first + i, (full >> i) & 1);
+        }
+      }
+    }
+    if (ok) send(-1, 0);
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // -------------------------------------------------------------- MMA
+      constexpr uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0);
+      const uint32_t id_kv = idesc_bf16_f32(128, a.d, 0, 1);
+      const int ksteps = a.d / 16;
+      const uint32_t k_desc = desc_low(sbase + C::OFF_K, 16);
+      const uint32_t v_desc = desc_low(sbase + C::OFF_V, 16);
+      auto scores = [&](uint32_t to, uint32_t kv, uint32_t rows) {
+        const uint32_t r = not_hoisted(desc_low(rows, 16));
+        kv = not_hoisted(kv);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          if (k >= ksteps) break;
+          const uint32_t off = ((k >> 2) * C::CHUNK + (k & 3) * 32) >> 4;
+          tc_mma_low(tmem + to, kv + off, r + off, id_s, k > 0);
+        }
+      };
+      auto add = [&](uint32_t to, uint32_t from, uint32_t rows, int it) {
+        const uint32_t r = not_hoisted(desc_low(rows, C::CHUNK));
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          tc_mma_ts_low(tmem + to, tmem + from + packed_col(k), r + k * 128, id_kv,
+                         (it | k) != 0);
+      };
+      // whether there is a tile `it`, with its Q loaded
+      auto wait_q = [&](int it, bool& more) -> bool {
+        if (!mbar_wait(q_full + 8 * (it % ST), (it / ST) & 1, err)) return false;
+        more = meta[it % ST].tile >= 0;
+        tc_fence_after();
+        return true;
+      };
+      auto wait = [&](uint32_t bar, int phase) -> bool {
+        if (!mbar_wait(bar, phase & 1, err)) return false;
+        tc_fence_after();
+        return true;
+      };
+      auto q_of = [&](int it) { return sbase + C::OFF_Q + (it % ST) * C::TILE; };
+      auto o_of = [&](int it) { return sbase + C::OFF_DO + (it % ST) * C::TILE; };
+      bool more = false;
+      bool ok = wait(kv_full, 0) && wait_q(0, more);
+      if (ok && more) {
+        scores(C::T_S, k_desc, q_of(0));
+        tc_commit(s_full);
+        ok = wait(o_full, 0);
+        if (ok) {
+          scores(C::T_DP, v_desc, o_of(0));
+          tc_commit(dp_full);
+        }
+      }
+      for (int it = 0; ok && more; ++it) {
+        const int st = it % ST;
+        if (!(ok = wait(p_ready, it))) break;
+        add(C::T_DV, C::T_S, o_of(it), it);
+        tc_commit(o_empty + 8 * st);
+        bool next = false;
+        if (!(ok = wait_q(it + 1, next))) break;
+        if (next) {  // after dV of this tile, which reads P from the same columns
+          scores(C::T_S, k_desc, q_of(it + 1));
+          tc_commit(s_full);
+        }
+        if (!(ok = wait(ds_ready, it))) break;
+        add(C::T_DK, C::T_DP, q_of(it), it);
+        tc_commit(q_empty + 8 * st);
+        if (next) {
+          if (!(ok = wait(o_full + 8 * ((it + 1) % ST), (it + 1) / ST))) break;
+          scores(C::T_DP, v_desc, o_of(it + 1));
+          tc_commit(dp_full);
+        }
+        more = next;
+      }
+      tc_commit(fin);
+      tc_commit(drain);
+      mbar_wait(drain, 0, nullptr);
+    }
+  } else if (warp >= 4) {
+    // ------------------------ P^T and dS^T: one key, 32 of a tile's 128 rows
+    const int quarter = warp & 3, block = (warp - 4) >> 2;
+    const int row = quarter * 32 + lane, key = n0 + row;
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t ts = tmem + lane_base + C::T_S + block * 32;
+    const uint32_t tdp = tmem + lane_base + C::T_DP + block * 32;
+    bool ok = true;
+    int it = 0;
+    for (;; ++it) {
+      const int st = it % ST;
+      ok = warp_wait(q_full + 8 * st, (it / ST) & 1, err);
+      if (!ok) break;
+      const Meta m = meta[st];
+      if (m.tile < 0) break;
+      const uint8_t* rows = smem + C::OFF_ROW + st * 2048 + block * 128;
+      const float4* lse4 = reinterpret_cast<const float4*>(rows);
+      const float4* d4 = reinterpret_cast<const float4*>(rows + 512);
+      const int4* lo4 = reinterpret_cast<const int4*>(rows + 1024);
+      const int4* len4 = reinterpret_cast<const int4*>(rows + 1536);
+      ok = warp_wait(s_full, it & 1, err);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t sv[32], pk[16];
+      uint32_t seen = 0xffffffffu;
+      tmem_ld32(ts, sv);
+      if (!m.full) {
+        seen = 0u;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const int4 lo = lo4[c], len = len4[c];
+          seen |= static_cast<uint32_t>(static_cast<uint32_t>(key - lo.x) <
+                                        static_cast<uint32_t>(len.x)) << (4 * c);
+          seen |= static_cast<uint32_t>(static_cast<uint32_t>(key - lo.y) <
+                                        static_cast<uint32_t>(len.y)) << (4 * c + 1);
+          seen |= static_cast<uint32_t>(static_cast<uint32_t>(key - lo.z) <
+                                        static_cast<uint32_t>(len.z)) << (4 * c + 2);
+          seen |= static_cast<uint32_t>(static_cast<uint32_t>(key - lo.w) <
+                                        static_cast<uint32_t>(len.w)) << (4 * c + 3);
+        }
+      }
+      tmem_ld_wait();
+      // sv: p, times the cap's slope
+#pragma unroll
+      for (int c = 0; c < 32; c += 4) {
+        const float4 nl = lse4[c / 4];
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+          float2 slope;
+          float2 p = p_of<CAP>(
+              make_float2(__uint_as_float(sv[c + e]), __uint_as_float(sv[c + e + 1])), ar,
+              e ? make_float2(nl.z, nl.w) : make_float2(nl.x, nl.y), slope);
+          if (!m.full) {
+            if (!((seen >> (c + e)) & 1)) p.x = 0.f;
+            if (!((seen >> (c + e + 1)) & 1)) p.y = 0.f;
+          }
+          pk[(c + e) / 2] = pack_bf16x2(p.x, p.y);
+          if constexpr (CAP) p = mul2(p, slope);
+          sv[c + e] = __float_as_uint(p.x);
+          sv[c + e + 1] = __float_as_uint(p.y);
+        }
+      }
+      tmem_st16(ts, pk);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(p_ready);
+      ok = warp_wait(dp_full, it & 1, err);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t dp[16];
+        tmem_ld16(tdp + 16 * h, dp);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 16; c += 4) {
+          const float4 nd = d4[4 * h + c / 4];
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            float2 ds = add2(make_float2(__uint_as_float(dp[c + e]), __uint_as_float(dp[c + e + 1])),
+                             e ? make_float2(nd.z, nd.w) : make_float2(nd.x, nd.y));
+            ds = mul2(ds, make_float2(__uint_as_float(sv[16 * h + c + e]),
+                                      __uint_as_float(sv[16 * h + c + e + 1])));
+            if (!m.full) {
+              if (!((seen >> (16 * h + c + e)) & 1)) ds.x = 0.f;
+              if (!((seen >> (16 * h + c + e + 1)) & 1)) ds.y = 0.f;
+            }
+            pk[8 * h + (c + e) / 2] = pack_bf16x2(ds.x, ds.y);
+          }
+        }
+      }
+      tmem_st16(tdp, pk);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(ds_ready);
+    }
+    if (ok && warp_wait(fin, 0, err)) {
+      tc_fence_after();
+      const int c0 = block * 32, left = a.d - c0;
+      if (left > 0) {
+        uint32_t r[32];
+        bool fine = true;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+          if (it > 0) {
+            tmem_ld32(tmem + lane_base + (which ? C::T_DV : C::T_DK) + c0, r);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) r[e] = 0u;
+          }
+          fine = fine && all_finite(r, left);
+          if (key < a.keys)
+            put_columns((which ? a.dv : a.dk).at(key, g) + c0, r, which ? 1.f : a.scale, left);
+        }
+        for (unsigned again = __ballot_sync(0xffffffffu, !fine && key < a.keys); again;
+             again &= again - 1)
+          row_dkdv(a, n0 + quarter * 32 + __ffs(again) - 1, g, c0, min(c0 + 32, a.d));
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  settle(err);
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// ---------------------------------------------------------------------- dQ
+template <int D>
+struct QCfg {
+  static constexpr uint32_t CHUNK = 128 * 128, TILE = 128 * D * 2;
+  // K is read by S, and a whole elementwise pass later by dQ; V by dP only
+  static constexpr int KST = D == 128 ? 3 : 4, VST = D == 128 ? 2 : 4;
+  static constexpr uint32_t OFF_Q = 0, OFF_DO = TILE, OFF_K = 2 * TILE, OFF_V = OFF_K + KST * TILE,
+                            OFF_BAR = OFF_V + VST * TILE;
+  static constexpr size_t SMEM = OFF_BAR + 256 + 1024;
+  static constexpr uint32_t T_S = 0, T_DP = 128, T_DQ = 256, T_DS = 384, TMEM_COLS = 512;
+  static_assert(SMEM <= 232448, "");
+};
+
+template <int D, bool CAP>
+__global__ void __launch_bounds__(kThreads, 1)
+    spans_dq_kernel(const __grid_constant__ CUtensorMap tq,
+                    const __grid_constant__ CUtensorMap tdo,
+                    const __grid_constant__ CUtensorMap tk,
+                    const __grid_constant__ CUtensorMap tv, const __grid_constant__ Args ar) {
+  using C = QCfg<D>;
+  constexpr int KST = C::KST, VST = C::VST;
+  const SpanArgs& a = ar.a;
+  int* err = ar.err;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + C::OFF_BAR;
+  const uint32_t q_full = bar0, q_empty = bar0 + 8, k_full = bar0 + 16, k_empty = k_full + 8 * KST,
+                 v_full = k_empty + 8 * KST, v_empty = v_full + 8 * VST, s_full = v_empty + 8 * VST,
+                 s_free = s_full + 8, dp_full = s_free + 8, dp_free = dp_full + 8,
+                 ds_ready = dp_free + 8, ds_free = ds_ready + 16, dq_done = ds_free + 16,
+                 dq_free = dq_done + 8, drain = dq_free + 8;
+  static_assert(8 * (2 + 2 * KST + 2 * VST + 11) <= 248, "");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 248);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int chunks = (a.d + 63) / 64, used = ar.tl.per * a.rep;
+  const int64_t items = static_cast<int64_t>(ar.tl.tiles) * a.nkv;
+  // item -> row tile (the last first), key head; its first key and key tiles
+  auto place = [&](int64_t item, int& tile, int& g, int& first, int& n) {
+    tile = ar.tl.tiles - 1 - static_cast<int>(item / a.nkv);
+    g = static_cast<int>(item % a.nkv);
+    const TileSpan s = ar.tiles[tile];
+    first = s.first;
+    n = (s.end - s.first + 127) / 128;
+  };
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int x = 0; x < KST; ++x) {
+      mbar_init(k_full + 8 * x, 1);
+      mbar_init(k_empty + 8 * x, 1);
+    }
+    for (int x = 0; x < VST; ++x) {
+      mbar_init(v_full + 8 * x, 1);
+      mbar_init(v_empty + 8 * x, 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(s_free, kEltThreads);
+    mbar_init(dp_full, 1);
+    mbar_init(dp_free, kEltThreads);
+    // one for each buffer: a warp may be done with the next key tile before another is with
+    // this one
+    mbar_init(ds_ready, kEltThreads);
+    mbar_init(ds_ready + 8, kEltThreads);
+    mbar_init(ds_free, 1);
+    mbar_init(ds_free + 8, 1);
+    mbar_init(dq_done, 1);
+    mbar_init(dq_free, kEltThreads);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tq);
+    tma_prefetch_desc(&tdo);
+    tma_prefetch_desc(&tk);
+    tma_prefetch_desc(&tv);
+  }
+  if (warp == 1) tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  after_previous_kernel();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // --------------------------------------------------------- producer
+      bool ok = true;
+      uint32_t jg = 0;
+      int loaded = 0;
+      for (int64_t item = blockIdx.x; item < items && ok; item += gridDim.x) {
+        int tile, g, first, n;
+        place(item, tile, g, first, n);
+        if (n == 0) continue;
+        ok = mbar_wait(q_empty, (loaded & 1) ^ 1, err);
+        if (!ok) break;
+        mbar_arrive_expect_tx(q_full, 2 * chunks * used * 128);
+        for (int c = 0; c < chunks; ++c) {
+          tma_load_3d(sbase + C::OFF_Q + c * C::CHUNK, &tq, q_full, c * 64, g * a.rep,
+                      tile * ar.tl.per);
+          tma_load_3d(sbase + C::OFF_DO + c * C::CHUNK, &tdo, q_full, c * 64, g * a.rep,
+                      tile * ar.tl.per);
+        }
+        for (int j = 0; j < n && ok; ++j) {
+          const int ks = (jg + j) % KST, vs = (jg + j) % VST;
+          ok = mbar_wait(k_empty + 8 * ks, (((jg + j) / KST) & 1) ^ 1, err);
+          if (!ok) break;
+          mbar_arrive_expect_tx(k_full + 8 * ks, chunks * C::CHUNK);
+          for (int c = 0; c < chunks; ++c)
+            tma_load_3d(sbase + C::OFF_K + ks * C::TILE + c * C::CHUNK, &tk, k_full + 8 * ks,
+                        c * 64, g, first + j * 128);
+          ok = mbar_wait(v_empty + 8 * vs, (((jg + j) / VST) & 1) ^ 1, err);
+          if (!ok) break;
+          mbar_arrive_expect_tx(v_full + 8 * vs, chunks * C::CHUNK);
+          for (int c = 0; c < chunks; ++c)
+            tma_load_3d(sbase + C::OFF_V + vs * C::TILE + c * C::CHUNK, &tv, v_full + 8 * vs,
+                        c * 64, g, first + j * 128);
+        }
+        jg += n;
+        ++loaded;
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // -------------------------------------------------------------- MMA
+      constexpr uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0);
+      const uint32_t id_q = idesc_bf16_f32(128, a.d, 0, 1);
+      const int ksteps = a.d / 16;
+      const uint32_t q_desc = desc_low(sbase + C::OFF_Q, 16);
+      const uint32_t o_desc = desc_low(sbase + C::OFF_DO, 16);
+      auto scores = [&](uint32_t to, uint32_t rows, uint32_t keys) {
+        const uint32_t k2 = not_hoisted(desc_low(keys, 16));
+        rows = not_hoisted(rows);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          if (k >= ksteps) break;
+          const uint32_t off = ((k >> 2) * C::CHUNK + (k & 3) * 32) >> 4;
+          tc_mma_low(tmem + to, rows + off, k2 + off, id_s, k > 0);
+        }
+      };
+      bool ok = true;
+      uint32_t jg = 0;
+      int loaded = 0;
+      for (int64_t item = blockIdx.x; item < items && ok; item += gridDim.x) {
+        int tile, g, first, n;
+        place(item, tile, g, first, n);
+        if (n == 0) continue;
+        // S and dP of key tile j, each once its columns have been read
+        auto issue = [&](int j) -> bool {
+          const uint32_t jj = jg + j;
+          const int ks = jj % KST, vs = jj % VST;
+          if (!mbar_wait(k_full + 8 * ks, (jj / KST) & 1, err) ||
+              !mbar_wait(s_free, (jj & 1) ^ 1, err))
+            return false;
+          tc_fence_after();
+          scores(C::T_S, q_desc, sbase + C::OFF_K + ks * C::TILE);
+          tc_commit(s_full);
+          if (!mbar_wait(v_full + 8 * vs, (jj / VST) & 1, err) ||
+              !mbar_wait(dp_free, (jj & 1) ^ 1, err))
+            return false;
+          tc_fence_after();
+          scores(C::T_DP, o_desc, sbase + C::OFF_V + vs * C::TILE);
+          tc_commit(dp_full);
+          tc_commit(v_empty + 8 * vs);
+          if (j + 1 == n) tc_commit(q_empty);  // the item's last read of Q and dO
+          return true;
+        };
+        ok = mbar_wait(q_full, loaded & 1, err) && issue(0);
+        for (int j = 0; j < n && ok; ++j) {
+          const uint32_t jj = jg + j;
+          const int ks = jj % KST;
+          if (j + 1 < n) ok = issue(j + 1);
+          // dQ of the item before has been read out of TMEM
+          if (ok && j == 0) ok = mbar_wait(dq_free, (loaded & 1) ^ 1, err);
+          if (ok) ok = mbar_wait(ds_ready + 8 * (jj & 1), (jj >> 1) & 1, err);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t k_desc = not_hoisted(desc_low(sbase + C::OFF_K + ks * C::TILE, C::CHUNK));
+          const uint32_t ds = tmem + C::T_DS + (jj & 1) * 64;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            tc_mma_ts_low(tmem + C::T_DQ, ds + 8 * k, k_desc + k * 128, id_q, (j | k) != 0);
+          tc_commit(ds_free + 8 * (jj & 1));
+          tc_commit(k_empty + 8 * ks);
+        }
+        if (ok) tc_commit(dq_done);
+        jg += n;
+        ++loaded;
+      }
+      tc_commit(drain);
+      mbar_wait(drain, 0, nullptr);
+    }
+  } else if (warp >= 4) {
+    // --------------------------- dS: one row, 32 of a key tile's 128 columns
+    const int quarter = warp & 3, block = (warp - 4) >> 2;
+    const int row = quarter * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    const int row_t = row / a.rep, row_h = row % a.rep;
+    bool ok = true;
+    uint32_t jg = 0;
+    int loaded = 0;
+    for (int64_t item = blockIdx.x; item < items && ok; item += gridDim.x) {
+      int tile, g, first, n;
+      place(item, tile, g, first, n);
+      const int t = tile * ar.tl.per + row_t, h = g * a.rep + row_h;
+      const bool real = row_t < ar.tl.per && t < a.queries;
+      const int64_t at = (static_cast<int64_t>(g) * ar.tl.tiles + tile) * 128 + row;
+      const float nl = ar.neg_lse[at], nd = ar.neg_d[at];
+      const int lo = ar.lo[tile * int64_t{128} + row], len = ar.len[tile * int64_t{128} + row];
+      const float2 nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
+      for (int j = 0; j < n; ++j) {
+        const uint32_t jj = jg + j;
+        const int buf = jj & 1;
+        ok = warp_wait(s_full, jj & 1, err);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t sv[32], pk[16];
+        tmem_ld32(tmem + lane_base + C::T_S + block * 32, sv);
+        tmem_ld_wait();
+        tc_fence_before();
+        mbar_arrive(s_free);
+        // columns l <= c < l + len are seen; a row that sees nothing has p = 0 as it is
+        const int l = lo - (first + j * 128 + block * 32);
+        const bool full = __all_sync(0xffffffffu, len == 0 || (l <= 0 && l + len >= 32));
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          float2 slope;
+          float2 p = p_of<CAP>(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), ar,
+                               nl2, slope);
+          if constexpr (CAP) p = mul2(p, slope);
+          sv[c] = __float_as_uint(p.x);
+          sv[c + 1] = __float_as_uint(p.y);
+        }
+        ok = warp_wait(dp_full, jj & 1, err);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          uint32_t dp[16];
+          tmem_ld16(tmem + lane_base + C::T_DP + block * 32 + 16 * x, dp);
+          tmem_ld_wait();
+          if (x == 1) {
+            tc_fence_before();
+            mbar_arrive(dp_free);
+          }
+#pragma unroll
+          for (int c = 0; c < 16; c += 2) {
+            float2 ds = add2(make_float2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])), nd2);
+            ds = mul2(ds, make_float2(__uint_as_float(sv[16 * x + c]),
+                                      __uint_as_float(sv[16 * x + c + 1])));
+            if (!full) {
+              if (static_cast<uint32_t>(16 * x + c - l) >= static_cast<uint32_t>(len)) ds.x = 0.f;
+              if (static_cast<uint32_t>(16 * x + c + 1 - l) >= static_cast<uint32_t>(len))
+                ds.y = 0.f;
+            }
+            pk[8 * x + c / 2] = pack_bf16x2(ds.x, ds.y);
+          }
+        }
+        // this buffer was last read by dQ += dS K two key tiles ago
+        ok = warp_wait(ds_free + 8 * buf, ((jj >> 1) & 1) ^ 1, err);
+        if (!ok) break;
+        tc_fence_after();
+        tmem_st16(tmem + lane_base + C::T_DS + buf * 64 + block * 16, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(ds_ready + 8 * buf);
+      }
+      if (!ok) break;
+      uint32_t r[32];
+      const int c0 = block * 32, left = a.d - c0;
+      if (n > 0) {
+        if (!warp_wait(dq_done, loaded & 1, err)) break;
+        tc_fence_after();
+        if (left > 0) {
+          tmem_ld32(tmem + lane_base + C::T_DQ + c0, r);
+          tmem_ld_wait();
+        }
+        tc_fence_before();
+        mbar_arrive(dq_free);
+        ++loaded;
+        jg += n;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) r[e] = 0u;
+      }
+      if (left > 0) {
+        if (real) put_columns(a.dq.at(t, h) + c0, r, a.scale, left);
+        for (unsigned again = __ballot_sync(0xffffffffu, real && !all_finite(r, left)); again;
+             again &= again - 1) {
+          const int from = __ffs(again) - 1;
+          row_dq(a, __shfl_sync(0xffffffffu, t, from), __shfl_sync(0xffffffffu, h, from), c0,
+                 min(c0 + 32, a.d));
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  settle(err);
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// -------------------------------------------------------------------- host
+template <int D, bool CAP>
+cudaError_t launch(const Args& ar, cudaStream_t s) {
+  const SpanArgs& a = ar.a;
+  CUtensorMap tq, tdo, tk, tv;
+  if (!make_tma_heads(&tq, a.q.p, a.queries, a.nh, a.d, a.q.ts, a.q.hs, a.rep, ar.tl.per) ||
+      !make_tma_heads(&tdo, a.d_o.p, a.queries, a.nh, a.d, a.d_o.ts, a.d_o.hs, a.rep, ar.tl.per) ||
+      !make_tma_heads(&tk, a.k.p, a.keys, a.nkv, a.d, a.k.ts, a.k.hs, 1, 128) ||
+      !make_tma_heads(&tv, a.v.p, a.keys, a.nkv, a.d, a.v.ts, a.v.hs, 1, 128))
+    return cudaErrorInvalidValue;
+  cudaError_t e = allow_smem(spans_dkdv_kernel<D, CAP>, KvCfg<D>::SMEM);
+  if (e == cudaSuccess) e = allow_smem(spans_dq_kernel<D, CAP>, QCfg<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  const int64_t rows = static_cast<int64_t>(a.nkv) * ar.tl.tiles * 128;
+  const int64_t prep = ar.groups + std::min<int64_t>((rows + 63) / 64, int64_t{num_sms()} * 8);
+  e = launch_overlapping(prepare_kernel, prep, kPrepThreads, 0, s, ar);
+  if (e != cudaSuccess) return e;
+  e = launch_overlapping(spans_dkdv_kernel<D, CAP>,
+                         static_cast<int64_t>((a.keys + 127) / 128) * a.nkv, kThreads,
+                         KvCfg<D>::SMEM, s, tq, tdo, tk, tv, ar);
+  if (e != cudaSuccess) return e;
+  return launch_overlapping(
+      spans_dq_kernel<D, CAP>,
+      std::min<int64_t>(static_cast<int64_t>(ar.tl.tiles) * a.nkv, num_sms()), kThreads,
+      QCfg<D>::SMEM, s, tq, tdo, tk, tv, ar);
+}
+
+// The workspace: rows' values, spans of rows, of tiles, of groups.
+size_t lay_out(Args* ar, int queries, int rep, int nkv, void* ws) {
+  ar->tl = Tiling::of(queries, rep);
+  ar->groups = (ar->tl.tiles + kGroup - 1) / kGroup;
+  const size_t rows = static_cast<size_t>(ar->tl.tiles) * 128;
+  uint8_t* p = static_cast<uint8_t*>(ws);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* here = p + at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  ar->neg_lse = reinterpret_cast<float*>(take(rows * nkv * sizeof(float)));
+  ar->neg_d = reinterpret_cast<float*>(take(rows * nkv * sizeof(float)));
+  ar->lo = reinterpret_cast<int*>(take(rows * sizeof(int)));
+  ar->len = reinterpret_cast<int*>(take(rows * sizeof(int)));
+  ar->tiles = reinterpret_cast<TileSpan*>(take(ar->tl.tiles * sizeof(TileSpan)));
+  ar->group = reinterpret_cast<int2*>(take(ar->groups * sizeof(int2)));
+  return at;
+}
+
+}  // namespace
+
+size_t backward_workspace(int queries, int nh, int nkv) {
+  Args ar = {};
+  return lay_out(&ar, queries, nh / nkv, nkv, nullptr);
+}
+
+cudaError_t backward_tiles(const SpanArgs& a, void* ws, cudaStream_t s) {
+  Args ar = {};
+  ar.a = a;
+  lay_out(&ar, a.queries, a.rep, a.nkv, ws);
+  ar.to_tanh = a.cap > 0.f ? a.scale / a.cap : 0.f;
+  ar.scale_log2 = (a.cap > 0.f ? a.cap : a.scale) * kLog2e;
+  ar.err = device_error_ptr();
+  if (a.d <= 64) return a.cap > 0.f ? launch<64, true>(ar, s) : launch<64, false>(ar, s);
+  return a.cap > 0.f ? launch<128, true>(ar, s) : launch<128, false>(ar, s);
+}
+
+}  // namespace rdt

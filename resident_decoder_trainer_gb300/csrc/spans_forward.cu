@@ -58,8 +58,7 @@ struct Cfg {
   static constexpr uint32_t TILE = 128 * D * 2;
   static constexpr int KS = D == 128 ? 2 : 4, VS = KS;
   static constexpr uint32_t OFF_Q = 0, OFF_K = OFF_Q + 2 * TILE, OFF_V = OFF_K + KS * TILE,
-                            OFF_MEM = OFF_V + VS * TILE,  // 8 warps x kMaxDim floats
-      OFF_ITEM = OFF_MEM + 8 * kMaxDim * 4, OFF_BAR = OFF_ITEM + kItemRing * sizeof(Item);
+                            OFF_ITEM = OFF_V + VS * TILE, OFF_BAR = OFF_ITEM + kItemRing * sizeof(Item);
   static constexpr size_t SMEM = OFF_BAR + 512 + 1024;
   static constexpr uint32_t TMEM_S = 0, TMEM_O = 256, TMEM_COLS = 512;
   static_assert(TMEM_O + 2 * D <= TMEM_COLS && SMEM <= 232448 && OFF_BAR % 8 == 0, "");
@@ -223,12 +222,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto issue_s = [&](int x, int j) {
           const uint32_t kb = sbase + C::OFF_K + ((jg + j) % KS) * C::TILE;
           const uint32_t qb = sbase + C::OFF_Q + x * C::TILE;
-          const uint64_t kd = sdesc_sw128(kb, 16, 1024), qd = sdesc_sw128(qb, 16, 1024);
+          const uint32_t kd = not_hoisted(desc_low(kb, 16)), qd = not_hoisted(desc_low(qb, 16));
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             if (k >= ksteps) break;
             const uint32_t off = ((k >> 2) * C::CHUNK + (k & 3) * 32) >> 4;
-            tc_mma_bf16(tmem + C::TMEM_S + x * BN, qd + off, kd + off, idesc_s, k > 0);
+            tc_mma_low(tmem + C::TMEM_S + x * BN, qd + off, kd + off, idesc_s, k > 0);
           }
           tc_commit(s_full + 8 * x);
         };
@@ -242,14 +241,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int jj = jg + j, vs = jj % VS;
           if (j == d.begin[x] && !mbar_wait(o_free + 8 * x, (rounds[x] & 1) ^ 1, err))
             return false;
-          const uint64_t vd = sdesc_sw128(sbase + C::OFF_V + vs * C::TILE, C::CHUNK, 1024);
+          const uint32_t vd = not_hoisted(desc_low(sbase + C::OFF_V + vs * C::TILE, C::CHUNK));
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             if (!mbar_wait(p_full + 16 * x + 8 * half, pv[x] & 1, err)) return false;
             tc_fence_after();
 #pragma unroll
             for (int k = 4 * half; k < 4 * half + 4; ++k)
-              tc_mma_bf16_ts(tmem + C::TMEM_O + x * D, tmem + C::TMEM_S + x * BN + k * 8,
+              tc_mma_ts_low(tmem + C::TMEM_O + x * D, tmem + C::TMEM_S + x * BN + k * 8,
                              vd + k * 128, idesc_o, j > d.begin[x] || k > 0);
           }
           ++pv[x];
@@ -296,7 +295,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lane_base + C::TMEM_S + x * BN;
     const uint32_t t_o = tmem + lane_base + C::TMEM_O + x * D;
-    float* mem = reinterpret_cast<float*>(smem + C::OFF_MEM) + (warp - 4) * kMaxDim;
     const int row_t = row / a.rep, row_h = row % a.rep;
     const float2 sc2 = make_float2(ar.scale_log2, ar.scale_log2);
     bool ok = true;
@@ -434,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (unsigned again = __ballot_sync(0xffffffffu, real && bad != 0.f); again;
              again &= again - 1) {
           const int from = __ffs(again) - 1;
-          row_forward(a, mem, __shfl_sync(0xffffffffu, t, from),
+          row_forward(a, __shfl_sync(0xffffffffu, t, from),
                       __shfl_sync(0xffffffffu, h, from), false);
         }
       }
@@ -511,7 +509,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
         make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
   }
   if (lane == 0 && a.lse) a.lse[th] = total != 0.f ? (top + log2f(total)) * kLn2 : -INFINITY;
-  if (__any_sync(0xffffffffu, bad)) row_forward(a, sums[1], t, h, false);
+  if (__any_sync(0xffffffffu, bad)) row_forward(a, t, h, false);
 }
 
 constexpr int kMinKeysOfSplit = 256;
