@@ -325,6 +325,32 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Work of a grid with one CTA per item, taken by the CTAs that run: asks for the
+// index of a CTA that has not started yet, which then never does. 16 bytes at
+// `dst` (16-byte aligned), completion on an mbarrier.
+__device__ __forceinline__ void next_cta_request(uint32_t dst, uint32_t bar) {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the last answer has been read
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], "
+      "[%1];" ::"r"(dst),
+      "r"(bar)
+      : "memory");
+}
+// The answer: blockIdx.x of that CTA, or -1 if none was left.
+__device__ __forceinline__ int next_cta_answer(uint32_t src) {
+  uint32_t got, x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t.reg .b32 y, z, w;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\tmov.b32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, h;\n\t}"
+      : "=r"(got), "=r"(x)
+      : "r"(src)
+      : "memory");
+  return got ? static_cast<int>(x) : -1;
+}
 // Register budget of a warpgroup (all its warps execute it).
 template <int N>
 __device__ __forceinline__ void regs_dec() {

@@ -148,14 +148,8 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_cons
 // the slope 1 - tanh^2 is left in `slope`.
 template <bool CAP>
 __device__ __forceinline__ float2 p_of(float2 s, const Args& ar, float2 neg_lse, float2& slope) {
-  const float2 k = make_float2(ar.scale_log2, ar.scale_log2);
-  if constexpr (CAP) {
-    const float w = 2.f * kLog2e * ar.to_tanh;
-    s.x = fmaf(-2.f, rcp_approx(1.f + ex2_approx(s.x * w)), 1.f);
-    s.y = fmaf(-2.f, rcp_approx(1.f + ex2_approx(s.y * w)), 1.f);
-    slope = fma2(make_float2(-s.x, -s.y), s, make_float2(1.f, 1.f));
-  }
-  float2 p = fma2(s, k, neg_lse);
+  if constexpr (CAP) slope = fma2(make_float2(-s.x, -s.y), s, make_float2(1.f, 1.f));
+  float2 p = fma2(s, make_float2(ar.scale_log2, ar.scale_log2), neg_lse);
   p.x = ex2_approx(p.x);
   p.y = ex2_approx(p.y);
   return p;
@@ -459,6 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tmem_ld_wait();
+      if constexpr (CAP) tanh_all(sv, ar.to_tanh);
       // sv: p, times the cap's slope
 #pragma unroll
       for (int c = 0; c < 32; c += 4) {
@@ -770,6 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_wait();
         tc_fence_before();
         mbar_arrive(s_free);
+        if constexpr (CAP) tanh_all(sv, ar.to_tanh);
         // columns l <= c < l + len are seen; a row that sees nothing has p = 0 as it is
         const int l = lo - (first + j * 128 + block * 32);
         const bool full = __all_sync(0xffffffffu, len == 0 || (l <= 0 && l + len >= 32));

@@ -2,7 +2,9 @@
 // tensor cores: S = Q K^T and O += P V by tcgen05.mma with accumulators in
 // TMEM, operands by TMA, softmax in registers.
 //
-// A CTA walks work items, one item being two tiles (A, B) of 128 rows of one
+// One CTA of the grid for each work item; a CTA that runs takes the items of
+// those that have not started, one after the other, so that short and long
+// spans even out over the SMs. An item is two tiles (A, B) of 128 rows of one
 // key head (spans.cuh) that share their K and V tiles of 128 keys. The key
 // tiles start at the least key that a row of the item sees, wherever that is.
 // Warps: 0 loads (and finds each item's spans, a few items ahead of the
@@ -17,7 +19,6 @@
 // A row whose O is not finite is computed again key by key (row_forward): a NaN
 // or infinity in a value that the row does not see, times p = 0, would reach it.
 #include <algorithm>
-#include <atomic>
 
 #include "spans.cuh"
 
@@ -33,6 +34,7 @@ constexpr int kItemReaders = 1 + 8;  // MMA thread, softmax warps
 
 // What the loading warp found out about an item.
 struct Item {
+  int index;     // of the item; -1: no more
   int first;     // first key of key tile 0
   int n;         // key tiles, of both row tiles together
   int begin[2];  // key tiles [begin, end) of each row tile; begin == end: none
@@ -43,7 +45,6 @@ struct Args {
   SpanArgs a;
   Tiling tl;
   int pairs, splits;
-  int64_t items;
   float to_tanh;     // scale / cap
   float scale_log2;  // of what is exponentiated: scale log2 e, or cap log2 e
   float* part_o;     // splits > 1: fp32 [splits][queries][nh][d] and lse (base 2)
@@ -58,20 +59,12 @@ struct Cfg {
   static constexpr uint32_t TILE = 128 * D * 2;
   static constexpr int KS = D == 128 ? 2 : 4, VS = KS;
   static constexpr uint32_t OFF_Q = 0, OFF_K = OFF_Q + 2 * TILE, OFF_V = OFF_K + KS * TILE,
-                            OFF_ITEM = OFF_V + VS * TILE, OFF_BAR = OFF_ITEM + kItemRing * sizeof(Item);
+                            OFF_NEXT = OFF_V + VS * TILE, OFF_ITEM = OFF_NEXT + 16,
+                            OFF_BAR = OFF_ITEM + kItemRing * sizeof(Item);
   static constexpr size_t SMEM = OFF_BAR + 512 + 1024;
   static constexpr uint32_t TMEM_S = 0, TMEM_O = 256, TMEM_COLS = 512;
   static_assert(TMEM_O + 2 * D <= TMEM_COLS && SMEM <= 232448 && OFF_BAR % 8 == 0, "");
 };
-
-// sv = tanh(to_tanh sv) of 1 - 2 / (1 + e^2x): off by a few 2^-23.
-__device__ __forceinline__ void tanh_all(uint32_t (&sv)[128], float to_tanh) {
-  const float w = 2.f * kLog2e * to_tanh;
-#pragma unroll
-  for (int c = 0; c < 128; ++c)
-    sv[c] = __float_as_uint(
-        fmaf(-2.f, rcp_approx(1.f + ex2_approx(__uint_as_float(sv[c]) * w)), 1.f));
-}
 
 template <int D, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -87,28 +80,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bar0 = sbase + C::OFF_BAR;
-  const uint32_t q_full = bar0, q_empty = bar0 + 8, k_full = bar0 + 16, k_empty = k_full + 8 * KS,
+  const uint32_t q_full = bar0, q_empty = bar0 + 16, k_full = bar0 + 32, k_empty = k_full + 8 * KS,
                  v_full = k_empty + 8 * KS, v_empty = v_full + 8 * VS, s_full = v_empty + 8 * VS,
                  p_full = s_full + 16,  // [tile][half]
       o_done = p_full + 32, o_free = o_done + 16, item_full = o_free + 16,
-                 item_empty = item_full + 8 * kItemRing, drain = item_empty + 8 * kItemRing;
+                 item_empty = item_full + 8 * kItemRing, drain = item_empty + 8 * kItemRing,
+                 next = drain + 8;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 448);
-  static_assert(8 * (2 + 2 * KS + 2 * VS + 2 + 4 + 2 + 2 + 2 * kItemRing + 1) <= 448, "");
+  static_assert(8 * (4 + 2 * KS + 2 * VS + 2 + 4 + 2 + 2 + 2 * kItemRing + 2) <= 448, "");
   Item* ring = reinterpret_cast<Item*>(smem + C::OFF_ITEM);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int chunks = (a.d + 63) / 64;
   // item -> pair (the last queries, whose spans are often the longest, first), key head, split
-  auto place = [&](int64_t item, int& t0, int& g, int& split) {
-    split = static_cast<int>(item % ar.splits);
-    const int64_t x = item / ar.splits;
-    g = static_cast<int>(x % a.nkv);
-    t0 = (ar.pairs - 1 - static_cast<int>(x / a.nkv)) * 2 * ar.tl.per;
+  auto place = [&](int item, int& t0, int& g, int& split) {
+    split = item % ar.splits;
+    const int x = item / ar.splits;
+    g = x % a.nkv;
+    t0 = (ar.pairs - 1 - x / a.nkv) * 2 * ar.tl.per;
   };
 
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
     for (int x = 0; x < KS; ++x) {
       mbar_init(k_full + 8 * x, 1);
       mbar_init(k_empty + 8 * x, 1);
@@ -116,6 +108,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(v_empty + 8 * x, 1);
     }
     for (int x = 0; x < 2; ++x) {
+      mbar_init(q_full + 8 * x, 1);
+      mbar_init(q_empty + 8 * x, 1);
       mbar_init(s_full + 8 * x, 1);
       mbar_init(p_full + 16 * x, 128);
       mbar_init(p_full + 16 * x + 8, 128);
@@ -127,6 +121,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(item_empty + 8 * x, kItemReaders);
     }
     mbar_init(drain, 1);
+    mbar_init(next, 1);
     fence_mbar_init();
     tma_prefetch_desc(&tq);
     tma_prefetch_desc(&tk);
@@ -145,14 +140,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------- producer
       bool ok = true;
       int jg = 0, loaded = 0;  // key tiles and items with any so far
-      int it = 0;
-      for (int64_t item = blockIdx.x; item < ar.items && ok; item += gridDim.x, ++it) {
+      int item = blockIdx.x;
+      for (int it = 0; ok; ++it) {
+        const int slot = it % kItemRing;
+        ok = warp_wait(item_empty + 8 * slot, ((it / kItemRing) & 1) ^ 1, err);
+        if (!ok) break;
+        if (item < 0) {
+          if (lane == 0) {
+            ring[slot].index = -1;
+            mbar_arrive(item_full + 8 * slot);
+          }
+          break;
+        }
+        if (lane == 0) next_cta_request(sbase + C::OFF_NEXT, next);
         int t0, g, split;
         place(item, t0, g, split);
         int lo[2], hi[2];
-        span_of_queries(a, t0, t0 + ar.tl.per, lo[0], hi[0]);
-        span_of_queries(a, t0 + ar.tl.per, t0 + 2 * ar.tl.per, lo[1], hi[1]);
+        spans_of_tiles(a, ar.tl, t0, lo, hi);
         Item d;
+        d.index = item;
         d.first = lo[0] >= hi[0] ? lo[1] : lo[1] >= hi[1] ? lo[0] : min(lo[0], lo[1]);
         const int all = (max(hi[0], hi[1]) - d.first + BN - 1) / BN;
         const int from = static_cast<int>(static_cast<int64_t>(all) * split / ar.splits);
@@ -166,23 +172,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             d.begin[x] = d.end[x] = 0;
         }
         if (d.end[0] == 0 && d.end[1] == 0) d.n = 0;
-        const int slot = it % kItemRing;
-        ok = warp_wait(item_empty + 8 * slot, ((it / kItemRing) & 1) ^ 1, err);
-        if (!ok) break;
         if (lane == 0) {
           ring[slot] = d;
           mbar_arrive(item_full + 8 * slot);
         }
-        if (d.n == 0) continue;
-        if (lane == 0) {
-          ok = mbar_wait(q_empty, (loaded & 1) ^ 1, err);
-          if (ok) {
-            mbar_arrive_expect_tx(q_full, 2 * chunks * (ar.tl.per * a.rep * 128));
-            for (int x = 0; x < 2; ++x)
-              for (int c = 0; c < chunks; ++c)
-                tma_load_3d(sbase + C::OFF_Q + x * C::TILE + c * C::CHUNK, &tq, q_full, c * 64,
-                            g * a.rep, t0 + x * ar.tl.per);
-          }
+        if (d.n > 0 && lane == 0) {
           auto load = [&](int j, uint32_t full, uint32_t empty, int stages, uint32_t off,
                           const CUtensorMap* map) -> bool {
             const int jj = jg + j, st = jj % stages;
@@ -193,7 +187,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                           d.first + j * BN);
             return true;
           };
-          for (int j = 0; j < KS - 1 && j < d.n && ok; ++j)
+          // K's first tile does not wait for the item before to be done with its Q
+          ok = load(0, k_full, k_empty, KS, C::OFF_K, &tk);
+          for (int x = 0; x < 2 && ok; ++x) {
+            ok = mbar_wait(q_empty + 8 * x, (loaded & 1) ^ 1, err);
+            if (!ok) break;
+            mbar_arrive_expect_tx(q_full + 8 * x, chunks * (ar.tl.per * a.rep * 128));
+            for (int c = 0; c < chunks; ++c)
+              tma_load_3d(sbase + C::OFF_Q + x * C::TILE + c * C::CHUNK, &tq, q_full + 8 * x,
+                          c * 64, g * a.rep, t0 + x * ar.tl.per);
+          }
+          for (int j = 1; j < KS - 1 && j < d.n && ok; ++j)
             ok = load(j, k_full, k_empty, KS, C::OFF_K, &tk);
           for (int j = 0; j < d.n && ok; ++j) {
             if (j + KS - 1 < d.n) ok = load(j + KS - 1, k_full, k_empty, KS, C::OFF_K, &tk);
@@ -201,8 +205,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0);
-        jg += d.n;
-        ++loaded;
+        if (d.n > 0) {
+          jg += d.n;
+          ++loaded;
+        }
+        // waited for on the way out too: the answer is written to this CTA's memory
+        const bool answered = warp_wait(next, it & 1, err);
+        ok = ok && answered;
+        if (ok) item = next_cta_answer(sbase + C::OFF_NEXT);
       }
     } else if (warp == 1 && lane == 0) {
       // ------------------------------------------------------------ MMA
@@ -212,11 +222,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int jg = 0, loaded = 0, it = 0;
       int pv[2] = {0, 0}, rounds[2] = {0, 0};  // P V issued; items with any, of each tile
-      for (int64_t item = blockIdx.x; item < ar.items && ok; item += gridDim.x, ++it) {
+      for (; ok; ++it) {
         const int slot = it % kItemRing;
         if (!mbar_wait(item_full + 8 * slot, (it / kItemRing) & 1, err)) break;
         const Item d = ring[slot];
         mbar_arrive(item_empty + 8 * slot);
+        if (d.index < 0) break;
         if (d.n == 0) continue;
         auto active = [&](int x, int j) { return j >= d.begin[x] && j < d.end[x]; };
         auto issue_s = [&](int x, int j) {
@@ -230,6 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_mma_low(tmem + C::TMEM_S + x * BN, qd + off, kd + off, idesc_s, k > 0);
           }
           tc_commit(s_full + 8 * x);
+          if (j + 1 == d.end[x]) tc_commit(q_empty + 8 * x);  // the item's last read of its Q
         };
         auto wait_k = [&](int j) -> bool {
           const int jj = jg + j;
@@ -258,12 +270,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           return true;
         };
-        ok = mbar_wait(q_full, loaded & 1, err) && wait_k(0);
-        if (!ok) break;
-        for (int x = 0; x < 2; ++x)
+        // the tiles' Q are waited for even where no key tile is theirs
+        ok = wait_k(0);
+        for (int x = 0; x < 2 && ok; ++x) {
+          ok = mbar_wait(q_full + 8 * x, loaded & 1, err);
+          if (!ok) break;
+          tc_fence_after();
           if (active(x, 0)) issue_s(x, 0);
+          if (d.end[x] == 0) mbar_arrive(q_empty + 8 * x);
+        }
+        if (!ok) break;
         tc_commit(k_empty + 8 * (jg % KS));
-        if (d.n == 1) tc_commit(q_empty);
         for (int j = 0; j < d.n && ok; ++j) {
           // waited for even where no row tile reads it: its place is free only once it is there
           ok = mbar_wait(v_full + 8 * ((jg + j) % VS), ((jg + j) / VS) & 1, err);
@@ -276,10 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!ok) break;
           tc_commit(v_empty + 8 * ((jg + j) % VS));
-          if (j + 1 < d.n) {
-            tc_commit(k_empty + 8 * ((jg + j + 1) % KS));
-            if (j + 2 == d.n) tc_commit(q_empty);  // the item's last Q K^T
-          }
+          if (j + 1 < d.n) tc_commit(k_empty + 8 * ((jg + j + 1) % KS));
         }
         jg += d.n;
         ++loaded;
@@ -299,18 +313,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float2 sc2 = make_float2(ar.scale_log2, ar.scale_log2);
     bool ok = true;
     int jx = 0, rounds = 0, it = 0;
-    for (int64_t item = blockIdx.x; item < ar.items && ok; item += gridDim.x, ++it) {
+    for (; ok; ++it) {
+      const int slot = it % kItemRing;
+      if (!warp_wait(item_full + 8 * slot, (it / kItemRing) & 1, err)) break;
+      const int item = ring[slot].index, first = ring[slot].first, begin = ring[slot].begin[x],
+                end = ring[slot].end[x];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(item_empty + 8 * slot);
+      if (item < 0) break;
       int t0, g, split;
       place(item, t0, g, split);
       const int t = t0 + x * ar.tl.per + row_t, h = g * a.rep + row_h;
       const bool real = row_t < ar.tl.per && t < a.queries;
       int lo = 0, hi = INT32_MAX;  // a row that is none needs no mask
       if (real) a.span(t, lo, hi);
-      const int slot = it % kItemRing;
-      if (!warp_wait(item_full + 8 * slot, (it / kItemRing) & 1, err)) break;
-      const int first = ring[slot].first, begin = ring[slot].begin[x], end = ring[slot].end[x];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(item_empty + 8 * slot);
       float m_run = -INFINITY, l_run = 0.f;
       for (int j = begin; j < end; ++j, ++jx) {
         if (!warp_wait(s_full + 8 * x, jx & 1, err)) {
@@ -386,40 +402,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int64_t th = static_cast<int64_t>(t) * a.nh + h;
       const float inv = l_run != 0.f ? 1.f / l_run : 0.f;
+      const bool some = l_run != 0.f;  // else p was 0 throughout: 0 times what was not seen
       float bad = 0.f;
 #pragma unroll 1
-      for (int c = 0; c < a.d; c += 16) {
-        uint32_t ov[16];
+      for (int c0 = 0; c0 < a.d; c0 += 32) {
+        uint32_t ov[32];
         if (begin < end) {
-          tmem_ld16(t_o + c, ov);
+          tmem_ld32(t_o + c0, ov);
           tmem_ld_wait();
+          if (c0 + 32 >= a.d) {  // this O is free for the next item
+            tc_fence_before();
+            mbar_arrive(o_free + 8 * x);
+          }
         }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          // a row that saw nothing has p = 0 throughout, but 0 times what was not seen
-          const float v = l_run != 0.f ? __uint_as_float(ov[e]) * inv : 0.f;
-          bad = fmaf(v, 0.f, bad);
-          ov[e] = __float_as_uint(v);
-        }
-        if (real && ar.splits > 1) {
-          float* out = ar.part_o + (static_cast<int64_t>(split) * a.queries * a.nh + th) * a.d + c;
+        for (int c = 0; c < 32; c += 16) {
+          if (c0 + c >= a.d) break;
 #pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<uint4*>(out + e) = make_uint4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
-        } else if (real) {
-          bf16* out = a.o.at(t, h) + c;
+          for (int e = c; e < c + 16; ++e) {
+            const float v = some ? __uint_as_float(ov[e]) * inv : 0.f;
+            bad = fmaf(v, 0.f, bad);
+            ov[e] = __float_as_uint(v);
+          }
+          if (real && ar.splits > 1) {
+            float* out =
+                ar.part_o + (static_cast<int64_t>(split) * a.queries * a.nh + th) * a.d + c0 + c;
 #pragma unroll
-          for (int e = 0; e < 16; e += 8)
-            *reinterpret_cast<uint4*>(out + e) = make_uint4(
-                pack_bf16x2(__uint_as_float(ov[e]), __uint_as_float(ov[e + 1])),
-                pack_bf16x2(__uint_as_float(ov[e + 2]), __uint_as_float(ov[e + 3])),
-                pack_bf16x2(__uint_as_float(ov[e + 4]), __uint_as_float(ov[e + 5])),
-                pack_bf16x2(__uint_as_float(ov[e + 6]), __uint_as_float(ov[e + 7])));
+            for (int e = 0; e < 16; e += 4)
+              *reinterpret_cast<uint4*>(out + e) =
+                  make_uint4(ov[c + e], ov[c + e + 1], ov[c + e + 2], ov[c + e + 3]);
+          } else if (real) {
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              w[e] =
+                  pack_bf16x2(__uint_as_float(ov[c + 2 * e]), __uint_as_float(ov[c + 2 * e + 1]));
+            bf16* out = a.o.at(t, h) + c0 + c;
+            *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(out + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+          }
         }
-      }
-      if (begin < end) {  // this O is free for the next item
-        tc_fence_before();
-        mbar_arrive(o_free + 8 * x);
       }
       const float lse2 = l_run != 0.f ? m_run + log2f(l_run) : -INFINITY;
       if (real) {
@@ -524,8 +546,8 @@ cudaError_t launch(const Args& ar, cudaStream_t s) {
     return cudaErrorInvalidValue;
   const cudaError_t e = allow_smem(spans_forward_kernel<D, CAP>, Cfg<D>::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_overlapping(spans_forward_kernel<D, CAP>, std::min<int64_t>(ar.items, num_sms()),
-                            kThreads, Cfg<D>::SMEM, s, tq, tk, tv, ar);
+  return launch_overlapping(spans_forward_kernel<D, CAP>,
+                            static_cast<int64_t>(ar.pairs) * a.nkv * ar.splits, kThreads, Cfg<D>::SMEM, s, tq, tk, tv, ar);
 }
 
 }  // namespace
@@ -549,7 +571,6 @@ cudaError_t forward_tiles(const SpanArgs& a, void* ws, cudaStream_t s) {
   ar.tl = Tiling::of(a.queries, a.rep);
   ar.pairs = (ar.tl.tiles + 1) / 2;
   ar.splits = forward_splits(a.queries, a.keys, a.nkv, a.rep);
-  ar.items = static_cast<int64_t>(ar.pairs) * a.nkv * ar.splits;
   ar.to_tanh = a.cap > 0.f ? a.scale / a.cap : 0.f;
   ar.scale_log2 = (a.cap > 0.f ? a.cap : a.scale) * kLog2e;
   const int64_t rows = static_cast<int64_t>(a.queries) * a.nh;
