@@ -23,7 +23,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_forward_kernel(const SpanArg
   const int64_t rows = static_cast<int64_t>(a.queries) * a.nh;
   for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRowWarps + warp; r < rows;
        r += static_cast<int64_t>(gridDim.x) * kRowWarps)
-    row_forward(a, static_cast<int>(r / a.nh), static_cast<int>(r % a.nh), true);
+    row_forward(a, static_cast<int>(r / a.nh), static_cast<int>(r % a.nh), 0, a.d, true);
 }
 
 // The rows of dq, then those of dk and dv, in one grid.

@@ -102,6 +102,24 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int* er
   }
 }
 
+// The same for threads that issue work: what follows a first look that fails is
+// one function for all of their waits, so that their loops stay short.
+__device__ __noinline__ static bool wait_longer(uint32_t bar, uint32_t parity, int* err) {
+  return mbar_wait(bar, parity, err);
+}
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, int* err) {
+  return mbar_try_wait(bar, parity) || wait_longer(bar, parity, err);
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // Warp-uniform bounded wait: every lane waits, and the warp proceeds only if
 // all lanes saw the phase complete (so warp-collective tcgen05 accesses that
 // follow are never executed by a partial warp).
@@ -172,6 +190,17 @@ __device__ __forceinline__ void bulk_load_1d(uint32_t dst, const void* src, uint
 // Named barrier over `count` threads (a multiple of 32) with id 1..15.
 __device__ __forceinline__ void named_bar_sync(int id, int count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+// The same, and whether any of the threads brought `mine`.
+__device__ __forceinline__ bool named_bar_any(int id, int count, bool mine) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(id), "r"(count), "r"(static_cast<uint32_t>(mine))
+      : "memory");
+  return any != 0;
 }
 
 // ------------------------------------------------------------------- tcgen05

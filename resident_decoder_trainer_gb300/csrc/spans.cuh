@@ -82,7 +82,8 @@ __device__ __forceinline__ void put_row(bf16* dst, const float (&acc)[4], float 
 }
 
 // o of query t, head h, and its lse where `with_lse`.
-__device__ __noinline__ static void row_forward(const SpanArgs& a, int t, int h, bool with_lse) {
+__device__ __noinline__ static void row_forward(const SpanArgs& a, int t, int h, int c0, int c1,
+                                              bool with_lse) {
   const int lane = threadIdx.x & 31, g = h / a.rep;
   int first, end;
   a.span(t, first, end);
@@ -104,7 +105,7 @@ __device__ __noinline__ static void row_forward(const SpanArgs& a, int t, int h,
     for (int i = 0; i < n; ++i)
       add_row(acc, __shfl_sync(0xffffffffu, p, i), a.v.at(base + i, g), a.d);
   }
-  put_row(a.o.at(t, h), acc, l != 0.f ? 1.f / l : 0.f, 0, a.d);
+  put_row(a.o.at(t, h), acc, l != 0.f ? 1.f / l : 0.f, c0, c1);
   if (with_lse && a.lse && lane == 0)
     a.lse[static_cast<int64_t>(t) * a.nh + h] = l != 0.f ? m + logf(l) : -INFINITY;
 }
@@ -218,13 +219,36 @@ __device__ __forceinline__ void spans_of_tiles(const SpanArgs& a, const Tiling& 
   }
 }
 
-// sv = tanh(w sv). Where the warp's arguments are all within 0.6 (scores below
-// 0.6 of the cap), an odd polynomial (least squares on [0, 0.6], reweighted
-// towards the least greatest error: 2^-25); it costs 7 instructions for two
-// scores, and the exact form 1 - 2 / (1 + e^2x), off by 2^-22, six of the
-// special-function unit.
+// The cap cap tanh(s scale / cap), in base 2 where scores are exponentiated.
+// Arguments of tanh within 0.3 (scores below 0.3 of the cap, nearly all in use)
+// go through an odd polynomial (least squares on [0, 0.3], reweighted towards
+// the least greatest error: 2^-22.5), whose coefficients take up the scale;
+// others through 1 - 2 / (1 + e^2x), off by 2^-22, which takes twice the
+// special-function unit, that the exponentials need.
+struct Cap {
+  float limit;    // scores beyond it: not the polynomial
+  float w;        // scale / cap
+  float t[3];     // tanh(w s) = s (t0 + t1 s^2 + t2 s^4)
+  float z[3];     // cap log2 e tanh(w s), alike
+};
+inline Cap cap_of(float scale, float cap) {
+  constexpr double c[3] = {0.99999601, -0.3329748, 0.12522591};
+  Cap x = {};
+  if (!(cap > 0.f)) return x;
+  const double w = static_cast<double>(scale) / cap;
+  x.w = static_cast<float>(w);
+  x.limit = w > 1e-4 && w < 1e4 ? static_cast<float>(0.3 / w) : -1.f;  // powers stay in range
+  double p = w;
+  for (int i = 0; i < 3; ++i, p *= w * w) {
+    x.t[i] = static_cast<float>(c[i] * p);
+    x.z[i] = static_cast<float>(cap * 1.4426950408889634 * c[i] * p);
+  }
+  return x;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+// Whether some lane of the warp has a score beyond the polynomial's range.
 template <int N>
-__device__ __forceinline__ void tanh_all(uint32_t (&sv)[N], float w) {
+__device__ __forceinline__ bool beyond(const uint32_t (&sv)[N], float limit) {
   float top[2] = {0.f, 0.f};
 #pragma unroll
   for (int c = 0; c < N; c += 4) {
@@ -233,28 +257,21 @@ __device__ __forceinline__ void tanh_all(uint32_t (&sv)[N], float w) {
       top[e] = max3(top[e], fabsf(__uint_as_float(sv[c + 2 * e])),
                     fabsf(__uint_as_float(sv[c + 2 * e + 1])));
   }
-  if (__any_sync(0xffffffffu, fmaxf(top[0], top[1]) * w > 0.6f)) {
-    const float k = 2.f * 1.4426950408889634f * w;
+  return __any_sync(0xffffffffu, fmaxf(top[0], top[1]) > limit);
+}
+template <int N>
+__device__ __forceinline__ void tanh_far(uint32_t (&sv)[N], float w) {
+  const float k = 2.f * 1.4426950408889634f * w;
 #pragma unroll
-    for (int c = 0; c < N; ++c)
-      sv[c] = __float_as_uint(
-          fmaf(-2.f, rcp_approx(1.f + ex2_approx(__uint_as_float(sv[c]) * k)), 1.f));
-    return;
-  }
-  auto both = [](float x) { return make_float2(x, x); };
-#pragma unroll
-  for (int c = 0; c < N; c += 2) {
-    const float2 x =
-        mul2(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), both(w));
-    const float2 y = mul2(x, x);
-    float2 p = fma2(y, both(0.01497696f), both(-0.05169674f));
-    p = fma2(p, y, both(0.1329921f));
-    p = fma2(p, y, both(-0.33331209f));
-    p = fma2(p, y, both(0.99999963f));
-    p = mul2(p, x);
-    sv[c] = __float_as_uint(p.x);
-    sv[c + 1] = __float_as_uint(p.y);
-  }
+  for (int c = 0; c < N; ++c)
+    sv[c] = __float_as_uint(
+        fmaf(-2.f, rcp_approx(1.f + ex2_approx(__uint_as_float(sv[c]) * k)), 1.f));
+}
+// t0 + t1 s^2 + .. of two scores.
+__device__ __forceinline__ float2 odd_factor(float2 s, const float (&t)[3]) {
+  const float2 y = mul2(s, s);
+  const float2 p = fma2(y, both(t[2]), both(t[1]));
+  return fma2(p, y, both(t[0]));
 }
 
 // Splits of the keys of one (pair of tiles, key head), and the forward pass'

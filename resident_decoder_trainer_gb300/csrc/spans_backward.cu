@@ -40,7 +40,8 @@ struct Args {
   SpanArgs a;
   Tiling tl;
   int groups;
-  float to_tanh, scale_log2;
+  Cap cap;
+  float scale_log2;
   float *neg_lse, *neg_d;  // [nkv][tiles][128]
   int *lo, *len;           // [tiles][128]
   TileSpan* tiles;
@@ -144,6 +145,21 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_cons
 }
 
 // ------------------------------------------------------------ elementwise
+// Scores to the tanh of their cap.
+__device__ __forceinline__ void tanh_all(uint32_t (&sv)[32], const Cap& cap) {
+  if (beyond(sv, cap.limit)) {
+    tanh_far(sv, cap.w);
+    return;
+  }
+#pragma unroll
+  for (int c = 0; c < 32; c += 2) {
+    const float2 s = make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+    const float2 t = mul2(s, odd_factor(s, cap.t));
+    sv[c] = __float_as_uint(t.x);
+    sv[c + 1] = __float_as_uint(t.y);
+  }
+}
+
 // p = 2^(score + neg_lse) of two scores; with a cap the score is its tanh, and
 // the slope 1 - tanh^2 is left in `slope`.
 template <bool CAP>
@@ -453,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tmem_ld_wait();
-      if constexpr (CAP) tanh_all(sv, ar.to_tanh);
+      if constexpr (CAP) tanh_all(sv, ar.cap);
       // sv: p, times the cap's slope
 #pragma unroll
       for (int c = 0; c < 32; c += 4) {
@@ -765,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_wait();
         tc_fence_before();
         mbar_arrive(s_free);
-        if constexpr (CAP) tanh_all(sv, ar.to_tanh);
+        if constexpr (CAP) tanh_all(sv, ar.cap);
         // columns l <= c < l + len are seen; a row that sees nothing has p = 0 as it is
         const int l = lo - (first + j * 128 + block * 32);
         const bool full = __all_sync(0xffffffffu, len == 0 || (l <= 0 && l + len >= 32));
@@ -910,7 +926,7 @@ cudaError_t backward_tiles(const SpanArgs& a, void* ws, cudaStream_t s) {
   Args ar = {};
   ar.a = a;
   lay_out(&ar, a.queries, a.rep, a.nkv, ws);
-  ar.to_tanh = a.cap > 0.f ? a.scale / a.cap : 0.f;
+  ar.cap = cap_of(a.scale, a.cap);
   ar.scale_log2 = (a.cap > 0.f ? a.cap : a.scale) * kLog2e;
   ar.err = device_error_ptr();
   if (a.d <= 64) return a.cap > 0.f ? launch<64, true>(ar, s) : launch<64, false>(ar, s);

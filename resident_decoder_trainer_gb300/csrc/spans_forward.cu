@@ -45,7 +45,7 @@ struct Args {
   SpanArgs a;
   Tiling tl;
   int pairs, splits;
-  float to_tanh;     // scale / cap
+  Cap cap;
   float scale_log2;  // of what is exponentiated: scale log2 e, or cap log2 e
   float* part_o;     // splits > 1: fp32 [splits][queries][nh][d] and lse (base 2)
   float* part_lse;
@@ -59,7 +59,8 @@ struct Cfg {
   static constexpr uint32_t TILE = 128 * D * 2;
   static constexpr int KS = D == 128 ? 2 : 4, VS = KS;
   static constexpr uint32_t OFF_Q = 0, OFF_K = OFF_Q + 2 * TILE, OFF_V = OFF_K + KS * TILE,
-                            OFF_NEXT = OFF_V + VS * TILE, OFF_ITEM = OFF_NEXT + 16,
+                            OFF_STAGE = OFF_V + VS * TILE,  // 4 KB of each softmax warp
+      OFF_NEXT = OFF_STAGE + 8 * 4096, OFF_ITEM = OFF_NEXT + 16,
                             OFF_BAR = OFF_ITEM + kItemRing * sizeof(Item);
   static constexpr size_t SMEM = OFF_BAR + 512 + 1024;
   static constexpr uint32_t TMEM_S = 0, TMEM_O = 256, TMEM_COLS = 512;
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   after_previous_kernel();
 
   if (warp < 4) {
-    regs_dec<88>();
+    regs_dec<72>();
     if (warp == 0) {
       // ------------------------------------------------------- producer
       bool ok = true;
@@ -214,95 +215,104 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = ok && answered;
         if (ok) item = next_cta_answer(sbase + C::OFF_NEXT);
       }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1 && elect_one()) {
       // ------------------------------------------------------------ MMA
       constexpr uint32_t idesc_s = idesc_bf16_f32(BM, BN, 0, 0);
       const uint32_t idesc_o = idesc_bf16_f32(BM, a.d, 0, 1);
       const int ksteps = a.d / 16;
       bool ok = true;
-      int jg = 0, loaded = 0, it = 0;
-      int pv[2] = {0, 0}, rounds[2] = {0, 0};  // P V issued; items with any, of each tile
+      uint32_t jg = 0, loaded = 0, it = 0;
+      uint32_t pv0 = 0, pv1 = 0, rounds0 = 0, rounds1 = 0;  // P V issued; items with any
       for (; ok; ++it) {
         const int slot = it % kItemRing;
-        if (!mbar_wait(item_full + 8 * slot, (it / kItemRing) & 1, err)) break;
-        const Item d = ring[slot];
+        if (!wait_for(item_full + 8 * slot, (it / kItemRing) & 1, err)) break;
+        const int index = ring[slot].index, n = ring[slot].n;
+        const int begin0 = ring[slot].begin[0], begin1 = ring[slot].begin[1],
+                  end0 = ring[slot].end[0], end1 = ring[slot].end[1];
         mbar_arrive(item_empty + 8 * slot);
-        if (d.index < 0) break;
-        if (d.n == 0) continue;
-        auto active = [&](int x, int j) { return j >= d.begin[x] && j < d.end[x]; };
-        auto issue_s = [&](int x, int j) {
-          const uint32_t kb = sbase + C::OFF_K + ((jg + j) % KS) * C::TILE;
-          const uint32_t qb = sbase + C::OFF_Q + x * C::TILE;
-          const uint32_t kd = not_hoisted(desc_low(kb, 16)), qd = not_hoisted(desc_low(qb, 16));
+        if (index < 0) break;
+        if (n == 0) continue;
+        // S_x = Q_x K^T of key tile j, where row tile x has any of it
+        auto issue_s = [&](auto which, int j) {
+          constexpr int x = decltype(which)::value;
+          const int end = x ? end1 : end0;
+          if (j < (x ? begin1 : begin0) || j >= end) return;
+          const uint32_t kd = desc_low(sbase + C::OFF_K + ((jg + j) % KS) * C::TILE, 16);
+          const uint32_t qd = desc_low(sbase + C::OFF_Q + x * C::TILE, 16);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             if (k >= ksteps) break;
             const uint32_t off = ((k >> 2) * C::CHUNK + (k & 3) * 32) >> 4;
-            tc_mma_low(tmem + C::TMEM_S + x * BN, qd + off, kd + off, idesc_s, k > 0);
+            tc_mma_low(tmem + C::TMEM_S + x * BN, not_hoisted(qd) + off, kd + off, idesc_s, k > 0);
           }
           tc_commit(s_full + 8 * x);
-          if (j + 1 == d.end[x]) tc_commit(q_empty + 8 * x);  // the item's last read of its Q
+          if (j + 1 == end) tc_commit(q_empty + 8 * x);  // the item's last read of its Q
         };
-        auto wait_k = [&](int j) -> bool {
-          const int jj = jg + j;
-          if (!mbar_wait(k_full + 8 * (jj % KS), (jj / KS) & 1, err)) return false;
-          tc_fence_after();
-          return true;
-        };
-        auto issue_pv = [&](int x, int j) -> bool {
-          const int jj = jg + j, vs = jj % VS;
-          if (j == d.begin[x] && !mbar_wait(o_free + 8 * x, (rounds[x] & 1) ^ 1, err))
-            return false;
-          const uint32_t vd = not_hoisted(desc_low(sbase + C::OFF_V + vs * C::TILE, C::CHUNK));
+        // O_x += P_x V
+        auto issue_pv = [&](auto which, int j) -> bool {
+          constexpr int x = decltype(which)::value;
+          const int begin = x ? begin1 : begin0, end = x ? end1 : end0;
+          if (j < begin || j >= end) return true;
+          uint32_t& pv = x ? pv1 : pv0;
+          uint32_t& rounds = x ? rounds1 : rounds0;
+          if (j == begin && !wait_for(o_free + 8 * x, (rounds & 1) ^ 1, err)) return false;
+          const uint32_t vd = desc_low(sbase + C::OFF_V + ((jg + j) % VS) * C::TILE, C::CHUNK);
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            if (!mbar_wait(p_full + 16 * x + 8 * half, pv[x] & 1, err)) return false;
+            if (!wait_for(p_full + 16 * x + 8 * half, pv & 1, err)) return false;
             tc_fence_after();
 #pragma unroll
             for (int k = 4 * half; k < 4 * half + 4; ++k)
               tc_mma_ts_low(tmem + C::TMEM_O + x * D, tmem + C::TMEM_S + x * BN + k * 8,
-                             vd + k * 128, idesc_o, j > d.begin[x] || k > 0);
+                            vd + k * 128, idesc_o, j > begin || k > 0);
           }
-          ++pv[x];
-          if (j + 1 == d.end[x]) {
+          ++pv;
+          if (j + 1 == end) {
             tc_commit(o_done + 8 * x);
-            ++rounds[x];
+            ++rounds;
           }
           return true;
         };
-        // the tiles' Q are waited for even where no key tile is theirs
-        ok = wait_k(0);
-        for (int x = 0; x < 2 && ok; ++x) {
-          ok = mbar_wait(q_full + 8 * x, loaded & 1, err);
+        constexpr std::integral_constant<int, 0> A{};
+        constexpr std::integral_constant<int, 1> B{};
+        auto wait_k = [&](int j) {
+          return wait_for(k_full + 8 * ((jg + j) % KS), ((jg + j) / KS) & 1, err);
+        };
+        // what is loaded is waited for even where no row tile reads it: its place is free
+        // only once it is there
+        ok = wait_k(0) && wait_for(q_full, loaded & 1, err);
+        if (!ok) break;
+        tc_fence_after();
+        issue_s(A, 0);
+        if (end0 == 0) mbar_arrive(q_empty);
+        ok = wait_for(q_full + 8, loaded & 1, err);
+        if (!ok) break;
+        tc_fence_after();
+        issue_s(B, 0);
+        if (end1 == 0) mbar_arrive(q_empty + 8);
+        tc_commit(k_empty + 8 * (jg % KS));
+        for (int j = 0; j < n; ++j) {
+          ok = wait_for(v_full + 8 * ((jg + j) % VS), ((jg + j) / VS) & 1, err) &&
+               issue_pv(A, j) && (j + 1 >= n || wait_k(j + 1));
           if (!ok) break;
           tc_fence_after();
-          if (active(x, 0)) issue_s(x, 0);
-          if (d.end[x] == 0) mbar_arrive(q_empty + 8 * x);
-        }
-        if (!ok) break;
-        tc_commit(k_empty + 8 * (jg % KS));
-        for (int j = 0; j < d.n && ok; ++j) {
-          // waited for even where no row tile reads it: its place is free only once it is there
-          ok = mbar_wait(v_full + 8 * ((jg + j) % VS), ((jg + j) / VS) & 1, err);
-          for (int x = 0; x < 2 && ok; ++x) {
-            if (active(x, j)) ok = issue_pv(x, j);
-            if (ok && j + 1 < d.n) {
-              if (x == 0) ok = wait_k(j + 1);
-              if (ok && active(x, j + 1)) issue_s(x, j + 1);
-            }
-          }
+          if (j + 1 < n) issue_s(A, j + 1);
+          ok = issue_pv(B, j);
           if (!ok) break;
           tc_commit(v_empty + 8 * ((jg + j) % VS));
-          if (j + 1 < d.n) tc_commit(k_empty + 8 * ((jg + j + 1) % KS));
+          if (j + 1 < n) {
+            issue_s(B, j + 1);
+            tc_commit(k_empty + 8 * ((jg + j + 1) % KS));
+          }
         }
-        jg += d.n;
+        jg += n;
         ++loaded;
       }
       tc_commit(drain);
       mbar_wait(drain, 0, nullptr);
     }
   } else {
-    regs_inc<208>();
+    regs_inc<216>();
     // --------------------------------- softmax: one row a thread
     const int x = (warp - 4) >> 2;
     const int row = (warp & 3) * 32 + lane;
@@ -339,21 +349,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 4; ++c)
           tmem_ld32(ts + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * c]));
         tmem_ld_wait();
-        if constexpr (CAP) tanh_all(sv, ar.to_tanh);
         // columns l <= c < r are seen by this row
         const int base = first + j * BN;
         const int l = lo - base, r = hi - base;
-        if (__any_sync(0xffffffffu, l > 0 || r < BN)) {
+        const bool masked = __any_sync(0xffffffffu, l > 0 || r < BN);
+        const bool poly = CAP && !beyond(sv, ar.cap.limit);
+        if (CAP && !poly) tanh_far(sv, ar.cap.w);
+        if (masked && !poly) {
 #pragma unroll
           for (int c = 0; c < 128; ++c)
             if (c < l || c >= r) sv[c] = __float_as_uint(-INFINITY);
         }
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (masked && poly) {  // -inf has no polynomial: p is cleared below
 #pragma unroll
-        for (int c = 0; c < 128; c += 2)
-          m4[(c >> 1) & 3] =
-              max3(m4[(c >> 1) & 3], __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
-        const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * ar.scale_log2;
+          for (int c = 0; c < 128; ++c)
+            if (c >= l && c < r) m4[c & 3] = fmaxf(m4[c & 3], __uint_as_float(sv[c]));
+        } else {
+#pragma unroll
+          for (int c = 0; c < 128; c += 2)
+            m4[(c >> 1) & 3] =
+                max3(m4[(c >> 1) & 3], __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+        }
+        float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
+        if (!poly)
+          mx *= ar.scale_log2;
+        else if (mx != -INFINITY)
+          mx *= odd_factor(both(mx), ar.cap.z).x;  // the cap rises with the score
         float alpha = 1.f;
         if (mx > m_run + kRescaleLog2) {
           alpha = m_run == -INFINITY ? 1.f : ex2_approx(m_run - mx);  // nothing summed: as it is
@@ -374,22 +396,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float nm = m_run == -INFINITY ? 0.f : -m_run;
         const float2 nm2 = make_float2(nm, nm);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        auto exps = [&](auto by_poly, auto clear) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
+          for (int half = 0; half < 2; ++half) {
 #pragma unroll
-          for (int c = 64 * half; c < 64 * half + 64; c += 2) {
-            float2 p = fma2(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), sc2,
-                            nm2);
-            p.x = ex2_approx(p.x);
-            p.y = ex2_approx(p.y);
-            sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], p);
-            sv[c / 2] = pack_bf16x2(p.x, p.y);
+            for (int c = 64 * half; c < 64 * half + 64; c += 2) {
+              float2 p = make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+              if constexpr (decltype(by_poly)::value)
+                p = fma2(p, odd_factor(p, ar.cap.z), nm2);
+              else
+                p = fma2(p, sc2, nm2);
+              p.x = ex2_approx(p.x);
+              p.y = ex2_approx(p.y);
+              if constexpr (decltype(clear)::value) {
+                if (c < l || c >= r) p.x = 0.f;
+                if (c + 1 < l || c + 1 >= r) p.y = 0.f;
+              }
+              sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], p);
+              sv[c / 2] = pack_bf16x2(p.x, p.y);
+            }
+            // 64 keys as 32 bf16 pairs over the first columns of S
+            tmem_st32(ts + 32 * half, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * half]));
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(p_full + 16 * x + 8 * half);
           }
-          // 64 keys as 32 bf16 pairs over the first columns of S
-          tmem_st32(ts + 32 * half, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * half]));
-          tmem_st_wait();
-          tc_fence_before();
-          mbar_arrive(p_full + 16 * x + 8 * half);
+        };
+        if constexpr (CAP) {
+          if (!poly)
+            exps(std::false_type{}, std::false_type{});
+          else if (masked)
+            exps(std::true_type{}, std::true_type{});
+          else
+            exps(std::true_type{}, std::false_type{});
+        } else {
+          exps(std::false_type{}, std::false_type{});
         }
         const float2 two = add2(sum[0], sum[1]);
         l_run = l_run * alpha + (two.x + two.y);
@@ -404,44 +445,64 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv = l_run != 0.f ? 1.f / l_run : 0.f;
       const bool some = l_run != 0.f;  // else p was 0 throughout: 0 times what was not seen
       float bad = 0.f;
+      // A thread's row goes through shared memory, so that a store takes whole
+      // 128-byte pieces of rows; 64 columns a round.
+      bf16* const own = real && ar.splits == 1 ? a.o.at(t, h) : nullptr;
+      uint8_t* stage = smem + C::OFF_STAGE + (warp - 4) * 4096;
+      const bool any = __any_sync(0xffffffffu, real);
 #pragma unroll 1
-      for (int c0 = 0; c0 < a.d; c0 += 32) {
-        uint32_t ov[32];
+      for (int c0 = 0; any && c0 < a.d; c0 += 64) {
+        uint32_t ov[64];
         if (begin < end) {
-          tmem_ld32(t_o + c0, ov);
+          tmem_ld32(t_o + c0, *reinterpret_cast<uint32_t(*)[32]>(&ov[0]));
+          tmem_ld32(t_o + c0 + 32, *reinterpret_cast<uint32_t(*)[32]>(&ov[32]));
           tmem_ld_wait();
-          if (c0 + 32 >= a.d) {  // this O is free for the next item
-            tc_fence_before();
-            mbar_arrive(o_free + 8 * x);
-          }
         }
+        const int left = a.d - c0;
+        float2 worst[2] = {both(0.f), both(0.f)};
 #pragma unroll
-        for (int c = 0; c < 32; c += 16) {
-          if (c0 + c >= a.d) break;
+        for (int e = 0; e < 64; e += 2) {
+          float2 v = mul2(make_float2(__uint_as_float(ov[e]), __uint_as_float(ov[e + 1])),
+                          both(inv));
+          if (!some) v = both(0.f);
+          if (e < left) worst[(e >> 1) & 1] = fma2(v, both(0.f), worst[(e >> 1) & 1]);
+          ov[e] = __float_as_uint(v.x);
+          ov[e + 1] = __float_as_uint(v.y);
+        }
+        bad += (worst[0].x + worst[0].y) + (worst[1].x + worst[1].y);
+        if (ar.splits > 1) {
+          float* out =
+              ar.part_o + (static_cast<int64_t>(split) * a.queries * a.nh + th) * a.d + c0;
 #pragma unroll
-          for (int e = c; e < c + 16; ++e) {
-            const float v = some ? __uint_as_float(ov[e]) * inv : 0.f;
-            bad = fmaf(v, 0.f, bad);
-            ov[e] = __float_as_uint(v);
-          }
-          if (real && ar.splits > 1) {
-            float* out =
-                ar.part_o + (static_cast<int64_t>(split) * a.queries * a.nh + th) * a.d + c0 + c;
-#pragma unroll
-            for (int e = 0; e < 16; e += 4)
+          for (int e = 0; e < 64; e += 4)
+            if (real && e < left)
               *reinterpret_cast<uint4*>(out + e) =
-                  make_uint4(ov[c + e], ov[c + e + 1], ov[c + e + 2], ov[c + e + 3]);
-          } else if (real) {
-            uint32_t w[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              w[e] =
-                  pack_bf16x2(__uint_as_float(ov[c + 2 * e]), __uint_as_float(ov[c + 2 * e + 1]));
-            bf16* out = a.o.at(t, h) + c0 + c;
-            *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<uint4*>(out + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-          }
+                  make_uint4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+          continue;
         }
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 8; ++e)  // 16-byte piece e of the row, at a place that spreads banks
+          *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+              make_uint4(pack_bf16x2(__uint_as_float(ov[8 * e]), __uint_as_float(ov[8 * e + 1])),
+                         pack_bf16x2(__uint_as_float(ov[8 * e + 2]), __uint_as_float(ov[8 * e + 3])),
+                         pack_bf16x2(__uint_as_float(ov[8 * e + 4]), __uint_as_float(ov[8 * e + 5])),
+                         pack_bf16x2(__uint_as_float(ov[8 * e + 6]), __uint_as_float(ov[8 * e + 7])));
+        __syncwarp();
+        const int piece = lane & 7;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int from = 4 * i + (lane >> 3);
+          bf16* const row_at = reinterpret_cast<bf16*>(
+              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(own), from));
+          const uint4 w =
+              *reinterpret_cast<const uint4*>(stage + from * 128 + ((piece ^ (from & 7)) << 4));
+          if (row_at && 8 * piece < left) *reinterpret_cast<uint4*>(row_at + c0 + 8 * piece) = w;
+        }
+      }
+      if (begin < end) {  // this O is free for the next item
+        tc_fence_before();
+        mbar_arrive(o_free + 8 * x);
       }
       const float lse2 = l_run != 0.f ? m_run + log2f(l_run) : -INFINITY;
       if (real) {
@@ -455,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
              again &= again - 1) {
           const int from = __ffs(again) - 1;
           row_forward(a, __shfl_sync(0xffffffffu, t, from),
-                      __shfl_sync(0xffffffffu, h, from), false);
+                      __shfl_sync(0xffffffffu, h, from), 0, a.d, false);
         }
       }
     }
@@ -531,7 +592,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
         make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
   }
   if (lane == 0 && a.lse) a.lse[th] = total != 0.f ? (top + log2f(total)) * kLn2 : -INFINITY;
-  if (__any_sync(0xffffffffu, bad)) row_forward(a, t, h, false);
+  if (__any_sync(0xffffffffu, bad)) row_forward(a, t, h, 0, a.d, false);
 }
 
 constexpr int kMinKeysOfSplit = 256;
@@ -571,7 +632,7 @@ cudaError_t forward_tiles(const SpanArgs& a, void* ws, cudaStream_t s) {
   ar.tl = Tiling::of(a.queries, a.rep);
   ar.pairs = (ar.tl.tiles + 1) / 2;
   ar.splits = forward_splits(a.queries, a.keys, a.nkv, a.rep);
-  ar.to_tanh = a.cap > 0.f ? a.scale / a.cap : 0.f;
+  ar.cap = cap_of(a.scale, a.cap);
   ar.scale_log2 = (a.cap > 0.f ? a.cap : a.scale) * kLog2e;
   const int64_t rows = static_cast<int64_t>(a.queries) * a.nh;
   ar.part_o = static_cast<float*>(ws);
