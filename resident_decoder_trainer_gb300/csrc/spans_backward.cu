@@ -288,6 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   after_previous_kernel();
 
+  if (warp < 4) regs_dec<56>();
   if (warp == 0) {
     // --------------------------------------------------------- producer
     if (lane == 0) {
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t ph = ((it / ST) & 1) ^ 1;
       ++it;
       if (lane == 0) {
-        ok = mbar_wait(q_empty + 8 * st, ph, err);
+        ok = wait_for(q_empty + 8 * st, ph, err);
         if (ok) {
           meta[st] = Meta{tile, full};
           if (tile < 0) {
@@ -323,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bulk_load_1d(row + 512, ar.neg_d + at, 512, q_full + 8 * st);
             bulk_load_1d(row + 1024, ar.lo + tile * int64_t{128}, 512, q_full + 8 * st);
             bulk_load_1d(row + 1536, ar.len + tile * int64_t{128}, 512, q_full + 8 * st);
-            ok = mbar_wait(o_empty + 8 * st, ph, err);
+            ok = wait_for(o_empty + 8 * st, ph, err);
             if (ok) {
               mbar_arrive_expect_tx(o_full + 8 * st, chunks * used * 128);
               for (int c = 0; c < chunks; ++c)
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (ok) send(-1, 0);
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       // -------------------------------------------------------------- MMA
       constexpr uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0);
       const uint32_t id_kv = idesc_bf16_f32(128, a.d, 0, 1);
@@ -379,13 +380,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // whether there is a tile `it`, with its Q loaded
       auto wait_q = [&](int it, bool& more) -> bool {
-        if (!mbar_wait(q_full + 8 * (it % ST), (it / ST) & 1, err)) return false;
+        if (!wait_for(q_full + 8 * (it % ST), (it / ST) & 1, err)) return false;
         more = meta[it % ST].tile >= 0;
         tc_fence_after();
         return true;
       };
       auto wait = [&](uint32_t bar, int phase) -> bool {
-        if (!mbar_wait(bar, phase & 1, err)) return false;
+        if (!wait_for(bar, phase & 1, err)) return false;
         tc_fence_after();
         return true;
       };
@@ -428,6 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(drain, 0, nullptr);
     }
   } else if (warp >= 4) {
+    regs_inc<104>();
     // ------------------------ P^T and dS^T: one key, 32 of a tile's 128 rows
     const int quarter = warp & 3, block = (warp - 4) >> 2;
     const int row = quarter * 32 + lane, key = n0 + row;
@@ -589,10 +591,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t bar0 = sbase + C::OFF_BAR;
   const uint32_t q_full = bar0, q_empty = bar0 + 8, k_full = bar0 + 16, k_empty = k_full + 8 * KST,
                  v_full = k_empty + 8 * KST, v_empty = v_full + 8 * VST, s_full = v_empty + 8 * VST,
-                 s_free = s_full + 8, dp_full = s_free + 8, dp_free = dp_full + 8,
-                 ds_ready = dp_free + 8, ds_free = ds_ready + 16, dq_done = ds_free + 16,
+                 s_free = s_full + 8, ds_ready = s_free + 8, ds_free = ds_ready + 16, dq_done = ds_free + 16,
                  dq_free = dq_done + 8, drain = dq_free + 8;
-  static_assert(8 * (2 + 2 * KST + 2 * VST + 11) <= 248, "");
+  static_assert(8 * (2 + 2 * KST + 2 * VST + 9) <= 248, "");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 248);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -620,8 +621,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(s_full, 1);
     mbar_init(s_free, kEltThreads);
-    mbar_init(dp_full, 1);
-    mbar_init(dp_free, kEltThreads);
     // one for each buffer: a warp may be done with the next key tile before another is with
     // this one
     mbar_init(ds_ready, kEltThreads);
@@ -644,6 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   after_previous_kernel();
 
+  if (warp < 4) regs_dec<56>();
   if (warp == 0) {
     if (lane == 0) {
       // --------------------------------------------------------- producer
@@ -654,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int tile, g, first, n;
         place(item, tile, g, first, n);
         if (n == 0) continue;
-        ok = mbar_wait(q_empty, (loaded & 1) ^ 1, err);
+        ok = wait_for(q_empty, (loaded & 1) ^ 1, err);
         if (!ok) break;
         mbar_arrive_expect_tx(q_full, 2 * chunks * used * 128);
         for (int c = 0; c < chunks; ++c) {
@@ -665,13 +665,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int j = 0; j < n && ok; ++j) {
           const int ks = (jg + j) % KST, vs = (jg + j) % VST;
-          ok = mbar_wait(k_empty + 8 * ks, (((jg + j) / KST) & 1) ^ 1, err);
+          ok = wait_for(k_empty + 8 * ks, (((jg + j) / KST) & 1) ^ 1, err);
           if (!ok) break;
           mbar_arrive_expect_tx(k_full + 8 * ks, chunks * C::CHUNK);
           for (int c = 0; c < chunks; ++c)
             tma_load_3d(sbase + C::OFF_K + ks * C::TILE + c * C::CHUNK, &tk, k_full + 8 * ks,
                         c * 64, g, first + j * 128);
-          ok = mbar_wait(v_empty + 8 * vs, (((jg + j) / VST) & 1) ^ 1, err);
+          ok = wait_for(v_empty + 8 * vs, (((jg + j) / VST) & 1) ^ 1, err);
           if (!ok) break;
           mbar_arrive_expect_tx(v_full + 8 * vs, chunks * C::CHUNK);
           for (int c = 0; c < chunks; ++c)
@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       // -------------------------------------------------------------- MMA
       constexpr uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0);
       const uint32_t id_q = idesc_bf16_f32(128, a.d, 0, 1);
@@ -707,34 +707,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         int tile, g, first, n;
         place(item, tile, g, first, n);
         if (n == 0) continue;
-        // S and dP of key tile j, each once its columns have been read
+        // S and dP of key tile j, once those of the one before are in registers
         auto issue = [&](int j) -> bool {
-          const uint32_t jj = jg + j;
-          const int ks = jj % KST, vs = jj % VST;
-          if (!mbar_wait(k_full + 8 * ks, (jj / KST) & 1, err) ||
-              !mbar_wait(s_free, (jj & 1) ^ 1, err))
+          const uint32_t jj = jg + j, ks = jj % KST, vs = jj % VST;
+          if (!wait_for(k_full + 8 * ks, (jj / KST) & 1, err) ||
+              !wait_for(v_full + 8 * vs, (jj / VST) & 1, err) ||
+              !wait_for(s_free, (jj & 1) ^ 1, err))
             return false;
           tc_fence_after();
           scores(C::T_S, q_desc, sbase + C::OFF_K + ks * C::TILE);
-          tc_commit(s_full);
-          if (!mbar_wait(v_full + 8 * vs, (jj / VST) & 1, err) ||
-              !mbar_wait(dp_free, (jj & 1) ^ 1, err))
-            return false;
-          tc_fence_after();
           scores(C::T_DP, o_desc, sbase + C::OFF_V + vs * C::TILE);
-          tc_commit(dp_full);
+          tc_commit(s_full);
           tc_commit(v_empty + 8 * vs);
           if (j + 1 == n) tc_commit(q_empty);  // the item's last read of Q and dO
           return true;
         };
-        ok = mbar_wait(q_full, loaded & 1, err) && issue(0);
+        ok = wait_for(q_full, loaded & 1, err) && issue(0);
         for (int j = 0; j < n && ok; ++j) {
           const uint32_t jj = jg + j;
           const int ks = jj % KST;
           if (j + 1 < n) ok = issue(j + 1);
           // dQ of the item before has been read out of TMEM
-          if (ok && j == 0) ok = mbar_wait(dq_free, (loaded & 1) ^ 1, err);
-          if (ok) ok = mbar_wait(ds_ready + 8 * (jj & 1), (jj >> 1) & 1, err);
+          if (ok && j == 0) ok = wait_for(dq_free, (loaded & 1) ^ 1, err);
+          if (ok) ok = wait_for(ds_ready + 8 * (jj & 1), (jj >> 1) & 1, err);
           if (!ok) break;
           tc_fence_after();
           const uint32_t k_desc = not_hoisted(desc_low(sbase + C::OFF_K + ks * C::TILE, C::CHUNK));
@@ -753,6 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(drain, 0, nullptr);
     }
   } else if (warp >= 4) {
+    regs_inc<104>();
     // --------------------------- dS: one row, 32 of a key tile's 128 columns
     const int quarter = warp & 3, block = (warp - 4) >> 2;
     const int row = quarter * 32 + lane;
@@ -776,8 +772,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = warp_wait(s_full, jj & 1, err);
         if (!ok) break;
         tc_fence_after();
-        uint32_t sv[32], pk[16];
+        uint32_t sv[32], dp[32], pk[16];
         tmem_ld32(tmem + lane_base + C::T_S + block * 32, sv);
+        tmem_ld32(tmem + lane_base + C::T_DP + block * 32, dp);
         tmem_ld_wait();
         tc_fence_before();
         mbar_arrive(s_free);
@@ -791,33 +788,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           float2 p = p_of<CAP>(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), ar,
                                nl2, slope);
           if constexpr (CAP) p = mul2(p, slope);
-          sv[c] = __float_as_uint(p.x);
-          sv[c + 1] = __float_as_uint(p.y);
-        }
-        ok = warp_wait(dp_full, jj & 1, err);
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          uint32_t dp[16];
-          tmem_ld16(tmem + lane_base + C::T_DP + block * 32 + 16 * x, dp);
-          tmem_ld_wait();
-          if (x == 1) {
-            tc_fence_before();
-            mbar_arrive(dp_free);
+          float2 ds = add2(make_float2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])), nd2);
+          ds = mul2(ds, p);
+          if (!full) {
+            if (static_cast<uint32_t>(c - l) >= static_cast<uint32_t>(len)) ds.x = 0.f;
+            if (static_cast<uint32_t>(c + 1 - l) >= static_cast<uint32_t>(len)) ds.y = 0.f;
           }
-#pragma unroll
-          for (int c = 0; c < 16; c += 2) {
-            float2 ds = add2(make_float2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])), nd2);
-            ds = mul2(ds, make_float2(__uint_as_float(sv[16 * x + c]),
-                                      __uint_as_float(sv[16 * x + c + 1])));
-            if (!full) {
-              if (static_cast<uint32_t>(16 * x + c - l) >= static_cast<uint32_t>(len)) ds.x = 0.f;
-              if (static_cast<uint32_t>(16 * x + c + 1 - l) >= static_cast<uint32_t>(len))
-                ds.y = 0.f;
-            }
-            pk[8 * x + c / 2] = pack_bf16x2(ds.x, ds.y);
-          }
+          pk[c / 2] = pack_bf16x2(ds.x, ds.y);
         }
         // this buffer was last read by dQ += dS K two key tiles ago
         ok = warp_wait(ds_free + 8 * buf, ((jj >> 1) & 1) ^ 1, err);
