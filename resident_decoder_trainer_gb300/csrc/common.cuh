@@ -478,6 +478,15 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
+// Four floats of another CTA's shared memory (shared::cluster address).
+__device__ __forceinline__ float4 load_cluster4(uint32_t cluster_addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr)
+               : "memory");
+  return v;
+}
 // Arrive on an mbarrier given by its shared::cluster address (possibly in the
 // peer CTA). Default (CTA-scope release) semantics: callers use it to hand back
 // TMEM after tcgen05.wait::ld + tcgen05.fence::before_thread_sync, which needs

@@ -138,8 +138,9 @@ __device__ __noinline__ static void row_dq(const SpanArgs& a, int t, int h, int 
   put_row(a.dq.at(t, h), acc, a.scale, c0, c1);
 }
 
-// dk and dv of key j, kv head g.
-__device__ __noinline__ static void row_dkdv(const SpanArgs& a, int j, int g, int c0, int c1) {
+// dk and dv of key j, kv head g, or one of them.
+__device__ __noinline__ static void row_dkdv(const SpanArgs& a, int j, int g, int c0, int c1,
+                                             bool put_dk, bool put_dv) {
   const int lane = threadIdx.x & 31;
   float ak[4] = {}, av[4] = {};
   for (int64_t base = 0; base < a.queries; base += 32) {
@@ -170,8 +171,8 @@ __device__ __noinline__ static void row_dkdv(const SpanArgs& a, int j, int g, in
       }
     }
   }
-  put_row(a.dk.at(j, g), ak, a.scale, c0, c1);
-  put_row(a.dv.at(j, g), av, 1.f, c0, c1);
+  if (put_dk) put_row(a.dk.at(j, g), ak, a.scale, c0, c1);
+  if (put_dv) put_row(a.dv.at(j, g), av, 1.f, c0, c1);
 }
 
 // ------------------------------------------------- tiles of the tensor-core kernels

@@ -223,7 +223,8 @@ struct KvCfg {
 // step kk (16 rows): 32 columns' pairs lie in the first 16 of their place.
 __device__ __forceinline__ uint32_t packed_col(int kk) { return (kk >> 1) * 32 + (kk & 1) * 8; }
 
-template <int D, bool CAP>
+// R CTAs (a cluster) share the row tiles of a key tile, every R-th each.
+template <int D, bool CAP, int R>
 __global__ void __launch_bounds__(kThreads, 1)
     spans_dkdv_kernel(const __grid_constant__ CUtensorMap tq,
                       const __grid_constant__ CUtensorMap tdo,
@@ -248,8 +249,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int chunks = (a.d + 63) / 64, used = ar.tl.per * a.rep;
-  const int n0 = static_cast<int>(blockIdx.x / a.nkv) * 128;
-  const int g = static_cast<int>(blockIdx.x % a.nkv);
+  const int rank = blockIdx.x % R;  // in the cluster
+  const int n0 = static_cast<int>(blockIdx.x / R / a.nkv) * 128;
+  const int g = static_cast<int>(blockIdx.x / R % a.nkv);
 
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
@@ -300,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const int n1 = min(n0 + 128, a.keys);
     bool ok = true;
-    int it = 0;
+    int it = 0, met = 0;
     // one row tile, or the end of them
     auto send = [&](int tile, int full) {
       const int st = it % ST;
@@ -348,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __ballot_sync(0xffffffffu, s.all_first <= n0 && s.all_end >= n1);
         for (; meets && ok; meets &= meets - 1) {
           const int i = __ffs(meets) - 1;
-          send(first + i, (full >> i) & 1);
+          if (met++ % R == rank) send(first + i, (full >> i) & 1);
         }
       }
     }
@@ -526,30 +528,65 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       mbar_arrive(ds_ready);
     }
-    if (ok && warp_wait(fin, 0, err)) {
-      tc_fence_after();
-      const int c0 = block * 32, left = a.d - c0;
+    ok = ok && warp_wait(fin, 0, err);
+    if (ok) tc_fence_after();
+    const int c0 = block * 32, left = a.d - c0;
+    // this thread's 32 columns of dK or dV, 0 if no row tile was this CTA's
+    auto fetch = [&](uint32_t from, uint32_t (&r)[32]) {
+      if (ok && it > 0) {
+        tmem_ld32(tmem + lane_base + from + c0, r);
+        tmem_ld_wait();
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) r[e] = 0u;
+      }
+    };
+    // four columns of a row at [column / 4][row], in what were the tiles of Q and dO
+    const uint32_t at = C::OFF_Q + (block * 8 * 128 + row) * 16;
+    if (R > 1) {
+      // rank 0 finishes dK and rank 1 dV; each leaves its part of the other's
       if (left > 0) {
         uint32_t r[32];
-        bool fine = true;
+        fetch(rank ? C::T_DK : C::T_DV, r);
 #pragma unroll
-        for (int which = 0; which < 2; ++which) {
-          if (it > 0) {
-            tmem_ld32(tmem + lane_base + (which ? C::T_DV : C::T_DK) + c0, r);
-            tmem_ld_wait();
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) r[e] = 0u;
-          }
-          fine = fine && all_finite(r, left);
-          if (key < a.keys)
-            put_columns((which ? a.dv : a.dk).at(key, g) + c0, r, which ? 1.f : a.scale, left);
-        }
-        for (unsigned again = __ballot_sync(0xffffffffu, !fine && key < a.keys); again;
-             again &= again - 1)
-          row_dkdv(a, n0 + quarter * 32 + __ffs(again) - 1, g, c0, min(c0 + 32, a.d));
+        for (int e = 0; e < 8; ++e)
+          *reinterpret_cast<uint4*>(smem + at + e * 2048) =
+              make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
       }
+      cluster_sync();
     }
+    if (left > 0) {
+      bool fine = true;
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        if (R > 1 && which != rank) continue;
+        uint32_t r[32];
+        fetch(which ? C::T_DV : C::T_DK, r);
+        if constexpr (R > 1) {
+          const uint32_t theirs = mapa_shared(sbase + at, rank ^ 1);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 v = load_cluster4(theirs + e * 2048);
+            r[4 * e] = __float_as_uint(__uint_as_float(r[4 * e]) + v.x);
+            r[4 * e + 1] = __float_as_uint(__uint_as_float(r[4 * e + 1]) + v.y);
+            r[4 * e + 2] = __float_as_uint(__uint_as_float(r[4 * e + 2]) + v.z);
+            r[4 * e + 3] = __float_as_uint(__uint_as_float(r[4 * e + 3]) + v.w);
+          }
+        }
+        fine = fine && all_finite(r, left);
+        if (key < a.keys && ok)
+          put_columns((which ? a.dv : a.dk).at(key, g) + c0, r, which ? 1.f : a.scale, left);
+      }
+      for (unsigned again = __ballot_sync(0xffffffffu, !fine && key < a.keys && ok); again;
+           again &= again - 1)
+        row_dkdv(a, n0 + quarter * 32 + __ffs(again) - 1, g, c0, min(c0 + 32, a.d),
+                 R == 1 || rank == 0, R == 1 || rank == 1);
+    }
+    if (R > 1) cluster_sync();  // what this CTA left has been read
+  }
+  if (R > 1 && warp < 4) {
+    cluster_sync();
+    cluster_sync();
   }
 
   tc_fence_before();
@@ -845,6 +882,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // -------------------------------------------------------------------- host
+constexpr int kSharedBelow = 3;
+
+template <int D, bool CAP, int R>
+cudaError_t launch_dkdv(const Args& ar, const CUtensorMap& tq, const CUtensorMap& tdo,
+                        const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+  const cudaError_t e = allow_smem(spans_dkdv_kernel<D, CAP, R>, KvCfg<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_clusters(spans_dkdv_kernel<D, CAP, R>, R,
+                         static_cast<int64_t>((ar.a.keys + 127) / 128) * ar.a.nkv * R, kThreads,
+                         KvCfg<D>::SMEM, s, tq, tdo, tk, tv, ar);
+}
+
 template <int D, bool CAP>
 cudaError_t launch(const Args& ar, cudaStream_t s) {
   const SpanArgs& a = ar.a;
@@ -854,16 +903,17 @@ cudaError_t launch(const Args& ar, cudaStream_t s) {
       !make_tma_heads(&tk, a.k.p, a.keys, a.nkv, a.d, a.k.ts, a.k.hs, 1, 128) ||
       !make_tma_heads(&tv, a.v.p, a.keys, a.nkv, a.d, a.v.ts, a.v.hs, 1, 128))
     return cudaErrorInvalidValue;
-  cudaError_t e = allow_smem(spans_dkdv_kernel<D, CAP>, KvCfg<D>::SMEM);
-  if (e == cudaSuccess) e = allow_smem(spans_dq_kernel<D, CAP>, QCfg<D>::SMEM);
+  cudaError_t e = allow_smem(spans_dq_kernel<D, CAP>, QCfg<D>::SMEM);
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(a.nkv) * ar.tl.tiles * 128;
   const int64_t prep = ar.groups + std::min<int64_t>((rows + 63) / 64, int64_t{num_sms()} * 8);
   e = launch_overlapping(prepare_kernel, prep, kPrepThreads, 0, s, ar);
   if (e != cudaSuccess) return e;
-  e = launch_overlapping(spans_dkdv_kernel<D, CAP>,
-                         static_cast<int64_t>((a.keys + 127) / 128) * a.nkv, kThreads,
-                         KvCfg<D>::SMEM, s, tq, tdo, tk, tv, ar);
+  // Few key tiles: two CTAs share the rows of each.
+  const int64_t key_tiles = static_cast<int64_t>((a.keys + 127) / 128) * a.nkv;
+  e = key_tiles < kSharedBelow * int64_t{num_sms()}
+          ? launch_dkdv<D, CAP, 2>(ar, tq, tdo, tk, tv, s)
+          : launch_dkdv<D, CAP, 1>(ar, tq, tdo, tk, tv, s);
   if (e != cudaSuccess) return e;
   return launch_overlapping(
       spans_dq_kernel<D, CAP>,
