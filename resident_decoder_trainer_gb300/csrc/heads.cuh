@@ -127,25 +127,4 @@ struct Eight<float> {
   }
 };
 
-// Rounds eight values to the type and stores them at element `at` of `base`.
-__device__ __forceinline__ void store_eight(void* base, int dtype, int64_t at, const float (&x)[8]) {
-  if (dtype == RDT_F32) {
-    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
-    p[0] = make_float4(x[0], x[1], x[2], x[3]);
-    p[1] = make_float4(x[4], x[5], x[6], x[7]);
-    return;
-  }
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (dtype == RDT_BF16) {
-      w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-    } else {
-      const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-  }
-  *reinterpret_cast<uint4*>(static_cast<bf16*>(base) + at) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 }  // namespace rdt

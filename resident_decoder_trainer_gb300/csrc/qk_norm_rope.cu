@@ -9,9 +9,10 @@
 //
 // Bound by DRAM: every value is read once and written once. A lane holds
 // eight neighbouring pairs (two 16-byte loads of a 16-bit type), so a head of
-// 128 is eight lanes and a warp takes four heads at a time, several such
-// passes' loads under way at once; all heads of a token share the lane's eight
-// cosines and sines.
+// 128 is eight lanes and a warp takes four heads at a time; all heads of a
+// token share the lane's eight cosines and sines. A pass's loads are under way
+// while the one before is computed, in pairs of fp32 (fma.f32x2). q and k have
+// CTAs of their own, so that a warp sums one gain's gradient.
 //
 // Angles: a full turn is 2^64. A pair's rate is kept as a 64-bit fraction of a
 // turn, the product with the position is taken modulo 2^64, and its upper 32
@@ -29,322 +30,416 @@ namespace {
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kMaxHalf = 128;  // pairs of a head of 256
 
+// Turns of a pair for each position, in 2^-64, and the pair's axis.
 struct Rates {
-  uint64_t turn[kMaxHalf];  // turns a position, in 2^-64
-  int end[3];               // first pair of axis 1, 2, 3
+  uint64_t turn[kMaxHalf];
+  uint8_t axis[kMaxHalf];
+};
+
+// q or k. A warp takes `per_pass` of its heads at a time; `slices` warps share
+// the passes over a token, and `blocks` CTAs the tokens.
+struct Side {
+  const void *x, *dy;
+  void* out;
+  const float* gain;  // null: no norm
+  int64_t x_ts, x_hs, dy_ts, dy_hs, out_ts, out_hs;
+  int heads, passes, slices, blocks;
 };
 
 struct NormArgs {
-  const void *q, *k;
-  int64_t q_ts, q_hs, k_ts, k_hs;
-  const float *gain_q, *gain_k;  // null: no norm
+  Side side[2];
   float eps;
   const int32_t* positions;  // null: no rotation
   int axes;
-  void *q_out, *k_out;
-  int64_t qo_ts, qo_hs, ko_ts, ko_hs;
-  int out_dtype;
-  int tokens, nh, nkv, d;
-  int lanes;       // lanes of a head, a power of two; those past d / 16 have nothing
-  int lanes_log2;
-  int passes;      // of a warp over a token's heads
-  int slices;      // warps that share a token's passes
+  int tokens, d;
+  int lanes, lanes_log2;  // lanes of a head, a power of two; those past d / 16 have nothing
+  int f16_in, f16_dy, f16_out;  // of 16-bit types: fp16 rather than bf16
+  float* partial;               // CTA's sums of gain gradients, [blocks of q, then of k][d]
 };
 
-// Where a lane stands: head slot within the pass and chunk of eight pairs.
-struct Lane {
-  int slot, chunk, per_pass;
-  bool has;
-  __device__ __forceinline__ explicit Lane(const NormArgs& a) {
-    const int lane = threadIdx.x & 31;
-    slot = lane >> a.lanes_log2;
-    chunk = lane & (a.lanes - 1);
-    per_pass = 32 >> a.lanes_log2;
-    has = 16 * chunk < a.d;
-  }
-};
-
-// A lane's rates and axes (two bits each), read once.
-struct Turning {
-  uint64_t turn[8];
-  uint32_t axis;
-  __device__ __forceinline__ Turning(const NormArgs& a, const Rates& r, int chunk) {
-    axis = 0;
+// A lane's eight pairs of a head as loaded, B bytes a value.
+template <int B>
+struct Pairs {
+  uint4 v[B];  // the lower half's eight values, then the upper's
+  __device__ __forceinline__ void load(const void* base, int64_t lo, int half) {
+    const char* p = static_cast<const char*>(base) + lo * B;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int pair = min(8 * chunk + i, kMaxHalf - 1);
-      turn[i] = r.turn[pair];
-      const int which = (pair >= r.end[0]) + (pair >= r.end[1]) + (pair >= r.end[2]);
-      axis |= static_cast<uint32_t>(which) << (2 * i);
+    for (int i = 0; i < B / 2; ++i) {
+      v[i] = reinterpret_cast<const uint4*>(p)[i];
+      v[B / 2 + i] = reinterpret_cast<const uint4*>(p + static_cast<int64_t>(half) * B)[i];
     }
   }
-  __device__ __forceinline__ void at(const NormArgs& a, int token, float (&cos)[8],
-                                     float (&sin)[8]) const {
-    if (!a.positions) {
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        cos[i] = 1.f;
-        sin[i] = 0.f;
+    for (int i = 0; i < B; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  // x: [0, 4) the lower half in twos, [4, 8) the upper
+  __device__ __forceinline__ void get(float2 (&x)[8], bool f16) const {
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      if constexpr (B == 4) {
+        x[2 * i] = make_float2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+        x[2 * i + 1] = make_float2(__uint_as_float(w[2]), __uint_as_float(w[3]));
+      } else if (f16) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          x[4 * i + e] = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[4 * i + e] = make_float2(bf16lo(w[e]), bf16hi(w[e]));
       }
-      return;
-    }
-    const int p0 = a.positions[token];
-    int p1 = p0, p2 = p0, p3 = p0;
-    if (a.axes > 1) p1 = a.positions[static_cast<int64_t>(a.tokens) + token];
-    if (a.axes > 2) p2 = a.positions[2 * static_cast<int64_t>(a.tokens) + token];
-    if (a.axes > 3) p3 = a.positions[3 * static_cast<int64_t>(a.tokens) + token];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t w = (axis >> (2 * i)) & 3;
-      const int64_t p = w == 0 ? p0 : w == 1 ? p1 : w == 2 ? p2 : p3;
-      const int32_t half_turns = static_cast<int32_t>((static_cast<uint64_t>(p) * turn[i]) >> 32);
-      sincospif(static_cast<float>(half_turns) * 0x1p-31f, &sin[i], &cos[i]);
     }
   }
 };
+
+template <int B>
+__device__ __forceinline__ void put_pairs(void* base, int64_t lo, int half, const float2 (&x)[8],
+                                          bool f16) {
+  char* p = static_cast<char*>(base) + lo * B;
+#pragma unroll
+  for (int side = 0; side < 2; ++side) {
+    uint4* to = reinterpret_cast<uint4*>(p + static_cast<int64_t>(side) * half * B);
+    const float2* y = x + 4 * side;
+    if constexpr (B == 4) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        to[i] = make_uint4(__float_as_uint(y[2 * i].x), __float_as_uint(y[2 * i].y),
+                           __float_as_uint(y[2 * i + 1].x), __float_as_uint(y[2 * i + 1].y));
+    } else {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (f16) {
+          const __half2 h = __floats2half2_rn(y[i].x, y[i].y);
+          w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+          w[i] = pack_bf16x2(y[i].x, y[i].y);
+        }
+      }
+      to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+// Cosine and sine of two angles in 2^-31 of a half turn: the nearest quarter
+// turn is taken off, exactly, and least-squares polynomials on the eighth turn
+// left (off by 2^-29 and 2^-34) do the rest.
+__device__ __forceinline__ void turn_two(int32_t a, int32_t b, float2& cos, float2& sin) {
+  const int32_t qa = (a + 0x20000000) >> 30, qb = (b + 0x20000000) >> 30;
+  const float unit = 1.4629180792671596e-9f;  // pi 2^-31
+  const float2 x = make_float2(static_cast<float>(static_cast<int32_t>(
+                                   static_cast<uint32_t>(a) - (static_cast<uint32_t>(qa) << 30))) *
+                                   unit,
+                               static_cast<float>(static_cast<int32_t>(
+                                   static_cast<uint32_t>(b) - (static_cast<uint32_t>(qb) << 30))) *
+                                   unit);
+  auto both = [](float v) { return make_float2(v, v); };
+  const float2 y = mul2(x, x);
+  float2 s = fma2(y, both(-0.000194956359f), both(0.00833197869f));
+  s = fma2(s, y, both(-0.166666508f));
+  s = fma2(mul2(s, y), x, x);
+  float2 c = fma2(y, both(2.43904506e-5f), both(-0.00138867635f));
+  c = fma2(c, y, both(0.0416666232f));
+  c = fma2(c, y, both(-0.5f));
+  c = fma2(c, y, both(1.f));
+  auto place = [](int32_t q, float s1, float c1, float& sn, float& cs) {
+    sn = q & 1 ? c1 : s1;
+    cs = q & 1 ? s1 : c1;
+    if (q & 2) sn = -sn;
+    if ((q + 1) & 2) cs = -cs;
+  };
+  place(qa, s.x, c.x, sin.x, cos.x);
+  place(qb, s.y, c.y, sin.y, cos.y);
+}
 
 __device__ __forceinline__ float head_sum(float v, int lanes) {
   for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-// kBatch passes' loads are under way at once.
-template <typename T, int kBatch>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormArgs a,
-                                                             const __grid_constant__ Rates rates) {
-  __shared__ float gain[2][2 * kMaxHalf];
-  after_previous_kernel();
-  const Lane at(a);
-  const int half = a.d >> 1, heads = a.nh + a.nkv;
-  for (int i = threadIdx.x; i < 2 * a.d; i += kThreads) {
-    const int which = i >= a.d, c = which ? i - a.d : i;
-    const float* g = which ? a.gain_k : a.gain_q;
-    gain[which][c] = g ? g[c] : 1.f;
+// Where a lane stands, and the passes its warp goes through: over (token,
+// slice) units and the passes of each, the loads of a pass under way while the
+// one before is computed.
+struct Walk {
+  const NormArgs& a;
+  const Side& s;
+  int slot, chunk, per_pass, per_slice;
+  bool has;
+  int64_t unit, units, step;
+  int token, pass, last;
+  __device__ __forceinline__ Walk(const NormArgs& args, const Side& side, int block)
+      : a(args), s(side) {
+    const int lane = threadIdx.x & 31;
+    slot = lane >> a.lanes_log2;
+    chunk = lane & (a.lanes - 1);
+    per_pass = 32 >> a.lanes_log2;
+    per_slice = (s.passes + s.slices - 1) / s.slices;
+    has = 16 * chunk < a.d;
+    units = static_cast<int64_t>(a.tokens) * s.slices;
+    step = static_cast<int64_t>(s.blocks) * kWarps;
+    unit = static_cast<int64_t>(block) * kWarps + (threadIdx.x >> 5);
+    enter();
   }
-  const Turning turning(a, rates, at.chunk);
-  __syncthreads();
-  const int64_t units = static_cast<int64_t>(a.tokens) * a.slices;
-  const int per_slice = (a.passes + a.slices - 1) / a.slices;
-  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); u < units;
-       u += static_cast<int64_t>(gridDim.x) * kWarps) {
-    const int token = static_cast<int>(u / a.slices), slice = static_cast<int>(u % a.slices);
-    const int last = min(a.passes, (slice + 1) * per_slice);
-    float cos[8], sin[8];
-    for (int first = slice * per_slice; first < last; first += kBatch) {
-      Eight<T> lo[kBatch], hi[kBatch];
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int h = (first + b) * at.per_pass + at.slot;
-        if (at.has && first + b < last && h < heads) {
-          const T* x = h < a.nh
-                           ? static_cast<const T*>(a.q) + token * a.q_ts + h * a.q_hs
-                           : static_cast<const T*>(a.k) + token * a.k_ts + (h - a.nh) * a.k_hs;
-          lo[b].load(x + 8 * at.chunk);
-          hi[b].load(x + half + 8 * at.chunk);
-        } else {
-          lo[b].zero();
-          hi[b].zero();
-        }
-      }
-      if (first == slice * per_slice) turning.at(a, token, cos, sin);
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        if (first + b >= last) break;
-        const int h = (first + b) * at.per_pass + at.slot;
-        const bool key = h >= a.nh;
-        float x[8], y[8];
-        lo[b].get(x);
-        hi[b].get(y);
-        float sq = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sq = fmaf(x[i], x[i], fmaf(y[i], y[i], sq));
-        sq = head_sum(sq, a.lanes);
-        const float r = (key ? a.gain_k : a.gain_q) ? rsqrtf(sq / a.d + a.eps) : 1.f;
-        if (!at.has || h >= heads) continue;
-        const float* g = gain[key] + 8 * at.chunk;
-        float u0[8], u1[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float p = x[i] * r * g[i], q = y[i] * r * g[half + i];
-          u0[i] = p * cos[i] - q * sin[i];
-          u1[i] = q * cos[i] + p * sin[i];
-        }
-        void* out = key ? a.k_out : a.q_out;
-        const int64_t o = key ? token * a.ko_ts + (h - a.nh) * a.ko_hs
-                              : token * a.qo_ts + h * a.qo_hs;
-        store_eight(out, a.out_dtype, o + 8 * at.chunk, u0);
-        store_eight(out, a.out_dtype, o + half + 8 * at.chunk, u1);
-      }
-    }
+  __device__ __forceinline__ bool more() const { return unit < units; }
+  __device__ __forceinline__ void enter() {
+    if (!more()) return;
+    token = static_cast<int>(s.slices == 1 ? unit : unit / s.slices);
+    const int slice = s.slices == 1 ? 0 : static_cast<int>(unit % s.slices);
+    pass = slice * per_slice;
+    last = min(s.passes, pass + per_slice);
   }
-}
-
-struct GradArgs {
-  NormArgs n;  // q_out and k_out are dq and dk
-  const void *d_q, *d_k;
-  int64_t dq_ts, dq_hs, dk_ts, dk_hs;
-  float* partial;  // [CTAs][2][d]: sums of the gains' gradients
+  // The next pass; whether it is of another unit.
+  __device__ __forceinline__ bool advance() {
+    if (++pass < last) return false;
+    unit += step;
+    enter();
+    return true;
+  }
+  __device__ __forceinline__ int head() const { return pass * per_pass + slot; }
+  __device__ __forceinline__ bool mine() const { return has && head() < s.heads; }
 };
 
-// G: type of the incoming gradient, T: type of q and k.
-template <typename G, typename T, int kBatch>
-__global__ void __launch_bounds__(kThreads)
-    norm_rope_grad_kernel(const GradArgs ga, const __grid_constant__ Rates rates) {
-  const NormArgs& a = ga.n;
-  __shared__ float gain[2][2 * kMaxHalf];
-  __shared__ float sums[kWarps][2 * kMaxHalf];
-  after_previous_kernel();
-  const Lane at(a);
-  const int half = a.d >> 1, heads = a.nh + a.nkv;
-  for (int i = threadIdx.x; i < 2 * a.d; i += kThreads) {
-    const int which = i >= a.d, c = which ? i - a.d : i;
-    const float* g = which ? a.gain_k : a.gain_q;
-    gain[which][c] = g ? g[c] : 1.f;
-  }
-  const Turning turning(a, rates, at.chunk);
-  __syncthreads();
-  const int64_t units = static_cast<int64_t>(a.tokens) * a.slices;
-  const int per_slice = (a.passes + a.slices - 1) / a.slices;
-  float acc[2][16] = {};  // [query, key][lower half, upper half]
-  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); u < units;
-       u += static_cast<int64_t>(gridDim.x) * kWarps) {
-    const int token = static_cast<int>(u / a.slices), slice = static_cast<int>(u % a.slices);
-    const int last = min(a.passes, (slice + 1) * per_slice);
-    float cos[8], sin[8];
-    for (int first = slice * per_slice; first < last; first += kBatch) {
-      Eight<T> xlo[kBatch], xhi[kBatch];
-      Eight<G> glo[kBatch], ghi[kBatch];
+// Cosines and sines of a lane's eight pairs at a token's positions.
+__device__ __forceinline__ void turns(const NormArgs& a, const Rates& rates, int chunk,
+                                      const int (&pos)[4], float2 (&cos)[4], float2 (&sin)[4]) {
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int h = (first + b) * at.per_pass + at.slot;
-        if (at.has && first + b < last && h < heads) {
-          const bool key = h >= a.nh;
-          const T* x = !key ? static_cast<const T*>(a.q) + token * a.q_ts + h * a.q_hs
-                            : static_cast<const T*>(a.k) + token * a.k_ts + (h - a.nh) * a.k_hs;
-          const G* g = !key
-                           ? static_cast<const G*>(ga.d_q) + token * ga.dq_ts + h * ga.dq_hs
-                           : static_cast<const G*>(ga.d_k) + token * ga.dk_ts +
-                                 (h - a.nh) * ga.dk_hs;
-          xlo[b].load(x + 8 * at.chunk);
-          xhi[b].load(x + half + 8 * at.chunk);
-          glo[b].load(g + 8 * at.chunk);
-          ghi[b].load(g + half + 8 * at.chunk);
-        } else {
-          xlo[b].zero();
-          xhi[b].zero();
-          glo[b].zero();
-          ghi[b].zero();
-        }
+  for (int i = 0; i < 4; ++i) {
+    int32_t angle[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int pair = (8 * chunk + 2 * i + e) & (kMaxHalf - 1);
+      int p = pos[0];
+      if (a.axes > 1) {
+        const int w = rates.axis[pair];
+        p = w == 0 ? pos[0] : w == 1 ? pos[1] : w == 2 ? pos[2] : pos[3];
       }
-      if (first == slice * per_slice) turning.at(a, token, cos, sin);
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        if (first + b >= last) break;
-        const int h = (first + b) * at.per_pass + at.slot;
-        const bool key = h >= a.nh;
-        const bool norm = (key ? a.gain_k : a.gain_q) != nullptr;
-        float x[8], y[8], d0[8], d1[8];
-        xlo[b].get(x);
-        xhi[b].get(y);
-        glo[b].get(d0);
-        ghi[b].get(d1);
-        float sq = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sq = fmaf(x[i], x[i], fmaf(y[i], y[i], sq));
-        sq = head_sum(sq, a.lanes);
-        const float r = norm ? rsqrtf(sq / a.d + a.eps) : 1.f;
-        const float* g = gain[key] + 8 * at.chunk;
-        float dot = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float p = d0[i] * cos[i] + d1[i] * sin[i];
-          const float q = d1[i] * cos[i] - d0[i] * sin[i];
-          x[i] *= r;
-          y[i] *= r;
-          if (at.has && h < heads) {  // a slot without a head may have r = inf (eps 0)
-            if (key) {
-              acc[1][i] += p * x[i];
-              acc[1][8 + i] += q * y[i];
-            } else {
-              acc[0][i] += p * x[i];
-              acc[0][8 + i] += q * y[i];
-            }
-            d0[i] = p * g[i];
-            d1[i] = q * g[half + i];
-          } else {
-            d0[i] = d1[i] = 0.f;
-          }
-          dot = fmaf(d0[i], x[i], fmaf(d1[i], y[i], dot));
-        }
-        dot = head_sum(dot, a.lanes);
-        const float mean = norm ? dot / a.d : 0.f;
-        if (!at.has || h >= heads) continue;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          d0[i] = r * (d0[i] - x[i] * mean);
-          d1[i] = r * (d1[i] - y[i] * mean);
-        }
-        void* out = key ? a.k_out : a.q_out;
-        const int64_t o = key ? token * a.ko_ts + (h - a.nh) * a.ko_hs
-                              : token * a.qo_ts + h * a.qo_hs;
-        store_eight(out, a.out_dtype, o + 8 * at.chunk, d0);
-        store_eight(out, a.out_dtype, o + half + 8 * at.chunk, d1);
-      }
+      angle[e] = static_cast<int32_t>(
+          (static_cast<uint64_t>(static_cast<int64_t>(p)) * rates.turn[pair]) >> 32);
     }
-  }
-  if (!ga.partial) return;
-  // lanes of one chunk, then the CTA's warps, each in a fixed order
-  for (int which = 0; which < 2; ++which) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      for (int o = a.lanes; o < 32; o <<= 1)
-        acc[which][i] += __shfl_xor_sync(0xffffffffu, acc[which][i], o);
-    if (at.slot == 0 && at.has) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        sums[threadIdx.x >> 5][8 * at.chunk + i] = acc[which][i];
-        sums[threadIdx.x >> 5][half + 8 * at.chunk + i] = acc[which][8 + i];
-      }
-    }
-    __syncthreads();
-    for (int c = threadIdx.x; c < a.d; c += kThreads) {
-      float sum = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) sum += sums[w][c];
-      ga.partial[(static_cast<int64_t>(blockIdx.x) * 2 + which) * a.d + c] = sum;
-    }
-    __syncthreads();
+    turn_two(angle[0], angle[1], cos[i], sin[i]);
   }
 }
 
-// d_gain[c] (= or +=) the sum of column c of partial [rows][2][d]: a CTA has 32
-// columns, its warps a share of the rows each, joined in order.
-__global__ void __launch_bounds__(1024) gain_sum_kernel(const float* partial, int rows, int d,
-                                                        float* dg_q, float* dg_k,
-                                                        int accumulate) {
+__device__ __forceinline__ void positions_of(const NormArgs& a, int token, int (&pos)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    pos[i] = i < a.axes ? a.positions[static_cast<int64_t>(i) * a.tokens + token] : 0;
+}
+
+// Rates and a side's gains (ones without any) to shared memory.
+__device__ __forceinline__ void stage_tables(const NormArgs& a, const Side& s, const Rates& from,
+                                             Rates& rates, float (&gain)[2 * kMaxHalf]) {
+  for (int i = threadIdx.x; i < a.d; i += kThreads) gain[i] = s.gain ? s.gain[i] : 1.f;
+  for (int i = threadIdx.x; i < kMaxHalf; i += kThreads) {
+    rates.turn[i] = from.turn[i];
+    rates.axis[i] = from.axis[i];
+  }
+  __syncthreads();
+}
+
+// IN, OUT: bytes of a value.
+template <int IN, int OUT>
+__global__ void __launch_bounds__(kThreads, IN == 2 ? 3 : 2)
+    norm_rope_kernel(const __grid_constant__ NormArgs a, const __grid_constant__ Rates given) {
+  __shared__ Rates rates;
+  __shared__ __align__(16) float gain[2 * kMaxHalf];
+  after_previous_kernel();
+  const bool second = static_cast<int>(blockIdx.x) >= a.side[0].blocks;
+  const Side& s = a.side[second];
+  stage_tables(a, s, given, rates, gain);
+  Walk w(a, s, second ? blockIdx.x - a.side[0].blocks : blockIdx.x);
+  if (!w.more()) return;
+  const int half = a.d >> 1;
+  const float inv_d = 1.f / static_cast<float>(a.d);
+  auto fetch = [&](Pairs<IN>& x) {
+    if (w.mine())
+      x.load(s.x, w.token * s.x_ts + w.head() * s.x_hs + 8 * w.chunk, half);
+    else
+      x.zero();
+  };
+  Pairs<IN> next;
+  fetch(next);
+  int pos[4] = {};
+  if (a.axes) positions_of(a, w.token, pos);
+  bool fresh = true;
+  float2 cos[4], sin[4];
+  while (w.more()) {
+    const Pairs<IN> now = next;
+    const bool mine = w.mine();
+    const int64_t to = w.token * s.out_ts + w.head() * s.out_hs + 8 * w.chunk;
+    if (fresh && a.axes) turns(a, rates, w.chunk, pos, cos, sin);
+    fresh = w.advance();
+    if (w.more()) {
+      fetch(next);
+      if (fresh && a.axes) positions_of(a, w.token, pos);
+    }
+    float2 x[8];
+    now.get(x, a.f16_in);
+    if (s.gain) {
+      float2 sq = mul2(x[0], x[0]);
+#pragma unroll
+      for (int i = 1; i < 8; ++i) sq = fma2(x[i], x[i], sq);
+      const float r = rsqrtf(head_sum(sq.x + sq.y, a.lanes) * inv_d + a.eps);
+      const float2 r2 = make_float2(r, r);
+      const float2* g = reinterpret_cast<const float2*>(gain + (w.has ? 8 * w.chunk : 0));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i] = mul2(mul2(x[i], r2), g[i]);
+        x[4 + i] = mul2(mul2(x[4 + i], r2), g[half / 2 + i]);
+      }
+    }
+    if (a.axes) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 p = x[i], q = x[4 + i];
+        const float2 minus = make_float2(-sin[i].x, -sin[i].y);
+        x[i] = fma2(q, minus, mul2(p, cos[i]));
+        x[4 + i] = fma2(p, sin[i], mul2(q, cos[i]));
+      }
+    }
+    if (mine) put_pairs<OUT>(s.out, to, half, x, a.f16_out);
+  }
+}
+
+// G, IN, OUT: bytes of a value of the incoming gradient, of q and k, of the result.
+template <int G, int IN, int OUT>
+__global__ void __launch_bounds__(kThreads, 2)
+    norm_rope_grad_kernel(const __grid_constant__ NormArgs a,
+                          const __grid_constant__ Rates given) {
+  __shared__ Rates rates;
+  __shared__ __align__(16) float gain[2 * kMaxHalf];
+  __shared__ float sums[kWarps][2 * kMaxHalf];
+  after_previous_kernel();
+  const bool second = static_cast<int>(blockIdx.x) >= a.side[0].blocks;
+  const Side& s = a.side[second];
+  stage_tables(a, s, given, rates, gain);
+  Walk w(a, s, second ? blockIdx.x - a.side[0].blocks : blockIdx.x);
+  const int half = a.d >> 1;
+  const float inv_d = 1.f / static_cast<float>(a.d);
+  Pairs<IN> next_x;
+  Pairs<G> next_g;
+  auto fetch = [&] {
+    if (w.mine()) {
+      next_x.load(s.x, w.token * s.x_ts + w.head() * s.x_hs + 8 * w.chunk, half);
+      next_g.load(s.dy, w.token * s.dy_ts + w.head() * s.dy_hs + 8 * w.chunk, half);
+    } else {
+      next_x.zero();
+      next_g.zero();
+    }
+  };
+  int pos[4] = {};
+  if (w.more()) {
+    fetch();
+    if (a.axes) positions_of(a, w.token, pos);
+  }
+  bool fresh = true;
+  float2 cos[4], sin[4], acc[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    cos[i] = make_float2(1.f, 1.f);
+    sin[i] = make_float2(0.f, 0.f);
+  }
+  while (w.more()) {
+    float2 x[8], d[8];
+    next_x.get(x, a.f16_in);
+    next_g.get(d, a.f16_dy);
+    const bool mine = w.mine();
+    const int64_t to = w.token * s.out_ts + w.head() * s.out_hs + 8 * w.chunk;
+    if (fresh && a.axes) turns(a, rates, w.chunk, pos, cos, sin);
+    fresh = w.advance();
+    if (w.more()) {
+      fetch();
+      if (fresh && a.axes) positions_of(a, w.token, pos);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // the gradient turned back
+      const float2 p = d[i], q = d[4 + i];
+      const float2 minus = make_float2(-sin[i].x, -sin[i].y);
+      d[i] = fma2(q, sin[i], mul2(p, cos[i]));
+      d[4 + i] = fma2(p, minus, mul2(q, cos[i]));
+    }
+    if (s.gain) {
+      float2 sq = mul2(x[0], x[0]);
+#pragma unroll
+      for (int i = 1; i < 8; ++i) sq = fma2(x[i], x[i], sq);
+      const float r = rsqrtf(head_sum(sq.x + sq.y, a.lanes) * inv_d + a.eps);
+      const float2 r2 = make_float2(r, r);
+      const float2* g = reinterpret_cast<const float2*>(gain + (w.has ? 8 * w.chunk : 0));
+      float2 dot = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[i] = mul2(x[i], r2);
+        if (mine) acc[i] = fma2(d[i], x[i], acc[i]);  // a lane without a head may have r = inf
+        d[i] = mul2(d[i], g[i < 4 ? i : half / 2 + i - 4]);
+        dot = fma2(d[i], x[i], dot);
+      }
+      // lanes of no head, and those past the head's end, hold zeros (or, of no head, are not kept)
+      const float mean = head_sum(dot.x + dot.y, a.lanes) * inv_d;
+      const float2 minus = make_float2(-mean, -mean);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) d[i] = mul2(fma2(x[i], minus, d[i]), r2);
+    }
+    if (mine) put_pairs<OUT>(s.out, to, half, d, a.f16_out);
+  }
+  if (!a.partial) return;
+  // lanes of one chunk, then the CTA's warps, each in a fixed order
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    for (int o = a.lanes; o < 32; o <<= 1) {
+      acc[i].x += __shfl_xor_sync(0xffffffffu, acc[i].x, o);
+      acc[i].y += __shfl_xor_sync(0xffffffffu, acc[i].y, o);
+    }
+  if (w.slot == 0 && w.has) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      *reinterpret_cast<float2*>(
+          &sums[threadIdx.x >> 5][(i < 4 ? 0 : half) + 8 * w.chunk + 2 * (i & 3)]) = acc[i];
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < a.d; c += kThreads) {
+    float sum = 0.f;
+#pragma unroll
+    for (int v = 0; v < kWarps; ++v) sum += sums[v][c];
+    a.partial[static_cast<int64_t>(blockIdx.x) * a.d + c] = sum;
+  }
+}
+
+// d_gain[c] (= or +=) the sum of column c of partial [blocks of q, then of k][d]:
+// a CTA has 32 columns of one of them, its warps a share of the rows each,
+// joined in order.
+__global__ void __launch_bounds__(1024) gain_sum_kernel(const float* partial, int q_rows,
+                                                        int k_rows, int d, float* dg_q,
+                                                        float* dg_k, int accumulate) {
   __shared__ float sums[32][33];
   after_previous_kernel();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
+  const int per_side = (d + 31) / 32;
+  const bool second = static_cast<int>(blockIdx.x) >= per_side;
+  const int c = (blockIdx.x - (second ? per_side : 0)) * 32 + lane;
+  const int rows = second ? k_rows : q_rows;
+  const float* from = partial + (second ? static_cast<int64_t>(q_rows) * d : 0);
   float sum = 0.f;
-  if (c < 2 * d)
-    for (int r = warp; r < rows; r += 32) sum += partial[static_cast<int64_t>(r) * 2 * d + c];
+  if (c < d) {
+#pragma unroll 4
+    for (int r = warp; r < rows; r += 32) sum += from[static_cast<int64_t>(r) * d + c];
+  }
   sums[warp][lane] = sum;
   __syncthreads();
   if (warp) return;
   sum = 0.f;
 #pragma unroll
   for (int w = 0; w < 32; ++w) sum += sums[w][lane];
-  float* out = c < d ? dg_q : dg_k;
-  if (c < 2 * d && out) {
-    out += c < d ? c : c - d;
-    *out = accumulate ? *out + sum : sum;
-  }
+  float* out = second ? dg_k : dg_q;
+  if (c < d && out) out[c] = accumulate ? out[c] + sum : sum;
 }
 
-constexpr int kCtasPerSm = 4;
-
-// Fills in the split of the work; returns the number of CTAs.
+// Splits the work: lanes of a head, and for q and k the warps that share a
+// token and the CTAs. Few tokens: their heads are spread over more warps, which
+// each take the token's sines again. CTAs are dealt out by passes, a token's
+// sines counting as one. Returns the number of CTAs.
 int64_t split_work(NormArgs* a, int ctas_per_sm) {
   int lanes = 1, log2 = 0;
   while (lanes * 16 < a->d) {
@@ -354,17 +449,27 @@ int64_t split_work(NormArgs* a, int ctas_per_sm) {
   a->lanes = lanes;
   a->lanes_log2 = log2;
   const int per_pass = 32 / lanes;
-  a->passes = (a->nh + a->nkv + per_pass - 1) / per_pass;
-  // few tokens: their heads are spread over more warps, which each take the
-  // token's sines again
-  const int64_t warps = static_cast<int64_t>(num_sms()) * ctas_per_sm * kWarps;
-  const int64_t want = (warps + a->tokens - 1) / a->tokens;
-  a->slices = static_cast<int>(std::min<int64_t>(want, a->passes));
-  const int per_slice = (a->passes + a->slices - 1) / a->slices;
-  a->slices = (a->passes + per_slice - 1) / per_slice;
-  const int64_t units = static_cast<int64_t>(a->tokens) * a->slices;
-  return std::min<int64_t>((units + kWarps - 1) / kWarps,
-                           static_cast<int64_t>(num_sms()) * ctas_per_sm);
+  int64_t work[2];
+  for (int i = 0; i < 2; ++i) {
+    a->side[i].passes = (a->side[i].heads + per_pass - 1) / per_pass;
+    work[i] = a->side[i].heads ? a->side[i].passes + 1 : 0;
+  }
+  const int64_t all = static_cast<int64_t>(num_sms()) * ctas_per_sm;
+  int64_t total = 0;
+  for (int i = 0; i < 2; ++i) {
+    Side& s = a->side[i];
+    s.blocks = s.slices = 0;
+    if (!s.heads) continue;
+    const int64_t share = std::max<int64_t>(1, all * work[i] / (work[0] + work[1]));
+    const int64_t want = (share * kWarps + a->tokens - 1) / a->tokens;
+    s.slices = static_cast<int>(std::min<int64_t>(want, s.passes));
+    const int per_slice = (s.passes + s.slices - 1) / s.slices;
+    s.slices = (s.passes + per_slice - 1) / per_slice;
+    const int64_t units = static_cast<int64_t>(a->tokens) * s.slices;
+    s.blocks = static_cast<int>(std::min<int64_t>((units + kWarps - 1) / kWarps, share));
+    total += s.blocks;
+  }
+  return total;
 }
 
 const char* shape_problem(int tokens, int nh, int nkv, int d) {
@@ -383,23 +488,29 @@ const char* common_problem(int tokens, int nh, int nkv, int d, const rdt_heads* 
                            int out_dtype, NormArgs* a, Rates* rates) {
   if (!dtype_ok(dtype) || !dtype_ok(out_dtype))
     return "dtypes must be RDT_F32, RDT_BF16 or RDT_F16";
-  const rdt_heads none = {};
+  *a = NormArgs{};
   const rdt_heads *ins[2] = {q, k}, *outs[2] = {q_out, k_out};
-  const int heads[2] = {nh, nkv};
+  const float* gains[2] = {gain_q, gain_k};
   for (int i = 0; i < 2; ++i) {
-    if (heads[i] == 0) continue;
-    if (const char* why = heads_problem(ins[i], tokens, heads[i], d, dtype_bytes(dtype), false))
+    Side& s = a->side[i];
+    s.heads = i ? nkv : nh;
+    if (s.heads == 0) continue;
+    if (const char* why = heads_problem(ins[i], tokens, s.heads, d, dtype_bytes(dtype), false))
       return why;
-    if (const char* why =
-            heads_problem(outs[i], tokens, heads[i], d, dtype_bytes(out_dtype), true))
+    if (const char* why = heads_problem(outs[i], tokens, s.heads, d, dtype_bytes(out_dtype), true))
       return why;
     if (ins[i]->data == outs[i]->data &&
         (dtype != out_dtype || (tokens > 1 && ins[i]->token_stride != outs[i]->token_stride) ||
-         (heads[i] > 1 && ins[i]->head_stride != outs[i]->head_stride)))
+         (s.heads > 1 && ins[i]->head_stride != outs[i]->head_stride)))
       return "an output at its input's place needs the input's type and strides";
+    s.x = ins[i]->data;
+    s.x_ts = ins[i]->token_stride;
+    s.x_hs = ins[i]->head_stride;
+    s.out = outs[i]->data;
+    s.out_ts = outs[i]->token_stride;
+    s.out_hs = outs[i]->head_stride;
+    s.gain = gains[i];
   }
-  if (nh == 0) q = q_out = &none;
-  if (nkv == 0) k = k_out = &none;
   if (!aligned4(gain_q) || !aligned4(gain_k) || !aligned4(positions))
     return "gains and positions must be 4-byte aligned";
   if (!(eps >= 0.f) || std::isinf(eps)) return "eps must be finite and >= 0";
@@ -408,13 +519,13 @@ const char* common_problem(int tokens, int nh, int nkv, int d, const rdt_heads* 
     if (axes < 1 || axes > 4) return "axes must be in [1, 4]";
     if (!(theta > 0.f) || std::isinf(theta)) return "theta must be finite and > 0";
     if (axes > 1 && !sections) return "sections are needed with more than one axis";
-    int sum = 0;
-    for (int i = 0; i < 3; ++i) rates->end[i] = INT32_MAX;
     if (sections) {
+      int sum = 0;
       for (int i = 0; i < axes; ++i) {
         if (sections[i] < 0 || sections[i] > d) return "a section must be in [0, head_dim / 2]";
+        for (int pair = sum; pair < sum + sections[i] && pair < d / 2; ++pair)
+          rates->axis[pair] = static_cast<uint8_t>(i);
         sum += sections[i];
-        if (i + 1 < axes) rates->end[i] = sum;
       }
       if (sum != d / 2) return "sections must add up to head_dim / 2";
     }
@@ -424,30 +535,33 @@ const char* common_problem(int tokens, int nh, int nkv, int d, const rdt_heads* 
       rates->turn[i] = static_cast<uint64_t>(std::ldexp(turns - std::floor(turns), 63)) * 2;
     }
   }
-  *a = NormArgs{q->data,         k->data,         q->token_stride, q->head_stride, k->token_stride,
-                k->head_stride,  gain_q,          gain_k,          eps,            positions,
-                axes,            q_out->data,     k_out->data,     q_out->token_stride,
-                q_out->head_stride, k_out->token_stride, k_out->head_stride, out_dtype,
-                tokens,          nh,              nkv,             d,              0, 0, 0, 0};
+  a->eps = eps;
+  a->positions = positions;
+  a->axes = positions ? axes : 0;
+  a->tokens = tokens;
+  a->d = d;
+  a->f16_in = dtype == RDT_F16;
+  a->f16_out = out_dtype == RDT_F16;
   return nullptr;
 }
 
-template <typename T, int kBatch>
-cudaError_t launch_norm(NormArgs a, const Rates& r, cudaStream_t s) {
-  const int64_t grid = split_work(&a, kCtasPerSm);
-  return launch_overlapping(norm_rope_kernel<T, kBatch>, grid, kThreads, 0, s, a, r);
+// CTAs of an SM, by the bytes of an input's value: what their registers leave.
+constexpr int kCtasPerSm[2] = {3, 2}, kGradCtasPerSm = 2;
+
+template <int IN>
+cudaError_t launch_norm(NormArgs a, int out_dtype, const Rates& r, cudaStream_t s) {
+  const int64_t grid = split_work(&a, kCtasPerSm[IN == 4]);
+  return out_dtype == RDT_F32
+             ? launch_overlapping(norm_rope_kernel<IN, 4>, grid, kThreads, 0, s, a, r)
+             : launch_overlapping(norm_rope_kernel<IN, 2>, grid, kThreads, 0, s, a, r);
 }
 
-constexpr int kGradCtasPerSm = 2;
-
-template <typename G>
-cudaError_t launch_grad(const GradArgs& a, int dtype, int64_t grid, const Rates& r,
+template <int G, int IN>
+cudaError_t launch_grad(const NormArgs& a, int out_dtype, int64_t grid, const Rates& r,
                         cudaStream_t s) {
-  if (dtype == RDT_F32)
-    return launch_overlapping(norm_rope_grad_kernel<G, float, 1>, grid, kThreads, 0, s, a, r);
-  if (dtype == RDT_BF16)
-    return launch_overlapping(norm_rope_grad_kernel<G, bf16, 2>, grid, kThreads, 0, s, a, r);
-  return launch_overlapping(norm_rope_grad_kernel<G, __half, 2>, grid, kThreads, 0, s, a, r);
+  return out_dtype == RDT_F32
+             ? launch_overlapping(norm_rope_grad_kernel<G, IN, 4>, grid, kThreads, 0, s, a, r)
+             : launch_overlapping(norm_rope_grad_kernel<G, IN, 2>, grid, kThreads, 0, s, a, r);
 }
 
 }  // namespace
@@ -473,9 +587,8 @@ rdt_status rdt_qk_norm_rope(int32_t tokens, int32_t n_heads, int32_t n_kv_heads,
                                        out_dtype, &a, &r))
     return refuse(why);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return launched(dtype == RDT_F32    ? launch_norm<float, 2>(a, r, s)
-                  : dtype == RDT_BF16 ? launch_norm<bf16, 4>(a, r, s)
-                                      : launch_norm<__half, 4>(a, r, s));
+  return launched(dtype == RDT_F32 ? launch_norm<4>(a, out_dtype, r, s)
+                                   : launch_norm<2>(a, out_dtype, r, s));
 }
 
 size_t rdt_qk_norm_rope_backward_workspace_bytes(int32_t tokens, int32_t n_heads,
@@ -483,10 +596,10 @@ size_t rdt_qk_norm_rope_backward_workspace_bytes(int32_t tokens, int32_t n_heads
   if (shape_problem(tokens, n_heads, n_kv_heads, head_dim) || tokens == 0) return 0;
   NormArgs a = {};
   a.tokens = tokens;
-  a.nh = n_heads;
-  a.nkv = n_kv_heads;
+  a.side[0].heads = n_heads;
+  a.side[1].heads = n_kv_heads;
   a.d = head_dim;
-  return static_cast<size_t>(split_work(&a, kGradCtasPerSm)) * 2 * head_dim * sizeof(float);
+  return static_cast<size_t>(split_work(&a, kGradCtasPerSm)) * head_dim * sizeof(float);
 }
 
 rdt_status rdt_qk_norm_rope_backward(int32_t tokens, int32_t n_heads, int32_t n_kv_heads,
@@ -512,48 +625,45 @@ rdt_status rdt_qk_norm_rope_backward(int32_t tokens, int32_t n_heads, int32_t n_
     return launched(e);
   }
   if (!dtype_ok(d_dtype)) return refuse("d_dtype must be RDT_F32, RDT_BF16 or RDT_F16");
-  GradArgs a = {};
+  NormArgs a;
   Rates r;
   if (const char* why = common_problem(tokens, n_heads, n_kv_heads, head_dim, q, k, dtype, gain_q,
                                        gain_k, eps, positions, axes, sections, theta, dq, dk,
-                                       out_dtype, &a.n, &r))
+                                       out_dtype, &a, &r))
     return refuse(why);
-  const rdt_heads none = {};
   for (int i = 0; i < 2; ++i) {
     const rdt_heads *g = i ? d_k_out : d_q_out, *o = i ? dk : dq;
-    const int heads = i ? n_kv_heads : n_heads;
-    if (heads == 0) continue;
+    Side& side = a.side[i];
+    if (side.heads == 0) continue;
     if (const char* why =
-            heads_problem(g, tokens, heads, head_dim, dtype_bytes(d_dtype), false))
+            heads_problem(g, tokens, side.heads, head_dim, dtype_bytes(d_dtype), false))
       return refuse(why);
     if (g->data == o->data &&
         (d_dtype != out_dtype || (tokens > 1 && g->token_stride != o->token_stride) ||
-         (heads > 1 && g->head_stride != o->head_stride)))
+         (side.heads > 1 && g->head_stride != o->head_stride)))
       return refuse("an output at its input's place needs the input's type and strides");
+    side.dy = g->data;
+    side.dy_ts = g->token_stride;
+    side.dy_hs = g->head_stride;
   }
-  if (n_heads == 0) d_q_out = &none;
-  if (n_kv_heads == 0) d_k_out = &none;
-  a.d_q = d_q_out->data;
-  a.d_k = d_k_out->data;
-  a.dq_ts = d_q_out->token_stride;
-  a.dq_hs = d_q_out->head_stride;
-  a.dk_ts = d_k_out->token_stride;
-  a.dk_hs = d_k_out->head_stride;
-  const int64_t grid = split_work(&a.n, kGradCtasPerSm);
+  a.f16_dy = d_dtype == RDT_F16;
+  const int64_t grid = split_work(&a, kGradCtasPerSm);
   const bool sums = d_gain_q || d_gain_k;
   if (sums) {
     if (!ws) return refuse("null pointer");
     if (reinterpret_cast<uintptr_t>(ws) & 255) return refuse("ws must be 256-byte aligned");
-    if (ws_bytes < static_cast<size_t>(grid) * 2 * head_dim * sizeof(float))
+    if (ws_bytes < static_cast<size_t>(grid) * head_dim * sizeof(float))
       return refuse("workspace too small");
     a.partial = static_cast<float*>(ws);
   }
-  cudaError_t e = d_dtype == RDT_F32    ? launch_grad<float>(a, dtype, grid, r, s)
-                  : d_dtype == RDT_BF16 ? launch_grad<bf16>(a, dtype, grid, r, s)
-                                        : launch_grad<__half>(a, dtype, grid, r, s);
+  const bool wide_g = d_dtype == RDT_F32, wide_x = dtype == RDT_F32;
+  cudaError_t e = wide_g ? (wide_x ? launch_grad<4, 4>(a, out_dtype, grid, r, s)
+                                   : launch_grad<4, 2>(a, out_dtype, grid, r, s))
+                         : (wide_x ? launch_grad<2, 4>(a, out_dtype, grid, r, s)
+                                   : launch_grad<2, 2>(a, out_dtype, grid, r, s));
   if (e == cudaSuccess && sums)
-    e = launch_overlapping(gain_sum_kernel, (2 * head_dim + 31) / 32, 1024, 0, s, a.partial,
-                           static_cast<int>(grid), head_dim, d_gain_q, d_gain_k,
+    e = launch_overlapping(gain_sum_kernel, 2 * ((head_dim + 31) / 32), 1024, 0, s, a.partial,
+                           a.side[0].blocks, a.side[1].blocks, head_dim, d_gain_q, d_gain_k,
                            accumulate ? 1 : 0);
   return launched(e);
 }
