@@ -10,8 +10,8 @@
 // Bound by DRAM: every value is read once and written once. A lane holds
 // eight neighbouring pairs (two 16-byte loads of a 16-bit type), so a head of
 // 128 is eight lanes and a warp takes four heads at a time; all heads of a
-// token share the lane's eight cosines and sines. A pass's loads are under way
-// while the one before is computed, in pairs of fp32 (fma.f32x2). q and k have
+// token share the lane's eight cosines and sines. The next heads' loads are under
+// way while some are computed, in pairs of fp32 (fma.f32x2). q and k have
 // CTAs of their own, so that a warp sums one gain's gradient.
 //
 // Angles: a full turn is 2^64. A pair's rate is kept as a 64-bit fraction of a
@@ -28,6 +28,7 @@ namespace rdt {
 namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kCtasPerSm = 2;  // what their registers leave
 constexpr int kMaxHalf = 128;  // pairs of a head of 256
 
 // Turns of a pair for each position, in 2^-64, and the pair's axis.
@@ -36,14 +37,14 @@ struct Rates {
   uint8_t axis[kMaxHalf];
 };
 
-// q or k. A warp takes `per_pass` of its heads at a time; `slices` warps share
-// the passes over a token, and `blocks` CTAs the tokens.
+// q or k. A warp takes `per_pass` of its heads at a time, in `passes` over a
+// token; the warps of `blocks` CTAs share the passes over all tokens evenly.
 struct Side {
   const void *x, *dy;
   void* out;
   const float* gain;  // null: no norm
   int64_t x_ts, x_hs, dy_ts, dy_hs, out_ts, out_hs;
-  int heads, passes, slices, blocks;
+  int heads, passes, blocks;
 };
 
 struct NormArgs {
@@ -61,12 +62,11 @@ struct NormArgs {
 template <int B>
 struct Pairs {
   uint4 v[B];  // the lower half's eight values, then the upper's
-  __device__ __forceinline__ void load(const void* base, int64_t lo, int half) {
-    const char* p = static_cast<const char*>(base) + lo * B;
+  __device__ __forceinline__ void load(const char* p, int half) {
 #pragma unroll
     for (int i = 0; i < B / 2; ++i) {
       v[i] = reinterpret_cast<const uint4*>(p)[i];
-      v[B / 2 + i] = reinterpret_cast<const uint4*>(p + static_cast<int64_t>(half) * B)[i];
+      v[B / 2 + i] = reinterpret_cast<const uint4*>(p + half * B)[i];
     }
   }
   __device__ __forceinline__ void zero() {
@@ -94,12 +94,10 @@ struct Pairs {
 };
 
 template <int B>
-__device__ __forceinline__ void put_pairs(void* base, int64_t lo, int half, const float2 (&x)[8],
-                                          bool f16) {
-  char* p = static_cast<char*>(base) + lo * B;
+__device__ __forceinline__ void put_pairs(char* p, int half, const float2 (&x)[8], bool f16) {
 #pragma unroll
   for (int side = 0; side < 2; ++side) {
-    uint4* to = reinterpret_cast<uint4*>(p + static_cast<int64_t>(side) * half * B);
+    uint4* to = reinterpret_cast<uint4*>(p + side * half * B);
     const float2* y = x + 4 * side;
     if constexpr (B == 4) {
 #pragma unroll
@@ -158,15 +156,15 @@ __device__ __forceinline__ float head_sum(float v, int lanes) {
   return v;
 }
 
-// Where a lane stands, and the passes its warp goes through: over (token,
-// slice) units and the passes of each, the loads of a pass under way while the
-// one before is computed.
+// Where a lane stands, and the passes its warp goes through, one run of them
+// token by token: the loads of a step under way while the one before is
+// computed.
 struct Walk {
   const NormArgs& a;
   const Side& s;
-  int slot, chunk, per_pass, per_slice;
+  int slot, chunk, per_pass;
   bool has;
-  int64_t unit, units, step;
+  int64_t left;  // passes
   int token, pass, last;
   __device__ __forceinline__ Walk(const NormArgs& args, const Side& side, int block)
       : a(args), s(side) {
@@ -174,50 +172,70 @@ struct Walk {
     slot = lane >> a.lanes_log2;
     chunk = lane & (a.lanes - 1);
     per_pass = 32 >> a.lanes_log2;
-    per_slice = (s.passes + s.slices - 1) / s.slices;
     has = 16 * chunk < a.d;
-    units = static_cast<int64_t>(a.tokens) * s.slices;
-    step = static_cast<int64_t>(s.blocks) * kWarps;
-    unit = static_cast<int64_t>(block) * kWarps + (threadIdx.x >> 5);
-    enter();
+    const int64_t all = static_cast<int64_t>(a.tokens) * s.passes, warps = s.blocks * kWarps;
+    const int64_t me = static_cast<int64_t>(block) * kWarps + (threadIdx.x >> 5);
+    // the first `all % warps` warps have one more
+    const int64_t each = all / warps, more_of = all % warps;
+    const int64_t first = me * each + min(me, more_of);
+    left = each + (me < more_of);
+    token = static_cast<int>(first / s.passes);
+    pass = static_cast<int>(first % s.passes);
+    last = static_cast<int>(min(static_cast<int64_t>(s.passes), pass + left));
   }
-  __device__ __forceinline__ bool more() const { return unit < units; }
-  __device__ __forceinline__ void enter() {
-    if (!more()) return;
-    token = static_cast<int>(s.slices == 1 ? unit : unit / s.slices);
-    const int slice = s.slices == 1 ? 0 : static_cast<int>(unit % s.slices);
-    pass = slice * per_slice;
-    last = min(s.passes, pass + per_slice);
-  }
-  // The next pass; whether it is of another unit.
-  __device__ __forceinline__ bool advance() {
-    if (++pass < last) return false;
-    unit += step;
-    enter();
+  __device__ __forceinline__ bool more() const { return left > 0; }
+  // The next `n` passes; whether they are of another token.
+  __device__ __forceinline__ bool advance(int n) {
+    left -= min(n, last - pass);
+    pass += n;
+    if (pass < last) return false;
+    ++token;
+    pass = 0;
+    last = static_cast<int>(min(static_cast<int64_t>(s.passes), left));
     return true;
   }
-  __device__ __forceinline__ int head() const { return pass * per_pass + slot; }
-  __device__ __forceinline__ bool mine() const { return has && head() < s.heads; }
+  __device__ __forceinline__ bool mine(int pass_of) const {
+    return has && pass_of < last && pass_of * per_pass + slot < s.heads;
+  }
+  // This lane's place in a tensor at the pass, in elements.
+  __device__ __forceinline__ int64_t at(int64_t ts, int64_t hs) const {
+    return token * ts + static_cast<int64_t>(pass * per_pass + slot) * hs + 8 * chunk;
+  }
 };
 
-// Cosines and sines of a lane's eight pairs at a token's positions.
-__device__ __forceinline__ void turns(const NormArgs& a, const Rates& rates, int chunk,
+// Cosines and sines of a lane's eight pairs at a token's positions. The lanes
+// that hold the same pairs of other heads compute a part each (two pairs, four
+// where only two heads fit a warp) and pass them on.
+__device__ __forceinline__ void turns(const NormArgs& a, const Rates& rates, const Walk& w,
                                       const int (&pos)[4], float2 (&cos)[4], float2 (&sin)[4]) {
+  const bool two = w.per_pass == 2;
+  float2 c[2], s[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int part = 0; part < 2; ++part) {
+    if (part && !two) break;
+    const int i = two ? w.slot + 2 * part : w.slot & 3;
     int32_t angle[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int pair = (8 * chunk + 2 * i + e) & (kMaxHalf - 1);
+      const int pair = (8 * w.chunk + 2 * i + e) & (kMaxHalf - 1);
       int p = pos[0];
       if (a.axes > 1) {
-        const int w = rates.axis[pair];
-        p = w == 0 ? pos[0] : w == 1 ? pos[1] : w == 2 ? pos[2] : pos[3];
+        const int which = rates.axis[pair];
+        p = which == 0 ? pos[0] : which == 1 ? pos[1] : which == 2 ? pos[2] : pos[3];
       }
       angle[e] = static_cast<int32_t>(
           (static_cast<uint64_t>(static_cast<int64_t>(p)) * rates.turn[pair]) >> 32);
     }
-    turn_two(angle[0], angle[1], cos[i], sin[i]);
+    turn_two(angle[0], angle[1], c[part], s[part]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int from = ((two ? i & 1 : i) << a.lanes_log2) + w.chunk;
+    const int part = two && i >= 2;
+    cos[i].x = __shfl_sync(0xffffffffu, part ? c[1].x : c[0].x, from);
+    cos[i].y = __shfl_sync(0xffffffffu, part ? c[1].y : c[0].y, from);
+    sin[i].x = __shfl_sync(0xffffffffu, part ? s[1].x : s[0].x, from);
+    sin[i].y = __shfl_sync(0xffffffffu, part ? s[1].y : s[0].y, from);
   }
 }
 
@@ -225,6 +243,18 @@ __device__ __forceinline__ void positions_of(const NormArgs& a, int token, int (
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     pos[i] = i < a.axes ? a.positions[static_cast<int64_t>(i) * a.tokens + token] : 0;
+}
+
+// A lane's gains: those of its lower eight pairs' values, then of the upper.
+__device__ __forceinline__ void gains_of(const float* gain, const Walk& w, int half,
+                                         float2 (&g)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 v = *reinterpret_cast<const float4*>(gain + (w.has ? 8 * w.chunk : 0) +
+                                                      (i >> 1) * half + 4 * (i & 1));
+    g[2 * i] = make_float2(v.x, v.y);
+    g[2 * i + 1] = make_float2(v.z, v.w);
+  }
 }
 
 // Rates and a side's gains (ones without any) to shared memory.
@@ -238,9 +268,9 @@ __device__ __forceinline__ void stage_tables(const NormArgs& a, const Side& s, c
   __syncthreads();
 }
 
-// IN, OUT: bytes of a value.
-template <int IN, int OUT>
-__global__ void __launch_bounds__(kThreads, IN == 2 ? 3 : 2)
+// IN, OUT: bytes of a value; BATCH passes at a time.
+template <int IN, int OUT, int BATCH>
+__global__ void __launch_bounds__(kThreads, 2)
     norm_rope_kernel(const __grid_constant__ NormArgs a, const __grid_constant__ Rates given) {
   __shared__ Rates rates;
   __shared__ __align__(16) float gain[2 * kMaxHalf];
@@ -252,53 +282,75 @@ __global__ void __launch_bounds__(kThreads, IN == 2 ? 3 : 2)
   if (!w.more()) return;
   const int half = a.d >> 1;
   const float inv_d = 1.f / static_cast<float>(a.d);
-  auto fetch = [&](Pairs<IN>& x) {
-    if (w.mine())
-      x.load(s.x, w.token * s.x_ts + w.head() * s.x_hs + 8 * w.chunk, half);
-    else
-      x.zero();
+  const int64_t x_pass = w.per_pass * s.x_hs * IN, out_pass = w.per_pass * s.out_hs * OUT;
+  float2 g[8];
+  gains_of(gain, w, half, g);
+  const char* from = static_cast<const char*>(s.x) + w.at(s.x_ts, s.x_hs) * IN;
+  char* to = static_cast<char*>(s.out) + w.at(s.out_ts, s.out_hs) * OUT;
+  Pairs<IN> next[BATCH];
+  auto fetch = [&] {
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b) {
+      if (w.mine(w.pass + b))
+        next[b].load(from + b * x_pass, half);
+      else
+        next[b].zero();
+    }
   };
-  Pairs<IN> next;
-  fetch(next);
+  fetch();
   int pos[4] = {};
   if (a.axes) positions_of(a, w.token, pos);
   bool fresh = true;
-  float2 cos[4], sin[4];
+  float2 cos[4], sin[4], minus[4];
   while (w.more()) {
-    const Pairs<IN> now = next;
-    const bool mine = w.mine();
-    const int64_t to = w.token * s.out_ts + w.head() * s.out_hs + 8 * w.chunk;
-    if (fresh && a.axes) turns(a, rates, w.chunk, pos, cos, sin);
-    fresh = w.advance();
-    if (w.more()) {
-      fetch(next);
-      if (fresh && a.axes) positions_of(a, w.token, pos);
+    Pairs<IN> now[BATCH];
+    bool mine[BATCH];
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b) {
+      now[b] = next[b];
+      mine[b] = w.mine(w.pass + b);
     }
-    float2 x[8];
-    now.get(x, a.f16_in);
-    if (s.gain) {
-      float2 sq = mul2(x[0], x[0]);
+    char* const to_now = to;
+    if (fresh && a.axes) {
+      turns(a, rates, w, pos, cos, sin);
 #pragma unroll
-      for (int i = 1; i < 8; ++i) sq = fma2(x[i], x[i], sq);
-      const float r = rsqrtf(head_sum(sq.x + sq.y, a.lanes) * inv_d + a.eps);
-      const float2 r2 = make_float2(r, r);
-      const float2* g = reinterpret_cast<const float2*>(gain + (w.has ? 8 * w.chunk : 0));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[i] = mul2(mul2(x[i], r2), g[i]);
-        x[4 + i] = mul2(mul2(x[4 + i], r2), g[half / 2 + i]);
+      for (int i = 0; i < 4; ++i) minus[i] = make_float2(-sin[i].x, -sin[i].y);
+    }
+    fresh = w.advance(BATCH);
+    if (fresh) {
+      if (w.more()) {
+        from = static_cast<const char*>(s.x) + w.at(s.x_ts, s.x_hs) * IN;
+        to = static_cast<char*>(s.out) + w.at(s.out_ts, s.out_hs) * OUT;
+        if (a.axes) positions_of(a, w.token, pos);
       }
+    } else {
+      from += BATCH * x_pass;
+      to += BATCH * out_pass;
     }
-    if (a.axes) {
+    if (w.more()) fetch();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 p = x[i], q = x[4 + i];
-        const float2 minus = make_float2(-sin[i].x, -sin[i].y);
-        x[i] = fma2(q, minus, mul2(p, cos[i]));
-        x[4 + i] = fma2(p, sin[i], mul2(q, cos[i]));
+    for (int b = 0; b < BATCH; ++b) {
+      float2 x[8];
+      now[b].get(x, a.f16_in);
+      if (s.gain) {
+        float2 sq = mul2(x[0], x[0]);
+#pragma unroll
+        for (int i = 1; i < 8; ++i) sq = fma2(x[i], x[i], sq);
+        const float r = rsqrtf(head_sum(sq.x + sq.y, a.lanes) * inv_d + a.eps);
+        const float2 r2 = make_float2(r, r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = mul2(mul2(x[i], r2), g[i]);
       }
+      if (a.axes) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 p = x[i], q = x[4 + i];
+          x[i] = fma2(q, minus[i], mul2(p, cos[i]));
+          x[4 + i] = fma2(p, sin[i], mul2(q, cos[i]));
+        }
+      }
+      if (mine[b]) put_pairs<OUT>(to_now + b * out_pass, half, x, a.f16_out);
     }
-    if (mine) put_pairs<OUT>(s.out, to, half, x, a.f16_out);
   }
 }
 
@@ -317,12 +369,21 @@ __global__ void __launch_bounds__(kThreads, 2)
   Walk w(a, s, second ? blockIdx.x - a.side[0].blocks : blockIdx.x);
   const int half = a.d >> 1;
   const float inv_d = 1.f / static_cast<float>(a.d);
+  const int64_t x_pass = w.per_pass * s.x_hs * IN, dy_pass = w.per_pass * s.dy_hs * G,
+                out_pass = w.per_pass * s.out_hs * OUT;
+  const char *from = nullptr, *from_dy = nullptr;
+  char* to = nullptr;
+  auto enter = [&] {
+    from = static_cast<const char*>(s.x) + w.at(s.x_ts, s.x_hs) * IN;
+    from_dy = static_cast<const char*>(s.dy) + w.at(s.dy_ts, s.dy_hs) * G;
+    to = static_cast<char*>(s.out) + w.at(s.out_ts, s.out_hs) * OUT;
+  };
   Pairs<IN> next_x;
   Pairs<G> next_g;
   auto fetch = [&] {
-    if (w.mine()) {
-      next_x.load(s.x, w.token * s.x_ts + w.head() * s.x_hs + 8 * w.chunk, half);
-      next_g.load(s.dy, w.token * s.dy_ts + w.head() * s.dy_hs + 8 * w.chunk, half);
+    if (w.mine(w.pass)) {
+      next_x.load(from, half);
+      next_g.load(from_dy, half);
     } else {
       next_x.zero();
       next_g.zero();
@@ -330,6 +391,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   };
   int pos[4] = {};
   if (w.more()) {
+    enter();
     fetch();
     if (a.axes) positions_of(a, w.token, pos);
   }
@@ -346,14 +408,21 @@ __global__ void __launch_bounds__(kThreads, 2)
     float2 x[8], d[8];
     next_x.get(x, a.f16_in);
     next_g.get(d, a.f16_dy);
-    const bool mine = w.mine();
-    const int64_t to = w.token * s.out_ts + w.head() * s.out_hs + 8 * w.chunk;
-    if (fresh && a.axes) turns(a, rates, w.chunk, pos, cos, sin);
-    fresh = w.advance();
-    if (w.more()) {
-      fetch();
-      if (fresh && a.axes) positions_of(a, w.token, pos);
+    const bool mine = w.mine(w.pass);
+    char* const to_now = to;
+    if (fresh && a.axes) turns(a, rates, w, pos, cos, sin);
+    fresh = w.advance(1);
+    if (fresh) {
+      if (w.more()) {
+        enter();
+        if (a.axes) positions_of(a, w.token, pos);
+      }
+    } else {
+      from += x_pass;
+      from_dy += dy_pass;
+      to += out_pass;
     }
+    if (w.more()) fetch();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {  // the gradient turned back
       const float2 p = d[i], q = d[4 + i];
@@ -367,13 +436,14 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int i = 1; i < 8; ++i) sq = fma2(x[i], x[i], sq);
       const float r = rsqrtf(head_sum(sq.x + sq.y, a.lanes) * inv_d + a.eps);
       const float2 r2 = make_float2(r, r);
-      const float2* g = reinterpret_cast<const float2*>(gain + (w.has ? 8 * w.chunk : 0));
+      float2 g[8];
+      gains_of(gain, w, half, g);
       float2 dot = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         x[i] = mul2(x[i], r2);
         if (mine) acc[i] = fma2(d[i], x[i], acc[i]);  // a lane without a head may have r = inf
-        d[i] = mul2(d[i], g[i < 4 ? i : half / 2 + i - 4]);
+        d[i] = mul2(d[i], g[i]);
         dot = fma2(d[i], x[i], dot);
       }
       // lanes of no head, and those past the head's end, hold zeros (or, of no head, are not kept)
@@ -382,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int i = 0; i < 8; ++i) d[i] = mul2(fma2(x[i], minus, d[i]), r2);
     }
-    if (mine) put_pairs<OUT>(s.out, to, half, d, a.f16_out);
+    if (mine) put_pairs<OUT>(to_now, half, d, a.f16_out);
   }
   if (!a.partial) return;
   // lanes of one chunk, then the CTA's warps, each in a fixed order
@@ -436,11 +506,9 @@ __global__ void __launch_bounds__(1024) gain_sum_kernel(const float* partial, in
   if (c < d && out) out[c] = accumulate ? out[c] + sum : sum;
 }
 
-// Splits the work: lanes of a head, and for q and k the warps that share a
-// token and the CTAs. Few tokens: their heads are spread over more warps, which
-// each take the token's sines again. CTAs are dealt out by passes, a token's
-// sines counting as one. Returns the number of CTAs.
-int64_t split_work(NormArgs* a, int ctas_per_sm) {
+// Splits the work: lanes of a head, and the CTAs of q and k, dealt out by passes,
+// a token's sines counting as one. Returns the number of CTAs.
+int64_t split_work(NormArgs* a) {
   int lanes = 1, log2 = 0;
   while (lanes * 16 < a->d) {
     lanes *= 2;
@@ -454,19 +522,13 @@ int64_t split_work(NormArgs* a, int ctas_per_sm) {
     a->side[i].passes = (a->side[i].heads + per_pass - 1) / per_pass;
     work[i] = a->side[i].heads ? a->side[i].passes + 1 : 0;
   }
-  const int64_t all = static_cast<int64_t>(num_sms()) * ctas_per_sm;
+  const int64_t all = static_cast<int64_t>(num_sms()) * kCtasPerSm;
   int64_t total = 0;
   for (int i = 0; i < 2; ++i) {
     Side& s = a->side[i];
-    s.blocks = s.slices = 0;
-    if (!s.heads) continue;
     const int64_t share = std::max<int64_t>(1, all * work[i] / (work[0] + work[1]));
-    const int64_t want = (share * kWarps + a->tokens - 1) / a->tokens;
-    s.slices = static_cast<int>(std::min<int64_t>(want, s.passes));
-    const int per_slice = (s.passes + s.slices - 1) / s.slices;
-    s.slices = (s.passes + per_slice - 1) / per_slice;
-    const int64_t units = static_cast<int64_t>(a->tokens) * s.slices;
-    s.blocks = static_cast<int>(std::min<int64_t>((units + kWarps - 1) / kWarps, share));
+    const int64_t steps = static_cast<int64_t>(a->tokens) * s.passes;
+    s.blocks = static_cast<int>(std::min<int64_t>((steps + kWarps - 1) / kWarps, share));
     total += s.blocks;
   }
   return total;
@@ -545,15 +607,12 @@ const char* common_problem(int tokens, int nh, int nkv, int d, const rdt_heads* 
   return nullptr;
 }
 
-// CTAs of an SM, by the bytes of an input's value: what their registers leave.
-constexpr int kCtasPerSm[2] = {3, 2}, kGradCtasPerSm = 2;
-
 template <int IN>
 cudaError_t launch_norm(NormArgs a, int out_dtype, const Rates& r, cudaStream_t s) {
-  const int64_t grid = split_work(&a, kCtasPerSm[IN == 4]);
+  const int64_t grid = split_work(&a);
   return out_dtype == RDT_F32
-             ? launch_overlapping(norm_rope_kernel<IN, 4>, grid, kThreads, 0, s, a, r)
-             : launch_overlapping(norm_rope_kernel<IN, 2>, grid, kThreads, 0, s, a, r);
+             ? launch_overlapping(norm_rope_kernel<IN, 4, 4 / IN>, grid, kThreads, 0, s, a, r)
+             : launch_overlapping(norm_rope_kernel<IN, 2, 4 / IN>, grid, kThreads, 0, s, a, r);
 }
 
 template <int G, int IN>
@@ -599,7 +658,7 @@ size_t rdt_qk_norm_rope_backward_workspace_bytes(int32_t tokens, int32_t n_heads
   a.side[0].heads = n_heads;
   a.side[1].heads = n_kv_heads;
   a.d = head_dim;
-  return static_cast<size_t>(split_work(&a, kGradCtasPerSm)) * head_dim * sizeof(float);
+  return static_cast<size_t>(split_work(&a)) * head_dim * sizeof(float);
 }
 
 rdt_status rdt_qk_norm_rope_backward(int32_t tokens, int32_t n_heads, int32_t n_kv_heads,
@@ -647,7 +706,7 @@ rdt_status rdt_qk_norm_rope_backward(int32_t tokens, int32_t n_heads, int32_t n_
     side.dy_hs = g->head_stride;
   }
   a.f16_dy = d_dtype == RDT_F16;
-  const int64_t grid = split_work(&a, kGradCtasPerSm);
+  const int64_t grid = split_work(&a);
   const bool sums = d_gain_q || d_gain_k;
   if (sums) {
     if (!ws) return refuse("null pointer");
