@@ -5,6 +5,7 @@
 
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "../../include/rdt.h"
@@ -49,11 +50,20 @@ cudaError_t launch_overlapping(void (*kernel)(P...), int64_t grid, int threads, 
   return launch_clusters(kernel, 1, grid, threads, smem, s, args...);
 }
 
-// Lets a kernel have `smem` bytes of dynamic shared memory on the current device.
-template <typename... P>
-cudaError_t allow_smem(void (*kernel)(P...), size_t smem) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(smem));
+// Lets a kernel have `smem` bytes of dynamic shared memory on the current device;
+// asked for once on each of the first 64 devices.
+template <auto kernel>
+cudaError_t allow_smem(size_t smem) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem));
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 inline rdt_status refuse(const char* msg) {

@@ -887,7 +887,7 @@ constexpr int kSharedBelow = 3;
 template <int D, bool CAP, int R>
 cudaError_t launch_dkdv(const Args& ar, const CUtensorMap& tq, const CUtensorMap& tdo,
                         const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
-  const cudaError_t e = allow_smem(spans_dkdv_kernel<D, CAP, R>, KvCfg<D>::SMEM);
+  const cudaError_t e = allow_smem<spans_dkdv_kernel<D, CAP, R>>(KvCfg<D>::SMEM);
   if (e != cudaSuccess) return e;
   return launch_clusters(spans_dkdv_kernel<D, CAP, R>, R,
                          static_cast<int64_t>((ar.a.keys + 127) / 128) * ar.a.nkv * R, kThreads,
@@ -903,7 +903,7 @@ cudaError_t launch(const Args& ar, cudaStream_t s) {
       !make_tma_heads(&tk, a.k.p, a.keys, a.nkv, a.d, a.k.ts, a.k.hs, 1, 128) ||
       !make_tma_heads(&tv, a.v.p, a.keys, a.nkv, a.d, a.v.ts, a.v.hs, 1, 128))
     return cudaErrorInvalidValue;
-  cudaError_t e = allow_smem(spans_dq_kernel<D, CAP>, QCfg<D>::SMEM);
+  cudaError_t e = allow_smem<spans_dq_kernel<D, CAP>>(QCfg<D>::SMEM);
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(a.nkv) * ar.tl.tiles * 128;
   const int64_t prep = ar.groups + std::min<int64_t>((rows + 63) / 64, int64_t{num_sms()} * 8);

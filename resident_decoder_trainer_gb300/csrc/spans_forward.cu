@@ -605,7 +605,7 @@ cudaError_t launch(const Args& ar, cudaStream_t s) {
       !make_tma_heads(&tk, a.k.p, a.keys, a.nkv, a.d, a.k.ts, a.k.hs, 1, 128) ||
       !make_tma_heads(&tv, a.v.p, a.keys, a.nkv, a.d, a.v.ts, a.v.hs, 1, 128))
     return cudaErrorInvalidValue;
-  const cudaError_t e = allow_smem(spans_forward_kernel<D, CAP>, Cfg<D>::SMEM);
+  const cudaError_t e = allow_smem<spans_forward_kernel<D, CAP>>(Cfg<D>::SMEM);
   if (e != cudaSuccess) return e;
   return launch_overlapping(spans_forward_kernel<D, CAP>,
                             static_cast<int64_t>(ar.pairs) * a.nkv * ar.splits, kThreads, Cfg<D>::SMEM, s, tq, tk, tv, ar);

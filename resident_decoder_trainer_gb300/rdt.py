@@ -84,7 +84,7 @@ def _load() -> ctypes.CDLL:
     lib = ctypes.CDLL(LIB_PATH)
     P, I32, I64, F32, SZ = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float,
                             ctypes.c_size_t)
-    CP, HP = ctypes.POINTER(Config), ctypes.POINTER(Heads)
+    CP = ctypes.POINTER(Config)
     sig = {
         "rdt_check_config": (I32, [CP]),
         "rdt_block_param_count": (I64, [CP]),
@@ -137,16 +137,16 @@ def _load() -> ctypes.CDLL:
         "rdt_tensors_sq_sum_workspace_bytes": (SZ, [P, I32]),
         "rdt_tensors_sq_sum": (I32, [P, I32, I32, P, P, SZ, P]),
         "rdt_tensors_adamw": (I32, [P, I32, I32, I32, I64, P, P, I32, P, F32, F32, F32, P]),
-        "rdt_qk_norm_rope": (I32, [I32, I32, I32, I32, HP, HP, I32, P, P, F32, P, I32, P, F32, HP,
-                                   HP, I32, P]),
+        "rdt_qk_norm_rope": (I32, [I32, I32, I32, I32, P, P, I32, P, P, F32, P, I32, P, F32, P,
+                                   P, I32, P]),
         "rdt_qk_norm_rope_backward_workspace_bytes": (SZ, [I32, I32, I32, I32]),
-        "rdt_qk_norm_rope_backward": (I32, [I32, I32, I32, I32, HP, HP, I32, P, P, F32, P, I32, P,
-                                            F32, HP, HP, I32, HP, HP, I32, P, P, I32, P, SZ, P]),
+        "rdt_qk_norm_rope_backward": (I32, [I32, I32, I32, I32, P, P, I32, P, P, F32, P, I32, P,
+                                            F32, P, P, I32, P, P, I32, P, P, I32, P, SZ, P]),
         "rdt_attention_workspace_bytes": (SZ, [I32, I32, I32, I32, I32, I32]),
-        "rdt_attention": (I32, [I32, I32, I32, I32, I32, HP, HP, HP, P, P, F32, F32, HP, P, P, SZ,
+        "rdt_attention": (I32, [I32, I32, I32, I32, I32, P, P, P, P, P, F32, F32, P, P, P, SZ,
                                 P]),
-        "rdt_attention_backward": (I32, [I32, I32, I32, I32, I32, HP, HP, HP, HP, P, HP, P, P, P,
-                                         F32, F32, HP, HP, HP, P, SZ, P]),
+        "rdt_attention_backward": (I32, [I32, I32, I32, I32, I32, P, P, P, P, P, P, P, P, P,
+                                         F32, F32, P, P, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -314,10 +314,14 @@ def gemm_nf4(a, codes, scales, w_rows, w_cols, b_mn, c, a2=None, b2=None, split_
 
 
 # ------------------------------------------------- token log probabilities
+# the current device's number without torch.cuda's own checks, where torch has it
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _device(t, what) -> int:
     """The current CUDA device, which t has to be on."""
     device = t.get_device()
-    if device < 0 or device != torch.cuda.current_device():
+    if device < 0 or device != _current_device():
         raise ValueError(f"{what} must be on the current CUDA device")
     return device
 
@@ -437,19 +441,29 @@ def head_logprobs(cfg, h, gamma_f, w_lm, ws, targets=None, logp=None, entropy=No
 
 
 # ------------------------------------- per-head norm with rotation, attention over spans
-def _heads(t, what, dtype, shape, device):
-    """rdt_heads of a [tokens, heads, head_dim] tensor, after the checks that the library may
-    be handed it; its own checks of strides and alignment follow there."""
-    if t.get_device() != device:
-        raise ValueError(f"{what} must be on the current CUDA device")
-    if t.dtype != dtype:
-        raise ValueError(f"{what} has type {t.dtype}, not {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    ts, hs, one = t.stride()
-    if one != 1 and shape[2] > 1:
-        raise ValueError(f"the values of a head of {what} must be contiguous")
-    return Heads(t.data_ptr(), ts, hs)
+def _heads(device, *tensors):
+    """The rdt_heads of [tokens, heads, head_dim] tensors, given as (tensor, its name, type,
+    shape), after the checks that the library may be handed them; its own checks of strides and
+    alignment follow there. A tensor may be None. Returns what keeps them alive, and the
+    address of each."""
+    fields = []
+    for t, what, dtype, shape in tensors:
+        if t is None:
+            fields += (0, 0, 0)
+            continue
+        if t.get_device() != device:
+            raise ValueError(f"{what} must be on the current CUDA device")
+        if t.dtype != dtype:
+            raise ValueError(f"{what} has type {t.dtype}, not {dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
+        ts, hs, one = t.stride()
+        if one != 1 and shape[2] > 1:
+            raise ValueError(f"the values of a head of {what} must be contiguous")
+        fields += (t.data_ptr(), ts, hs)
+    block = (ctypes.c_int64 * len(fields))(*fields)
+    at = ctypes.addressof(block)
+    return block, [at + 24 * i if t[0] is not None else None for i, t in enumerate(tensors)]
 
 
 def _qk_shapes(q, k):
@@ -484,6 +498,13 @@ def _gain(t, what, d, device):
     return None if t is None else _here(t, what, _F32, (d,), device)
 
 
+def _stream_on(device, stream):
+    """_stream for a device that is known to be the current one."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device)
+    return _stream(stream)
+
+
 def qk_norm_rope(q, k, q_out, k_out, gain_q=None, gain_k=None, eps=1e-6, positions=None,
                  sections=None, theta=1e6, stream=None):
     """RMSNorm of every head of q and k and the rotation at given positions, in one pass
@@ -493,17 +514,17 @@ def qk_norm_rope(q, k, q_out, k_out, gain_q=None, gain_k=None, eps=1e-6, positio
     be None. gain fp32 [head_dim], None: no norm. positions int32 [tokens] or [axes, tokens],
     None: no rotation; sections: pairs of each axis."""
     tokens, nh, nkv, d = _qk_shapes(q, k)
-    some, some_out = (q, q_out) if q is not None else (k, k_out)
+    some, out = (q, q_out) if q is not None else (k, k_out)
     dev = _device(some, "q" if q is not None else "k")
     pos, axes, sec = _rotation(positions, sections, tokens, dev)
-    ins = [None if t is None else _heads(t, n, some.dtype, (tokens, h, d), dev)
-           for t, n, h in ((q, "q", nh), (k, "k", nkv))]
-    outs = [None if src is None else _heads(t, n, some_out.dtype, (tokens, h, d), dev)
-            for src, t, n, h in ((q, q_out, "q_out", nh), (k, k_out, "k_out", nkv))]
+    qs, ks = (tokens, nh, d), (tokens, nkv, d)
+    block, at = _heads(dev, (q, "q", some.dtype, qs), (k, "k", some.dtype, ks),
+                       (None if q is None else q_out, "q_out", out.dtype, qs),
+                       (None if k is None else k_out, "k_out", out.dtype, ks))
     _check(lib().rdt_qk_norm_rope(
-        tokens, nh, nkv, d, *ins, _DTYPE.get(some.dtype, -1), _gain(gain_q, "gain_q", d, dev),
-        _gain(gain_k, "gain_k", d, dev), eps, pos, axes, sec, theta, *outs,
-        _DTYPE.get(some_out.dtype, -1), _stream(stream)))
+        tokens, nh, nkv, d, at[0], at[1], _DTYPE.get(some.dtype, -1),
+        _gain(gain_q, "gain_q", d, dev), _gain(gain_k, "gain_k", d, dev), eps, pos, axes, sec,
+        theta, at[2], at[3], _DTYPE.get(out.dtype, -1), _stream_on(dev, stream)))
 
 
 def qk_norm_rope_backward_workspace_bytes(tokens, n_heads, n_kv_heads, head_dim) -> int:
@@ -521,19 +542,19 @@ def qk_norm_rope_backward(q, k, d_q_out, d_k_out, dq, dk, ws=None, gain_q=None, 
     some, grad, out = (q, d_q_out, dq) if q is not None else (k, d_k_out, dk)
     dev = _device(some, "q" if q is not None else "k")
     pos, axes, sec = _rotation(positions, sections, tokens, dev)
-
-    def pair(tq, tk, nq, nk, dtype):
-        return [None if src is None else _heads(t, n, dtype, (tokens, h, d), dev)
-                for src, t, n, h in ((q, tq, nq, nh), (k, tk, nk, nkv))]
-
+    qs, ks = (tokens, nh, d), (tokens, nkv, d)
+    block, at = _heads(dev, (q, "q", some.dtype, qs), (k, "k", some.dtype, ks),
+                       (None if q is None else d_q_out, "d_q_out", grad.dtype, qs),
+                       (None if k is None else d_k_out, "d_k_out", grad.dtype, ks),
+                       (None if q is None else dq, "dq", out.dtype, qs),
+                       (None if k is None else dk, "dk", out.dtype, ks))
     _check(lib().rdt_qk_norm_rope_backward(
-        tokens, nh, nkv, d, *pair(q, k, "q", "k", some.dtype), _DTYPE.get(some.dtype, -1),
+        tokens, nh, nkv, d, at[0], at[1], _DTYPE.get(some.dtype, -1),
         _gain(gain_q, "gain_q", d, dev), _gain(gain_k, "gain_k", d, dev), eps, pos, axes, sec,
-        theta, *pair(d_q_out, d_k_out, "d_q_out", "d_k_out", grad.dtype),
-        _DTYPE.get(grad.dtype, -1), *pair(dq, dk, "dq", "dk", out.dtype),
-        _DTYPE.get(out.dtype, -1), _gain(d_gain_q, "d_gain_q", d, dev),
-        _gain(d_gain_k, "d_gain_k", d, dev), int(bool(accumulate)),
-        *((None, 0) if ws is None else _scratch(ws, "ws", dev)), _stream(stream)))
+        theta, at[2], at[3], _DTYPE.get(grad.dtype, -1), at[4], at[5], _DTYPE.get(out.dtype, -1),
+        _gain(d_gain_q, "d_gain_q", d, dev), _gain(d_gain_k, "d_gain_k", d, dev),
+        int(bool(accumulate)), *((None, 0) if ws is None else _scratch(ws, "ws", dev)),
+        _stream_on(dev, stream)))
 
 
 def attention_workspace_bytes(queries, keys, n_heads, n_kv_heads, head_dim, backward=False) -> int:
@@ -547,9 +568,11 @@ _BF16 = torch.bfloat16
 def _attention_shapes(q, k):
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q, k and v must be [tokens, heads, head_dim]")
-    if q.shape[0] >= 1 << 31 or k.shape[0] >= 1 << 31:
+    t, nh, d = q.shape
+    n, nkv, _ = k.shape
+    if t >= 1 << 31 or n >= 1 << 31:
         raise ValueError("more than 2^31 - 1 queries or keys")
-    return q.shape[0], k.shape[0], q.shape[1], k.shape[1], q.shape[2]
+    return t, n, nh, nkv, d
 
 
 def attention(q, k, v, o, ws=None, lse=None, lo=None, hi=None, scale=None, softcap=0.0,
@@ -561,14 +584,16 @@ def attention(q, k, v, o, ws=None, lse=None, lo=None, hi=None, scale=None, softc
     0: scores become softcap tanh(score / softcap). ws: attention_workspace_bytes of scratch."""
     t, n, nh, nkv, d = _attention_shapes(q, k)
     dev = _device(q, "q")
+    qs, ks = (t, nh, d), (n, nkv, d)
+    block, at = _heads(dev, (q, "q", _BF16, qs), (k, "k", _BF16, ks), (v, "v", _BF16, ks),
+                       (o, "o", _BF16, qs))
     _check(lib().rdt_attention(
-        t, n, nh, nkv, d, _heads(q, "q", _BF16, (t, nh, d), dev),
-        _heads(k, "k", _BF16, (n, nkv, d), dev), _heads(v, "v", _BF16, (n, nkv, d), dev),
+        t, n, nh, nkv, d, at[0], at[1], at[2],
         None if lo is None else _here(lo, "lo", _I32, (t,), dev),
         None if hi is None else _here(hi, "hi", _I32, (t,), dev),
-        d ** -0.5 if scale is None else scale, softcap, _heads(o, "o", _BF16, (t, nh, d), dev),
+        d ** -0.5 if scale is None else scale, softcap, at[3],
         None if lse is None else _here(lse, "lse", _F32, (t, nh), dev),
-        *((None, 0) if ws is None else _scratch(ws, "ws", dev)), _stream(stream)))
+        *((None, 0) if ws is None else _scratch(ws, "ws", dev)), _stream_on(dev, stream)))
 
 
 def attention_backward(q, k, v, o, lse, d_o, dq, dk, dv, ws=None, d_lse=None, lo=None, hi=None,
@@ -579,16 +604,16 @@ def attention_backward(q, k, v, o, lse, d_o, dq, dk, dv, ws=None, d_lse=None, lo
     t, n, nh, nkv, d = _attention_shapes(q, k)
     dev = _device(q, "q")
     qs, ks = (t, nh, d), (n, nkv, d)
+    block, at = _heads(dev, (q, "q", _BF16, qs), (k, "k", _BF16, ks), (v, "v", _BF16, ks),
+                       (o, "o", _BF16, qs), (d_o, "d_o", _BF16, qs), (dq, "dq", _BF16, qs),
+                       (dk, "dk", _BF16, ks), (dv, "dv", _BF16, ks))
     _check(lib().rdt_attention_backward(
-        t, n, nh, nkv, d, _heads(q, "q", _BF16, qs, dev), _heads(k, "k", _BF16, ks, dev),
-        _heads(v, "v", _BF16, ks, dev), _heads(o, "o", _BF16, qs, dev),
-        _here(lse, "lse", _F32, (t, nh), dev), _heads(d_o, "d_o", _BF16, qs, dev),
+        t, n, nh, nkv, d, at[0], at[1], at[2], at[3], _here(lse, "lse", _F32, (t, nh), dev), at[4],
         None if d_lse is None else _here(d_lse, "d_lse", _F32, (t, nh), dev),
         None if lo is None else _here(lo, "lo", _I32, (t,), dev),
         None if hi is None else _here(hi, "hi", _I32, (t,), dev),
-        d ** -0.5 if scale is None else scale, softcap, _heads(dq, "dq", _BF16, qs, dev),
-        _heads(dk, "dk", _BF16, ks, dev), _heads(dv, "dv", _BF16, ks, dev),
-        *((None, 0) if ws is None else _scratch(ws, "ws", dev)), _stream(stream)))
+        d ** -0.5 if scale is None else scale, softcap, at[5], at[6], at[7],
+        *((None, 0) if ws is None else _scratch(ws, "ws", dev)), _stream_on(dev, stream)))
 
 
 # ------------------------------------------------- many tensors: clip and AdamW
