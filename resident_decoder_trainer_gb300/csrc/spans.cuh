@@ -247,18 +247,19 @@ inline Cap cap_of(float scale, float cap) {
   return x;
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
-// Whether some lane of the warp has a score beyond the polynomial's range.
+// The greatest of a row's scores, and whether some lane of the warp has one
+// beyond the polynomial's range.
 template <int N>
-__device__ __forceinline__ bool beyond(const uint32_t (&sv)[N], float limit) {
-  float top[2] = {0.f, 0.f};
+__device__ __forceinline__ bool beyond(const uint32_t (&sv)[N], float limit, float& top) {
+  float hi[2] = {-INFINITY, -INFINITY}, lo[2] = {INFINITY, INFINITY};
 #pragma unroll
-  for (int c = 0; c < N; c += 4) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      top[e] = max3(top[e], fabsf(__uint_as_float(sv[c + 2 * e])),
-                    fabsf(__uint_as_float(sv[c + 2 * e + 1])));
+  for (int c = 0; c < N; c += 2) {
+    const int e = (c >> 1) & 1;
+    hi[e] = max3(hi[e], __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+    lo[e] = min3(lo[e], __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
   }
-  return __any_sync(0xffffffffu, fmaxf(top[0], top[1]) > limit);
+  top = fmaxf(hi[0], hi[1]);
+  return __any_sync(0xffffffffu, fmaxf(top, -fminf(lo[0], lo[1])) > limit);
 }
 template <int N>
 __device__ __forceinline__ void tanh_far(uint32_t (&sv)[N], float w) {
@@ -273,6 +274,13 @@ __device__ __forceinline__ float2 odd_factor(float2 s, const float (&t)[3]) {
   const float2 y = mul2(s, s);
   const float2 p = fma2(y, both(t[2]), both(t[1]));
   return fma2(p, y, both(t[0]));
+}
+
+// Bits c of a word with lo <= c < hi.
+__device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
+  const uint32_t below_hi = hi >= 32 ? ~0u : hi <= 0 ? 0u : (1u << hi) - 1u;
+  const uint32_t below_lo = lo >= 32 ? ~0u : lo <= 0 ? 0u : (1u << lo) - 1u;
+  return below_hi & ~below_lo;
 }
 
 // Splits of the keys of one (pair of tiles, key head), and the forward pass'

@@ -147,7 +147,8 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_cons
 // ------------------------------------------------------------ elementwise
 // Scores to the tanh of their cap.
 __device__ __forceinline__ void tanh_all(uint32_t (&sv)[32], const Cap& cap) {
-  if (beyond(sv, cap.limit)) {
+  float top;
+  if (beyond(sv, cap.limit, top)) {
     tanh_far(sv, cap.w);
     return;
   }
@@ -457,20 +458,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t sv[32], pk[16];
       uint32_t seen = 0xffffffffu;
       tmem_ld32(ts, sv);
-      if (!m.full) {
+      bool full = m.full;
+      if (!full) {
         seen = 0u;
+        auto sees = [&](int lo, int len) {
+          return static_cast<uint32_t>(key - lo) < static_cast<uint32_t>(len);
+        };
+        if (a.rep % 4 == 0) {  // four columns are rows of one query
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const int4 lo = lo4[c], len = len4[c];
-          seen |= static_cast<uint32_t>(static_cast<uint32_t>(key - lo.x) <
-                                        static_cast<uint32_t>(len.x)) << (4 * c);
-          seen |= static_cast<uint32_t>(static_cast<uint32_t>(key - lo.y) <
-                                        static_cast<uint32_t>(len.y)) << (4 * c + 1);
-          seen |= static_cast<uint32_t>(static_cast<uint32_t>(key - lo.z) <
-                                        static_cast<uint32_t>(len.z)) << (4 * c + 2);
-          seen |= static_cast<uint32_t>(static_cast<uint32_t>(key - lo.w) <
-                                        static_cast<uint32_t>(len.w)) << (4 * c + 3);
+          for (int c = 0; c < 8; ++c) seen |= sees(lo4[c].x, len4[c].x) ? 15u << (4 * c) : 0u;
+        } else {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const int4 lo = lo4[c], len = len4[c];
+            seen |= sees(lo.x, len.x) ? 1u << (4 * c) : 0u;
+            seen |= sees(lo.y, len.y) ? 2u << (4 * c) : 0u;
+            seen |= sees(lo.z, len.z) ? 4u << (4 * c) : 0u;
+            seen |= sees(lo.w, len.w) ? 8u << (4 * c) : 0u;
+          }
         }
+        full = __all_sync(0xffffffffu, seen == ~0u);
       }
       tmem_ld_wait();
       if constexpr (CAP) tanh_all(sv, ar.cap);
@@ -484,9 +491,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           float2 p = p_of<CAP>(
               make_float2(__uint_as_float(sv[c + e]), __uint_as_float(sv[c + e + 1])), ar,
               e ? make_float2(nl.z, nl.w) : make_float2(nl.x, nl.y), slope);
-          if (!m.full) {
-            if (!((seen >> (c + e)) & 1)) p.x = 0.f;
-            if (!((seen >> (c + e + 1)) & 1)) p.y = 0.f;
+          if (!full) {
+            if (!(seen & (1u << (c + e)))) p.x = 0.f;
+            if (!(seen & (2u << (c + e)))) p.y = 0.f;
           }
           pk[(c + e) / 2] = pack_bf16x2(p.x, p.y);
           if constexpr (CAP) p = mul2(p, slope);
@@ -515,9 +522,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                              e ? make_float2(nd.z, nd.w) : make_float2(nd.x, nd.y));
             ds = mul2(ds, make_float2(__uint_as_float(sv[16 * h + c + e]),
                                       __uint_as_float(sv[16 * h + c + e + 1])));
-            if (!m.full) {
-              if (!((seen >> (16 * h + c + e)) & 1)) ds.x = 0.f;
-              if (!((seen >> (16 * h + c + e + 1)) & 1)) ds.y = 0.f;
+            if (!full) {
+              if (!(seen & (1u << (16 * h + c + e)))) ds.x = 0.f;
+              if (!(seen & (2u << (16 * h + c + e)))) ds.y = 0.f;
             }
             pk[8 * h + (c + e) / 2] = pack_bf16x2(ds.x, ds.y);
           }
@@ -635,11 +642,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int chunks = (a.d + 63) / 64, used = ar.tl.per * a.rep;
-  const int64_t items = static_cast<int64_t>(ar.tl.tiles) * a.nkv;
+  const int items = ar.tl.tiles * a.nkv;
   // item -> row tile (the last first), key head; its first key and key tiles
-  auto place = [&](int64_t item, int& tile, int& g, int& first, int& n) {
-    tile = ar.tl.tiles - 1 - static_cast<int>(item / a.nkv);
-    g = static_cast<int>(item % a.nkv);
+  auto place = [&](int item, int& tile, int& g, int& first, int& n) {
+    tile = ar.tl.tiles - 1 - item / a.nkv;
+    g = item % a.nkv;
     const TileSpan s = ar.tiles[tile];
     first = s.first;
     n = (s.end - s.first + 127) / 128;
@@ -687,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       uint32_t jg = 0;
       int loaded = 0;
-      for (int64_t item = blockIdx.x; item < items && ok; item += gridDim.x) {
+      for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
         int tile, g, first, n;
         place(item, tile, g, first, n);
         if (n == 0) continue;
@@ -740,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       uint32_t jg = 0;
       int loaded = 0;
-      for (int64_t item = blockIdx.x; item < items && ok; item += gridDim.x) {
+      for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
         int tile, g, first, n;
         place(item, tile, g, first, n);
         if (n == 0) continue;
@@ -794,11 +801,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     uint32_t jg = 0;
     int loaded = 0;
-    for (int64_t item = blockIdx.x; item < items && ok; item += gridDim.x) {
+    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
       int tile, g, first, n;
       place(item, tile, g, first, n);
-      const int t = tile * ar.tl.per + row_t, h = g * a.rep + row_h;
-      const bool real = row_t < ar.tl.per && t < a.queries;
       const int64_t at = (static_cast<int64_t>(g) * ar.tl.tiles + tile) * 128 + row;
       const float nl = ar.neg_lse[at], nd = ar.neg_d[at];
       const int lo = ar.lo[tile * int64_t{128} + row], len = ar.len[tile * int64_t{128} + row];
@@ -819,6 +824,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // columns l <= c < l + len are seen; a row that sees nothing has p = 0 as it is
         const int l = lo - (first + j * 128 + block * 32);
         const bool full = __all_sync(0xffffffffu, len == 0 || (l <= 0 && l + len >= 32));
+        const uint32_t seen = full ? ~0u : bits_between(l, l + len);
 #pragma unroll
         for (int c = 0; c < 32; c += 2) {
           float2 slope;
@@ -828,8 +834,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           float2 ds = add2(make_float2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])), nd2);
           ds = mul2(ds, p);
           if (!full) {
-            if (static_cast<uint32_t>(c - l) >= static_cast<uint32_t>(len)) ds.x = 0.f;
-            if (static_cast<uint32_t>(c + 1 - l) >= static_cast<uint32_t>(len)) ds.y = 0.f;
+            if (!(seen & (1u << c))) ds.x = 0.f;
+            if (!(seen & (2u << c))) ds.y = 0.f;
           }
           pk[c / 2] = pack_bf16x2(ds.x, ds.y);
         }
@@ -861,6 +867,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 32; ++e) r[e] = 0u;
       }
       if (left > 0) {
+        const int again_of = not_hoisted(item);  // not held meanwhile: registers are short
+        const int t = (ar.tl.tiles - 1 - again_of / a.nkv) * ar.tl.per + row_t;
+        const int h = again_of % a.nkv * a.rep + row_h;
+        const bool real = row_t < ar.tl.per && t < a.queries;
         if (real) put_columns(a.dq.at(t, h) + c0, r, a.scale, left);
         for (unsigned again = __ballot_sync(0xffffffffu, real && !all_finite(r, left)); again;
              again &= again - 1) {

@@ -12,8 +12,9 @@
 // one thread a row. The MMA warp interleaves
 //   S_A(0) S_B(0) | PV_A(0) S_A(1) | PV_B(0) S_B(1) | PV_A(1) ...
 // so that one tile's products run while the other's softmax does. P (bf16) is
-// written over its S in TMEM and read from there; its first 64 keys are handed
-// over while the exponentials of the others are formed. O is rescaled only
+// written over its S in TMEM (next to it, for heads up to 64) and read from
+// there; its first 64 keys are handed over while the exponentials of the others
+// are formed. O is rescaled only
 // when a row's maximum grows by more than 2^8.
 //
 // A row whose O is not finite is computed again key by key (row_forward): a NaN
@@ -63,8 +64,12 @@ struct Cfg {
       OFF_NEXT = OFF_STAGE + 8 * 4096, OFF_ITEM = OFF_NEXT + 16,
                             OFF_BAR = OFF_ITEM + kItemRing * sizeof(Item);
   static constexpr size_t SMEM = OFF_BAR + 512 + 1024;
-  static constexpr uint32_t TMEM_S = 0, TMEM_O = 256, TMEM_COLS = 512;
-  static_assert(TMEM_O + 2 * D <= TMEM_COLS && SMEM <= 232448 && OFF_BAR % 8 == 0, "");
+  // Heads up to 64 leave columns for P apart from S: the next scores are formed
+  // as soon as these are in registers.
+  static constexpr bool APART = D == 64;
+  static constexpr uint32_t TMEM_S = 0, TMEM_O = 256, TMEM_P = APART ? 384 : 0,
+                            P_STEP = APART ? 64 : 128, TMEM_COLS = 512;
+  static_assert(TMEM_O + 2 * D <= (APART ? TMEM_P : TMEM_COLS) && SMEM <= 232448 && OFF_BAR % 8 == 0, "");
 };
 
 template <int D, bool CAP>
@@ -86,9 +91,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                  p_full = s_full + 16,  // [tile][half]
       o_done = p_full + 32, o_free = o_done + 16, item_full = o_free + 16,
                  item_empty = item_full + 8 * kItemRing, drain = item_empty + 8 * kItemRing,
-                 next = drain + 8;
+                 next = drain + 8, s_free = next + 8, pv_done = s_free + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 448);
-  static_assert(8 * (4 + 2 * KS + 2 * VS + 2 + 4 + 2 + 2 + 2 * kItemRing + 2) <= 448, "");
+  static_assert(8 * (4 + 2 * KS + 2 * VS + 2 + 4 + 2 + 2 + 2 * kItemRing + 2 + 4) <= 448, "");
   Item* ring = reinterpret_cast<Item*>(smem + C::OFF_ITEM);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -115,6 +120,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(p_full + 16 * x, 128);
       mbar_init(p_full + 16 * x + 8, 128);
       mbar_init(o_done + 8 * x, 1);
+      mbar_init(s_free + 8 * x, 128);
+      mbar_init(pv_done + 8 * x, 1);
       mbar_init(o_free + 8 * x, 128);
     }
     for (int x = 0; x < kItemRing; ++x) {
@@ -223,6 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       uint32_t jg = 0, loaded = 0, it = 0;
       uint32_t pv0 = 0, pv1 = 0, rounds0 = 0, rounds1 = 0;  // P V issued; items with any
+      uint32_t s0 = 0, s1 = 0;                               // S issued
       for (; ok; ++it) {
         const int slot = it % kItemRing;
         if (!wait_for(item_full + 8 * slot, (it / kItemRing) & 1, err)) break;
@@ -233,10 +241,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (index < 0) break;
         if (n == 0) continue;
         // S_x = Q_x K^T of key tile j, where row tile x has any of it
-        auto issue_s = [&](auto which, int j) {
+        auto issue_s = [&](auto which, int j) -> bool {
           constexpr int x = decltype(which)::value;
           const int end = x ? end1 : end0;
-          if (j < (x ? begin1 : begin0) || j >= end) return;
+          if (j < (x ? begin1 : begin0) || j >= end) return true;
+          if constexpr (C::APART) {  // else P V of the scores before, in order, comes after them
+            uint32_t& issued = x ? s1 : s0;
+            if (issued && !wait_for(s_free + 8 * x, (issued - 1) & 1, err)) return false;
+            ++issued;
+            tc_fence_after();
+          }
           const uint32_t kd = desc_low(sbase + C::OFF_K + ((jg + j) % KS) * C::TILE, 16);
           const uint32_t qd = desc_low(sbase + C::OFF_Q + x * C::TILE, 16);
 #pragma unroll
@@ -247,6 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_commit(s_full + 8 * x);
           if (j + 1 == end) tc_commit(q_empty + 8 * x);  // the item's last read of its Q
+          return true;
         };
         // O_x += P_x V
         auto issue_pv = [&](auto which, int j) -> bool {
@@ -263,10 +278,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
 #pragma unroll
             for (int k = 4 * half; k < 4 * half + 4; ++k)
-              tc_mma_ts_low(tmem + C::TMEM_O + x * D, tmem + C::TMEM_S + x * BN + k * 8,
+              tc_mma_ts_low(tmem + C::TMEM_O + x * D, tmem + C::TMEM_P + x * C::P_STEP + k * 8,
                             vd + k * 128, idesc_o, j > begin || k > 0);
           }
           ++pv;
+          if constexpr (C::APART) tc_commit(pv_done + 8 * x);
           if (j + 1 == end) {
             tc_commit(o_done + 8 * x);
             ++rounds;
@@ -283,26 +299,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait_k(0) && wait_for(q_full, loaded & 1, err);
         if (!ok) break;
         tc_fence_after();
-        issue_s(A, 0);
+        ok = issue_s(A, 0);
         if (end0 == 0) mbar_arrive(q_empty);
-        ok = wait_for(q_full + 8, loaded & 1, err);
+        ok = ok && wait_for(q_full + 8, loaded & 1, err);
         if (!ok) break;
         tc_fence_after();
-        issue_s(B, 0);
+        ok = issue_s(B, 0);
         if (end1 == 0) mbar_arrive(q_empty + 8);
         tc_commit(k_empty + 8 * (jg % KS));
-        for (int j = 0; j < n; ++j) {
-          ok = wait_for(v_full + 8 * ((jg + j) % VS), ((jg + j) / VS) & 1, err) &&
-               issue_pv(A, j) && (j + 1 >= n || wait_k(j + 1));
-          if (!ok) break;
-          tc_fence_after();
-          if (j + 1 < n) issue_s(A, j + 1);
-          ok = issue_pv(B, j);
-          if (!ok) break;
-          tc_commit(v_empty + 8 * ((jg + j) % VS));
-          if (j + 1 < n) {
-            issue_s(B, j + 1);
-            tc_commit(k_empty + 8 * ((jg + j + 1) % KS));
+        for (int j = 0; j < n && ok; ++j) {
+          if constexpr (C::APART) {
+            if (j + 1 < n) {
+              ok = wait_k(j + 1);
+              if (!ok) break;
+              tc_fence_after();
+              ok = issue_s(A, j + 1) && issue_s(B, j + 1);
+              if (!ok) break;
+              tc_commit(k_empty + 8 * ((jg + j + 1) % KS));
+            }
+            ok = wait_for(v_full + 8 * ((jg + j) % VS), ((jg + j) / VS) & 1, err) &&
+                 issue_pv(A, j) && issue_pv(B, j);
+            if (!ok) break;
+            tc_commit(v_empty + 8 * ((jg + j) % VS));
+          } else {
+            ok = wait_for(v_full + 8 * ((jg + j) % VS), ((jg + j) / VS) & 1, err) &&
+                 issue_pv(A, j) && (j + 1 >= n || wait_k(j + 1));
+            if (!ok) break;
+            tc_fence_after();
+            if (j + 1 < n) issue_s(A, j + 1);
+            ok = issue_pv(B, j);
+            if (!ok) break;
+            tc_commit(v_empty + 8 * ((jg + j) % VS));
+            if (j + 1 < n) {
+              issue_s(B, j + 1);
+              tc_commit(k_empty + 8 * ((jg + j + 1) % KS));
+            }
           }
         }
         jg += n;
@@ -318,6 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lane_base + C::TMEM_S + x * BN;
+    const uint32_t tp = tmem + lane_base + C::TMEM_P + x * C::P_STEP;
     const uint32_t t_o = tmem + lane_base + C::TMEM_O + x * D;
     const int row_t = row / a.rep, row_h = row % a.rep;
     const float2 sc2 = make_float2(ar.scale_log2, ar.scale_log2);
@@ -331,12 +363,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(item_empty + 8 * slot);
       if (item < 0) break;
-      int t0, g, split;
-      place(item, t0, g, split);
-      const int t = t0 + x * ar.tl.per + row_t, h = g * a.rep + row_h;
-      const bool real = row_t < ar.tl.per && t < a.queries;
+      // this thread's query and head; whether they exist
+      auto whose = [&](int of, int& t, int& h, int& split) {
+        int t0, g;
+        place(of, t0, g, split);
+        t = t0 + x * ar.tl.per + row_t;
+        h = g * a.rep + row_h;
+        return row_t < ar.tl.per && t < a.queries;
+      };
       int lo = 0, hi = INT32_MAX;  // a row that is none needs no mask
-      if (real) a.span(t, lo, hi);
+      {
+        int t, h, split;
+        if (whose(item, t, h, split)) a.span(t, lo, hi);
+      }
       float m_run = -INFINITY, l_run = 0.f;
       for (int j = begin; j < end; ++j, ++jx) {
         if (!warp_wait(s_full + 8 * x, jx & 1, err)) {
@@ -349,29 +388,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 4; ++c)
           tmem_ld32(ts + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * c]));
         tmem_ld_wait();
+        if constexpr (C::APART) {
+          tc_fence_before();
+          mbar_arrive(s_free + 8 * x);
+        }
         // columns l <= c < r are seen by this row
         const int base = first + j * BN;
         const int l = lo - base, r = hi - base;
         const bool masked = __any_sync(0xffffffffu, l > 0 || r < BN);
-        const bool poly = CAP && !beyond(sv, ar.cap.limit);
+        float mx = 0.f;
+        const bool poly = CAP && !beyond(sv, ar.cap.limit, mx);
         if (CAP && !poly) tanh_far(sv, ar.cap.w);
         if (masked && !poly) {
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c < l || c >= r) sv[c] = __float_as_uint(-INFINITY);
-        }
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        if (masked && poly) {  // -inf has no polynomial: p is cleared below
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t seen = bits_between(l - 32 * q, r - 32 * q);
+            if (__all_sync(0xffffffffu, seen == ~0u)) continue;
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c >= l && c < r) m4[c & 3] = fmaxf(m4[c & 3], __uint_as_float(sv[c]));
-        } else {
-#pragma unroll
-          for (int c = 0; c < 128; c += 2)
-            m4[(c >> 1) & 3] =
-                max3(m4[(c >> 1) & 3], __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+            for (int c = 0; c < 32; ++c)
+              if (!(seen & (1u << c))) sv[32 * q + c] = __float_as_uint(-INFINITY);
+          }
         }
-        float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
+        if (!poly || masked) {
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          if (poly) {  // -inf has no polynomial: p is cleared below
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t seen = bits_between(l - 32 * q, r - 32 * q);
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                m4[c & 3] = fmaxf(m4[c & 3], seen & (1u << c) ? __uint_as_float(sv[32 * q + c])
+                                                              : -INFINITY);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 128; c += 2)
+              m4[(c >> 1) & 3] =
+                  max3(m4[(c >> 1) & 3], __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+          }
+          mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
+        }
         if (!poly)
           mx *= ar.scale_log2;
         else if (mx != -INFINITY)
@@ -381,8 +437,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           alpha = m_run == -INFINITY ? 1.f : ex2_approx(m_run - mx);  // nothing summed: as it is
           m_run = mx;
         }
+        if constexpr (C::APART) {  // P of the tile before has been read, and added to O
+          if (jx > 0 && !warp_wait(pv_done + 8 * x, (jx - 1) & 1, err)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+        }
         if (__any_sync(0xffffffffu, alpha != 1.f)) {
-          // the products so far have completed: the scores were issued after them
+          // the products so far have completed: else the scores were issued after them
 #pragma unroll 1
           for (int c = 0; c < a.d; c += 16) {
             uint32_t ov[16];
@@ -399,8 +462,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto exps = [&](auto by_poly, auto clear) {
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
+            uint32_t seen = 0;
 #pragma unroll
             for (int c = 64 * half; c < 64 * half + 64; c += 2) {
+              if (decltype(clear)::value && (c & 31) == 0) seen = bits_between(l - c, r - c);
               float2 p = make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
               if constexpr (decltype(by_poly)::value)
                 p = fma2(p, odd_factor(p, ar.cap.z), nm2);
@@ -409,14 +474,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               p.x = ex2_approx(p.x);
               p.y = ex2_approx(p.y);
               if constexpr (decltype(clear)::value) {
-                if (c < l || c >= r) p.x = 0.f;
-                if (c + 1 < l || c + 1 >= r) p.y = 0.f;
+                if (!(seen & (1u << (c & 31)))) p.x = 0.f;
+                if (!(seen & (2u << (c & 31)))) p.y = 0.f;
               }
               sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], p);
               sv[c / 2] = pack_bf16x2(p.x, p.y);
             }
-            // 64 keys as 32 bf16 pairs over the first columns of S
-            tmem_st32(ts + 32 * half, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * half]));
+            // 64 keys as 32 bf16 pairs
+            tmem_st32(tp + 32 * half, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * half]));
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(p_full + 16 * x + 8 * half);
@@ -441,6 +506,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         ++rounds;
       }
+      int t, h, split;  // found again: registers are short between
+      const bool real = whose(not_hoisted(item), t, h, split);
       const int64_t th = static_cast<int64_t>(t) * a.nh + h;
       const float inv = l_run != 0.f ? 1.f / l_run : 0.f;
       const bool some = l_run != 0.f;  // else p was 0 throughout: 0 times what was not seen
