@@ -101,46 +101,50 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_cons
     }
     return;
   }
-  // a row is `lanes` lanes of eight columns
-  int lanes = 2;
-  while (lanes * 8 < a.d) lanes *= 2;
-  const int per_warp = 32 / lanes, c = 8 * (lane & (lanes - 1));
-  const int64_t rows = static_cast<int64_t>(a.nkv) * ar.tl.tiles * 128;
-  const int64_t step = static_cast<int64_t>(gridDim.x - ar.groups) * (kPrepThreads / 32) * per_warp;
-  for (int64_t base = (static_cast<int64_t>(blockIdx.x - ar.groups) * (kPrepThreads / 32) + warp) *
-                      per_warp;
-       base < rows; base += step) {
-    const int64_t at = base + lane / lanes;  // rows is a multiple of per_warp
-    const int row = static_cast<int>(at & 127);
-    const int tile = static_cast<int>((at >> 7) % ar.tl.tiles);
-    const int g = static_cast<int>((at >> 7) / ar.tl.tiles);
-    const int in = row / a.rep, t = tile * ar.tl.per + in, h = g * a.rep + row % a.rep;
-    const bool real = in < ar.tl.per && t < a.queries;
-    float own = 0.f;
-    if (real && c < a.d) {
-      Eight<bf16> x, y;
-      float u[8], v[8];
-      x.load(a.d_o.at(t, h) + c);
-      y.load(a.o.at(t, h) + c);
-      x.get(u);
-      y.get(v);
+  // a row is `lanes` lanes of eight columns; a CTA takes a key head's row tile at
+  // a time, its warps 16 rows each
+  int log2 = 1;
+  while ((8 << log2) < a.d) ++log2;
+  const int lanes = 1 << log2, per_warp = 32 >> log2, c = 8 * (lane & (lanes - 1));
+  const uint32_t inv_rep = (65536u + a.rep - 1) / a.rep;  // row / rep of rows below 128
+  const int units = a.nkv * ar.tl.tiles, ctas = gridDim.x - ar.groups;
+  for (int unit = blockIdx.x - ar.groups; unit < units; unit += ctas) {
+    const int g = unit / ar.tl.tiles, tile = unit - g * ar.tl.tiles;
+#pragma unroll 4
+    for (int base = 16 * warp; base < 16 * warp + 16; base += per_warp) {
+      const int row = base + (lane >> log2);
+      const int in = static_cast<int>(row * inv_rep >> 16), t = tile * ar.tl.per + in;
+      const int h = g * a.rep + row - in * a.rep;
+      const bool real = in < ar.tl.per && t < a.queries;
+      float own = 0.f;
+      if (real && c < a.d) {
+        Eight<bf16> x, y;
+        float u[8], v[8];
+        x.load(a.d_o.at(t, h) + c);
+        y.load(a.o.at(t, h) + c);
+        x.get(u);
+        y.get(v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) own = fmaf(u[i], v[i], own);
-    }
-    for (int o = lanes >> 1; o > 0; o >>= 1) own += __shfl_xor_sync(0xffffffffu, own, o);
-    if (lane & (lanes - 1)) continue;
-    float neg_lse = kNoRow, neg_d = 0.f;
-    if (real) {
-      const int64_t th = static_cast<int64_t>(t) * a.nh + h;
-      int x, y;
-      a.span(t, x, y);
-      if (x < y) {
-        neg_lse = -a.lse[th] * kLog2e;
-        neg_d = (a.d_lse ? a.d_lse[th] : 0.f) - own;
+        for (int i = 0; i < 8; ++i) own = fmaf(u[i], v[i], own);
       }
+      for (int o = lanes >> 1; o > 0; o >>= 1) own += __shfl_xor_sync(0xffffffffu, own, o);
+      if ((lane & (lanes - 1)) == 0) {
+        float neg_lse = kNoRow, neg_d = 0.f;
+        if (real) {
+          const int64_t th = static_cast<int64_t>(t) * a.nh + h;
+          int x, y;
+          a.span(t, x, y);
+          if (x < y) {
+            neg_lse = -a.lse[th] * kLog2e;
+            neg_d = (a.d_lse ? a.d_lse[th] : 0.f) - own;
+          }
+        }
+        const int64_t at = (static_cast<int64_t>(g) * ar.tl.tiles + tile) * 128 + row;
+        ar.neg_lse[at] = neg_lse;
+        ar.neg_d[at] = neg_d;
+      }
+      __syncwarp();
     }
-    ar.neg_lse[at] = neg_lse;
-    ar.neg_d[at] = neg_d;
   }
 }
 
@@ -170,6 +174,13 @@ __device__ __forceinline__ float2 p_of(float2 s, const Args& ar, float2 neg_lse,
   p.x = ex2_approx(p.x);
   p.y = ex2_approx(p.y);
   return p;
+}
+
+// 32 bf16 values of which those with a bit in `seen` stay, whatever the others hold.
+__device__ __forceinline__ void clear_unseen(uint32_t (&pk)[16], uint32_t seen) {
+#pragma unroll
+  for (int c = 0; c < 32; c += 2)
+    pk[c / 2] &= (seen & (1u << c) ? 0xffffu : 0u) | (seen & (2u << c) ? 0xffff0000u : 0u);
 }
 
 // Rows of 32 columns, bf16, of which those below `d` exist.
@@ -491,16 +502,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           float2 p = p_of<CAP>(
               make_float2(__uint_as_float(sv[c + e]), __uint_as_float(sv[c + e + 1])), ar,
               e ? make_float2(nl.z, nl.w) : make_float2(nl.x, nl.y), slope);
-          if (!full) {
-            if (!(seen & (1u << (c + e)))) p.x = 0.f;
-            if (!(seen & (2u << (c + e)))) p.y = 0.f;
-          }
           pk[(c + e) / 2] = pack_bf16x2(p.x, p.y);
           if constexpr (CAP) p = mul2(p, slope);
           sv[c + e] = __float_as_uint(p.x);
           sv[c + e + 1] = __float_as_uint(p.y);
         }
       }
+      if (!full) clear_unseen(pk, seen);
       tmem_st16(ts, pk);
       tmem_st_wait();
       tc_fence_before();
@@ -522,14 +530,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                              e ? make_float2(nd.z, nd.w) : make_float2(nd.x, nd.y));
             ds = mul2(ds, make_float2(__uint_as_float(sv[16 * h + c + e]),
                                       __uint_as_float(sv[16 * h + c + e + 1])));
-            if (!full) {
-              if (!(seen & (1u << (16 * h + c + e)))) ds.x = 0.f;
-              if (!(seen & (2u << (16 * h + c + e)))) ds.y = 0.f;
-            }
             pk[8 * h + (c + e) / 2] = pack_bf16x2(ds.x, ds.y);
           }
         }
       }
+      if (!full) clear_unseen(pk, seen);
       tmem_st16(tdp, pk);
       tmem_st_wait();
       tc_fence_before();
@@ -833,12 +838,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (CAP) p = mul2(p, slope);
           float2 ds = add2(make_float2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])), nd2);
           ds = mul2(ds, p);
-          if (!full) {
-            if (!(seen & (1u << c))) ds.x = 0.f;
-            if (!(seen & (2u << c))) ds.y = 0.f;
-          }
           pk[c / 2] = pack_bf16x2(ds.x, ds.y);
         }
+        if (!full) clear_unseen(pk, seen);
         // this buffer was last read by dQ += dS K two key tiles ago
         ok = warp_wait(ds_free + 8 * buf, ((jj >> 1) & 1) ^ 1, err);
         if (!ok) break;
@@ -915,8 +917,8 @@ cudaError_t launch(const Args& ar, cudaStream_t s) {
     return cudaErrorInvalidValue;
   cudaError_t e = allow_smem<spans_dq_kernel<D, CAP>>(QCfg<D>::SMEM);
   if (e != cudaSuccess) return e;
-  const int64_t rows = static_cast<int64_t>(a.nkv) * ar.tl.tiles * 128;
-  const int64_t prep = ar.groups + std::min<int64_t>((rows + 63) / 64, int64_t{num_sms()} * 8);
+  const int64_t units = static_cast<int64_t>(a.nkv) * ar.tl.tiles;
+  const int64_t prep = ar.groups + std::min<int64_t>(units, int64_t{num_sms()} * 8);
   e = launch_overlapping(prepare_kernel, prep, kPrepThreads, 0, s, ar);
   if (e != cudaSuccess) return e;
   // Few key tiles: two CTAs share the rows of each.
