@@ -59,6 +59,10 @@ const char* shape_problem(int queries, int keys, int nh, int nkv, int d) {
     return "n_heads must be a positive multiple of n_kv_heads, at most 4096";
   if (nh / nkv > 128) return "at most 128 query heads may share a key head";
   if (d < 16 || d > kMaxDim || d % 16) return "head_dim must be a multiple of 16 in [16, 128]";
+  // tiles are counted in 32 bits
+  if (int64_t{Tiling::of(queries, nh / nkv).tiles} * nkv > 1 << 29 ||
+      (int64_t{keys} + 127) / 128 * nkv > 1 << 29)
+    return "queries or keys times heads are too many";
   return nullptr;
 }
 

@@ -47,6 +47,7 @@ struct Args {
   TileSpan* tiles;
   int2* group;  // first, end
   int* err;
+  bool wide_dq, wide_dk, wide_dv;  // rows at multiples of 32 bytes
 };
 
 // ---------------------------------------------------------------- prepare
@@ -183,16 +184,24 @@ __device__ __forceinline__ void clear_unseen(uint32_t (&pk)[16], uint32_t seen) 
     pk[c / 2] &= (seen & (1u << c) ? 0xffffu : 0u) | (seen & (2u << c) ? 0xffff0000u : 0u);
 }
 
-// Rows of 32 columns, bf16, of which those below `d` exist.
-__device__ __forceinline__ void put_columns(bf16* dst, const uint32_t (&r)[32], float w, int left) {
+// 32 columns of a row, bf16, of which `left` (a multiple of 16) exist; in pieces
+// of 32 bytes where the tensor's rows allow it.
+__device__ __forceinline__ void put_columns(bf16* dst, const uint32_t (&r)[32], float w, int left,
+                                            bool wide) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if (8 * e >= left) break;
-    reinterpret_cast<uint4*>(dst)[e] = make_uint4(
-        pack_bf16x2(__uint_as_float(r[8 * e]) * w, __uint_as_float(r[8 * e + 1]) * w),
-        pack_bf16x2(__uint_as_float(r[8 * e + 2]) * w, __uint_as_float(r[8 * e + 3]) * w),
-        pack_bf16x2(__uint_as_float(r[8 * e + 4]) * w, __uint_as_float(r[8 * e + 5]) * w),
-        pack_bf16x2(__uint_as_float(r[8 * e + 6]) * w, __uint_as_float(r[8 * e + 7]) * w));
+  for (int e = 0; e < 2; ++e) {
+    if (16 * e >= left) break;
+    uint32_t v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i] = pack_bf16x2(__uint_as_float(r[16 * e + 2 * i]) * w,
+                         __uint_as_float(r[16 * e + 2 * i + 1]) * w);
+    if (wide) {
+      store32(dst + 16 * e, v);
+    } else {
+      reinterpret_cast<uint4*>(dst)[2 * e] = make_uint4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<uint4*>(dst)[2 * e + 1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
   }
 }
 __device__ __forceinline__ bool all_finite(const uint32_t (&r)[32], int left) {
@@ -587,7 +596,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fine = fine && all_finite(r, left);
         if (key < a.keys && ok)
-          put_columns((which ? a.dv : a.dk).at(key, g) + c0, r, which ? 1.f : a.scale, left);
+          put_columns((which ? a.dv : a.dk).at(key, g) + c0, r, which ? 1.f : a.scale, left,
+                      which ? ar.wide_dv : ar.wide_dk);
       }
       for (unsigned again = __ballot_sync(0xffffffffu, !fine && key < a.keys && ok); again;
            again &= again - 1)
@@ -611,14 +621,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------------- dQ
+constexpr int kItemRing = 4;
+struct Item {
+  int index;     // row tile and key head; -1: no more
+  int first, n;  // first key, key tiles
+  int unused;
+};
+
 template <int D>
 struct QCfg {
   static constexpr uint32_t CHUNK = 128 * 128, TILE = 128 * D * 2;
   // K is read by S, and a whole elementwise pass later by dQ; V by dP only
   static constexpr int KST = D == 128 ? 3 : 4, VST = D == 128 ? 2 : 4;
   static constexpr uint32_t OFF_Q = 0, OFF_DO = TILE, OFF_K = 2 * TILE, OFF_V = OFF_K + KST * TILE,
-                            OFF_BAR = OFF_V + VST * TILE;
-  static constexpr size_t SMEM = OFF_BAR + 256 + 1024;
+                            OFF_ROW = OFF_V + VST * TILE,  // [neg_lse, neg_d, lo, len][128]
+      OFF_ITEM = OFF_ROW + 2048, OFF_BAR = OFF_ITEM + kItemRing * sizeof(Item);
+  static constexpr size_t SMEM = OFF_BAR + 320;  // at a multiple of 1024, which is checked
   static constexpr uint32_t T_S = 0, T_DP = 128, T_DQ = 256, T_DS = 384, TMEM_COLS = 512;
   static_assert(SMEM <= 232448, "");
 };
@@ -633,33 +651,39 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int KST = C::KST, VST = C::VST;
   const SpanArgs& a = ar.a;
   int* err = ar.err;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem_tiles[];
+  uint8_t* smem = smem_tiles;
   const uint32_t sbase = smem_u32(smem);
+  if (sbase & 1023u) {  // the swizzled tiles' layout counts on it
+    record_error(err, kErrTimeout);
+    return;
+  }
   const uint32_t bar0 = sbase + C::OFF_BAR;
   const uint32_t q_full = bar0, q_empty = bar0 + 8, k_full = bar0 + 16, k_empty = k_full + 8 * KST,
                  v_full = k_empty + 8 * KST, v_empty = v_full + 8 * VST, s_full = v_empty + 8 * VST,
                  s_free = s_full + 8, ds_ready = s_free + 8, ds_free = ds_ready + 16, dq_done = ds_free + 16,
-                 dq_free = dq_done + 8, drain = dq_free + 8;
-  static_assert(8 * (2 + 2 * KST + 2 * VST + 9) <= 248, "");
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 248);
+                 dq_free = dq_done + 8, drain = dq_free + 8, item_full = drain + 8,
+                 item_empty = item_full + 8 * kItemRing;
+  static_assert(8 * (2 + 2 * KST + 2 * VST + 9 + 2 * kItemRing) <= 312, "");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 312);
+  Item* ring = reinterpret_cast<Item*>(smem + C::OFF_ITEM);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int chunks = (a.d + 63) / 64, used = ar.tl.per * a.rep;
   const int items = ar.tl.tiles * a.nkv;
-  // item -> row tile (the last first), key head; its first key and key tiles
-  auto place = [&](int item, int& tile, int& g, int& first, int& n) {
+  // item -> row tile (the last first), key head
+  auto place = [&](int item, int& tile, int& g) {
     tile = ar.tl.tiles - 1 - item / a.nkv;
     g = item % a.nkv;
-    const TileSpan s = ar.tiles[tile];
-    first = s.first;
-    n = (s.end - s.first + 127) / 128;
   };
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
+    mbar_init(q_empty, 1 + kEltThreads / 32);  // the MMAs; the warps that read the rows' values
+    for (int x = 0; x < kItemRing; ++x) {
+      mbar_init(item_full + 8 * x, 1);
+      mbar_init(item_empty + 8 * x, 1 + kEltThreads / 32);
+    }
     for (int x = 0; x < KST; ++x) {
       mbar_init(k_full + 8 * x, 1);
       mbar_init(k_empty + 8 * x, 1);
@@ -699,33 +723,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       uint32_t jg = 0;
       int loaded = 0;
-      for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-        int tile, g, first, n;
-        place(item, tile, g, first, n);
-        if (n == 0) continue;
-        ok = wait_for(q_empty, (loaded & 1) ^ 1, err);
+      auto span_at = [&](int item) {
+        int tile, g;
+        place(item, tile, g);
+        return make_int2(ar.tiles[tile].first, ar.tiles[tile].end);
+      };
+      int2 span = span_at(blockIdx.x);
+      int item = blockIdx.x;
+      for (int it = 0; ok; ++it, item += gridDim.x) {
+        const int slot = it % kItemRing;
+        ok = wait_for(item_empty + 8 * slot, ((it / kItemRing) & 1) ^ 1, err);
         if (!ok) break;
-        mbar_arrive_expect_tx(q_full, 2 * chunks * used * 128);
+        const bool more = item < items;
+        const int first = span.x, n = (span.y - span.x + 127) / 128;
+        ring[slot] = Item{more ? item : -1, first, n, 0};
+        mbar_arrive(item_full + 8 * slot);
+        if (!more) break;
+        if (item + static_cast<int>(gridDim.x) < items) span = span_at(item + gridDim.x);
+        if (n == 0) continue;
+        int tile, g;
+        place(item, tile, g);
+        auto load = [&](int j, uint32_t full, uint32_t empty, int stages, uint32_t off,
+                        const CUtensorMap* map) -> bool {
+          const uint32_t jj = jg + j, st = jj % stages;
+          if (!wait_for(empty + 8 * st, ((jj / stages) & 1) ^ 1, err)) return false;
+          mbar_arrive_expect_tx(full + 8 * st, chunks * C::CHUNK);
+          for (int c = 0; c < chunks; ++c)
+            tma_load_3d(sbase + off + st * C::TILE + c * C::CHUNK, map, full + 8 * st, c * 64, g,
+                        first + j * 128);
+          return true;
+        };
+        // K's first tile does not wait for the item before to be done with its Q
+        ok = load(0, k_full, k_empty, KST, C::OFF_K, &tk) &&
+             wait_for(q_empty, (loaded & 1) ^ 1, err);
+        if (!ok) break;
+        const int64_t at = (static_cast<int64_t>(g) * ar.tl.tiles + tile) * 128;
+        mbar_arrive_expect_tx(q_full, 2 * chunks * used * 128 + 2048);
         for (int c = 0; c < chunks; ++c) {
           tma_load_3d(sbase + C::OFF_Q + c * C::CHUNK, &tq, q_full, c * 64, g * a.rep,
                       tile * ar.tl.per);
           tma_load_3d(sbase + C::OFF_DO + c * C::CHUNK, &tdo, q_full, c * 64, g * a.rep,
                       tile * ar.tl.per);
         }
+        bulk_load_1d(sbase + C::OFF_ROW, ar.neg_lse + at, 512, q_full);
+        bulk_load_1d(sbase + C::OFF_ROW + 512, ar.neg_d + at, 512, q_full);
+        bulk_load_1d(sbase + C::OFF_ROW + 1024, ar.lo + tile * int64_t{128}, 512, q_full);
+        bulk_load_1d(sbase + C::OFF_ROW + 1536, ar.len + tile * int64_t{128}, 512, q_full);
         for (int j = 0; j < n && ok; ++j) {
-          const int ks = (jg + j) % KST, vs = (jg + j) % VST;
-          ok = wait_for(k_empty + 8 * ks, (((jg + j) / KST) & 1) ^ 1, err);
-          if (!ok) break;
-          mbar_arrive_expect_tx(k_full + 8 * ks, chunks * C::CHUNK);
-          for (int c = 0; c < chunks; ++c)
-            tma_load_3d(sbase + C::OFF_K + ks * C::TILE + c * C::CHUNK, &tk, k_full + 8 * ks,
-                        c * 64, g, first + j * 128);
-          ok = wait_for(v_empty + 8 * vs, (((jg + j) / VST) & 1) ^ 1, err);
-          if (!ok) break;
-          mbar_arrive_expect_tx(v_full + 8 * vs, chunks * C::CHUNK);
-          for (int c = 0; c < chunks; ++c)
-            tma_load_3d(sbase + C::OFF_V + vs * C::TILE + c * C::CHUNK, &tv, v_full + 8 * vs,
-                        c * 64, g, first + j * 128);
+          ok = (j == 0 || load(j, k_full, k_empty, KST, C::OFF_K, &tk)) &&
+               load(j, v_full, v_empty, VST, C::OFF_V, &tv);
         }
         jg += n;
         ++loaded;
@@ -752,9 +798,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       uint32_t jg = 0;
       int loaded = 0;
-      for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-        int tile, g, first, n;
-        place(item, tile, g, first, n);
+      for (int it = 0; ok; ++it) {
+        const int slot = it % kItemRing;
+        if (!wait_for(item_full + 8 * slot, (it / kItemRing) & 1, err)) break;
+        const int index = ring[slot].index, n = ring[slot].n;
+        mbar_arrive(item_empty + 8 * slot);
+        if (index < 0) break;
         if (n == 0) continue;
         // S and dP of key tile j, once those of the one before are in registers
         auto issue = [&](int j) -> bool {
@@ -806,12 +855,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     uint32_t jg = 0;
     int loaded = 0;
-    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      int tile, g, first, n;
-      place(item, tile, g, first, n);
-      const int64_t at = (static_cast<int64_t>(g) * ar.tl.tiles + tile) * 128 + row;
-      const float nl = ar.neg_lse[at], nd = ar.neg_d[at];
-      const int lo = ar.lo[tile * int64_t{128} + row], len = ar.len[tile * int64_t{128} + row];
+    for (int it = 0; ok; ++it) {
+      const int slot = it % kItemRing;
+      if (!warp_wait(item_full + 8 * slot, (it / kItemRing) & 1, err)) break;
+      const int item = ring[slot].index, first = ring[slot].first, n = ring[slot].n;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(item_empty + 8 * slot);
+      if (item < 0) break;
+      float nl = 0.f, nd = 0.f;
+      int lo = 0, len = 0;
+      if (n > 0) {
+        if (!warp_wait(q_full, loaded & 1, err)) break;
+        const float* rows = reinterpret_cast<const float*>(smem + C::OFF_ROW);
+        nl = rows[row];
+        nd = rows[128 + row];
+        lo = __float_as_int(rows[256 + row]);
+        len = __float_as_int(rows[384 + row]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_empty);
+      }
       const float2 nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
       for (int j = 0; j < n; ++j) {
         const uint32_t jj = jg + j;
@@ -873,7 +935,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t = (ar.tl.tiles - 1 - again_of / a.nkv) * ar.tl.per + row_t;
         const int h = again_of % a.nkv * a.rep + row_h;
         const bool real = row_t < ar.tl.per && t < a.queries;
-        if (real) put_columns(a.dq.at(t, h) + c0, r, a.scale, left);
+        if (real) put_columns(a.dq.at(t, h) + c0, r, a.scale, left, ar.wide_dq);
         for (unsigned again = __ballot_sync(0xffffffffu, real && !all_finite(r, left)); again;
              again &= again - 1) {
           const int from = __ffs(again) - 1;
@@ -968,6 +1030,13 @@ cudaError_t backward_tiles(const SpanArgs& a, void* ws, cudaStream_t s) {
   ar.cap = cap_of(a.scale, a.cap);
   ar.scale_log2 = (a.cap > 0.f ? a.cap : a.scale) * kLog2e;
   ar.err = device_error_ptr();
+  auto wide = [](const View& x, int64_t tokens, int64_t heads) {
+    return (reinterpret_cast<uintptr_t>(x.p) | (tokens > 1 ? x.ts * 2 : 0) |
+            (heads > 1 ? x.hs * 2 : 0)) % 32 == 0;
+  };
+  ar.wide_dq = wide(a.dq, a.queries, a.nh);
+  ar.wide_dk = wide(a.dk, a.keys, a.nkv);
+  ar.wide_dv = wide(a.dv, a.keys, a.nkv);
   if (a.d <= 64) return a.cap > 0.f ? launch<64, true>(ar, s) : launch<64, false>(ar, s);
   return a.cap > 0.f ? launch<128, true>(ar, s) : launch<128, false>(ar, s);
 }
