@@ -106,7 +106,7 @@ size_t rdt_attention_workspace_bytes(int32_t queries, int32_t keys, int32_t n_he
   if (shape_problem(queries, keys, n_heads, n_kv_heads, head_dim)) return 0;
   if (!in_tiles(queries, keys)) return 0;
   const size_t n = backward
-                       ? backward_workspace(queries, n_heads, n_kv_heads)
+                       ? backward_workspace(queries, keys, n_heads, n_kv_heads, head_dim)
                        : forward_workspace(queries, keys, n_heads, n_kv_heads, head_dim);
   return (n + 255) / 256 * 256;
 }

@@ -23,31 +23,22 @@ __device__ __forceinline__ void after_previous_kernel() {
   asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Launches `kernel`, in clusters of `cluster` CTAs, so that it may start while the
-// stream's previous one ends.
+// Launches `kernel` so that it may start while the stream's previous one ends.
 template <typename... P, typename... A>
-cudaError_t launch_clusters(void (*kernel)(P...), int cluster, int64_t grid, int threads,
-                            size_t smem, cudaStream_t s, A... args) {
-  cudaLaunchAttribute at[2] = {};
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = cluster;
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+cudaError_t launch_overlapping(void (*kernel)(P...), int64_t grid, int threads, size_t smem,
+                               cudaStream_t s, A... args) {
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
   cfg.blockDim = dim3(threads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cfg.attrs = at;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
   note_launch();
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
-}
-template <typename... P, typename... A>
-cudaError_t launch_overlapping(void (*kernel)(P...), int64_t grid, int threads, size_t smem,
-                               cudaStream_t s, A... args) {
-  return launch_clusters(kernel, 1, grid, threads, smem, s, args...);
 }
 
 // Lets a kernel have `smem` bytes of dynamic shared memory on the current device;

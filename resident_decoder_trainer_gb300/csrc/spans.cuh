@@ -290,7 +290,7 @@ int forward_splits(int queries, int keys, int nkv, int rep);
 size_t forward_workspace(int queries, int keys, int nh, int nkv, int d);
 cudaError_t forward_tiles(const SpanArgs& a, void* ws, cudaStream_t s);
 
-size_t backward_workspace(int queries, int nh, int nkv);
+size_t backward_workspace(int queries, int keys, int nh, int nkv, int d);
 cudaError_t backward_tiles(const SpanArgs& a, void* ws, cudaStream_t s);
 
 }  // namespace rdt

@@ -4,11 +4,11 @@
 //  * prepare: D = d_o . o - d_lse and the base-2 log-sum-exp of every row, tile
 //    by tile (spans.cuh), both negated; the spans of tiles and of groups of 32
 //    tiles, by which the others find what meets what;
-//  * dK/dV: one CTA per (128 keys, key head) walks the row tiles that see any
-//    of its keys. S^T = K Q^T, P^T, dV += P^T dO; dP^T = V dO^T,
+//  * dK/dV: a CTA takes (128 keys, key head) items and walks the row tiles that
+//    see any of the keys. S^T = K Q^T, P^T, dV += P^T dO; dP^T = V dO^T,
 //    dS^T = P^T o (dP^T - D) slope, dK += dS^T Q. P^T and dS^T are written over
 //    their scores in TMEM as bf16 and read from there; dK and dV stay in TMEM;
-//  * dQ: a CTA walks (row tile, key head) items; S and dP once more,
+//  * dQ: a CTA takes (row tile, key head) items; S and dP once more,
 //    dQ += dS K.
 // In both, warp 0 loads by TMA, warp 1 issues the MMAs, and warps 4-19 do the
 // elementwise work: TMEM lanes 32 (w mod 4) on, columns 32 (w / 4 - 1) on.
@@ -46,6 +46,10 @@ struct Args {
   int *lo, *len;           // [tiles][128]
   TileSpan* tiles;
   int2* group;  // first, end
+  int64_t key_tiles;  // of all key heads
+  int parts;          // items of a key tile
+  float4* part;       // parts = 2: sums of each half
+  int* arrived;       // and how many of a key tile's are there
   int* err;
   bool wide_dq, wide_dk, wide_dv;  // rows at multiples of 32 bytes
 };
@@ -53,53 +57,54 @@ struct Args {
 // ---------------------------------------------------------------- prepare
 constexpr int kPrepThreads = 256;
 
-// Blocks [0, groups) find the spans, the others the rows' D and lse.
+// Blocks [0, groups) find the groups' spans, the others the tiles' and the rows'
+// D and lse.
 __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_constant__ Args ar) {
   const SpanArgs& a = ar.a;
+  __shared__ TileSpan found[kPrepThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   after_previous_kernel();
-  if (static_cast<int>(blockIdx.x) < ar.groups) {
-    __shared__ int2 mine[kPrepThreads / 32];
-    int lo_all = INT32_MAX, hi_all = 0;
-    for (int i = warp; i < kGroup; i += kPrepThreads / 32) {
-      const int tile = blockIdx.x * kGroup + i;
-      if (tile >= ar.tl.tiles) break;
-      TileSpan s = {INT32_MAX, 0, 0, INT32_MAX};
-      for (int row = lane; row < 128; row += 32) {
-        const int in = row / a.rep, t = tile * ar.tl.per + in;
-        int x = 0, y = 0;
-        if (in < ar.tl.per && t < a.queries) a.span(t, x, y);
-        if (x < y) {
-          s.first = min(s.first, x);
-          s.end = max(s.end, y);
-          s.all_first = max(s.all_first, x);
-          s.all_end = min(s.all_end, y);
-        } else {
-          x = y = 0;
-        }
-        ar.lo[tile * int64_t{128} + row] = x;
-        ar.len[tile * int64_t{128} + row] = y - x;
-      }
-      s.first = __reduce_min_sync(0xffffffffu, s.first);
-      s.end = __reduce_max_sync(0xffffffffu, s.end);
-      s.all_first = __reduce_max_sync(0xffffffffu, s.all_first);
-      s.all_end = __reduce_min_sync(0xffffffffu, s.all_end);
-      if (s.first >= s.end) s.first = s.end = 0;
-      if (lane == 0) ar.tiles[tile] = s;
-      if (s.first < s.end) {
-        lo_all = min(lo_all, s.first);
-        hi_all = max(hi_all, s.end);
-      }
-    }
-    if (lane == 0) mine[warp] = make_int2(lo_all, hi_all);
+  // the warps' spans together: whole block
+  auto joined = [&](TileSpan s) {
+    s.first = __reduce_min_sync(0xffffffffu, s.first);
+    s.end = __reduce_max_sync(0xffffffffu, s.end);
+    s.all_first = __reduce_max_sync(0xffffffffu, s.all_first);
+    s.all_end = __reduce_min_sync(0xffffffffu, s.all_end);
+    if (lane == 0) found[warp] = s;
     __syncthreads();
-    if (threadIdx.x == 0) {
-      for (int w = 1; w < kPrepThreads / 32; ++w) {
-        lo_all = min(lo_all, mine[w].x);
-        hi_all = max(hi_all, mine[w].y);
-      }
-      ar.group[blockIdx.x] = lo_all < hi_all ? make_int2(lo_all, hi_all) : make_int2(0, 0);
+    for (int w = 0; w < kPrepThreads / 32; ++w) {
+      s.first = min(s.first, found[w].first);
+      s.end = max(s.end, found[w].end);
+      s.all_first = max(s.all_first, found[w].all_first);
+      s.all_end = min(s.all_end, found[w].all_end);
     }
+    __syncthreads();
+    if (s.first >= s.end) s.first = s.end = 0;
+    return s;
+  };
+  auto take = [](TileSpan& s, int x, int y) {
+    s.first = min(s.first, x);
+    s.end = max(s.end, y);
+    s.all_first = max(s.all_first, x);
+    s.all_end = min(s.all_end, y);
+  };
+  const TileSpan none = {INT32_MAX, 0, 0, INT32_MAX};
+  if (static_cast<int>(blockIdx.x) < ar.groups) {
+    if (ar.parts > 1)
+      for (int i = blockIdx.x * kPrepThreads + threadIdx.x; i < ar.key_tiles;
+           i += ar.groups * kPrepThreads)
+        ar.arrived[i] = 0;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kGroup * ar.tl.per;
+    const int64_t t1 = min(t0 + kGroup * ar.tl.per, static_cast<int64_t>(a.queries));
+    TileSpan s = none;
+#pragma unroll 4
+    for (int64_t t = t0 + threadIdx.x; t < t1; t += kPrepThreads) {
+      int x, y;
+      a.span(static_cast<int>(t), x, y);
+      if (x < y) take(s, x, y);
+    }
+    s = joined(s);
+    if (threadIdx.x == 0) ar.group[blockIdx.x] = make_int2(s.first, s.end);
     return;
   }
   // a row is `lanes` lanes of eight columns; a CTA takes a key head's row tile at
@@ -111,14 +116,33 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_cons
   const int units = a.nkv * ar.tl.tiles, ctas = gridDim.x - ar.groups;
   for (int unit = blockIdx.x - ar.groups; unit < units; unit += ctas) {
     const int g = unit / ar.tl.tiles, tile = unit - g * ar.tl.tiles;
-#pragma unroll 4
-    for (int base = 16 * warp; base < 16 * warp + 16; base += per_warp) {
-      const int row = base + (lane >> log2);
+    if (g == 0) {
+      const int row = threadIdx.x;
+      TileSpan s = none;
+      if (row < 128) {
+        const int in = static_cast<int>(row * inv_rep >> 16), t = tile * ar.tl.per + in;
+        int x = 0, y = 0;
+        if (in < ar.tl.per && t < a.queries) a.span(t, x, y);
+        if (x < y)
+          take(s, x, y);
+        else
+          x = y = 0;
+        ar.lo[tile * int64_t{128} + row] = x;
+        ar.len[tile * int64_t{128} + row] = y - x;
+      }
+      s = joined(s);
+      if (row == 0) ar.tiles[tile] = s;
+    }
+    // this lane's part of each of the warp's rows
+    float part[8];
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      part[b] = 0.f;
+      if (b * per_warp >= 16) break;
+      const int row = 16 * warp + b * per_warp + (lane >> log2);
       const int in = static_cast<int>(row * inv_rep >> 16), t = tile * ar.tl.per + in;
       const int h = g * a.rep + row - in * a.rep;
-      const bool real = in < ar.tl.per && t < a.queries;
-      float own = 0.f;
-      if (real && c < a.d) {
+      if (in < ar.tl.per && t < a.queries && c < a.d) {
         Eight<bf16> x, y;
         float u[8], v[8];
         x.load(a.d_o.at(t, h) + c);
@@ -126,25 +150,35 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_cons
         x.get(u);
         y.get(v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) own = fmaf(u[i], v[i], own);
+        for (int i = 0; i < 8; ++i) part[b] = fmaf(u[i], v[i], part[b]);
       }
-      for (int o = lanes >> 1; o > 0; o >>= 1) own += __shfl_xor_sync(0xffffffffu, own, o);
-      if ((lane & (lanes - 1)) == 0) {
-        float neg_lse = kNoRow, neg_d = 0.f;
-        if (real) {
-          const int64_t th = static_cast<int64_t>(t) * a.nh + h;
-          int x, y;
-          a.span(t, x, y);
-          if (x < y) {
-            neg_lse = -a.lse[th] * kLog2e;
-            neg_d = (a.d_lse ? a.d_lse[th] : 0.f) - own;
-          }
+    }
+    // the rows' sums, each to the lane that finishes its row
+    float own = 0.f;
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      if (b * per_warp >= 16) break;
+      float sum = part[b];
+      for (int o = lanes >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      sum = __shfl_sync(0xffffffffu, sum, (lane & (per_warp - 1)) << log2);
+      if (lane / per_warp == b) own = sum;
+    }
+    if (lane < 16) {
+      const int row = 16 * warp + lane;
+      const int in = static_cast<int>(row * inv_rep >> 16), t = tile * ar.tl.per + in;
+      float neg_lse = kNoRow, neg_d = 0.f;
+      if (in < ar.tl.per && t < a.queries) {
+        const int64_t th = static_cast<int64_t>(t) * a.nh + g * a.rep + row - in * a.rep;
+        int x, y;
+        a.span(t, x, y);
+        if (x < y) {
+          neg_lse = -a.lse[th] * kLog2e;
+          neg_d = (a.d_lse ? a.d_lse[th] : 0.f) - own;
         }
-        const int64_t at = (static_cast<int64_t>(g) * ar.tl.tiles + tile) * 128 + row;
-        ar.neg_lse[at] = neg_lse;
-        ar.neg_d[at] = neg_d;
       }
-      __syncwarp();
+      const int64_t at = (static_cast<int64_t>(g) * ar.tl.tiles + tile) * 128 + row;
+      ar.neg_lse[at] = neg_lse;
+      ar.neg_d[at] = neg_d;
     }
   }
 }
@@ -223,70 +257,100 @@ __device__ __forceinline__ void settle(int* err) {
 }
 
 // ------------------------------------------------------------------ dK, dV
+// What the loading warp says of a step: a row tile, or the end of an item.
 struct Meta {
-  int tile;  // -1: no more
-  int full;  // every row that sees anything sees all of the CTA's keys
+  int tile;  // row tile; kEnd: the item's tiles are through; kStop: all items are
+  int full;  // every row that sees anything sees all of the item's keys; with kEnd, how to end
+  int n0, g; // the item's first key and key head
 };
+constexpr int kEnd = -1, kStop = -2;
+constexpr int kNothing = 0, kAlone = 1, kShared = 2;  // ways to end; the second half: kShared + 1
 
 template <int D>
 struct KvCfg {
   static constexpr uint32_t CHUNK = 128 * 128, TILE = 128 * D * 2;
-  static constexpr int ST = D == 128 ? 2 : 4;  // stages of Q and of dO
-  static constexpr uint32_t OFF_K = 0, OFF_V = TILE, OFF_Q = 2 * TILE, OFF_DO = OFF_Q + ST * TILE,
-                            OFF_ROW = OFF_DO + ST * TILE,  // [ST][neg_lse, neg_d, lo, len][128]
-      OFF_META = OFF_ROW + ST * 2048, OFF_BAR = OFF_META + ST * sizeof(Meta);
-  static constexpr size_t SMEM = OFF_BAR + 256 + 1024;
+  // Stages: Q is read by S and, an elementwise pass later, by dK; its copies take
+  // longer than that pass, so it has one stage more than dO where memory is short
+  // (two: 3370 cycles a row tile; three: 2900).
+  static constexpr int QST = D == 128 ? 3 : 4, OST = D == 128 ? 2 : 4, IST = 2;
+  static constexpr uint32_t OFF_K = 0, OFF_V = TILE, OFF_Q = 2 * TILE, OFF_DO = OFF_Q + QST * TILE,
+                            OFF_ROW = OFF_DO + OST * TILE,  // [IST][neg_lse, neg_d][128]
+      OFF_META = OFF_ROW + IST * 1024, OFF_NEXT = OFF_META + IST * sizeof(Meta),
+                            OFF_BAR = OFF_NEXT + 16;
+  static constexpr size_t SMEM = OFF_BAR + 288;  // at a multiple of 1024, which is checked
   static constexpr uint32_t T_DK = 0, T_DV = 128, T_S = 256, T_DP = 384, TMEM_COLS = 512;
-  static_assert(SMEM <= 232448 && OFF_BAR % 8 == 0, "");
+  static_assert(SMEM <= 232448 && OFF_NEXT % 16 == 0, "");
 };
 
 // TMEM column, relative to a block of 128, of the packed bf16 A operand for K
 // step kk (16 rows): 32 columns' pairs lie in the first 16 of their place.
 __device__ __forceinline__ uint32_t packed_col(int kk) { return (kk >> 1) * 32 + (kk & 1) * 8; }
 
-// R CTAs (a cluster) share the row tiles of a key tile, every R-th each.
-template <int D, bool CAP, int R>
+// An item is a key tile of a key head, or (parts = 2) one of two halves of it.
+// Where a key tile is seen by fewer than kShareFrom row tiles (45 us of work) its
+// first half takes them all; else each takes every second, leaves its sums in
+// the workspace, and the one that is done last adds the two (in either order
+// the same). 4096 packed tokens, 32 / 8 heads of 128: 133 us in all from 32 row
+// tiles on, 141 from 24, 145 from 8, 151 without halves. One CTA of the grid an
+// item, taken as CTAs get free, as in the forward pass.
+constexpr int kShareFrom = 32;
+
+template <int D, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
     spans_dkdv_kernel(const __grid_constant__ CUtensorMap tq,
                       const __grid_constant__ CUtensorMap tdo,
                       const __grid_constant__ CUtensorMap tk,
                       const __grid_constant__ CUtensorMap tv, const __grid_constant__ Args ar) {
   using C = KvCfg<D>;
-  constexpr int ST = C::ST;
+  constexpr uint32_t QST = C::QST, OST = C::OST, IST = C::IST;
   const SpanArgs& a = ar.a;
   int* err = ar.err;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem_tiles[];
+  uint8_t* smem = smem_tiles;
   const uint32_t sbase = smem_u32(smem);
+  if (sbase & 1023u) {  // the swizzled tiles' layout counts on it
+    record_error(err, kErrTimeout);
+    return;
+  }
   const uint32_t bar0 = sbase + C::OFF_BAR;
-  const uint32_t kv_full = bar0, q_full = bar0 + 8, q_empty = q_full + 8 * ST,
-                 o_full = q_empty + 8 * ST, o_empty = o_full + 8 * ST, s_full = o_empty + 8 * ST,
+  const uint32_t kv_full = bar0, kv_empty = bar0 + 8, q_full = bar0 + 16,
+                 q_empty = q_full + 8 * QST, o_full = q_empty + 8 * QST, o_empty = o_full + 8 * OST,
+                 i_full = o_empty + 8 * OST, i_empty = i_full + 8 * IST, s_full = i_empty + 8 * IST,
                  dp_full = s_full + 8, p_ready = dp_full + 8, ds_ready = p_ready + 8,
-                 fin = ds_ready + 8, drain = fin + 8;
-  static_assert(8 * (1 + 4 * ST + 6) <= 248, "");
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 248);
+                 fin = ds_ready + 8, acc_free = fin + 8, next = acc_free + 8, left_it = next + 8,
+                 decided = left_it + 8, drain = decided + 8;
+  static_assert(8 * (2 * (QST + OST + IST) + 12) <= 280, "");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 280);
+  volatile int* decision = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + 284);
   Meta* meta = reinterpret_cast<Meta*>(smem + C::OFF_META);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int chunks = (a.d + 63) / 64, used = ar.tl.per * a.rep;
-  const int rank = blockIdx.x % R;  // in the cluster
-  const int n0 = static_cast<int>(blockIdx.x / R / a.nkv) * 128;
-  const int g = static_cast<int>(blockIdx.x / R % a.nkv);
 
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
-    for (int x = 0; x < ST; ++x) {
+    mbar_init(kv_empty, 1);
+    for (uint32_t x = 0; x < QST; ++x) {
       mbar_init(q_full + 8 * x, 1);
       mbar_init(q_empty + 8 * x, 1);
+    }
+    for (uint32_t x = 0; x < OST; ++x) {
       mbar_init(o_full + 8 * x, 1);
       mbar_init(o_empty + 8 * x, 1);
+    }
+    for (uint32_t x = 0; x < IST; ++x) {
+      mbar_init(i_full + 8 * x, 1);
+      mbar_init(i_empty + 8 * x, 1 + kEltThreads / 32);  // the MMA thread, the elementwise warps
     }
     mbar_init(s_full, 1);
     mbar_init(dp_full, 1);
     mbar_init(p_ready, kEltThreads);
     mbar_init(ds_ready, kEltThreads);
     mbar_init(fin, 1);
+    mbar_init(acc_free, kEltThreads);
+    mbar_init(next, 1);
+    mbar_init(left_it, kEltThreads);
+    mbar_init(decided, 1);
     mbar_init(drain, 1);
     fence_mbar_init();
     tma_prefetch_desc(&tq);
@@ -297,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (used < 128) {
     // rows past a tile's last are never loaded, and p = 0 does not clear a NaN
     const int words = (128 - used) * 32;
-    for (int i = threadIdx.x; i < 2 * ST * chunks * words; i += kThreads) {
+    for (int i = threadIdx.x; i < static_cast<int>(QST + OST) * chunks * words; i += kThreads) {
       const int w = i % words, block = i / words;
       const uint32_t base = C::OFF_Q + (block / chunks) * C::TILE + (block % chunks) * C::CHUNK;
       *reinterpret_cast<uint32_t*>(smem + base + used * 128 + 4 * w) = 0u;
@@ -314,68 +378,105 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < 4) regs_dec<56>();
   if (warp == 0) {
     // --------------------------------------------------------- producer
-    if (lane == 0) {
-      mbar_arrive_expect_tx(kv_full, 2 * chunks * C::CHUNK);
-      for (int c = 0; c < chunks; ++c) {
-        tma_load_3d(sbase + C::OFF_K + c * C::CHUNK, &tk, kv_full, c * 64, g, n0);
-        tma_load_3d(sbase + C::OFF_V + c * C::CHUNK, &tv, kv_full, c * 64, g, n0);
-      }
-    }
-    const int n1 = min(n0 + 128, a.keys);
     bool ok = true;
-    int it = 0, met = 0;
-    // one row tile, or the end of them
-    auto send = [&](int tile, int full) {
-      const int st = it % ST;
-      const uint32_t ph = ((it / ST) & 1) ^ 1;
-      ++it;
-      if (lane == 0) {
-        ok = wait_for(q_empty + 8 * st, ph, err);
-        if (ok) {
-          meta[st] = Meta{tile, full};
-          if (tile < 0) {
-            mbar_arrive(q_full + 8 * st);
-          } else {
-            const uint32_t q = sbase + C::OFF_Q + st * C::TILE, o = sbase + C::OFF_DO + st * C::TILE;
-            const uint32_t row = sbase + C::OFF_ROW + st * 2048;
-            const int64_t at = (static_cast<int64_t>(g) * ar.tl.tiles + tile) * 128;
-            mbar_arrive_expect_tx(q_full + 8 * st, chunks * used * 128 + 2048);
-            for (int c = 0; c < chunks; ++c)
-              tma_load_3d(q + c * C::CHUNK, &tq, q_full + 8 * st, c * 64, g * a.rep,
-                          tile * ar.tl.per);
-            bulk_load_1d(row, ar.neg_lse + at, 512, q_full + 8 * st);
-            bulk_load_1d(row + 512, ar.neg_d + at, 512, q_full + 8 * st);
-            bulk_load_1d(row + 1024, ar.lo + tile * int64_t{128}, 512, q_full + 8 * st);
-            bulk_load_1d(row + 1536, ar.len + tile * int64_t{128}, 512, q_full + 8 * st);
-            ok = wait_for(o_empty + 8 * st, ph, err);
-            if (ok) {
-              mbar_arrive_expect_tx(o_full + 8 * st, chunks * used * 128);
-              for (int c = 0; c < chunks; ++c)
-                tma_load_3d(o + c * C::CHUNK, &tdo, o_full + 8 * st, c * 64, g * a.rep,
-                            tile * ar.tl.per);
+    uint32_t r = 0, tiles = 0, loaded = 0;  // steps, row tiles, items with any so far
+    int item = blockIdx.x;
+    for (uint32_t it = 0; ok && item >= 0; ++it) {
+      const int half = item % ar.parts, x = item / ar.parts;
+      const int g = x % a.nkv, n0 = x / a.nkv * 128, n1 = min(n0 + 128, a.keys);
+      // calls f(tile, full) for the row tiles that see any of the keys, until it is false
+      auto each = [&](auto f) {
+        bool on = true;
+        for (int g0 = 0; g0 < ar.groups && on; g0 += 32) {
+          const int2 span = g0 + lane < ar.groups ? ar.group[g0 + lane] : make_int2(0, 0);
+          unsigned some = __ballot_sync(0xffffffffu, span.x < n1 && span.y > n0);
+          for (; some && on; some &= some - 1) {
+            const int first = (g0 + __ffs(some) - 1) * kGroup, tile = first + lane;
+            TileSpan s = {0, 0, 0, 0};
+            if (tile < ar.tl.tiles) s = ar.tiles[tile];
+            unsigned meets = __ballot_sync(0xffffffffu, s.first < n1 && s.end > n0);
+            const unsigned full =
+                __ballot_sync(0xffffffffu, s.all_first <= n0 && s.all_end >= n1);
+            for (; meets && on; meets &= meets - 1) {
+              const int i = __ffs(meets) - 1;
+              on = f(first + i, (full >> i) & 1);
             }
           }
         }
+      };
+      bool shared = false;
+      if (ar.parts > 1) {
+        int count = 0;
+        each([&](int, int) { return ++count < kShareFrom; });
+        shared = count >= kShareFrom;
       }
-      ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0);
-    };
-    for (int g0 = 0; g0 < ar.groups && ok; g0 += 32) {
-      const int2 span = g0 + lane < ar.groups ? ar.group[g0 + lane] : make_int2(0, 0);
-      unsigned some = __ballot_sync(0xffffffffu, span.x < n1 && span.y > n0);
-      for (; some && ok; some &= some - 1) {
-        const int first = (g0 + __ffs(some) - 1) * kGroup, tile = first + lane;
-        TileSpan s = {0, 0, 0, 0};
-        if (tile < ar.tl.tiles) s = ar.tiles[tile];
-        unsigned meets = __ballot_sync(0xffffffffu, s.first < n1 && s.end > n0);
-        const unsigned full =
-            __ballot_sync(0xffffffffu, s.all_first <= n0 && s.all_end >= n1);
-        for (; meets && ok; meets &= meets - 1) {
-          const int i = __ffs(meets) - 1;
-          if (met++ % R == rank) send(first + i, (full >> i) & 1);
+      const bool mine = shared || half == 0;
+      bool some = false;  // K and V are under way
+      int met = 0;
+      auto send = [&](int tile, int full) {
+        if (lane == 0) {
+          if (tile >= 0) {
+            const uint32_t sq = tiles % QST, q = sbase + C::OFF_Q + sq * C::TILE;
+            ok = wait_for(q_empty + 8 * sq, ((tiles / QST) & 1) ^ 1, err);
+            if (ok) {
+              mbar_arrive_expect_tx(q_full + 8 * sq, chunks * used * 128);
+              for (int c = 0; c < chunks; ++c)
+                tma_load_3d(q + c * C::CHUNK, &tq, q_full + 8 * sq, c * 64, g * a.rep,
+                            tile * ar.tl.per);
+            }
+            if (ok && !some) ok = wait_for(kv_empty, (loaded & 1) ^ 1, err);
+            if (ok && !some) {
+              mbar_arrive_expect_tx(kv_full, 2 * chunks * C::CHUNK);
+              for (int c = 0; c < chunks; ++c) {
+                tma_load_3d(sbase + C::OFF_K + c * C::CHUNK, &tk, kv_full, c * 64, g, n0);
+                tma_load_3d(sbase + C::OFF_V + c * C::CHUNK, &tv, kv_full, c * 64, g, n0);
+              }
+            }
+          }
+          const uint32_t si = r % IST, row = sbase + C::OFF_ROW + si * 1024;
+          ok = ok && wait_for(i_empty + 8 * si, ((r / IST) & 1) ^ 1, err);
+          if (ok) {
+            meta[si] = Meta{tile, full, n0, g};
+            if (tile < 0) {
+              mbar_arrive(i_full + 8 * si);
+            } else {
+              const int64_t at = (static_cast<int64_t>(g) * ar.tl.tiles + tile) * 128;
+              mbar_arrive_expect_tx(i_full + 8 * si, 1024);
+              bulk_load_1d(row, ar.neg_lse + at, 512, i_full + 8 * si);
+              bulk_load_1d(row + 512, ar.neg_d + at, 512, i_full + 8 * si);
+              const uint32_t so = tiles % OST, o = sbase + C::OFF_DO + so * C::TILE;
+              ok = wait_for(o_empty + 8 * so, ((tiles / OST) & 1) ^ 1, err);
+              if (ok) {
+                mbar_arrive_expect_tx(o_full + 8 * so, chunks * used * 128);
+                for (int c = 0; c < chunks; ++c)
+                  tma_load_3d(o + c * C::CHUNK, &tdo, o_full + 8 * so, c * 64, g * a.rep,
+                              tile * ar.tl.per);
+              }
+            }
+          }
         }
-      }
+        ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0);
+        ++r;
+        if (tile >= 0) {
+          ++tiles;
+          some = true;
+        }
+      };
+      if (mine)
+        each([&](int tile, int full) {
+          if (!shared || (met++ & 1) == half) send(tile, full);
+          return ok;
+        });
+      if (some) ++loaded;
+      // asked for now, not before: an item that waits here could have been another SM's
+      if (lane == 0) next_cta_request(sbase + C::OFF_NEXT, next);
+      if (ok) send(kEnd, shared ? kShared + half : mine ? kAlone : kNothing);
+      // waited for on the way out too: the answer is written to this CTA's memory
+      const bool answered = warp_wait(next, it & 1, err);
+      ok = ok && answered;
+      if (ok) item = next_cta_answer(sbase + C::OFF_NEXT);
+      if (ok && item < 0) send(kStop, 0);
     }
-    if (ok) send(-1, 0);
   } else if (warp == 1) {
     if (elect_one()) {
       // -------------------------------------------------------------- MMA
@@ -385,69 +486,77 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t k_desc = desc_low(sbase + C::OFF_K, 16);
       const uint32_t v_desc = desc_low(sbase + C::OFF_V, 16);
       auto scores = [&](uint32_t to, uint32_t kv, uint32_t rows) {
-        const uint32_t r = not_hoisted(desc_low(rows, 16));
+        const uint32_t row = not_hoisted(desc_low(rows, 16));
         kv = not_hoisted(kv);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           if (k >= ksteps) break;
           const uint32_t off = ((k >> 2) * C::CHUNK + (k & 3) * 32) >> 4;
-          tc_mma_low(tmem + to, kv + off, r + off, id_s, k > 0);
+          tc_mma_low(tmem + to, kv + off, row + off, id_s, k > 0);
         }
       };
-      auto add = [&](uint32_t to, uint32_t from, uint32_t rows, int it) {
-        const uint32_t r = not_hoisted(desc_low(rows, C::CHUNK));
+      auto add = [&](uint32_t to, uint32_t from, uint32_t rows, bool first) {
+        const uint32_t row = not_hoisted(desc_low(rows, C::CHUNK));
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          tc_mma_ts_low(tmem + to, tmem + from + packed_col(k), r + k * 128, id_kv,
-                         (it | k) != 0);
+          tc_mma_ts_low(tmem + to, tmem + from + packed_col(k), row + k * 128, id_kv,
+                        !first || k > 0);
       };
-      // whether there is a tile `it`, with its Q loaded
-      auto wait_q = [&](int it, bool& more) -> bool {
-        if (!wait_for(q_full + 8 * (it % ST), (it / ST) & 1, err)) return false;
-        more = meta[it % ST].tile >= 0;
-        tc_fence_after();
-        return true;
-      };
-      auto wait = [&](uint32_t bar, int phase) -> bool {
+      auto wait = [&](uint32_t bar, uint32_t phase) -> bool {
         if (!wait_for(bar, phase & 1, err)) return false;
         tc_fence_after();
         return true;
       };
-      auto q_of = [&](int it) { return sbase + C::OFF_Q + (it % ST) * C::TILE; };
-      auto o_of = [&](int it) { return sbase + C::OFF_DO + (it % ST) * C::TILE; };
-      bool more = false;
-      bool ok = wait(kv_full, 0) && wait_q(0, more);
-      if (ok && more) {
-        scores(C::T_S, k_desc, q_of(0));
+      auto q_of = [&](uint32_t at) { return sbase + C::OFF_Q + (at % QST) * C::TILE; };
+      auto o_of = [&](uint32_t at) { return sbase + C::OFF_DO + (at % OST) * C::TILE; };
+      uint32_t r = 0, it = 0, u = 0;  // steps, row tiles, items with any
+      // the row tile of step r, or what else it is
+      auto step = [&](int& tile) -> bool {
+        if (!wait_for(i_full + 8 * (r % IST), (r / IST) & 1, err)) return false;
+        tile = meta[r % IST].tile;
+        mbar_arrive(i_empty + 8 * (r % IST));
+        ++r;
+        return true;
+      };
+      while (true) {
+        int tile;
+        if (!step(tile) || tile == kStop) break;
+        if (tile < 0) continue;
+        if (!wait(kv_full, u) || !wait(q_full + 8 * (it % QST), it / QST)) break;
+        scores(C::T_S, k_desc, q_of(it));
         tc_commit(s_full);
-        ok = wait(o_full, 0);
-        if (ok) {
-          scores(C::T_DP, v_desc, o_of(0));
-          tc_commit(dp_full);
+        if (!wait(o_full + 8 * (it % OST), it / OST)) break;
+        scores(C::T_DP, v_desc, o_of(it));
+        tc_commit(dp_full);
+        bool first = true, ok = true;
+        while (tile >= 0) {
+          if (!(ok = wait(p_ready, it))) break;
+          // dK and dV of the item before have been read out
+          if (first && !(ok = wait(acc_free, u ^ 1))) break;
+          add(C::T_DV, C::T_S, o_of(it), first);
+          tc_commit(o_empty + 8 * (it % OST));
+          if (!(ok = step(tile))) break;
+          if (tile >= 0) {  // after dV of this tile, which reads P from the same columns
+            if (!(ok = wait(q_full + 8 * ((it + 1) % QST), (it + 1) / QST))) break;
+            scores(C::T_S, k_desc, q_of(it + 1));
+            tc_commit(s_full);
+          }
+          if (!(ok = wait(ds_ready, it))) break;
+          add(C::T_DK, C::T_DP, q_of(it), first);
+          tc_commit(q_empty + 8 * (it % QST));
+          ++it;
+          first = false;
+          if (tile >= 0) {
+            if (!(ok = wait(o_full + 8 * (it % OST), it / OST))) break;
+            scores(C::T_DP, v_desc, o_of(it));
+            tc_commit(dp_full);
+          }
         }
+        if (!ok) break;
+        tc_commit(fin);
+        tc_commit(kv_empty);
+        ++u;
       }
-      for (int it = 0; ok && more; ++it) {
-        const int st = it % ST;
-        if (!(ok = wait(p_ready, it))) break;
-        add(C::T_DV, C::T_S, o_of(it), it);
-        tc_commit(o_empty + 8 * st);
-        bool next = false;
-        if (!(ok = wait_q(it + 1, next))) break;
-        if (next) {  // after dV of this tile, which reads P from the same columns
-          scores(C::T_S, k_desc, q_of(it + 1));
-          tc_commit(s_full);
-        }
-        if (!(ok = wait(ds_ready, it))) break;
-        add(C::T_DK, C::T_DP, q_of(it), it);
-        tc_commit(q_empty + 8 * st);
-        if (next) {
-          if (!(ok = wait(o_full + 8 * ((it + 1) % ST), (it + 1) / ST))) break;
-          scores(C::T_DP, v_desc, o_of(it + 1));
-          tc_commit(dp_full);
-        }
-        more = next;
-      }
-      tc_commit(fin);
       tc_commit(drain);
       mbar_wait(drain, 0, nullptr);
     }
@@ -455,160 +564,193 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_inc<104>();
     // ------------------------ P^T and dS^T: one key, 32 of a tile's 128 rows
     const int quarter = warp & 3, block = (warp - 4) >> 2;
-    const int row = quarter * 32 + lane, key = n0 + row;
+    const int row = quarter * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t ts = tmem + lane_base + C::T_S + block * 32;
     const uint32_t tdp = tmem + lane_base + C::T_DP + block * 32;
-    bool ok = true;
-    int it = 0;
-    for (;; ++it) {
-      const int st = it % ST;
-      ok = warp_wait(q_full + 8 * st, (it / ST) & 1, err);
-      if (!ok) break;
-      const Meta m = meta[st];
-      if (m.tile < 0) break;
-      const uint8_t* rows = smem + C::OFF_ROW + st * 2048 + block * 128;
-      const float4* lse4 = reinterpret_cast<const float4*>(rows);
-      const float4* d4 = reinterpret_cast<const float4*>(rows + 512);
-      const int4* lo4 = reinterpret_cast<const int4*>(rows + 1024);
-      const int4* len4 = reinterpret_cast<const int4*>(rows + 1536);
-      ok = warp_wait(s_full, it & 1, err);
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t sv[32], pk[16];
-      uint32_t seen = 0xffffffffu;
-      tmem_ld32(ts, sv);
-      bool full = m.full;
-      if (!full) {
-        seen = 0u;
-        auto sees = [&](int lo, int len) {
-          return static_cast<uint32_t>(key - lo) < static_cast<uint32_t>(len);
-        };
-        if (a.rep % 4 == 0) {  // four columns are rows of one query
+    uint32_t it = 0, u = 0, shares = 0;
+    bool had = false;  // a row tile of this item
+    for (uint32_t r = 0;; ++r) {
+      const uint32_t si = r % IST;
+      if (!warp_wait(i_full + 8 * si, (r / IST) & 1, err)) break;
+      const Meta m = meta[si];
+      if (m.tile == kStop) break;
+      const int key = m.n0 + row;
+      if (m.tile >= 0) {
+        had = true;
+        const uint8_t* rows = smem + C::OFF_ROW + si * 1024 + block * 128;
+        const float4* lse4 = reinterpret_cast<const float4*>(rows);
+        const float4* d4 = reinterpret_cast<const float4*>(rows + 512);
+        uint32_t seen = 0xffffffffu;
+        bool full = m.full;
+        if (!full) {
+          const int64_t at = m.tile * int64_t{128} + block * 32;
+          const int4* lo4 = reinterpret_cast<const int4*>(ar.lo + at);
+          const int4* len4 = reinterpret_cast<const int4*>(ar.len + at);
+          seen = 0u;
+          auto sees = [&](int lo, int len) {
+            return static_cast<uint32_t>(key - lo) < static_cast<uint32_t>(len);
+          };
+          if (a.rep % 4 == 0) {  // four columns are rows of one query
 #pragma unroll
-          for (int c = 0; c < 8; ++c) seen |= sees(lo4[c].x, len4[c].x) ? 15u << (4 * c) : 0u;
-        } else {
+            for (int c = 0; c < 8; ++c) seen |= sees(lo4[c].x, len4[c].x) ? 15u << (4 * c) : 0u;
+          } else {
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const int4 lo = lo4[c], len = len4[c];
-            seen |= sees(lo.x, len.x) ? 1u << (4 * c) : 0u;
-            seen |= sees(lo.y, len.y) ? 2u << (4 * c) : 0u;
-            seen |= sees(lo.z, len.z) ? 4u << (4 * c) : 0u;
-            seen |= sees(lo.w, len.w) ? 8u << (4 * c) : 0u;
+            for (int c = 0; c < 8; ++c) {
+              const int4 lo = lo4[c], len = len4[c];
+              seen |= sees(lo.x, len.x) ? 1u << (4 * c) : 0u;
+              seen |= sees(lo.y, len.y) ? 2u << (4 * c) : 0u;
+              seen |= sees(lo.z, len.z) ? 4u << (4 * c) : 0u;
+              seen |= sees(lo.w, len.w) ? 8u << (4 * c) : 0u;
+            }
           }
+          full = __all_sync(0xffffffffu, seen == ~0u);
         }
-        full = __all_sync(0xffffffffu, seen == ~0u);
-      }
-      tmem_ld_wait();
-      if constexpr (CAP) tanh_all(sv, ar.cap);
-      // sv: p, times the cap's slope
-#pragma unroll
-      for (int c = 0; c < 32; c += 4) {
-        const float4 nl = lse4[c / 4];
-#pragma unroll
-        for (int e = 0; e < 4; e += 2) {
-          float2 slope;
-          float2 p = p_of<CAP>(
-              make_float2(__uint_as_float(sv[c + e]), __uint_as_float(sv[c + e + 1])), ar,
-              e ? make_float2(nl.z, nl.w) : make_float2(nl.x, nl.y), slope);
-          pk[(c + e) / 2] = pack_bf16x2(p.x, p.y);
-          if constexpr (CAP) p = mul2(p, slope);
-          sv[c + e] = __float_as_uint(p.x);
-          sv[c + e + 1] = __float_as_uint(p.y);
-        }
-      }
-      if (!full) clear_unseen(pk, seen);
-      tmem_st16(ts, pk);
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(p_ready);
-      ok = warp_wait(dp_full, it & 1, err);
-      if (!ok) break;
-      tc_fence_after();
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t dp[16];
-        tmem_ld16(tdp + 16 * h, dp);
+        if (!warp_wait(s_full, it & 1, err)) break;
+        tc_fence_after();
+        uint32_t sv[32], pk[16];
+        tmem_ld32(ts, sv);
         tmem_ld_wait();
+        if constexpr (CAP) tanh_all(sv, ar.cap);
+        // sv: p, times the cap's slope
 #pragma unroll
-        for (int c = 0; c < 16; c += 4) {
-          const float4 nd = d4[4 * h + c / 4];
+        for (int c = 0; c < 32; c += 4) {
+          const float4 nl = lse4[c / 4];
 #pragma unroll
           for (int e = 0; e < 4; e += 2) {
-            float2 ds = add2(make_float2(__uint_as_float(dp[c + e]), __uint_as_float(dp[c + e + 1])),
-                             e ? make_float2(nd.z, nd.w) : make_float2(nd.x, nd.y));
-            ds = mul2(ds, make_float2(__uint_as_float(sv[16 * h + c + e]),
-                                      __uint_as_float(sv[16 * h + c + e + 1])));
-            pk[8 * h + (c + e) / 2] = pack_bf16x2(ds.x, ds.y);
+            float2 slope;
+            float2 p = p_of<CAP>(
+                make_float2(__uint_as_float(sv[c + e]), __uint_as_float(sv[c + e + 1])), ar,
+                e ? make_float2(nl.z, nl.w) : make_float2(nl.x, nl.y), slope);
+            pk[(c + e) / 2] = pack_bf16x2(p.x, p.y);
+            if constexpr (CAP) p = mul2(p, slope);
+            sv[c + e] = __float_as_uint(p.x);
+            sv[c + e + 1] = __float_as_uint(p.y);
           }
         }
-      }
-      if (!full) clear_unseen(pk, seen);
-      tmem_st16(tdp, pk);
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(ds_ready);
-    }
-    ok = ok && warp_wait(fin, 0, err);
-    if (ok) tc_fence_after();
-    const int c0 = block * 32, left = a.d - c0;
-    // this thread's 32 columns of dK or dV, 0 if no row tile was this CTA's
-    auto fetch = [&](uint32_t from, uint32_t (&r)[32]) {
-      if (ok && it > 0) {
-        tmem_ld32(tmem + lane_base + from + c0, r);
-        tmem_ld_wait();
-      } else {
+        if (!full) clear_unseen(pk, seen);
+        tmem_st16(ts, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(p_ready);
+        if (!warp_wait(dp_full, it & 1, err)) break;
+        tc_fence_after();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) r[e] = 0u;
-      }
-    };
-    // four columns of a row at [column / 4][row], in what were the tiles of Q and dO
-    const uint32_t at = C::OFF_Q + (block * 8 * 128 + row) * 16;
-    if (R > 1) {
-      // rank 0 finishes dK and rank 1 dV; each leaves its part of the other's
-      if (left > 0) {
-        uint32_t r[32];
-        fetch(rank ? C::T_DK : C::T_DV, r);
+        for (int h = 0; h < 2; ++h) {
+          uint32_t dp[16];
+          tmem_ld16(tdp + 16 * h, dp);
+          tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          *reinterpret_cast<uint4*>(smem + at + e * 2048) =
-              make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+          for (int c = 0; c < 16; c += 4) {
+            const float4 nd = d4[4 * h + c / 4];
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+              float2 ds =
+                  add2(make_float2(__uint_as_float(dp[c + e]), __uint_as_float(dp[c + e + 1])),
+                       e ? make_float2(nd.z, nd.w) : make_float2(nd.x, nd.y));
+              ds = mul2(ds, make_float2(__uint_as_float(sv[16 * h + c + e]),
+                                        __uint_as_float(sv[16 * h + c + e + 1])));
+              pk[8 * h + (c + e) / 2] = pack_bf16x2(ds.x, ds.y);
+            }
+          }
+        }
+        if (!full) clear_unseen(pk, seen);
+        tmem_st16(tdp, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(ds_ready);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(i_empty + 8 * si);
+        ++it;
+        continue;
       }
-      cluster_sync();
-    }
-    if (left > 0) {
+      // ------------------------------------------------ the item's end
+      __syncwarp();
+      if (lane == 0) mbar_arrive(i_empty + 8 * si);
+      if (had && !warp_wait(fin, u & 1, err)) break;
+      tc_fence_after();
+      const int c0 = block * 32, left = a.d - c0;
+      // this thread's 32 columns of dK or dV, 0 if the item had no row tile
+      auto fetch = [&](uint32_t from, uint32_t (&x)[32]) {
+        if (had) {
+          tmem_ld32(tmem + lane_base + from + c0, x);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] = 0u;
+        }
+      };
+      bool finish = m.full == kAlone;
+      // the two halves' sums: four columns of a row at [half][dK, dV][column / 4][row]
+      float4* part = nullptr;
+      if (m.full >= kShared) {
+        const int64_t pair = static_cast<int64_t>(m.n0 >> 7) * a.nkv + m.g;
+        const int half = m.full - kShared, quads = a.d / 4;
+        float4* const mine = ar.part + (pair * 2 + half) * 2 * quads * 128;
+        part = ar.part + (pair * 2 + (half ^ 1)) * 2 * quads * 128;
+        if (left > 0) {
+#pragma unroll
+          for (int which = 0; which < 2; ++which) {
+            uint32_t x[32];
+            fetch(which ? C::T_DV : C::T_DK, x);
+            float4* to = mine + (which * quads + c0 / 4) * 128 + row;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (4 * e < left)
+                __stcg(to + e * 128,
+                       make_float4(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1]),
+                                   __uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3])));
+          }
+        }
+        __threadfence();
+        mbar_arrive(left_it);
+        if (warp == 4 && lane == 0) {
+          if (mbar_wait(left_it, shares & 1, err)) {
+            __threadfence();
+            *decision = atomicAdd(ar.arrived + pair, 1);
+            __threadfence();
+            mbar_arrive(decided);
+          }
+        }
+        __syncwarp();
+        if (!warp_wait(decided, shares & 1, err)) break;
+        ++shares;
+        finish = *decision == 1;  // the other half has been left
+      }
       bool fine = true;
+      if (finish && left > 0) {
 #pragma unroll
-      for (int which = 0; which < 2; ++which) {
-        if (R > 1 && which != rank) continue;
-        uint32_t r[32];
-        fetch(which ? C::T_DV : C::T_DK, r);
-        if constexpr (R > 1) {
-          const uint32_t theirs = mapa_shared(sbase + at, rank ^ 1);
+        for (int which = 0; which < 2; ++which) {
+          uint32_t x[32];
+          fetch(which ? C::T_DV : C::T_DK, x);
+          if (part) {
+            const float4* from = part + (which * (a.d / 4) + c0 / 4) * 128 + row;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 v = load_cluster4(theirs + e * 2048);
-            r[4 * e] = __float_as_uint(__uint_as_float(r[4 * e]) + v.x);
-            r[4 * e + 1] = __float_as_uint(__uint_as_float(r[4 * e + 1]) + v.y);
-            r[4 * e + 2] = __float_as_uint(__uint_as_float(r[4 * e + 2]) + v.z);
-            r[4 * e + 3] = __float_as_uint(__uint_as_float(r[4 * e + 3]) + v.w);
+            for (int e = 0; e < 8; ++e)
+              if (4 * e < left) {
+                const float4 v = __ldcg(from + e * 128);
+                x[4 * e] = __float_as_uint(__uint_as_float(x[4 * e]) + v.x);
+                x[4 * e + 1] = __float_as_uint(__uint_as_float(x[4 * e + 1]) + v.y);
+                x[4 * e + 2] = __float_as_uint(__uint_as_float(x[4 * e + 2]) + v.z);
+                x[4 * e + 3] = __float_as_uint(__uint_as_float(x[4 * e + 3]) + v.w);
+              }
           }
+          fine = fine && all_finite(x, left);
+          if (key < a.keys)
+            put_columns((which ? a.dv : a.dk).at(key, m.g) + c0, x, which ? 1.f : a.scale, left,
+                        which ? ar.wide_dv : ar.wide_dk);
         }
-        fine = fine && all_finite(r, left);
-        if (key < a.keys && ok)
-          put_columns((which ? a.dv : a.dk).at(key, g) + c0, r, which ? 1.f : a.scale, left,
-                      which ? ar.wide_dv : ar.wide_dk);
       }
-      for (unsigned again = __ballot_sync(0xffffffffu, !fine && key < a.keys && ok); again;
+      if (had) {  // dK and dV are free for the next item
+        tc_fence_before();
+        mbar_arrive(acc_free);
+        ++u;
+        had = false;
+      }
+      for (unsigned again = __ballot_sync(0xffffffffu, !fine && key < a.keys); again;
            again &= again - 1)
-        row_dkdv(a, n0 + quarter * 32 + __ffs(again) - 1, g, c0, min(c0 + 32, a.d),
-                 R == 1 || rank == 0, R == 1 || rank == 1);
+        row_dkdv(a, m.n0 + quarter * 32 + __ffs(again) - 1, m.g, c0, min(c0 + 32, a.d), true, true);
     }
-    if (R > 1) cluster_sync();  // what this CTA left has been read
-  }
-  if (R > 1 && warp < 4) {
-    cluster_sync();
-    cluster_sync();
   }
 
   tc_fence_before();
@@ -636,7 +778,8 @@ struct QCfg {
   static constexpr uint32_t OFF_Q = 0, OFF_DO = TILE, OFF_K = 2 * TILE, OFF_V = OFF_K + KST * TILE,
                             OFF_ROW = OFF_V + VST * TILE,  // [neg_lse, neg_d, lo, len][128]
       OFF_ITEM = OFF_ROW + 2048, OFF_BAR = OFF_ITEM + kItemRing * sizeof(Item);
-  static constexpr size_t SMEM = OFF_BAR + 320;  // at a multiple of 1024, which is checked
+  static constexpr uint32_t OFF_NEXT = OFF_BAR + 320;
+  static constexpr size_t SMEM = OFF_NEXT + 16;  // at a multiple of 1024, which is checked
   static constexpr uint32_t T_S = 0, T_DP = 128, T_DQ = 256, T_DS = 384, TMEM_COLS = 512;
   static_assert(SMEM <= 232448, "");
 };
@@ -663,14 +806,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                  v_full = k_empty + 8 * KST, v_empty = v_full + 8 * VST, s_full = v_empty + 8 * VST,
                  s_free = s_full + 8, ds_ready = s_free + 8, ds_free = ds_ready + 16, dq_done = ds_free + 16,
                  dq_free = dq_done + 8, drain = dq_free + 8, item_full = drain + 8,
-                 item_empty = item_full + 8 * kItemRing;
-  static_assert(8 * (2 + 2 * KST + 2 * VST + 9 + 2 * kItemRing) <= 312, "");
+                 item_empty = item_full + 8 * kItemRing, next = item_empty + 8 * kItemRing;
+  static_assert(8 * (2 + 2 * KST + 2 * VST + 10 + 2 * kItemRing) <= 312, "");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 312);
   Item* ring = reinterpret_cast<Item*>(smem + C::OFF_ITEM);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int chunks = (a.d + 63) / 64, used = ar.tl.per * a.rep;
-  const int items = ar.tl.tiles * a.nkv;
   // item -> row tile (the last first), key head
   auto place = [&](int item, int& tile, int& g) {
     tile = ar.tl.tiles - 1 - item / a.nkv;
@@ -703,6 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(dq_done, 1);
     mbar_init(dq_free, kEltThreads);
     mbar_init(drain, 1);
+    mbar_init(next, 1);
     fence_mbar_init();
     tma_prefetch_desc(&tq);
     tma_prefetch_desc(&tdo);
@@ -723,26 +866,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       uint32_t jg = 0;
       int loaded = 0;
-      auto span_at = [&](int item) {
-        int tile, g;
-        place(item, tile, g);
-        return make_int2(ar.tiles[tile].first, ar.tiles[tile].end);
-      };
-      int2 span = span_at(blockIdx.x);
       int item = blockIdx.x;
-      for (int it = 0; ok; ++it, item += gridDim.x) {
+      for (uint32_t it = 0; ok; ++it) {
         const int slot = it % kItemRing;
         ok = wait_for(item_empty + 8 * slot, ((it / kItemRing) & 1) ^ 1, err);
         if (!ok) break;
-        const bool more = item < items;
-        const int first = span.x, n = (span.y - span.x + 127) / 128;
-        ring[slot] = Item{more ? item : -1, first, n, 0};
-        mbar_arrive(item_full + 8 * slot);
-        if (!more) break;
-        if (item + static_cast<int>(gridDim.x) < items) span = span_at(item + gridDim.x);
-        if (n == 0) continue;
+        if (item < 0) {
+          ring[slot].index = -1;
+          mbar_arrive(item_full + 8 * slot);
+          break;
+        }
         int tile, g;
         place(item, tile, g);
+        const int first = ar.tiles[tile].first, n = (ar.tiles[tile].end - first + 127) / 128;
+        ring[slot] = Item{item, first, n, 0};
+        mbar_arrive(item_full + 8 * slot);
         auto load = [&](int j, uint32_t full, uint32_t empty, int stages, uint32_t off,
                         const CUtensorMap* map) -> bool {
           const uint32_t jj = jg + j, st = jj % stages;
@@ -753,28 +891,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                         first + j * 128);
           return true;
         };
-        // K's first tile does not wait for the item before to be done with its Q
-        ok = load(0, k_full, k_empty, KST, C::OFF_K, &tk) &&
-             wait_for(q_empty, (loaded & 1) ^ 1, err);
-        if (!ok) break;
-        const int64_t at = (static_cast<int64_t>(g) * ar.tl.tiles + tile) * 128;
-        mbar_arrive_expect_tx(q_full, 2 * chunks * used * 128 + 2048);
-        for (int c = 0; c < chunks; ++c) {
-          tma_load_3d(sbase + C::OFF_Q + c * C::CHUNK, &tq, q_full, c * 64, g * a.rep,
-                      tile * ar.tl.per);
-          tma_load_3d(sbase + C::OFF_DO + c * C::CHUNK, &tdo, q_full, c * 64, g * a.rep,
-                      tile * ar.tl.per);
+        if (n > 0) {
+          // K's first tile does not wait for the item before to be done with its Q
+          ok = load(0, k_full, k_empty, KST, C::OFF_K, &tk) &&
+               wait_for(q_empty, (loaded & 1) ^ 1, err);
+          if (ok) {
+            const int64_t at = (static_cast<int64_t>(g) * ar.tl.tiles + tile) * 128;
+            mbar_arrive_expect_tx(q_full, 2 * chunks * used * 128 + 2048);
+            for (int c = 0; c < chunks; ++c) {
+              tma_load_3d(sbase + C::OFF_Q + c * C::CHUNK, &tq, q_full, c * 64, g * a.rep,
+                          tile * ar.tl.per);
+              tma_load_3d(sbase + C::OFF_DO + c * C::CHUNK, &tdo, q_full, c * 64, g * a.rep,
+                          tile * ar.tl.per);
+            }
+            bulk_load_1d(sbase + C::OFF_ROW, ar.neg_lse + at, 512, q_full);
+            bulk_load_1d(sbase + C::OFF_ROW + 512, ar.neg_d + at, 512, q_full);
+            bulk_load_1d(sbase + C::OFF_ROW + 1024, ar.lo + tile * int64_t{128}, 512, q_full);
+            bulk_load_1d(sbase + C::OFF_ROW + 1536, ar.len + tile * int64_t{128}, 512, q_full);
+          }
+          for (int j = 0; j < n && ok; ++j) {
+            ok = (j == 0 || load(j, k_full, k_empty, KST, C::OFF_K, &tk)) &&
+                 load(j, v_full, v_empty, VST, C::OFF_V, &tv);
+          }
+          jg += n;
+          ++loaded;
         }
-        bulk_load_1d(sbase + C::OFF_ROW, ar.neg_lse + at, 512, q_full);
-        bulk_load_1d(sbase + C::OFF_ROW + 512, ar.neg_d + at, 512, q_full);
-        bulk_load_1d(sbase + C::OFF_ROW + 1024, ar.lo + tile * int64_t{128}, 512, q_full);
-        bulk_load_1d(sbase + C::OFF_ROW + 1536, ar.len + tile * int64_t{128}, 512, q_full);
-        for (int j = 0; j < n && ok; ++j) {
-          ok = (j == 0 || load(j, k_full, k_empty, KST, C::OFF_K, &tk)) &&
-               load(j, v_full, v_empty, VST, C::OFF_V, &tv);
-        }
-        jg += n;
-        ++loaded;
+        // asked for now, not before: an item that waits here could have been another SM's;
+        // waited for on the way out too: the answer is written to this CTA's memory
+        next_cta_request(sbase + C::OFF_NEXT, next);
+        const bool answered = wait_for(next, it & 1, err);
+        ok = ok && answered;
+        if (ok) item = next_cta_answer(sbase + C::OFF_NEXT);
       }
     }
   } else if (warp == 1) {
@@ -956,18 +1103,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // -------------------------------------------------------------------- host
-constexpr int kSharedBelow = 3;
-
-template <int D, bool CAP, int R>
-cudaError_t launch_dkdv(const Args& ar, const CUtensorMap& tq, const CUtensorMap& tdo,
-                        const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
-  const cudaError_t e = allow_smem<spans_dkdv_kernel<D, CAP, R>>(KvCfg<D>::SMEM);
-  if (e != cudaSuccess) return e;
-  return launch_clusters(spans_dkdv_kernel<D, CAP, R>, R,
-                         static_cast<int64_t>((ar.a.keys + 127) / 128) * ar.a.nkv * R, kThreads,
-                         KvCfg<D>::SMEM, s, tq, tdo, tk, tv, ar);
-}
-
 template <int D, bool CAP>
 cudaError_t launch(const Args& ar, cudaStream_t s) {
   const SpanArgs& a = ar.a;
@@ -977,27 +1112,29 @@ cudaError_t launch(const Args& ar, cudaStream_t s) {
       !make_tma_heads(&tk, a.k.p, a.keys, a.nkv, a.d, a.k.ts, a.k.hs, 1, 128) ||
       !make_tma_heads(&tv, a.v.p, a.keys, a.nkv, a.d, a.v.ts, a.v.hs, 1, 128))
     return cudaErrorInvalidValue;
-  cudaError_t e = allow_smem<spans_dq_kernel<D, CAP>>(QCfg<D>::SMEM);
+  cudaError_t e = allow_smem<spans_dkdv_kernel<D, CAP>>(KvCfg<D>::SMEM);
+  if (e == cudaSuccess) e = allow_smem<spans_dq_kernel<D, CAP>>(QCfg<D>::SMEM);
   if (e != cudaSuccess) return e;
   const int64_t units = static_cast<int64_t>(a.nkv) * ar.tl.tiles;
   const int64_t prep = ar.groups + std::min<int64_t>(units, int64_t{num_sms()} * 8);
   e = launch_overlapping(prepare_kernel, prep, kPrepThreads, 0, s, ar);
   if (e != cudaSuccess) return e;
-  // Few key tiles: two CTAs share the rows of each.
-  const int64_t key_tiles = static_cast<int64_t>((a.keys + 127) / 128) * a.nkv;
-  e = key_tiles < kSharedBelow * int64_t{num_sms()}
-          ? launch_dkdv<D, CAP, 2>(ar, tq, tdo, tk, tv, s)
-          : launch_dkdv<D, CAP, 1>(ar, tq, tdo, tk, tv, s);
+  e = launch_overlapping(spans_dkdv_kernel<D, CAP>, ar.key_tiles * ar.parts, kThreads,
+                         KvCfg<D>::SMEM, s, tq, tdo, tk, tv, ar);
   if (e != cudaSuccess) return e;
-  return launch_overlapping(
-      spans_dq_kernel<D, CAP>,
-      std::min<int64_t>(static_cast<int64_t>(ar.tl.tiles) * a.nkv, num_sms()), kThreads,
-      QCfg<D>::SMEM, s, tq, tdo, tk, tv, ar);
+  return launch_overlapping(spans_dq_kernel<D, CAP>, static_cast<int64_t>(ar.tl.tiles) * a.nkv,
+                            kThreads, QCfg<D>::SMEM, s, tq, tdo, tk, tv, ar);
 }
 
-// The workspace: rows' values, spans of rows, of tiles, of groups.
-size_t lay_out(Args* ar, int queries, int rep, int nkv, void* ws) {
+// Key tiles are halved where there are fewer than this times the SMs.
+constexpr int kHalvedBelow = 3;
+
+// The workspace: rows' values, spans of rows, of tiles, of groups; halves' sums.
+size_t lay_out(Args* ar, int queries, int keys, int rep, int nkv, int d, void* ws) {
   ar->tl = Tiling::of(queries, rep);
+  ar->key_tiles = static_cast<int64_t>((keys + 127) / 128) * nkv;
+  // a second half needs row tiles enough to share
+  ar->parts = ar->tl.tiles >= kShareFrom && ar->key_tiles < kHalvedBelow * int64_t{num_sms()} ? 2 : 1;
   ar->groups = (ar->tl.tiles + kGroup - 1) / kGroup;
   const size_t rows = static_cast<size_t>(ar->tl.tiles) * 128;
   uint8_t* p = static_cast<uint8_t*>(ws);
@@ -1013,20 +1150,24 @@ size_t lay_out(Args* ar, int queries, int rep, int nkv, void* ws) {
   ar->len = reinterpret_cast<int*>(take(rows * sizeof(int)));
   ar->tiles = reinterpret_cast<TileSpan*>(take(ar->tl.tiles * sizeof(TileSpan)));
   ar->group = reinterpret_cast<int2*>(take(ar->groups * sizeof(int2)));
+  if (ar->parts > 1) {
+    ar->part = reinterpret_cast<float4*>(take(ar->key_tiles * 4 * 128 * d * sizeof(float)));
+    ar->arrived = reinterpret_cast<int*>(take(ar->key_tiles * sizeof(int)));
+  }
   return at;
 }
 
 }  // namespace
 
-size_t backward_workspace(int queries, int nh, int nkv) {
+size_t backward_workspace(int queries, int keys, int nh, int nkv, int d) {
   Args ar = {};
-  return lay_out(&ar, queries, nh / nkv, nkv, nullptr);
+  return lay_out(&ar, queries, keys, nh / nkv, nkv, d, nullptr);
 }
 
 cudaError_t backward_tiles(const SpanArgs& a, void* ws, cudaStream_t s) {
   Args ar = {};
   ar.a = a;
-  lay_out(&ar, a.queries, a.rep, a.nkv, ws);
+  lay_out(&ar, a.queries, a.keys, a.rep, a.nkv, a.d, ws);
   ar.cap = cap_of(a.scale, a.cap);
   ar.scale_log2 = (a.cap > 0.f ? a.cap : a.scale) * kLog2e;
   ar.err = device_error_ptr();

@@ -160,7 +160,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           break;
         }
-        if (lane == 0) next_cta_request(sbase + C::OFF_NEXT, next);
         int t0, g, split;
         place(item, t0, g, split);
         int lo[2], hi[2];
@@ -217,6 +216,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           jg += d.n;
           ++loaded;
         }
+        // asked for now, not before: an item that waits here could have been another SM's
+        if (lane == 0) next_cta_request(sbase + C::OFF_NEXT, next);
         // waited for on the way out too: the answer is written to this CTA's memory
         const bool answered = warp_wait(next, it & 1, err);
         ok = ok && answered;
