@@ -261,13 +261,14 @@ __device__ __forceinline__ bool beyond(const uint32_t (&sv)[N], float limit, flo
   top = fmaxf(hi[0], hi[1]);
   return __any_sync(0xffffffffu, fmaxf(top, -fminf(lo[0], lo[1])) > limit);
 }
+// sv = c tanh(w sv), any sv.
 template <int N>
-__device__ __forceinline__ void tanh_far(uint32_t (&sv)[N], float w) {
+__device__ __forceinline__ void tanh_far(uint32_t (&sv)[N], float w, float c) {
   const float k = 2.f * 1.4426950408889634f * w;
 #pragma unroll
-  for (int c = 0; c < N; ++c)
-    sv[c] = __float_as_uint(
-        fmaf(-2.f, rcp_approx(1.f + ex2_approx(__uint_as_float(sv[c]) * k)), 1.f));
+  for (int i = 0; i < N; ++i)
+    sv[i] = __float_as_uint(
+        fmaf(-2.f * c, rcp_approx(1.f + ex2_approx(__uint_as_float(sv[i]) * k)), c));
 }
 // t0 + t1 s^2 + .. of two scores.
 __device__ __forceinline__ float2 odd_factor(float2 s, const float (&t)[3]) {

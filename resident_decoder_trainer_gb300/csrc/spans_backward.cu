@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_cons
 __device__ __forceinline__ void tanh_all(uint32_t (&sv)[32], const Cap& cap) {
   float top;
   if (beyond(sv, cap.limit, top)) {
-    tanh_far(sv, cap.w);
+    tanh_far(sv, cap.w, 1.f);
     return;
   }
 #pragma unroll
@@ -1028,7 +1028,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = warp_wait(s_full, jj & 1, err);
         if (!ok) break;
         tc_fence_after();
-        uint32_t sv[32], dp[32], pk[16];
+        uint32_t sv[32], dp[32];
         tmem_ld32(tmem + lane_base + C::T_S + block * 32, sv);
         tmem_ld32(tmem + lane_base + C::T_DP + block * 32, dp);
         tmem_ld_wait();
@@ -1047,8 +1047,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (CAP) p = mul2(p, slope);
           float2 ds = add2(make_float2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])), nd2);
           ds = mul2(ds, p);
-          pk[c / 2] = pack_bf16x2(ds.x, ds.y);
+          sv[c / 2] = pack_bf16x2(ds.x, ds.y);  // over what has been used
         }
+        uint32_t(&pk)[16] = *reinterpret_cast<uint32_t(*)[16]>(&sv[0]);
         if (!full) clear_unseen(pk, seen);
         // this buffer was last read by dQ += dS K two key tiles ago
         ok = warp_wait(ds_free + 8 * buf, ((jj >> 1) & 1) ^ 1, err);

@@ -397,10 +397,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int base = first + j * BN;
         const int l = lo - base, r = hi - base;
         const bool masked = __any_sync(0xffffffffu, l > 0 || r < BN);
+        // With a cap, scores become what is exponentiated, in base 2, here; without,
+        // the factor to base 2 goes into the exponentials.
         float mx = 0.f;
-        const bool poly = CAP && !beyond(sv, ar.cap.limit, mx);
-        if (CAP && !poly) tanh_far(sv, ar.cap.w);
-        if (masked && !poly) {
+        bool known = false;  // mx
+        if constexpr (CAP) {
+          if (!beyond(sv, ar.cap.limit, mx)) {
+            known = !masked;
+            mx *= odd_factor(both(mx), ar.cap.z).x;  // the cap rises with the score
+#pragma unroll
+            for (int c = 0; c < 128; c += 2) {
+              const float2 s = make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+              const float2 z = mul2(s, odd_factor(s, ar.cap.z));
+              sv[c] = __float_as_uint(z.x);
+              sv[c + 1] = __float_as_uint(z.y);
+            }
+          } else {
+            tanh_far(sv, ar.cap.w, ar.scale_log2);
+          }
+        }
+        if (masked) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const uint32_t seen = bits_between(l - 32 * q, r - 32 * q);
@@ -410,29 +426,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!(seen & (1u << c))) sv[32 * q + c] = __float_as_uint(-INFINITY);
           }
         }
-        if (!poly || masked) {
+        if (!known) {
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          if (poly) {  // -inf has no polynomial: p is cleared below
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t seen = bits_between(l - 32 * q, r - 32 * q);
-#pragma unroll
-              for (int c = 0; c < 32; ++c)
-                m4[c & 3] = fmaxf(m4[c & 3], seen & (1u << c) ? __uint_as_float(sv[32 * q + c])
-                                                              : -INFINITY);
-            }
-          } else {
-#pragma unroll
-            for (int c = 0; c < 128; c += 2)
-              m4[(c >> 1) & 3] =
-                  max3(m4[(c >> 1) & 3], __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
-          }
+          for (int c = 0; c < 128; c += 2)
+            m4[(c >> 1) & 3] =
+                max3(m4[(c >> 1) & 3], __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
           mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
+          if constexpr (!CAP) mx *= ar.scale_log2;
         }
-        if (!poly)
-          mx *= ar.scale_log2;
-        else if (mx != -INFINITY)
-          mx *= odd_factor(both(mx), ar.cap.z).x;  // the cap rises with the score
         float alpha = 1.f;
         if (mx > m_run + kRescaleLog2) {
           alpha = m_run == -INFINITY ? 1.f : ex2_approx(m_run - mx);  // nothing summed: as it is
@@ -460,43 +462,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float nm = m_run == -INFINITY ? 0.f : -m_run;
         const float2 nm2 = make_float2(nm, nm);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        auto exps = [&](auto by_poly, auto clear) {
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t seen = 0;
+        for (int half = 0; half < 2; ++half) {
 #pragma unroll
-            for (int c = 64 * half; c < 64 * half + 64; c += 2) {
-              if (decltype(clear)::value && (c & 31) == 0) seen = bits_between(l - c, r - c);
-              float2 p = make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
-              if constexpr (decltype(by_poly)::value)
-                p = fma2(p, odd_factor(p, ar.cap.z), nm2);
-              else
-                p = fma2(p, sc2, nm2);
-              p.x = ex2_approx(p.x);
-              p.y = ex2_approx(p.y);
-              if constexpr (decltype(clear)::value) {
-                if (!(seen & (1u << (c & 31)))) p.x = 0.f;
-                if (!(seen & (2u << (c & 31)))) p.y = 0.f;
-              }
-              sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], p);
-              sv[c / 2] = pack_bf16x2(p.x, p.y);
-            }
-            // 64 keys as 32 bf16 pairs
-            tmem_st32(tp + 32 * half, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * half]));
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive(p_full + 16 * x + 8 * half);
+          for (int c = 64 * half; c < 64 * half + 64; c += 2) {
+            float2 p = make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+            p = CAP ? add2(p, nm2) : fma2(p, sc2, nm2);
+            p.x = ex2_approx(p.x);
+            p.y = ex2_approx(p.y);
+            sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], p);
+            sv[c / 2] = pack_bf16x2(p.x, p.y);
           }
-        };
-        if constexpr (CAP) {
-          if (!poly)
-            exps(std::false_type{}, std::false_type{});
-          else if (masked)
-            exps(std::true_type{}, std::true_type{});
-          else
-            exps(std::true_type{}, std::false_type{});
-        } else {
-          exps(std::false_type{}, std::false_type{});
+          // 64 keys as 32 bf16 pairs
+          tmem_st32(tp + 32 * half, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * half]));
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(p_full + 16 * x + 8 * half);
         }
         const float2 two = add2(sum[0], sum[1]);
         l_run = l_run * alpha + (two.x + two.y);
