@@ -247,20 +247,19 @@ inline Cap cap_of(float scale, float cap) {
   return x;
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
-// The greatest of a row's scores, and whether some lane of the warp has one
-// beyond the polynomial's range.
-template <int N>
-__device__ __forceinline__ bool beyond(const uint32_t (&sv)[N], float limit, float& top) {
+// How far a row's scores reach.
+struct Reach {
   float hi[2] = {-INFINITY, -INFINITY}, lo[2] = {INFINITY, INFINITY};
-#pragma unroll
-  for (int c = 0; c < N; c += 2) {
-    const int e = (c >> 1) & 1;
-    hi[e] = max3(hi[e], __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
-    lo[e] = min3(lo[e], __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+  __device__ __forceinline__ void take(float2 s, int e) {
+    hi[e] = max3(hi[e], s.x, s.y);
+    lo[e] = min3(lo[e], s.x, s.y);
   }
-  top = fmaxf(hi[0], hi[1]);
-  return __any_sync(0xffffffffu, fmaxf(top, -fminf(lo[0], lo[1])) > limit);
-}
+  __device__ __forceinline__ float top() const { return fmaxf(hi[0], hi[1]); }
+  // Whether some lane of the warp has a score beyond the polynomial's range.
+  __device__ __forceinline__ bool beyond(float limit) const {
+    return __any_sync(0xffffffffu, fmaxf(top(), -fminf(lo[0], lo[1])) > limit);
+  }
+};
 // sv = c tanh(w sv), any sv.
 template <int N>
 __device__ __forceinline__ void tanh_far(uint32_t (&sv)[N], float w, float c) {

@@ -186,8 +186,11 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_cons
 // ------------------------------------------------------------ elementwise
 // Scores to the tanh of their cap.
 __device__ __forceinline__ void tanh_all(uint32_t (&sv)[32], const Cap& cap) {
-  float top;
-  if (beyond(sv, cap.limit, top)) {
+  Reach reach;
+#pragma unroll
+  for (int c = 0; c < 32; c += 2)
+    reach.take(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), (c >> 1) & 1);
+  if (reach.beyond(cap.limit)) {
     tanh_far(sv, cap.w, 1.f);
     return;
   }

@@ -389,10 +389,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 4; ++c)
           tmem_ld32(ts + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * c]));
         tmem_ld_wait();
-        if constexpr (C::APART) {
-          tc_fence_before();
-          mbar_arrive(s_free + 8 * x);
-        }
         // columns l <= c < r are seen by this row
         const int base = first + j * BN;
         const int l = lo - base, r = hi - base;
@@ -402,19 +398,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         float mx = 0.f;
         bool known = false;  // mx
         if constexpr (CAP) {
-          if (!beyond(sv, ar.cap.limit, mx)) {
-            known = !masked;
-            mx *= odd_factor(both(mx), ar.cap.z).x;  // the cap rises with the score
+          // the polynomial, and beside it whether it holds; else the scores are read again
+          Reach reach;
 #pragma unroll
-            for (int c = 0; c < 128; c += 2) {
-              const float2 s = make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
-              const float2 z = mul2(s, odd_factor(s, ar.cap.z));
-              sv[c] = __float_as_uint(z.x);
-              sv[c + 1] = __float_as_uint(z.y);
-            }
+          for (int c = 0; c < 128; c += 2) {
+            const float2 s = make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+            reach.take(s, (c >> 1) & 1);
+            const float2 z = mul2(s, odd_factor(s, ar.cap.z));
+            sv[c] = __float_as_uint(z.x);
+            sv[c + 1] = __float_as_uint(z.y);
+          }
+          if (!reach.beyond(ar.cap.limit)) {
+            known = !masked;
+            mx = reach.top();
+            mx *= odd_factor(both(mx), ar.cap.z).x;  // the cap rises with the score
           } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              tmem_ld32(ts + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * c]));
+            tmem_ld_wait();
             tanh_far(sv, ar.cap.w, ar.scale_log2);
           }
+        }
+        if constexpr (C::APART) {
+          tc_fence_before();
+          mbar_arrive(s_free + 8 * x);
         }
         if (masked) {
 #pragma unroll
