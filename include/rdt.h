@@ -607,7 +607,9 @@ rdt_status rdt_qk_norm_rope_backward(int32_t tokens, int32_t n_heads, int32_t n_
  * batch, packed documents, a prompt that is seen whole, a sliding window, or
  * new tokens against a cache: any mask in which a query sees a run of keys.
  * lo and hi int32 [queries], device memory; lo null: 0, hi null: keys.
- * What a query does not see does not reach its results, whatever it holds.
+ * What a query does not see does not reach its results, whatever it holds
+ * (nor a key's gradients what does not see it, unless a query that does is not
+ * finite itself).
  * The cost goes by the keys between the least lo and the largest hi of
  * neighbouring queries, so queries of one document belong together.
  *

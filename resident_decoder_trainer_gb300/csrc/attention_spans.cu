@@ -38,8 +38,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_backward_kernel(const SpanAr
       row_dq(a, static_cast<int>(r / a.nh), static_cast<int>(r % a.nh), 0, a.d);
     } else {
       const int64_t x = r - dq_rows;
-      row_dkdv(a, static_cast<int>(x / a.nkv), static_cast<int>(x % a.nkv), 0, a.d,
-               true, true);
+      row_dkdv(a, static_cast<int>(x / a.nkv), static_cast<int>(x % a.nkv), 0, a.d);
     }
   }
 }

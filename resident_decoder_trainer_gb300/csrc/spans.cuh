@@ -138,9 +138,8 @@ __device__ __noinline__ static void row_dq(const SpanArgs& a, int t, int h, int 
   put_row(a.dq.at(t, h), acc, a.scale, c0, c1);
 }
 
-// dk and dv of key j, kv head g, or one of them.
-__device__ __noinline__ static void row_dkdv(const SpanArgs& a, int j, int g, int c0, int c1,
-                                             bool put_dk, bool put_dv) {
+// dk and dv of key j, kv head g.
+__device__ __noinline__ static void row_dkdv(const SpanArgs& a, int j, int g, int c0, int c1) {
   const int lane = threadIdx.x & 31;
   float ak[4] = {}, av[4] = {};
   for (int64_t base = 0; base < a.queries; base += 32) {
@@ -171,8 +170,8 @@ __device__ __noinline__ static void row_dkdv(const SpanArgs& a, int j, int g, in
       }
     }
   }
-  if (put_dk) put_row(a.dk.at(j, g), ak, a.scale, c0, c1);
-  if (put_dv) put_row(a.dv.at(j, g), av, 1.f, c0, c1);
+  put_row(a.dk.at(j, g), ak, a.scale, c0, c1);
+  put_row(a.dv.at(j, g), av, 1.f, c0, c1);
 }
 
 // ------------------------------------------------- tiles of the tensor-core kernels
@@ -250,9 +249,10 @@ __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 // How far a row's scores reach.
 struct Reach {
   float hi[2] = {-INFINITY, -INFINITY}, lo[2] = {INFINITY, INFINITY};
+  template <bool DOWN>
   __device__ __forceinline__ void take(float2 s, int e) {
     hi[e] = max3(hi[e], s.x, s.y);
-    lo[e] = min3(lo[e], s.x, s.y);
+    if (DOWN) lo[e] = min3(lo[e], s.x, s.y);
   }
   __device__ __forceinline__ float top() const { return fmaxf(hi[0], hi[1]); }
   // Whether some lane of the warp has a score beyond the polynomial's range.
@@ -260,14 +260,10 @@ struct Reach {
     return __any_sync(0xffffffffu, fmaxf(top(), -fminf(lo[0], lo[1])) > limit);
   }
 };
-// sv = c tanh(w sv), any sv.
-template <int N>
-__device__ __forceinline__ void tanh_far(uint32_t (&sv)[N], float w, float c) {
-  const float k = 2.f * 1.4426950408889634f * w;
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    sv[i] = __float_as_uint(
-        fmaf(-2.f * c, rcp_approx(1.f + ex2_approx(__uint_as_float(sv[i]) * k)), c));
+// c tanh(w s), any s.
+__device__ __forceinline__ float tanh_far(float s, float w, float c) {
+  const float e = ex2_approx(s * (2.f * 1.4426950408889634f * w));
+  return fmaf(-2.f * c, rcp_approx(1.f + e), c);
 }
 // t0 + t1 s^2 + .. of two scores.
 __device__ __forceinline__ float2 odd_factor(float2 s, const float (&t)[3]) {

@@ -15,7 +15,9 @@
 //
 // Rows of dq, dk and dv that are not finite are computed again one by one
 // (row_dq, row_dkdv): a NaN or infinity where a query does not see a key, times
-// 0, would reach them.
+// 0, would reach them. Not where they see a query whose own values are not
+// finite: what they hold is not finite by right, and a batch that has diverged
+// throughout costs no more than another.
 #include <algorithm>
 
 #include "spans.cuh"
@@ -189,9 +191,11 @@ __device__ __forceinline__ void tanh_all(uint32_t (&sv)[32], const Cap& cap) {
   Reach reach;
 #pragma unroll
   for (int c = 0; c < 32; c += 2)
-    reach.take(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), (c >> 1) & 1);
+    reach.take<true>(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), (c >> 1) & 1);
   if (reach.beyond(cap.limit)) {
-    tanh_far(sv, cap.w, 1.f);
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+      sv[c] = __float_as_uint(tanh_far(__uint_as_float(sv[c]), cap.w, 1.f));
     return;
   }
 #pragma unroll
@@ -247,6 +251,30 @@ __device__ __forceinline__ bool all_finite(const uint32_t (&r)[32], int left) {
   for (int e = 0; e < 32; ++e)
     if (e < left) bad = fmaf(__uint_as_float(r[e]), 0.f, bad);
   return bad == 0.f;
+}
+
+__device__ __forceinline__ bool finite_row(float neg_lse, float neg_d) {
+  return fabsf(neg_lse) < INFINITY && fabsf(neg_d) < INFINITY;
+}
+
+// Whether some query that sees key j has a row (of key head g's) that is not finite. Whole warp.
+__device__ __noinline__ bool sees_nonfinite(const Args& ar, int j, int g) {
+  const SpanArgs& a = ar.a;
+  for (int64_t base = 0; base < a.queries; base += 32) {
+    const int64_t t = base + (threadIdx.x & 31);
+    bool bad = false;
+    if (t < a.queries) {
+      int first, end;
+      a.span(static_cast<int>(t), first, end);
+      if (first <= j && j < end) {
+        const int tile = static_cast<int>(t / ar.tl.per), in = static_cast<int>(t % ar.tl.per);
+        const int64_t at = (static_cast<int64_t>(g) * ar.tl.tiles + tile) * 128 + in * a.rep;
+        for (int r = 0; r < a.rep; ++r) bad |= !finite_row(ar.neg_lse[at + r], ar.neg_d[at + r]);
+      }
+    }
+    if (__any_sync(0xffffffffu, bad)) return true;
+  }
+  return false;
 }
 
 __device__ __forceinline__ void settle(int* err) {
@@ -751,8 +779,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         had = false;
       }
       for (unsigned again = __ballot_sync(0xffffffffu, !fine && key < a.keys); again;
-           again &= again - 1)
-        row_dkdv(a, m.n0 + quarter * 32 + __ffs(again) - 1, m.g, c0, min(c0 + 32, a.d), true, true);
+           again &= again - 1) {
+        const int j = m.n0 + quarter * 32 + __ffs(again) - 1;
+        if (!sees_nonfinite(ar, j, m.g)) row_dkdv(a, j, m.g, c0, min(c0 + 32, a.d));
+      }
     }
   }
 
@@ -1025,6 +1055,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(q_empty);
       }
       const float2 nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
+      const bool finite = finite_row(nl, nd);
       for (int j = 0; j < n; ++j) {
         const uint32_t jj = jg + j;
         const int buf = jj & 1;
@@ -1087,7 +1118,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int h = again_of % a.nkv * a.rep + row_h;
         const bool real = row_t < ar.tl.per && t < a.queries;
         if (real) put_columns(a.dq.at(t, h) + c0, r, a.scale, left, ar.wide_dq);
-        for (unsigned again = __ballot_sync(0xffffffffu, real && !all_finite(r, left)); again;
+        for (unsigned again = __ballot_sync(0xffffffffu, real && finite && !all_finite(r, left)); again;
              again &= again - 1) {
           const int from = __ffs(again) - 1;
           row_dq(a, __shfl_sync(0xffffffffu, t, from), __shfl_sync(0xffffffffu, h, from), c0,

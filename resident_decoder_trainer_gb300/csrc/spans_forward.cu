@@ -17,8 +17,9 @@
 // are formed. O is rescaled only
 // when a row's maximum grows by more than 2^8.
 //
-// A row whose O is not finite is computed again key by key (row_forward): a NaN
-// or infinity in a value that the row does not see, times p = 0, would reach it.
+// A row whose O is not finite, though its sum is, is computed again key by key
+// (row_forward): a NaN or infinity in a value that the row does not see, times
+// p = 0, would reach it.
 #include <algorithm>
 
 #include "spans.cuh"
@@ -384,65 +385,71 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        uint32_t sv[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          tmem_ld32(ts + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * c]));
-        tmem_ld_wait();
         // columns l <= c < r are seen by this row
         const int base = first + j * BN;
         const int l = lo - base, r = hi - base;
         const bool masked = __any_sync(0xffffffffu, l > 0 || r < BN);
-        // With a cap, scores become what is exponentiated, in base 2, here; without,
-        // the factor to base 2 goes into the exponentials.
-        float mx = 0.f;
-        bool known = false;  // mx
-        if constexpr (CAP) {
-          // the polynomial, and beside it whether it holds; else the scores are read again
+        // -inf where the row does not see 32 columns from q on
+        auto mask = [&](uint32_t (&s)[32], int q) {
+          const uint32_t seen = bits_between(l - 32 * q, r - 32 * q);
+          if (__all_sync(0xffffffffu, seen == ~0u)) return;
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (!(seen & (1u << c))) s[c] = __float_as_uint(-INFINITY);
+        };
+        // The scores are read twice, for their maximum and for the exponentials, the
+        // second time in a loop over halves. Held in registers and unrolled, they spill
+        // 80 bytes and masks and all take 16 KB of instructions: 4096 packed tokens took
+        // 44.5 us and not 42.7 (8192 tokens of a seen prompt, few masked tiles, 386 and
+        // not 404).
+        bool far = false;  // a score beyond the cap's polynomial
+        float mx;
+        if (!masked) {
+          uint32_t sv[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            tmem_ld32(ts + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * c]));
+          tmem_ld_wait();
           Reach reach;
 #pragma unroll
-          for (int c = 0; c < 128; c += 2) {
-            const float2 s = make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
-            reach.take(s, (c >> 1) & 1);
-            const float2 z = mul2(s, odd_factor(s, ar.cap.z));
-            sv[c] = __float_as_uint(z.x);
-            sv[c + 1] = __float_as_uint(z.y);
-          }
-          if (!reach.beyond(ar.cap.limit)) {
-            known = !masked;
-            mx = reach.top();
-            mx *= odd_factor(both(mx), ar.cap.z).x;  // the cap rises with the score
-          } else {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              tmem_ld32(ts + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * c]));
-            tmem_ld_wait();
-            tanh_far(sv, ar.cap.w, ar.scale_log2);
-          }
-        }
-        if constexpr (C::APART) {
-          tc_fence_before();
-          mbar_arrive(s_free + 8 * x);
-        }
-        if (masked) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t seen = bits_between(l - 32 * q, r - 32 * q);
-            if (__all_sync(0xffffffffu, seen == ~0u)) continue;
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (!(seen & (1u << c))) sv[32 * q + c] = __float_as_uint(-INFINITY);
-          }
-        }
-        if (!known) {
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
           for (int c = 0; c < 128; c += 2)
-            m4[(c >> 1) & 3] =
-                max3(m4[(c >> 1) & 3], __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
-          mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
-          if constexpr (!CAP) mx *= ar.scale_log2;
+            reach.take<CAP>(
+                make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), (c >> 1) & 1);
+          mx = reach.top();
+          if constexpr (CAP) far = reach.beyond(ar.cap.limit);
+        } else {
+          Reach all, own;
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            uint32_t sv[32];
+            tmem_ld32(ts + 32 * q, sv);
+            tmem_ld_wait();
+            if constexpr (CAP) {
+#pragma unroll
+              for (int c = 0; c < 32; c += 2)
+                all.take<true>(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])),
+                               (c >> 1) & 1);
+            }
+            mask(sv, q);
+#pragma unroll
+            for (int c = 0; c < 32; c += 2)
+              own.take<false>(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])),
+                              (c >> 1) & 1);
+          }
+          mx = own.top();
+          if constexpr (CAP) far = all.beyond(ar.cap.limit);
         }
+        uint32_t near[2][32];
+        auto fetch = [&](int half) {
+          tmem_ld32(ts + 64 * half, near[0]);
+          tmem_ld32(ts + 64 * half + 32, near[1]);
+        };
+        fetch(0);
+        // what is exponentiated, in base 2, rises with the score
+        if (!CAP)
+          mx *= ar.scale_log2;
+        else if (mx != -INFINITY)
+          mx = far ? tanh_far(mx, ar.cap.w, ar.scale_log2) : mx * odd_factor(both(mx), ar.cap.z).x;
         float alpha = 1.f;
         if (mx > m_run + kRescaleLog2) {
           alpha = m_run == -INFINITY ? 1.f : ex2_approx(m_run - mx);  // nothing summed: as it is
@@ -470,19 +477,55 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float nm = m_run == -INFINITY ? 0.f : -m_run;
         const float2 nm2 = make_float2(nm, nm);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
+#pragma unroll 1
         for (int half = 0; half < 2; ++half) {
-#pragma unroll
-          for (int c = 64 * half; c < 64 * half + 64; c += 2) {
-            float2 p = make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
-            p = CAP ? add2(p, nm2) : fma2(p, sc2, nm2);
-            p.x = ex2_approx(p.x);
-            p.y = ex2_approx(p.y);
-            sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], p);
-            sv[c / 2] = pack_bf16x2(p.x, p.y);
+          uint32_t pk[32];  // 64 keys as bf16 pairs
+          tmem_ld_wait();
+          if (C::APART && half) {
+            tc_fence_before();
+            mbar_arrive(s_free + 8 * x);
           }
-          // 64 keys as 32 bf16 pairs
-          tmem_st32(tp + 32 * half, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * half]));
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t(&s)[32] = near[q];
+            auto exps = [&](auto ready) {
+#pragma unroll
+              for (int c = 0; c < 32; c += 2) {
+                float2 p = make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+                if constexpr (decltype(ready)::value)
+                  p = add2(p, nm2);
+                else
+                  p = fma2(p, CAP ? odd_factor(p, ar.cap.z) : sc2, nm2);
+                p.x = ex2_approx(p.x);
+                p.y = ex2_approx(p.y);
+                sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], p);
+                pk[16 * q + c / 2] = pack_bf16x2(p.x, p.y);
+              }
+            };
+            if (!masked && !far) {
+              exps(std::false_type{});
+              continue;
+            }
+            // to base 2 and masked first
+            if (CAP && far) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                s[c] =
+                    __float_as_uint(tanh_far(__uint_as_float(s[c]), ar.cap.w, ar.scale_log2));
+            } else {
+#pragma unroll
+              for (int c = 0; c < 32; c += 2) {
+                float2 z = make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+                z = mul2(z, CAP ? odd_factor(z, ar.cap.z) : sc2);
+                s[c] = __float_as_uint(z.x);
+                s[c + 1] = __float_as_uint(z.y);
+              }
+            }
+            mask(s, 2 * half + q);
+            exps(std::true_type{});
+          }
+          if (half == 0) fetch(1);
+          tmem_st32(tp + 32 * half, pk);
           tmem_st_wait();
           tc_fence_before();
           mbar_arrive(p_full + 16 * x + 8 * half);
@@ -569,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           a.lse[th] = lse2 * kLn2;
       }
       if (ar.splits == 1) {
-        for (unsigned again = __ballot_sync(0xffffffffu, real && bad != 0.f); again;
+        for (unsigned again = __ballot_sync(0xffffffffu, real && bad != 0.f && l_run == l_run); again;
              again &= again - 1) {
           const int from = __ffs(again) - 1;
           row_forward(a, __shfl_sync(0xffffffffu, t, from),

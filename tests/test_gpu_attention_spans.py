@@ -387,6 +387,97 @@ def test_what_is_not_seen_does_not_count(heads, junk):
     same(got, "q", slice(111, None))
 
 
+@pytest.mark.parametrize("heads", [(4, 2, 16), (4, 1, 128)], ids=str)
+def test_what_is_not_finite_stays_so(heads):
+    """A query that is NaN, a key that all see, a batch that is NaN throughout."""
+    st = problem("documents", heads)  # 1, 2, 130, 17, 255, 95 tokens
+    o, lse = run_forward(st)
+    q = st["q"].clone()
+    q[200] = math.nan  # in the fifth document, tokens 150 to 404
+    bad = dict(st, q=q)
+    o2, lse2 = run_forward(bad)
+    assert o2[200].isnan().all() and lse2[200].isnan().all()
+    keep = torch.arange(len(q), device="cuda") != 200
+    assert o2[keep].isfinite().all() and torch.equal(lse[keep], lse2[keep])
+    got = run_backward(bad, o2, lse2)
+    assert got["q"][200].isnan().all() and got["q"][keep].isfinite().all()
+    seen = torch.zeros(len(q), dtype=torch.bool, device="cuda")
+    seen[150:201] = True  # the keys that query 200 sees
+    for n in ("k", "v"):
+        assert not got[n][seen].isfinite().any() and got[n][~seen].isfinite().all()
+    v = st["v"].clone()
+    v[150] = math.inf  # seen by the whole document
+    o2, _ = run_forward(dict(st, v=v))
+    assert not o2[150:405].isfinite().any()
+    assert o2[:150].isfinite().all() and o2[405:].isfinite().all()
+    nan = dict(st, **{n: torch.full_like(st[n], math.nan) for n in ("q", "k", "v", "d_o")})
+    o2, lse2 = run_forward(nan)
+    assert o2.isnan().all() and lse2.isnan().all()
+    assert all(x.isnan().all() for x in run_backward(nan, o2, lse2).values())
+
+
+@pytest.mark.parametrize("heads", [(128, 1, 16), (71, 1, 32), (100, 2, 64), (33, 3, 112)], ids=str)
+def test_many_query_heads_of_a_key_head(heads):
+    for mask in ("causal 1", "documents of ones", "cache 5", "scattered short"):
+        st = problem(mask, heads)
+        o, lse = run_forward(st)
+        check_forward(st, o, lse)
+        check_backward(st, o, lse, run_backward(st, o, lse))
+
+
+def test_offsets_beyond_32_bits():
+    """A cache whose elements lie up to 2^31 and more apart: results as of its copy."""
+    keys, nkv, d = 33000, 2, 64
+    cache = torch.empty(keys, 1 << 16, device="cuda", dtype=BF16)  # 2.2e9 elements
+    g = torch.Generator(device="cuda").manual_seed(0)
+    k = cache[:, :nkv * d].view(keys, nkv, d)
+    v = cache[:, 4096:4096 + nkv * d].view(keys, nkv, d)
+    for x in (k, v):
+        x.copy_(torch.randn(keys, nkv, d, generator=g, device="cuda"))
+    q = torch.randn(70, 4, d, generator=g, device="cuda").to(BF16)
+    hi = torch.arange(keys - 69, keys + 1, device="cuda", dtype=torch.int32)
+    st = dict(q=q, k=k, v=v, d_o=q.flip(0).contiguous(), d_lse=None, lo=hi - 32900, hi=hi,
+              scale=d ** -0.5, cap=0.0)
+    st["lo"].clamp_(min=0)
+    copy = dict(st, k=k.contiguous(), v=v.contiguous())
+    o, lse = run_forward(st)
+    o2, lse2 = run_forward(copy)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    check_forward(copy, o, lse)
+    a, b = (run_backward(x, o, lse, d_lse=False) for x in (st, copy))
+    assert all(torch.equal(a[n], b[n]) for n in a)
+
+
+def test_far_past_the_cap():
+    """Scores past the cap's polynomial in some tiles and rows only."""
+    st = dict(problem("causal 257", (4, 2, 64), seed=9), cap=3.0)
+    st["q"][130:140] *= 30
+    st["k"][200] *= 40
+    o, lse = run_forward(st)
+    check_forward(st, o, lse)
+    check_backward(st, o, lse, run_backward(st, o, lse))
+
+
+def test_two_calls_at_once():
+    """On two streams, each with its own workspace."""
+    sts = [problem("documents", (8, 2, 128), seed=s) for s in range(2)]
+    want = [run_forward(st) for st in sts]
+    grads = [run_backward(st, *w) for st, w in zip(sts, want)]
+    streams = [torch.cuda.Stream() for _ in sts]
+    for _ in range(5):
+        got = []
+        for st, s in zip(sts, streams):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                o, lse = run_forward(st)
+                got.append((o, lse, run_backward(st, o, lse)))
+        for s in streams:
+            torch.cuda.current_stream().wait_stream(s)
+        for (o, lse, g), w, wg in zip(got, want, grads):
+            assert torch.equal(o, w[0]) and torch.equal(lse, w[1])
+            assert all(torch.equal(g[n], wg[n]) for n in g)
+
+
 def test_rows_around_are_left():
     st = problem("padded", (8, 2, 64))
     t, nh, d = st["q"].shape
