@@ -82,8 +82,10 @@ View view_of(const rdt_heads* x) {
 const char* common_problem(const SpanArgs& a, const void* ws, size_t ws_bytes, size_t need) {
   if (!aligned4(a.lo) || !aligned4(a.hi) || !aligned4(a.lse) || !aligned4(a.d_lse))
     return "lo, hi and lse must be 4-byte aligned";
-  if (!(a.scale > 0.f) || std::isinf(a.scale)) return "scale must be finite and > 0";
-  if (!(a.cap >= 0.f) || std::isinf(a.cap)) return "softcap must be finite and >= 0";
+  // quotient, product and the cap's powers of them stay finite and normal
+  if (!(a.scale >= 1e-6f && a.scale <= 1e6f)) return "scale must be in [1e-6, 1e6]";
+  if (a.cap != 0.f && !(a.cap >= 1e-6f && a.cap <= 1e6f))
+    return "softcap must be 0 or in [1e-6, 1e6]";
   if (need) {
     if (!ws) return "null pointer";
     if (reinterpret_cast<uintptr_t>(ws) & 255) return "ws must be 256-byte aligned";

@@ -342,11 +342,6 @@ __device__ __forceinline__ float min3(float a, float b, float c) {
   asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-__device__ __forceinline__ float rcp_approx(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // Work of a grid with one CTA per item, taken by the CTAs that run: asks for the
 // index of a CTA that has not started yet, which then never does. 16 bytes at
 // `dst` (16-byte aligned), completion on an mbarrier.

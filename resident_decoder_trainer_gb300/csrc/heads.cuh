@@ -1,12 +1,10 @@
 // What the per-head norm with rotation and the attention over spans share:
-// the checks of a [tokens, heads, head_dim] tensor, launches that overlap, and
-// eight values of any of the three types.
+// the checks of a [tokens, heads, head_dim] tensor and launches that overlap.
 #pragma once
 
 #include <cuda_fp16.h>
 
 #include <atomic>
-#include <type_traits>
 
 #include "../../include/rdt.h"
 #include "common.cuh"
@@ -92,40 +90,5 @@ inline const char* heads_problem(const rdt_heads* x, int64_t tokens, int64_t hea
   }
   return nullptr;
 }
-
-// Eight consecutive values, as loaded: 16 bytes of a 16-bit type, 32 of fp32.
-template <typename T>
-struct Eight {
-  uint4 a;
-  __device__ __forceinline__ void load(const T* p) { a = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (sizeof(T) == 2 && !std::is_same<T, __half>::value) {
-        x[2 * i] = bf16lo(w[i]);
-        x[2 * i + 1] = bf16hi(w[i]);
-      } else {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
-      }
-    }
-  }
-};
-template <>
-struct Eight<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
-  }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  }
-};
 
 }  // namespace rdt

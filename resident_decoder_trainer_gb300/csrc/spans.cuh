@@ -1,6 +1,7 @@
 // Attention over spans of keys: what its files share. The arguments of a call,
-// and the computation of one output row by one warp, in fp32: the variant of
-// small problems, and what repairs rows of the tensor-core kernels.
+// and the computation of one output row by one warp, in fp32: what fills rows
+// where there are no queries or no keys, and what repairs rows of the tensor-core
+// kernels that are not finite.
 #pragma once
 
 #include "heads.cuh"
@@ -32,11 +33,25 @@ constexpr int kMaxDim = 128;  // of a head
 // Lanes take 32 keys (or queries) at a time for the scores, and four columns
 // each for the sums. All in fp32. Columns [c0, c1) are written.
 
+// Eight consecutive values, as loaded.
+struct Eight {
+  uint4 a;
+  __device__ __forceinline__ void load(const bf16* p) { a = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = bf16lo(w[i]);
+      x[2 * i + 1] = bf16hi(w[i]);
+    }
+  }
+};
+
 __device__ __forceinline__ float dot_rows(const bf16* a, const bf16* b, int d) {
   float s0 = 0.f, s1 = 0.f;
 #pragma unroll 4
   for (int c = 0; c < d; c += 8) {
-    Eight<bf16> e, f;
+    Eight e, f;
     float x[8], y[8];
     e.load(a + c);
     f.load(b + c);
@@ -220,26 +235,26 @@ __device__ __forceinline__ void spans_of_tiles(const SpanArgs& a, const Tiling& 
 }
 
 // The cap cap tanh(s scale / cap), in base 2 where scores are exponentiated.
-// Arguments of tanh within 0.3 (scores below 0.3 of the cap, nearly all in use)
-// go through an odd polynomial (least squares on [0, 0.3], reweighted towards
-// the least greatest error: 2^-22.5), whose coefficients take up the scale;
-// others through 1 - 2 / (1 + e^2x), off by 2^-22, which takes twice the
-// special-function unit, that the exponentials need.
+// Arguments of tanh within 0.35 (scores below 0.35 of the cap, nearly all in use)
+// go through an odd polynomial (least squares on [0, 0.35], reweighted towards
+// the least greatest error: 2^-27.3; with one term less, 2^-22 of a cap of 50
+// showed in the log-sum-exp), whose coefficients take up the scale; others
+// through the library's tanh.
 struct Cap {
   float limit;    // scores beyond it: not the polynomial
   float w;        // scale / cap
-  float t[3];     // tanh(w s) = s (t0 + t1 s^2 + t2 s^4)
-  float z[3];     // cap log2 e tanh(w s), alike
+  float t[4];     // tanh(w s) = s (t0 + t1 s^2 + ..)
+  float z[4];     // cap log2 e tanh(w s), alike
 };
 inline Cap cap_of(float scale, float cap) {
-  constexpr double c[3] = {0.99999601, -0.3329748, 0.12522591};
+  constexpr double c[4] = {0.999999848, -0.33331657, 0.132833236, -0.0483769203};
   Cap x = {};
   if (!(cap > 0.f)) return x;
   const double w = static_cast<double>(scale) / cap;
   x.w = static_cast<float>(w);
-  x.limit = w > 1e-4 && w < 1e4 ? static_cast<float>(0.3 / w) : -1.f;  // powers stay in range
+  x.limit = w > 1e-4 && w < 1e4 ? static_cast<float>(0.35 / w) : -1.f;  // powers stay in range
   double p = w;
-  for (int i = 0; i < 3; ++i, p *= w * w) {
+  for (int i = 0; i < 4; ++i, p *= w * w) {
     x.t[i] = static_cast<float>(c[i] * p);
     x.z[i] = static_cast<float>(cap * 1.4426950408889634 * c[i] * p);
   }
@@ -260,15 +275,11 @@ struct Reach {
     return __any_sync(0xffffffffu, fmaxf(top(), -fminf(lo[0], lo[1])) > limit);
   }
 };
-// c tanh(w s), any s.
-__device__ __forceinline__ float tanh_far(float s, float w, float c) {
-  const float e = ex2_approx(s * (2.f * 1.4426950408889634f * w));
-  return fmaf(-2.f * c, rcp_approx(1.f + e), c);
-}
 // t0 + t1 s^2 + .. of two scores.
-__device__ __forceinline__ float2 odd_factor(float2 s, const float (&t)[3]) {
+__device__ __forceinline__ float2 odd_factor(float2 s, const float (&t)[4]) {
   const float2 y = mul2(s, s);
-  const float2 p = fma2(y, both(t[2]), both(t[1]));
+  float2 p = fma2(y, both(t[3]), both(t[2]));
+  p = fma2(p, y, both(t[1]));
   return fma2(p, y, both(t[0]));
 }
 

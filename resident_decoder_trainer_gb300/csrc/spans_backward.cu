@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_cons
       const int in = static_cast<int>(row * inv_rep >> 16), t = tile * ar.tl.per + in;
       const int h = g * a.rep + row - in * a.rep;
       if (in < ar.tl.per && t < a.queries && c < a.d) {
-        Eight<bf16> x, y;
+        Eight x, y;
         float u[8], v[8];
         x.load(a.d_o.at(t, h) + c);
         y.load(a.o.at(t, h) + c);
@@ -195,7 +195,7 @@ __device__ __forceinline__ void tanh_all(uint32_t (&sv)[32], const Cap& cap) {
   if (reach.beyond(cap.limit)) {
 #pragma unroll
     for (int c = 0; c < 32; ++c)
-      sv[c] = __float_as_uint(tanh_far(__uint_as_float(sv[c]), cap.w, 1.f));
+      sv[c] = __float_as_uint(tanhf(cap.w * __uint_as_float(sv[c])));
     return;
   }
 #pragma unroll

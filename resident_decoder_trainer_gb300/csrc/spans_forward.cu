@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!CAP)
           mx *= ar.scale_log2;
         else if (mx != -INFINITY)
-          mx = far ? tanh_far(mx, ar.cap.w, ar.scale_log2) : mx * odd_factor(both(mx), ar.cap.z).x;
+          mx = far ? ar.scale_log2 * tanhf(ar.cap.w * mx) : mx * odd_factor(both(mx), ar.cap.z).x;
         float alpha = 1.f;
         if (mx > m_run + kRescaleLog2) {
           alpha = m_run == -INFINITY ? 1.f : ex2_approx(m_run - mx);  // nothing summed: as it is
@@ -510,8 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (CAP && far) {
 #pragma unroll
               for (int c = 0; c < 32; ++c)
-                s[c] =
-                    __float_as_uint(tanh_far(__uint_as_float(s[c]), ar.cap.w, ar.scale_log2));
+                s[c] = __float_as_uint(ar.scale_log2 * tanhf(ar.cap.w * __uint_as_float(s[c])));
             } else {
 #pragma unroll
               for (int c = 0; c < 32; c += 2) {

@@ -458,6 +458,28 @@ def test_far_past_the_cap():
     check_backward(st, o, lse, run_backward(st, o, lse))
 
 
+@pytest.mark.parametrize("cap,scale", [(1e6, 0.125), (1e-6, 1e-6), (1e-6, 1.0), (1e-6, 1e6),
+                                       (0.0, 1e-6), (20.0, 1e-6)])
+def test_caps_and_scales_at_the_ends_of_their_range(cap, scale):
+    """A cap far above every score caps nothing: held to the formula without one. Where scores
+    pass the cap by more than 2^15, a score's own error (2^-21 of its size and more) moves
+    score / cap by more than the whole width of the slope 1 - tanh^2, so that no figure of a
+    gradient of q or k is left to hold it to: those only have to be finite."""
+    st = dict(problem("documents", (4, 2, 64), seed=12), cap=cap, scale=scale)
+    st["q"][7] = 0
+    o, lse = run_forward(st)
+    got = run_backward(st, o, lse)
+    if cap == 1e6:
+        st["cap"] = 0.0
+    check_forward(st, o, lse)
+    if cap and scale / cap > 2.0 ** 15:
+        assert all(x.isfinite().all() for x in got.values())
+        want, bound = backward_exact(st, o, lse)
+        within(got["v"], want["v"], bound["v"], "dv")
+    else:
+        check_backward(st, o, lse, got)
+
+
 def test_two_calls_at_once():
     """On two streams, each with its own workspace."""
     sts = [problem("documents", (8, 2, 128), seed=s) for s in range(2)]
