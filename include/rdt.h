@@ -617,8 +617,8 @@ rdt_status rdt_qk_norm_rope_backward(int32_t tokens, int32_t n_heads, int32_t n_
  * of n_kv_heads, at most 128 times it, at most 4096; queries and keys in
  * [0, 2^30]. n_kv_heads times the groups of floor(128 / (n_heads / n_kv_heads))
  * queries, and times the groups of 128 keys, at most 2^29. scale in
- * [1e-6, 1e6]; softcap 0 (none) or in [1e-6, 1e6]. Scores, softmax and sums are
- * fp32, p is rounded to bf16 for its product with v. lse fp32 [queries,
+ * [1e-6, 1e6]; softcap 0 (none) or scale times [1e-5, 1e5]. Scores, softmax and
+ * sums are fp32, p is rounded to bf16 for its product with v. lse fp32 [queries,
  * n_heads], natural logarithm; may be null. Outputs overlap nothing else. ws:
  * rdt_attention_workspace_bytes(..., 0) bytes, 256-byte aligned (may be 0
  * bytes). Results do not depend on scheduling.

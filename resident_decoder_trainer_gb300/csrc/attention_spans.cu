@@ -82,10 +82,10 @@ View view_of(const rdt_heads* x) {
 const char* common_problem(const SpanArgs& a, const void* ws, size_t ws_bytes, size_t need) {
   if (!aligned4(a.lo) || !aligned4(a.hi) || !aligned4(a.lse) || !aligned4(a.d_lse))
     return "lo, hi and lse must be 4-byte aligned";
-  // quotient, product and the cap's powers of them stay finite and normal
   if (!(a.scale >= 1e-6f && a.scale <= 1e6f)) return "scale must be in [1e-6, 1e6]";
-  if (a.cap != 0.f && !(a.cap >= 1e-6f && a.cap <= 1e6f))
-    return "softcap must be 0 or in [1e-6, 1e6]";
+  // the seventh power of the quotient, in the cap's polynomial, is a normal number
+  if (a.cap != 0.f && !(a.cap >= 1e-5f * a.scale && a.cap <= 1e5f * a.scale))
+    return "softcap must be 0 or scale times [1e-5, 1e5]";
   if (need) {
     if (!ws) return "null pointer";
     if (reinterpret_cast<uintptr_t>(ws) & 255) return "ws must be 256-byte aligned";

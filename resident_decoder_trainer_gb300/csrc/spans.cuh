@@ -252,7 +252,7 @@ inline Cap cap_of(float scale, float cap) {
   if (!(cap > 0.f)) return x;
   const double w = static_cast<double>(scale) / cap;
   x.w = static_cast<float>(w);
-  x.limit = w > 1e-4 && w < 1e4 ? static_cast<float>(0.35 / w) : -1.f;  // powers stay in range
+  x.limit = static_cast<float>(0.35 / w);
   double p = w;
   for (int i = 0; i < 4; ++i, p *= w * w) {
     x.t[i] = static_cast<float>(c[i] * p);

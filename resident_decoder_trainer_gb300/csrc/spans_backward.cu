@@ -194,8 +194,14 @@ __device__ __forceinline__ void tanh_all(uint32_t (&sv)[32], const Cap& cap) {
     reach.take<true>(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), (c >> 1) & 1);
   if (reach.beyond(cap.limit)) {
 #pragma unroll
-    for (int c = 0; c < 32; ++c)
-      sv[c] = __float_as_uint(tanhf(cap.w * __uint_as_float(sv[c])));
+    for (int c = 0; c < 32; ++c) {  // a score by itself decides, not what its warp holds
+      const float s = __uint_as_float(sv[c]);
+      const float near = s * odd_factor(both(s), cap.t).x;
+      // 1 - 2 / (1 + e^2x), off by 2^-23: p and the slope become bf16
+      const float e = ex2_approx(2.f * kLog2e * cap.w * fabsf(s));
+      const float far = copysignf(1.f - __fdividef(2.f, 1.f + e), s);
+      sv[c] = __float_as_uint(fabsf(s) > cap.limit ? far : near);
+    }
     return;
   }
 #pragma unroll

@@ -449,7 +449,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!CAP)
           mx *= ar.scale_log2;
         else if (mx != -INFINITY)
-          mx = far ? ar.scale_log2 * tanhf(ar.cap.w * mx) : mx * odd_factor(both(mx), ar.cap.z).x;
+          mx = far && fabsf(mx) > ar.cap.limit ? ar.scale_log2 * tanhf(ar.cap.w * mx)
+                                               : mx * odd_factor(both(mx), ar.cap.z).x;
         float alpha = 1.f;
         if (mx > m_run + kRescaleLog2) {
           alpha = m_run == -INFINITY ? 1.f : ex2_approx(m_run - mx);  // nothing summed: as it is
@@ -492,9 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int c = 0; c < 32; c += 2) {
                 float2 p = make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-                if constexpr (decltype(ready)::value)
-                  p = add2(p, nm2);
-                else
+                if constexpr (!decltype(ready)::value)
                   p = fma2(p, CAP ? odd_factor(p, ar.cap.z) : sc2, nm2);
                 p.x = ex2_approx(p.x);
                 p.y = ex2_approx(p.y);
@@ -506,16 +505,21 @@ __global__ void __launch_bounds__(kThreads, 1)
               exps(std::false_type{});
               continue;
             }
-            // to base 2 and masked first
+            // to base 2, less the maximum, and masked first
             if (CAP && far) {
 #pragma unroll
-              for (int c = 0; c < 32; ++c)
-                s[c] = __float_as_uint(ar.scale_log2 * tanhf(ar.cap.w * __uint_as_float(s[c])));
+              for (int c = 0; c < 32; ++c) {  // a score by itself decides, not what its warp holds
+                const float u = __uint_as_float(s[c]);
+                const float z = fabsf(u) > ar.cap.limit
+                                    ? fmaf(ar.scale_log2, tanhf(ar.cap.w * u), nm)
+                                    : fmaf(u, odd_factor(both(u), ar.cap.z).x, nm);
+                s[c] = __float_as_uint(z);
+              }
             } else {
 #pragma unroll
               for (int c = 0; c < 32; c += 2) {
-                float2 z = make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-                z = mul2(z, CAP ? odd_factor(z, ar.cap.z) : sc2);
+                const float2 u = make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+                const float2 z = fma2(u, CAP ? odd_factor(u, ar.cap.z) : sc2, nm2);
                 s[c] = __float_as_uint(z.x);
                 s[c + 1] = __float_as_uint(z.y);
               }

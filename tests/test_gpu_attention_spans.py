@@ -458,18 +458,19 @@ def test_far_past_the_cap():
     check_backward(st, o, lse, run_backward(st, o, lse))
 
 
-@pytest.mark.parametrize("cap,scale", [(1e6, 0.125), (1e-6, 1e-6), (1e-6, 1.0), (1e-6, 1e6),
-                                       (0.0, 1e-6), (20.0, 1e-6)])
+@pytest.mark.parametrize("cap,scale", [(12400.0, 0.125), (1e-6, 1e-6), (1.1e-5, 1.0), (11.0, 1e6),
+                                       (0.0, 1e-6), (0.09, 1e-6)])
 def test_caps_and_scales_at_the_ends_of_their_range(cap, scale):
-    """A cap far above every score caps nothing: held to the formula without one. Where scores
-    pass the cap by more than 2^15, a score's own error (2^-21 of its size and more) moves
-    score / cap by more than the whole width of the slope 1 - tanh^2, so that no figure of a
-    gradient of q or k is left to hold it to: those only have to be finite."""
+    """A cap far above every score caps nothing: held to the formula without one (a score of 20
+    loses 20^3 / (3 12400^2) < 2^-15). Where scores pass the cap by more than 2^15, a score's own
+    error (2^-21 of its size and more) moves score / cap by a good part of the slope's width, so
+    that no figure of a gradient of q or k is left to hold it to: those only have to be
+    finite."""
     st = dict(problem("documents", (4, 2, 64), seed=12), cap=cap, scale=scale)
     st["q"][7] = 0
     o, lse = run_forward(st)
     got = run_backward(st, o, lse)
-    if cap == 1e6:
+    if cap > 1e4:
         st["cap"] = 0.0
     check_forward(st, o, lse)
     if cap and scale / cap > 2.0 ** 15:
@@ -478,6 +479,30 @@ def test_caps_and_scales_at_the_ends_of_their_range(cap, scale):
         within(got["v"], want["v"], bound["v"], "dv")
     else:
         check_backward(st, o, lse, got)
+
+
+@pytest.mark.parametrize("heads", [(3, 1, 48), (10, 2, 80), (31, 1, 96), (100, 1, 32), (4, 2, 128)],
+                         ids=str)
+@pytest.mark.parametrize("cap", [0.0, 3.0])
+def test_results_do_not_hang_on_what_else_is_there(cap, heads):
+    """Not on what a call before left on the chip, nor on large values in keys that nobody sees:
+    scores on both sides of where the cap's polynomial ends."""
+    st = dict(problem("padded", heads, seed=6), cap=cap)
+    o, lse = run_forward(st)
+    check_forward(st, o, lse)
+    got = run_backward(st, o, lse)
+    check_backward(st, o, lse, got)
+    large = dict(problem("causal 257", heads, seed=7, size=50.0), cap=cap)
+    for value in (0.0, 1e4, -1e4):
+        run_backward(large, *run_forward(large))
+        other = dict(st, **{n: st[n].clone() for n in ("k", "v")})
+        for n in ("k", "v"):
+            other[n][157:] = value
+        o2, lse2 = run_forward(other)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2), value
+        run_backward(large, *run_forward(large))
+        again = run_backward(other, o, lse)
+        assert all(torch.equal(got[n], again[n]) for n in got), value
 
 
 def test_two_calls_at_once():

@@ -92,7 +92,7 @@ BAD_SHAPES = [
     (dict(nh=258, nkv=2), b"128 query heads"), (dict(d=8), b"head_dim"), (dict(d=40), b"head_dim"),
     (dict(d=144), b"head_dim"), (dict(scale=0.0), b"scale"), (dict(scale=-1.0), b"scale"),
     (dict(scale=9e-7), b"scale"), (dict(scale=2e6), b"scale"),
-    (dict(softcap=9e-7), b"softcap"), (dict(softcap=2e6), b"softcap"),
+    (dict(softcap=1e-6), b"softcap"), (dict(softcap=2e4), b"softcap"),
     (dict(scale=INF), b"scale"), (dict(scale=NAN), b"scale"), (dict(softcap=-1.0), b"softcap"),
     (dict(softcap=INF), b"softcap"), (dict(softcap=NAN), b"softcap"),
     (dict(lo=P(A + 2)), b"aligned"), (dict(hi=P(A + 1)), b"aligned"),
