@@ -13,6 +13,9 @@
 // token share the lane's eight cosines and sines. The next heads' loads are under
 // way while some are computed, in pairs of fp32 (fma.f32x2). q and k have
 // CTAs of their own, so that a warp sums one gain's gradient.
+// Heads 32 / 8 of 128: 32,768 tokens bf16 112.5 us, 5.96 TB/s (a copy: 6.78); 4096
+// tokens fp32 to bf16 25.0 us, 5.0 TB/s, of them 5 us start and end; gradient of 16,384 bf16
+// 97 us, 5.2 TB/s, of them 4 us the sums of the gains' gradients.
 //
 // Angles: a full turn is 2^64. A pair's rate is kept as a 64-bit fraction of a
 // turn, the product with the position is taken modulo 2^64, and its upper 32
