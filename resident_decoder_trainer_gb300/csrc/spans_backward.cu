@@ -1176,7 +1176,10 @@ cudaError_t launch(const Args& ar, cudaStream_t s) {
                             kThreads, QCfg<D>::SMEM, s, tq, tdo, tk, tv, ar);
 }
 
-// Key tiles are halved where there are fewer than this times the SMs.
+// Key tiles are halved where there are fewer than this times the SMs: with halves /
+// without, documents up to 1024 in 4096 tokens 128 / 145 us, one of 4096 349 / 340;
+// from 512 key tiles on nothing is won (8192 tokens in one 1189 / 1158, in eight 297
+// / 284).
 constexpr int kHalvedBelow = 3;
 
 // The workspace: rows' values, spans of rows, of tiles, of groups; halves' sums.

@@ -705,7 +705,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
   if (__any_sync(0xffffffffu, bad)) row_forward(a, t, h, 0, a.d, false);
 }
 
-constexpr int kMinKeysOfSplit = 256;
+// Keys are split where items leave SMs idle, unless joining the rows takes longer
+// than the key tiles that are saved: the join as long as two tiles, and one more for
+// every 640 rows. Heads 32 / 8 of 128, split into single tiles / not: 1 query and 2
+// tiles 8.7 / 8.1 us, 4 tiles 8.8 / 10.8, 8 tiles 9.4 / 16.4; 64 queries and 4 tiles 16.3 /
+// 12.5, 8 tiles 17.0 / 18.8; 128 queries and 8 tiles 21.2 / 19.0, 16 tiles 23.0 / 30.9.
+// All parts but the last take as many tiles (1 query, 8192 keys: 16 parts of
+// four 14.2 us, 19 of three or four 15.9).
+constexpr int kRowsOfTile = 640;
 
 template <int D, bool CAP>
 cudaError_t launch(const Args& ar, cudaStream_t s) {
@@ -727,8 +734,11 @@ int forward_splits(int queries, int keys, int nkv, int rep) {
   const Tiling tl = Tiling::of(queries, rep);
   const int64_t items = static_cast<int64_t>((tl.tiles + 1) / 2) * nkv;
   if (items < 1) return 1;
-  return static_cast<int>(
-      std::max<int64_t>(1, std::min<int64_t>(num_sms() / items, keys / kMinKeysOfSplit)));
+  const int64_t tiles = (keys + 127) / 128, most = num_sms() / items;
+  const int64_t rows = static_cast<int64_t>(queries) * nkv * rep;
+  if (most < 2 || (tiles - 2) * kRowsOfTile < rows) return 1;
+  const int64_t each = (tiles + most - 1) / most;
+  return static_cast<int>((tiles + each - 1) / each);
 }
 
 size_t forward_workspace(int queries, int keys, int nh, int nkv, int d) {
