@@ -648,8 +648,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the splits of a row: o = sum_s w_s o_s, w_s = 2^(lse_s - lse). One CTA a
-// row, its warps share the splits, a lane has four columns; fixed order.
-constexpr int kJoinWarps = 4;
+// row, its warps share the splits, a lane has four columns; fixed order. Bound by
+// the latency of its start and of two loads, one behind the other where the first
+// parts waited for their weights (1 query, 1024 keys: 9.4 us in all and not 8.9).
+constexpr int kJoinWarps = 4, kJoinAhead = 5;
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ Args ar) {
   __shared__ float sums[kJoinWarps][kMaxDim];
   __shared__ float weight[1024];
@@ -657,6 +659,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t rows = static_cast<int64_t>(a.queries) * a.nh, th = blockIdx.x;
   after_previous_kernel();
+  auto part = [&](int s) {
+    return *reinterpret_cast<const float4*>(ar.part_o + (s * rows + th) * a.d + 4 * lane);
+  };
+  float4 ahead[kJoinAhead];  // these loads do not wait for the weights
+#pragma unroll
+  for (int i = 0; i < kJoinAhead; ++i)
+    if (warp + i * kJoinWarps < ar.splits && 4 * lane < a.d) ahead[i] = part(warp + i * kJoinWarps);
   float top = -INFINITY;
   for (int s = lane; s < ar.splits; s += 32) top = fmaxf(top, ar.part_lse[s * rows + th]);
   top = warp_max(top);
@@ -671,16 +680,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
   __syncthreads();
   float acc[4] = {};
   if (4 * lane < a.d) {
-    for (int s = warp; s < ar.splits; s += kJoinWarps) {
+    auto add = [&](int s, float4 o) {
       const float w = weight[s];
-      if (w == 0.f) continue;
-      const float4 o =
-          *reinterpret_cast<const float4*>(ar.part_o + (s * rows + th) * a.d + 4 * lane);
+      if (w == 0.f) return;
       acc[0] = fmaf(w, o.x, acc[0]);
       acc[1] = fmaf(w, o.y, acc[1]);
       acc[2] = fmaf(w, o.z, acc[2]);
       acc[3] = fmaf(w, o.w, acc[3]);
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < kJoinAhead; ++i)
+      if (warp + i * kJoinWarps < ar.splits) add(warp + i * kJoinWarps, ahead[i]);
+    for (int s = warp + kJoinAhead * kJoinWarps; s < ar.splits; s += kJoinWarps) add(s, part(s));
 #pragma unroll
     for (int i = 0; i < 4; ++i) sums[warp][4 * lane + i] = acc[i];
   }
@@ -708,10 +719,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
 // Keys are split where items leave SMs idle, unless joining the rows takes longer
 // than the key tiles that are saved: the join as long as two tiles, and one more for
 // every 640 rows. Heads 32 / 8 of 128, split into single tiles / not: 1 query and 2
-// tiles 8.7 / 8.1 us, 4 tiles 8.8 / 10.8, 8 tiles 9.4 / 16.4; 64 queries and 4 tiles 16.3 /
-// 12.5, 8 tiles 17.0 / 18.8; 128 queries and 8 tiles 21.2 / 19.0, 16 tiles 23.0 / 30.9.
-// All parts but the last take as many tiles (1 query, 8192 keys: 16 parts of
-// four 14.2 us, 19 of three or four 15.9).
+// tiles 8.7 / 8.0 us, 4 tiles 8.5 / 10.8, 8 tiles 8.9 / 16.4; 64 queries and 4 tiles 15.9 /
+// 12.4, 8 tiles 16.6 / 18.8; 128 queries and 8 tiles 20.1 / 19.0, 16 tiles 22.0 / 30.9.
+// Parts of as many tiles each, but the last (1 query, 8192 keys: 16 parts of four
+// 13.9 us, 19 of three or four 15.5).
 constexpr int kRowsOfTile = 640;
 
 template <int D, bool CAP>
