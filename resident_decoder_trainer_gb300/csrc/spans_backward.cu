@@ -143,24 +143,43 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_cons
       s = joined(s);
       if (row == 0) ar.tiles[tile] = s;
     }
-    // this lane's part of each of the warp's rows
-    float part[8];
+    // the row that this lane finishes
+    const int done = 16 * warp + (lane & 15);
+    const int done_in = static_cast<int>(done * inv_rep >> 16), done_t = tile * ar.tl.per + done_in;
+    float lse = 0.f, d_lse = 0.f;
+    bool sees = false;
+    if (done_in < ar.tl.per && done_t < a.queries) {
+      const int64_t th = static_cast<int64_t>(done_t) * a.nh + g * a.rep + done - done_in * a.rep;
+      int x, y;
+      a.span(done_t, x, y);
+      sees = x < y;
+      lse = a.lse[th];
+      if (a.d_lse) d_lse = a.d_lse[th];
+    }
+    // this lane's part of each of the warp's rows, the loads of four rows at a time
+    float part[8] = {};
 #pragma unroll
-    for (int b = 0; b < 8; ++b) {
-      part[b] = 0.f;
-      if (b * per_warp >= 16) break;
-      const int row = 16 * warp + b * per_warp + (lane >> log2);
-      const int in = static_cast<int>(row * inv_rep >> 16), t = tile * ar.tl.per + in;
-      const int h = g * a.rep + row - in * a.rep;
-      if (in < ar.tl.per && t < a.queries && c < a.d) {
-        Eight x, y;
+    for (int b0 = 0; b0 < 8; b0 += 4) {
+      if (b0 * per_warp >= 16) break;
+      Eight x[4], y[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int row = 16 * warp + (b0 + b) * per_warp + (lane >> log2);
+        const int in = static_cast<int>(row * inv_rep >> 16), t = tile * ar.tl.per + in;
+        const int h = g * a.rep + row - in * a.rep;
+        x[b].a = y[b].a = make_uint4(0u, 0u, 0u, 0u);
+        if ((b0 + b) * per_warp < 16 && in < ar.tl.per && t < a.queries && c < a.d) {
+          x[b].load(a.d_o.at(t, h) + c);
+          y[b].load(a.o.at(t, h) + c);
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
         float u[8], v[8];
-        x.load(a.d_o.at(t, h) + c);
-        y.load(a.o.at(t, h) + c);
-        x.get(u);
-        y.get(v);
+        x[b].get(u);
+        y[b].get(v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) part[b] = fmaf(u[i], v[i], part[b]);
+        for (int i = 0; i < 8; ++i) part[b0 + b] = fmaf(u[i], v[i], part[b0 + b]);
       }
     }
     // the rows' sums, each to the lane that finishes its row
@@ -174,21 +193,9 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_cons
       if (lane / per_warp == b) own = sum;
     }
     if (lane < 16) {
-      const int row = 16 * warp + lane;
-      const int in = static_cast<int>(row * inv_rep >> 16), t = tile * ar.tl.per + in;
-      float neg_lse = kNoRow, neg_d = 0.f;
-      if (in < ar.tl.per && t < a.queries) {
-        const int64_t th = static_cast<int64_t>(t) * a.nh + g * a.rep + row - in * a.rep;
-        int x, y;
-        a.span(t, x, y);
-        if (x < y) {
-          neg_lse = -a.lse[th] * kLog2e;
-          neg_d = (a.d_lse ? a.d_lse[th] : 0.f) - own;
-        }
-      }
-      const int64_t at = (static_cast<int64_t>(g) * ar.tl.tiles + tile) * 128 + row;
-      ar.neg_lse[at] = neg_lse;
-      ar.neg_d[at] = neg_d;
+      const int64_t at = (static_cast<int64_t>(g) * ar.tl.tiles + tile) * 128 + done;
+      ar.neg_lse[at] = sees ? -lse * kLog2e : kNoRow;
+      ar.neg_d[at] = sees ? d_lse - own : 0.f;
     }
   }
 }
