@@ -24,7 +24,7 @@
 // products where many tiles are seen whole: 8192 tokens of 32 / 8 heads of 128, a
 // quarter of them a prefix, 1199 us (651 dK/dV, 510 dQ), 0.96 and 0.92 of 1890
 // TFLOP/s for the four and the three products they form. 4096 tokens in documents up
-// to 1024: 126 us, of them 20 prepare (67 MB), 60 dK/dV, 50 dQ; bound by
+// to 1024: 124 us, of them 17 prepare (67 MB), 58 dK/dV, 50 dQ; bound by
 // the starts and ends of short items.
 #include <algorithm>
 
@@ -69,7 +69,7 @@ constexpr int kPrepThreads = 256;
 
 // Blocks [0, groups) find the groups' spans, the others the tiles' and the rows'
 // D and lse.
-__global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_constant__ Args ar) {
+__global__ void __launch_bounds__(kPrepThreads, 4) prepare_kernel(const __grid_constant__ Args ar) {
   const SpanArgs& a = ar.a;
   __shared__ TileSpan found[kPrepThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
