@@ -565,8 +565,9 @@ typedef struct rdt_heads {
  * in fp32, rounded once to out_dtype. positions int32 [axes, tokens], any
  * value; axes in [1, 4]. sections is a HOST array of `axes` counts that add up
  * to head_dim / 2: the first sections[0] pairs turn by axis 0, the next
- * sections[1] by axis 1, and so on; null with one axis. Angles are exact to
- * 2^-31 of a half turn, however far the position.
+ * sections[1] by axis 1, and so on; null with one axis. An angle is that of the
+ * pair's rate theta^(-2i / head_dim) as rounded in 64 bits (2^-51 of the rate),
+ * and exact to 2^-31 of a half turn beside that, however far the position.
  * head_dim a multiple of 16 in [16, 256]; n_heads and n_kv_heads in [0, 4096],
  * not both 0 (a tensor without heads is not looked at and may be null);
  * gain_q, gain_k fp32 [head_dim]; eps >= 0; theta > 0. tokens may be 0.
