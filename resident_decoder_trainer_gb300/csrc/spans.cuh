@@ -21,9 +21,10 @@ struct SpanArgs {
   const float* d_lse;  // null: 0
   float* lse;
   float scale, cap;  // cap 0: none
+  // from 0 on both: differences with a key's index stay within 32 bits
   __device__ __forceinline__ void span(int t, int& first, int& end) const {
     first = lo ? max(lo[t], 0) : 0;
-    end = hi ? min(hi[t], keys) : keys;
+    end = hi ? max(min(hi[t], keys), 0) : keys;
   }
 };
 

@@ -505,6 +505,20 @@ def test_results_do_not_hang_on_what_else_is_there(cap, heads):
         assert all(torch.equal(got[n], again[n]) for n in got), value
 
 
+@pytest.mark.parametrize("heads", [(8, 2, 64), (4, 1, 128)], ids=str)
+def test_spans_at_the_ends_of_their_type(heads):
+    """Between queries that see something: ends of -2^31 and 2^31 - 1 either way round."""
+    st = problem("causal 257", heads, seed=3)
+    low, high = -(1 << 31), (1 << 31) - 1
+    for part, lo, hi in ((0, 0, low), (1, high, low), (2, low, high), (3, high, high),
+                         (4, low, low)):
+        st["lo"][3 + part::9] = lo
+        st["hi"][3 + part::9] = hi
+    o, lse = run_forward(st)
+    check_forward(st, o, lse)
+    check_backward(st, o, lse, run_backward(st, o, lse))
+
+
 def test_two_calls_at_once():
     """On two streams, each with its own workspace."""
     sts = [problem("documents", (8, 2, 128), seed=s) for s in range(2)]
