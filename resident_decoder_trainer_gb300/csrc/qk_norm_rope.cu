@@ -545,6 +545,8 @@ const char* shape_problem(int tokens, int nh, int nkv, int d) {
   return nullptr;
 }
 
+constexpr char kShared[] = "an output is at the other tensor's place";
+
 // Checks what both calls have in common and fills in the arguments.
 const char* common_problem(int tokens, int nh, int nkv, int d, const rdt_heads* q,
                            const rdt_heads* k, int dtype, const float* gain_q, const float* gain_k,
@@ -576,6 +578,9 @@ const char* common_problem(int tokens, int nh, int nkv, int d, const rdt_heads* 
     s.out_hs = outs[i]->head_stride;
     s.gain = gains[i];
   }
+  if (nh && nkv &&
+      (q_out->data == k_out->data || q_out->data == k->data || k_out->data == q->data))
+    return kShared;
   if (!aligned4(gain_q) || !aligned4(gain_k) || !aligned4(positions))
     return "gains and positions must be 4-byte aligned";
   if (!(eps >= 0.f) || std::isinf(eps)) return "eps must be finite and >= 0";
@@ -714,6 +719,8 @@ rdt_status rdt_qk_norm_rope_backward(int32_t tokens, int32_t n_heads, int32_t n_
     side.dy_ts = g->token_stride;
     side.dy_hs = g->head_stride;
   }
+  if (n_heads && n_kv_heads && (dq->data == d_k_out->data || dk->data == d_q_out->data))
+    return refuse(kShared);
   a.f16_dy = d_dtype == RDT_F16;
   const int64_t grid = split_work(&a);
   const bool sums = d_gain_q || d_gain_k;

@@ -44,6 +44,8 @@ BAD_NORM = [
     (dict(k_out=heads(2, at=2 * A, ts=64, hs=64)), b"overlaps itself"),
     (dict(q_out=heads(4), out_dtype=0), b"place"),
     (dict(q_out=heads(4, ts=512)), b"place"),
+    (dict(q_out=heads(4, at=3 * A)), b"other"), (dict(k=heads(2, at=2 * A)), b"other"),
+    (dict(q=heads(4, at=3 * A)), b"other"),
     (dict(gain_q=P(A + 2)), b"aligned"), (dict(positions=P(A + 1)), b"aligned"),
     (dict(eps=-1.0), b"eps"), (dict(eps=INF), b"eps"), (dict(eps=NAN), b"eps"),
     (dict(axes=0), b"axes"), (dict(axes=5), b"axes"), (dict(sections=None), b"sections"),
@@ -71,6 +73,8 @@ GRAD = dict(tokens=5, nh=4, nkv=2, d=64, q=heads(4), k=heads(2), dtype=1, gain_q
     (dict(d_gain_k=P(A + 1)), b"aligned"), (dict(ws=None), b"null"),
     (dict(ws=P(A + 64)), b"256-byte"), (dict(ws_bytes=64), b"workspace"),
     (dict(d_q=heads(4, at=2 * A, ts=512)), b"place"), (dict(d=20), b"head_dim"),
+    (dict(d_q=heads(4, at=3 * A)), b"other"), (dict(d_k=heads(2, at=2 * A)), b"other"),
+    (dict(dk=heads(2, at=2 * A)), b"other"),
     (dict(axes=7), b"axes"), (dict(theta=0.0), b"theta")])
 def test_norm_backward_refuses(lib, change, text):
     einval(lib, lib.rdt_qk_norm_rope_backward(*{**GRAD, **change}.values()), text)
