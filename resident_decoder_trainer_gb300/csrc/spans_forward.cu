@@ -721,8 +721,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
 // every 640 rows. Heads 32 / 8 of 128, split into single tiles / not: 1 query and 2
 // tiles 8.7 / 8.0 us, 4 tiles 8.5 / 10.8, 8 tiles 8.9 / 16.4; 64 queries and 4 tiles 15.9 /
 // 12.4, 8 tiles 16.6 / 18.8; 128 queries and 8 tiles 20.1 / 19.0, 16 tiles 22.0 / 30.9.
-// Parts of as many tiles each, but the last (1 query, 8192 keys: 16 parts of four
-// 13.9 us, 19 of three or four 15.5).
+// As few parts as keep the longest as short (1 query, 8192 keys: 16 parts of four
+// tiles 13.9 us, 19 of three or four 15.5).
 constexpr int kRowsOfTile = 640;
 
 template <int D, bool CAP>
