@@ -30,6 +30,31 @@ struct SpanArgs {
 
 constexpr int kMaxDim = 128;  // of a head
 
+// ------------------------------------------------------------------- waits
+// A tensor-core kernel's warp computes its rows that came out not finite again,
+// one after the other, while its CTA's others wait for it; and the warps of a row
+// tile that sees few keys or none wait while their item's other tile walks
+// through its own. Both take the longer the more there is to see. So a wait
+// gives up after kWaitLimitNs and eight times what 32 rows have been seen to take:
+// 16 us a key that a query sees, 30 us a query that sees a key (heads of 128).
+constexpr uint64_t kNsOfKey = 8 * 16000, kNsOfQuery = 8 * 30000;
+struct Patience {
+  int* err;
+  uint64_t limit_ns;
+};
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const Patience& p) {
+  return mbar_wait(bar, parity, p.err, p.limit_ns);
+}
+__device__ __noinline__ static bool wait_longer(uint32_t bar, uint32_t parity, Patience p) {
+  return mbar_wait(bar, parity, p);
+}
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, const Patience& p) {
+  return mbar_try_wait(bar, parity) || wait_longer(bar, parity, p);
+}
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const Patience& p) {
+  return warp_wait(bar, parity, p.err, p.limit_ns);
+}
+
 // ------------------------------------------------- one warp per row of an output
 // Lanes take 32 keys (or queries) at a time for the scores, and four columns
 // each for the sums. All in fp32. Columns [c0, c1) are written.

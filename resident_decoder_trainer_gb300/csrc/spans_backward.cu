@@ -60,7 +60,7 @@ struct Args {
   int parts;          // items of a key tile
   float4* part;       // parts = 2: sums of each half
   int* arrived;       // and how many of a key tile's are there
-  int* err;
+  Patience err_rows, err_keys;  // where row tiles are walked through, where key tiles are
   bool wide_dq, wide_dk, wide_dv;  // rows at multiples of 32 bytes
 };
 
@@ -357,12 +357,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = KvCfg<D>;
   constexpr uint32_t QST = C::QST, OST = C::OST, IST = C::IST;
   const SpanArgs& a = ar.a;
-  int* err = ar.err;
+  const Patience& err = ar.err_rows;
   extern __shared__ __align__(1024) uint8_t smem_tiles[];
   uint8_t* smem = smem_tiles;
   const uint32_t sbase = smem_u32(smem);
   if (sbase & 1023u) {  // the swizzled tiles' layout counts on it
-    record_error(err, kErrTimeout);
+    record_error(err.err, kErrTimeout);
     return;
   }
   const uint32_t bar0 = sbase + C::OFF_BAR;
@@ -810,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  settle(err);
+  settle(err.err);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
@@ -848,12 +848,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = QCfg<D>;
   constexpr int KST = C::KST, VST = C::VST;
   const SpanArgs& a = ar.a;
-  int* err = ar.err;
+  const Patience& err = ar.err_keys;
   extern __shared__ __align__(1024) uint8_t smem_tiles[];
   uint8_t* smem = smem_tiles;
   const uint32_t sbase = smem_u32(smem);
   if (sbase & 1023u) {  // the swizzled tiles' layout counts on it
-    record_error(err, kErrTimeout);
+    record_error(err.err, kErrTimeout);
     return;
   }
   const uint32_t bar0 = sbase + C::OFF_BAR;
@@ -1152,7 +1152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  settle(err);
+  settle(err.err);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
@@ -1230,7 +1230,9 @@ cudaError_t backward_tiles(const SpanArgs& a, void* ws, cudaStream_t s) {
   lay_out(&ar, a.queries, a.keys, a.rep, a.nkv, a.d, ws);
   ar.cap = cap_of(a.scale, a.cap);
   ar.scale_log2 = (a.cap > 0.f ? a.cap : a.scale) * kLog2e;
-  ar.err = device_error_ptr();
+  int* const err = device_error_ptr();
+  ar.err_rows = {err, kWaitLimitNs + kNsOfQuery * a.queries * a.rep};
+  ar.err_keys = {err, kWaitLimitNs + kNsOfKey * a.keys};
   auto wide = [](const View& x, int64_t tokens, int64_t heads) {
     return (reinterpret_cast<uintptr_t>(x.p) | (tokens > 1 ? x.ts * 2 : 0) |
             (heads > 1 ? x.hs * 2 : 0)) % 32 == 0;

@@ -58,7 +58,7 @@ struct Args {
   float scale_log2;  // of what is exponentiated: scale log2 e, or cap log2 e
   float* part_o;     // splits > 1: fp32 [splits][queries][nh][d] and lse (base 2)
   float* part_lse;
-  int* err;
+  Patience err;
 };
 
 template <int D>
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Cfg<D>;
   constexpr int BM = C::BM, BN = C::BN, KS = C::KS, VS = C::VS;
   const SpanArgs& a = ar.a;
-  int* err = ar.err;
+  const Patience& err = ar.err;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (err && *reinterpret_cast<volatile int*>(err) != 0) {
+  if (err.err && *reinterpret_cast<volatile int*>(err.err) != 0) {
     // after a timed-out wait, copies issued just before may still be landing
     // in this CTA's shared memory: let them finish before it exits
     const uint64_t w0 = global_timer_ns();
@@ -768,7 +768,7 @@ cudaError_t forward_tiles(const SpanArgs& a, void* ws, cudaStream_t s) {
   const int64_t rows = static_cast<int64_t>(a.queries) * a.nh;
   ar.part_o = static_cast<float*>(ws);
   ar.part_lse = ar.part_o + ar.splits * rows * a.d;
-  ar.err = device_error_ptr();
+  ar.err = {device_error_ptr(), kWaitLimitNs + kNsOfKey * a.keys};
   cudaError_t e;
   if (a.d <= 64)
     e = a.cap > 0.f ? launch<64, true>(ar, s) : launch<64, false>(ar, s);
