@@ -800,8 +800,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++u;
         had = false;
       }
-      for (unsigned again = __ballot_sync(0xffffffffu, !fine && key < a.keys); again;
-           again &= again - 1) {
+      unsigned again = __ballot_sync(0xffffffffu, !fine && key < a.keys);
+      if (again) __syncwarp();  // other lanes store what a row's own lane stored
+      for (; again; again &= again - 1) {
         const int j = m.n0 + quarter * 32 + __ffs(again) - 1;
         if (!sees_nonfinite(ar, j, m.g)) row_dkdv(a, j, m.g, c0, min(c0 + 32, a.d));
       }
@@ -1140,8 +1141,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int h = again_of % a.nkv * a.rep + row_h;
         const bool real = row_t < ar.tl.per && t < a.queries;
         if (real) put_columns(a.dq.at(t, h) + c0, r, a.scale, left, ar.wide_dq);
-        for (unsigned again = __ballot_sync(0xffffffffu, real && finite && !all_finite(r, left)); again;
-             again &= again - 1) {
+        unsigned again = __ballot_sync(0xffffffffu, real && finite && !all_finite(r, left));
+        if (again) __syncwarp();  // other lanes store what a row's own lane stored
+        for (; again; again &= again - 1) {
           const int from = __ffs(again) - 1;
           row_dq(a, __shfl_sync(0xffffffffu, t, from), __shfl_sync(0xffffffffu, h, from), c0,
                  min(c0 + 32, a.d));

@@ -622,8 +622,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           a.lse[th] = lse2 * kLn2;
       }
       if (ar.splits == 1) {
-        for (unsigned again = __ballot_sync(0xffffffffu, real && bad != 0.f && l_run == l_run); again;
-             again &= again - 1) {
+        unsigned again = __ballot_sync(0xffffffffu, real && bad != 0.f && l_run == l_run);
+        if (again) __syncwarp();  // other lanes stored parts of these rows
+        for (; again; again &= again - 1) {
           const int from = __ffs(again) - 1;
           row_forward(a, __shfl_sync(0xffffffffu, t, from),
                       __shfl_sync(0xffffffffu, h, from), 0, a.d, false);
@@ -713,7 +714,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
         make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
   }
   if (lane == 0 && a.lse) a.lse[th] = total != 0.f ? (top + log2f(total)) * kLn2 : -INFINITY;
-  if (__any_sync(0xffffffffu, bad)) row_forward(a, t, h, 0, a.d, false);
+  if (__any_sync(0xffffffffu, bad)) {
+    __syncwarp();  // other lanes store what this one stored
+    row_forward(a, t, h, 0, a.d, false);
+  }
 }
 
 // Keys are split where items leave SMs idle, unless joining the rows takes longer
