@@ -215,6 +215,61 @@ __device__ __noinline__ static void row_dkdv(const SpanArgs& a, int j, int g, in
   put_row(a.dv.at(j, g), av, 1.f, c0, c1);
 }
 
+// Whether one of the two bf16 values is not finite.
+__device__ __forceinline__ bool bad_pair(uint32_t two) {
+  return (two & 0x7f80u) == 0x7f80u || (two & 0x7f800000u) == 0x7f800000u;
+}
+
+// A lane has the columns [c0, c1) of a row of sums over keys (null: none) as stored,
+// and which keys it sees: the lanes (bits) in whose row some column is not finite
+// though no seen key is in that column of x, key head g: what is not finite by
+// right is not computed again. Whole warp. Reads the seen keys until every such
+// column has found one.
+__device__ __noinline__ static unsigned bad_rows(const SpanArgs& a, const View& x, int g,
+                                                const bf16* row, int c0, int c1, int first,
+                                                int end) {
+  const int lane = threadIdx.x & 31;
+  uint32_t bad[kMaxDim / 32] = {};
+  if (row) {
+#pragma unroll
+    for (int w = 0; w < kMaxDim / 32; ++w)
+#pragma unroll 1
+      for (int c = max(c0, 32 * w); c < min(c1, 32 * w + 32); ++c)
+        if ((*reinterpret_cast<const uint16_t*>(row + c) & 0x7f80u) == 0x7f80u)
+          bad[w] |= 1u << (c - 32 * w);
+  }
+  auto any = [&] { return (bad[0] | bad[1] | bad[2] | bad[3]) != 0u; };
+  const int from = __reduce_min_sync(0xffffffffu, any() ? first : INT32_MAX);
+  const int to = __reduce_max_sync(0xffffffffu, any() ? end : 0);
+  // a lane takes eight columns of one of `at_once` keys
+  const int pieces = a.d / 8, at_once = 32 / pieces, key = lane / pieces;
+  const bf16* const piece = x.p + g * x.hs + 8 * (lane % pieces);
+  for (int64_t j0 = from; j0 < to && __any_sync(0xffffffffu, any()); j0 += 4 * at_once) {
+    Eight e[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t j = j0 + u * at_once + key;
+      e[u].a = make_uint4(0u, 0u, 0u, 0u);
+      if (key < at_once && j < to) e[u].load(piece + j * x.ts);
+    }
+    bool some = false;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      some |= bad_pair(e[u].a.x) || bad_pair(e[u].a.y) || bad_pair(e[u].a.z) || bad_pair(e[u].a.w);
+    if (!__any_sync(0xffffffffu, some)) continue;
+    const int64_t j1 = min(j0 + 4 * at_once, static_cast<int64_t>(to));
+    for (int64_t j = j0; j < j1; ++j)
+#pragma unroll
+      for (int w = 0; w < kMaxDim / 32; ++w) {
+        const int c = 32 * w + lane;
+        const uint32_t v = c < a.d ? *reinterpret_cast<const uint16_t*>(x.at(j, g) + c) : 0u;
+        const uint32_t which = __ballot_sync(0xffffffffu, (v & 0x7f80u) == 0x7f80u);
+        if (first <= j && j < end) bad[w] &= ~which;
+      }
+  }
+  return __ballot_sync(0xffffffffu, any());
+}
+
 // ------------------------------------------------- tiles of the tensor-core kernels
 // A tile of 128 rows is 128 / rep neighbouring queries times the rep query
 // heads that share a key head, query by query (rep = 3: 126 rows are used).

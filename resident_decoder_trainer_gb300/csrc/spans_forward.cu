@@ -17,9 +17,9 @@
 // are formed. O is rescaled only
 // when a row's maximum grows by more than 2^8.
 //
-// A row whose O is not finite, though its sum is, is computed again key by key
-// (row_forward): a NaN or infinity in a value that the row does not see, times
-// p = 0, would reach it.
+// A row whose O is not finite, though its sum and the values it sees are, is
+// computed again key by key (row_forward): a NaN or infinity in a value that the
+// row does not see, times p = 0, would reach it.
 //
 // Bound by the softmax: over all 1850 cycles for 128 x 128 scores, whose two products
 // take 1400. 8192 tokens of 32 / 8 heads of 128, a quarter of them a prefix: 407 us
@@ -622,12 +622,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           a.lse[th] = lse2 * kLn2;
       }
       if (ar.splits == 1) {
-        unsigned again = __ballot_sync(0xffffffffu, real && bad != 0.f && l_run == l_run);
-        if (again) __syncwarp();  // other lanes stored parts of these rows
-        for (; again; again &= again - 1) {
-          const int from = __ffs(again) - 1;
-          row_forward(a, __shfl_sync(0xffffffffu, t, from),
-                      __shfl_sync(0xffffffffu, h, from), 0, a.d, false);
+        const bool mine = real && bad != 0.f && l_run == l_run;
+        if (__any_sync(0xffffffffu, mine)) {
+          __syncwarp();  // other lanes stored parts of these rows
+          int first = 0, end = 0;
+          if (mine) a.span(t, first, end);
+          for (unsigned again = bad_rows(a, a.v, not_hoisted(item) % a.nkv,
+                                         mine ? a.o.at(t, h) : nullptr, 0, a.d, first, end);
+               again; again &= again - 1) {
+            const int from = __ffs(again) - 1;
+            row_forward(a, __shfl_sync(0xffffffffu, t, from), __shfl_sync(0xffffffffu, h, from), 0,
+                        a.d, false);
+          }
         }
       }
     }

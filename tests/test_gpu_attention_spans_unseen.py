@@ -83,3 +83,77 @@ def test_a_row_tile_that_sees_nothing_beside_one_that_sees_2_28_keys():
     assert rdt.device_error() == 0
     assert (o[0] == 4).all() and lse[0, 0] == 64
     assert (o[1:] == 0).all() and (lse[1:] == -math.inf).all()
+
+
+def time_us(call):
+    """The least of three, after a first."""
+    call()
+    least = math.inf
+    for _ in range(3):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        call()
+        b.record()
+        b.synchronize()
+        least = min(least, 1e3 * a.elapsed_time(b))
+    return least
+
+
+def forward_call(st):
+    t, nh, d = st["q"].shape
+    keys, nkv = st["k"].shape[:2]
+    o, lse = torch.empty_like(st["q"]), torch.empty(t, nh, device="cuda")
+    ws = torch.empty(rdt.attention_workspace_bytes(t, keys, nh, nkv, d), dtype=torch.uint8,
+                     device="cuda")
+    return lambda: rdt.attention(st["q"], st["k"], st["v"], o, ws, lse=lse, lo=st["lo"],
+                                 hi=st["hi"], scale=st["scale"], softcap=st["cap"])
+
+
+def backward_call(st):
+    """The gradient, of o and lse as the forward call writes them."""
+    o, lse = spans.run_forward(st)
+    t, nh, d = st["q"].shape
+    keys, nkv = st["k"].shape[:2]
+    dq, dk, dv = (torch.empty_like(st[n]) for n in ("q", "k", "v"))
+    ws = torch.empty(rdt.attention_workspace_bytes(t, keys, nh, nkv, d, backward=True),
+                     dtype=torch.uint8, device="cuda")
+    return lambda: rdt.attention_backward(st["q"], st["k"], st["v"], o, lse, st["d_o"], dq, dk, dv,
+                                          ws, lo=st["lo"], hi=st["hi"], scale=st["scale"],
+                                          softcap=st["cap"])
+
+
+@pytest.mark.parametrize("heads", [(32, 8, 128), (16, 16, 64)], ids=str)
+def test_an_infinity_that_all_see_costs_little(heads):
+    """Rows that are not finite by right are not computed again, which took 600 times as long."""
+    lo, hi = spans.causal(4096)
+    st = problem(lo, hi, 4096, heads)
+    clean = time_us(forward_call(st))
+    st["v"][5] = math.inf
+    assert time_us(forward_call(st)) < 20 * clean
+
+
+@pytest.mark.parametrize("heads", [(8, 2, 64), (4, 1, 128), (10, 2, 80), (4, 2, 16), (9, 3, 48)],
+                         ids=str)
+def test_columns_that_are_not_finite(heads):
+    """Infinities and NaN in single columns of values: what sees them is not finite in those
+    columns and is within its bounds in the others, whatever it does not see has in them."""
+    lo, hi = spans.documents([100, 300], window=90)
+    st = problem(lo, hi, 400, heads, seed=8)
+    bad = dict(st, v=st["v"].clone())
+    places = [(120, 3, math.inf), (150, 5, math.nan), (151, 3, -math.inf), (230, 5, math.inf),
+              (95, heads[2] - 1, math.nan)]
+    for key, column, value in places:
+        bad["v"][key, :, column] = value
+    o, lse = spans.run_forward(bad)
+    want, _, p = spans.forward_exact(st)
+    rep = heads[0] // heads[1]
+    av = st["v"].double().abs().repeat_interleave(rep, 1)
+    room = (torch.einsum("htj,jhd->thd", (spans.HALF + spans.delta(st)) * p, av)
+            + spans.HALF * want.abs())
+    sees = torch.zeros_like(o, dtype=torch.bool)
+    for key, column, _ in places:
+        rows = (st["lo"] <= key) & (key < st["hi"])
+        sees[rows, :, column] = True
+        # a weight that is 0 in fp32 makes NaN of an infinity, as 0 times it is
+        assert not o[rows][:, :, column].isfinite().any()
+    spans.within(o.masked_fill(sees, 0.0), want.masked_fill(sees, 0.0), room, "o")
