@@ -720,10 +720,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
         make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
   }
   if (lane == 0 && a.lse) a.lse[th] = total != 0.f ? (top + log2f(total)) * kLn2 : -INFINITY;
-  if (__any_sync(0xffffffffu, bad)) {
-    __syncwarp();  // other lanes store what this one stored
+  // not where the weights are NaN, or what the row sees is not finite
+  if (total != total || !__any_sync(0xffffffffu, bad)) return;
+  __syncwarp();  // other lanes read, and store, what this one stored
+  int first, end;
+  a.span(t, first, end);
+  if (bad_rows(a, a.v, h / a.rep, lane == 0 ? a.o.at(t, h) : nullptr, 0, a.d, first, end))
     row_forward(a, t, h, 0, a.d, false);
-  }
 }
 
 // Keys are split where items leave SMs idle, unless joining the rows takes longer

@@ -157,3 +157,35 @@ def test_columns_that_are_not_finite(heads):
         # a weight that is 0 in fp32 makes NaN of an infinity, as 0 times it is
         assert not o[rows][:, :, column].isfinite().any()
     spans.within(o.masked_fill(sees, 0.0), want.masked_fill(sees, 0.0), room, "o")
+
+
+def test_a_query_that_is_nan_costs_little_where_keys_are_split():
+    """Nor does an infinity that it sees. Took 500 times as long."""
+    st = problem(torch.tensor([0]), torch.tensor([32768]), 32768, (32, 8, 128))
+    clean = time_us(forward_call(st))
+    for n, at in (("q", 0), ("v", 5)):
+        bad = dict(st, **{n: st[n].clone()})
+        bad[n][at] = math.nan
+        assert time_us(forward_call(bad)) < 20 * clean, n
+        o, _ = spans.run_forward(bad)
+        assert o.isnan().all()
+
+
+@pytest.mark.parametrize("heads", [(8, 2, 64), (4, 1, 128), (10, 2, 80), (4, 2, 16)], ids=str)
+def test_columns_that_are_not_finite_where_keys_are_split(heads):
+    """Two queries, of which the first does not see the last key: NaN in a column of that, an
+    infinity in a column of a key that both see."""
+    st = problem(torch.tensor([0, 40]), torch.tensor([2999, 3000]), 3000, heads, seed=9)
+    bad = dict(st, v=st["v"].clone())
+    bad["v"][2999, :, 7] = math.nan
+    bad["v"][1000, :, 2] = math.inf
+    o, lse = spans.run_forward(bad)
+    sees = torch.zeros_like(o, dtype=torch.bool)
+    sees[1, :, 7] = True
+    sees[:, :, 2] = True
+    assert not o[sees].isfinite().any()
+    want, _, p = spans.forward_exact(st)
+    av = st["v"].double().abs().repeat_interleave(heads[0] // heads[1], 1)
+    room = (torch.einsum("htj,jhd->thd", (spans.HALF + spans.delta(st)) * p, av)
+            + spans.HALF * want.abs())
+    spans.within(o.masked_fill(sees, 0.0), want.masked_fill(sees, 0.0), room, "o")
