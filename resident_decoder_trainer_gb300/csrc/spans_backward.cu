@@ -1141,12 +1141,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int h = again_of % a.nkv * a.rep + row_h;
         const bool real = row_t < ar.tl.per && t < a.queries;
         if (real) put_columns(a.dq.at(t, h) + c0, r, a.scale, left, ar.wide_dq);
-        unsigned again = __ballot_sync(0xffffffffu, real && finite && !all_finite(r, left));
-        if (again) __syncwarp();  // other lanes store what a row's own lane stored
-        for (; again; again &= again - 1) {
-          const int from = __ffs(again) - 1;
-          row_dq(a, __shfl_sync(0xffffffffu, t, from), __shfl_sync(0xffffffffu, h, from), c0,
-                 min(c0 + 32, a.d));
+        const bool mine = real && finite && !all_finite(r, left);
+        if (__any_sync(0xffffffffu, mine)) {
+          __syncwarp();  // other lanes store what a row's own lane stored
+          int first_of = 0, end_of = 0;
+          if (mine) a.span(t, first_of, end_of);
+          const int c1 = min(c0 + 32, a.d);
+          for (unsigned again = bad_rows(a, a.k, again_of % a.nkv, mine ? a.dq.at(t, h) : nullptr,
+                                         c0, c1, first_of, end_of);
+               again; again &= again - 1) {
+            const int from = __ffs(again) - 1;
+            row_dq(a, __shfl_sync(0xffffffffu, t, from), __shfl_sync(0xffffffffu, h, from), c0, c1);
+          }
         }
       }
     }

@@ -189,3 +189,50 @@ def test_columns_that_are_not_finite_where_keys_are_split(heads):
     room = (torch.einsum("htj,jhd->thd", (spans.HALF + spans.delta(st)) * p, av)
             + spans.HALF * want.abs())
     spans.within(o.masked_fill(sees, 0.0), want.masked_fill(sees, 0.0), room, "o")
+
+
+def minus_infinite_key(heads, tokens, key, column):
+    """A causal batch whose key `key` is -infinity in one column in which every query is above 0:
+    its weight is 0, and a gradient of a query that sees it is not finite in that column."""
+    lo, hi = spans.causal(tokens)
+    st = problem(lo, hi, tokens, heads, seed=4)
+    st["q"][:, :, column] = st["q"][:, :, column].abs() + 0.5
+    bad = dict(st, k=st["k"].clone())
+    bad["k"][key, :, column] = -math.inf
+    return st, bad
+
+
+def test_the_gradient_of_a_key_with_an_infinity_costs_little():
+    """Took 350 times as long."""
+    st, bad = minus_infinite_key((32, 8, 128), 4096, 5, 3)
+    clean = time_us(backward_call(st))
+    assert time_us(backward_call(bad)) < 20 * clean
+
+
+@pytest.mark.parametrize("heads", [(8, 2, 64), (4, 1, 128), (10, 2, 80)], ids=str)
+def test_the_gradient_of_a_key_with_an_infinity(heads):
+    """Finite, and within its bounds, in the other columns and for queries before the key."""
+    st, bad = minus_infinite_key(heads, 300, 150, 3)
+    o, lse = spans.run_forward(bad)
+    assert o.isfinite().all() and lse.isfinite().all()
+    # as if nobody saw the key: two spans for the queries after it, so by a mask of its own
+    q, k, v, g = (st[n].double() for n in ("q", "k", "v", "d_o"))
+    rep = heads[0] // heads[1]
+    kk, vv = k.repeat_interleave(rep, 1), v.repeat_interleave(rep, 1)
+    s, sees, _ = spans.scores(q, k, st["lo"], st["hi"], st["scale"], 0.0)
+    sees[:, 150] = False
+    p = torch.exp(s - lse.double().T[..., None]).masked_fill(~sees, 0.0)
+    own = (g * o.double()).sum(2)
+    dp = torch.einsum("thd,jhd->htj", g, vv)
+    ds = p * (dp - own.T[..., None])
+    dl = spans.delta(st)
+    sizes = torch.einsum("thd,jhd->htj", g.abs(), vv.abs())
+    own_size = (g * o.double()).abs().sum(2).T[..., None]
+    e = (spans.HALF + dl) * ds.abs() + p * ((dl + 2.0 ** -17) * sizes + 2.0 ** -17 * own_size)
+    want = st["scale"] * torch.einsum("htj,jhd->thd", ds, kk)
+    room = (st["scale"] * torch.einsum("htj,jhd->thd", e, kk.abs()) + spans.HALF * want.abs())
+    got = spans.run_backward(bad, o, lse, d_lse=False)["q"]
+    after = torch.zeros_like(o, dtype=torch.bool)
+    after[150:, :, 3] = True
+    assert not got[after].isfinite().any()
+    spans.within(got.masked_fill(after, 0.0), want.masked_fill(after, 0.0), room, "dq")
