@@ -270,6 +270,20 @@ __device__ __noinline__ static unsigned bad_rows(const SpanArgs& a, const View& 
   return __ballot_sync(0xffffffffu, any());
 }
 
+// The rows of o that a warp has found not finite (query t and head h of each lane,
+// t = -1: none), all of key head g, computed again unless they are so by right.
+__device__ __noinline__ static void forward_again(const SpanArgs& a, int g, int t, int h) {
+  __syncwarp();  // other lanes stored parts of these rows
+  int first = 0, end = 0;
+  if (t >= 0) a.span(t, first, end);
+  for (unsigned again = bad_rows(a, a.v, g, t >= 0 ? a.o.at(t, h) : nullptr, 0, a.d, first, end);
+       again; again &= again - 1) {
+    const int from = __ffs(again) - 1;
+    row_forward(a, __shfl_sync(0xffffffffu, t, from), __shfl_sync(0xffffffffu, h, from), 0, a.d,
+                false);
+  }
+}
+
 // ------------------------------------------------- tiles of the tensor-core kernels
 // A tile of 128 rows is 128 / rep neighbouring queries times the rep query
 // heads that share a key head, query by query (rep = 3: 126 rows are used).
@@ -369,6 +383,72 @@ __device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
   const uint32_t below_hi = hi >= 32 ? ~0u : hi <= 0 ? 0u : (1u << hi) - 1u;
   const uint32_t below_lo = lo >= 32 ? ~0u : lo <= 0 ? 0u : (1u << lo) - 1u;
   return below_hi & ~below_lo;
+}
+
+// ------------------------------------------------- what nobody sees
+// What lies beside the keys that are seen (the end of a cache, the rows behind a
+// batch's last token) may be memory that nobody wrote. Where it is NaN or infinite,
+// 0 times it reaches sums over keys. So a CTA goes through its items in rounds of at
+// most kRound: where some came out not finite, the round after takes those once more
+// (`kSecond` in their number), with the keys that none of an item's rows sees cleared
+// in shared memory, and only what is not finite then is computed again row by row.
+// Others pay for one look at a word of shared memory.
+constexpr int kRound = 64, kSecond = 1 << 30;
+struct Rounds {
+  unsigned long long redo;  // the round's items that are to be taken once more, a bit each
+  int left;                 // there are items behind the round's
+  int lost;                 // a wait has given up: no more rounds
+  uint32_t start;           // items before the round
+};
+// Says so of item `it`, counted over all rounds. One lane of a warp.
+__device__ __forceinline__ void take_again(Rounds* r, uint32_t it) {
+  atomicOr(&r->redo, 1ull << (it - *reinterpret_cast<volatile uint32_t*>(&r->start)));
+}
+// A round's end: whether there is another, and the items it takes once more, if any.
+// All threads of the CTA, in whole warps, of which thread 0 belongs to the one that hands
+// out the items; waits for all of them.
+template <bool MORE>
+__device__ __forceinline__ bool next_round(Rounds* r, int threads, unsigned long long& redo) {
+  named_bar_sync(1, threads);
+  if (!MORE) return false;
+  volatile Rounds* v = r;
+  redo = v->redo;
+  if ((redo == 0ull && v->left == 0) || v->lost) return false;
+  named_bar_sync(1, threads);
+  if (threadIdx.x == 0) v->redo = 0ull;
+  return true;
+}
+
+// Waits for a tile of 128 keys from `base` on (chunks of 64 columns, 128 bytes a row,
+// one behind the other) and clears the rows that none of the `n` queries from t0 on
+// sees; then arrives on `full`. Whole warp.
+__device__ __forceinline__ bool clear_unseen(const SpanArgs& a, int t0, int n, int base,
+                                             uint8_t* tile, uint32_t raw, uint32_t parity,
+                                             uint32_t full, const Patience& err) {
+  const int lane = threadIdx.x & 31;
+  if (!warp_wait(raw, parity, err)) return false;
+#pragma unroll 1
+  for (int w = 0; w < 4; ++w) {
+    uint32_t seen = 0u;
+#pragma unroll 1
+    for (int i = lane; i < n; i += 32) {
+      int x, y;
+      a.span(t0 + i, x, y);
+      if (x < y) seen |= bits_between(x - base - 32 * w, y - base - 32 * w);
+    }
+    seen = __reduce_or_sync(0xffffffffu, seen);
+#pragma unroll 1
+    for (int row = lane >> 3; row < 32; row += 4)
+      if (!(seen >> row & 1u))
+#pragma unroll 1
+        for (int c = 0; c < a.d; c += 64)
+          *reinterpret_cast<uint4*>(tile + c * 256 + (32 * w + row) * 128 + 16 * (lane & 7)) =
+              make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();  // for the tensor cores
+  __syncwarp();
+  if (lane == 0) mbar_arrive(full);
+  return true;
 }
 
 // Splits of the keys of one (pair of tiles, key head), and the forward pass'

@@ -9,7 +9,7 @@ import torch
 import test_gpu_attention_spans as spans
 from gpu_helpers import ensure_built
 from resident_decoder_trainer_gb300 import rdt
-from test_gpu_attention_spans_items import problem
+from test_gpu_attention_spans_items import caches, problem
 
 pytestmark = pytest.mark.gpu
 
@@ -236,3 +236,88 @@ def test_the_gradient_of_a_key_with_an_infinity(heads):
     after[150:, :, 3] = True
     assert not got[after].isfinite().any()
     spans.within(got.masked_fill(after, 0.0), want.masked_fill(after, 0.0), room, "dq")
+
+
+UNSEEN = {  # keys, spans; what no query sees is what lies between and behind
+    "1 of a cache": (3000, lambda: (torch.tensor([0]), torch.tensor([2700]))),
+    "1 of a short cache": (300, lambda: (torch.tensor([3]), torch.tensor([130]))),
+    "5 of a cache": (900, lambda: (torch.zeros(5, dtype=torch.int64), torch.arange(641, 646))),
+    "caches": (8 * 300, lambda: caches([300, 1, 17, 128, 129, 0, 255, 256], 1, 300)),
+    "many caches": (70 * 64, lambda: caches([(7 * i) % 65 for i in range(70)], 1, 64)),
+    "long caches": (3 * 2500, lambda: caches([2400, 77, 1300], 2, 2500)),
+    "unused end": (500, lambda: spans.with_nothing(spans.documents([100, 57, 203]), 140)),
+    "unused start": (500, lambda: tuple(x.roll(140) for x in spans.with_nothing(
+        spans.documents([100, 57, 203]), 140))),
+    "a window's past": (900, lambda: (torch.arange(400, 600), torch.arange(431, 631))),
+    "descending": (1000, lambda: (torch.arange(900, 0, -3), torch.arange(902, 2, -3))),
+    "none": (200, lambda: spans.with_nothing(spans.documents([0]), 60)),
+}
+
+
+def unseen_keys(st):
+    seen = torch.zeros(st["k"].shape[0] + 1, dtype=torch.int64, device="cuda")
+    lo = st["lo"].long().clamp(min=0)
+    hi = st["hi"].long().clamp(max=st["k"].shape[0])
+    some = lo < hi
+    seen.index_add_(0, lo[some], torch.ones_like(lo[some]))
+    seen.index_add_(0, hi[some], -torch.ones_like(lo[some]))
+    return seen.cumsum(0)[:-1] == 0
+
+
+@pytest.mark.parametrize("mask", UNSEEN)
+@pytest.mark.parametrize("heads,cap", [((32, 8, 128), 0.0), ((8, 8, 64), 30.0), ((4, 1, 128), 20.0),
+                                       ((9, 3, 48), 0.0), ((4, 2, 16), 0.0)], ids=str)
+@pytest.mark.parametrize("junk", [math.nan, -math.inf])
+def test_keys_that_nobody_sees(mask, heads, cap, junk):
+    """Results are those with zeros there: within the same bounds, whether a row's item is taken
+    once more with these keys cleared or a part's sum formed again key by key (without the rounding
+    of p to bf16, so not to the bit)."""
+    keys, of = UNSEEN[mask]
+    lo, hi = of()
+    st = problem(lo, hi, keys, heads, seed=11, cap=cap)
+    empty = unseen_keys(st)
+    assert empty.any()
+    for n in ("k", "v"):
+        st[n][empty] = 0
+    o, lse = spans.run_forward(st)
+    spans.check_forward(st, o, lse)
+    bad = dict(st, **{n: st[n].clone() for n in ("k", "v")})
+    for n in ("k", "v"):
+        bad[n][empty] = junk
+    o2, lse2 = spans.run_forward(bad)
+    spans.check_forward(st, o2, lse2)
+    assert torch.equal(lse, lse2)
+
+
+def test_keys_that_nobody_sees_cost_little():
+    """NaN past the end of a cache and between caches; took 480 and 24 times as long."""
+    for lo, hi, keys in ((torch.tensor([0]), torch.tensor([32700]), 33000),
+                         (*caches([1000 + 61 * i for i in range(16)], 1, 2048), 16 * 2048)):
+        st = problem(lo, hi, keys, (32, 8, 128))
+        clean = time_us(forward_call(st))
+        for n in ("k", "v"):
+            st[n][unseen_keys(st)] = math.nan
+        assert time_us(forward_call(st)) < 10 * clean
+
+
+@pytest.mark.parametrize("junk", [0.0, math.nan])
+def test_more_items_than_a_round_has(junk):
+    """80 items an SM, of heads that are all the same; where keys that nobody sees are NaN, the
+    items that load some are taken twice."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    heads = 256
+    total = -(-80 * sms // heads) * 256 - 57
+    lengths, g = [], torch.Generator().manual_seed(5)
+    while sum(lengths) < total - 300:
+        lengths.append(int(torch.randint(1, 200, (1,), generator=g)))
+    lengths[-1] -= sum(lengths) - (total - 300)
+    lo, hi = spans.with_nothing(spans.documents(lengths), 300)
+    one = problem(lo, hi, total, (1, 1, 16), seed=6)
+    for n in ("k", "v"):
+        one[n][total - 300:] = junk
+    every = {n: one[n].expand(total, heads, 16).contiguous() for n in ("q", "k", "v")}
+    o, lse = spans.run_forward(dict(one, **every))
+    assert torch.equal(o, o[:, :1].expand_as(o)) and torch.equal(lse, lse[:, :1].expand_as(lse))
+    for n in ("k", "v"):
+        one[n][total - 300:] = 0
+    spans.check_forward(one, o[:, :1], lse[:, :1])
