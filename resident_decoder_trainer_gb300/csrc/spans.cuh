@@ -419,35 +419,42 @@ __device__ __forceinline__ bool next_round(Rounds* r, int threads, unsigned long
   return true;
 }
 
-// Waits for a tile of 128 keys from `base` on (chunks of 64 columns, 128 bytes a row,
-// one behind the other) and clears the rows that none of the `n` queries from t0 on
-// sees; then arrives on `full`. Whole warp.
+// Clears the rows 32 w + i of a tile of 128 rows (chunks of 64 columns, 128 bytes a row,
+// one behind the other) that have no bit i in `keep`. Whole warp.
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int d, int w, uint32_t keep) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int row = lane >> 3; row < 32; row += 4)
+    if (!(keep >> row & 1u))
+#pragma unroll 1
+      for (int c = 0; c < d; c += 64)
+        *reinterpret_cast<uint4*>(tile + c * 256 + (32 * w + row) * 128 + 16 * (lane & 7)) =
+            make_uint4(0u, 0u, 0u, 0u);
+}
+// What a warp has cleared, where the tensor cores see it once `bar` has been arrived on.
+__device__ __forceinline__ void hand_over(uint32_t bar) {
+  fence_proxy_async_smem();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+// Waits for a tile of 128 keys from `base` on and clears the rows that none of the `n`
+// queries from t0 on sees; then arrives on `full`. Whole warp.
 __device__ __forceinline__ bool clear_unseen(const SpanArgs& a, int t0, int n, int base,
                                              uint8_t* tile, uint32_t raw, uint32_t parity,
                                              uint32_t full, const Patience& err) {
-  const int lane = threadIdx.x & 31;
   if (!warp_wait(raw, parity, err)) return false;
 #pragma unroll 1
   for (int w = 0; w < 4; ++w) {
     uint32_t seen = 0u;
 #pragma unroll 1
-    for (int i = lane; i < n; i += 32) {
+    for (int i = threadIdx.x & 31; i < n; i += 32) {
       int x, y;
       a.span(t0 + i, x, y);
       if (x < y) seen |= bits_between(x - base - 32 * w, y - base - 32 * w);
     }
-    seen = __reduce_or_sync(0xffffffffu, seen);
-#pragma unroll 1
-    for (int row = lane >> 3; row < 32; row += 4)
-      if (!(seen >> row & 1u))
-#pragma unroll 1
-        for (int c = 0; c < a.d; c += 64)
-          *reinterpret_cast<uint4*>(tile + c * 256 + (32 * w + row) * 128 + 16 * (lane & 7)) =
-              make_uint4(0u, 0u, 0u, 0u);
+    clear_rows(tile, a.d, w, __reduce_or_sync(0xffffffffu, seen));
   }
-  fence_proxy_async_smem();  // for the tensor cores
-  __syncwarp();
-  if (lane == 0) mbar_arrive(full);
+  hand_over(full);
   return true;
 }
 

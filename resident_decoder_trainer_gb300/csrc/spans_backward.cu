@@ -13,9 +13,10 @@
 // In both, warp 0 loads by TMA, warp 1 issues the MMAs, and warps 4-19 do the
 // elementwise work: TMEM lanes 32 (w mod 4) on, columns 32 (w / 4 - 1) on.
 //
-// Rows of dq, dk and dv that are not finite are computed again one by one
-// (row_dq, row_dkdv): a NaN or infinity where a query does not see a key, times
-// 0, would reach them. Not where they see a query whose own values are not
+// A NaN or infinity where a query does not see a key, times 0, would reach sums. Rows of
+// queries that see nothing may be memory that nobody wrote: they are cleared in
+// shared memory. Other rows of dq, dk and dv that are not finite are computed again
+// one by one (row_dq, row_dkdv). Not where they see a query whose own values are not
 // finite: what they hold is not finite by right, and a batch that has diverged
 // throughout costs no more than another.
 //
@@ -43,7 +44,7 @@ constexpr float kNoRow = -1e30f;  // negated lse of a row that sees nothing: p =
 // that see nothing (or are none) are left out of both: their p is 0 unmasked.
 struct TileSpan {
   int first, end;          // any
-  int all_first, all_end;  // all
+  int all_first, all_end;  // all; ~all_first where some row of a query sees nothing
 };
 
 struct Args {
@@ -129,10 +130,14 @@ __global__ void __launch_bounds__(kPrepThreads, 4) prepare_kernel(const __grid_c
     if (g == 0) {
       const int row = threadIdx.x;
       TileSpan s = none;
+      bool blind = false;
       if (row < 128) {
         const int in = static_cast<int>(row * inv_rep >> 16), t = tile * ar.tl.per + in;
         int x = 0, y = 0;
-        if (in < ar.tl.per && t < a.queries) a.span(t, x, y);
+        if (in < ar.tl.per && t < a.queries) {
+          a.span(t, x, y);
+          blind = x >= y;
+        }
         if (x < y)
           take(s, x, y);
         else
@@ -141,6 +146,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) prepare_kernel(const __grid_c
         ar.len[tile * int64_t{128} + row] = y - x;
       }
       s = joined(s);
+      if (__syncthreads_or(blind)) s.all_first = ~s.all_first;
       if (row == 0) ar.tiles[tile] = s;
     }
     // the row that this lane finishes
@@ -371,8 +377,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                  i_full = o_empty + 8 * OST, i_empty = i_full + 8 * IST, s_full = i_empty + 8 * IST,
                  dp_full = s_full + 8, p_ready = dp_full + 8, ds_ready = p_ready + 8,
                  fin = ds_ready + 8, acc_free = fin + 8, next = acc_free + 8, left_it = next + 8,
-                 decided = left_it + 8, drain = decided + 8;
-  static_assert(8 * (2 * (QST + OST + IST) + 12) <= 280, "");
+                 decided = left_it + 8, drain = decided + 8,
+                 q_raw = drain + 8, o_raw = q_raw + 8;  // come, but with rows to be cleared
+  static_assert(8 * (2 * (QST + OST + IST) + 14) <= 280, "");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 280);
   volatile int* decision = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + 284);
   Meta* meta = reinterpret_cast<Meta*>(smem + C::OFF_META);
@@ -405,6 +412,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(left_it, kEltThreads);
     mbar_init(decided, 1);
     mbar_init(drain, 1);
+    mbar_init(q_raw, 1);
+    mbar_init(o_raw, 1);
     fence_mbar_init();
     tma_prefetch_desc(&tq);
     tma_prefetch_desc(&tdo);
@@ -433,11 +442,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // --------------------------------------------------------- producer
     bool ok = true;
     uint32_t r = 0, tiles = 0, loaded = 0;  // steps, row tiles, items with any so far
+    uint32_t raws = 0;                      // row tiles with rows to be cleared
     int item = blockIdx.x;
     for (uint32_t it = 0; ok && item >= 0; ++it) {
       const int half = item % ar.parts, x = item / ar.parts;
       const int g = x % a.nkv, n0 = x / a.nkv * 128, n1 = min(n0 + 128, a.keys);
-      // calls f(tile, full) for the row tiles that see any of the keys, until it is false
+      // calls f(tile, full, blind) for the row tiles that see any of the keys, until it is false
       auto each = [&](auto f) {
         bool on = true;
         for (int g0 = 0; g0 < ar.groups && on; g0 += 32) {
@@ -448,11 +458,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             TileSpan s = {0, 0, 0, 0};
             if (tile < ar.tl.tiles) s = ar.tiles[tile];
             unsigned meets = __ballot_sync(0xffffffffu, s.first < n1 && s.end > n0);
-            const unsigned full =
-                __ballot_sync(0xffffffffu, s.all_first <= n0 && s.all_end >= n1);
+            const unsigned blind = __ballot_sync(0xffffffffu, s.all_first < 0);
+            const unsigned full = __ballot_sync(
+                0xffffffffu, (s.all_first ^ (s.all_first >> 31)) <= n0 && s.all_end >= n1);
             for (; meets && on; meets &= meets - 1) {
               const int i = __ffs(meets) - 1;
-              on = f(first + i, (full >> i) & 1);
+              on = f(first + i, (full >> i) & 1, (blind >> i) & 1);
             }
           }
         }
@@ -460,22 +471,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool shared = false;
       if (ar.parts > 1) {
         int count = 0;
-        each([&](int, int) { return ++count < kShareFrom; });
+        each([&](int, int, int) { return ++count < kShareFrom; });
         shared = count >= kShareFrom;
       }
       const bool mine = shared || half == 0;
       bool some = false;  // K and V are under way
       int met = 0;
-      auto send = [&](int tile, int full) {
+      // blind: rows that see nothing, and may be anything, are cleared in Q and dO
+      auto send = [&](int tile, int full, int blind) {
+        const uint32_t sq = tiles % QST, so = tiles % OST;
         if (lane == 0) {
           if (tile >= 0) {
-            const uint32_t sq = tiles % QST, q = sbase + C::OFF_Q + sq * C::TILE;
+            const uint32_t q = sbase + C::OFF_Q + sq * C::TILE,
+                           bar = blind ? q_raw : q_full + 8 * sq;
             ok = wait_for(q_empty + 8 * sq, ((tiles / QST) & 1) ^ 1, err);
             if (ok) {
-              mbar_arrive_expect_tx(q_full + 8 * sq, chunks * used * 128);
+              mbar_arrive_expect_tx(bar, chunks * used * 128);
               for (int c = 0; c < chunks; ++c)
-                tma_load_3d(q + c * C::CHUNK, &tq, q_full + 8 * sq, c * 64, g * a.rep,
-                            tile * ar.tl.per);
+                tma_load_3d(q + c * C::CHUNK, &tq, bar, c * 64, g * a.rep, tile * ar.tl.per);
             }
             if (ok && !some) ok = wait_for(kv_empty, (loaded & 1) ^ 1, err);
             if (ok && !some) {
@@ -497,18 +510,27 @@ __global__ void __launch_bounds__(kThreads, 1)
               mbar_arrive_expect_tx(i_full + 8 * si, 1024);
               bulk_load_1d(row, ar.neg_lse + at, 512, i_full + 8 * si);
               bulk_load_1d(row + 512, ar.neg_d + at, 512, i_full + 8 * si);
-              const uint32_t so = tiles % OST, o = sbase + C::OFF_DO + so * C::TILE;
+              const uint32_t o = sbase + C::OFF_DO + so * C::TILE,
+                             bar = blind ? o_raw : o_full + 8 * so;
               ok = wait_for(o_empty + 8 * so, ((tiles / OST) & 1) ^ 1, err);
               if (ok) {
-                mbar_arrive_expect_tx(o_full + 8 * so, chunks * used * 128);
+                mbar_arrive_expect_tx(bar, chunks * used * 128);
                 for (int c = 0; c < chunks; ++c)
-                  tma_load_3d(o + c * C::CHUNK, &tdo, o_full + 8 * so, c * 64, g * a.rep,
-                              tile * ar.tl.per);
+                  tma_load_3d(o + c * C::CHUNK, &tdo, bar, c * 64, g * a.rep, tile * ar.tl.per);
               }
             }
           }
         }
         ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0);
+        for (int x = 0; x < 2 && ok && blind; ++x) {
+          ok = warp_wait(x ? o_raw : q_raw, raws & 1, err);
+          if (!ok) break;
+          for (int w = 0; w < 4; ++w)
+            clear_rows(smem + (x ? C::OFF_DO + so * C::TILE : C::OFF_Q + sq * C::TILE), a.d, w,
+                       __ballot_sync(0xffffffffu, ar.len[tile * int64_t{128} + 32 * w + lane] > 0));
+          hand_over(x ? o_full + 8 * so : q_full + 8 * sq);
+        }
+        raws += blind;
         ++r;
         if (tile >= 0) {
           ++tiles;
@@ -516,19 +538,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       if (mine)
-        each([&](int tile, int full) {
-          if (!shared || (met++ & 1) == half) send(tile, full);
+        each([&](int tile, int full, int blind) {
+          if (!shared || (met++ & 1) == half) send(tile, full, blind);
           return ok;
         });
       if (some) ++loaded;
       // asked for now, not before: an item that waits here could have been another SM's
       if (lane == 0) next_cta_request(sbase + C::OFF_NEXT, next);
-      if (ok) send(kEnd, shared ? kShared + half : mine ? kAlone : kNothing);
+      if (ok) send(kEnd, shared ? kShared + half : mine ? kAlone : kNothing, 0);
       // waited for on the way out too: the answer is written to this CTA's memory
       const bool answered = warp_wait(next, it & 1, err);
       ok = ok && answered;
       if (ok) item = next_cta_answer(sbase + C::OFF_NEXT);
-      if (ok && item < 0) send(kStop, 0);
+      if (ok && item < 0) send(kStop, 0, 0);
     }
   } else if (warp == 1) {
     if (elect_one()) {

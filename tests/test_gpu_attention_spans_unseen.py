@@ -321,3 +321,46 @@ def test_more_items_than_a_round_has(junk):
     for n in ("k", "v"):
         one[n][total - 300:] = 0
     spans.check_forward(one, o[:, :1], lse[:, :1])
+
+
+def blind_queries(st):
+    return st["lo"].clamp(min=0) >= st["hi"].clamp(max=st["k"].shape[0])
+
+
+def packed(heads=(32, 8, 128)):
+    g, lengths, unused = torch.Generator().manual_seed(1), [], 131
+    while sum(lengths) < 4096 - unused:
+        n = int(torch.randint(1, 1025, (1,), generator=g))
+        lengths.append(min(n, 4096 - unused - sum(lengths)))
+    lo, hi = spans.with_nothing(spans.documents(lengths), unused)
+    return problem(lo, hi, 4096, heads)
+
+
+@pytest.mark.parametrize("mask", UNSEEN)
+@pytest.mark.parametrize("heads,cap", [((32, 8, 128), 0.0), ((8, 8, 64), 30.0), ((4, 1, 128), 20.0),
+                                       ((9, 3, 48), 0.0), ((4, 2, 16), 0.0)], ids=str)
+def test_the_gradient_of_queries_that_see_nothing(mask, heads, cap):
+    """Whatever their rows hold."""
+    keys, of = UNSEEN[mask]
+    lo, hi = of()
+    lo, hi = (torch.cat([x[:7], torch.tensor([3, 9, 2]), x[7:]]) for x in (lo, hi))
+    hi[len(hi[:7]):len(hi[:7]) + 3] = 1  # some between the others
+    st = problem(lo, hi, keys, heads, seed=13, cap=cap)
+    blind = blind_queries(st)
+    o, lse = spans.run_forward(st)
+    bad = dict(st, **{n: st[n].clone() for n in ("q", "d_o", "d_lse")})
+    for n, junk in (("q", math.nan), ("d_o", -math.inf), ("d_lse", math.nan)):
+        bad[n][blind] = junk
+    got = spans.run_backward(bad, o, lse)
+    spans.check_backward(st, o, lse, got)
+    want = spans.run_backward(st, o, lse)
+    assert all(torch.equal(got[n], want[n]) for n in ("k", "v"))
+
+
+def test_the_gradient_of_queries_that_see_nothing_costs_little():
+    """NaN in the unused end of a packed batch's q and d_o; took 100 times as long."""
+    st = packed()
+    clean = time_us(backward_call(st))
+    for n in ("q", "d_o"):
+        st[n][blind_queries(st)] = math.nan
+    assert time_us(backward_call(st)) < 3 * clean
