@@ -841,11 +841,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------------- dQ
+// The columns [c0, c1) of rows of dq that a warp has found not finite (query t and head
+// h of each lane, t = -1: none), all of key head g, computed again unless they are so
+// by right.
+__device__ __noinline__ void dq_again(const SpanArgs& a, int g, int t, int h, int c0, int c1) {
+  __syncwarp();  // other lanes store what a row's own lane stored
+  int first = 0, end = 0;
+  if (t >= 0) a.span(t, first, end);
+  for (unsigned again = bad_rows(a, a.k, g, t >= 0 ? a.dq.at(t, h) : nullptr, c0, c1, first, end);
+       again; again &= again - 1) {
+    const int from = __ffs(again) - 1;
+    row_dq(a, __shfl_sync(0xffffffffu, t, from), __shfl_sync(0xffffffffu, h, from), c0, c1);
+  }
+}
+
 constexpr int kItemRing = 4;
 struct Item {
-  int index;     // row tile and key head; -1: no more
+  int index;     // row tile and key head, with kSecond or not; -1: no more in this round
   int first, n;  // first key, key tiles
-  int unused;
 };
 
 template <int D>
@@ -855,11 +868,12 @@ struct QCfg {
   static constexpr int KST = D == 128 ? 3 : 4, VST = D == 128 ? 2 : 4;
   static constexpr uint32_t OFF_Q = 0, OFF_DO = TILE, OFF_K = 2 * TILE, OFF_V = OFF_K + KST * TILE,
                             OFF_ROW = OFF_V + VST * TILE,  // [neg_lse, neg_d, lo, len][128]
-      OFF_ITEM = OFF_ROW + 2048, OFF_BAR = OFF_ITEM + kItemRing * sizeof(Item);
-  static constexpr uint32_t OFF_NEXT = OFF_BAR + 320;
+      OFF_ITEM = OFF_ROW + 2048, OFF_RAN = OFF_ITEM + kItemRing * sizeof(Item),
+                            OFF_BAR = OFF_RAN + kRound * sizeof(int);
+  static constexpr uint32_t OFF_NEXT = OFF_BAR + 352;
   static constexpr size_t SMEM = OFF_NEXT + 16;  // at a multiple of 1024, which is checked
   static constexpr uint32_t T_S = 0, T_DP = 128, T_DQ = 256, T_DS = 384, TMEM_COLS = 512;
-  static_assert(SMEM <= 232448, "");
+  static_assert(SMEM <= 232448 && OFF_NEXT % 16 == 0, "");
 };
 
 template <int D, bool CAP>
@@ -884,9 +898,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                  v_full = k_empty + 8 * KST, v_empty = v_full + 8 * VST, s_full = v_empty + 8 * VST,
                  s_free = s_full + 8, ds_ready = s_free + 8, ds_free = ds_ready + 16, dq_done = ds_free + 16,
                  dq_free = dq_done + 8, drain = dq_free + 8, item_full = drain + 8,
-                 item_empty = item_full + 8 * kItemRing, next = item_empty + 8 * kItemRing;
-  static_assert(8 * (2 + 2 * KST + 2 * VST + 10 + 2 * kItemRing) <= 312, "");
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 312);
+                 item_empty = item_full + 8 * kItemRing, next = item_empty + 8 * kItemRing,
+                 k_raw = next + 8;  // K has come that is to be cleared
+  static_assert(8 * (2 + 2 * KST + 2 * VST + 11 + 2 * kItemRing) <= 312, "");
+  Rounds* rounds = reinterpret_cast<Rounds*>(smem + C::OFF_BAR + 312);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 344);
+  static_assert(312 + sizeof(Rounds) <= 344 && C::OFF_BAR % 8 == 0, "");
+  int* ran = reinterpret_cast<int*>(smem + C::OFF_RAN);  // the items of the round
   Item* ring = reinterpret_cast<Item*>(smem + C::OFF_ITEM);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -924,6 +942,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(dq_free, kEltThreads);
     mbar_init(drain, 1);
     mbar_init(next, 1);
+    mbar_init(k_raw, 1);
+    *rounds = Rounds{};
     fence_mbar_init();
     tma_prefetch_desc(&tq);
     tma_prefetch_desc(&tdo);
@@ -937,140 +957,207 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   after_previous_kernel();
 
+  unsigned long long redo = 0ull;
   if (warp < 4) regs_dec<56>();
   if (warp == 0) {
-    if (lane == 0) {
-      // --------------------------------------------------------- producer
-      bool ok = true;
-      uint32_t jg = 0;
-      int loaded = 0;
-      int item = blockIdx.x;
-      for (uint32_t it = 0; ok; ++it) {
-        const int slot = it % kItemRing;
-        ok = wait_for(item_empty + 8 * slot, ((it / kItemRing) & 1) ^ 1, err);
-        if (!ok) break;
-        if (item < 0) {
-          ring[slot].index = -1;
-          mbar_arrive(item_full + 8 * slot);
-          break;
+    // ----------------------------------------------------------- producer
+    bool ok = true;
+    uint32_t jg = 0, it = 0, asked = 0, raws = 0;
+    int loaded = 0;
+    int item = blockIdx.x;
+    // an item's place in the ring; what it needs of its row tile
+    auto publish = [&](int index, int first, int n) {
+      ring[it % kItemRing] = Item{index, first, n};
+      mbar_arrive(item_full + 8 * (it % kItemRing));
+    };
+    auto free_slot = [&]() {
+      return wait_for(item_empty + 8 * (it % kItemRing), ((it / kItemRing) & 1) ^ 1, err);
+    };
+    do {
+      if (lane == 0) rounds->start = it;
+      const bool second = redo != 0ull;
+      // a step of an item's loads: tile j of K or V
+      auto load = [&](int j, int first, int g, uint32_t bar, uint32_t empty, int stages,
+                      uint32_t off, const CUtensorMap* map) -> bool {
+        const uint32_t jj = jg + j, st = jj % stages;
+        if (!wait_for(empty + 8 * st, ((jj / stages) & 1) ^ 1, err)) return false;
+        if (!bar) bar = empty - 8 * stages + 8 * st;  // the stage's own, which lie before
+        mbar_arrive_expect_tx(bar, chunks * C::CHUNK);
+        for (int c = 0; c < chunks; ++c)
+          tma_load_3d(sbase + off + st * C::TILE + c * C::CHUNK, map, bar, c * 64, g,
+                      first + j * 128);
+        return true;
+      };
+      auto load_rows = [&](int tile, int g) -> bool {
+        if (!wait_for(q_empty, (loaded & 1) ^ 1, err)) return false;
+        const int64_t at = (static_cast<int64_t>(g) * ar.tl.tiles + tile) * 128;
+        mbar_arrive_expect_tx(q_full, 2 * chunks * used * 128 + 2048);
+        for (int c = 0; c < chunks; ++c) {
+          tma_load_3d(sbase + C::OFF_Q + c * C::CHUNK, &tq, q_full, c * 64, g * a.rep,
+                      tile * ar.tl.per);
+          tma_load_3d(sbase + C::OFF_DO + c * C::CHUNK, &tdo, q_full, c * 64, g * a.rep,
+                      tile * ar.tl.per);
         }
-        int tile, g;
-        place(item, tile, g);
-        const int first = ar.tiles[tile].first, n = (ar.tiles[tile].end - first + 127) / 128;
-        ring[slot] = Item{item, first, n, 0};
-        mbar_arrive(item_full + 8 * slot);
-        auto load = [&](int j, uint32_t full, uint32_t empty, int stages, uint32_t off,
-                        const CUtensorMap* map) -> bool {
-          const uint32_t jj = jg + j, st = jj % stages;
-          if (!wait_for(empty + 8 * st, ((jj / stages) & 1) ^ 1, err)) return false;
-          mbar_arrive_expect_tx(full + 8 * st, chunks * C::CHUNK);
-          for (int c = 0; c < chunks; ++c)
-            tma_load_3d(sbase + off + st * C::TILE + c * C::CHUNK, map, full + 8 * st, c * 64, g,
-                        first + j * 128);
-          return true;
-        };
-        if (n > 0) {
-          // K's first tile does not wait for the item before to be done with its Q
-          ok = load(0, k_full, k_empty, KST, C::OFF_K, &tk) &&
-               wait_for(q_empty, (loaded & 1) ^ 1, err);
-          if (ok) {
-            const int64_t at = (static_cast<int64_t>(g) * ar.tl.tiles + tile) * 128;
-            mbar_arrive_expect_tx(q_full, 2 * chunks * used * 128 + 2048);
-            for (int c = 0; c < chunks; ++c) {
-              tma_load_3d(sbase + C::OFF_Q + c * C::CHUNK, &tq, q_full, c * 64, g * a.rep,
-                          tile * ar.tl.per);
-              tma_load_3d(sbase + C::OFF_DO + c * C::CHUNK, &tdo, q_full, c * 64, g * a.rep,
-                          tile * ar.tl.per);
+        bulk_load_1d(sbase + C::OFF_ROW, ar.neg_lse + at, 512, q_full);
+        bulk_load_1d(sbase + C::OFF_ROW + 512, ar.neg_d + at, 512, q_full);
+        bulk_load_1d(sbase + C::OFF_ROW + 1024, ar.lo + tile * int64_t{128}, 512, q_full);
+        bulk_load_1d(sbase + C::OFF_ROW + 1536, ar.len + tile * int64_t{128}, 512, q_full);
+        return true;
+      };
+      if (second) {
+        // items once more, K by way of k_raw, its rows that nobody sees cleared; whole warp
+        for (; redo && ok; redo &= redo - 1, ++it) {
+          const int again = ran[__ffsll(redo) - 1];
+          int tile, g;
+          place(again, tile, g);
+          const int first = ar.tiles[tile].first, n = (ar.tiles[tile].end - first + 127) / 128;
+          if (lane == 0) {
+            ok = free_slot();
+            if (ok) publish(again | kSecond, first, n);
+          }
+          ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0);
+          for (int j = 0; j < n && ok; ++j, ++raws) {
+            if (lane == 0)
+              ok = load(j, first, g, k_raw, k_empty, KST, C::OFF_K, &tk) &&
+                   (j > 0 || load_rows(tile, g)) &&
+                   load(j, first, g, 0u, v_empty, VST, C::OFF_V, &tv);
+            ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0);
+            const uint32_t st = (jg + j) % KST;
+            const int t0 = tile * ar.tl.per;
+            ok = ok && clear_unseen(a, t0, min(ar.tl.per, a.queries - t0), first + j * 128,
+                                    smem + C::OFF_K + st * C::TILE, k_raw, raws & 1,
+                                    k_full + 8 * st, err);
+          }
+          if (n > 0) {
+            jg += n;
+            ++loaded;
+          }
+        }
+      }
+      if (lane == 0) {
+        for (int of = 0; ok; ++of, ++it) {
+          ok = free_slot();
+          if (!ok) break;
+          if (item < 0 || second || of == kRound) {
+            rounds->left = item >= 0;
+            publish(-1, 0, 0);
+            ++it;
+            break;
+          }
+          int tile, g;
+          place(item, tile, g);
+          const int first = ar.tiles[tile].first, n = (ar.tiles[tile].end - first + 127) / 128;
+          publish(item, first, n);
+          ran[of] = item;
+          if (n > 0) {
+            // K's first tile does not wait for the item before to be done with its Q
+            ok = load(0, first, g, 0u, k_empty, KST, C::OFF_K, &tk) && load_rows(tile, g);
+            for (int j = 0; j < n && ok; ++j) {
+              ok = (j == 0 || load(j, first, g, 0u, k_empty, KST, C::OFF_K, &tk)) &&
+                   load(j, first, g, 0u, v_empty, VST, C::OFF_V, &tv);
             }
-            bulk_load_1d(sbase + C::OFF_ROW, ar.neg_lse + at, 512, q_full);
-            bulk_load_1d(sbase + C::OFF_ROW + 512, ar.neg_d + at, 512, q_full);
-            bulk_load_1d(sbase + C::OFF_ROW + 1024, ar.lo + tile * int64_t{128}, 512, q_full);
-            bulk_load_1d(sbase + C::OFF_ROW + 1536, ar.len + tile * int64_t{128}, 512, q_full);
+            jg += n;
+            ++loaded;
           }
+          // asked for now, not before: an item that waits here could have been another SM's;
+          // waited for on the way out too: the answer is written to this CTA's memory
+          next_cta_request(sbase + C::OFF_NEXT, next);
+          const bool answered = wait_for(next, asked++ & 1, err);
+          ok = ok && answered;
+          if (ok) item = next_cta_answer(sbase + C::OFF_NEXT);
+        }
+        if (!ok) rounds->lost = 1;
+      }
+      // the whole warp goes on from what its first lane has counted
+      ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0);
+      it = __shfl_sync(0xffffffffu, it, 0);
+      jg = __shfl_sync(0xffffffffu, jg, 0);
+      loaded = __shfl_sync(0xffffffffu, loaded, 0);
+    } while (next_round<true>(rounds, kThreads, redo));
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA
+    constexpr uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0);
+    const uint32_t id_q = idesc_bf16_f32(128, a.d, 0, 1);
+    const int ksteps = a.d / 16;
+    const uint32_t q_desc = desc_low(sbase + C::OFF_Q, 16);
+    const uint32_t o_desc = desc_low(sbase + C::OFF_DO, 16);
+    auto scores = [&](uint32_t to, uint32_t rows, uint32_t keys) {
+      const uint32_t k2 = not_hoisted(desc_low(keys, 16));
+      rows = not_hoisted(rows);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        if (k >= ksteps) break;
+        const uint32_t off = ((k >> 2) * C::CHUNK + (k & 3) * 32) >> 4;
+        tc_mma_low(tmem + to, rows + off, k2 + off, id_s, k > 0);
+      }
+    };
+    bool ok = true;
+    uint32_t jg = 0;
+    int loaded = 0, it = 0;
+    do {
+      if (elect_one()) {
+        bool stop = false;
+        for (; ok; ++it) {
+          const int slot = it % kItemRing;
+          if (!wait_for(item_full + 8 * slot, (it / kItemRing) & 1, err)) break;
+          const int index = ring[slot].index, n = ring[slot].n;
+          mbar_arrive(item_empty + 8 * slot);
+          if (index < 0) {
+            ++it;
+            stop = true;
+            break;
+          }
+          if (n == 0) continue;
+          // S and dP of key tile j, once those of the one before are in registers
+          auto issue = [&](int j) -> bool {
+            const uint32_t jj = jg + j, ks = jj % KST, vs = jj % VST;
+            if (!wait_for(k_full + 8 * ks, (jj / KST) & 1, err) ||
+                !wait_for(v_full + 8 * vs, (jj / VST) & 1, err) ||
+                !wait_for(s_free, (jj & 1) ^ 1, err))
+              return false;
+            tc_fence_after();
+            scores(C::T_S, q_desc, sbase + C::OFF_K + ks * C::TILE);
+            scores(C::T_DP, o_desc, sbase + C::OFF_V + vs * C::TILE);
+            tc_commit(s_full);
+            tc_commit(v_empty + 8 * vs);
+            if (j + 1 == n) tc_commit(q_empty);  // the item's last read of Q and dO
+            return true;
+          };
+          ok = wait_for(q_full, loaded & 1, err) && issue(0);
           for (int j = 0; j < n && ok; ++j) {
-            ok = (j == 0 || load(j, k_full, k_empty, KST, C::OFF_K, &tk)) &&
-                 load(j, v_full, v_empty, VST, C::OFF_V, &tv);
+            const uint32_t jj = jg + j;
+            const int ks = jj % KST;
+            if (j + 1 < n) ok = issue(j + 1);
+            // dQ of the item before has been read out of TMEM
+            if (ok && j == 0) ok = wait_for(dq_free, (loaded & 1) ^ 1, err);
+            if (ok) ok = wait_for(ds_ready + 8 * (jj & 1), (jj >> 1) & 1, err);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t k_desc =
+                not_hoisted(desc_low(sbase + C::OFF_K + ks * C::TILE, C::CHUNK));
+            const uint32_t ds = tmem + C::T_DS + (jj & 1) * 64;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              tc_mma_ts_low(tmem + C::T_DQ, ds + 8 * k, k_desc + k * 128, id_q, (j | k) != 0);
+            tc_commit(ds_free + 8 * (jj & 1));
+            tc_commit(k_empty + 8 * ks);
           }
+          if (ok) tc_commit(dq_done);
           jg += n;
           ++loaded;
         }
-        // asked for now, not before: an item that waits here could have been another SM's;
-        // waited for on the way out too: the answer is written to this CTA's memory
-        next_cta_request(sbase + C::OFF_NEXT, next);
-        const bool answered = wait_for(next, it & 1, err);
-        ok = ok && answered;
-        if (ok) item = next_cta_answer(sbase + C::OFF_NEXT);
+        if (!stop) rounds->lost = 1;
       }
-    }
-  } else if (warp == 1) {
+      __syncwarp();
+    } while (next_round<true>(rounds, kThreads, redo));
     if (elect_one()) {
-      // -------------------------------------------------------------- MMA
-      constexpr uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0);
-      const uint32_t id_q = idesc_bf16_f32(128, a.d, 0, 1);
-      const int ksteps = a.d / 16;
-      const uint32_t q_desc = desc_low(sbase + C::OFF_Q, 16);
-      const uint32_t o_desc = desc_low(sbase + C::OFF_DO, 16);
-      auto scores = [&](uint32_t to, uint32_t rows, uint32_t keys) {
-        const uint32_t k2 = not_hoisted(desc_low(keys, 16));
-        rows = not_hoisted(rows);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          if (k >= ksteps) break;
-          const uint32_t off = ((k >> 2) * C::CHUNK + (k & 3) * 32) >> 4;
-          tc_mma_low(tmem + to, rows + off, k2 + off, id_s, k > 0);
-        }
-      };
-      bool ok = true;
-      uint32_t jg = 0;
-      int loaded = 0;
-      for (int it = 0; ok; ++it) {
-        const int slot = it % kItemRing;
-        if (!wait_for(item_full + 8 * slot, (it / kItemRing) & 1, err)) break;
-        const int index = ring[slot].index, n = ring[slot].n;
-        mbar_arrive(item_empty + 8 * slot);
-        if (index < 0) break;
-        if (n == 0) continue;
-        // S and dP of key tile j, once those of the one before are in registers
-        auto issue = [&](int j) -> bool {
-          const uint32_t jj = jg + j, ks = jj % KST, vs = jj % VST;
-          if (!wait_for(k_full + 8 * ks, (jj / KST) & 1, err) ||
-              !wait_for(v_full + 8 * vs, (jj / VST) & 1, err) ||
-              !wait_for(s_free, (jj & 1) ^ 1, err))
-            return false;
-          tc_fence_after();
-          scores(C::T_S, q_desc, sbase + C::OFF_K + ks * C::TILE);
-          scores(C::T_DP, o_desc, sbase + C::OFF_V + vs * C::TILE);
-          tc_commit(s_full);
-          tc_commit(v_empty + 8 * vs);
-          if (j + 1 == n) tc_commit(q_empty);  // the item's last read of Q and dO
-          return true;
-        };
-        ok = wait_for(q_full, loaded & 1, err) && issue(0);
-        for (int j = 0; j < n && ok; ++j) {
-          const uint32_t jj = jg + j;
-          const int ks = jj % KST;
-          if (j + 1 < n) ok = issue(j + 1);
-          // dQ of the item before has been read out of TMEM
-          if (ok && j == 0) ok = wait_for(dq_free, (loaded & 1) ^ 1, err);
-          if (ok) ok = wait_for(ds_ready + 8 * (jj & 1), (jj >> 1) & 1, err);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t k_desc = not_hoisted(desc_low(sbase + C::OFF_K + ks * C::TILE, C::CHUNK));
-          const uint32_t ds = tmem + C::T_DS + (jj & 1) * 64;
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            tc_mma_ts_low(tmem + C::T_DQ, ds + 8 * k, k_desc + k * 128, id_q, (j | k) != 0);
-          tc_commit(ds_free + 8 * (jj & 1));
-          tc_commit(k_empty + 8 * ks);
-        }
-        if (ok) tc_commit(dq_done);
-        jg += n;
-        ++loaded;
-      }
       tc_commit(drain);
       mbar_wait(drain, 0, nullptr);
     }
-  } else if (warp >= 4) {
+  } else if (warp < 4) {
+    while (next_round<true>(rounds, kThreads, redo)) {
+    }
+  } else {
     regs_inc<104>();
     // --------------------------- dS: one row, 32 of a key tile's 128 columns
     const int quarter = warp & 3, block = (warp - 4) >> 2;
@@ -1079,109 +1166,113 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row_t = row / a.rep, row_h = row % a.rep;
     bool ok = true;
     uint32_t jg = 0;
-    int loaded = 0;
-    for (int it = 0; ok; ++it) {
-      const int slot = it % kItemRing;
-      if (!warp_wait(item_full + 8 * slot, (it / kItemRing) & 1, err)) break;
-      const int item = ring[slot].index, first = ring[slot].first, n = ring[slot].n;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(item_empty + 8 * slot);
-      if (item < 0) break;
-      float nl = 0.f, nd = 0.f;
-      int lo = 0, len = 0;
-      if (n > 0) {
-        if (!warp_wait(q_full, loaded & 1, err)) break;
-        const float* rows = reinterpret_cast<const float*>(smem + C::OFF_ROW);
-        nl = rows[row];
-        nd = rows[128 + row];
-        lo = __float_as_int(rows[256 + row]);
-        len = __float_as_int(rows[384 + row]);
+    int loaded = 0, it = 0;
+    do {
+      bool stop = false;
+      for (; ok; ++it) {
+        const int slot = it % kItemRing;
+        if (!warp_wait(item_full + 8 * slot, (it / kItemRing) & 1, err)) break;
+        const int item = ring[slot].index, first = ring[slot].first, n = ring[slot].n;
         __syncwarp();
-        if (lane == 0) mbar_arrive(q_empty);
-      }
-      const float2 nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
-      const bool finite = finite_row(nl, nd);
-      for (int j = 0; j < n; ++j) {
-        const uint32_t jj = jg + j;
-        const int buf = jj & 1;
-        ok = warp_wait(s_full, jj & 1, err);
-        if (!ok) break;
-        tc_fence_after();
-        uint32_t sv[32], dp[32];
-        tmem_ld32(tmem + lane_base + C::T_S + block * 32, sv);
-        tmem_ld32(tmem + lane_base + C::T_DP + block * 32, dp);
-        tmem_ld_wait();
-        tc_fence_before();
-        mbar_arrive(s_free);
-        if constexpr (CAP) tanh_all(sv, ar.cap);
-        // columns l <= c < l + len are seen; a row that sees nothing has p = 0 as it is
-        const int l = lo - (first + j * 128 + block * 32);
-        const bool full = __all_sync(0xffffffffu, len == 0 || (l <= 0 && l + len >= 32));
-        const uint32_t seen = full ? ~0u : bits_between(l, l + len);
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-          float2 slope;
-          float2 p = p_of<CAP>(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), ar,
-                               nl2, slope);
-          if constexpr (CAP) p = mul2(p, slope);
-          float2 ds = add2(make_float2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])), nd2);
-          ds = mul2(ds, p);
-          sv[c / 2] = pack_bf16x2(ds.x, ds.y);  // over what has been used
+        if (lane == 0) mbar_arrive(item_empty + 8 * slot);
+        if (item < 0) {
+          ++it;
+          stop = true;
+          break;
         }
-        uint32_t(&pk)[16] = *reinterpret_cast<uint32_t(*)[16]>(&sv[0]);
-        if (!full) clear_unseen(pk, seen);
-        // this buffer was last read by dQ += dS K two key tiles ago
-        ok = warp_wait(ds_free + 8 * buf, ((jj >> 1) & 1) ^ 1, err);
-        if (!ok) break;
-        tc_fence_after();
-        tmem_st16(tmem + lane_base + C::T_DS + buf * 64 + block * 16, pk);
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(ds_ready + 8 * buf);
-      }
-      if (!ok) break;
-      uint32_t r[32];
-      const int c0 = block * 32, left = a.d - c0;
-      if (n > 0) {
-        if (!warp_wait(dq_done, loaded & 1, err)) break;
-        tc_fence_after();
-        if (left > 0) {
-          tmem_ld32(tmem + lane_base + C::T_DQ + c0, r);
+        float nl = 0.f, nd = 0.f;
+        int lo = 0, len = 0;
+        if (n > 0) {
+          if (!warp_wait(q_full, loaded & 1, err)) break;
+          const float* rows = reinterpret_cast<const float*>(smem + C::OFF_ROW);
+          nl = rows[row];
+          nd = rows[128 + row];
+          lo = __float_as_int(rows[256 + row]);
+          len = __float_as_int(rows[384 + row]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(q_empty);
+        }
+        const float2 nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
+        const bool finite = finite_row(nl, nd);
+        for (int j = 0; j < n; ++j) {
+          const uint32_t jj = jg + j;
+          const int buf = jj & 1;
+          ok = warp_wait(s_full, jj & 1, err);
+          if (!ok) break;
+          tc_fence_after();
+          uint32_t sv[32], dp[32];
+          tmem_ld32(tmem + lane_base + C::T_S + block * 32, sv);
+          tmem_ld32(tmem + lane_base + C::T_DP + block * 32, dp);
           tmem_ld_wait();
-        }
-        tc_fence_before();
-        mbar_arrive(dq_free);
-        ++loaded;
-        jg += n;
-      } else {
+          tc_fence_before();
+          mbar_arrive(s_free);
+          if constexpr (CAP) tanh_all(sv, ar.cap);
+          // columns l <= c < l + len are seen; a row that sees nothing has p = 0 as it is
+          const int l = lo - (first + j * 128 + block * 32);
+          const bool full = __all_sync(0xffffffffu, len == 0 || (l <= 0 && l + len >= 32));
+          const uint32_t seen = full ? ~0u : bits_between(l, l + len);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) r[e] = 0u;
-      }
-      if (left > 0) {
-        const int again_of = not_hoisted(item);  // not held meanwhile: registers are short
-        const int t = (ar.tl.tiles - 1 - again_of / a.nkv) * ar.tl.per + row_t;
-        const int h = again_of % a.nkv * a.rep + row_h;
-        const bool real = row_t < ar.tl.per && t < a.queries;
-        if (real) put_columns(a.dq.at(t, h) + c0, r, a.scale, left, ar.wide_dq);
-        const bool mine = real && finite && !all_finite(r, left);
-        if (__any_sync(0xffffffffu, mine)) {
-          __syncwarp();  // other lanes store what a row's own lane stored
-          int first_of = 0, end_of = 0;
-          if (mine) a.span(t, first_of, end_of);
-          const int c1 = min(c0 + 32, a.d);
-          for (unsigned again = bad_rows(a, a.k, again_of % a.nkv, mine ? a.dq.at(t, h) : nullptr,
-                                         c0, c1, first_of, end_of);
-               again; again &= again - 1) {
-            const int from = __ffs(again) - 1;
-            row_dq(a, __shfl_sync(0xffffffffu, t, from), __shfl_sync(0xffffffffu, h, from), c0, c1);
+          for (int c = 0; c < 32; c += 2) {
+            float2 slope;
+            float2 p = p_of<CAP>(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), ar,
+                                 nl2, slope);
+            if constexpr (CAP) p = mul2(p, slope);
+            float2 ds = add2(make_float2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])), nd2);
+            ds = mul2(ds, p);
+            sv[c / 2] = pack_bf16x2(ds.x, ds.y);  // over what has been used
+          }
+          uint32_t(&pk)[16] = *reinterpret_cast<uint32_t(*)[16]>(&sv[0]);
+          if (!full) clear_unseen(pk, seen);
+          // this buffer was last read by dQ += dS K two key tiles ago
+          ok = warp_wait(ds_free + 8 * buf, ((jj >> 1) & 1) ^ 1, err);
+          if (!ok) break;
+          tc_fence_after();
+          tmem_st16(tmem + lane_base + C::T_DS + buf * 64 + block * 16, pk);
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(ds_ready + 8 * buf);
+        }
+        if (!ok) break;
+        uint32_t r[32];
+        const int c0 = block * 32, left = a.d - c0;
+        if (n > 0) {
+          if (!warp_wait(dq_done, loaded & 1, err)) break;
+          tc_fence_after();
+          if (left > 0) {
+            tmem_ld32(tmem + lane_base + C::T_DQ + c0, r);
+            tmem_ld_wait();
+          }
+          tc_fence_before();
+          mbar_arrive(dq_free);
+          ++loaded;
+          jg += n;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) r[e] = 0u;
+        }
+        if (left > 0) {
+          const int again_of = not_hoisted(item);  // not held meanwhile: registers are short
+          int tile, g;
+          place(again_of & (kSecond - 1), tile, g);
+          const int t = tile * ar.tl.per + row_t, h = g * a.rep + row_h;
+          const bool real = row_t < ar.tl.per && t < a.queries;
+          if (real) put_columns(a.dq.at(t, h) + c0, r, a.scale, left, ar.wide_dq);
+          const bool mine = real && finite && !all_finite(r, left);
+          if (__any_sync(0xffffffffu, mine)) {
+            if (again_of & kSecond)
+              dq_again(a, g, mine ? t : -1, h, c0, min(c0 + 32, a.d));
+            else if (lane == 0)
+              take_again(rounds, it);
           }
         }
       }
-    }
+      if (!stop && lane == 0) rounds->lost = 1;
+      __syncwarp();
+      tc_fence_before();
+    } while (next_round<true>(rounds, kThreads, redo));
   }
 
-  tc_fence_before();
-  __syncthreads();
+  // the last round's end has been waited for by all
   settle(err.err);
   if (warp == 1) {
     tc_fence_after();

@@ -364,3 +364,58 @@ def test_the_gradient_of_queries_that_see_nothing_costs_little():
     for n in ("q", "d_o"):
         st[n][blind_queries(st)] = math.nan
     assert time_us(backward_call(st)) < 3 * clean
+
+
+@pytest.mark.parametrize("mask", UNSEEN)
+@pytest.mark.parametrize("heads,cap", [((32, 8, 128), 0.0), ((8, 8, 64), 30.0), ((4, 1, 128), 20.0),
+                                       ((9, 3, 48), 0.0), ((4, 2, 16), 0.0)], ids=str)
+@pytest.mark.parametrize("junk", [math.nan, math.inf])
+def test_the_gradient_beside_keys_that_nobody_sees(mask, heads, cap, junk):
+    keys, of = UNSEEN[mask]
+    lo, hi = of()
+    st = problem(lo, hi, keys, heads, seed=14, cap=cap)
+    empty = unseen_keys(st)
+    o, lse = spans.run_forward(st)
+    bad = dict(st, **{n: st[n].clone() for n in ("k", "v")})
+    for n in ("k", "v"):
+        bad[n][empty] = junk
+    got = spans.run_backward(bad, o, lse)
+    for n in ("k", "v"):
+        assert (got[n][empty] == 0).all()
+    spans.check_backward(st, o, lse, got)
+
+
+def test_the_gradient_beside_keys_that_nobody_sees_costs_little():
+    """NaN in the unused end of a packed batch, in all that the call reads; took 140 times as long."""
+    st = packed()
+    clean = time_us(backward_call(st))
+    for n, which in (("k", unseen_keys(st)), ("v", unseen_keys(st)), ("q", blind_queries(st)),
+                     ("d_o", blind_queries(st))):
+        st[n][which] = math.nan
+    assert time_us(backward_call(st)) < 4 * clean
+
+
+@pytest.mark.parametrize("junk", [0.0, math.nan])
+def test_the_gradient_of_more_items_than_a_round_has(junk):
+    """As above, 80 items an SM of dQ."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    heads = 256
+    total = -(-80 * sms // heads) * 128 - 57
+    lengths, g = [], torch.Generator().manual_seed(5)
+    while sum(lengths) < total - 300:
+        lengths.append(int(torch.randint(1, 200, (1,), generator=g)))
+    lengths[-1] -= sum(lengths) - (total - 300)
+    lo, hi = spans.with_nothing(spans.documents(lengths), 300)
+    one = problem(lo, hi, total, (1, 1, 16), seed=6)
+    o, lse = spans.run_forward(one)
+    for n in ("q", "k", "v", "d_o"):
+        one[n][total - 300:] = junk
+    every = {n: one[n].expand(total, heads, 16).contiguous() for n in ("q", "k", "v", "d_o")}
+    every["d_lse"] = one["d_lse"].expand(total, heads).contiguous()
+    got = spans.run_backward(dict(one, **every), o.expand(total, heads, 16).contiguous(),
+                             lse.expand(total, heads).contiguous())
+    for n in got:
+        assert torch.equal(got[n], got[n][:, :1].expand_as(got[n])), n
+    for n in ("q", "k", "v", "d_o"):
+        one[n][total - 300:] = 0
+    spans.check_backward(one, o, lse, {n: got[n][:, :1] for n in got})
