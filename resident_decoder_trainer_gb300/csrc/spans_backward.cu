@@ -207,42 +207,59 @@ __global__ void __launch_bounds__(kPrepThreads, 4) prepare_kernel(const __grid_c
 }
 
 // ------------------------------------------------------------ elementwise
-// Scores to the tanh of their cap.
-__device__ __forceinline__ void tanh_all(uint32_t (&sv)[32], const Cap& cap) {
-  Reach reach;
+// Scores sv of 32 columns to p = 2^(score + neg_lse(c)) times the slope of their cap,
+// c a multiple of two; put(c, p) takes what p of c and c + 1 were. tanh and its slope
+// 1 - tanh^2 by the cap's polynomial; past it, u = 2 / (1 + e^2x), tanh = 1 - u and the
+// slope u (2 - u), which loses nothing where tanh is close to 1 (1 - tanh^2 is off by half
+// of itself at x = 8).
+template <bool CAP, typename N, typename P>
+__device__ __forceinline__ void weights(uint32_t (&sv)[32], const Args& ar, N neg_lse, P put) {
+  auto of = [&](int c) {
+    return make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+  };
+  auto leave = [&](int c, float2 s, float2 slope) {
+    float2 p = fma2(s, make_float2(ar.scale_log2, ar.scale_log2), neg_lse(c));
+    p.x = ex2_approx(p.x);
+    p.y = ex2_approx(p.y);
+    put(c, p);
+    if constexpr (CAP) p = mul2(p, slope);
+    sv[c] = __float_as_uint(p.x);
+    sv[c + 1] = __float_as_uint(p.y);
+  };
+  auto slope_of = [](float2 t) {
+    return fma2(make_float2(-t.x, -t.y), t, make_float2(1.f, 1.f));
+  };
+  if constexpr (CAP) {
+    const Cap& cap = ar.cap;
+    Reach reach;
 #pragma unroll
-  for (int c = 0; c < 32; c += 2)
-    reach.take<true>(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), (c >> 1) & 1);
-  if (reach.beyond(cap.limit)) {
+    for (int c = 0; c < 32; c += 2) reach.take<true>(of(c), (c >> 1) & 1);
+    if (reach.beyond(cap.limit)) {
 #pragma unroll
-    for (int c = 0; c < 32; ++c) {  // a score by itself decides, not what its warp holds
-      const float s = __uint_as_float(sv[c]);
-      const float near = s * odd_factor(both(s), cap.t).x;
-      // 1 - 2 / (1 + e^2x), off by 2^-23: p and the slope become bf16
-      const float e = ex2_approx(2.f * kLog2e * cap.w * fabsf(s));
-      const float far = copysignf(1.f - __fdividef(2.f, 1.f + e), s);
-      sv[c] = __float_as_uint(fabsf(s) > cap.limit ? far : near);
+      for (int c = 0; c < 32; c += 2) {  // a score by itself decides, not what its warp holds
+        const float2 s = of(c);
+        float2 t = mul2(s, odd_factor(s, cap.t)), slope = slope_of(t);
+        auto far = [&](float x, float& tanh, float& its) {  // without a branch
+          const float u = __fdividef(2.f, 1.f + ex2_approx(2.f * kLog2e * cap.w * fabsf(x)));
+          const bool past = fabsf(x) > cap.limit;
+          tanh = past ? copysignf(1.f - u, x) : tanh;
+          its = past ? fmaf(-u, u, 2.f * u) : its;
+        };
+        far(s.x, t.x, slope.x);
+        far(s.y, t.y, slope.y);
+        leave(c, t, slope);
+      }
+      return;
     }
-    return;
-  }
 #pragma unroll
-  for (int c = 0; c < 32; c += 2) {
-    const float2 s = make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
-    const float2 t = mul2(s, odd_factor(s, cap.t));
-    sv[c] = __float_as_uint(t.x);
-    sv[c + 1] = __float_as_uint(t.y);
+    for (int c = 0; c < 32; c += 2) {
+      const float2 s = of(c), t = mul2(s, odd_factor(s, cap.t));
+      leave(c, t, slope_of(t));
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) leave(c, of(c), both(1.f));
   }
-}
-
-// p = 2^(score + neg_lse) of two scores; with a cap the score is its tanh, and
-// the slope 1 - tanh^2 is left in `slope`.
-template <bool CAP>
-__device__ __forceinline__ float2 p_of(float2 s, const Args& ar, float2 neg_lse, float2& slope) {
-  if constexpr (CAP) slope = fma2(make_float2(-s.x, -s.y), s, make_float2(1.f, 1.f));
-  float2 p = fma2(s, make_float2(ar.scale_log2, ar.scale_log2), neg_lse);
-  p.x = ex2_approx(p.x);
-  p.y = ex2_approx(p.y);
-  return p;
 }
 
 // 32 bf16 values of which those with a bit in `seen` stay, whatever the others hold.
@@ -686,23 +703,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t sv[32], pk[16];
         tmem_ld32(ts, sv);
         tmem_ld_wait();
-        if constexpr (CAP) tanh_all(sv, ar.cap);
-        // sv: p, times the cap's slope
-#pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const float4 nl = lse4[c / 4];
-#pragma unroll
-          for (int e = 0; e < 4; e += 2) {
-            float2 slope;
-            float2 p = p_of<CAP>(
-                make_float2(__uint_as_float(sv[c + e]), __uint_as_float(sv[c + e + 1])), ar,
-                e ? make_float2(nl.z, nl.w) : make_float2(nl.x, nl.y), slope);
-            pk[(c + e) / 2] = pack_bf16x2(p.x, p.y);
-            if constexpr (CAP) p = mul2(p, slope);
-            sv[c + e] = __float_as_uint(p.x);
-            sv[c + e + 1] = __float_as_uint(p.y);
-          }
-        }
+        weights<CAP>(
+            sv, ar,
+            [&](int c) {
+              const float4 nl = lse4[c / 4];
+              return c & 2 ? make_float2(nl.z, nl.w) : make_float2(nl.x, nl.y);
+            },
+            [&](int c, float2 p) { pk[c / 2] = pack_bf16x2(p.x, p.y); });
         if (!full) clear_unseen(pk, seen);
         tmem_st16(ts, pk);
         tmem_st_wait();
@@ -1094,6 +1101,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     uint32_t jg = 0;
     int loaded = 0, it = 0;
+    uint32_t drains = 0;
     do {
       if (elect_one()) {
         bool stop = false;
@@ -1147,13 +1155,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++loaded;
         }
         if (!stop) rounds->lost = 1;
+        tc_commit(drain);
+        mbar_wait(drain, drains++ & 1, nullptr);
       }
       __syncwarp();
     } while (next_round<true>(rounds, kThreads, redo));
-    if (elect_one()) {
-      tc_commit(drain);
-      mbar_wait(drain, 0, nullptr);
-    }
   } else if (warp < 4) {
     while (next_round<true>(rounds, kThreads, redo)) {
     }
@@ -1206,19 +1212,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_wait();
           tc_fence_before();
           mbar_arrive(s_free);
-          if constexpr (CAP) tanh_all(sv, ar.cap);
           // columns l <= c < l + len are seen; a row that sees nothing has p = 0 as it is
           const int l = lo - (first + j * 128 + block * 32);
           const bool full = __all_sync(0xffffffffu, len == 0 || (l <= 0 && l + len >= 32));
           const uint32_t seen = full ? ~0u : bits_between(l, l + len);
+          weights<CAP>(sv, ar, [&](int) { return nl2; }, [](int, float2) {});
 #pragma unroll
           for (int c = 0; c < 32; c += 2) {
-            float2 slope;
-            float2 p = p_of<CAP>(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), ar,
-                                 nl2, slope);
-            if constexpr (CAP) p = mul2(p, slope);
             float2 ds = add2(make_float2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])), nd2);
-            ds = mul2(ds, p);
+            ds = mul2(ds, make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])));
             sv[c / 2] = pack_bf16x2(ds.x, ds.y);  // over what has been used
           }
           uint32_t(&pk)[16] = *reinterpret_cast<uint32_t(*)[16]>(&sv[0]);

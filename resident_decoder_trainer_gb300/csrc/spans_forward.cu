@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t idesc_o = idesc_bf16_f32(BM, a.d, 0, 1);
       const int ksteps = a.d / 16;
       bool ok = true;
-      uint32_t jg = 0, loaded = 0, it = 0;
+      uint32_t jg = 0, loaded = 0, it = 0, drains = 0;
       uint32_t pv0 = 0, pv1 = 0, rounds0 = 0, rounds1 = 0;  // P V issued; items with any
       uint32_t s0 = 0, s1 = 0;                               // S issued
       do {
@@ -410,13 +410,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++loaded;
           }
           if (!stop) rounds_of->lost = 1;
+          tc_commit(drain);
+          mbar_wait(drain, drains++ & 1, nullptr);
         }
         __syncwarp();
       } while (next_round<!SPLIT>(rounds_of, kThreads, redo));
-      if (elect_one()) {
-        tc_commit(drain);
-        mbar_wait(drain, 0, nullptr);
-      }
     } else {
       while (next_round<!SPLIT>(rounds_of, kThreads, redo)) {
       }
