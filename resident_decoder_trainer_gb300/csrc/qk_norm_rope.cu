@@ -125,9 +125,12 @@ __device__ __forceinline__ void put_pairs(char* p, int half, const float2 (&x)[8
 
 // Cosine and sine of two angles in 2^-31 of a half turn: the nearest quarter
 // turn is taken off, exactly, and least-squares polynomials on the eighth turn
-// left (off by 2^-29 and 2^-34) do the rest.
+// left (with these coefficients off by 2^-29.1 and 2^-28.7) do the rest.
 __device__ __forceinline__ void turn_two(int32_t a, int32_t b, float2& cos, float2& sin) {
-  const int32_t qa = (a + 0x20000000) >> 30, qb = (b + 0x20000000) >> 30;
+  auto quarter = [](int32_t v) {  // the sum passes the type's end, so not in its own
+    return static_cast<int32_t>(static_cast<uint32_t>(v) + 0x20000000u) >> 30;
+  };
+  const int32_t qa = quarter(a), qb = quarter(b);
   const float unit = 1.4629180792671596e-9f;  // pi 2^-31
   const float2 x = make_float2(static_cast<float>(static_cast<int32_t>(
                                    static_cast<uint32_t>(a) - (static_cast<uint32_t>(qa) << 30))) *
