@@ -610,7 +610,11 @@ rdt_status rdt_qk_norm_rope_backward(int32_t tokens, int32_t n_heads, int32_t n_
  * lo and hi int32 [queries], device memory; lo null: 0, hi null: keys.
  * What a query does not see does not reach its results, whatever it holds
  * (nor a key's gradients what does not see it, unless a query that does is not
- * finite itself).
+ * finite itself); where an infinity that it sees makes a result not finite, that
+ * may be NaN. NaN or infinities in memory that no query sees make a call a few
+ * times as long; in keys (queries) that some queries (keys) of a neighbourhood see
+ * and others do not, the others' rows are computed one by one, by one warp each:
+ * some 16 us for 32 keys seen, 30 us for 32 queries and heads.
  * The cost goes by the keys between the least lo and the largest hi of
  * neighbouring queries, so queries of one document belong together.
  *
@@ -626,7 +630,8 @@ rdt_status rdt_qk_norm_rope_backward(int32_t tokens, int32_t n_heads, int32_t n_
  *
  * rdt_attention_backward: gradients of sum(d_o o) + sum(d_lse lse) with
  * respect to q, k and v, those of k and v summed over the query heads that
- * share them, each rounded once to bf16. o and lse as rdt_attention wrote
+ * share them, each rounded once to bf16; p and the scores' gradients are rounded
+ * to bf16 for their products. o and lse as rdt_attention wrote
  * them; d_o bf16, d_lse fp32 [queries, n_heads] or null. Rows that nothing
  * sees or that see nothing get zeros. ws:
  * rdt_attention_workspace_bytes(..., 1) bytes, 256-byte aligned. */

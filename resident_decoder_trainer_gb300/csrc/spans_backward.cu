@@ -14,19 +14,21 @@
 // elementwise work: TMEM lanes 32 (w mod 4) on, columns 32 (w / 4 - 1) on.
 //
 // A NaN or infinity where a query does not see a key, times 0, would reach sums. Rows of
-// queries that see nothing may be memory that nobody wrote: they are cleared in
-// shared memory. Other rows of dq, dk and dv that are not finite are computed again
-// one by one (row_dq, row_dkdv). Not where they see a query whose own values are not
-// finite: what they hold is not finite by right, and a batch that has diverged
-// throughout costs no more than another.
+// queries that see nothing may be memory that nobody wrote: dK/dV clears them in
+// shared memory; dQ takes items once more that came out not finite, with the keys
+// cleared that none of their rows sees (spans.cuh). 4096 packed tokens of which the
+// unused end is NaN: 171 us, without 143. Other rows of dq, dk and dv that are not
+// finite are computed again one by one (row_dq, row_dkdv). Not where they see a query
+// (dq: in the columns of a key) that is not finite itself: what they hold is so by
+// right, and a batch that has diverged throughout costs no more than another.
 //
 // Seven products are formed where five would do: dQ summed beside dK and dV needs
 // atomics, whose order changes bits, or key tiles in a fixed order. Bound by the
 // products where many tiles are seen whole: 8192 tokens of 32 / 8 heads of 128, a
-// quarter of them a prefix, 1199 us (651 dK/dV, 510 dQ), 0.96 and 0.92 of 1890
-// TFLOP/s for the four and the three products they form. 4096 tokens in documents up
-// to 1024: 124 us, of them 17 prepare (67 MB), 58 dK/dV, 50 dQ; bound by
-// the starts and ends of short items.
+// quarter of them a prefix, 1189 us (651 dK/dV, 510 dQ), 0.96 and 0.92 of 1890
+// TFLOP/s for the four and the three products they form; back to back 1261, by the
+// power limit. 4096 tokens in documents up to 1024: 124 us, of them 17 prepare (67
+// MB), 58 dK/dV, 50 dQ; bound by the starts and ends of short items.
 #include <algorithm>
 
 #include "spans.cuh"

@@ -25,11 +25,11 @@
 // that to the join: 1 token against 32,700 keys, NaN behind them, 130 us, without 36.
 //
 // Bound by the softmax: over all 1850 cycles for 128 x 128 scores, whose two products
-// take 1400. 8192 tokens of 32 / 8 heads of 128, a quarter of them a prefix: 407 us
-// (0.76 of 1890 TFLOP/s); 4096 in documents up to 1024: 42 us, bound by the starts and
-// ends of short items (2 us each); 8191 of 16 / 8 heads of 64, capped, a window of
-// 1024: 98 us, the elementwise work of the cap; one token against 32,768 keys: 33
-// us, 4.0 TB/s, with the join.
+// take 1400; 2700 where rows begin or end in the key tile. 8192 tokens of 32 / 8 heads
+// of 128, a quarter of them a prefix: 405 us (0.76 of 1890 TFLOP/s); 4096 in documents
+// up to 1024: 42 us, bound by masked tiles and by the starts and ends of short items (2 us
+// each); 8191 of 16 / 8 heads of 64, capped, a window of 1024: 97 us, the elementwise
+// work of the cap; one token against 32,768 keys: 32 us, 4.2 TB/s, with the join.
 #include <algorithm>
 
 #include "spans.cuh"

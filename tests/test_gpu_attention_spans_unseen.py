@@ -9,7 +9,7 @@ import torch
 import test_gpu_attention_spans as spans
 from gpu_helpers import ensure_built
 from resident_decoder_trainer_gb300 import rdt
-from test_gpu_attention_spans_items import caches, problem
+from test_gpu_attention_spans_items import caches, check_by_key_heads, problem
 
 pytestmark = pytest.mark.gpu
 
@@ -419,3 +419,57 @@ def test_the_gradient_of_more_items_than_a_round_has(junk):
     for n in ("q", "k", "v", "d_o"):
         one[n][total - 300:] = 0
     spans.check_backward(one, o, lse, {n: got[n][:, :1] for n in got})
+
+
+def test_nan_beside_replays_and_other_streams():
+    """A captured layer's attention whose unused memory turns to NaN and back between replays, and
+    two such calls at once."""
+    st = packed((8, 2, 128))
+    sts = [st, problem(*caches([300, 1, 17, 128, 129, 0, 255, 256], 1, 300), 2400, (8, 2, 128))]
+    calls = []
+    for x in sts:
+        t, nh, d = x["q"].shape
+        keys, nkv = x["k"].shape[:2]
+        out = {n: torch.zeros_like(x[n]) for n in ("q", "k", "v")}
+        o, lse = torch.zeros_like(x["q"]), torch.zeros(t, nh, device="cuda")
+        ws = torch.empty(max(rdt.attention_workspace_bytes(t, keys, nh, nkv, d, backward=b)
+                             for b in (False, True)), dtype=torch.uint8, device="cuda")
+
+        def call(x=x, o=o, lse=lse, ws=ws, out=out):
+            common = dict(lo=x["lo"], hi=x["hi"], scale=x["scale"])
+            rdt.attention(x["q"], x["k"], x["v"], o, ws, lse=lse, **common)
+            rdt.attention_backward(x["q"], x["k"], x["v"], o, lse, x["d_o"], out["q"], out["k"],
+                                   out["v"], ws, d_lse=x["d_lse"], **common)
+
+        calls.append((call, o, lse, out, ws))
+    streams = [torch.cuda.Stream() for _ in sts]
+    graphs = []
+    for call, *_ in calls:
+        call()
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call()
+    for junk in (0.0, math.nan, 0.0, math.inf, 0.0):
+        for x in sts:
+            for n in ("k", "v"):
+                x[n][unseen_keys(x)] = junk
+            for n in ("q", "d_o"):
+                x[n][blind_queries(x)] = junk
+        torch.cuda.synchronize()
+        for graph, s, (_, o, lse, out, ws) in zip(graphs, streams, calls):
+            with torch.cuda.stream(s):
+                for y in (o, lse, *out.values()):
+                    y.fill_(3.0)
+                ws.fill_(255)
+                for _ in range(3):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for x, (_, o, lse, out, _) in zip(sts, calls):
+            clean = dict(x, **{n: x[n].clone() for n in ("q", "k", "v", "d_o")})
+            for n in ("k", "v"):
+                clean[n][unseen_keys(x)] = 0
+            for n in ("q", "d_o"):
+                clean[n][blind_queries(x)] = 0
+            check_by_key_heads(clean, o, lse, out)
+    assert rdt.device_error() == 0
