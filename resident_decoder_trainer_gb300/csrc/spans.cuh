@@ -420,16 +420,15 @@ __device__ __forceinline__ bool next_round(Rounds* r, int threads, unsigned long
 }
 
 // Clears the rows 32 w + i of a tile of 128 rows (chunks of 64 columns, 128 bytes a row,
-// one behind the other) that have no bit i in `keep`. Whole warp.
-__device__ __forceinline__ void clear_rows(uint8_t* tile, int d, int w, uint32_t keep) {
+// one behind the other) that have a bit i in `which`. Whole warp.
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int d, int w, uint32_t which) {
   const int lane = threadIdx.x & 31;
+  uint8_t* const at = tile + (lane >> 3) * (128 * 128) + 16 * (lane & 7) + 32 * w * 128;
+  const bool has = 64 * (lane >> 3) < d;
 #pragma unroll 1
-  for (int row = lane >> 3; row < 32; row += 4)
-    if (!(keep >> row & 1u))
-#pragma unroll 1
-      for (int c = 0; c < d; c += 64)
-        *reinterpret_cast<uint4*>(tile + c * 256 + (32 * w + row) * 128 + 16 * (lane & 7)) =
-            make_uint4(0u, 0u, 0u, 0u);
+  for (; which; which &= which - 1)
+    if (has)
+      *reinterpret_cast<uint4*>(at + (__ffs(which) - 1) * 128) = make_uint4(0u, 0u, 0u, 0u);
 }
 // What a warp has cleared, where the tensor cores see it once `bar` has been arrived on.
 __device__ __forceinline__ void hand_over(uint32_t bar) {
@@ -452,7 +451,7 @@ __device__ __forceinline__ bool clear_unseen(const SpanArgs& a, int t0, int n, i
       a.span(t0 + i, x, y);
       if (x < y) seen |= bits_between(x - base - 32 * w, y - base - 32 * w);
     }
-    clear_rows(tile, a.d, w, __reduce_or_sync(0xffffffffu, seen));
+    clear_rows(tile, a.d, w, ~__reduce_or_sync(0xffffffffu, seen));
   }
   hand_over(full);
   return true;

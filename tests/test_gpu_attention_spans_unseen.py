@@ -353,8 +353,6 @@ def test_the_gradient_of_queries_that_see_nothing(mask, heads, cap):
         bad[n][blind] = junk
     got = spans.run_backward(bad, o, lse)
     spans.check_backward(st, o, lse, got)
-    want = spans.run_backward(st, o, lse)
-    assert all(torch.equal(got[n], want[n]) for n in ("k", "v"))
 
 
 def test_the_gradient_of_queries_that_see_nothing_costs_little():
