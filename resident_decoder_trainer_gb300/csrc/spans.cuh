@@ -406,7 +406,9 @@ __device__ __forceinline__ void take_again(Rounds* r, uint32_t it) {
 }
 // A round's end: whether there is another, and the items it takes once more, if any.
 // All threads of the CTA, in whole warps, of which thread 0 belongs to the one that hands
-// out the items; waits for all of them.
+// out the items; waits for all of them. Not behind a __syncwarp() of the warps of rows,
+// whose loops leave as whole warps: with it heads of 64 took 194 us in place of 179 (8192
+// causal tokens, 16 heads).
 template <bool MORE>
 __device__ __forceinline__ bool next_round(Rounds* r, int threads, unsigned long long& redo) {
   named_bar_sync(1, threads);

@@ -1307,7 +1307,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!stop && lane == 0) rounds->lost = 1;
-      __syncwarp();
       tc_fence_before();
     } while (next_round<true>(rounds, kThreads, redo));
   }

@@ -709,7 +709,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!stop && lane == 0) rounds_of->lost = 1;
-      __syncwarp();
       tc_fence_before();
     } while (next_round<!SPLIT>(rounds_of, kThreads, redo));
   }
