@@ -97,9 +97,9 @@ __device__ __forceinline__ float score_of(const SpanArgs& a, float dot, float& s
   const float s = dot * a.scale;
   slope = 1.f;
   if (a.cap == 0.f) return s;
-  const float th = tanhf(s / a.cap);
-  slope = 1.f - th * th;
-  return a.cap * th;
+  const float x = s / a.cap, e = expf(-2.f * fabsf(x));
+  slope = 4.f * e / ((1.f + e) * (1.f + e));  // 1 - tanh^2, which cancels
+  return a.cap * tanhf(x);
 }
 
 // acc[i] += w src[column i], columns 2 lane, 2 lane + 1, and those 64 further.

@@ -15,12 +15,13 @@
 //
 // A NaN or infinity where a query does not see a key, times 0, would reach sums. Rows of
 // queries that see nothing may be memory that nobody wrote: before and behind a batch
-// dK/dV clears them in shared memory (warp 2); dQ takes items once more that came out not finite, with the keys
-// cleared that none of their rows sees (spans.cuh). 4096 packed tokens of which the
-// unused end is NaN: 171 us, without 143. Other rows of dq, dk and dv that are not
-// finite are computed again one by one (row_dq, row_dkdv). Not where they see a query
-// (dq: in the columns of a key) that is not finite itself: what they hold is so by
-// right, and a batch that has diverged throughout costs no more than another.
+// dK/dV clears them in shared memory (warp 2); dQ takes items once more that came out
+// not finite, with the keys cleared that none of their rows sees (spans.cuh). 4096
+// packed tokens of which the unused end is NaN: 171 us, without 143. Other rows of dq,
+// dk and dv that are not finite are computed again one by one (row_dq, row_dkdv). Not
+// where they see a query (dq: in the columns of a key) that is not finite itself: what
+// they hold is so by right, and a batch that has diverged throughout costs no more than
+// another.
 //
 // Seven products are formed where five would do: dQ summed beside dK and dV needs
 // atomics, whose order changes bits, or key tiles in a fixed order. Bound by the
