@@ -17,7 +17,7 @@ def built():
 
 
 def check_by_key_heads(st, o, lse, got, d_lse=True):
-    """The checks of one key head and its query heads at a time: all at once take too much memory."""
+    """The checks of one key head and its query heads at a time: all at once take much memory."""
     rep = st["q"].shape[1] // st["k"].shape[1]
     for g in range(st["k"].shape[1]):
         heads, one = slice(g * rep, (g + 1) * rep), slice(g, g + 1)

@@ -384,7 +384,7 @@ def test_the_gradient_beside_keys_that_nobody_sees(mask, heads, cap, junk):
 
 
 def test_the_gradient_beside_keys_that_nobody_sees_costs_little():
-    """NaN in the unused end of a packed batch, in all that the call reads; took 140 times as long."""
+    """NaN in the unused end of a packed batch, in all that it reads; took 140 times as long."""
     st = packed()
     clean = time_us(backward_call(st))
     for n, which in (("k", unseen_keys(st)), ("v", unseen_keys(st)), ("q", blind_queries(st)),
