@@ -733,11 +733,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 // parts waited for their weights (1 query, 1024 keys: 9.4 us in all and not 8.9).
 // A part whose o is not finite though its lse is may owe that to values that the row
 // does not see: its sum is formed again from the keys that the row sees of it, by all
-// warps, groups of lanes_of(d) lanes a key and four keys of a group under way at a time.
+// warps, groups of 2 to 16 lanes a key and four keys of a group under way at a time.
 constexpr int kJoinWarps = 4, kJoinAhead = 5, kJoinKeys = 4;
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ Args ar) {
   __shared__ float sums[kJoinWarps][kMaxDim];
   __shared__ float weight[1024];
+  __shared__ int bad;  // a warp's share of the sum is not finite
   const SpanArgs& a = ar.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t rows = static_cast<int64_t>(a.queries) * a.nh, th = blockIdx.x;
@@ -760,6 +761,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
     total += w;
   }
   total = warp_sum(total);
+  if (threadIdx.x == 0) bad = 0;
   __syncthreads();
   float acc[4] = {};
   auto add = [&](int s, float4 o) {
@@ -775,34 +777,33 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
     for (int i = 0; i < kJoinAhead; ++i)
       if (warp + i * kJoinWarps < ar.splits) add(warp + i * kJoinWarps, ahead[i]);
     for (int s = warp + kJoinAhead * kJoinWarps; s < ar.splits; s += kJoinWarps) add(s, part(s));
+    float worst = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sums[warp][4 * lane + i] = acc[i];
+    for (int i = 0; i < 4; ++i) {
+      sums[warp][4 * lane + i] = acc[i];
+      worst = fmaf(acc[i], 0.f, worst);
+    }
+    if (worst != 0.f) bad = 1;
   }
   __syncthreads();
   const int t = static_cast<int>(th / a.nh), h = static_cast<int>(th % a.nh);
-  // the row's four columns of this lane; whether they are finite
-  auto finish = [&]() -> bool {
-    bool fine = true;
-    if (4 * lane < a.d) {
-      float o[4];
+  auto finish = [&]() {
+    if (warp || 4 * lane >= a.d) return;
+    float o[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        o[i] = sums[0][4 * lane + i];
+    for (int i = 0; i < 4; ++i) {
+      o[i] = sums[0][4 * lane + i];
 #pragma unroll
-        for (int w = 1; w < kJoinWarps; ++w) o[i] += sums[w][4 * lane + i];
-        o[i] = total != 0.f ? o[i] / total : 0.f;
-        fine = fine && fabsf(o[i]) <= 3e38f;
-      }
-      if (warp == 0)
-        *reinterpret_cast<uint2*>(a.o.at(t, h) + 4 * lane) =
-            make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+      for (int w = 1; w < kJoinWarps; ++w) o[i] += sums[w][4 * lane + i];
+      o[i] = total != 0.f ? o[i] / total : 0.f;
     }
-    return __all_sync(0xffffffffu, fine);
+    *reinterpret_cast<uint2*>(a.o.at(t, h) + 4 * lane) =
+        make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
   };
-  const bool fine = finish();
+  finish();
   if (threadIdx.x == 0 && a.lse)
     a.lse[th] = total != 0.f ? (top + log2f(total)) * kLn2 : -INFINITY;
-  if (fine || total != total) return;  // the same in each warp
+  if (!bad || total != total) return;  // the same in each warp
   __syncthreads();  // the sums have been read
   auto finite = [](float4 o) {
     return fabsf(o.x) < INFINITY && fabsf(o.y) < INFINITY && fabsf(o.z) < INFINITY &&
